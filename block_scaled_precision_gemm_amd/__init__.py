@@ -20,6 +20,7 @@ __all__ = [
     "bsmm_fp8_mx32_mm", "OP_FP8_MX32_MM", "bsmm_fp8_groupwise", "OP_FP8_GROUPWISE",
     "bsmm_quant_int8_rowwise", "bsmm_quant_fp8_blockwise", "bsmm_quant_fp8_mx",
     "bsmm_quant_fp8_columns", "bsmm_quant_fp8_weight", "bsmm_quant_fp8_blockwise_columns",
+    "bsmm_quant_w4", "bsmm_w4_mm", "bsmm_w4_expert_mm",
     "bsmm_workspace_bytes", "bsmm_query_plan", "bsmm_set_override", "bsmm_set_override_tail", "bsmm_set_streamk_grid", "bsmm_mfma_probe",
     "bsmm_variant_names", "bsmm_version", "bsmm_timing_enable", "bsmm_timing_read",
     "I32", "F32", "BF16", "E4M3", "OP_INT8_ROWWISE", "OP_FP8_BLOCKWISE", "OP_FP8_MX_BMM",
@@ -96,12 +97,20 @@ def load():
                                         vp]
     L.bsmm_quant_fp8_blockwise_columns.argtypes = [vp, i64, st, vp, i64, vp, i64, i64, vp, i64,
                                                    vp, i64, i64, i64, i64, vp]
+    L.bsmm_quant_w4.argtypes = [vp, i64, st, vp, i64, vp, i64, st, vp, i64, vp, i64, st, i64,
+                                i64, vp]
+    L.bsmm_w4_mm.argtypes = [vp, i64, st, vp, i64, vp, i64, st, vp, i64, st, vp, i64, st,
+                             i64, i64, i64, vp, sz, vp]
+    L.bsmm_w4_expert_mm.argtypes = [vp, i64, st, vp, i64, i64, vp, i64, i64, st, vp, i64, i64, st,
+                                    vp, vp, st, vp, vp, i64, st, i64, i64, i64, i64, i64, vp, sz,
+                                    vp]
     for f in ("bsmm_int8_rowwise", "bsmm_fp8_blockwise", "bsmm_fp8_blockwise_scratch",
               "bsmm_fp8_mx_bmm", "bsmm_fp8_scaled_mm",
               "bsmm_fp8_mx32_mm",
               "bsmm_quant_int8_rowwise", "bsmm_quant_fp8_blockwise", "bsmm_quant_fp8_mx",
               "bsmm_quant_fp8_mx32", "bsmm_quant_fp8_columns", "bsmm_quant_fp8_weight",
-              "bsmm_quant_fp8_blockwise_columns"):
+              "bsmm_quant_fp8_blockwise_columns", "bsmm_quant_w4", "bsmm_w4_mm",
+              "bsmm_w4_expert_mm"):
         getattr(L, f).restype = st
     L.bsmm_workspace_bytes.argtypes = [st, i64, i64, i64, i64, st]
     L.bsmm_workspace_bytes.restype = sz
@@ -760,6 +769,143 @@ def bsmm_quant_fp8_mx(x, *, block=128, q=None, scale=None, stream=None):
     _check(fn(x2.data_ptr(), x2.stride(0), code, q8.data_ptr(), K,
               scale.data_ptr(), K // block, 1, M, K, _stream(stream)))
     return q, scale
+
+
+def bsmm_quant_w4(w, *, group=128, symmetric=True, scale_dtype="f32", values=False, stream=None):
+    """4-bit quantisation of a weight w [..., K] (bf16 or fp32; at least two
+    dimensions) with one scale, and unless ``symmetric`` one zero point, per
+    ``group`` (32, 64 or 128) elements of a row.
+
+    Returns (q uint8 [..., K/2], scale [..., K/group] of ``scale_dtype``,
+    zero uint8 [..., K/group] or None): the operands of bsmm_w4_mm ([N, K])
+    and bsmm_w4_expert_mm ([E, N, K]).  ``values=True`` appends what the
+    codes stand for, (code - zero) * scale, as a tensor like w.
+    """
+    torch = _torch()
+    w2, code = _quant_input(w, "w")
+    sc = _dtype_code(scale_dtype)
+    if sc not in (F32, BF16):
+        raise ValueError("scale_dtype must be f32 or bf16")
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    R, K = w2.shape
+    if K % group:
+        raise ValueError(f"the last dimension ({K}) must be a multiple of group ({group})")
+    lead = tuple(w.shape[:-1])
+    q = torch.empty(lead + (K // 2,), dtype=torch.uint8, device=w.device)
+    scale = torch.empty(lead + (K // group,), dtype=_torch_dtype(sc), device=w.device)
+    zero = None if symmetric else torch.empty(lead + (K // group,), dtype=torch.uint8,
+                                              device=w.device)
+    v = torch.empty(lead + (K,), dtype=w.dtype, device=w.device) if values else None
+    _check(load().bsmm_quant_w4(
+        w2.data_ptr(), w2.stride(0), code, q.data_ptr(), K // 2, scale.data_ptr(), K // group,
+        sc, None if symmetric else zero.data_ptr(), K // group,
+        v.data_ptr() if values else None, K, group, R, K, _stream(stream)))
+    return (q, scale, zero, v) if values else (q, scale, zero)
+
+
+def _float_code(dt, name):
+    """F32 or BF16 for a float tensor's dtype."""
+    torch = _torch()
+    if dt is torch.bfloat16:
+        return BF16
+    if dt is torch.float32:
+        return F32
+    raise ValueError(f"{name}: expected bf16 or fp32, got {dt}")
+
+
+def _w4_weight(w, scale, zero, lead, K):
+    """Check a 4-bit weight with leading shape ``lead`` against K input
+    features; returns (group, scale dtype code)."""
+    torch = _torch()
+    if w.dtype is not torch.uint8 or tuple(w.shape) != (*lead, K // 2):
+        raise ValueError(f"w must be uint8 {(*lead, K // 2)}, got {w.dtype} {tuple(w.shape)}")
+    code = _float_code(scale.dtype, "scale")
+    if scale.shape[:-1] != w.shape[:-1] or scale.dim() != w.dim():
+        raise ValueError(f"scale {tuple(scale.shape)} does not fit w {tuple(w.shape)}")
+    KG = scale.shape[-1]
+    if K % 2 or (K and (KG == 0 or K % KG)):
+        raise ValueError(f"scale has {KG} groups for K = {K}")
+    if (K and w.stride(-1) != 1) or (KG > 1 and scale.stride(-1) != 1):
+        raise ValueError("w and scale must be contiguous along their last dimension")
+    if zero is not None:
+        if zero.dtype is not torch.uint8 or zero.shape != scale.shape:
+            raise ValueError(f"zero must be uint8 {tuple(scale.shape)}, got {zero.dtype} "
+                             f"{tuple(zero.shape)}")
+        if KG > 1 and zero.stride(-1) != 1:
+            raise ValueError("zero must be contiguous along its last dimension")
+    return (K // KG if K else 32), code
+
+
+def bsmm_w4_mm(x, w, scale, zero=None, *, out_dtype="bf16", out=None, stream=None):
+    """Activations times a 4-bit weight: x @ W.T with W = (code - zero) * scale.
+
+    x: bf16 or fp32 [M, K].  w: uint8 [N, K/2], scale: bf16 or fp32
+    [N, K/group], zero: uint8 [N, K/group] or None (8), as bsmm_quant_w4
+    returns them (group 32, 64 or 128).  Returns [M, N], fp32 or bf16.
+    """
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x and w must be 2-D")
+    code = _dtype_code(out_dtype)
+    xc = _float_code(x.dtype, "x")
+    M, K = x.shape
+    N = w.shape[0]
+    group, sc = _w4_weight(w, scale, zero, (N,), K)
+    if K and x.stride(1) != 1:
+        raise ValueError(f"x must be row-major, got stride {x.stride()}")
+    o = _out(out, (M, N), code, x.device)
+    if N and o.stride(1) != 1:
+        raise ValueError("out must be contiguous along N")
+    _check(load().bsmm_w4_mm(
+        x.data_ptr(), x.stride(0), xc, w.data_ptr(), w.stride(0), scale.data_ptr(),
+        scale.stride(0), sc, None if zero is None else zero.data_ptr(),
+        0 if zero is None else zero.stride(0), group, o.data_ptr(), o.stride(0), code, M, N, K,
+        None, 0, _stream(stream)))
+    return o
+
+
+def bsmm_w4_expert_mm(x, w, scale, zero, order, offsets, *, slots_per_row=1, row_scale=None,
+                      out_dtype="bf16", out=None, stream=None):
+    """Routed rows times their experts' 4-bit weights.
+
+    x: bf16 or fp32 [R, K].  w: uint8 [E, N, K/2], scale [E, N, K/group], zero
+    [E, N, K/group] or None, as bsmm_quant_w4 returns them for a weight
+    [E, N, K].  order: int32 [S] and offsets: int32 [E + 1] as bsmm_route_topk
+    returns them.  Slot s reads row s // slots_per_row of x: slots_per_row is
+    the number of choices where x holds tokens, 1 where it holds slots.
+    row_scale: fp32 [S] (the routing weights, slot order) or None.  Returns
+    [S, N] in slot order, zeros for slots without an expert.
+    """
+    torch = _torch()
+    if x.dim() != 2 or w.dim() != 3:
+        raise ValueError("x must be 2-D and w 3-D")
+    code = _dtype_code(out_dtype)
+    xc = _float_code(x.dtype, "x")
+    R, K = x.shape
+    E, N = w.shape[0], w.shape[1]
+    group, sc = _w4_weight(w, scale, zero, (E, N), K)
+    if K and x.stride(1) != 1:
+        raise ValueError(f"x must be row-major, got stride {x.stride()}")
+    if order.dtype is not torch.int32 or order.dim() != 1 or not order.is_contiguous():
+        raise ValueError("order must be a contiguous int32 [S] tensor")
+    S = order.shape[0]
+    if offsets.dtype is not torch.int32 or tuple(offsets.shape) != (E + 1,) or \
+            not offsets.is_contiguous():
+        raise ValueError(f"offsets must be a contiguous int32 [{E + 1}] tensor")
+    if row_scale is not None and (row_scale.dtype is not torch.float32 or
+                                  row_scale.numel() != S or not row_scale.is_contiguous()):
+        raise ValueError(f"row_scale must be contiguous fp32 of {S} elements")
+    o = _out(out, (S, N), code, x.device)
+    if N and o.stride(1) != 1:
+        raise ValueError("out must be contiguous along N")
+    _check(load().bsmm_w4_expert_mm(
+        x.data_ptr(), x.stride(0), xc, w.data_ptr(), w.stride(0), w.stride(1), scale.data_ptr(),
+        scale.stride(0), scale.stride(1), sc, None if zero is None else zero.data_ptr(),
+        0 if zero is None else zero.stride(0), 0 if zero is None else zero.stride(1), group,
+        order.data_ptr(), offsets.data_ptr(), slots_per_row,
+        None if row_scale is None else row_scale.data_ptr(), o.data_ptr(), o.stride(0), code,
+        E, R, S, N, K, None, 0, _stream(stream)))
+    return o
 
 
 def bsmm_workspace_bytes(op, G, M, N, K, out_dtype):

@@ -30,7 +30,8 @@ def device_objects():
     """The regular build's device objects (kernels, packing, quantisers,
     probe, scratch); empty if it has not run."""
     objs = sorted(glob.glob(os.path.join(OBJDIR, "bsmm_kernels_*.o")))
-    for name in ("bsmm_pack.o", "bsmm_quant.o", "bsmm_probe.o", "bsmm_scratch.o"):
+    for name in ("bsmm_pack.o", "bsmm_quant.o", "bsmm_probe.o", "bsmm_scratch.o",
+                 "bsmm_w4.o"):
         objs.append(os.path.join(OBJDIR, name))
     return [o for o in objs if os.path.exists(o)]
 

@@ -11,6 +11,7 @@
 #include <string>
 
 #include "bsmm.h"
+#include "bsmm_check.h"
 #include "bsmm_internal.h"
 #include "bsmm_tuned.h"
 
@@ -19,6 +20,8 @@ namespace {
 
 thread_local char g_err[512] = "";
 
+}  // namespace
+
 bsmm_status fail(bsmm_status s, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -26,6 +29,8 @@ bsmm_status fail(bsmm_status s, const char* fmt, ...) {
   va_end(ap);
   return s;
 }
+
+namespace {
 
 // ---- override (tests / tuning) and logging --------------------------------
 // The environment is read once; after that the planning path takes no lock
@@ -90,11 +95,8 @@ unsigned plan_hash(const PlanKey& k) {
   return (unsigned)(h >> 32) % kPlanCache;
 }
 
-constexpr int64_t kMaxDim = (int64_t)1 << 31;
 constexpr int64_t kMaxLd = (int64_t)1 << 23;    // 256 rows * ld + K < 2^32
 constexpr int64_t kMaxInt8K = 130944;           // largest multiple of 128 below 2^31 / 2^14
-
-bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 
 const char* op_name(bsmm_op op) {
   switch (op) {
@@ -413,9 +415,6 @@ static bsmm_status run(const Problem& p, size_t workspace_bytes, void* ws,
 }  // namespace bsmm
 
 using namespace bsmm;
-
-#define CHECK(cond, status, ...) \
-  do { if (!(cond)) return fail(status, __VA_ARGS__); } while (0)
 
 extern "C" {
 

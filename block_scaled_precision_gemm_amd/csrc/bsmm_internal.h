@@ -183,6 +183,43 @@ struct QuantArgs {
 };
 int launch_quant(const QuantArgs& a, void* stream);
 
+// 4-bit group quantisation of w [R, K] (bsmm_quant.hip): codes q [R, K/2]
+// (row stride ldq bytes), scale (r, g) at scale[r*s_r + g], zero (r, g) at
+// zero[r*z_r + g] (null: symmetric), values [R, K] of w's type or null.
+// Validated by the entry point; R * K / group in [1, 2^30).
+struct QuantW4Args {
+  const void* w; int64_t ldw; bsmm_dtype w_dtype;
+  uint8_t* q; int64_t ldq;
+  void* scale; int64_t s_r; bsmm_dtype scale_dtype;
+  uint8_t* zero; int64_t z_r;
+  void* values; int64_t ldv;
+  int group;
+  int64_t R, K;
+};
+int launch_quant_w4(const QuantW4Args& a, void* stream);
+
+// A product with 4-bit weights (bsmm_w4.hip), dense (offsets null: E = 1, S
+// rows of x and out) or routed: positions [offsets[e], offsets[e + 1]) of
+// order[S] name the output rows ("slots") of expert e, slot s reads row s /
+// x_div of x (R rows) and is multiplied by row_scale[s] (null: 1); slots at
+// positions from offsets[E] on get zero rows.  K % group == 0 and all sizes
+// are positive; validated by the entry points except for the contents of
+// order and offsets, which the kernels clamp.
+struct W4Args {
+  const void* x; int64_t ldx; bsmm_dtype x_dtype;
+  const uint8_t* w; int64_t w_se, ldw;
+  const void* scale; int64_t s_se, s_n; int s_bf16;
+  const uint8_t* zero; int64_t z_se, z_n;
+  int group;
+  const int32_t* order;
+  const int32_t* offsets;
+  const float* row_scale;
+  int x_div;
+  void* out; int64_t ldo; bsmm_dtype out_dtype;
+  int E, R, S, N, K;
+};
+int launch_w4(const W4Args& a, void* stream);
+
 // The static device scratch of the allocation-free entry point
 // (bsmm_scratch.hip): its size, and the current device's copy's address
 // (null, with *err the HIP error, on failure).

@@ -18,7 +18,10 @@
 //     consecutive rows of one column (the weight gradient contracts over
 //     tokens), and per 128 x 128 block of a weight; both write the codes
 //     transposed (the layout in which the GEMM that consumes them reads its
-//     contraction contiguously), the weight optionally also as it is.
+//     contraction contiguously), the weight optionally also as it is;
+//   4-bit weights: one scale (and optionally one zero point) per group of
+//     32, 64 or 128 elements of a row, two codes to a byte, for the 4-bit
+//     products (quant_w4_groups).
 //
 // Every quotient is the correctly rounded binary32 quotient; rounding is to
 // nearest, ties to even; e4m3 saturates at +-448.  A row or block whose
@@ -522,7 +525,168 @@ void launch_blocks(const QuantArgs& a, hipStream_t st) {
                      a.scale, a.s_m, a.s_kb, nblocks, KB);
 }
 
+// ---- 4-bit weights, one scale per group of a row --------------------------------
+
+// Two fp32 to packed bf16 (nearest even, the kernels' float mode).
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+__device__ inline uint32_t bf16x2(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), bf16x2_t));
+}
+
+// Extremes over groups of LPB = 4, 8 or 16 consecutive lanes: xor 1 and 2
+// inside each quad, then the mirrored half row (8 lanes), or the rotations
+// by 4 and 8 of a 16-lane row.
+template <int CTRL>
+__device__ inline float dpp(float v) {
+  return __int_as_float(
+      __builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+template <int LPB>
+__device__ inline float lanes_max(float v) {
+  v = fmaxf(v, dpp<0xB1>(v));
+  v = fmaxf(v, dpp<0x4E>(v));
+  if constexpr (LPB == 8) v = fmaxf(v, dpp<0x141>(v));
+  if constexpr (LPB == 16) {
+    v = fmaxf(v, dpp<0x124>(v));
+    v = fmaxf(v, dpp<0x128>(v));
+  }
+  return v;
+}
+
+// scale and zero strides in elements; values (optional) is [R, K] of T
+template <typename T>
+struct W4Quant {
+  const T* w; int64_t ldw;
+  uint8_t* q; int64_t ldq;
+  void* scale; int64_t s_r;
+  uint8_t* zero; int64_t z_r;
+  T* values; int64_t ldv;
+  uint32_t ngroups, KG;        // groups in all, and per row
+};
+
+__device__ inline void store8_values(uint16_t* p, const float v[8]) {
+  const u32x4 o = {bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
+                   bf16x2(v[6], v[7])};
+  __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(p));
+}
+__device__ inline void store8_values(float* p, const float v[8]) {
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  const f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+  __builtin_nontemporal_store(a, reinterpret_cast<f32x4*>(p));
+  __builtin_nontemporal_store(b, reinterpret_cast<f32x4*>(p) + 1);
+}
+
+// LPB lanes of 8 elements hold one group; one read of w gives the group's
+// extremes, its scale and its codes.  Symmetric (ASYM false): s = amax / 7,
+// code = clamp(rne(w / s), -8, 7) + 8.  ASYM: with lo = min(0, min w) and hi
+// = max(0, max w), s = (hi - lo) / 15, z = clamp(rne(-lo / s), 0, 15), code
+// = clamp(rne(w / s) + z, 0, 15).  A bf16 scale (SBF) is rounded (nearest
+// even) before it divides, so codes and z fit the scale that is stored.  A
+// group whose scale is 0 stores scale 1 and codes that stand for 0.
+template <typename T, int LPB, bool ASYM, bool SBF>
+__global__ void __launch_bounds__(256) quant_w4_groups(W4Quant<T> a) {
+  constexpr int GROUP = 8 * LPB;
+  constexpr int PER_ITER = 256 / LPB;
+  const int l = threadIdx.x % LPB;
+  const uint32_t b0 = blockIdx.x * (PER_ITER * kIters) + threadIdx.x / LPB;
+  Raw8<T> buf[kIters];
+  uint32_t row[kIters], kg[kIters];
+  // a group past the end loads the last one (in bounds, ngroups >= 1) and
+  // stores nothing
+#pragma unroll
+  for (int u = 0; u < kIters; ++u) {
+    const uint32_t b = min(b0 + u * PER_ITER, a.ngroups - 1);
+    row[u] = b / a.KG;
+    kg[u] = b - row[u] * a.KG;
+    load8(buf[u], a.w + (int64_t)row[u] * a.ldw + (int64_t)kg[u] * GROUP + l * 8);
+  }
+#pragma unroll
+  for (int u = 0; u < kIters; ++u) {
+    float f[8];
+    widen(buf[u], f);
+    float hi = ASYM ? 0.0f : fabsf(f[0]), nlo = 0.0f;      // nlo = -lo
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      hi = fmaxf(hi, ASYM ? f[i] : fabsf(f[i]));
+      if (ASYM) nlo = fmaxf(nlo, -f[i]);
+    }
+    hi = lanes_max<LPB>(hi);
+    if (ASYM) nlo = lanes_max<LPB>(nlo);
+    if (b0 + u * PER_ITER >= a.ngroups) continue;     // the group's lanes together
+    float s = ASYM ? __fadd_rn(hi, nlo) / 15.0f : hi / 7.0f;
+    uint32_t sb = __float_as_uint(s);
+    if (SBF) {
+      sb = (sb + 0x7FFFu + ((sb >> 16) & 1u)) >> 16;
+      s = __uint_as_float(sb << 16);
+    }
+    const bool none = !(s > 0.0f);
+    if (none) {
+      s = 1.0f;
+      sb = SBF ? 0x3F80u : 0x3F800000u;
+    }
+    const bool fast = s >= kFastDivMin;
+    const float r = 1.0f / s;
+    float z = 8.0f;
+    if (ASYM)
+      z = none ? 0.0f
+               : __builtin_amdgcn_fmed3f(
+                     __builtin_rintf(fast ? div_fast(nlo, s, r) : nlo / s), 0.0f, 15.0f);
+    uint32_t code = 0;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float t = __builtin_rintf(fast ? div_fast(f[i], s, r) : f[i] / s);
+      float c = __builtin_amdgcn_fmed3f(t + z, 0.0f, 15.0f);
+      if (none) c = z;
+      code |= (uint32_t)(int)c << (4 * i);
+      v[i] = __fmul_rn(c - z, s);
+    }
+    const int64_t at = (int64_t)kg[u] * GROUP + l * 8;
+    __builtin_nontemporal_store(
+        code, reinterpret_cast<uint32_t*>(a.q + (int64_t)row[u] * a.ldq + at / 2));
+    if (a.values != nullptr) store8_values(a.values + (int64_t)row[u] * a.ldv + at, v);
+    if (l == 0) {
+      const int64_t i = (int64_t)row[u] * a.s_r + kg[u];
+      if (SBF) static_cast<uint16_t*>(a.scale)[i] = (uint16_t)sb;
+      else static_cast<uint32_t*>(a.scale)[i] = sb;
+      if (ASYM) a.zero[(int64_t)row[u] * a.z_r + kg[u]] = (uint8_t)(int)z;
+    }
+  }
+}
+
+template <typename T, int LPB>
+void launch_w4_groups(const QuantW4Args& p, hipStream_t st) {
+  const uint32_t KG = (uint32_t)(p.K / (8 * LPB));
+  W4Quant<T> a{static_cast<const T*>(p.w), p.ldw, p.q, p.ldq, p.scale, p.s_r, p.zero, p.z_r,
+               static_cast<T*>(p.values), p.ldv, (uint32_t)(p.R * KG), KG};
+  const uint32_t per_wg = 256 / LPB * kIters;
+  const dim3 grid((a.ngroups + per_wg - 1) / per_wg);
+  const bool sbf = p.scale_dtype == BSMM_BF16;
+  if (p.zero != nullptr) {
+    if (sbf) hipLaunchKernelGGL((quant_w4_groups<T, LPB, true, true>), grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((quant_w4_groups<T, LPB, true, false>), grid, dim3(256), 0, st, a);
+  } else {
+    if (sbf) hipLaunchKernelGGL((quant_w4_groups<T, LPB, false, true>), grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((quant_w4_groups<T, LPB, false, false>), grid, dim3(256), 0, st, a);
+  }
+}
+
+template <typename T>
+void launch_w4(const QuantW4Args& p, hipStream_t st) {
+  if (p.group == 32) launch_w4_groups<T, 4>(p, st);
+  else if (p.group == 64) launch_w4_groups<T, 8>(p, st);
+  else launch_w4_groups<T, 16>(p, st);
+}
+
 }  // namespace
+
+int launch_quant_w4(const QuantW4Args& a, void* stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (a.w_dtype == BSMM_BF16) launch_w4<uint16_t>(a, st);
+  else launch_w4<float>(a, st);
+  return hipGetLastError() == hipSuccess ? 0 : 1;
+}
 
 int launch_quant(const QuantArgs& a, void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);

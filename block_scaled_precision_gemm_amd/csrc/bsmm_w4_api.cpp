@@ -1,0 +1,167 @@
+// Host front end of the 4-bit weight operations: argument validation and the
+// C entry points bsmm_quant_w4, bsmm_w4_mm and bsmm_w4_expert_mm of
+// include/bsmm.h.  Everything here runs on the host before any HIP call.
+
+#include <cstdint>
+
+#include "bsmm.h"
+#include "bsmm_check.h"
+#include "bsmm_internal.h"
+
+using namespace bsmm;
+
+namespace {
+
+bool float_dtype(bsmm_dtype d) { return d == BSMM_F32 || d == BSMM_BF16; }
+size_t dtype_bytes(bsmm_dtype d) { return d == BSMM_BF16 ? 2 : 4; }
+
+bsmm_status check_group(int group, int64_t K) {
+  CHECK(group == 32 || group == 64 || group == 128, BSMM_ERR_ARG,
+        "group=%d (32, 64 or 128 elements)", group);
+  CHECK(K % group == 0, BSMM_ERR_UNSUPPORTED, "K=%lld is not a multiple of the group of %d",
+        (long long)K, group);
+  return BSMM_OK;
+}
+
+// Checks of the operands both products share; sizes are non-negative and
+// below 2^31.  `experts` weights at strides w_se, s_se, z_se.
+bsmm_status check_operands(const W4Args& a) {
+  const int64_t KG = a.K / a.group;
+  CHECK(a.out != nullptr, BSMM_ERR_NULL, "out is NULL");
+  CHECK(a.ldo >= a.N, BSMM_ERR_SHAPE, "ldo=%lld below N", (long long)a.ldo);
+  CHECK(aligned(a.out, 4), BSMM_ERR_ALIGN, "out not 4-byte aligned");
+  // the grid's workgroups, at least 16 rows by 16 columns each
+  CHECK(((int64_t)a.S / 16 + a.E + 1) * ((int64_t)a.N / 16 + 1) < kMaxDim, BSMM_ERR_UNSUPPORTED,
+        "rows * N beyond the largest grid");
+  if (a.K == 0) return BSMM_OK;      // zeros are written, nothing is read
+  CHECK(a.x != nullptr && a.w != nullptr && a.scale != nullptr, BSMM_ERR_NULL,
+        "x, w or scale is NULL");
+  CHECK(a.ldx >= a.K && a.ldw >= a.K / 2, BSMM_ERR_SHAPE,
+        "row strides ldx=%lld ldw=%lld below the rows", (long long)a.ldx, (long long)a.ldw);
+  CHECK(a.w_se >= 0, BSMM_ERR_LAYOUT, "negative expert stride");
+  CHECK((a.s_n == 0 || a.s_n >= KG) && a.s_se >= 0, BSMM_ERR_SCALE_SHAPE,
+        "scale strides: a row holds %lld groups (0 repeats one row)", (long long)KG);
+  CHECK(a.zero == nullptr || ((a.z_n == 0 || a.z_n >= KG) && a.z_se >= 0), BSMM_ERR_SCALE_SHAPE,
+        "zero strides: a row holds %lld groups (0 repeats one row)", (long long)KG);
+  CHECK(aligned(a.x, 16) && a.ldx % 8 == 0, BSMM_ERR_ALIGN,
+        "x not 16-byte aligned or ldx=%lld not a multiple of 8", (long long)a.ldx);
+  CHECK(aligned(a.w, 16) && a.ldw % 16 == 0 && a.w_se % 16 == 0, BSMM_ERR_ALIGN,
+        "w, its row stride or its expert stride not 16-byte aligned");
+  CHECK(aligned(a.scale, a.s_bf16 ? 2 : 4), BSMM_ERR_ALIGN, "scale not aligned to its type");
+  return BSMM_OK;
+}
+
+bsmm_status run(const W4Args& a, void* workspace, size_t workspace_bytes, void* stream) {
+  (void)workspace;
+  (void)workspace_bytes;
+  const bsmm_status st = check_operands(a);
+  if (st != BSMM_OK) return st;
+  if (launch_w4(a, stream) != 0) return fail(BSMM_ERR_HIP, "kernel launch failed (w4)");
+  return BSMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+bsmm_status bsmm_quant_w4(const void* w, int64_t ldw, bsmm_dtype w_dtype, uint8_t* q,
+                          int64_t ldq, void* scale, int64_t s_r, bsmm_dtype scale_dtype,
+                          uint8_t* zero, int64_t z_r, void* values, int64_t ldv, int group,
+                          int64_t R, int64_t K, void* stream) {
+  CHECK(float_dtype(w_dtype) && float_dtype(scale_dtype), BSMM_ERR_DTYPE,
+        "w and scale must be fp32 or bf16 (got %d, %d)", (int)w_dtype, (int)scale_dtype);
+  CHECK(R >= 0 && K >= 0, BSMM_ERR_SHAPE, "negative size R=%lld K=%lld", (long long)R,
+        (long long)K);
+  CHECK(R < kMaxDim && K < kMaxDim, BSMM_ERR_UNSUPPORTED, "size beyond 2^31");
+  bsmm_status st = check_group(group, K);
+  if (st != BSMM_OK || R == 0 || K == 0) return st;
+  const int64_t KG = K / group;
+  CHECK(R * KG < ((int64_t)1 << 30), BSMM_ERR_UNSUPPORTED, "R * K / group = %lld beyond 2^30",
+        (long long)(R * KG));
+  CHECK(w != nullptr && q != nullptr && scale != nullptr, BSMM_ERR_NULL,
+        "w, q or scale is NULL");
+  CHECK(ldw >= K && ldq >= K / 2, BSMM_ERR_SHAPE, "row strides ldw=%lld ldq=%lld below the row",
+        (long long)ldw, (long long)ldq);
+  CHECK(values == nullptr || ldv >= K, BSMM_ERR_SHAPE, "ldv=%lld below K", (long long)ldv);
+  CHECK(s_r >= (R > 1 ? KG : 0), BSMM_ERR_SCALE_SHAPE,
+        "scale row stride %lld below the %lld groups of a row", (long long)s_r, (long long)KG);
+  CHECK(zero == nullptr || z_r >= (R > 1 ? KG : 0), BSMM_ERR_SCALE_SHAPE,
+        "zero row stride %lld below the %lld groups of a row", (long long)z_r, (long long)KG);
+  CHECK(aligned(w, 16) && ldw % 8 == 0, BSMM_ERR_ALIGN,
+        "w not 16-byte aligned or ldw=%lld not a multiple of 8", (long long)ldw);
+  CHECK(aligned(q, 16) && ldq % 16 == 0, BSMM_ERR_ALIGN, "q or ldq not 16-byte aligned");
+  CHECK(values == nullptr || (aligned(values, 16) && ldv % 8 == 0), BSMM_ERR_ALIGN,
+        "values not 16-byte aligned or ldv=%lld not a multiple of 8", (long long)ldv);
+  CHECK(aligned(scale, dtype_bytes(scale_dtype)), BSMM_ERR_ALIGN,
+        "scale not aligned to its type");
+  QuantW4Args a{w, ldw, w_dtype, q, ldq, scale, s_r, scale_dtype, zero, z_r, values, ldv, group,
+                R, K};
+  if (launch_quant_w4(a, stream) != 0) return fail(BSMM_ERR_HIP, "quantiser launch failed");
+  return BSMM_OK;
+}
+
+bsmm_status bsmm_w4_mm(const void* x, int64_t ldx, bsmm_dtype x_dtype, const uint8_t* w,
+                       int64_t ldw, const void* scale, int64_t s_n, bsmm_dtype scale_dtype,
+                       const uint8_t* zero, int64_t z_n, int group, void* out, int64_t ldo,
+                       bsmm_dtype out_dtype, int64_t M, int64_t N, int64_t K, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  CHECK(float_dtype(x_dtype) && float_dtype(scale_dtype) && float_dtype(out_dtype),
+        BSMM_ERR_DTYPE, "x, scale and out must be fp32 or bf16 (got %d, %d, %d)", (int)x_dtype,
+        (int)scale_dtype, (int)out_dtype);
+  CHECK(M >= 0 && N >= 0 && K >= 0, BSMM_ERR_SHAPE, "negative size M=%lld N=%lld K=%lld",
+        (long long)M, (long long)N, (long long)K);
+  CHECK(M < kMaxDim && N < kMaxDim && K < kMaxDim, BSMM_ERR_UNSUPPORTED, "size beyond 2^31");
+  bsmm_status st = check_group(group, K);
+  if (st != BSMM_OK || M == 0 || N == 0) return st;
+  W4Args a{};
+  a.x = x; a.ldx = ldx; a.x_dtype = x_dtype;
+  a.w = w; a.ldw = ldw;
+  a.scale = scale; a.s_n = s_n; a.s_bf16 = scale_dtype == BSMM_BF16;
+  a.zero = zero; a.z_n = z_n;
+  a.group = group;
+  a.x_div = 1;
+  a.out = out; a.ldo = ldo; a.out_dtype = out_dtype;
+  a.E = 1; a.R = (int)M; a.S = (int)M; a.N = (int)N; a.K = (int)K;
+  return run(a, workspace, workspace_bytes, stream);
+}
+
+bsmm_status bsmm_w4_expert_mm(const void* x, int64_t ldx, bsmm_dtype x_dtype, const uint8_t* w,
+                              int64_t w_se, int64_t ldw, const void* scale, int64_t s_se,
+                              int64_t s_n, bsmm_dtype scale_dtype, const uint8_t* zero,
+                              int64_t z_se, int64_t z_n, int group, const int32_t* order,
+                              const int32_t* offsets, int slots_per_row, const float* row_scale,
+                              void* out, int64_t ldo, bsmm_dtype out_dtype, int64_t E, int64_t R,
+                              int64_t S, int64_t N, int64_t K, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  CHECK(float_dtype(x_dtype) && float_dtype(scale_dtype) && float_dtype(out_dtype),
+        BSMM_ERR_DTYPE, "x, scale and out must be fp32 or bf16 (got %d, %d, %d)", (int)x_dtype,
+        (int)scale_dtype, (int)out_dtype);
+  CHECK(E >= 0 && R >= 0 && S >= 0 && N >= 0 && K >= 0, BSMM_ERR_SHAPE,
+        "negative size E=%lld R=%lld S=%lld N=%lld K=%lld", (long long)E, (long long)R,
+        (long long)S, (long long)N, (long long)K);
+  CHECK(R < kMaxDim && S < kMaxDim && N < kMaxDim && K < kMaxDim, BSMM_ERR_UNSUPPORTED,
+        "size beyond 2^31");
+  CHECK(E <= 1024, BSMM_ERR_UNSUPPORTED, "E=%lld beyond 1024 experts", (long long)E);
+  CHECK(slots_per_row >= 1, BSMM_ERR_ARG, "slots_per_row=%d", slots_per_row);
+  CHECK(S <= R * slots_per_row, BSMM_ERR_SHAPE, "S=%lld slots beyond R * slots_per_row = %lld",
+        (long long)S, (long long)(R * slots_per_row));
+  bsmm_status st = check_group(group, K);
+  if (st != BSMM_OK || S == 0 || N == 0) return st;
+  CHECK(E > 0, BSMM_ERR_SHAPE, "slots but no experts");
+  CHECK(order != nullptr && offsets != nullptr, BSMM_ERR_NULL, "order or offsets is NULL");
+  CHECK(aligned(order, 4) && aligned(offsets, 4) && aligned(row_scale, 4), BSMM_ERR_ALIGN,
+        "order, offsets or row_scale not 4-byte aligned");
+  W4Args a{};
+  a.x = x; a.ldx = ldx; a.x_dtype = x_dtype;
+  a.w = w; a.w_se = w_se; a.ldw = ldw;
+  a.scale = scale; a.s_se = s_se; a.s_n = s_n; a.s_bf16 = scale_dtype == BSMM_BF16;
+  a.zero = zero; a.z_se = z_se; a.z_n = z_n;
+  a.group = group;
+  a.order = order; a.offsets = offsets; a.row_scale = row_scale;
+  a.x_div = slots_per_row;
+  a.out = out; a.ldo = ldo; a.out_dtype = out_dtype;
+  a.E = (int)E; a.R = (int)R; a.S = (int)S; a.N = (int)N; a.K = (int)K;
+  return run(a, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

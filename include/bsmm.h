@@ -418,6 +418,83 @@ bsmm_status bsmm_quant_fp8_blockwise_columns(const void* x, int64_t ldx, bsmm_dt
                                              int64_t sc_c, int64_t R, int64_t C,
                                              void* stream);
 
+/*
+ * 4-bit weights.  A weight [R, K] is kept as codes 0..15, two to a byte along
+ * K (element k in byte k / 2, the low nibble for even k), with one scale and
+ * optionally one zero point per `group` consecutive elements of a row (32, 64
+ * or 128):
+ *   value(r, k) = (code(r, k) - zero(r, k / group)) * scale(r, k / group)
+ * zero is 8 everywhere where no zero points are kept.  Scales are fp32 or
+ * bf16, zero points bytes; the groups of a row are contiguous in both.
+ *
+ * bsmm_quant_w4 makes them from w (fp32 or bf16, row stride ldw elements):
+ *   symmetric (zero NULL):  scale = amax / 7,
+ *     code = clamp(rne(w / scale), -8, 7) + 8
+ *   with zero points:  lo = min(0, min w), hi = max(0, max w),
+ *     scale = (hi - lo) / 15,  zero = clamp(rne(-lo / scale), 0, 15),
+ *     code = clamp(rne(w / scale) + zero, 0, 15)
+ * Each quotient and hi - lo is one correctly rounded binary32 operation; a
+ * bf16 scale is rounded to nearest even before it divides.  A group whose
+ * scale is 0 stores scale 1, zero 0 and codes that stand for 0.  NaN and
+ * infinite inputs, and a hi - lo beyond binary32, are unsupported.
+ * values (NULL or [R, K] of w's type, row stride ldv): what the codes stand
+ * for, (code - zero) * scale rounded once to binary32 (and once more to bf16).
+ *   q [R, K/2], row stride ldq bytes; scale (r, g) at scale[r*s_r + g], zero
+ *   (r, g) at zero[r*z_r + g].
+ *   Requirements: K % group == 0, R * K / group < 2^30; w, q and values
+ *   16-byte aligned, ldw and ldv multiples of 8 elements, ldq of 16 bytes;
+ *   s_r and z_r at least K / group when R > 1.  R == 0 or K == 0 does nothing.
+ */
+bsmm_status bsmm_quant_w4(const void* w, int64_t ldw, bsmm_dtype w_dtype, uint8_t* q,
+                          int64_t ldq, void* scale, int64_t s_r, bsmm_dtype scale_dtype,
+                          uint8_t* zero, int64_t z_r, void* values, int64_t ldv, int group,
+                          int64_t R, int64_t K, void* stream);
+
+/*
+ * Activations times a 4-bit weight (the format above, [N, K]):
+ *   out(m, n) = sum_g scale(n, g) * sum_{k in group g} (code(n, k) - zero(n, g)) * x(m, k)
+ * with fp32 sums over unrounded products, stored as fp32 or bf16 (RNE).
+ *   x    (m, k) at x[m*ldx + k]     fp32 or bf16
+ *   w    row n at w[n*ldw] (bytes), two codes to a byte
+ *   scale (n, g) at scale[n*s_n + g], zero (n, g) at zero[n*z_n + g] (NULL: 8);
+ *   s_n or z_n 0 repeats one row
+ *   out  (m, n) at out[m*ldo + n]
+ * Any M and N; K a multiple of group (32, 64 or 128).  x, w and their row
+ * strides 16-byte aligned (ldx a multiple of 8 elements), out 4-byte aligned.
+ * |x| up to 2^100: NaN, infinities and larger values are unsupported.  fp32
+ * activations are used in full precision.  M == 0 or N == 0 does nothing, K
+ * == 0 writes zeros.
+ */
+bsmm_status bsmm_w4_mm(const void* x, int64_t ldx, bsmm_dtype x_dtype, const uint8_t* w,
+                       int64_t ldw, const void* scale, int64_t s_n, bsmm_dtype scale_dtype,
+                       const uint8_t* zero, int64_t z_n, int group, void* out, int64_t ldo,
+                       bsmm_dtype out_dtype, int64_t M, int64_t N, int64_t K, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * Routed rows times their experts' 4-bit weights w [E, N, K] (expert e at
+ * w + e*w_se, scale + e*s_se, zero + e*z_se, each as for bsmm_w4_mm).  A slot
+ * is one (token, choice) pair; order [S] lists the slots by expert and
+ * offsets [E + 1] says where each expert's run of order begins and ends, as
+ * bsmm_route_topk writes them:
+ *   out(s, :) = row_scale[s] * W_e x(s / slots_per_row, :)
+ *     for every s = order[i], offsets[e] <= i < offsets[e + 1]
+ *   out(s, :) = 0 for s = order[i], i >= offsets[E]
+ * x has R rows, S <= R * slots_per_row (slots_per_row = the choices per token
+ * where x holds tokens, 1 where it holds slots).  row_scale NULL: 1.  order
+ * must hold every slot once and offsets must rise from 0; other contents give
+ * undefined rows of out (never an access outside the arrays).  E <= 1024;
+ * everything else as for bsmm_w4_mm.
+ */
+bsmm_status bsmm_w4_expert_mm(const void* x, int64_t ldx, bsmm_dtype x_dtype, const uint8_t* w,
+                              int64_t w_se, int64_t ldw, const void* scale, int64_t s_se,
+                              int64_t s_n, bsmm_dtype scale_dtype, const uint8_t* zero,
+                              int64_t z_se, int64_t z_n, int group, const int32_t* order,
+                              const int32_t* offsets, int slots_per_row, const float* row_scale,
+                              void* out, int64_t ldo, bsmm_dtype out_dtype, int64_t E, int64_t R,
+                              int64_t S, int64_t N, int64_t K, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 /* Workspace bytes the fastest plan for this problem wants (0 if none). */
 size_t bsmm_workspace_bytes(bsmm_op op, int64_t G, int64_t M, int64_t N,
                             int64_t K, bsmm_dtype out_dtype);
