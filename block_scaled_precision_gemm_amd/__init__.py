@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 __all__ = [
     "load", "lib_path", "BsmmError",
@@ -21,6 +22,7 @@ __all__ = [
     "bsmm_quant_int8_rowwise", "bsmm_quant_fp8_blockwise", "bsmm_quant_fp8_mx",
     "bsmm_quant_fp8_columns", "bsmm_quant_fp8_weight", "bsmm_quant_fp8_blockwise_columns",
     "bsmm_quant_w4", "bsmm_w4_mm", "bsmm_w4_expert_mm",
+    "bsmm_route_topk", "bsmm_route_topk_backward", "Route",
     "bsmm_workspace_bytes", "bsmm_query_plan", "bsmm_set_override", "bsmm_set_override_tail", "bsmm_set_streamk_grid", "bsmm_mfma_probe",
     "bsmm_variant_names", "bsmm_version", "bsmm_timing_enable", "bsmm_timing_read",
     "I32", "F32", "BF16", "E4M3", "OP_INT8_ROWWISE", "OP_FP8_BLOCKWISE", "OP_FP8_MX_BMM",
@@ -104,13 +106,19 @@ def load():
     L.bsmm_w4_expert_mm.argtypes = [vp, i64, st, vp, i64, i64, vp, i64, i64, st, vp, i64, i64, st,
                                     vp, vp, st, vp, vp, i64, st, i64, i64, i64, i64, i64, vp, sz,
                                     vp]
+    L.bsmm_route_workspace_bytes.argtypes = [i64, i64]
+    L.bsmm_route_workspace_bytes.restype = sz
+    L.bsmm_route_topk.argtypes = [vp, i64, st, vp, st, st, ctypes.c_float, vp, vp, vp, vp, vp, vp,
+                                  vp, vp, i64, i64, vp, sz, vp]
+    L.bsmm_route_topk_backward.argtypes = [vp, i64, st, vp, vp, vp, vp, vp, st, st,
+                                           ctypes.c_float, vp, vp, vp, i64, i64, i64, vp]
     for f in ("bsmm_int8_rowwise", "bsmm_fp8_blockwise", "bsmm_fp8_blockwise_scratch",
               "bsmm_fp8_mx_bmm", "bsmm_fp8_scaled_mm",
               "bsmm_fp8_mx32_mm",
               "bsmm_quant_int8_rowwise", "bsmm_quant_fp8_blockwise", "bsmm_quant_fp8_mx",
               "bsmm_quant_fp8_mx32", "bsmm_quant_fp8_columns", "bsmm_quant_fp8_weight",
               "bsmm_quant_fp8_blockwise_columns", "bsmm_quant_w4", "bsmm_w4_mm",
-              "bsmm_w4_expert_mm"):
+              "bsmm_w4_expert_mm", "bsmm_route_topk", "bsmm_route_topk_backward"):
         getattr(L, f).restype = st
     L.bsmm_workspace_bytes.argtypes = [st, i64, i64, i64, i64, st]
     L.bsmm_workspace_bytes.restype = sz
@@ -173,18 +181,23 @@ _WS_NEED = {}     # workspace bytes per (op, G, M, N, K, out dtype); cleared by 
 
 
 def _workspace(op, G, M, N, K, out_dtype, device, stream, handle):
-    """Workspace for the fastest plan, cached per (device, stream) and grown
-    when a call needs more.  Calls on one stream run in order, so they may
-    share a buffer; calls on different streams get different buffers.  A
-    buffer is allocated while its stream is current, so the caching
-    allocator hands its memory to no other stream before the work queued on
-    that stream has finished, even once the buffer is replaced by a larger
-    one."""
+    """Workspace for the fastest plan of a GEMM (see _buffer)."""
     key = (op, G, M, N, K, out_dtype)
     need = _WS_NEED.get(key)
     if need is None:
         need = load().bsmm_workspace_bytes(op, G, M, N, K, out_dtype)
         _WS_NEED[key] = need
+    return _buffer(need, device, stream, handle)
+
+
+def _buffer(need, device, stream, handle):
+    """A workspace of at least ``need`` bytes, cached per (device, stream) and
+    grown when a call needs more.  Calls on one stream run in order, so they
+    may share a buffer; calls on different streams get different buffers.  A
+    buffer is allocated while its stream is current, so the caching
+    allocator hands its memory to no other stream before the work queued on
+    that stream has finished, even once the buffer is replaced by a larger
+    one."""
     if need == 0:
         return None, 0
     wkey = (device, handle)
@@ -905,6 +918,117 @@ def bsmm_w4_expert_mm(x, w, scale, zero, order, offsets, *, slots_per_row=1, row
         order.data_ptr(), offsets.data_ptr(), slots_per_row,
         None if row_scale is None else row_scale.data_ptr(), o.data_ptr(), o.stride(0), code,
         E, R, S, N, K, None, 0, _stream(stream)))
+    return o
+
+
+class Route(NamedTuple):
+    """What bsmm_route_topk returns; live, prob_sum and loss are None without
+    a loss."""
+    index: object        # int32 [T, k]
+    weight: object       # fp32 [T, k]
+    counts: object       # int32 [E]
+    offsets: object      # int32 [E + 1]
+    order: object        # int32 [T * k]
+    live: object         # int32 [1]
+    prob_sum: object     # fp32 [E]
+    loss: object         # fp32 [1]
+
+
+def _route_mask(mask, T):
+    torch = _torch()
+    if mask is None:
+        return None
+    if mask.dtype not in (torch.bool, torch.uint8) or tuple(mask.shape) != (T,) or \
+            (T > 1 and mask.stride(0) != 1):
+        raise ValueError(f"mask must be a contiguous bool or uint8 [{T}] tensor")
+    return mask.data_ptr()
+
+
+def bsmm_route_topk(logits, k, *, mask=None, renorm=True, alpha=None, stream=None):
+    """Top-k experts of every token, with what their products need.
+
+    logits: bf16 or fp32 [T, E], unit stride along E.  mask: bool or uint8
+    [T], false for tokens to leave out.  renorm: the weights of a token sum to
+    one.  alpha: weight of the balance loss; None for serving (no loss).
+    Returns a Route: index and weight [T, k], counts [E], offsets [E + 1] and
+    order [T * k] (the slots t * k + j sorted by expert, for
+    bsmm_w4_expert_mm), and with a loss live [1], prob_sum [E] and loss [1].
+    """
+    torch = _torch()
+    code = _float_code(logits.dtype, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be 2-D [T, E]")
+    T, E = logits.shape
+    if E and logits.stride(1) != 1:
+        raise ValueError(f"logits must be row-major, got stride {logits.stride()}")
+    if not 1 <= k <= min(E, 32):
+        raise ValueError(f"k must be 1 to 32 and at most E = {E}, got {k}")
+    mp = _route_mask(mask, T)
+    dev = logits.device
+    # one allocation for the integers, one for the floats: a decode step is
+    # bound by the host
+    S = T * k
+    ints = torch.empty(2 * S + 2 * E + 2, dtype=torch.int32, device=dev)
+    floats = torch.empty(S + E + 1, dtype=torch.float32, device=dev)
+    ip, fp = ints.data_ptr(), floats.data_ptr()
+    hs = _stream(stream)
+    wbuf, wn = _buffer(load().bsmm_route_workspace_bytes(T, E), dev, stream, hs)
+    loss = alpha is not None
+    _check(load().bsmm_route_topk(
+        logits.data_ptr(), logits.stride(0), code, mp, k, 1 if renorm else 0,
+        alpha if loss else 0.0, ip, fp, ip + 8 * S, ip + 8 * S + 4 * E, ip + 4 * S,
+        ip + 8 * S + 8 * E + 4 if loss else None, fp + 4 * S if loss else None,
+        fp + 4 * (S + E) if loss else None, T, E, wbuf.data_ptr() if wn else None, wn, hs))
+    index, order, counts, offsets, live = ints.split((S, S, E, E + 1, 1))
+    weight, prob_sum, total = floats.split((S, E, 1))
+    return Route(index.view(T, k), weight.view(T, k), counts, offsets, order,
+                 live if loss else None, prob_sum if loss else None, total if loss else None)
+
+
+def bsmm_route_topk_backward(logits, index, weight, counts, live, *, dweight=None, dloss=None,
+                             alpha=0.0, mask=None, renorm=True, out=None, stream=None):
+    """The logits' gradient of bsmm_route_topk.
+
+    logits, mask, renorm and alpha as given to the forward call; index,
+    weight, counts and live from its Route (counts and live may be sums over
+    data-parallel ranks).  dweight: fp32 [T, k] or None; dloss: fp32 of one
+    element or None.  Returns dlogits like logits.
+    """
+    torch = _torch()
+    code = _float_code(logits.dtype, "logits")
+    if logits.dim() != 2 or index.dim() != 2:
+        raise ValueError("logits and index must be 2-D")
+    T, E = logits.shape
+    k = index.shape[1]
+    if E and logits.stride(1) != 1:
+        raise ValueError(f"logits must be row-major, got stride {logits.stride()}")
+    for t, n, dt in ((index, "index", torch.int32), (weight, "weight", torch.float32),
+                     (dweight, "dweight", torch.float32)):
+        if t is None and n != "index":
+            continue
+        if t.dtype is not dt or tuple(t.shape) != (T, k) or not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous {dt} [{T}, {k}]")
+    if dloss is not None:
+        if dloss.dtype is not torch.float32 or dloss.numel() != 1:
+            raise ValueError("dloss must be one fp32 value")
+        if counts is None or counts.dtype is not torch.int32 or tuple(counts.shape) != (E,) or \
+                not counts.is_contiguous():
+            raise ValueError(f"counts must be contiguous int32 [{E}]")
+        if live is None or live.dtype is not torch.int32 or live.numel() != 1:
+            raise ValueError("live must be one int32 value")
+    mp = _route_mask(mask, T)
+    o = _out(out, (T, E), code, logits.device)
+    if E and o.stride(1) != 1:
+        raise ValueError("out must be row-major")
+
+    def ptr(t):
+        return None if t is None else t.data_ptr()
+
+    _check(load().bsmm_route_topk_backward(
+        logits.data_ptr(), logits.stride(0), code, mp, index.data_ptr(), ptr(weight),
+        ptr(counts) if dloss is not None else None, ptr(live) if dloss is not None else None, k,
+        1 if renorm else 0, alpha, ptr(dweight), ptr(dloss), o.data_ptr(), o.stride(0), T, E,
+        _stream(stream)))
     return o
 
 

@@ -22,7 +22,7 @@ OBJDIR = os.path.join(PKG, "_build")
 ARCH = "gfx950"
 
 HOST_SOURCES = ["bsmm_api.cpp", "bsmm_tuned.cpp", "bsmm_variants.cpp", "bsmm_timing.cpp",
-                "bsmm_w4_api.cpp"]
+                "bsmm_w4_api.cpp", "bsmm_route_api.cpp"]
 HIP_SOURCE = "bsmm_kernels.hip"
 # The kernel source is compiled once per (operation, output type) pair, in
 # parallel; each object holds that pair's kernels for every configuration.
@@ -67,7 +67,7 @@ def build(verbose: bool = False) -> str:
                      f"-DBSMM_TU_OUT={out}", "-x", "hip", "-c",
                      os.path.join(CSRC, HIP_SOURCE), "-o", o])
     for src in ("bsmm_pack.hip", "bsmm_quant.hip", "bsmm_probe.hip", "bsmm_scratch.hip",
-                "bsmm_w4.hip"):
+                "bsmm_w4.hip", "bsmm_route.hip"):
         o = os.path.join(OBJDIR, src.replace(".hip", ".o"))
         jobs.append([hipcc, *COMMON, *HIP_FLAGS, "-x", "hip", "-c",
                      os.path.join(CSRC, src), "-o", o])

@@ -220,6 +220,40 @@ struct W4Args {
 };
 int launch_w4(const W4Args& a, void* stream);
 
+// The expert router (bsmm_route.hip).  logits [T, E], row stride ldl; index,
+// weight [T, k] and order [T * k] contiguous; counts [E], offsets [E + 1].
+// loss, live and prob_sum are null together.  Tokens go to workgroups in
+// blocks of `block` (a multiple of 64, at most 65535 tokens); with more than
+// one block, hist [blocks][hist_ld] holds each block's counts and, in column
+// E, its live tokens (hist_ld a multiple of 8 above E), prob [blocks][E] its
+// sums of probabilities.
+constexpr int kRouteMaxE = 1024, kRouteMaxK = 32, kRouteMaxBlocks = 256;
+struct RouteArgs {
+  const void* logits; int64_t ldl; bsmm_dtype dtype;
+  const uint8_t* mask;
+  int k, renorm;
+  float alpha;
+  int32_t* index; float* weight; int32_t* counts; int32_t* offsets; int32_t* order;
+  int32_t* live; float* prob_sum; float* loss;
+  int T, E, block;
+  uint16_t* hist; int hist_ld;
+  float* prob;
+};
+int launch_route(const RouteArgs& a, int blocks, void* stream);
+
+// Gradient of the logits; dweight and dloss may each be null.
+struct RouteBackArgs {
+  const void* logits; int64_t ldl; bsmm_dtype dtype;
+  const uint8_t* mask;
+  const int32_t* index; const float* weight; const int32_t* counts; const int32_t* live;
+  int k, renorm;
+  float alpha;
+  const float* dweight; const float* dloss;
+  void* dlogits; int64_t ldd;
+  int T, E;
+};
+int launch_route_backward(const RouteBackArgs& a, void* stream);
+
 // The static device scratch of the allocation-free entry point
 // (bsmm_scratch.hip): its size, and the current device's copy's address
 // (null, with *err the HIP error, on failure).

@@ -1,0 +1,525 @@
+// The router of a mixture-of-experts layer (gfx950): top-k choice, per-expert
+// counts, the slots sorted by expert, the balance loss and its gradient.
+//
+//   p = softmax(logits[t]);  index[t, j] = the j-th largest logit's expert
+//   weight[t, j] = p[index], or p[index] / sum_j p[index]
+//   loss = alpha * E / (k L^2) * sum_e counts[e] * prob_sum[e]
+//
+// A wave holds one token's logits in registers, expert i * 64 + lane in
+// element i, so that loads are coalesced whatever the row stride.  The k
+// rounds of the choice are integer maxima over order-preserving keys; ties
+// go to the lowest expert by looking at the ballots of elements 0, 1, ... in
+// turn.
+//
+// The order of the slots is a stable counting sort.  A token's choices are
+// distinct experts, so 64 tokens make one 64-bit mask per expert, and a
+// slot's rank among them is the number of mask bits below its token: no
+// atomic's order can change a result.  Blocks of tokens write their counts,
+// and a second launch gives every block its bases from all blocks' counts.
+// At most kMaxBlocks blocks (one per compute unit) keep that table small;
+// more tokens make larger blocks.
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "bsmm_internal.h"
+
+namespace bsmm {
+namespace {
+
+constexpr int kWaves = 16;              // waves of a workgroup
+constexpr int kThreads = kWaves * 64;
+constexpr uint32_t kNoKey = 0x007FFFFFu;   // the key of -inf; nothing at or below it is chosen
+
+typedef unsigned long long u64;
+
+__device__ __forceinline__ float load_logit(const uint16_t* p) {
+  return __uint_as_float((uint32_t)*p << 16);
+}
+__device__ __forceinline__ float load_logit(const float* p) { return *p; }
+__device__ __forceinline__ void store_grad(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_grad(uint16_t* p, float v) {
+  uint32_t b = __float_as_uint(v);
+  b = v != v ? b | 0x400000u : b + 0x7FFFu + ((b >> 16) & 1u);
+  *p = (uint16_t)(b >> 16);
+}
+
+// Integers in the order of the floats; -0 as +0; a NaN below everything.
+__device__ __forceinline__ uint32_t key_of(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return v != v ? 0u : b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float of_key(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+// Wave reductions by row shifts and row broadcasts; the total is lane 63's.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = dpp_max<0x111>(v);
+  v = dpp_max<0x112>(v);
+  v = dpp_max<0x114>(v);
+  v = dpp_max<0x118>(v);
+  v = dpp_max<0x142>(v);
+  v = dpp_max<0x143>(v);
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __int_as_float(
+                 __builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = dpp_add<0x111>(v);
+  v = dpp_add<0x112>(v);
+  v = dpp_add<0x114>(v);
+  v = dpp_add<0x118>(v);
+  v = dpp_add<0x142>(v);
+  v = dpp_add<0x143>(v);
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+__device__ __forceinline__ int wave_scan(int v) {      // inclusive
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int t = __shfl_up(v, d);
+    if (lane >= d) v += t;
+  }
+  return v;
+}
+
+// e^d for d <= 0 (0 below -200, NaN kept): 2^(d log2 e) with the product's
+// rounding error and the constant's low part put back, so the error stays
+// that of the hardware's 2^x instead of growing with |d|.
+__device__ __forceinline__ float exp_neg(float d) {
+  constexpr float kL = 0x1.715476p+0f, kLo = 0x1.4ae0c0p-26f, kLn2 = 0x1.62e430p-1f;
+  d = d < -200.0f ? -200.0f : d;
+  const float t = d * kL;
+  const float r = __builtin_fmaf(d, kLo, __builtin_fmaf(d, kL, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e, r * kLn2, e);
+}
+
+struct Shared {
+  u64 mask[kRouteMaxE];
+  int hist[kRouteMaxE];
+  int total[kRouteMaxE];
+  int base[kRouteMaxE];
+  int unused[64];
+  int scan[kWaves];
+  int live, used, unused_base;
+  float sum[kWaves];
+};
+
+// Tokens [t0, t1): choice and weights, counts into sh.hist, live tokens into
+// sh.live, and each wave's sums of probabilities into prob[wave][E] (loss
+// only).  sh.hist and sh.live are zero before, complete after a barrier.
+template <typename T, int PER>
+__device__ void choose(const RouteArgs& a, Shared& sh, float* prob, int t0, int t1) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int E = a.E;
+  float psum[PER] = {};
+  for (int t = t0 + wave; t < t1; t += kWaves) {
+    const T* row = static_cast<const T*>(a.logits) + (int64_t)t * a.ldl;
+    float v[PER];
+    uint32_t key[PER];
+    const bool on = a.mask == nullptr || a.mask[t] != 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = i * 64 + lane;
+      v[i] = on && e < E ? load_logit(row + e) : -__builtin_inff();
+      key[i] = key_of(v[i]);
+    }
+    int idx = -1;                 // lane j: the j-th choice
+    float chosen = 0.0f;
+    float top = 0.0f;
+    bool live = false;
+    for (int j = 0; j < a.k; ++j) {
+      uint32_t m = key[0];
+#pragma unroll
+      for (int i = 1; i < PER; ++i) m = max(m, key[i]);
+      m = wave_max(m);
+      if (m <= kNoKey) break;     // uniform
+      int found = -1;
+#pragma unroll
+      for (int i = PER - 1; i >= 0; --i) {
+        const u64 b = __ballot(key[i] == m);
+        if (b) found = i * 64 + __ffsll(b) - 1;
+      }
+#pragma unroll
+      for (int i = 0; i < PER; ++i) key[i] = found == i * 64 + lane ? 0u : key[i];
+      const float val = of_key(m);
+      if (j == 0) {
+        top = val;
+        live = true;
+      }
+      if (lane == j) {
+        idx = found;
+        chosen = val;
+      }
+    }
+    float ex[PER], s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const bool in = live && i * 64 + lane < E;
+      ex[i] = in ? exp_neg(v[i] - top) : 0.0f;
+      s += ex[i];
+    }
+    s = wave_sum(s);
+    float w = idx >= 0 ? exp_neg(chosen - top) : 0.0f;
+    const float den = a.renorm ? wave_sum(w) + (s - s) : s;     // s - s: a NaN in the row stays
+    if (lane < a.k) {
+      a.index[(int64_t)t * a.k + lane] = idx;
+      a.weight[(int64_t)t * a.k + lane] = idx >= 0 ? w / den : 0.0f;
+      if (idx >= 0) atomicAdd(&sh.hist[idx], 1);
+    }
+    if (live && lane == 0) atomicAdd(&sh.live, 1);
+    if (a.loss != nullptr && live) {
+      const float r = 1.0f / s;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) psum[i] += ex[i] * r;
+    }
+  }
+  if (a.loss != nullptr) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (i * 64 + lane < E) prob[wave * E + i * 64 + lane] = psum[i];
+  }
+}
+
+// Sum of the wave rows of prob for expert e.
+__device__ __forceinline__ float prob_of(const float* prob, int E, int e) {
+  float p = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) p += prob[w * E + e];
+  return p;
+}
+
+// From sh.total: sh.base[e] += the expert's offset; the number of chosen
+// slots into sh.used.  `write`: also counts and offsets to memory.
+__device__ void expert_offsets(const RouteArgs& a, Shared& sh, bool write) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int e = threadIdx.x;
+  const int n = e < a.E ? sh.total[e] : 0;
+  const int incl = wave_scan(n);
+  if (lane == 63) sh.scan[wave] = incl;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    if (w < wave) before += sh.scan[w];
+    all += sh.scan[w];
+  }
+  const int off = before + incl - n;
+  if (e < a.E) {
+    sh.base[e] += off;
+    if (write) {
+      a.counts[e] = n;
+      a.offsets[e] = off;
+    }
+  }
+  if (e == 0) {
+    sh.used = all;
+    if (write) a.offsets[a.E] = all;
+  }
+  __syncthreads();
+}
+
+// loss, prob_sum and live from sh.total, the live tokens and the
+// probabilities' sums (p: thread e's expert).
+__device__ void write_loss(const RouteArgs& a, Shared& sh, float p, int live) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int e = threadIdx.x;
+  const float n = (float)max(live, 1);
+  float c = 0.0f;
+  if (e < a.E) {
+    a.prob_sum[e] = p;
+    c = ((float)sh.total[e] / n) * (p / n);
+  }
+  c = wave_sum(c);
+  if (lane == 0) sh.sum[wave] = c;
+  __syncthreads();
+  if (e == 0) {
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) s += sh.sum[w];
+    a.loss[0] = a.alpha * (float)a.E / (float)a.k * s;
+    a.live[0] = live;
+  }
+}
+
+// Order of the slots of tokens [t0, t1): sh.base holds the position of each
+// expert's next slot, sh.unused_base that of the next slot without one.
+__device__ void place(const RouteArgs& a, Shared& sh, int t0, int t1) {
+  for (int tb = t0; tb < t1; tb += 64) {
+    const int nt = min(t1 - tb, 64);
+    const int slots = nt * a.k;
+    for (int e = threadIdx.x; e < a.E; e += kThreads) sh.mask[e] = 0;
+    __syncthreads();
+    const int32_t* index = a.index + (int64_t)tb * a.k;
+    for (int s = threadIdx.x; s < slots; s += kThreads) {
+      const int e = index[s];
+      if (e >= 0) atomicOr(&sh.mask[e], 1ull << (s / a.k));
+    }
+    if (threadIdx.x < 64) {
+      // slots without an expert before each token
+      int n = 0;
+      if ((int)threadIdx.x < nt)
+        for (int j = 0; j < a.k; ++j) n += index[threadIdx.x * a.k + j] < 0;
+      const int incl = wave_scan(n);
+      sh.unused[threadIdx.x] = sh.unused_base + incl - n;
+      __builtin_amdgcn_wave_barrier();
+      if (threadIdx.x == 63) sh.unused_base += incl;
+    }
+    __syncthreads();
+    for (int s = threadIdx.x; s < slots; s += kThreads) {
+      const int t = s / a.k, e = index[s];
+      int at;
+      if (e >= 0) {
+        at = sh.base[e] + __popcll(sh.mask[e] & ((1ull << t) - 1));
+      } else {
+        // the slots without an expert are a token's last ones
+        at = sh.unused[t];
+        for (int j = s - t * a.k - 1; j >= 0 && index[t * a.k + j] < 0; --j) ++at;
+      }
+      a.order[at] = tb * a.k + s;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += kThreads) sh.base[e] += __popcll(sh.mask[e]);
+    __syncthreads();
+  }
+}
+
+// First launch: one block of tokens per workgroup.  With one block in all,
+// it also writes the rest.
+template <typename T, int PER>
+__global__ void __launch_bounds__(kThreads) route_choose(RouteArgs a) {
+  __shared__ Shared sh;
+  extern __shared__ float prob[];       // [kWaves][E], loss only
+  for (int e = threadIdx.x; e < a.E; e += kThreads) {
+    sh.hist[e] = 0;
+    sh.base[e] = 0;
+  }
+  if (threadIdx.x == 0) sh.live = 0;
+  __syncthreads();
+  const int t0 = blockIdx.x * a.block, t1 = min(a.T, t0 + a.block);
+  choose<T, PER>(a, sh, prob, t0, t1);
+  __syncthreads();
+  const int e = threadIdx.x;
+  if (gridDim.x > 1) {
+    if (e < a.E) {
+      a.hist[(int64_t)blockIdx.x * a.hist_ld + e] = (uint16_t)sh.hist[e];
+      if (a.loss != nullptr) a.prob[(int64_t)blockIdx.x * a.E + e] = prob_of(prob, a.E, e);
+    }
+    if (e == 0) a.hist[(int64_t)blockIdx.x * a.hist_ld + a.E] = (uint16_t)sh.live;
+    return;
+  }
+  if (e < a.E) sh.total[e] = sh.hist[e];
+  __syncthreads();
+  expert_offsets(a, sh, true);
+  if (a.loss != nullptr) write_loss(a, sh, e < a.E ? prob_of(prob, a.E, e) : 0.0f, sh.live);
+  if (e == 0) sh.unused_base = sh.used;
+  __syncthreads();
+  place(a, sh, t0, t1);
+}
+
+// Second launch: workgroups 1.. place one block's slots each; workgroup 0
+// writes counts, offsets and the loss.
+__global__ void __launch_bounds__(kThreads) route_place(RouteArgs a) {
+  __shared__ Shared sh;
+  __shared__ float part[kThreads];
+  const int blocks = gridDim.x - 1;
+  const int me = (int)blockIdx.x - 1;     // -1: counts and loss
+  for (int e = threadIdx.x; e < a.E; e += kThreads) {
+    sh.total[e] = 0;
+    sh.base[e] = 0;
+  }
+  if (threadIdx.x == 0) sh.live = 0;
+  __syncthreads();
+  // column sums of the blocks' counts: 8 experts to a thread, rows shared out
+  const int cols = a.hist_ld / 8;
+  const int rows = kThreads / cols;
+  const int col = threadIdx.x % cols, r0 = threadIdx.x / cols;
+  if (r0 < rows) {
+    int all[8] = {}, mine[8] = {};
+    for (int b = r0; b < blocks; b += rows) {
+      const uint4 v = *reinterpret_cast<const uint4*>(a.hist + (int64_t)b * a.hist_ld + col * 8);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      const uint32_t before = b < me ? 0xFFFFu : 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t c = i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu;
+        all[i] += c;
+        mine[i] += c & before;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = col * 8 + i;
+      if (e < a.E) {
+        atomicAdd(&sh.total[e], all[i]);
+        atomicAdd(&sh.base[e], mine[i]);
+      } else if (e == a.E) {
+        atomicAdd(&sh.live, all[i]);
+      }
+    }
+  }
+  __syncthreads();
+  if (me < 0) {
+    expert_offsets(a, sh, true);
+    if (a.loss == nullptr) return;
+    // the blocks' sums of probabilities: `seg` threads to an expert
+    int width = 64;
+    while (width < a.E) width *= 2;
+    const int seg = kThreads / width, e = threadIdx.x & (width - 1), s0 = threadIdx.x / width;
+    float p = 0.0f;
+    if (e < a.E)
+      for (int b = s0; b < blocks; b += seg) p += a.prob[(int64_t)b * a.E + e];
+    part[threadIdx.x] = p;
+    __syncthreads();
+    p = 0.0f;
+    if ((int)threadIdx.x < a.E)
+      for (int s = 0; s < seg; ++s) p += part[s * width + threadIdx.x];
+    write_loss(a, sh, p, sh.live);
+    return;
+  }
+  // slots without an expert in the blocks before
+  int n = (int)threadIdx.x < a.E ? sh.base[threadIdx.x] : 0;
+  n = wave_scan(n);
+  if ((threadIdx.x & 63) == 63) sh.unused[threadIdx.x >> 6] = n;
+  __syncthreads();
+  int used_before = 0;
+  for (int w = 0; w < kWaves; ++w) used_before += sh.unused[w];
+  __syncthreads();
+  expert_offsets(a, sh, false);
+  const int t0 = me * a.block, t1 = min(a.T, t0 + a.block);
+  if (threadIdx.x == 0) sh.unused_base = sh.used + t0 * a.k - used_before;
+  __syncthreads();
+  place(a, sh, t0, t1);
+}
+
+// Gradient of the logits, one wave per token:
+//   d_e = p_e (c_e - sum p c) + [plain] p_e (g_e - sum_j w_j dw_j)
+//       + [renormalised] w_j (dw_j - sum w dw) at e = index[j],
+// c_e = dloss * alpha * E * counts_e / (k L^2), g_e = dw_j at e = index[j].
+template <typename T, int PER>
+__global__ void __launch_bounds__(256) route_backward(RouteBackArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int E = a.E;
+  float c[PER];
+  {
+    float f = 0.0f;
+    if (a.dloss != nullptr) {
+      const float n = (float)max(a.live[0], 1);
+      f = a.dloss[0] * (a.alpha * (float)E / (float)a.k) / n / n;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = i * 64 + lane;
+      c[i] = a.dloss != nullptr && e < E ? f * (float)a.counts[e] : 0.0f;
+    }
+  }
+  const int waves = gridDim.x * 4;
+  for (int t = blockIdx.x * 4 + (threadIdx.x >> 6); t < a.T; t += waves) {
+    const T* row = static_cast<const T*>(a.logits) + (int64_t)t * a.ldl;
+    T* out = static_cast<T*>(a.dlogits) + (int64_t)t * a.ldd;
+    const bool on = a.mask == nullptr || a.mask[t] != 0;
+    int idx = -1;
+    float w = 0.0f, dw = 0.0f;
+    if (lane < a.k) {
+      idx = a.index[(int64_t)t * a.k + lane];
+      if (idx >= E) idx = -1;
+      if (a.dweight != nullptr && idx >= 0) {
+        w = a.weight[(int64_t)t * a.k + lane];
+        dw = a.dweight[(int64_t)t * a.k + lane];
+      }
+    }
+    const bool live = on && __builtin_amdgcn_readlane(idx, 0) >= 0;
+    if (!live) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (i * 64 + lane < E) store_grad(out + i * 64 + lane, 0.0f);
+      continue;
+    }
+    float v[PER];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = i * 64 + lane;
+      v[i] = e < E ? load_logit(row + e) : -__builtin_inff();
+      m = max(m, key_of(v[i]));
+    }
+    const float top = of_key(wave_max(m));
+    float s = 0.0f, pc = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      v[i] = i * 64 + lane < E ? exp_neg(v[i] - top) : 0.0f;
+      s += v[i];
+      pc += v[i] * c[i];
+    }
+    s = wave_sum(s);
+    const float r = 1.0f / s;
+    const float dot = wave_sum(w * dw);
+    const float sub = wave_sum(pc) * r + (a.renorm ? 0.0f : dot);
+    float d[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) d[i] = v[i] * r * (c[i] - sub);
+    const float add = w * (a.renorm ? dw - dot : dw);
+    if (a.dweight != nullptr) {
+      for (int j = 0; j < a.k; ++j) {
+        const int e = __builtin_amdgcn_readlane(idx, j);
+        const float g = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(add), j));
+#pragma unroll
+        for (int i = 0; i < PER; ++i) d[i] += e == i * 64 + lane ? g : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (i * 64 + lane < E) store_grad(out + i * 64 + lane, d[i]);
+  }
+}
+
+template <typename T>
+void launch_choose(const RouteArgs& a, int blocks, hipStream_t st) {
+  const size_t lds = a.loss != nullptr ? (size_t)kWaves * a.E * 4 : 0;
+  const dim3 g(blocks), b(kThreads);
+  if (a.E <= 64) hipLaunchKernelGGL((route_choose<T, 1>), g, b, lds, st, a);
+  else if (a.E <= 128) hipLaunchKernelGGL((route_choose<T, 2>), g, b, lds, st, a);
+  else if (a.E <= 256) hipLaunchKernelGGL((route_choose<T, 4>), g, b, lds, st, a);
+  else if (a.E <= 512) hipLaunchKernelGGL((route_choose<T, 8>), g, b, lds, st, a);
+  else hipLaunchKernelGGL((route_choose<T, 16>), g, b, lds, st, a);
+}
+
+template <typename T>
+void launch_backward(const RouteBackArgs& a, hipStream_t st) {
+  const int blocks = (a.T + 3) / 4 < 4096 ? (a.T + 3) / 4 : 4096;
+  const dim3 g(blocks), b(256);
+  if (a.E <= 64) hipLaunchKernelGGL((route_backward<T, 1>), g, b, 0, st, a);
+  else if (a.E <= 128) hipLaunchKernelGGL((route_backward<T, 2>), g, b, 0, st, a);
+  else if (a.E <= 256) hipLaunchKernelGGL((route_backward<T, 4>), g, b, 0, st, a);
+  else if (a.E <= 512) hipLaunchKernelGGL((route_backward<T, 8>), g, b, 0, st, a);
+  else hipLaunchKernelGGL((route_backward<T, 16>), g, b, 0, st, a);
+}
+
+}  // namespace
+
+int launch_route(const RouteArgs& a, int blocks, void* stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (a.dtype == BSMM_BF16) launch_choose<uint16_t>(a, blocks, st);
+  else launch_choose<float>(a, blocks, st);
+  if (blocks > 1) hipLaunchKernelGGL(route_place, dim3(blocks + 1), dim3(kThreads), 0, st, a);
+  return hipGetLastError() == hipSuccess ? 0 : 1;
+}
+
+int launch_route_backward(const RouteBackArgs& a, void* stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (a.dtype == BSMM_BF16) launch_backward<uint16_t>(a, st);
+  else launch_backward<float>(a, st);
+  return hipGetLastError() == hipSuccess ? 0 : 1;
+}
+
+}  // namespace bsmm

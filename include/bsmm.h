@@ -495,6 +495,58 @@ bsmm_status bsmm_w4_expert_mm(const void* x, int64_t ldx, bsmm_dtype x_dtype, co
                               int64_t S, int64_t N, int64_t K, void* workspace,
                               size_t workspace_bytes, void* stream);
 
+/*
+ * The router of a mixture-of-experts layer: every token's k experts, their
+ * weights, the experts' loads, the slots sorted by expert and, for training,
+ * the balance loss.  logits [T, E] (fp32 or bf16, row stride ldl elements);
+ * mask NULL or T bytes, 0 for tokens to leave out (padding).
+ *   index(t, j)   the expert of the j-th largest logit; equal logits in order
+ *                 of their experts; -inf and NaN are never chosen; -1 where
+ *                 nothing is left or the token is masked
+ *   p = softmax(logits(t, :))
+ *   weight(t, j)  p(index), with renorm p(index) / sum_j p(index); 0 where -1
+ *   counts(e)     slots (t, j) with index e;  slot number t*k + j
+ *   offsets(e)    sum of counts before e, e = 0 .. E
+ *   order         all T*k slots sorted by expert, ascending within one; the
+ *                 slots without an expert at the end, from offsets(E) on
+ *   live          L, the tokens with at least one expert
+ *   prob_sum(e)   sum of p(t, e) over those
+ *   loss          alpha * E / (k L^2) * sum_e counts(e) * prob_sum(e); 0 if L = 0
+ * live, prob_sum and loss are given together or all NULL (serving).  A NaN or
+ * +inf in a live row makes that row's weights, and the sums, NaN, as softmax
+ * does.  Sums are fp32 in a fixed order: equal inputs give equal bits.
+ *   E 1 to 1024, k 1 to 32 and at most E, T up to 2^23.  index and weight are
+ *   [T, k], order [T*k], contiguous.  T == 0 writes zero counts and offsets.
+ *   The workspace must hold bsmm_route_workspace_bytes(T, E) bytes, 16-byte
+ *   aligned (BSMM_ERR_ARG otherwise); no clearing is needed.
+ */
+size_t bsmm_route_workspace_bytes(int64_t T, int64_t E);
+bsmm_status bsmm_route_topk(const void* logits, int64_t ldl, bsmm_dtype dtype,
+                            const uint8_t* mask, int k, int renorm, float alpha, int32_t* index,
+                            float* weight, int32_t* counts, int32_t* offsets, int32_t* order,
+                            int32_t* live, float* prob_sum, float* loss, int64_t T, int64_t E,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of bsmm_route_topk: dlogits [T, E] (the logits' type, row stride
+ * ldd) from dweight [T, k] (NULL: none) and dloss, one fp32 (NULL: none),
+ * with the forward call's logits, mask, index, weight, counts, live, alpha and
+ * renorm.  The choice and the counts are constants of the derivative:
+ *   c_e = dloss * alpha * E * counts(e) / (k L^2)
+ *   dlogit_e = p_e (c_e - sum p c)
+ *            + [plain]   p_e (g_e - sum_j w_j dw_j),  g_e = dw_j at e = index(j)
+ *            + [renorm]  w_j (dw_j - sum_j w_j dw_j)  at e = index(j)
+ * Rows that are masked or have no expert get zeros.  counts and live may be
+ * sums over several calls (data-parallel training) where the loss is theirs.
+ * Entries of index outside [0, E) count as -1.
+ */
+bsmm_status bsmm_route_topk_backward(const void* logits, int64_t ldl, bsmm_dtype dtype,
+                                     const uint8_t* mask, const int32_t* index,
+                                     const float* weight, const int32_t* counts,
+                                     const int32_t* live, int k, int renorm, float alpha,
+                                     const float* dweight, const float* dloss, void* dlogits,
+                                     int64_t ldd, int64_t T, int64_t E, void* stream);
+
 /* Workspace bytes the fastest plan for this problem wants (0 if none). */
 size_t bsmm_workspace_bytes(bsmm_op op, int64_t G, int64_t M, int64_t N,
                             int64_t K, bsmm_dtype out_dtype);
