@@ -106,6 +106,8 @@ def load():
     L.bsmm_w4_expert_mm.argtypes = [vp, i64, st, vp, i64, i64, vp, i64, i64, st, vp, i64, i64, st,
                                     vp, vp, st, vp, vp, i64, st, i64, i64, i64, i64, i64, vp, sz,
                                     vp]
+    L.bsmm_w4_workspace_bytes.argtypes = [st, i64, i64, i64, i64]
+    L.bsmm_w4_workspace_bytes.restype = sz
     L.bsmm_route_workspace_bytes.argtypes = [i64, i64]
     L.bsmm_route_workspace_bytes.restype = sz
     L.bsmm_route_topk.argtypes = [vp, i64, st, vp, st, st, ctypes.c_float, vp, vp, vp, vp, vp, vp,
@@ -850,6 +852,14 @@ def _w4_weight(w, scale, zero, lead, K):
     return (K // KG if K else 32), code
 
 
+def _w4_workspace(xc, E, R, S, K, dev, stream, handle):
+    """Workspace pointer and bytes of a 4-bit product (fp32 x, many rows)."""
+    if xc != F32:
+        return None, 0
+    buf, n = _buffer(load().bsmm_w4_workspace_bytes(xc, E, R, S, K), dev, stream, handle)
+    return (buf.data_ptr(), n) if n else (None, 0)
+
+
 def bsmm_w4_mm(x, w, scale, zero=None, *, out_dtype="bf16", out=None, stream=None):
     """Activations times a 4-bit weight: x @ W.T with W = (code - zero) * scale.
 
@@ -869,11 +879,13 @@ def bsmm_w4_mm(x, w, scale, zero=None, *, out_dtype="bf16", out=None, stream=Non
     o = _out(out, (M, N), code, x.device)
     if N and o.stride(1) != 1:
         raise ValueError("out must be contiguous along N")
+    hs = _stream(stream)
+    wsp, wsn = _w4_workspace(xc, 1, M, M, K, x.device, stream, hs)
     _check(load().bsmm_w4_mm(
         x.data_ptr(), x.stride(0), xc, w.data_ptr(), w.stride(0), scale.data_ptr(),
         scale.stride(0), sc, None if zero is None else zero.data_ptr(),
         0 if zero is None else zero.stride(0), group, o.data_ptr(), o.stride(0), code, M, N, K,
-        None, 0, _stream(stream)))
+        wsp, wsn, hs))
     return o
 
 
@@ -911,13 +923,15 @@ def bsmm_w4_expert_mm(x, w, scale, zero, order, offsets, *, slots_per_row=1, row
     o = _out(out, (S, N), code, x.device)
     if N and o.stride(1) != 1:
         raise ValueError("out must be contiguous along N")
+    hs = _stream(stream)
+    wsp, wsn = _w4_workspace(xc, E, R, S, K, x.device, stream, hs)
     _check(load().bsmm_w4_expert_mm(
         x.data_ptr(), x.stride(0), xc, w.data_ptr(), w.stride(0), w.stride(1), scale.data_ptr(),
         scale.stride(0), scale.stride(1), sc, None if zero is None else zero.data_ptr(),
         0 if zero is None else zero.stride(0), 0 if zero is None else zero.stride(1), group,
         order.data_ptr(), offsets.data_ptr(), slots_per_row,
         None if row_scale is None else row_scale.data_ptr(), o.data_ptr(), o.stride(0), code,
-        E, R, S, N, K, None, 0, _stream(stream)))
+        E, R, S, N, K, wsp, wsn, hs))
     return o
 
 

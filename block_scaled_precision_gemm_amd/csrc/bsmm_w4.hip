@@ -325,6 +325,330 @@ __global__ void __launch_bounds__(NW * 64) w4_rows_kernel(W4Args a, int ntn) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// Many rows: tiles of BM = 64 * WM rows by BN = 64 * WN columns, a wave to
+// each 64 x 64 (2 x 2 blocks of 32 x 32 x 16 instructions), K in steps of 64.
+//
+// The x tile goes global -> LDS directly into a ring of three slots, two
+// steps ahead.  The weight tile is held in LDS as bf16 integers code - zero
+// (exact), in two slots: each thread keeps the codes of one column's run two
+// steps ahead in registers and unpacks the next step's while this step's
+// matrix instructions run, so that a code is unpacked once per workgroup and
+// not once per wave.  A group's sum is then folded into the accumulator with
+// one multiply-add by the lane's column scale.
+//
+// LDS rows are 128 bytes (64 bf16) with the 16-byte chunks XOR-swizzled, so
+// that the 16 consecutive rows of a fragment read hit distinct banks.
+// ---------------------------------------------------------------------------
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+constexpr int kStepK = 64;
+
+__device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+__device__ __forceinline__ int lds_off(int r, int c) { return (r << 7) + ((c ^ swz(r)) << 4); }
+
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void wait_lgkm0() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+}
+__device__ __forceinline__ void barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// 8 codes of a dword -> code - z as bf16, in order (integers of 5 bits: the
+// upper halves of their fp32 forms)
+__device__ __forceinline__ u32x4 unpack_signed(uint32_t w, float z) {
+  const uint32_t e = w & 0x0F0F0F0Fu, o = (w >> 4) & 0x0F0F0F0Fu;
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = (float)((e >> (8 * i)) & 0xFFu) - z, b = (float)((o >> (8 * i)) & 0xFFu) - z;
+    r[i] = hi2(__float_as_uint(a), __float_as_uint(b));
+  }
+  return r;
+}
+
+// Logical workgroup ids: contiguous runs per XCD (hardware ids go round robin
+// over 8), then groups of 8 row blocks by all column blocks, so that the
+// workgroups an XCD holds at a time share x rows and weight columns in its L2.
+__device__ __forceinline__ void tile_of(int items, int ntn, int& item, int& tn) {
+  const int total = gridDim.x, hw = blockIdx.x;
+  const int per = total >> 3, rem = total & 7, xcd = hw & 7, local = hw >> 3;
+  const int id = xcd < rem ? xcd * (per + 1) + local : rem * (per + 1) + (xcd - rem) * per + local;
+  const int width = 8 * ntn, g = id / width, first = 8 * g, n = min(items - first, 8);
+  const int in = id - g * width;
+  item = first + in % n;
+  tn = in / n;
+}
+
+struct TileArgs {
+  const uint16_t* x;      // bf16 planes [planes][R][ldx]
+  int64_t ldx;
+  uint32_t plane;         // bytes from one plane to the next
+  int planes;
+  uint32_t x_bytes;       // of all planes, below 2^32
+  int items, ntn;
+};
+
+template <int G, int WM, int WN, bool ROUTED>
+__global__ void __launch_bounds__(WM * WN * 64, 2) w4_tile_kernel(W4Args a, TileArgs ta) {
+  constexpr int NW = WM * WN, NT = NW * 64;
+  constexpr int BM = 64 * WM, BN = 64 * WN;
+  constexpr int XS = BM * 128, BS = BN * 128;       // bytes of a slot
+  constexpr int LA = BM / 8 / NW;                   // x loads per wave and step
+  constexpr int CB = BN * 32 / NT;                  // code bytes per thread and step (8 or 16)
+  constexpr int CW = CB / 4;
+  constexpr int NG = G < 64 ? 64 / G : 1;           // scale groups in a step
+  static_assert(CB == 8 || CB == 16, "one wide load of codes per thread");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[3 * XS + 2 * BS];
+  uint8_t* const xs = smem;
+  uint8_t* const bs = smem + 3 * XS;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wm = wave / WN, wn = wave % WN;
+  const int c32 = lane & 31, half = lane >> 5;
+  int item, tn;
+  tile_of(ta.items, ta.ntn, item, tn);
+  Item it;
+  if (ROUTED) {
+    it = find_item(a.offsets, a.E, a.S, BM, item);
+    const int used = min(max(a.offsets[a.E], 0), a.S);
+    for (int p = used + item; p < a.S; p += ta.items) {     // slots of no expert
+      const int slot = a.order[p];
+      if (slot < 0 || slot >= a.S) continue;
+      for (int i = threadIdx.x; i < BN; i += NT)
+        if (tn * BN + i < a.N) store_out(a, slot * a.ldo + tn * BN + i, 0.0f);
+    }
+    if (it.rows == 0) return;
+  } else {
+    it = Item{0, item * BM, min(a.S - item * BM, BM)};
+  }
+
+  // x: wave instruction t brings rows 8 (t NW + wave) + lane / 8 of the tile;
+  // rows past the end repeat the first
+  uint32_t xo[LA];
+#pragma unroll
+  for (int t = 0; t < LA; ++t) {
+    const int r = (t * NW + wave) * 8 + (lane >> 3);
+    int64_t row = it.p0 + (r < it.rows ? r : 0);
+    if (ROUTED) row = min(max(a.order[row] / a.x_div, 0), a.R - 1);
+    xo[t] = (uint32_t)(row * ta.ldx * 2) + (((lane & 7) ^ swz(r)) << 4);
+  }
+  const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint16_t*>(ta.x), (short)0, (int)ta.x_bytes, 0x00020000);
+
+  // codes: this thread's column and its run of CB bytes of every step
+  const int bc = threadIdx.x / (32 / CB), part = threadIdx.x % (32 / CB);
+  const int64_t bn = min(tn * BN + bc, a.N - 1);
+  const uint8_t* wp = a.w + it.e * a.w_se + bn * a.ldw;
+  const uint8_t* zp = a.zero ? a.zero + it.e * a.z_se + bn * a.z_n : nullptr;
+  int64_t sp[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    sp[j] = it.e * a.s_se + (int64_t)min(tn * BN + wn * 64 + j * 32 + c32, a.N - 1) * a.s_n;
+
+  const int K = a.K, KG = K / G;
+  const int steps1 = (K + kStepK - 1) / kStepK;       // per plane
+  const int steps = steps1 * ta.planes;
+  struct Codes { uint32_t w[CW]; float z; };
+  struct Scales { float s[NG][2]; };
+
+  // K step within its plane; the plane's byte offset
+  auto k_step = [&](int s) { return s % steps1; };
+  auto load_x = [&](int s) {
+    const int slot = s % 3;
+    const uint32_t so = (uint32_t)(s / steps1) * ta.plane + (uint32_t)k_step(s) * (kStepK * 2);
+    // the missing half of a half step repeats the first (never read): no
+    // load reaches past its row
+    const bool tail = G == 32 && (k_step(s) + 1) * kStepK > K;
+    const uint32_t back = tail && (((lane & 7) ^ (lane >> 3)) & 4) ? 64u : 0u;
+#pragma unroll
+    for (int t = 0; t < LA; ++t) {
+      const lds_ptr_t l =
+          (lds_ptr_t)(uintptr_t)(uint32_t)(uintptr_t)(xs + slot * XS + (t * NW + wave) * 1024);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, l, 16, (int)(xo[t] - back), (int)so, 0, 0);
+    }
+  };
+  auto load_codes = [&](Codes& c, int s) {
+    const int ks = k_step(s);
+    int at = ks * 32 + part * CB;
+    if (at + CB > K / 2) at = 0;                       // past a half step: not used
+    if constexpr (CB == 16) {
+      const u32x4 v = *reinterpret_cast<const u32x4*>(wp + at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c.w[i] = v[i];
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(wp + at);
+      c.w[0] = v.x;
+      c.w[1] = v.y;
+    }
+    c.z = zp ? (float)zp[at * 2 / G] : 8.0f;
+  };
+  auto load_scales = [&](Scales& c, int s) {
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const int i = min(k_step(s) * kStepK / G + g, KG - 1);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        c.s[g][j] = a.s_bf16
+                        ? __uint_as_float(
+                              (uint32_t)static_cast<const uint16_t*>(a.scale)[sp[j] + i] << 16)
+                        : static_cast<const float*>(a.scale)[sp[j] + i];
+    }
+  };
+  auto write_codes = [&](const Codes& c, int s) {
+    uint8_t* slot = bs + (s & 1) * BS;
+#pragma unroll
+    for (int i = 0; i < CW; ++i)
+      *reinterpret_cast<u32x4*>(slot + lds_off(bc, part * CW + i)) = unpack_signed(c.w[i], c.z);
+  };
+
+  f32x16 acc[2][2] = {}, d[2][2];
+  auto compute = [&](const Scales& c, int s) {
+    const uint8_t* xt = xs + (s % 3) * XS + wm * 64 * 128;
+    const uint8_t* bt = bs + (s & 1) * BS + wn * 64 * 128;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      if (G == 32 && t == 2 && k_step(s) * kStepK + 32 >= K) break;     // half step
+      u32x4 af[2], bf[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        af[i] = *reinterpret_cast<const u32x4*>(xt + lds_off(32 * i + c32, 2 * t + half));
+        bf[i] = *reinterpret_cast<const u32x4*>(bt + lds_off(32 * i + c32, 2 * t + half));
+      }
+      const bool first = G == 128 ? (s & 1) == 0 && t == 0 : t * 16 % G == 0;
+      const bool last = G == 128 ? (s & 1) == 1 && t == 3 : (t + 1) * 16 % G == 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          d[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              __builtin_bit_cast(bf16x8, af[i]), __builtin_bit_cast(bf16x8, bf[j]),
+              first ? f32x16{} : d[i][j], 0, 0, 0);
+      if (last) {
+        const int g = G < 64 ? t * 16 / G : 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              acc[i][j][r] = __builtin_fmaf(c.s[g][j], d[i][j][r], acc[i][j][r]);
+      }
+    }
+  };
+
+  // prologue: x of steps 0 and 1, codes of 0 (unpacked), 1; scales of 0
+  Codes c0, c1;
+  Scales s0, s1;
+  load_codes(c0, 0);
+  load_scales(s0, 0);
+  load_x(0);
+  if (steps > 1) {
+    load_codes(c1, 1);
+    load_x(1);
+  }
+  write_codes(c0, 0);
+  auto step = [&](int s, Codes& next, Codes& after, Scales& now, Scales& later) {
+    // this step's x slot: this wave's loads have landed, then everyone's
+    if (s + 1 < steps) wait_vmcnt<LA>(); else wait_vmcnt<0>();
+    wait_lgkm0();
+    barrier();
+    if (s + 2 < steps) load_codes(after, s + 2);
+    if (s + 1 < steps) load_scales(later, s + 1);
+    if (s + 2 < steps) load_x(s + 2);
+    compute(now, s);
+    if (s + 1 < steps) write_codes(next, s + 1);
+  };
+  for (int s = 0; s < steps; s += 2) {
+    step(s, c1, c0, s0, s1);
+    if (s + 1 >= steps) break;
+    step(s + 1, c0, c1, s1, s0);
+  }
+
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int m = wm * 64 + i * 32 + (r >> 2) * 8 + half * 4 + (r & 3);
+      if (m >= it.rows) continue;
+      int64_t row = it.p0 + m;
+      float rsc = 1.0f;
+      if (ROUTED) {
+        row = a.order[row];
+        if (row < 0 || row >= a.S) continue;
+        if (a.row_scale) rsc = a.row_scale[row];
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int n = tn * BN + wn * 64 + j * 32 + c32;
+        if (n < a.N) store_out(a, row * a.ldo + n, acc[i][j][r] * rsc);
+      }
+    }
+}
+
+// fp32 activations as three bf16 planes that add up to them exactly
+__global__ void __launch_bounds__(256) split_planes(const float* __restrict__ x, int64_t ldx,
+                                                    uint16_t* __restrict__ planes, int64_t plane,
+                                                    int K, int64_t chunks) {
+  const int per_row = K / 8;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < chunks;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / per_row;
+    const int k = (int)(i - row * per_row) * 8;
+    const u32x4* src = reinterpret_cast<const u32x4*>(x + row * ldx + k);
+    u32x4 u = src[0], v = src[1];
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      *reinterpret_cast<u32x4*>(planes + p * plane + row * K + k) =
+          u32x4{hi2(u.x, u.y), hi2(u.z, u.w), hi2(v.x, v.y), hi2(v.z, v.w)};
+      if (p < 2) {
+        u = u32x4{below(u.x), below(u.y), below(u.z), below(u.w)};
+        v = u32x4{below(v.x), below(v.y), below(v.z), below(v.w)};
+      }
+    }
+  }
+}
+
+template <int G, int WM, int WN>
+void launch_tiles(const W4Args& a, void* ws, hipStream_t st) {
+  constexpr int BM = 64 * WM, BN = 64 * WN;
+  TileArgs t{};
+  t.ntn = (a.N + BN - 1) / BN;
+  if (a.x_dtype == BSMM_F32) {
+    uint16_t* planes = static_cast<uint16_t*>(ws);
+    const int64_t chunks = (int64_t)a.R * (a.K / 8);
+    const int64_t blocks = (chunks + 255) / 256;
+    hipLaunchKernelGGL(split_planes, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256),
+                       0, st, static_cast<const float*>(a.x), a.ldx, planes,
+                       (int64_t)a.R * a.K, a.K, chunks);
+    t.x = planes;
+    t.ldx = a.K;
+    t.planes = 3;
+    t.plane = (uint32_t)((int64_t)a.R * a.K * 2);
+    t.x_bytes = 3 * t.plane;
+  } else {
+    t.x = static_cast<const uint16_t*>(a.x);
+    t.ldx = a.ldx;
+    t.planes = 1;
+    t.x_bytes = (uint32_t)(((int64_t)(a.R - 1) * a.ldx + a.K) * 2);
+  }
+  if (a.offsets) {
+    t.items = (int)(((int64_t)a.S + (int64_t)(a.E < a.S ? a.E : a.S) * (BM - 1)) / BM);
+    hipLaunchKernelGGL((w4_tile_kernel<G, WM, WN, true>), dim3((unsigned)(t.items * t.ntn)),
+                       dim3(WM * WN * 64), 0, st, a, t);
+  } else {
+    t.items = (a.S + BM - 1) / BM;
+    hipLaunchKernelGGL((w4_tile_kernel<G, WM, WN, false>), dim3((unsigned)(t.items * t.ntn)),
+                       dim3(WM * WN * 64), 0, st, a, t);
+  }
+}
+
 template <bool XF32, int G, int MT, int NT, int NW>
 void launch_rows(const W4Args& a, hipStream_t st) {
   constexpr int BM = 16 * MT, BN = 16 * NT;
@@ -341,26 +665,29 @@ void launch_rows(const W4Args& a, hipStream_t st) {
   }
 }
 
-template <bool XF32, int G>
-void launch_group(const W4Args& a, hipStream_t st) {
-  const int64_t rows = a.offsets ? (a.S + a.E - 1) / a.E : a.S;
-  if (rows <= 16) launch_rows<XF32, G, 1, 1, 8>(a, st);
-  else launch_rows<XF32, G, 2, 1, 8>(a, st);
-}
-
-template <bool XF32>
-void launch_x(const W4Args& a, hipStream_t st) {
-  if (a.group == 32) launch_group<XF32, 32>(a, st);
-  else if (a.group == 64) launch_group<XF32, 64>(a, st);
-  else launch_group<XF32, 128>(a, st);
+template <int G>
+void launch_group(const W4Args& a, void* ws, hipStream_t st) {
+  if (w4_tiled(a) && (a.x_dtype != BSMM_F32 || ws != nullptr)) {
+    launch_tiles<G, 4, 2>(a, ws, st);
+    return;
+  }
+  const bool many = (a.offsets ? (a.S + a.E - 1) / a.E : a.S) > 16;
+  if (a.x_dtype == BSMM_F32) {
+    if (many) launch_rows<true, G, 2, 1, 8>(a, st);
+    else launch_rows<true, G, 1, 1, 8>(a, st);
+  } else {
+    if (many) launch_rows<false, G, 2, 1, 8>(a, st);
+    else launch_rows<false, G, 1, 1, 8>(a, st);
+  }
 }
 
 }  // namespace
 
-int launch_w4(const W4Args& a, void* stream) {
+int launch_w4(const W4Args& a, void* ws, void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (a.x_dtype == BSMM_F32) launch_x<true>(a, st);
-  else launch_x<false>(a, st);
+  if (a.group == 32) launch_group<32>(a, ws, st);
+  else if (a.group == 64) launch_group<64>(a, ws, st);
+  else launch_group<128>(a, ws, st);
   return hipGetLastError() == hipSuccess ? 0 : 1;
 }
 

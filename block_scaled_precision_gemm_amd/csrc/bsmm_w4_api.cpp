@@ -52,11 +52,11 @@ bsmm_status check_operands(const W4Args& a) {
 }
 
 bsmm_status run(const W4Args& a, void* workspace, size_t workspace_bytes, void* stream) {
-  (void)workspace;
-  (void)workspace_bytes;
   const bsmm_status st = check_operands(a);
   if (st != BSMM_OK) return st;
-  if (launch_w4(a, stream) != 0) return fail(BSMM_ERR_HIP, "kernel launch failed (w4)");
+  if (workspace == nullptr || workspace_bytes < w4_plane_bytes(a) || !aligned(workspace, 16))
+    workspace = nullptr;
+  if (launch_w4(a, workspace, stream) != 0) return fail(BSMM_ERR_HIP, "kernel launch failed (w4)");
   return BSMM_OK;
 }
 
@@ -98,6 +98,19 @@ bsmm_status bsmm_quant_w4(const void* w, int64_t ldw, bsmm_dtype w_dtype, uint8_
                 R, K};
   if (launch_quant_w4(a, stream) != 0) return fail(BSMM_ERR_HIP, "quantiser launch failed");
   return BSMM_OK;
+}
+
+size_t bsmm_w4_workspace_bytes(bsmm_dtype x_dtype, int64_t E, int64_t R, int64_t S, int64_t K) {
+  if (E <= 0 || R <= 0 || S <= 0 || K <= 0 || E > 1024 || R >= kMaxDim || S >= kMaxDim ||
+      K >= kMaxDim)
+    return 0;
+  W4Args a{};
+  a.x_dtype = x_dtype;
+  a.E = (int)E; a.R = (int)R; a.S = (int)S; a.K = (int)K;
+  a.ldx = K;
+  static const int32_t routed = 0;
+  a.offsets = E > 1 || R != S ? &routed : nullptr;
+  return w4_tiled(a) ? w4_plane_bytes(a) : 0;
 }
 
 bsmm_status bsmm_w4_mm(const void* x, int64_t ldx, bsmm_dtype x_dtype, const uint8_t* w,
