@@ -18,6 +18,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "bsmm_internal.h"
 
@@ -396,7 +397,7 @@ struct TileArgs {
   int items, ntn;
 };
 
-template <int G, int WM, int WN, bool ROUTED>
+template <int G, bool S16, int WM, int WN, bool ROUTED>
 __global__ void __launch_bounds__(WM * WN * 64, 2) w4_tile_kernel(W4Args a, TileArgs ta) {
   constexpr int NW = WM * WN, NT = NW * 64;
   constexpr int BM = 64 * WM, BN = 64 * WN;
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) w4_tile_kernel(W4Args a, Tile
   __shared__ __attribute__((aligned(1024))) uint8_t smem[3 * XS + 2 * BS];
   uint8_t* const xs = smem;
   uint8_t* const bs = smem + 3 * XS;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm = wave / WN, wn = wave % WN;
   const int c32 = lane & 31, half = lane >> 5;
   int item, tn;
@@ -446,38 +447,47 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) w4_tile_kernel(W4Args a, Tile
   const int bc = threadIdx.x / (32 / CB), part = threadIdx.x % (32 / CB);
   const int64_t bn = min(tn * BN + bc, a.N - 1);
   const uint8_t* wp = a.w + it.e * a.w_se + bn * a.ldw;
-  const uint8_t* zp = a.zero ? a.zero + it.e * a.z_se + bn * a.z_n : nullptr;
-  int64_t sp[2];
+  // without zero points the byte that is read (a scale's) is not used
+  const uint8_t* zp = a.zero ? a.zero + it.e * a.z_se + bn * a.z_n
+                             : static_cast<const uint8_t*>(a.scale);
+  using scale_t = std::conditional_t<S16, uint16_t, uint32_t>;
+  const scale_t* sp[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j)
-    sp[j] = it.e * a.s_se + (int64_t)min(tn * BN + wn * 64 + j * 32 + c32, a.N - 1) * a.s_n;
+    sp[j] = static_cast<const scale_t*>(a.scale) + it.e * a.s_se +
+            (int64_t)min(tn * BN + wn * 64 + j * 32 + c32, a.N - 1) * a.s_n;
 
   const int K = a.K, KG = K / G;
   const int steps1 = (K + kStepK - 1) / kStepK;       // per plane
   const int steps = steps1 * ta.planes;
-  struct Codes { uint32_t w[CW]; float z; };
-  struct Scales { float s[NG][2]; };
+  struct Codes { uint32_t w[CW]; uint8_t z; };
+  struct Scales { scale_t s[NG][2]; };
+  // A step: its K step within the plane, its byte offset in x
+  struct Pos {
+    int ks;
+    uint32_t off;
+  };
+  auto next_pos = [&](Pos p) {
+    const bool wrap = p.ks + 1 == steps1;
+    return Pos{wrap ? 0 : p.ks + 1,
+               p.off + (wrap ? ta.plane - (uint32_t)(steps1 - 1) * (kStepK * 2) : kStepK * 2)};
+  };
 
-  // K step within its plane; the plane's byte offset
-  auto k_step = [&](int s) { return s % steps1; };
-  auto load_x = [&](int s) {
-    const int slot = s % 3;
-    const uint32_t so = (uint32_t)(s / steps1) * ta.plane + (uint32_t)k_step(s) * (kStepK * 2);
+  auto load_x = [&](Pos p, uint32_t slot) {
     // the missing half of a half step repeats the first (never read): no
     // load reaches past its row
-    const bool tail = G == 32 && (k_step(s) + 1) * kStepK > K;
+    const bool tail = G == 32 && (p.ks + 1) * kStepK > K;
     const uint32_t back = tail && (((lane & 7) ^ (lane >> 3)) & 4) ? 64u : 0u;
 #pragma unroll
     for (int t = 0; t < LA; ++t) {
       const lds_ptr_t l =
-          (lds_ptr_t)(uintptr_t)(uint32_t)(uintptr_t)(xs + slot * XS + (t * NW + wave) * 1024);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, l, 16, (int)(xo[t] - back), (int)so, 0, 0);
+          (lds_ptr_t)(uintptr_t)(uint32_t)(uintptr_t)(xs + slot + (t * NW + wave) * 1024);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, l, 16, (int)(xo[t] - back), (int)p.off, 0, 0);
     }
   };
-  auto load_codes = [&](Codes& c, int s) {
-    const int ks = k_step(s);
-    int at = ks * 32 + part * CB;
-    if (at + CB > K / 2) at = 0;                       // past a half step: not used
+  auto load_codes = [&](Codes& c, Pos p) {
+    int at = p.ks * 32 + part * CB;
+    if (G == 32 && at + CB > K / 2) at = 0;            // past a half step: not used
     if constexpr (CB == 16) {
       const u32x4 v = *reinterpret_cast<const u32x4*>(wp + at);
 #pragma unroll
@@ -487,88 +497,110 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) w4_tile_kernel(W4Args a, Tile
       c.w[0] = v.x;
       c.w[1] = v.y;
     }
-    c.z = zp ? (float)zp[at * 2 / G] : 8.0f;
+    c.z = zp[at * 2 / G];
   };
-  auto load_scales = [&](Scales& c, int s) {
+  auto load_scales = [&](Scales& c, Pos p) {
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      const int i = min(k_step(s) * kStepK / G + g, KG - 1);
+      const int i = G == 32 ? min(p.ks * 2 + g, KG - 1) : p.ks * kStepK / G;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        c.s[g][j] = a.s_bf16
-                        ? __uint_as_float(
-                              (uint32_t)static_cast<const uint16_t*>(a.scale)[sp[j] + i] << 16)
-                        : static_cast<const float*>(a.scale)[sp[j] + i];
+      for (int j = 0; j < 2; ++j) c.s[g][j] = sp[j][i];
     }
   };
-  auto write_codes = [&](const Codes& c, int s) {
-    uint8_t* slot = bs + (s & 1) * BS;
-#pragma unroll
-    for (int i = 0; i < CW; ++i)
-      *reinterpret_cast<u32x4*>(slot + lds_off(bc, part * CW + i)) = unpack_signed(c.w[i], c.z);
+  const bool has_zero = a.zero != nullptr;
+  auto write_code = [&](const Codes& c, int i, uint32_t slot) {
+    const float z = has_zero ? (float)c.z : 8.0f;
+    *reinterpret_cast<u32x4*>(bs + slot + lds_off(bc, part * CW + i)) = unpack_signed(c.w[i], z);
   };
 
   f32x16 acc[2][2] = {}, d[2][2];
-  auto compute = [&](const Scales& c, int s) {
-    const uint8_t* xt = xs + (s % 3) * XS + wm * 64 * 128;
-    const uint8_t* bt = bs + (s & 1) * BS + wn * 64 * 128;
+  struct Frag { u32x4 a[2], b[2]; };
+  auto frags = [&](Frag& f, int t, const uint8_t* xt, const uint8_t* bt) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f.a[i] = *reinterpret_cast<const u32x4*>(xt + lds_off(32 * i + c32, 2 * t + half));
+      f.b[i] = *reinterpret_cast<const u32x4*>(bt + lds_off(32 * i + c32, 2 * t + half));
+    }
+  };
+
+  // prologue: codes of steps 0 and 1, x of 0 and 1, scales of 0
+  Codes c0, c1;
+  Scales s0, s1;
+  Pos p0{0, 0};
+  Pos p1 = next_pos(p0), p2 = next_pos(p1);
+  uint32_t x0 = 0, x1 = XS, x2 = 2 * XS;     // x slots of this step, the next, the one after
+  load_codes(c0, p0);
+  load_scales(s0, p0);
+  load_x(p0, x0);
+  c1 = c0;
+  if (steps > 1) {
+    load_codes(c1, p1);
+    load_x(p1, x1);
+  }
+#pragma unroll
+  for (int i = 0; i < CW; ++i) write_code(c0, i, 0);
+  // ODD: this step's parity (weight slot; for G = 128 the group's half)
+  auto step = [&](auto odd, int s, const Codes& next, Codes& after, const Scales& now,
+                  Scales& later) {
+    constexpr int ODD = decltype(odd)::value;
+    // this step's x: this wave's loads have landed, then everyone's
+    if (s + 1 < steps) wait_vmcnt<LA>(); else wait_vmcnt<0>();
+    wait_lgkm0();
+    barrier();
+    const uint8_t* xt = xs + x0 + wm * 64 * 128;
+    const uint8_t* bt = bs + ODD * BS + wn * 64 * 128;
+    Frag f[2];
+    frags(f[0], 0, xt, bt);
+    if (s + 1 < steps) load_scales(later, p1);
+    if (s + 2 < steps) {
+      load_codes(after, p2);
+      load_x(p2, x2);
+    }
+    // the second group of a half step is not there: its x and codes repeat
+    // finite values, its scale is 0
+    const bool half_step = G == 32 && (p0.ks + 1) * kStepK > K;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      if (G == 32 && t == 2 && k_step(s) * kStepK + 32 >= K) break;     // half step
-      u32x4 af[2], bf[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        af[i] = *reinterpret_cast<const u32x4*>(xt + lds_off(32 * i + c32, 2 * t + half));
-        bf[i] = *reinterpret_cast<const u32x4*>(bt + lds_off(32 * i + c32, 2 * t + half));
-      }
-      const bool first = G == 128 ? (s & 1) == 0 && t == 0 : t * 16 % G == 0;
-      const bool last = G == 128 ? (s & 1) == 1 && t == 3 : (t + 1) * 16 % G == 0;
+      if (t < 3) frags(f[(t + 1) & 1], t + 1, xt, bt);
+      const bool first = G == 128 ? ODD == 0 && t == 0 : t * 16 % G == 0;
+      const bool last = G == 128 ? ODD == 1 && t == 3 : (t + 1) * 16 % G == 0;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
           d[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              __builtin_bit_cast(bf16x8, af[i]), __builtin_bit_cast(bf16x8, bf[j]),
-              first ? f32x16{} : d[i][j], 0, 0, 0);
+              __builtin_bit_cast(bf16x8, f[t & 1].a[i]),
+              __builtin_bit_cast(bf16x8, f[t & 1].b[j]), first ? f32x16{} : d[i][j], 0, 0, 0);
+      // the next step's weights (after the last step: to a slot nobody
+      // reads), while the matrix instructions run
+#pragma unroll
+      for (int i = t * CW / 4; i < (t + 1) * CW / 4; ++i) write_code(next, i, (1 - ODD) * BS);
       if (last) {
         const int g = G < 64 ? t * 16 / G : 0;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < 2; ++j) {
+            float sc = __uint_as_float(S16 ? (uint32_t)now.s[g][j] << 16 : now.s[g][j]);
+            if (g == 1 && half_step) sc = 0.0f;
 #pragma unroll
             for (int r = 0; r < 16; ++r)
-              acc[i][j][r] = __builtin_fmaf(c.s[g][j], d[i][j][r], acc[i][j][r]);
+              acc[i][j][r] = __builtin_fmaf(sc, d[i][j][r], acc[i][j][r]);
+          }
       }
     }
-  };
-
-  // prologue: x of steps 0 and 1, codes of 0 (unpacked), 1; scales of 0
-  Codes c0, c1;
-  Scales s0, s1;
-  load_codes(c0, 0);
-  load_scales(s0, 0);
-  load_x(0);
-  if (steps > 1) {
-    load_codes(c1, 1);
-    load_x(1);
-  }
-  write_codes(c0, 0);
-  auto step = [&](int s, Codes& next, Codes& after, Scales& now, Scales& later) {
-    // this step's x slot: this wave's loads have landed, then everyone's
-    if (s + 1 < steps) wait_vmcnt<LA>(); else wait_vmcnt<0>();
-    wait_lgkm0();
-    barrier();
-    if (s + 2 < steps) load_codes(after, s + 2);
-    if (s + 1 < steps) load_scales(later, s + 1);
-    if (s + 2 < steps) load_x(s + 2);
-    compute(now, s);
-    if (s + 1 < steps) write_codes(next, s + 1);
+    p0 = p1;
+    p1 = p2;
+    p2 = next_pos(p2);
+    const uint32_t x = x0;
+    x0 = x1;
+    x1 = x2;
+    x2 = x;
   };
   for (int s = 0; s < steps; s += 2) {
-    step(s, c1, c0, s0, s1);
+    step(std::integral_constant<int, 0>{}, s, c1, c0, s0, s1);
     if (s + 1 >= steps) break;
-    step(s + 1, c0, c1, s1, s0);
+    step(std::integral_constant<int, 1>{}, s + 1, c0, c1, s1, s0);
   }
 
 #pragma unroll
@@ -615,7 +647,7 @@ __global__ void __launch_bounds__(256) split_planes(const float* __restrict__ x,
   }
 }
 
-template <int G, int WM, int WN>
+template <int G, bool S16, int WM, int WN>
 void launch_tiles(const W4Args& a, void* ws, hipStream_t st) {
   constexpr int BM = 64 * WM, BN = 64 * WN;
   TileArgs t{};
@@ -640,11 +672,11 @@ void launch_tiles(const W4Args& a, void* ws, hipStream_t st) {
   }
   if (a.offsets) {
     t.items = (int)(((int64_t)a.S + (int64_t)(a.E < a.S ? a.E : a.S) * (BM - 1)) / BM);
-    hipLaunchKernelGGL((w4_tile_kernel<G, WM, WN, true>), dim3((unsigned)(t.items * t.ntn)),
+    hipLaunchKernelGGL((w4_tile_kernel<G, S16, WM, WN, true>), dim3((unsigned)(t.items * t.ntn)),
                        dim3(WM * WN * 64), 0, st, a, t);
   } else {
     t.items = (a.S + BM - 1) / BM;
-    hipLaunchKernelGGL((w4_tile_kernel<G, WM, WN, false>), dim3((unsigned)(t.items * t.ntn)),
+    hipLaunchKernelGGL((w4_tile_kernel<G, S16, WM, WN, false>), dim3((unsigned)(t.items * t.ntn)),
                        dim3(WM * WN * 64), 0, st, a, t);
   }
 }
@@ -668,7 +700,8 @@ void launch_rows(const W4Args& a, hipStream_t st) {
 template <int G>
 void launch_group(const W4Args& a, void* ws, hipStream_t st) {
   if (w4_tiled(a) && (a.x_dtype != BSMM_F32 || ws != nullptr)) {
-    launch_tiles<G, 4, 2>(a, ws, st);
+    if (a.s_bf16) launch_tiles<G, true, 4, 2>(a, ws, st);
+    else launch_tiles<G, false, 4, 2>(a, ws, st);
     return;
   }
   const bool many = (a.offsets ? (a.S + a.E - 1) / a.E : a.S) > 16;
