@@ -362,17 +362,12 @@ __device__ __forceinline__ void barrier() {
   asm volatile("" ::: "memory");
 }
 
-// 8 codes of a dword -> code - z as bf16, in order (integers of 5 bits: the
-// upper halves of their fp32 forms)
-__device__ __forceinline__ u32x4 unpack_signed(uint32_t w, float z) {
+// Codes 2q and 2q + 1 of a dword -> code - z as a pair of bf16 (integers of 5
+// bits: the upper halves of their fp32 forms)
+__device__ __forceinline__ uint32_t unpack_pair(uint32_t w, int q, float z) {
   const uint32_t e = w & 0x0F0F0F0Fu, o = (w >> 4) & 0x0F0F0F0Fu;
-  u32x4 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = (float)((e >> (8 * i)) & 0xFFu) - z, b = (float)((o >> (8 * i)) & 0xFFu) - z;
-    r[i] = hi2(__float_as_uint(a), __float_as_uint(b));
-  }
-  return r;
+  const float a = (float)((e >> (8 * q)) & 0xFFu) - z, b = (float)((o >> (8 * q)) & 0xFFu) - z;
+  return hi2(__float_as_uint(a), __float_as_uint(b));
 }
 
 // Logical workgroup ids: contiguous runs per XCD (hardware ids go round robin
@@ -406,7 +401,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) w4_tile_kernel(W4Args a, Tile
   constexpr int CB = BN * 32 / NT;                  // code bytes per thread and step (8 or 16)
   constexpr int CW = CB / 4;
   constexpr int NG = G < 64 ? 64 / G : 1;           // scale groups in a step
-  static_assert(CB == 8 || CB == 16, "one wide load of codes per thread");
+  static_assert(CB == 4 || CB == 8 || CB == 16, "one wide load of codes per thread");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[3 * XS + 2 * BS];
   uint8_t* const xs = smem;
   uint8_t* const bs = smem + 3 * XS;
@@ -446,10 +441,11 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) w4_tile_kernel(W4Args a, Tile
   // codes: this thread's column and its run of CB bytes of every step
   const int bc = threadIdx.x / (32 / CB), part = threadIdx.x % (32 / CB);
   const int64_t bn = min(tn * BN + bc, a.N - 1);
-  const uint8_t* wp = a.w + it.e * a.w_se + bn * a.ldw;
+  const uint8_t* wp = a.w + it.e * a.w_se + bn * a.ldw + part * CB;
   // without zero points the byte that is read (a scale's) is not used
-  const uint8_t* zp = a.zero ? a.zero + it.e * a.z_se + bn * a.z_n
-                             : static_cast<const uint8_t*>(a.scale);
+  const uint8_t* zp = (a.zero ? a.zero + it.e * a.z_se + bn * a.z_n
+                              : static_cast<const uint8_t*>(a.scale)) + part * CB * 2 / G;
+  const bool has_zero = a.zero != nullptr;
   using scale_t = std::conditional_t<S16, uint16_t, uint32_t>;
   const scale_t* sp[2];
 #pragma unroll
@@ -457,9 +453,11 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) w4_tile_kernel(W4Args a, Tile
     sp[j] = static_cast<const scale_t*>(a.scale) + it.e * a.s_se +
             (int64_t)min(tn * BN + wn * 64 + j * 32 + c32, a.N - 1) * a.s_n;
 
-  const int K = a.K, KG = K / G;
+  const int K = a.K;
   const int steps1 = (K + kStepK - 1) / kStepK;       // per plane
   const int steps = steps1 * ta.planes;
+  // the last step of a plane has only its first group (G = 32)
+  auto half_step = [&](int ks) { return G == 32 && (ks + 1) * kStepK > K; };
   struct Codes { uint32_t w[CW]; uint8_t z; };
   struct Scales { scale_t s[NG][2]; };
   // A step: its K step within the plane, its byte offset in x
@@ -476,8 +474,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) w4_tile_kernel(W4Args a, Tile
   auto load_x = [&](Pos p, uint32_t slot) {
     // the missing half of a half step repeats the first (never read): no
     // load reaches past its row
-    const bool tail = G == 32 && (p.ks + 1) * kStepK > K;
-    const uint32_t back = tail && (((lane & 7) ^ (lane >> 3)) & 4) ? 64u : 0u;
+    const uint32_t back = half_step(p.ks) && (((lane & 7) ^ (lane >> 3)) & 4) ? 64u : 0u;
 #pragma unroll
     for (int t = 0; t < LA; ++t) {
       const lds_ptr_t l =
@@ -486,40 +483,55 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) w4_tile_kernel(W4Args a, Tile
     }
   };
   auto load_codes = [&](Codes& c, Pos p) {
-    int at = p.ks * 32 + part * CB;
-    if (G == 32 && at + CB > K / 2) at = 0;            // past a half step: not used
+    // past a half step: the row's start again, not used
+    const bool past = half_step(p.ks) && part * CB >= 16;
+    const int at = past ? -part * CB : p.ks * 32;
     if constexpr (CB == 16) {
       const u32x4 v = *reinterpret_cast<const u32x4*>(wp + at);
 #pragma unroll
       for (int i = 0; i < 4; ++i) c.w[i] = v[i];
-    } else {
+    } else if constexpr (CB == 8) {
       const uint2 v = *reinterpret_cast<const uint2*>(wp + at);
       c.w[0] = v.x;
       c.w[1] = v.y;
+    } else {
+      c.w[0] = *reinterpret_cast<const uint32_t*>(wp + at);
     }
-    c.z = zp[at * 2 / G];
+    c.z = zp[past ? -(part * CB * 2 / G) : p.ks * kStepK / G];
   };
-  auto load_scales = [&](Scales& c, Pos p) {
+  auto load_scales = [&](Scales& c, int ks) {
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      const int i = G == 32 ? min(p.ks * 2 + g, KG - 1) : p.ks * kStepK / G;
+      const int i = g == 1 && half_step(ks) ? 0 : ks * kStepK / G + g;
 #pragma unroll
       for (int j = 0; j < 2; ++j) c.s[g][j] = sp[j][i];
     }
   };
-  const bool has_zero = a.zero != nullptr;
-  auto write_code = [&](const Codes& c, int i, uint32_t slot) {
-    const float z = has_zero ? (float)c.z : 8.0f;
-    *reinterpret_cast<u32x4*>(bs + slot + lds_off(bc, part * CW + i)) = unpack_signed(c.w[i], z);
+  uint32_t wo[CW];      // where this thread's unpacked codes go in a weight slot
+#pragma unroll
+  for (int i = 0; i < CW; ++i) wo[i] = lds_off(bc, part * CW + i);
+  auto zero_of = [&](const Codes& c) { return has_zero ? (float)c.z : 8.0f; };
+  auto write_code = [&](u32x4 v, int i, uint32_t slot) {
+    *reinterpret_cast<u32x4*>(bs + slot + wo[i]) = v;
   };
 
-  f32x16 acc[2][2] = {}, d[2][2];
+  // d: the open group's sums; pend: the scales of the group that d holds
+  // until its next group's first product replaces it
+  f32x16 acc[2][2] = {}, d[2][2] = {};
+  float pend[2] = {0.0f, 0.0f};
+  auto fold = [&](int i, int j) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[i][j][r] = __builtin_fmaf(pend[j], d[i][j][r], acc[i][j][r]);
+  };
   struct Frag { u32x4 a[2], b[2]; };
+  uint32_t fo[4];       // a lane's fragment offsets in either tile, rows c32
+#pragma unroll
+  for (int t = 0; t < 4; ++t) fo[t] = lds_off(c32, 2 * t + half);
   auto frags = [&](Frag& f, int t, const uint8_t* xt, const uint8_t* bt) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      f.a[i] = *reinterpret_cast<const u32x4*>(xt + lds_off(32 * i + c32, 2 * t + half));
-      f.b[i] = *reinterpret_cast<const u32x4*>(bt + lds_off(32 * i + c32, 2 * t + half));
+      f.a[i] = *reinterpret_cast<const u32x4*>(xt + fo[t] + i * 4096);
+      f.b[i] = *reinterpret_cast<const u32x4*>(bt + fo[t] + i * 4096);
     }
   };
 
@@ -530,7 +542,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) w4_tile_kernel(W4Args a, Tile
   Pos p1 = next_pos(p0), p2 = next_pos(p1);
   uint32_t x0 = 0, x1 = XS, x2 = 2 * XS;     // x slots of this step, the next, the one after
   load_codes(c0, p0);
-  load_scales(s0, p0);
+  load_scales(s0, 0);
   load_x(p0, x0);
   c1 = c0;
   if (steps > 1) {
@@ -538,55 +550,71 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) w4_tile_kernel(W4Args a, Tile
     load_x(p1, x1);
   }
 #pragma unroll
-  for (int i = 0; i < CW; ++i) write_code(c0, i, 0);
-  // ODD: this step's parity (weight slot; for G = 128 the group's half)
-  auto step = [&](auto odd, int s, const Codes& next, Codes& after, const Scales& now,
+  for (int i = 0; i < CW; ++i) {
+    u32x4 v;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = unpack_pair(c0.w[i], q, zero_of(c0));
+    write_code(v, i, 0);
+  }
+  // ODD: this step's parity (weight slot; for G = 128 the group's half).
+  // HOT: two more steps follow, so the body has no branch and is scheduled
+  // as one block.
+  auto step = [&](auto odd, auto hot, int s, const Codes& next, Codes& after, const Scales& now,
                   Scales& later) {
     constexpr int ODD = decltype(odd)::value;
+    constexpr bool HOT = decltype(hot)::value;
     // this step's x: this wave's loads have landed, then everyone's
-    if (s + 1 < steps) wait_vmcnt<LA>(); else wait_vmcnt<0>();
+    if (HOT || s + 1 < steps) wait_vmcnt<LA>(); else wait_vmcnt<0>();
     wait_lgkm0();
     barrier();
     const uint8_t* xt = xs + x0 + wm * 64 * 128;
     const uint8_t* bt = bs + ODD * BS + wn * 64 * 128;
     Frag f[2];
     frags(f[0], 0, xt, bt);
-    if (s + 1 < steps) load_scales(later, p1);
-    if (s + 2 < steps) {
-      load_codes(after, p2);
-      load_x(p2, x2);
-    }
+    const float z = zero_of(next);
     // the second group of a half step is not there: its x and codes repeat
     // finite values, its scale is 0
-    const bool half_step = G == 32 && (p0.ks + 1) * kStepK > K;
+    const bool cut = half_step(p0.ks);
+    u32x4 v;
+    // Four products (k 16 t .. 16 t + 15) a turn.  The source order is the
+    // schedule: each product is followed by a share of the VALU work (a
+    // quarter of an unpacked dword, the fold of the block's last group), so
+    // that neither unit waits for the other, and the turn's first share
+    // fetches the next turn's fragments.
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      if (t < 3) frags(f[(t + 1) & 1], t + 1, xt, bt);
       const bool first = G == 128 ? ODD == 0 && t == 0 : t * 16 % G == 0;
       const bool last = G == 128 ? ODD == 1 && t == 3 : (t + 1) * 16 % G == 0;
+      // the dword of codes that this turn unpacks (-1: none)
+      const int w = CW == 4 ? t : CW == 2 ? (t & 1 ? t / 2 : -1) : (t == 3 ? 0 : -1);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int q = 0; q < 4; ++q) {
+        const int i = q >> 1, j = q & 1;
+        if (first) fold(i, j);
+        d[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            __builtin_bit_cast(bf16x8, f[t & 1].a[i]), __builtin_bit_cast(bf16x8, f[t & 1].b[j]),
+            first ? f32x16{} : d[i][j], 0, 0, 0);
+        if (q == 0 && t < 3) frags(f[(t + 1) & 1], t + 1, xt, bt);
+        if (q == 1 && t == 0) {
+          if (HOT || s + 1 < steps) load_scales(later, p1.ks);
+          if (HOT || s + 2 < steps) load_codes(after, p2);
+        }
+        // after the codes: they are waited for first
+        if (q == 3 && t == 0 && (HOT || s + 2 < steps)) load_x(p2, x2);
+        if (w >= 0) {
+          v[q] = unpack_pair(next.w[w < 0 ? 0 : w], q, z);
+          // the next step's weights (after the last step: to a slot nobody reads)
+          if (q == 3) write_code(v, w, (1 - ODD) * BS);
+        }
+        if (last && q == 3) {
+          const int g = G < 64 ? t * 16 / G : 0;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          d[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              __builtin_bit_cast(bf16x8, f[t & 1].a[i]),
-              __builtin_bit_cast(bf16x8, f[t & 1].b[j]), first ? f32x16{} : d[i][j], 0, 0, 0);
-      // the next step's weights (after the last step: to a slot nobody
-      // reads), while the matrix instructions run
-#pragma unroll
-      for (int i = t * CW / 4; i < (t + 1) * CW / 4; ++i) write_code(next, i, (1 - ODD) * BS);
-      if (last) {
-        const int g = G < 64 ? t * 16 / G : 0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float sc = __uint_as_float(S16 ? (uint32_t)now.s[g][j] << 16 : now.s[g][j]);
-            if (g == 1 && half_step) sc = 0.0f;
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-              acc[i][j][r] = __builtin_fmaf(sc, d[i][j][r], acc[i][j][r]);
+          for (int n = 0; n < 2; ++n) {
+            pend[n] = __uint_as_float(S16 ? (uint32_t)now.s[g][n] << 16 : now.s[g][n]);
+            if (g == 1 && cut) pend[n] = 0.0f;
           }
+        }
+        if (HOT) __builtin_amdgcn_sched_barrier(0);
       }
     }
     p0 = p1;
@@ -597,12 +625,23 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) w4_tile_kernel(W4Args a, Tile
     x1 = x2;
     x2 = x;
   };
-  for (int s = 0; s < steps; s += 2) {
-    step(std::integral_constant<int, 0>{}, s, c1, c0, s0, s1);
+  constexpr std::integral_constant<int, 0> even{};
+  constexpr std::integral_constant<int, 1> odd{};
+  int s = 0;
+  for (; s + 3 < steps; s += 2) {
+    step(even, std::true_type{}, s, c1, c0, s0, s1);
+    step(odd, std::true_type{}, s + 1, c0, c1, s1, s0);
+  }
+  for (; s < steps; s += 2) {
+    step(even, std::false_type{}, s, c1, c0, s0, s1);
     if (s + 1 >= steps) break;
-    step(std::integral_constant<int, 1>{}, s + 1, c0, c1, s1, s0);
+    step(odd, std::false_type{}, s + 1, c0, c1, s1, s0);
   }
 
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) fold(i, j);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
