@@ -365,7 +365,9 @@ __device__ __forceinline__ void barrier() {
 // Codes 2q and 2q + 1 of a dword -> code - z as a pair of bf16 (integers of 5
 // bits: the upper halves of their fp32 forms)
 __device__ __forceinline__ uint32_t unpack_pair(uint32_t w, int q, float z) {
-  const uint32_t e = w & 0x0F0F0F0Fu, o = (w >> 4) & 0x0F0F0F0Fu;
+  uint32_t e = w & 0x0F0F0F0Fu, o = (w >> 4) & 0x0F0F0F0Fu;
+  // opaque: keeps the byte conversions from being split into shift and convert
+  asm("" : "+v"(e), "+v"(o));
   const float a = (float)((e >> (8 * q)) & 0xFFu) - z, b = (float)((o >> (8 * q)) & 0xFFu) - z;
   return hi2(__float_as_uint(a), __float_as_uint(b));
 }
@@ -556,63 +558,70 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) w4_tile_kernel(W4Args a, Tile
     for (int q = 0; q < 4; ++q) v[q] = unpack_pair(c0.w[i], q, zero_of(c0));
     write_code(v, i, 0);
   }
-  // ODD: this step's parity (weight slot; for G = 128 the group's half).
-  // HOT: two more steps follow, so the body has no branch and is scheduled
-  // as one block.
+  // One step: the products of 64 k, in four turns of 16 k by four blocks.
+  // ODD: its parity (weight slot; for G = 128 the group's half).  HOT: two
+  // more steps follow, so the body has no branch.
+  //
+  // The source order is the schedule.  A turn's fragments are read during the
+  // turn before; the barrier stands before the last turn, whose products then
+  // cover the first fragments of the next step.  Unpacking and folds are
+  // shared out between the products, which leave the VALU about four
+  // instructions each.  A group's blocks (0, 0) and (0, 1) are folded in its
+  // last turn, the other two in the next group's first.
+  Frag f[2];
   auto step = [&](auto odd, auto hot, int s, const Codes& next, Codes& after, const Scales& now,
                   Scales& later) {
     constexpr int ODD = decltype(odd)::value;
     constexpr bool HOT = decltype(hot)::value;
-    // this step's x: this wave's loads have landed, then everyone's
-    if (HOT || s + 1 < steps) wait_vmcnt<LA>(); else wait_vmcnt<0>();
-    wait_lgkm0();
-    barrier();
     const uint8_t* xt = xs + x0 + wm * 64 * 128;
     const uint8_t* bt = bs + ODD * BS + wn * 64 * 128;
-    Frag f[2];
-    frags(f[0], 0, xt, bt);
     const float z = zero_of(next);
     // the second group of a half step is not there: its x and codes repeat
     // finite values, its scale is 0
     const bool cut = half_step(p0.ks);
     u32x4 v;
-    // Four products (k 16 t .. 16 t + 15) a turn.  The source order is the
-    // schedule: each product is followed by a share of the VALU work (a
-    // quarter of an unpacked dword, the fold of the block's last group), so
-    // that neither unit waits for the other, and the turn's first share
-    // fetches the next turn's fragments.
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const bool first = G == 128 ? ODD == 0 && t == 0 : t * 16 % G == 0;
       const bool last = G == 128 ? ODD == 1 && t == 3 : (t + 1) * 16 % G == 0;
       // the dword of codes that this turn unpacks (-1: none)
-      const int w = CW == 4 ? t : CW == 2 ? (t & 1 ? t / 2 : -1) : (t == 3 ? 0 : -1);
+      const int w = CW == 4 ? t : t - 1 < CW ? t - 1 : -1;
+      if (t == 3) {
+        // this wave's x loads of the next step have landed (newer: this
+        // step's codes, zero point and x), its fragments and weights too;
+        // then everyone's
+        if (HOT || s + 2 < steps) wait_vmcnt<LA + 2>(); else wait_vmcnt<0>();
+        wait_lgkm0();
+        barrier();
+        if (HOT || s + 1 < steps)
+          frags(f[0], 0, xs + x1 + wm * 64 * 128, bs + (1 - ODD) * BS + wn * 64 * 128);
+      }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int i = q >> 1, j = q & 1;
-        if (first) fold(i, j);
         d[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
             __builtin_bit_cast(bf16x8, f[t & 1].a[i]), __builtin_bit_cast(bf16x8, f[t & 1].b[j]),
             first ? f32x16{} : d[i][j], 0, 0, 0);
         if (q == 0 && t < 3) frags(f[(t + 1) & 1], t + 1, xt, bt);
-        if (q == 1 && t == 0) {
-          if (HOT || s + 1 < steps) load_scales(later, p1.ks);
-          if (HOT || s + 2 < steps) load_codes(after, p2);
-        }
-        // after the codes: they are waited for first
-        if (q == 3 && t == 0 && (HOT || s + 2 < steps)) load_x(p2, x2);
-        if (w >= 0) {
-          v[q] = unpack_pair(next.w[w < 0 ? 0 : w], q, z);
-          // the next step's weights (after the last step: to a slot nobody reads)
-          if (q == 3) write_code(v, w, (1 - ODD) * BS);
-        }
-        if (last && q == 3) {
+        if (first && q < 2) fold(1, q);
+        if (last && q == 0) {
           const int g = G < 64 ? t * 16 / G : 0;
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
             pend[n] = __uint_as_float(S16 ? (uint32_t)now.s[g][n] << 16 : now.s[g][n]);
             if (g == 1 && cut) pend[n] = 0.0f;
           }
+        }
+        if (last && q >= 2) fold(0, q - 2);
+        if (q == 1 && t == 0) {
+          if (HOT || s + 1 < steps) load_scales(later, p1.ks);
+          if (HOT || s + 2 < steps) load_codes(after, p2);
+        }
+        if (q == 3 && t == 0 && (HOT || s + 2 < steps)) load_x(p2, x2);
+        if (w >= 0) {
+          v[q] = unpack_pair(next.w[w < 0 ? 0 : w], q, z);
+          // the next step's weights (after the last step: to a slot nobody reads)
+          if (q == 3) write_code(v, w, (1 - ODD) * BS);
         }
         if (HOT) __builtin_amdgcn_sched_barrier(0);
       }
@@ -625,6 +634,10 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) w4_tile_kernel(W4Args a, Tile
     x1 = x2;
     x2 = x;
   };
+  if (steps > 1) wait_vmcnt<LA>(); else wait_vmcnt<0>();      // x of step 0
+  wait_lgkm0();
+  barrier();
+  frags(f[0], 0, xs + x0 + wm * 64 * 128, bs + wn * 64 * 128);
   constexpr std::integral_constant<int, 0> even{};
   constexpr std::integral_constant<int, 1> odd{};
   int s = 0;
@@ -639,9 +652,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) w4_tile_kernel(W4Args a, Tile
   }
 
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) fold(i, j);
+  for (int j = 0; j < 2; ++j) fold(1, j);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
