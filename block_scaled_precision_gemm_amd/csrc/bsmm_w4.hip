@@ -150,91 +150,163 @@ __device__ __forceinline__ void store_out(const W4Args& a, int64_t at, float v) 
   else static_cast<float*>(a.out)[at] = v;
 }
 
-// One workgroup: 16 * MT rows by 16 * NT columns, NW waves that split K in
-// chunks of 128 and are added through LDS in wave order.
-template <bool XF32, int G, int MT, int NT, int NW, bool ROUTED>
-__global__ void __launch_bounds__(NW * 64) w4_rows_kernel(W4Args a, int ntn) {
-  constexpr int BM = 16 * MT, BN = 16 * NT;
-  extern __shared__ float red[];        // [NW][MT * NT][4][64]
+// Routed: zero rows for the slots of no expert, columns [col, col + cols),
+// shared out over the items.
+__device__ __forceinline__ void zero_unused(const W4Args& a, int col, int cols, int item,
+                                            int items, int threads) {
+  const int used = min(max(a.offsets[a.E], 0), a.S);
+  for (int p = used + item; p < a.S; p += items) {
+    const int slot = a.order[p];
+    if (slot < 0 || slot >= a.S) continue;
+    for (int i = threadIdx.x; i < cols; i += threads)
+      if (col + i < a.N) store_out(a, slot * a.ldo + col + i, 0.0f);
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void wait_lgkm0() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+}
+
+// A lane's SIZE bytes at src to dst + 16 * lane (SIZE 16) or dst + 4 * lane
+// (SIZE 4, or 1 and 2, widened with zeros); dst is the wave's.
+template <int SIZE>
+__device__ __forceinline__ void to_lds(const void* src, uint8_t* dst) {
+  auto* const from = (__attribute__((address_space(1))) void*)(uintptr_t)src;
+  auto* const to = (__attribute__((address_space(3))) void*)(uintptr_t)(uint32_t)(uintptr_t)dst;
+  if constexpr (SIZE == 1) __builtin_amdgcn_global_load_lds(from, to, 1, 0, 0);
+  else if constexpr (SIZE == 2) __builtin_amdgcn_global_load_lds(from, to, 2, 0, 0);
+  else if constexpr (SIZE == 4) __builtin_amdgcn_global_load_lds(from, to, 4, 0, 0);
+  else __builtin_amdgcn_global_load_lds(from, to, 16, 0, 0);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: items of BM rows (4, 16 or 32); each of the 8 waves of a workgroup
+// has 16 * NT columns and one of ks ranges of K (8 / ks column groups a
+// workgroup), and the ks partial sums are added through LDS in order.  A
+// wave's share is cut so that enough waves are in flight whatever the sizes.
+//
+// Codes, scales, zero points and x of a chunk of 128 k go global -> LDS
+// directly, into a ring of D slots of the wave's own: no barrier, D - 1 chunks
+// in flight and one loop body.  The body's size matters more than its work:
+// a decode call runs each wave through a handful of chunks, and straight-line
+// code for them was slower by the instruction fetches (1 x 1024 x 4096: 8.7 us
+// with four chunks unrolled).  LDS also does the cross-lane part: with G = 128
+// a lane's 16 bytes of codes are 32 consecutive k; with smaller groups a lane
+// reads one dword of each 32-element block, so that one product stays inside
+// one group, and every lane reads the scale of the block's own lanes.
+// ---------------------------------------------------------------------------
+constexpr int kRowWaves = 8;
+constexpr int64_t kRowTarget = 2048;    // waves that fill the chip: 8 a CU
+
+// bytes of a ring slot, and slots within 152 KB for 8 waves
+template <bool XF32, int BM, int NT>
+struct RowRing {
+  static constexpr int XL = BM * (XF32 ? 512 : 256) / 1024;     // x loads of a chunk
+  static constexpr int PER = XL + 3 * NT;                       // loads of a chunk
+  static constexpr int SLOT = XL * 1024 + NT * 1536;
+  static constexpr int FIT = 152 * 1024 / kRowWaves / SLOT;
+  static constexpr int D = FIT < 4 ? FIT : 4;
+  static constexpr int BYTES = kRowWaves * D * SLOT;
+  static_assert(D >= 2 && (D - 1) * PER < 64, "ring depth");
+};
+
+template <bool XF32, int G, int BM, int NT, bool ROUTED>
+__global__ void __launch_bounds__(kRowWaves * 64) w4_rows_kernel(W4Args a, int ntn, int ks) {
+  using Ring = RowRing<XF32, BM, NT>;
+  constexpr int MT = (BM + 15) / 16, WN = 16 * NT, ES = XF32 ? 4 : 2;
+  constexpr int UNITS = 128 * ES / 16;  // 16-byte units of a row's chunk
+  constexpr int D = Ring::D;
+  const int cn = kRowWaves / ks, BN = WN * cn;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   const int tn = blockIdx.x % ntn, item = blockIdx.x / ntn;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int kw = wave % ks, cw = wave / ks;
   const int c16 = lane & 15, quad = lane >> 4;
   Item it;
   if (ROUTED) {
     it = find_item(a.offsets, a.E, a.S, BM, item);
-    // slots of no expert: zero rows, shared out over the items
-    const int used = min(max(a.offsets[a.E], 0), a.S);
-    const int items = gridDim.x / ntn;
-    for (int p = used + item; p < a.S; p += items) {
-      const int slot = a.order[p];
-      if (slot < 0 || slot >= a.S) continue;
-      for (int i = threadIdx.x; i < BN; i += NW * 64)
-        if (tn * BN + i < a.N) store_out(a, slot * a.ldo + tn * BN + i, 0.0f);
-    }
+    zero_unused(a, tn * BN, BN, item, gridDim.x / ntn, kRowWaves * 64);
     if (it.rows == 0) return;
   } else {
     it = Item{0, item * BM, min(a.S - item * BM, BM)};
   }
-  // rows past the item's end repeat its first row: their results are not
-  // stored, and a row of the product depends on its own row of x alone
-  int64_t xoff[MT];
+  const int K = a.K, KG = K / G;
+  const int chunks = (K + 127) / 128, per = (chunks + ks - 1) / ks;
+  const int c0 = kw * per, c1 = min(c0 + per, chunks);
+  const int col0 = tn * BN + cw * WN;
+
+  // Sources.  x: load t brings units 64 t + lane of the slot's x, unit p of
+  // row r at p ^ (r % 16) so that 16 rows' reads of one unit spread over the
+  // banks; rows past the end repeat the first (a row of the product depends
+  // on its own row of x alone, and theirs are not stored).
+  const uint8_t* xp[Ring::XL];
+  int xk[Ring::XL];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int m = 16 * i + c16;
-    int64_t row = it.p0 + (m < it.rows ? m : 0);
+  for (int t = 0; t < Ring::XL; ++t) {
+    const int r = (64 * t + lane) / UNITS, u = ((lane % UNITS) ^ (r & 15));
+    int64_t row = it.p0 + (r < it.rows ? r : 0);
     if (ROUTED) row = min(max(a.order[row] / a.x_div, 0), a.R - 1);
-    xoff[i] = row * a.ldx;
+    xp[t] = static_cast<const uint8_t*>(a.x) + row * a.ldx * ES;
+    xk[t] = u * (16 / ES);
   }
   const uint8_t* wp[NT];
-  int64_t sp[NT];
+  const uint8_t* sp[NT];
   const uint8_t* zp[NT];
+  const bool s16 = a.s_bf16 != 0;
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    const int64_t n = min(tn * BN + 16 * j + c16, a.N - 1);
+    const int64_t n = min(col0 + 16 * j + c16, a.N - 1);
     wp[j] = a.w + it.e * a.w_se + n * a.ldw;
-    sp[j] = it.e * a.s_se + n * a.s_n;
-    zp[j] = a.zero ? a.zero + it.e * a.z_se + n * a.z_n : nullptr;
+    sp[j] = static_cast<const uint8_t*>(a.scale) + (it.e * a.s_se + n * a.s_n) * (s16 ? 2 : 4);
+    // without zero points the byte that is read (a scale's) is not used
+    zp[j] = a.zero ? a.zero + it.e * a.z_se + n * a.z_n
+                   : static_cast<const uint8_t*>(a.scale);
   }
-  const int K = a.K, KG = K / G;
-  const int chunks = (K + 127) / 128;
-  f32x4 acc[MT][NT] = {};
-
-  struct Chunk {
-    u32x4 w[NT];
-    X8<XF32> x[MT][4];
-    float s[NT], z[NT];
-  };
-  // chunk of this wave's step: pairs of chunks (one 128-byte line of codes)
-  auto chunk_of = [&](int s) { return ((s >> 1) * NW + wave) * 2 + (s & 1); };
-  auto load = [&](Chunk& b, int c) {
+  uint8_t* const ring = smem + wave * (D * Ring::SLOT);
+  auto load = [&](int c, uint8_t* slot) {
     const int kc = c * 128;
-    const int wo = kc / 2 + quad * 16 < K / 2 ? kc / 2 + quad * 16 : 0;
-    // the group whose scale this lane brings: its own for G = 128, else
-    // the one of its quad's 32-element block
-    int g = G == 128 ? c : G == 64 ? 2 * c + (quad >> 1) : 4 * c + quad;
-    g = min(g, KG - 1);
+    // past the end of the row: its start again, in products that are left out
+#pragma unroll
+    for (int t = 0; t < Ring::XL; ++t) {
+      const int k = kc + xk[t];
+      to_lds<16>(xp[t] + (G == 128 || k < K ? k : xk[t] % 32) * ES,
+                 slot + t * 1024);
+    }
+    const int k = kc + quad * 32, kk = G == 128 || k < K ? k : 0, g = min(k / G, KG - 1);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      b.w[j] = *reinterpret_cast<const u32x4*>(wp[j] + wo);
-      b.s[j] = a.s_bf16 ? __uint_as_float(
-                              (uint32_t)static_cast<const uint16_t*>(a.scale)[sp[j] + g] << 16)
-                        : static_cast<const float*>(a.scale)[sp[j] + g];
-      b.z[j] = 16.0f + (zp[j] ? (float)zp[j][g] : 8.0f);
+      uint8_t* const ws = slot + Ring::XL * 1024 + j * 1536;
+      to_lds<16>(wp[j] + kk / 2, ws);
+      if (s16) to_lds<2>(sp[j] + 2 * g, ws + 1024);
+      else to_lds<4>(sp[j] + 4 * g, ws + 1024);
+      to_lds<1>(zp[j] + g, ws + 1280);
     }
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        // G = 128: a lane's 16 code bytes are 32 consecutive k; else step t
-        // takes the 32-element block t, 8 elements to a quad
-        int k = G == 128 ? kc + quad * 32 + t * 8 : kc + t * 32 + quad * 8;
-        if (k >= K) k = quad * 8;
-        b.x[i][t] = load_x<XF32>(a.x, xoff[i] + k);
-      }
   };
-  auto compute = [&](Chunk& b, int c) {
-    const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+
+  f32x4 acc[MT][NT] = {};
+  const bool has_zero = a.zero != nullptr;
+  const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+#pragma unroll 1
+  for (int u = 0; u < D && c0 + u < c1; ++u) load(c0 + u, ring + u * Ring::SLOT);
+  uint8_t* slot = ring;
+#pragma unroll 1
+  for (int c = c0; c < c1; ++c) {
+    // the loads of this chunk: those of the chunks after it may be in flight
+    const int newer = c1 - 1 - c;
+    if (newer >= D - 1) wait_vmcnt<(D - 1) * Ring::PER>();
+    else if (D > 3 && newer == 2) wait_vmcnt<(D > 3 ? 2 : 0) * Ring::PER>();
+    else if (D > 2 && newer == 1) wait_vmcnt<(D > 2 ? 1 : 0) * Ring::PER>();
+    else wait_vmcnt<0>();
     f32x4 d[MT][NT], e[MT];
+    u32x4 wv[NT];
+    if (G == 128)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        wv[j] = *reinterpret_cast<const u32x4*>(slot + Ring::XL * 1024 + j * 1536 + lane * 16);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       if (G != 128 && c * 128 + t * 32 >= K) break;      // uniform
@@ -248,20 +320,24 @@ __global__ void __launch_bounds__(NW * 64) w4_rows_kernel(W4Args a, int ntn) {
       }
       u32x4 wb[NT];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        uint32_t w = b.w[j][t];
-        if (G != 128) {
-          // dword `quad` of block t, which quad t loaded
-          const int src = (t << 4) | c16;
-          const uint32_t w0 = __shfl(b.w[j].x, src), w1 = __shfl(b.w[j].y, src);
-          const uint32_t w2 = __shfl(b.w[j].z, src), w3 = __shfl(b.w[j].w, src);
-          w = quad == 0 ? w0 : quad == 1 ? w1 : quad == 2 ? w2 : w3;
-        }
-        wb[j] = unpack(w);
-      }
+      for (int j = 0; j < NT; ++j)
+        wb[j] = unpack(G == 128 ? wv[j][t]
+                                : *reinterpret_cast<const uint32_t*>(
+                                      slot + Ring::XL * 1024 + j * 1536 + (16 * t + c16) * 16 +
+                                      quad * 4));
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        const Parts<XF32> p = parts(b.x[i][t]);
+        const int r = BM < 16 ? c16 % BM : 16 * i + c16;
+        const int k = G == 128 ? quad * 32 + t * 8 : t * 32 + quad * 8;
+        const uint8_t* xr = slot + r * (UNITS * 16);
+        X8<XF32> x;
+        if constexpr (XF32) {
+          x.a = *reinterpret_cast<const u32x4*>(xr + ((k / 4) ^ (r & 15)) * 16);
+          x.b = *reinterpret_cast<const u32x4*>(xr + ((k / 4 + 1) ^ (r & 15)) * 16);
+        } else {
+          x.v = *reinterpret_cast<const u32x4*>(xr + ((k / 8) ^ (r & 15)) * 16);
+        }
+        const Parts<XF32> p = parts(x);
 #pragma unroll
         for (int h = (XF32 ? 3 : 1) - 1; h >= 0; --h) {
           e[i] = mfma(p.p[h], ones, e[i]);
@@ -272,12 +348,11 @@ __global__ void __launch_bounds__(NW * 64) w4_rows_kernel(W4Args a, int ntn) {
       if ((t + 1) * 32 % G == 0) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          float s = b.s[j], z = b.z[j];
-          if (G != 128) {
-            const int src = (G == 64 ? (t >> 1) << 5 : t << 4) | c16;
-            s = __shfl(s, src);
-            z = __shfl(z, src);
-          }
+          const uint8_t* const ss = slot + Ring::XL * 1024 + j * 1536 + 1024 + (16 * t + c16) * 4;
+          const uint32_t sb = *reinterpret_cast<const uint32_t*>(ss);
+          const float s = __uint_as_float(s16 ? sb << 16 : sb);
+          const float z =
+              16.0f + (has_zero ? (float)*reinterpret_cast<const uint32_t*>(ss + 256) : 8.0f);
 #pragma unroll
           for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -287,43 +362,55 @@ __global__ void __launch_bounds__(NW * 64) w4_rows_kernel(W4Args a, int ntn) {
         }
       }
     }
-  };
-
-  Chunk b0, b1;
-  int s = 0;
-  if (chunk_of(0) < chunks) load(b0, chunk_of(0));
-  while (chunk_of(s) < chunks) {
-    if (chunk_of(s + 1) < chunks) load(b1, chunk_of(s + 1));
-    compute(b0, chunk_of(s));
-    if (chunk_of(s + 1) >= chunks) break;
-    if (chunk_of(s + 2) < chunks) load(b0, chunk_of(s + 2));
-    compute(b1, chunk_of(s + 1));
-    s += 2;
+    wait_lgkm0();             // the slot has been read
+    if (c + D < c1) load(c + D, slot);
+    slot = slot == ring + (D - 1) * Ring::SLOT ? ring : slot + Ring::SLOT;
   }
 
+  // partial sums of K ranges 1 .. ks - 1 to LDS (over the rings, whose loads
+  // have all landed), added in order by range 0
+  if (ks > 1) {
+    float* const red = reinterpret_cast<float*>(smem);
+    __syncthreads();
+    if (kw > 0) {
+      float* r0 = red + ((kw - 1) * cn + cw) * (MT * NT * 256);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          *reinterpret_cast<f32x4*>(r0 + (i * NT + j) * 256 + lane * 4) = acc[i][j];
+    }
+    __syncthreads();
+    if (kw > 0) return;
+#pragma unroll 1
+    for (int w = 0; w < ks - 1; ++w) {
+      const float* r0 = red + (w * cn + cw) * (MT * NT * 256);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          acc[i][j] += *reinterpret_cast<const f32x4*>(r0 + (i * NT + j) * 256 + lane * 4);
+    }
+  }
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int r = 0; r < 4; ++r) {
+      const int m = 16 * i + 4 * quad + r;
+      if (m >= it.rows) continue;
+      int64_t row = it.p0 + m;
+      float rsc = 1.0f;
+      if (ROUTED) {
+        row = a.order[row];
+        if (row < 0 || row >= a.S) continue;
+        if (a.row_scale) rsc = a.row_scale[row];
+      }
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        red[((wave * MT * NT + i * NT + j) * 4 + r) * 64 + lane] = acc[i][j][r];
-  __syncthreads();
-  for (int i = threadIdx.x; i < BM * BN; i += NW * 64) {
-    const int m = i / BN, n = i % BN;
-    if (m >= it.rows || tn * BN + n >= a.N) continue;
-    const int at = (((m >> 4) * NT + (n >> 4)) * 4 + (m & 3)) * 64 + ((m & 15) >> 2) * 16 + (n & 15);
-    float v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) v += red[w * MT * NT * 256 + at];
-    int64_t row = it.p0 + m;
-    if (ROUTED) {
-      row = a.order[row];
-      if (row < 0 || row >= a.S) continue;
-      if (a.row_scale) v *= a.row_scale[row];
+      for (int j = 0; j < NT; ++j) {
+        const int n = col0 + 16 * j + c16;
+        if (n < a.N) store_out(a, row * a.ldo + n, acc[i][j][r] * rsc);
+      }
     }
-    store_out(a, row * a.ldo + tn * BN + n, v);
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -349,13 +436,6 @@ constexpr int kStepK = 64;
 __device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 __device__ __forceinline__ int lds_off(int r, int c) { return (r << 7) + ((c ^ swz(r)) << 4); }
 
-template <int N>
-__device__ __forceinline__ void wait_vmcnt() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void wait_lgkm0() {
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-}
 __device__ __forceinline__ void barrier() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
@@ -415,13 +495,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) w4_tile_kernel(W4Args a, Tile
   Item it;
   if (ROUTED) {
     it = find_item(a.offsets, a.E, a.S, BM, item);
-    const int used = min(max(a.offsets[a.E], 0), a.S);
-    for (int p = used + item; p < a.S; p += ta.items) {     // slots of no expert
-      const int slot = a.order[p];
-      if (slot < 0 || slot >= a.S) continue;
-      for (int i = threadIdx.x; i < BN; i += NT)
-        if (tn * BN + i < a.N) store_out(a, slot * a.ldo + tn * BN + i, 0.0f);
-    }
+    zero_unused(a, tn * BN, BN, item, ta.items, NT);
     if (it.rows == 0) return;
   } else {
     it = Item{0, item * BM, min(a.S - item * BM, BM)};
@@ -731,20 +805,33 @@ void launch_tiles(const W4Args& a, void* ws, hipStream_t st) {
   }
 }
 
-template <bool XF32, int G, int MT, int NT, int NW>
+// As many K ranges as leave about 8 waves to a CU, at most one per chunk.
+template <bool XF32, int G, int BM, int NT>
 void launch_rows(const W4Args& a, hipStream_t st) {
-  constexpr int BM = 16 * MT, BN = 16 * NT;
+  const int64_t act = a.E < a.S ? a.E : a.S;
+  const int64_t items = a.offsets ? (a.S + act * (BM - 1)) / BM : ((int64_t)a.S + BM - 1) / BM;
+  // routed: about half of a block is missing from an expert's last one
+  const int64_t busy = a.offsets ? (a.S + act * (BM / 2)) / BM + 1 : items;
+  const int64_t tiles = busy * ((a.N + 16 * NT - 1) / (16 * NT));
+  const int chunks = (a.K + 127) / 128;
+  int ks = 1;
+  while (ks < kRowWaves && tiles * ks < kRowTarget && 2 * ks <= chunks) ks *= 2;
+  const int BN = 16 * NT * (kRowWaves / ks);
   const int ntn = (a.N + BN - 1) / BN;
-  const size_t lds = (size_t)NW * MT * NT * 1024;
-  if (a.offsets) {
-    const int64_t items = ((int64_t)a.S + (int64_t)(a.E < a.S ? a.E : a.S) * (BM - 1)) / BM;
-    hipLaunchKernelGGL((w4_rows_kernel<XF32, G, MT, NT, NW, true>), dim3((unsigned)(items * ntn)),
-                       dim3(NW * 64), lds, st, a, ntn);
-  } else {
-    const int64_t items = ((int64_t)a.S + BM - 1) / BM;
-    hipLaunchKernelGGL((w4_rows_kernel<XF32, G, MT, NT, NW, false>),
-                       dim3((unsigned)(items * ntn)), dim3(NW * 64), lds, st, a, ntn);
-  }
+  const dim3 grid((unsigned)(items * ntn)), block(kRowWaves * 64);
+  constexpr int lds = RowRing<XF32, BM, NT>::BYTES;
+  if (a.offsets)
+    hipLaunchKernelGGL((w4_rows_kernel<XF32, G, BM, NT, true>), grid, block, lds, st, a, ntn, ks);
+  else
+    hipLaunchKernelGGL((w4_rows_kernel<XF32, G, BM, NT, false>), grid, block, lds, st, a, ntn, ks);
+}
+
+template <bool XF32, int G>
+void launch_few(const W4Args& a, hipStream_t st) {
+  const int64_t rows = a.offsets ? (a.S + a.E - 1) / a.E : a.S;
+  if (rows <= 4) launch_rows<XF32, G, 4, 1>(a, st);
+  else if (rows <= 16 || XF32) launch_rows<XF32, G, 16, 1>(a, st);
+  else launch_rows<XF32, G, XF32 ? 16 : 32, 1>(a, st);
 }
 
 template <int G>
@@ -754,14 +841,8 @@ void launch_group(const W4Args& a, void* ws, hipStream_t st) {
     else launch_tiles<G, false, 4, 2>(a, ws, st);
     return;
   }
-  const bool many = (a.offsets ? (a.S + a.E - 1) / a.E : a.S) > 16;
-  if (a.x_dtype == BSMM_F32) {
-    if (many) launch_rows<true, G, 2, 1, 8>(a, st);
-    else launch_rows<true, G, 1, 1, 8>(a, st);
-  } else {
-    if (many) launch_rows<false, G, 2, 1, 8>(a, st);
-    else launch_rows<false, G, 1, 1, 8>(a, st);
-  }
+  if (a.x_dtype == BSMM_F32) launch_few<true, G>(a, st);
+  else launch_few<false, G>(a, st);
 }
 
 }  // namespace
