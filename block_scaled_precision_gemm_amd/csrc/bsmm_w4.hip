@@ -184,8 +184,8 @@ __device__ __forceinline__ void to_lds(const void* src, uint8_t* dst) {
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: items of BM rows (4, 16 or 32); each of the 8 waves of a workgroup
-// has 16 * NT columns and one of ks ranges of K (8 / ks column groups a
+// Few rows: items of BM rows (4, 16 or 32); each of the W waves of a workgroup
+// has 16 * NT columns and one of ks ranges of K (W / ks column groups a
 // workgroup), and the ks partial sums are added through LDS in order.  A
 // wave's share is cut so that enough waves are in flight whatever the sizes.
 //
@@ -199,28 +199,38 @@ __device__ __forceinline__ void to_lds(const void* src, uint8_t* dst) {
 // reads one dword of each 32-element block, so that one product stays inside
 // one group, and every lane reads the scale of the block's own lanes.
 // ---------------------------------------------------------------------------
-constexpr int kRowWaves = 8;
 constexpr int64_t kRowTarget = 2048;    // waves that fill the chip: 8 a CU
 
-// bytes of a ring slot, and slots within 152 KB for 8 waves
+// A wave's LDS: the ring, and two regions of scales and zero points, which
+// come for SG groups at a time (a segment): loads of 4 groups, a group to a
+// quad.  A workgroup's is at most half of a CU's 160 KB: two workgroups a CU,
+// so that a grid a little above the number of CUs does not take two rounds.
 template <bool XF32, int BM, int NT>
 struct RowRing {
+  static constexpr int W = BM <= 4 ? 8 : 4;                     // waves of a workgroup
   static constexpr int XL = BM * (XF32 ? 512 : 256) / 1024;     // x loads of a chunk
-  static constexpr int PER = XL + 3 * NT;                       // loads of a chunk
-  static constexpr int SLOT = XL * 1024 + NT * 1536;
-  static constexpr int FIT = 152 * 1024 / kRowWaves / SLOT;
+  static constexpr int PER = XL + NT;                           // loads of a chunk
+  static constexpr int SLOT = PER * 1024;
+  static constexpr int SG = PER > 8 ? 8 : 16;
+  static constexpr int SEG_BYTES = SG * 16 * 4;                 // of one column tile
+  static constexpr int SCALES = 4 * NT * SEG_BYTES;
+  static constexpr int FIT = (80 * 1024 / W - SCALES) / SLOT;
   static constexpr int D = FIT < 4 ? FIT : 4;
-  static constexpr int BYTES = kRowWaves * D * SLOT;
+  static constexpr int WAVE = D * SLOT + SCALES;
+  static constexpr int BYTES = W * WAVE;
   static_assert(D >= 2 && (D - 1) * PER < 64, "ring depth");
+  // a segment is loaded before the last chunk that precedes its own
+  static_assert(SG * 32 / 128 >= D, "segment length");
 };
 
 template <bool XF32, int G, int BM, int NT, bool ROUTED>
-__global__ void __launch_bounds__(kRowWaves * 64) w4_rows_kernel(W4Args a, int ntn, int ks) {
+__global__ void __launch_bounds__((RowRing<XF32, BM, NT>::W * 64))
+w4_rows_kernel(W4Args a, int ntn, int ks) {
   using Ring = RowRing<XF32, BM, NT>;
   constexpr int MT = (BM + 15) / 16, WN = 16 * NT, ES = XF32 ? 4 : 2;
   constexpr int UNITS = 128 * ES / 16;  // 16-byte units of a row's chunk
   constexpr int D = Ring::D;
-  const int cn = kRowWaves / ks, BN = WN * cn;
+  const int cn = Ring::W / ks, BN = WN * cn;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   const int tn = blockIdx.x % ntn, item = blockIdx.x / ntn;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -229,7 +239,7 @@ __global__ void __launch_bounds__(kRowWaves * 64) w4_rows_kernel(W4Args a, int n
   Item it;
   if (ROUTED) {
     it = find_item(a.offsets, a.E, a.S, BM, item);
-    zero_unused(a, tn * BN, BN, item, gridDim.x / ntn, kRowWaves * 64);
+    zero_unused(a, tn * BN, BN, item, gridDim.x / ntn, Ring::W * 64);
     if (it.rows == 0) return;
   } else {
     it = Item{0, item * BM, min(a.S - item * BM, BM)};
@@ -256,57 +266,70 @@ __global__ void __launch_bounds__(kRowWaves * 64) w4_rows_kernel(W4Args a, int n
   const uint8_t* wp[NT];
   const uint8_t* sp[NT];
   const uint8_t* zp[NT];
-  const bool s16 = a.s_bf16 != 0;
+  const bool s16 = a.s_bf16 != 0, has_zero = a.zero != nullptr;
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int64_t n = min(col0 + 16 * j + c16, a.N - 1);
     wp[j] = a.w + it.e * a.w_se + n * a.ldw;
     sp[j] = static_cast<const uint8_t*>(a.scale) + (it.e * a.s_se + n * a.s_n) * (s16 ? 2 : 4);
-    // without zero points the byte that is read (a scale's) is not used
-    zp[j] = a.zero ? a.zero + it.e * a.z_se + n * a.z_n
-                   : static_cast<const uint8_t*>(a.scale);
+    zp[j] = has_zero ? a.zero + it.e * a.z_se + n * a.z_n : nullptr;
   }
-  uint8_t* const ring = smem + wave * (D * Ring::SLOT);
+  uint8_t* const ring = smem + wave * Ring::WAVE;
+  uint8_t* const scl = ring + D * Ring::SLOT;
   auto load = [&](int c, uint8_t* slot) {
     const int kc = c * 128;
     // past the end of the row: its start again, in products that are left out
 #pragma unroll
     for (int t = 0; t < Ring::XL; ++t) {
       const int k = kc + xk[t];
-      to_lds<16>(xp[t] + (G == 128 || k < K ? k : xk[t] % 32) * ES,
-                 slot + t * 1024);
+      to_lds<16>(xp[t] + (G == 128 || k < K ? k : xk[t] % 32) * ES, slot + t * 1024);
     }
-    const int k = kc + quad * 32, kk = G == 128 || k < K ? k : 0, g = min(k / G, KG - 1);
+    const int k = kc + quad * 32, kk = G == 128 || k < K ? k : 0;
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      uint8_t* const ws = slot + Ring::XL * 1024 + j * 1536;
-      to_lds<16>(wp[j] + kk / 2, ws);
-      if (s16) to_lds<2>(sp[j] + 2 * g, ws + 1024);
-      else to_lds<4>(sp[j] + 4 * g, ws + 1024);
-      to_lds<1>(zp[j] + g, ws + 1280);
-    }
+    for (int j = 0; j < NT; ++j) to_lds<16>(wp[j] + kk / 2, slot + (Ring::XL + j) * 1024);
+  };
+  // segment i of the wave's groups, to region i % 2
+  constexpr int SEG = Ring::SG * G / 128;        // chunks of a segment
+  const int g0 = c0 * 128 / G;
+  auto load_segment = [&](int i) {
+    uint8_t* const dst = scl + (i & 1) * (2 * NT * Ring::SEG_BYTES);
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int h = 0; h < Ring::SG / 4; ++h) {
+        const int g = min(g0 + i * Ring::SG + 4 * h + quad, KG - 1);
+        if (s16) to_lds<2>(sp[j] + 2 * g, dst + j * Ring::SEG_BYTES + h * 256);
+        else to_lds<4>(sp[j] + 4 * g, dst + j * Ring::SEG_BYTES + h * 256);
+        if (has_zero) to_lds<1>(zp[j] + g, dst + (NT + j) * Ring::SEG_BYTES + h * 256);
+      }
   };
 
   f32x4 acc[MT][NT] = {};
-  const bool has_zero = a.zero != nullptr;
   const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+  if (c0 < c1) load_segment(0);
 #pragma unroll 1
   for (int u = 0; u < D && c0 + u < c1; ++u) load(c0 + u, ring + u * Ring::SLOT);
   uint8_t* slot = ring;
 #pragma unroll 1
   for (int c = c0; c < c1; ++c) {
-    // the loads of this chunk: those of the chunks after it may be in flight
+    // This chunk's loads have landed, and those of the chunks after it may be
+    // in flight: the newest ones, whatever scales were loaded among them.
     const int newer = c1 - 1 - c;
     if (newer >= D - 1) wait_vmcnt<(D - 1) * Ring::PER>();
     else if (D > 3 && newer == 2) wait_vmcnt<(D > 3 ? 2 : 0) * Ring::PER>();
     else if (D > 2 && newer == 1) wait_vmcnt<(D > 2 ? 1 : 0) * Ring::PER>();
     else wait_vmcnt<0>();
+    // a segment's first chunk fetches the next segment; its own one landed
+    // before this chunk did
+    const int in = (c - c0) % SEG, seg = (c - c0) / SEG;
+    if (in == 0 && c + SEG < c1) load_segment(seg + 1);
+    const uint8_t* const sc = scl + (seg & 1) * (2 * NT * Ring::SEG_BYTES) + in * (128 / G) * 64;
     f32x4 d[MT][NT], e[MT];
     u32x4 wv[NT];
     if (G == 128)
 #pragma unroll
       for (int j = 0; j < NT; ++j)
-        wv[j] = *reinterpret_cast<const u32x4*>(slot + Ring::XL * 1024 + j * 1536 + lane * 16);
+        wv[j] = *reinterpret_cast<const u32x4*>(slot + (Ring::XL + j) * 1024 + lane * 16);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       if (G != 128 && c * 128 + t * 32 >= K) break;      // uniform
@@ -323,7 +346,7 @@ __global__ void __launch_bounds__(kRowWaves * 64) w4_rows_kernel(W4Args a, int n
       for (int j = 0; j < NT; ++j)
         wb[j] = unpack(G == 128 ? wv[j][t]
                                 : *reinterpret_cast<const uint32_t*>(
-                                      slot + Ring::XL * 1024 + j * 1536 + (16 * t + c16) * 16 +
+                                      slot + (Ring::XL + j) * 1024 + (16 * t + c16) * 16 +
                                       quad * 4));
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
@@ -348,11 +371,12 @@ __global__ void __launch_bounds__(kRowWaves * 64) w4_rows_kernel(W4Args a, int n
       if ((t + 1) * 32 % G == 0) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          const uint8_t* const ss = slot + Ring::XL * 1024 + j * 1536 + 1024 + (16 * t + c16) * 4;
+          const uint8_t* const ss = sc + j * Ring::SEG_BYTES + (t * 32 / G * 16 + c16) * 4;
           const uint32_t sb = *reinterpret_cast<const uint32_t*>(ss);
           const float s = __uint_as_float(s16 ? sb << 16 : sb);
-          const float z =
-              16.0f + (has_zero ? (float)*reinterpret_cast<const uint32_t*>(ss + 256) : 8.0f);
+          const float z = 16.0f + (has_zero ? (float)*reinterpret_cast<const uint32_t*>(
+                                                  ss + NT * Ring::SEG_BYTES)
+                                            : 8.0f);
 #pragma unroll
           for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -814,11 +838,12 @@ void launch_rows(const W4Args& a, hipStream_t st) {
   const int64_t busy = a.offsets ? (a.S + act * (BM / 2)) / BM + 1 : items;
   const int64_t tiles = busy * ((a.N + 16 * NT - 1) / (16 * NT));
   const int chunks = (a.K + 127) / 128;
+  constexpr int W = RowRing<XF32, BM, NT>::W;
   int ks = 1;
-  while (ks < kRowWaves && tiles * ks < kRowTarget && 2 * ks <= chunks) ks *= 2;
-  const int BN = 16 * NT * (kRowWaves / ks);
+  while (ks < W && tiles * ks < kRowTarget && 2 * ks <= chunks) ks *= 2;
+  const int BN = 16 * NT * (W / ks);
   const int ntn = (a.N + BN - 1) / BN;
-  const dim3 grid((unsigned)(items * ntn)), block(kRowWaves * 64);
+  const dim3 grid((unsigned)(items * ntn)), block(W * 64);
   constexpr int lds = RowRing<XF32, BM, NT>::BYTES;
   if (a.offsets)
     hipLaunchKernelGGL((w4_rows_kernel<XF32, G, BM, NT, true>), grid, block, lds, st, a, ntn, ks);
