@@ -796,60 +796,80 @@ def bsmm_quant_w4(w, *, group=128, symmetric=True, scale_dtype="f32", values=Fal
     and bsmm_w4_expert_mm ([E, N, K]).  ``values=True`` appends what the
     codes stand for, (code - zero) * scale, as a tensor like w.
     """
-    torch = _torch()
     w2, code = _quant_input(w, "w")
-    sc = _dtype_code(scale_dtype)
-    if sc not in (F32, BF16):
-        raise ValueError("scale_dtype must be f32 or bf16")
+    sc = _float_code(scale_dtype, "scale_dtype")
+    torch, dtypes, u8, _, _ = _DTYPES["torch"]
     if group not in (32, 64, 128):
         raise ValueError("group must be 32, 64 or 128")
     R, K = w2.shape
     if K % group:
         raise ValueError(f"the last dimension ({K}) must be a multiple of group ({group})")
-    lead = tuple(w.shape[:-1])
-    q = torch.empty(lead + (K // 2,), dtype=torch.uint8, device=w.device)
-    scale = torch.empty(lead + (K // group,), dtype=_torch_dtype(sc), device=w.device)
-    zero = None if symmetric else torch.empty(lead + (K // group,), dtype=torch.uint8,
-                                              device=w.device)
-    v = torch.empty(lead + (K,), dtype=w.dtype, device=w.device) if values else None
+    lead, dev, KG = w.shape[:-1], w.device, K // group
+
+    def new(cols, dtype):
+        if len(lead) == 1:            # the cheapest allocation on the host
+            return torch.empty_strided((R, cols), (cols, 1), dtype=dtype, device=dev)
+        return torch.empty((*lead, cols), dtype=dtype, device=dev)
+
+    q = new(K // 2, u8)
+    scale = new(KG, dtypes[sc])
+    zero = None if symmetric else new(KG, u8)
+    v = new(K, w.dtype) if values else None
     _check(load().bsmm_quant_w4(
-        w2.data_ptr(), w2.stride(0), code, q.data_ptr(), K // 2, scale.data_ptr(), K // group,
-        sc, None if symmetric else zero.data_ptr(), K // group,
+        w2.data_ptr(), w2.stride(0), code, q.data_ptr(), K // 2, scale.data_ptr(), KG,
+        sc, None if symmetric else zero.data_ptr(), KG,
         v.data_ptr() if values else None, K, group, R, K, _stream(stream)))
     return (q, scale, zero, v) if values else (q, scale, zero)
 
 
+_DTYPES = {}      # torch dtype, name or code -> library code, for float tensors (filled once)
+
+
+def _float_codes():
+    """The codes of the float dtypes by torch dtype, name and code."""
+    if not _DTYPES:
+        torch = _torch()
+        _DTYPES.update({torch.bfloat16: BF16, torch.float32: F32, "bf16": BF16, "f32": F32,
+                        BF16: BF16, F32: F32})
+        _DTYPES["torch"] = (torch, {BF16: torch.bfloat16, F32: torch.float32}, torch.uint8,
+                            torch.int32, torch.float32)
+    return _DTYPES
+
+
 def _float_code(dt, name):
     """F32 or BF16 for a float tensor's dtype."""
-    torch = _torch()
-    if dt is torch.bfloat16:
-        return BF16
-    if dt is torch.float32:
-        return F32
-    raise ValueError(f"{name}: expected bf16 or fp32, got {dt}")
+    code = _float_codes().get(dt)
+    if code is None:
+        raise ValueError(f"{name}: expected bf16 or fp32, got {dt}")
+    return code
 
 
-def _w4_weight(w, scale, zero, lead, K):
-    """Check a 4-bit weight with leading shape ``lead`` against K input
-    features; returns (group, scale dtype code)."""
-    torch = _torch()
-    if w.dtype is not torch.uint8 or tuple(w.shape) != (*lead, K // 2):
-        raise ValueError(f"w must be uint8 {(*lead, K // 2)}, got {w.dtype} {tuple(w.shape)}")
+def _w4_weight(w, ws, wst, scale, zero, K, u8):
+    """Check a 4-bit weight (shape ws, strides wst) against K input features;
+    returns (group, scale dtype code, scale strides, zero pointer, zero
+    strides).  A decode call is bound by the host: one read of each shape and
+    stride."""
     code = _float_code(scale.dtype, "scale")
-    if scale.shape[:-1] != w.shape[:-1] or scale.dim() != w.dim():
-        raise ValueError(f"scale {tuple(scale.shape)} does not fit w {tuple(w.shape)}")
-    KG = scale.shape[-1]
-    if K % 2 or (K and (KG == 0 or K % KG)):
+    if w.dtype is not u8 or 2 * ws[-1] != K:
+        raise ValueError(f"w must be uint8 with {K // 2} bytes a row (K = {K}), got {w.dtype} "
+                         f"{tuple(ws)}")
+    ss, sst = scale.shape, scale.stride()
+    KG = ss[-1]
+    if ss[:-1] != ws[:-1]:
+        raise ValueError(f"scale {tuple(ss)} does not fit w {tuple(ws)}")
+    if K and (KG == 0 or K % KG):
         raise ValueError(f"scale has {KG} groups for K = {K}")
-    if (K and w.stride(-1) != 1) or (KG > 1 and scale.stride(-1) != 1):
+    if (K and wst[-1] != 1) or (KG > 1 and sst[-1] != 1):
         raise ValueError("w and scale must be contiguous along their last dimension")
-    if zero is not None:
-        if zero.dtype is not torch.uint8 or zero.shape != scale.shape:
-            raise ValueError(f"zero must be uint8 {tuple(scale.shape)}, got {zero.dtype} "
-                             f"{tuple(zero.shape)}")
-        if KG > 1 and zero.stride(-1) != 1:
-            raise ValueError("zero must be contiguous along its last dimension")
-    return (K // KG if K else 32), code
+    group = K // KG if K else 32
+    if zero is None:
+        return group, code, sst, None, (0, 0, 0)
+    zst = zero.stride()
+    if zero.dtype is not u8 or zero.shape != ss:
+        raise ValueError(f"zero must be uint8 {tuple(ss)}, got {zero.dtype} {tuple(zero.shape)}")
+    if KG > 1 and zst[-1] != 1:
+        raise ValueError("zero must be contiguous along its last dimension")
+    return group, code, sst, zero.data_ptr(), zst
 
 
 def _w4_workspace(xc, E, R, S, K, dev, stream, handle):
@@ -860,6 +880,20 @@ def _w4_workspace(xc, E, R, S, K, dev, stream, handle):
     return (buf.data_ptr(), n) if n else (None, 0)
 
 
+def _w4_out(out, rows, cols, code, torch, dtypes, dev):
+    """The output tensor [rows, cols] and its row stride."""
+    if out is None:
+        # the cheapest allocation on the host
+        return torch.empty_strided((rows, cols), (cols, 1), dtype=dtypes[code], device=dev), cols
+    if tuple(out.shape) != (rows, cols) or out.dtype is not dtypes[code]:
+        raise ValueError(f"out must be {(rows, cols)} {dtypes[code]}, got {tuple(out.shape)} "
+                         f"{out.dtype}")
+    st = out.stride()
+    if cols and st[1] != 1:
+        raise ValueError("out must be contiguous along its last dimension")
+    return out, st[0]
+
+
 def bsmm_w4_mm(x, w, scale, zero=None, *, out_dtype="bf16", out=None, stream=None):
     """Activations times a 4-bit weight: x @ W.T with W = (code - zero) * scale.
 
@@ -867,25 +901,27 @@ def bsmm_w4_mm(x, w, scale, zero=None, *, out_dtype="bf16", out=None, stream=Non
     [N, K/group], zero: uint8 [N, K/group] or None (8), as bsmm_quant_w4
     returns them (group 32, 64 or 128).  Returns [M, N], fp32 or bf16.
     """
-    if x.dim() != 2 or w.dim() != 2:
+    xs, ws = x.shape, w.shape
+    if len(xs) != 2 or len(ws) != 2:
         raise ValueError("x and w must be 2-D")
-    code = _dtype_code(out_dtype)
     xc = _float_code(x.dtype, "x")
-    M, K = x.shape
-    N = w.shape[0]
-    group, sc = _w4_weight(w, scale, zero, (N,), K)
-    if K and x.stride(1) != 1:
-        raise ValueError(f"x must be row-major, got stride {x.stride()}")
-    o = _out(out, (M, N), code, x.device)
-    if N and o.stride(1) != 1:
-        raise ValueError("out must be contiguous along N")
+    code = _float_code(out_dtype, "out_dtype")
+    torch, dtypes, u8, _, _ = _DTYPES["torch"]
+    M, K = xs
+    N = ws[0]
+    xst, wst = x.stride(), w.stride()
+    group, sc, sst, zp, zst = _w4_weight(w, ws, wst, scale, zero, K, u8)
+    if K and xst[1] != 1:
+        raise ValueError(f"x must be row-major, got stride {xst}")
+    dev = x.device
+    o, ldo = _w4_out(out, M, N, code, torch, dtypes, dev)
     hs = _stream(stream)
-    wsp, wsn = _w4_workspace(xc, 1, M, M, K, x.device, stream, hs)
-    _check(load().bsmm_w4_mm(
-        x.data_ptr(), x.stride(0), xc, w.data_ptr(), w.stride(0), scale.data_ptr(),
-        scale.stride(0), sc, None if zero is None else zero.data_ptr(),
-        0 if zero is None else zero.stride(0), group, o.data_ptr(), o.stride(0), code, M, N, K,
-        wsp, wsn, hs))
+    wsp, wsn = _w4_workspace(xc, 1, M, M, K, dev, stream, hs)
+    status = load().bsmm_w4_mm(x.data_ptr(), xst[0], xc, w.data_ptr(), wst[0], scale.data_ptr(),
+                               sst[0], sc, zp, zst[0], group, o.data_ptr(), ldo, code, M, N, K,
+                               wsp, wsn, hs)
+    if status:
+        _check(status)
     return o
 
 
@@ -901,37 +937,37 @@ def bsmm_w4_expert_mm(x, w, scale, zero, order, offsets, *, slots_per_row=1, row
     row_scale: fp32 [S] (the routing weights, slot order) or None.  Returns
     [S, N] in slot order, zeros for slots without an expert.
     """
-    torch = _torch()
-    if x.dim() != 2 or w.dim() != 3:
+    xs, ws = x.shape, w.shape
+    if len(xs) != 2 or len(ws) != 3:
         raise ValueError("x must be 2-D and w 3-D")
-    code = _dtype_code(out_dtype)
     xc = _float_code(x.dtype, "x")
-    R, K = x.shape
-    E, N = w.shape[0], w.shape[1]
-    group, sc = _w4_weight(w, scale, zero, (E, N), K)
-    if K and x.stride(1) != 1:
-        raise ValueError(f"x must be row-major, got stride {x.stride()}")
-    if order.dtype is not torch.int32 or order.dim() != 1 or not order.is_contiguous():
+    code = _float_code(out_dtype, "out_dtype")
+    torch, dtypes, u8, i32, f32 = _DTYPES["torch"]
+    R, K = xs
+    E, N = ws[0], ws[1]
+    xst, wst = x.stride(), w.stride()
+    group, sc, sst, zp, zst = _w4_weight(w, ws, wst, scale, zero, K, u8)
+    if K and xst[1] != 1:
+        raise ValueError(f"x must be row-major, got stride {xst}")
+    if order.dtype is not i32 or order.dim() != 1 or not order.is_contiguous():
         raise ValueError("order must be a contiguous int32 [S] tensor")
     S = order.shape[0]
-    if offsets.dtype is not torch.int32 or tuple(offsets.shape) != (E + 1,) or \
-            not offsets.is_contiguous():
+    if offsets.dtype is not i32 or offsets.shape != (E + 1,) or not offsets.is_contiguous():
         raise ValueError(f"offsets must be a contiguous int32 [{E + 1}] tensor")
-    if row_scale is not None and (row_scale.dtype is not torch.float32 or
-                                  row_scale.numel() != S or not row_scale.is_contiguous()):
+    if row_scale is not None and (row_scale.dtype is not f32 or row_scale.numel() != S or
+                                  not row_scale.is_contiguous()):
         raise ValueError(f"row_scale must be contiguous fp32 of {S} elements")
-    o = _out(out, (S, N), code, x.device)
-    if N and o.stride(1) != 1:
-        raise ValueError("out must be contiguous along N")
+    dev = x.device
+    o, ldo = _w4_out(out, S, N, code, torch, dtypes, dev)
     hs = _stream(stream)
-    wsp, wsn = _w4_workspace(xc, E, R, S, K, x.device, stream, hs)
-    _check(load().bsmm_w4_expert_mm(
-        x.data_ptr(), x.stride(0), xc, w.data_ptr(), w.stride(0), w.stride(1), scale.data_ptr(),
-        scale.stride(0), scale.stride(1), sc, None if zero is None else zero.data_ptr(),
-        0 if zero is None else zero.stride(0), 0 if zero is None else zero.stride(1), group,
-        order.data_ptr(), offsets.data_ptr(), slots_per_row,
-        None if row_scale is None else row_scale.data_ptr(), o.data_ptr(), o.stride(0), code,
-        E, R, S, N, K, wsp, wsn, hs))
+    wsp, wsn = _w4_workspace(xc, E, R, S, K, dev, stream, hs)
+    status = load().bsmm_w4_expert_mm(
+        x.data_ptr(), xst[0], xc, w.data_ptr(), wst[0], wst[1], scale.data_ptr(), sst[0], sst[1],
+        sc, zp, zst[0], zst[1], group, order.data_ptr(), offsets.data_ptr(), slots_per_row,
+        None if row_scale is None else row_scale.data_ptr(), o.data_ptr(), ldo, code, E, R, S, N,
+        K, wsp, wsn, hs)
+    if status:
+        _check(status)
     return o
 
 
@@ -958,6 +994,17 @@ def _route_mask(mask, T):
     return mask.data_ptr()
 
 
+def _route_logits(logits):
+    """(T, E, row stride, dtype code) of a logits tensor."""
+    code = _float_code(logits.dtype, "logits")
+    shape, st = logits.shape, logits.stride()
+    if len(shape) != 2:
+        raise ValueError("logits must be 2-D [T, E]")
+    if shape[1] and st[1] != 1:
+        raise ValueError(f"logits must be row-major, got stride {st}")
+    return shape[0], shape[1], st[0], code
+
+
 def bsmm_route_topk(logits, k, *, mask=None, renorm=True, alpha=None, stream=None):
     """Top-k experts of every token, with what their products need.
 
@@ -968,35 +1015,39 @@ def bsmm_route_topk(logits, k, *, mask=None, renorm=True, alpha=None, stream=Non
     order [T * k] (the slots t * k + j sorted by expert, for
     bsmm_w4_expert_mm), and with a loss live [1], prob_sum [E] and loss [1].
     """
-    torch = _torch()
-    code = _float_code(logits.dtype, "logits")
-    if logits.dim() != 2:
-        raise ValueError("logits must be 2-D [T, E]")
-    T, E = logits.shape
-    if E and logits.stride(1) != 1:
-        raise ValueError(f"logits must be row-major, got stride {logits.stride()}")
+    T, E, ldl, code = _route_logits(logits)
     if not 1 <= k <= min(E, 32):
         raise ValueError(f"k must be 1 to 32 and at most E = {E}, got {k}")
-    mp = _route_mask(mask, T)
+    torch, _, _, i32, f32 = _DTYPES["torch"]
+    mp = None if mask is None else _route_mask(mask, T)
     dev = logits.device
-    # one allocation for the integers, one for the floats: a decode step is
-    # bound by the host
+    # few allocations and views: a decode step is bound by the host
     S = T * k
-    ints = torch.empty(2 * S + 2 * E + 2, dtype=torch.int32, device=dev)
-    floats = torch.empty(S + E + 1, dtype=torch.float32, device=dev)
-    ip, fp = ints.data_ptr(), floats.data_ptr()
+    new = torch.empty_strided
+    index = new((T, k), (k, 1), dtype=i32, device=dev)
+    weight = new((T, k), (k, 1), dtype=f32, device=dev)
+    ints = new((S + 2 * E + 2,), (1,), dtype=i32, device=dev)
+    op = ints.data_ptr()
+    cp = op + 4 * S
     hs = _stream(stream)
-    wbuf, wn = _buffer(load().bsmm_route_workspace_bytes(T, E), dev, stream, hs)
-    loss = alpha is not None
-    _check(load().bsmm_route_topk(
-        logits.data_ptr(), logits.stride(0), code, mp, k, 1 if renorm else 0,
-        alpha if loss else 0.0, ip, fp, ip + 8 * S, ip + 8 * S + 4 * E, ip + 4 * S,
-        ip + 8 * S + 8 * E + 4 if loss else None, fp + 4 * S if loss else None,
-        fp + 4 * (S + E) if loss else None, T, E, wbuf.data_ptr() if wn else None, wn, hs))
-    index, order, counts, offsets, live = ints.split((S, S, E, E + 1, 1))
-    weight, prob_sum, total = floats.split((S, E, 1))
-    return Route(index.view(T, k), weight.view(T, k), counts, offsets, order,
-                 live if loss else None, prob_sum if loss else None, total if loss else None)
+    lib = load()
+    wbuf, wn = _buffer(lib.bsmm_route_workspace_bytes(T, E), dev, stream, hs)
+    lp = pp = tp = None
+    if alpha is not None:
+        sums = new((E + 1,), (1,), dtype=f32, device=dev)
+        lp, pp = cp + 8 * E + 4, sums.data_ptr()
+        tp = pp + 4 * E
+    status = lib.bsmm_route_topk(
+        logits.data_ptr(), ldl, code, mp, k, 1 if renorm else 0, alpha or 0.0, index.data_ptr(),
+        weight.data_ptr(), cp, cp + 4 * E, op, lp, pp, tp, T, E, wbuf.data_ptr() if wn else None,
+        wn, hs)
+    if status:
+        _check(status)
+    order, counts, offsets, live = torch.unsafe_split_with_sizes(ints, (S, E, E + 1, 1))
+    if alpha is None:
+        return Route(index, weight, counts, offsets, order, None, None, None)
+    prob_sum, total = torch.unsafe_split_with_sizes(sums, (E, 1))
+    return Route(index, weight, counts, offsets, order, live, prob_sum, total)
 
 
 def bsmm_route_topk_backward(logits, index, weight, counts, live, *, dweight=None, dloss=None,
@@ -1008,41 +1059,36 @@ def bsmm_route_topk_backward(logits, index, weight, counts, live, *, dweight=Non
     data-parallel ranks).  dweight: fp32 [T, k] or None; dloss: fp32 of one
     element or None.  Returns dlogits like logits.
     """
-    torch = _torch()
-    code = _float_code(logits.dtype, "logits")
-    if logits.dim() != 2 or index.dim() != 2:
-        raise ValueError("logits and index must be 2-D")
-    T, E = logits.shape
-    k = index.shape[1]
-    if E and logits.stride(1) != 1:
-        raise ValueError(f"logits must be row-major, got stride {logits.stride()}")
-    for t, n, dt in ((index, "index", torch.int32), (weight, "weight", torch.float32),
-                     (dweight, "dweight", torch.float32)):
-        if t is None and n != "index":
-            continue
-        if t.dtype is not dt or tuple(t.shape) != (T, k) or not t.is_contiguous():
-            raise ValueError(f"{n} must be contiguous {dt} [{T}, {k}]")
+    T, E, ldl, code = _route_logits(logits)
+    torch, dtypes, _, i32, f32 = _DTYPES["torch"]
+    if index.dim() != 2:
+        raise ValueError("index must be 2-D [T, k]")
+    shape = index.shape
+    k = shape[1]
+    if shape[0] != T or index.dtype is not i32 or not index.is_contiguous():
+        raise ValueError(f"index must be contiguous int32 [{T}, k]")
+    for t, n in ((weight, "weight"), (dweight, "dweight")):
+        if t is not None and (t.dtype is not f32 or t.shape != shape or not t.is_contiguous()):
+            raise ValueError(f"{n} must be contiguous fp32 [{T}, {k}]")
+    cp = lp = None
     if dloss is not None:
-        if dloss.dtype is not torch.float32 or dloss.numel() != 1:
+        if dloss.dtype is not f32 or dloss.numel() != 1:
             raise ValueError("dloss must be one fp32 value")
-        if counts is None or counts.dtype is not torch.int32 or tuple(counts.shape) != (E,) or \
+        if counts is None or counts.dtype is not i32 or counts.shape != (E,) or \
                 not counts.is_contiguous():
             raise ValueError(f"counts must be contiguous int32 [{E}]")
-        if live is None or live.dtype is not torch.int32 or live.numel() != 1:
+        if live is None or live.dtype is not i32 or live.numel() != 1:
             raise ValueError("live must be one int32 value")
-    mp = _route_mask(mask, T)
-    o = _out(out, (T, E), code, logits.device)
-    if E and o.stride(1) != 1:
-        raise ValueError("out must be row-major")
-
-    def ptr(t):
-        return None if t is None else t.data_ptr()
-
-    _check(load().bsmm_route_topk_backward(
-        logits.data_ptr(), logits.stride(0), code, mp, index.data_ptr(), ptr(weight),
-        ptr(counts) if dloss is not None else None, ptr(live) if dloss is not None else None, k,
-        1 if renorm else 0, alpha, ptr(dweight), ptr(dloss), o.data_ptr(), o.stride(0), T, E,
-        _stream(stream)))
+        cp, lp = counts.data_ptr(), live.data_ptr()
+    mp = None if mask is None else _route_mask(mask, T)
+    o, ldd = _w4_out(out, T, E, code, torch, dtypes, logits.device)
+    status = load().bsmm_route_topk_backward(
+        logits.data_ptr(), ldl, code, mp, index.data_ptr(),
+        None if weight is None else weight.data_ptr(), cp, lp, k, 1 if renorm else 0, alpha,
+        None if dweight is None else dweight.data_ptr(),
+        None if dloss is None else dloss.data_ptr(), o.data_ptr(), ldd, T, E, _stream(stream))
+    if status:
+        _check(status)
     return o
 
 

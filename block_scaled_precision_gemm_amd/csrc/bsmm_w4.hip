@@ -225,27 +225,28 @@ struct RowRing {
 
 template <bool XF32, int G, int BM, int NT, bool ROUTED>
 __global__ void __launch_bounds__((RowRing<XF32, BM, NT>::W * 64))
-w4_rows_kernel(W4Args a, int ntn, int ks) {
+w4_rows_kernel(W4Args a, int item0, int log_ks) {
   using Ring = RowRing<XF32, BM, NT>;
   constexpr int MT = (BM + 15) / 16, WN = 16 * NT, ES = XF32 ? 4 : 2;
   constexpr int UNITS = 128 * ES / 16;  // 16-byte units of a row's chunk
   constexpr int D = Ring::D;
-  const int cn = Ring::W / ks, BN = WN * cn;
+  // no division on the way to the first load: it is a microsecond of a call
+  const int ks = 1 << log_ks, cn = Ring::W >> log_ks, BN = WN * cn;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-  const int tn = blockIdx.x % ntn, item = blockIdx.x / ntn;
+  const int tn = blockIdx.x, item = item0 + blockIdx.y;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int kw = wave % ks, cw = wave / ks;
+  const int kw = wave & (ks - 1), cw = wave >> log_ks;
   const int c16 = lane & 15, quad = lane >> 4;
   Item it;
   if (ROUTED) {
     it = find_item(a.offsets, a.E, a.S, BM, item);
-    zero_unused(a, tn * BN, BN, item, gridDim.x / ntn, Ring::W * 64);
+    zero_unused(a, tn * BN, BN, item, gridDim.y, Ring::W * 64);
     if (it.rows == 0) return;
   } else {
     it = Item{0, item * BM, min(a.S - item * BM, BM)};
   }
-  const int K = a.K, KG = K / G;
-  const int chunks = (K + 127) / 128, per = (chunks + ks - 1) / ks;
+  const int K = a.K, KG = (int)((unsigned)K / G);
+  const int chunks = (int)(((unsigned)K + 127) / 128), per = (chunks + ks - 1) >> log_ks;
   const int c0 = kw * per, c1 = min(c0 + per, chunks);
   const int col0 = tn * BN + cw * WN;
 
@@ -293,22 +294,31 @@ w4_rows_kernel(W4Args a, int ntn, int ks) {
   const int g0 = c0 * 128 / G;
   auto load_segment = [&](int i) {
     uint8_t* const dst = scl + (i & 1) * (2 * NT * Ring::SEG_BYTES);
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
+    const int g = g0 + i * Ring::SG + quad;
+    const int left = (c1 - c0) * (128 / G) - i * Ring::SG;     // groups the wave has left
+    auto each = [&](auto one) {
 #pragma unroll
       for (int h = 0; h < Ring::SG / 4; ++h) {
-        const int g = min(g0 + i * Ring::SG + 4 * h + quad, KG - 1);
-        if (s16) to_lds<2>(sp[j] + 2 * g, dst + j * Ring::SEG_BYTES + h * 256);
-        else to_lds<4>(sp[j] + 4 * g, dst + j * Ring::SEG_BYTES + h * 256);
-        if (has_zero) to_lds<1>(zp[j] + g, dst + (NT + j) * Ring::SEG_BYTES + h * 256);
+        if (4 * h >= left) break;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          one(j, min(g + 4 * h, KG - 1), dst + j * Ring::SEG_BYTES + h * 256);
       }
+    };
+    if (s16) each([&](int j, int gg, uint8_t* to) { to_lds<2>(sp[j] + 2 * gg, to); });
+    else each([&](int j, int gg, uint8_t* to) { to_lds<4>(sp[j] + 4 * gg, to); });
+    if (has_zero)
+      each([&](int j, int gg, uint8_t* to) { to_lds<1>(zp[j] + gg, to + NT * Ring::SEG_BYTES); });
   };
 
   f32x4 acc[MT][NT] = {};
   const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-  if (c0 < c1) load_segment(0);
+  if (c0 < c1) {
+    load(c0, ring);
+    load_segment(0);
 #pragma unroll 1
-  for (int u = 0; u < D && c0 + u < c1; ++u) load(c0 + u, ring + u * Ring::SLOT);
+    for (int u = 1; u < D && c0 + u < c1; ++u) load(c0 + u, ring + u * Ring::SLOT);
+  }
   uint8_t* slot = ring;
 #pragma unroll 1
   for (int c = c0; c < c1; ++c) {
@@ -320,8 +330,8 @@ w4_rows_kernel(W4Args a, int ntn, int ks) {
     else if (D > 2 && newer == 1) wait_vmcnt<(D > 2 ? 1 : 0) * Ring::PER>();
     else wait_vmcnt<0>();
     // a segment's first chunk fetches the next segment; its own one landed
-    // before this chunk did
-    const int in = (c - c0) % SEG, seg = (c - c0) / SEG;
+    // before this chunk did, or with it (the first)
+    const int in = (c - c0) & (SEG - 1), seg = (unsigned)(c - c0) / SEG;
     if (in == 0 && c + SEG < c1) load_segment(seg + 1);
     const uint8_t* const sc = scl + (seg & 1) * (2 * NT * Ring::SEG_BYTES) + in * (128 / G) * 64;
     f32x4 d[MT][NT], e[MT];
@@ -839,16 +849,22 @@ void launch_rows(const W4Args& a, hipStream_t st) {
   const int64_t tiles = busy * ((a.N + 16 * NT - 1) / (16 * NT));
   const int chunks = (a.K + 127) / 128;
   constexpr int W = RowRing<XF32, BM, NT>::W;
-  int ks = 1;
-  while (ks < W && tiles * ks < kRowTarget && 2 * ks <= chunks) ks *= 2;
-  const int BN = 16 * NT * (W / ks);
-  const int ntn = (a.N + BN - 1) / BN;
-  const dim3 grid((unsigned)(items * ntn)), block(W * 64);
+  int log_ks = 0;
+  while ((1 << log_ks) < W && (tiles << log_ks) < kRowTarget && (2 << log_ks) <= chunks) ++log_ks;
+  const int BN = 16 * NT * (W >> log_ks);
+  const dim3 block(W * 64);
   constexpr int lds = RowRing<XF32, BM, NT>::BYTES;
-  if (a.offsets)
-    hipLaunchKernelGGL((w4_rows_kernel<XF32, G, BM, NT, true>), grid, block, lds, st, a, ntn, ks);
-  else
-    hipLaunchKernelGGL((w4_rows_kernel<XF32, G, BM, NT, false>), grid, block, lds, st, a, ntn, ks);
+  // at most 65535 items a launch
+  for (int64_t i = 0; i < items; i += 65535) {
+    const dim3 grid((unsigned)((a.N + BN - 1) / BN),
+                    (unsigned)(items - i < 65535 ? items - i : 65535));
+    if (a.offsets)
+      hipLaunchKernelGGL((w4_rows_kernel<XF32, G, BM, NT, true>), grid, block, lds, st, a, (int)i,
+                         log_ks);
+    else
+      hipLaunchKernelGGL((w4_rows_kernel<XF32, G, BM, NT, false>), grid, block, lds, st, a, (int)i,
+                         log_ks);
+  }
 }
 
 template <bool XF32, int G>
