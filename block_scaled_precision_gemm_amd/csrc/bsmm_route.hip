@@ -68,6 +68,24 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   v = dpp_max<0x143>(v);
   return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
+// the same of several values, their chains interleaved
+template <int N>
+__device__ __forceinline__ void wave_max_all(uint32_t (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = dpp_max<0x111>(v[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = dpp_max<0x112>(v[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = dpp_max<0x114>(v[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = dpp_max<0x118>(v[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = dpp_max<0x142>(v[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = dpp_max<0x143>(v[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = (uint32_t)__builtin_amdgcn_readlane((int)v[i], 63);
+}
 template <int CTRL>
 __device__ __forceinline__ float dpp_add(float v) {
   return v + __int_as_float(
@@ -104,11 +122,16 @@ __device__ __forceinline__ float exp_neg(float d) {
   return __builtin_fmaf(e, r * kLn2, e);
 }
 
+// A wave's LDS accesses run in order; this keeps the compiler from moving
+// them past each other.
+__device__ __forceinline__ void order_lds() { asm volatile("" ::: "memory"); }
+
 struct Shared {
   u64 mask[kRouteMaxE];
   int hist[kRouteMaxE];
   int total[kRouteMaxE];
   int base[kRouteMaxE];
+  int index[64 * kRouteMaxK];     // the choices of 64 tokens
   int unused[64];
   int scan[kWaves];
   int live, used, unused_base;
@@ -117,71 +140,101 @@ struct Shared {
 
 // Tokens [t0, t1): choice and weights, counts into sh.hist, live tokens into
 // sh.live, and each wave's sums of probabilities into prob[wave][E] (loss
-// only).  sh.hist and sh.live are zero before, complete after a barrier.
-template <typename T, int PER>
-__device__ void choose(const RouteArgs& a, Shared& sh, float* prob, int t0, int t1) {
+// only).  sh.hist and sh.live are zero before, complete after a barrier.  A
+// wave takes U tokens at a time: the rounds of one token are a chain of
+// dependent wave reductions, and U chains fill each other's gaps (16384 x 256
+// top-8: 19 us with one, see the launch for U).  `keep`: the choices also go
+// to sh.index (64 tokens at most).
+template <typename T, int PER, int U>
+__device__ void choose(const RouteArgs& a, Shared& sh, float* prob, int t0, int t1, bool keep) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int E = a.E;
+  const int E = a.E, k = a.k;
   float psum[PER] = {};
-  for (int t = t0 + wave; t < t1; t += kWaves) {
-    const T* row = static_cast<const T*>(a.logits) + (int64_t)t * a.ldl;
-    float v[PER];
-    uint32_t key[PER];
-    const bool on = a.mask == nullptr || a.mask[t] != 0;
+  for (int tb = t0 + wave * U; tb < t1; tb += kWaves * U) {
+    float v[U][PER];
+    uint32_t key[U][PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = i * 64 + lane;
-      v[i] = on && e < E ? load_logit(row + e) : -__builtin_inff();
-      key[i] = key_of(v[i]);
-    }
-    int idx = -1;                 // lane j: the j-th choice
-    float chosen = 0.0f;
-    float top = 0.0f;
-    bool live = false;
-    for (int j = 0; j < a.k; ++j) {
-      uint32_t m = key[0];
+    for (int u = 0; u < U; ++u) {
+      const int t = min(tb + u, t1 - 1);
+      const T* row = static_cast<const T*>(a.logits) + (int64_t)t * a.ldl;
+      const bool on = tb + u < t1 && (a.mask == nullptr || a.mask[t] != 0);
 #pragma unroll
-      for (int i = 1; i < PER; ++i) m = max(m, key[i]);
-      m = wave_max(m);
-      if (m <= kNoKey) break;     // uniform
-      int found = -1;
-#pragma unroll
-      for (int i = PER - 1; i >= 0; --i) {
-        const u64 b = __ballot(key[i] == m);
-        if (b) found = i * 64 + __ffsll(b) - 1;
-      }
-#pragma unroll
-      for (int i = 0; i < PER; ++i) key[i] = found == i * 64 + lane ? 0u : key[i];
-      const float val = of_key(m);
-      if (j == 0) {
-        top = val;
-        live = true;
-      }
-      if (lane == j) {
-        idx = found;
-        chosen = val;
+      for (int i = 0; i < PER; ++i) {
+        const int e = i * 64 + lane;
+        v[u][i] = load_logit(row + min(e, E - 1));
+        if (!on || e >= E) v[u][i] = -__builtin_inff();
       }
     }
-    float ex[PER], s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const bool in = live && i * 64 + lane < E;
-      ex[i] = in ? exp_neg(v[i] - top) : 0.0f;
-      s += ex[i];
-    }
-    s = wave_sum(s);
-    float w = idx >= 0 ? exp_neg(chosen - top) : 0.0f;
-    const float den = a.renorm ? wave_sum(w) + (s - s) : s;     // s - s: a NaN in the row stays
-    if (lane < a.k) {
-      a.index[(int64_t)t * a.k + lane] = idx;
-      a.weight[(int64_t)t * a.k + lane] = idx >= 0 ? w / den : 0.0f;
-      if (idx >= 0) atomicAdd(&sh.hist[idx], 1);
-    }
-    if (live && lane == 0) atomicAdd(&sh.live, 1);
-    if (a.loss != nullptr && live) {
-      const float r = 1.0f / s;
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < PER; ++i) psum[i] += ex[i] * r;
+      for (int i = 0; i < PER; ++i) key[u][i] = key_of(v[u][i]);
+    int idx[U];                   // lane j: the j-th choice
+    uint32_t chosen[U], top[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      idx[u] = -1;
+      chosen[u] = 0;
+      top[u] = 0;
+    }
+    for (int j = 0; j < k; ++j) {
+      uint32_t m[U], any = 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        m[u] = key[u][0];
+#pragma unroll
+        for (int i = 1; i < PER; ++i) m[u] = max(m[u], key[u][i]);
+      }
+      wave_max_all(m);
+#pragma unroll
+      for (int u = 0; u < U; ++u) any = max(any, m[u]);
+      if (any <= kNoKey) break;   // uniform
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (m[u] <= kNoKey) m[u] = 0xFFFFFFFFu;      // nothing left: matches no key
+        int found = -1;
+#pragma unroll
+        for (int i = PER - 1; i >= 0; --i) {
+          const u64 b = __ballot(key[u][i] == m[u]);
+          if (b) found = i * 64 + __ffsll(b) - 1;
+        }
+        const int away = found - lane;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) key[u][i] = away == i * 64 ? 0u : key[u][i];
+        if (j == 0) top[u] = m[u];
+        if (lane == j) {
+          idx[u] = found;
+          chosen[u] = m[u];
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = tb + u;
+      if (t >= t1) break;         // uniform
+      const bool live = top[u] != 0 && top[u] != 0xFFFFFFFFu;
+      const float mx = of_key(top[u]);
+      float ex[PER], s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        ex[i] = live && i * 64 + lane < E ? exp_neg(v[u][i] - mx) : 0.0f;
+        s += ex[i];
+      }
+      s = wave_sum(s);
+      const float w = idx[u] >= 0 ? exp_neg(of_key(chosen[u]) - mx) : 0.0f;
+      const float den = a.renorm ? wave_sum(w) + (s - s) : s;     // s - s: a NaN in the row stays
+      if (lane < k) {
+        a.index[(int64_t)t * k + lane] = idx[u];
+        a.weight[(int64_t)t * k + lane] = idx[u] >= 0 ? w / den : 0.0f;
+        if (idx[u] >= 0) atomicAdd(&sh.hist[idx[u]], 1);
+        if (keep) sh.index[(t - t0) * k + lane] = idx[u];
+      }
+      if (live && lane == 0) atomicAdd(&sh.live, 1);
+      if (a.loss != nullptr && live) {
+        const float r = 1.0f / s;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) psum[i] += ex[i] * r;
+      }
     }
   }
   if (a.loss != nullptr) {
@@ -254,22 +307,28 @@ __device__ void write_loss(const RouteArgs& a, Shared& sh, float p, int live) {
 
 // Order of the slots of tokens [t0, t1): sh.base holds the position of each
 // expert's next slot, sh.unused_base that of the next slot without one.
-__device__ void place(const RouteArgs& a, Shared& sh, int t0, int t1) {
+// `kept`: sh.index already has the choices (64 tokens at most).
+__device__ void place(const RouteArgs& a, Shared& sh, int t0, int t1, bool kept) {
+  const int k = a.k;
+  // s / k for s < 64 * 32: the multiplier's error stays below 1 / k
+  const uint32_t inv = (65536u + k - 1) / k;
   for (int tb = t0; tb < t1; tb += 64) {
     const int nt = min(t1 - tb, 64);
-    const int slots = nt * a.k;
+    const int slots = nt * k;
     for (int e = threadIdx.x; e < a.E; e += kThreads) sh.mask[e] = 0;
+    if (!kept)
+      for (int s = threadIdx.x; s < slots; s += kThreads)
+        sh.index[s] = a.index[(int64_t)tb * k + s];
     __syncthreads();
-    const int32_t* index = a.index + (int64_t)tb * a.k;
     for (int s = threadIdx.x; s < slots; s += kThreads) {
-      const int e = index[s];
-      if (e >= 0) atomicOr(&sh.mask[e], 1ull << (s / a.k));
+      const int e = sh.index[s];
+      if (e >= 0) atomicOr(&sh.mask[e], 1ull << (s * inv >> 16));
     }
     if (threadIdx.x < 64) {
-      // slots without an expert before each token
+      // slots without an expert before each token: its last ones
       int n = 0;
       if ((int)threadIdx.x < nt)
-        for (int j = 0; j < a.k; ++j) n += index[threadIdx.x * a.k + j] < 0;
+        for (int j = k - 1; j >= 0 && sh.index[threadIdx.x * k + j] < 0; --j) ++n;
       const int incl = wave_scan(n);
       sh.unused[threadIdx.x] = sh.unused_base + incl - n;
       __builtin_amdgcn_wave_barrier();
@@ -277,17 +336,17 @@ __device__ void place(const RouteArgs& a, Shared& sh, int t0, int t1) {
     }
     __syncthreads();
     for (int s = threadIdx.x; s < slots; s += kThreads) {
-      const int t = s / a.k, e = index[s];
+      const int t = s * inv >> 16, e = sh.index[s];
       int at;
       if (e >= 0) {
         at = sh.base[e] + __popcll(sh.mask[e] & ((1ull << t) - 1));
       } else {
-        // the slots without an expert are a token's last ones
         at = sh.unused[t];
-        for (int j = s - t * a.k - 1; j >= 0 && index[t * a.k + j] < 0; --j) ++at;
+        for (int j = s - 1; j >= t * k && sh.index[j] < 0; --j) ++at;
       }
-      a.order[at] = tb * a.k + s;
+      a.order[at] = tb * k + s;
     }
+    if (tb + 64 >= t1) break;
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += kThreads) sh.base[e] += __popcll(sh.mask[e]);
     __syncthreads();
@@ -296,7 +355,7 @@ __device__ void place(const RouteArgs& a, Shared& sh, int t0, int t1) {
 
 // First launch: one block of tokens per workgroup.  With one block in all,
 // it also writes the rest.
-template <typename T, int PER>
+template <typename T, int PER, int U>
 __global__ void __launch_bounds__(kThreads) route_choose(RouteArgs a) {
   __shared__ Shared sh;
   extern __shared__ float prob[];       // [kWaves][E], loss only
@@ -307,7 +366,7 @@ __global__ void __launch_bounds__(kThreads) route_choose(RouteArgs a) {
   if (threadIdx.x == 0) sh.live = 0;
   __syncthreads();
   const int t0 = blockIdx.x * a.block, t1 = min(a.T, t0 + a.block);
-  choose<T, PER>(a, sh, prob, t0, t1);
+  choose<T, PER, U>(a, sh, prob, t0, t1, gridDim.x == 1);
   __syncthreads();
   const int e = threadIdx.x;
   if (gridDim.x > 1) {
@@ -324,48 +383,59 @@ __global__ void __launch_bounds__(kThreads) route_choose(RouteArgs a) {
   if (a.loss != nullptr) write_loss(a, sh, e < a.E ? prob_of(prob, a.E, e) : 0.0f, sh.live);
   if (e == 0) sh.unused_base = sh.used;
   __syncthreads();
-  place(a, sh, t0, t1);
+  place(a, sh, t0, t1, true);
 }
 
 // Second launch: workgroups 1.. place one block's slots each; workgroup 0
 // writes counts, offsets and the loss.
 __global__ void __launch_bounds__(kThreads) route_place(RouteArgs a) {
   __shared__ Shared sh;
-  __shared__ float part[kThreads];
+  extern __shared__ float dyn[];          // kThreads * 16 floats
   const int blocks = gridDim.x - 1;
   const int me = (int)blockIdx.x - 1;     // -1: counts and loss
-  for (int e = threadIdx.x; e < a.E; e += kThreads) {
-    sh.total[e] = 0;
-    sh.base[e] = 0;
-  }
-  if (threadIdx.x == 0) sh.live = 0;
-  __syncthreads();
-  // column sums of the blocks' counts: 8 experts to a thread, rows shared out
+  // column sums of the blocks' counts: 8 experts to a thread, rows shared out,
+  // eight rows' loads in flight; then over the row shares
   const int cols = a.hist_ld / 8;
   const int rows = kThreads / cols;
   const int col = threadIdx.x % cols, r0 = threadIdx.x / cols;
+  int2* const share = reinterpret_cast<int2*>(dyn);      // [rows][cols * 8]
   if (r0 < rows) {
     int all[8] = {}, mine[8] = {};
-    for (int b = r0; b < blocks; b += rows) {
-      const uint4 v = *reinterpret_cast<const uint4*>(a.hist + (int64_t)b * a.hist_ld + col * 8);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      const uint32_t before = b < me ? 0xFFFFu : 0u;
+    for (int b0 = r0; b0 < blocks; b0 += 8 * rows) {
+      uint4 v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t c = i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu;
-        all[i] += c;
-        mine[i] += c & before;
+      for (int u = 0; u < 8; ++u)
+        v[u] = *reinterpret_cast<const uint4*>(
+            a.hist + (int64_t)min(b0 + u * rows, blocks - 1) * a.hist_ld + col * 8);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int b = b0 + u * rows;
+        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        const uint32_t in = b < blocks ? 0xFFFFu : 0u, before = b < me ? 0xFFFFu : 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t c = i & 1 ? w[i / 2] >> 16 : w[i / 2];
+          all[i] += c & in;
+          mine[i] += c & before;
+        }
       }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int e = col * 8 + i;
-      if (e < a.E) {
-        atomicAdd(&sh.total[e], all[i]);
-        atomicAdd(&sh.base[e], mine[i]);
-      } else if (e == a.E) {
-        atomicAdd(&sh.live, all[i]);
-      }
+    for (int i = 0; i < 8; ++i) share[r0 * cols * 8 + col * 8 + i] = make_int2(all[i], mine[i]);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e <= a.E; e += kThreads) {
+    int all = 0, mine = 0;
+    for (int r = 0; r < rows; ++r) {
+      const int2 c = share[r * cols * 8 + e];
+      all += c.x;
+      mine += c.y;
+    }
+    if (e < a.E) {
+      sh.total[e] = all;
+      sh.base[e] = me < 0 ? 0 : mine;
+    } else {
+      sh.live = all;
     }
   }
   __syncthreads();
@@ -377,13 +447,19 @@ __global__ void __launch_bounds__(kThreads) route_place(RouteArgs a) {
     while (width < a.E) width *= 2;
     const int seg = kThreads / width, e = threadIdx.x & (width - 1), s0 = threadIdx.x / width;
     float p = 0.0f;
-    if (e < a.E)
-      for (int b = s0; b < blocks; b += seg) p += a.prob[(int64_t)b * a.E + e];
-    part[threadIdx.x] = p;
+    for (int b0 = s0; b0 < blocks; b0 += 16 * seg) {
+      float v[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u)
+        v[u] = a.prob[(int64_t)min(b0 + u * seg, blocks - 1) * a.E + min(e, a.E - 1)];
+#pragma unroll
+      for (int u = 0; u < 16; ++u) p += b0 + u * seg < blocks ? v[u] : 0.0f;
+    }
+    dyn[threadIdx.x] = p;
     __syncthreads();
     p = 0.0f;
     if ((int)threadIdx.x < a.E)
-      for (int s = 0; s < seg; ++s) p += part[s * width + threadIdx.x];
+      for (int s = 0; s < seg; ++s) p += dyn[s * width + threadIdx.x];
     write_loss(a, sh, p, sh.live);
     return;
   }
@@ -399,110 +475,139 @@ __global__ void __launch_bounds__(kThreads) route_place(RouteArgs a) {
   const int t0 = me * a.block, t1 = min(a.T, t0 + a.block);
   if (threadIdx.x == 0) sh.unused_base = sh.used + t0 * a.k - used_before;
   __syncthreads();
-  place(a, sh, t0, t1);
+  place(a, sh, t0, t1, false);
 }
 
 // Gradient of the logits, one wave per token:
 //   d_e = p_e (c_e - sum p c) + [plain] p_e (g_e - sum_j w_j dw_j)
 //       + [renormalised] w_j (dw_j - sum w dw) at e = index[j],
 // c_e = dloss * alpha * E * counts_e / (k L^2), g_e = dw_j at e = index[j].
-template <typename T, int PER>
+// A wave takes U tokens at a time, all their loads first; the chosen experts'
+// part goes through a row of LDS of the wave's own.
+template <typename T, int PER, int U>
 __global__ void __launch_bounds__(256) route_backward(RouteBackArgs a) {
+  extern __shared__ float dyn[];          // [4][E]
   const int lane = threadIdx.x & 63;
-  const int E = a.E;
-  float c[PER];
-  {
-    float f = 0.0f;
+  const int E = a.E, k = a.k;
+  float* const add_row = dyn + (threadIdx.x >> 6) * E;
+  const int waves = gridDim.x * 4;
+  for (int tb = (blockIdx.x * 4 + (threadIdx.x >> 6)) * U; tb < a.T; tb += waves * U) {
+    float v[U][PER], w[U], dw[U];
+    int idx[U];
+    bool on[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = min(tb + u, a.T - 1);
+      const T* row = static_cast<const T*>(a.logits) + (int64_t)t * a.ldl;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) v[u][i] = load_logit(row + min(i * 64 + lane, E - 1));
+      const int64_t at = (int64_t)t * k + min(lane, k - 1);
+      idx[u] = a.index[at];
+      w[u] = dw[u] = 0.0f;
+      if (a.dweight != nullptr) {
+        w[u] = a.weight[at];
+        dw[u] = a.dweight[at];
+      }
+      on[u] = a.mask == nullptr || a.mask[t] != 0;
+    }
+    float c[PER], f = 0.0f;
     if (a.dloss != nullptr) {
       const float n = (float)max(a.live[0], 1);
-      f = a.dloss[0] * (a.alpha * (float)E / (float)a.k) / n / n;
+      f = a.dloss[0] * (a.alpha * (float)E / (float)k) / n / n;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) c[i] = f * (float)a.counts[min(i * 64 + lane, E - 1)];
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) c[i] = 0.0f;
     }
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = i * 64 + lane;
-      c[i] = a.dloss != nullptr && e < E ? f * (float)a.counts[e] : 0.0f;
+    for (int u = 0; u < U; ++u) {
+      const int t = tb + u;
+      if (t >= a.T) break;        // uniform
+      T* out = static_cast<T*>(a.dlogits) + (int64_t)t * a.ldd;
+      if (lane >= k || idx[u] >= E) idx[u] = -1;
+      if (idx[u] < 0) w[u] = dw[u] = 0.0f;
+      const bool live = on[u] && __builtin_amdgcn_readlane(idx[u], 0) >= 0;
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if (i * 64 + lane >= E) v[u][i] = -__builtin_inff();
+        m = max(m, key_of(v[u][i]));
+      }
+      const float top = of_key(wave_max(m));
+      float s = 0.0f, pc = 0.0f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        v[u][i] = i * 64 + lane < E ? exp_neg(v[u][i] - top) : 0.0f;
+        s += v[u][i];
+        pc += v[u][i] * c[i];
+      }
+      s = wave_sum(s);
+      const float r = 1.0f / s;
+      const float dot = wave_sum(w[u] * dw[u]);
+      const float sub = wave_sum(pc) * r + (a.renorm ? 0.0f : dot);
+      if (a.dweight != nullptr) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (i * 64 + lane < E) add_row[i * 64 + lane] = 0.0f;
+        order_lds();
+        if (idx[u] >= 0) add_row[idx[u]] = w[u] * (a.renorm ? dw[u] - dot : dw[u]);
+        order_lds();
+      }
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if (i * 64 + lane >= E) continue;
+        float d = v[u][i] * r * (c[i] - sub);
+        if (a.dweight != nullptr) d += add_row[i * 64 + lane];
+        store_grad(out + i * 64 + lane, live ? d : 0.0f);
+      }
+      order_lds();
     }
   }
-  const int waves = gridDim.x * 4;
-  for (int t = blockIdx.x * 4 + (threadIdx.x >> 6); t < a.T; t += waves) {
-    const T* row = static_cast<const T*>(a.logits) + (int64_t)t * a.ldl;
-    T* out = static_cast<T*>(a.dlogits) + (int64_t)t * a.ldd;
-    const bool on = a.mask == nullptr || a.mask[t] != 0;
-    int idx = -1;
-    float w = 0.0f, dw = 0.0f;
-    if (lane < a.k) {
-      idx = a.index[(int64_t)t * a.k + lane];
-      if (idx >= E) idx = -1;
-      if (a.dweight != nullptr && idx >= 0) {
-        w = a.weight[(int64_t)t * a.k + lane];
-        dw = a.dweight[(int64_t)t * a.k + lane];
-      }
-    }
-    const bool live = on && __builtin_amdgcn_readlane(idx, 0) >= 0;
-    if (!live) {
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (i * 64 + lane < E) store_grad(out + i * 64 + lane, 0.0f);
-      continue;
-    }
-    float v[PER];
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = i * 64 + lane;
-      v[i] = e < E ? load_logit(row + e) : -__builtin_inff();
-      m = max(m, key_of(v[i]));
-    }
-    const float top = of_key(wave_max(m));
-    float s = 0.0f, pc = 0.0f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      v[i] = i * 64 + lane < E ? exp_neg(v[i] - top) : 0.0f;
-      s += v[i];
-      pc += v[i] * c[i];
-    }
-    s = wave_sum(s);
-    const float r = 1.0f / s;
-    const float dot = wave_sum(w * dw);
-    const float sub = wave_sum(pc) * r + (a.renorm ? 0.0f : dot);
-    float d[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) d[i] = v[i] * r * (c[i] - sub);
-    const float add = w * (a.renorm ? dw - dot : dw);
-    if (a.dweight != nullptr) {
-      for (int j = 0; j < a.k; ++j) {
-        const int e = __builtin_amdgcn_readlane(idx, j);
-        const float g = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(add), j));
-#pragma unroll
-        for (int i = 0; i < PER; ++i) d[i] += e == i * 64 + lane ? g : 0.0f;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (i * 64 + lane < E) store_grad(out + i * 64 + lane, d[i]);
-  }
+}
+
+// Tokens a wave takes at a time: as many chains as registers allow.
+template <int PER> constexpr int kTokens = PER <= 4 ? 4 : PER <= 8 ? 2 : 1;
+
+template <typename T, int PER>
+void launch_choose_per(const RouteArgs& a, int blocks, hipStream_t st) {
+  const size_t lds = a.loss != nullptr ? (size_t)kWaves * a.E * 4 : 0;
+  // with few tokens to a workgroup every wave takes one
+  if (a.T <= kWaves)
+    hipLaunchKernelGGL((route_choose<T, PER, 1>), dim3(blocks), dim3(kThreads), lds, st, a);
+  else
+    hipLaunchKernelGGL((route_choose<T, PER, kTokens<PER>>), dim3(blocks), dim3(kThreads), lds, st,
+                       a);
+}
+
+template <typename T, int PER>
+void launch_backward_per(const RouteBackArgs& a, hipStream_t st) {
+  // two tokens a wave where that still leaves 4 waves to a SIMD
+  constexpr int U = PER <= 8 ? 2 : 1;
+  const size_t lds = a.dweight != nullptr ? (size_t)4 * a.E * 4 : 0;
+  if (a.T <= 4096 || U == 1)
+    hipLaunchKernelGGL((route_backward<T, PER, 1>), dim3((a.T + 3) / 4), dim3(256), lds, st, a);
+  else
+    hipLaunchKernelGGL((route_backward<T, PER, U>), dim3((a.T + 4 * U - 1) / (4 * U)), dim3(256),
+                       lds, st, a);
 }
 
 template <typename T>
 void launch_choose(const RouteArgs& a, int blocks, hipStream_t st) {
-  const size_t lds = a.loss != nullptr ? (size_t)kWaves * a.E * 4 : 0;
-  const dim3 g(blocks), b(kThreads);
-  if (a.E <= 64) hipLaunchKernelGGL((route_choose<T, 1>), g, b, lds, st, a);
-  else if (a.E <= 128) hipLaunchKernelGGL((route_choose<T, 2>), g, b, lds, st, a);
-  else if (a.E <= 256) hipLaunchKernelGGL((route_choose<T, 4>), g, b, lds, st, a);
-  else if (a.E <= 512) hipLaunchKernelGGL((route_choose<T, 8>), g, b, lds, st, a);
-  else hipLaunchKernelGGL((route_choose<T, 16>), g, b, lds, st, a);
+  if (a.E <= 64) launch_choose_per<T, 1>(a, blocks, st);
+  else if (a.E <= 128) launch_choose_per<T, 2>(a, blocks, st);
+  else if (a.E <= 256) launch_choose_per<T, 4>(a, blocks, st);
+  else if (a.E <= 512) launch_choose_per<T, 8>(a, blocks, st);
+  else launch_choose_per<T, 16>(a, blocks, st);
 }
 
 template <typename T>
 void launch_backward(const RouteBackArgs& a, hipStream_t st) {
-  const int blocks = (a.T + 3) / 4 < 4096 ? (a.T + 3) / 4 : 4096;
-  const dim3 g(blocks), b(256);
-  if (a.E <= 64) hipLaunchKernelGGL((route_backward<T, 1>), g, b, 0, st, a);
-  else if (a.E <= 128) hipLaunchKernelGGL((route_backward<T, 2>), g, b, 0, st, a);
-  else if (a.E <= 256) hipLaunchKernelGGL((route_backward<T, 4>), g, b, 0, st, a);
-  else if (a.E <= 512) hipLaunchKernelGGL((route_backward<T, 8>), g, b, 0, st, a);
-  else hipLaunchKernelGGL((route_backward<T, 16>), g, b, 0, st, a);
+  if (a.E <= 64) launch_backward_per<T, 1>(a, st);
+  else if (a.E <= 128) launch_backward_per<T, 2>(a, st);
+  else if (a.E <= 256) launch_backward_per<T, 4>(a, st);
+  else if (a.E <= 512) launch_backward_per<T, 8>(a, st);
+  else launch_backward_per<T, 16>(a, st);
 }
 
 }  // namespace
@@ -511,7 +616,7 @@ int launch_route(const RouteArgs& a, int blocks, void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (a.dtype == BSMM_BF16) launch_choose<uint16_t>(a, blocks, st);
   else launch_choose<float>(a, blocks, st);
-  if (blocks > 1) hipLaunchKernelGGL(route_place, dim3(blocks + 1), dim3(kThreads), 0, st, a);
+  if (blocks > 1) hipLaunchKernelGGL(route_place, dim3(blocks + 1), dim3(kThreads), kThreads * 64, st, a);
   return hipGetLastError() == hipSuccess ? 0 : 1;
 }
 
