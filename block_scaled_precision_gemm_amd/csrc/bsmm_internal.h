@@ -238,7 +238,7 @@ int launch_w4(const W4Args& a, void* ws, void* stream);
 // blocks of `block` (a multiple of 64, at most 65535 tokens); with more than
 // one block, hist [blocks][hist_ld] holds each block's counts and, in column
 // E, its live tokens (hist_ld a multiple of 8 above E), prob [blocks][E] its
-// sums of probabilities.
+// sums of probabilities, before [blocks][E] the slots of the blocks before it.
 constexpr int kRouteMaxE = 1024, kRouteMaxK = 32, kRouteMaxBlocks = 256;
 struct RouteArgs {
   const void* logits; int64_t ldl; bsmm_dtype dtype;
@@ -249,7 +249,7 @@ struct RouteArgs {
   int32_t* live; float* prob_sum; float* loss;
   int T, E, block;
   uint16_t* hist; int hist_ld;
-  float* prob;
+  float* prob; int32_t* before;
 };
 int launch_route(const RouteArgs& a, int blocks, void* stream);
 

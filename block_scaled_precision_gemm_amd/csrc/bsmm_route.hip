@@ -5,19 +5,19 @@
 //   weight[t, j] = p[index], or p[index] / sum_j p[index]
 //   loss = alpha * E / (k L^2) * sum_e counts[e] * prob_sum[e]
 //
-// A wave holds one token's logits in registers, expert i * 64 + lane in
-// element i, so that loads are coalesced whatever the row stride.  The k
-// rounds of the choice are integer maxima over order-preserving keys; ties
-// go to the lowest expert by looking at the ballots of elements 0, 1, ... in
-// turn.
+// A wave holds one token's logits in registers, PER neighbouring experts a
+// lane.  The k rounds of the choice are integer maxima over order-preserving
+// keys; of equal keys the lowest lane's, and in a lane the lowest expert's,
+// is taken.  A lane's keys are sorted once, so that a round looks at its
+// first one only.
 //
 // The order of the slots is a stable counting sort.  A token's choices are
 // distinct experts, so 64 tokens make one 64-bit mask per expert, and a
 // slot's rank among them is the number of mask bits below its token: no
-// atomic's order can change a result.  Blocks of tokens write their counts,
-// and a second launch gives every block its bases from all blocks' counts.
-// At most kMaxBlocks blocks (one per compute unit) keep that table small;
-// more tokens make larger blocks.
+// atomic's order can change a result.  Blocks of tokens write their counts, a
+// second launch sums them over the blocks before each, and a third places the
+// slots.  At most one block per compute unit keeps that table small; more
+// tokens make larger blocks.  Up to 64 tokens are one block and one launch.
 
 #include <hip/hip_runtime.h>
 
@@ -151,24 +151,42 @@ __device__ void choose(const RouteArgs& a, Shared& sh, float* prob, int t0, int 
   const int E = a.E, k = a.k;
   float psum[PER] = {};
   for (int tb = t0 + wave * U; tb < t1; tb += kWaves * U) {
+    // all loads before their first use; lane u has token u's mask
+    const int tu = tb + (lane & (U - 1));
+    const int open = tu < t1 && (a.mask == nullptr || a.mask[min(tu, t1 - 1)] != 0);
     float v[U][PER];
     uint32_t key[U][PER];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int t = min(tb + u, t1 - 1);
-      const T* row = static_cast<const T*>(a.logits) + (int64_t)t * a.ldl;
-      const bool on = tb + u < t1 && (a.mask == nullptr || a.mask[t] != 0);
+      const T* row = static_cast<const T*>(a.logits) + (int64_t)min(tb + u, t1 - 1) * a.ldl;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int e = i * 64 + lane;
-        v[u][i] = load_logit(row + min(e, E - 1));
-        if (!on || e >= E) v[u][i] = -__builtin_inff();
-      }
+      for (int i = 0; i < PER; ++i) v[u][i] = load_logit(row + min(lane * PER + i, E - 1));
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool on = __builtin_amdgcn_readlane(open, u) != 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        v[u][i] = on && lane * PER + i < E ? v[u][i] : -__builtin_inff();
+    }
+    // stable insertion sort of a lane's keys, largest first; id: their places
+    uint32_t id[U][PER];
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < PER; ++i) key[u][i] = key_of(v[u][i]);
+      for (int i = 0; i < PER; ++i) {
+        key[u][i] = key_of(v[u][i]);
+        id[u][i] = i;
+#pragma unroll
+        for (int j = i; j > 0; --j) {
+          const bool up = key[u][j] > key[u][j - 1];
+          const uint32_t k0 = key[u][j - 1], k1 = key[u][j], i0 = id[u][j - 1], i1 = id[u][j];
+          key[u][j - 1] = up ? k1 : k0;
+          key[u][j] = up ? k0 : k1;
+          id[u][j - 1] = up ? i1 : i0;
+          id[u][j] = up ? i0 : i1;
+        }
+      }
     int idx[U];                   // lane j: the j-th choice
     uint32_t chosen[U], top[U];
 #pragma unroll
@@ -180,27 +198,24 @@ __device__ void choose(const RouteArgs& a, Shared& sh, float* prob, int t0, int 
     for (int j = 0; j < k; ++j) {
       uint32_t m[U], any = 0;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        m[u] = key[u][0];
-#pragma unroll
-        for (int i = 1; i < PER; ++i) m[u] = max(m[u], key[u][i]);
-      }
+      for (int u = 0; u < U; ++u) m[u] = key[u][0];
       wave_max_all(m);
 #pragma unroll
       for (int u = 0; u < U; ++u) any = max(any, m[u]);
       if (any <= kNoKey) break;   // uniform
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (m[u] <= kNoKey) m[u] = 0xFFFFFFFFu;      // nothing left: matches no key
-        int found = -1;
+        if (m[u] <= kNoKey) continue;       // uniform: this token has none left
+        const int from = __ffsll((u64)__ballot(key[u][0] == m[u])) - 1;
+        const int found = from * PER + __builtin_amdgcn_readlane((int)id[u][0], from);
+        if (lane == from) {
 #pragma unroll
-        for (int i = PER - 1; i >= 0; --i) {
-          const u64 b = __ballot(key[u][i] == m[u]);
-          if (b) found = i * 64 + __ffsll(b) - 1;
+          for (int i = 0; i + 1 < PER; ++i) {
+            key[u][i] = key[u][i + 1];
+            id[u][i] = id[u][i + 1];
+          }
+          key[u][PER - 1] = 0;
         }
-        const int away = found - lane;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) key[u][i] = away == i * 64 ? 0u : key[u][i];
         if (j == 0) top[u] = m[u];
         if (lane == j) {
           idx[u] = found;
@@ -212,16 +227,18 @@ __device__ void choose(const RouteArgs& a, Shared& sh, float* prob, int t0, int 
     for (int u = 0; u < U; ++u) {
       const int t = tb + u;
       if (t >= t1) break;         // uniform
-      const bool live = top[u] != 0 && top[u] != 0xFFFFFFFFu;
-      const float mx = of_key(top[u]);
+      const bool live = top[u] != 0;
+      // -inf stands in all places without a logit: its exponential is 0
+      const float mx = live ? of_key(top[u]) : 0.0f;
       float ex[PER], s = 0.0f;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        ex[i] = live && i * 64 + lane < E ? exp_neg(v[u][i] - mx) : 0.0f;
+        ex[i] = exp_neg(v[u][i] - mx);
         s += ex[i];
       }
       s = wave_sum(s);
-      const float w = idx[u] >= 0 ? exp_neg(of_key(chosen[u]) - mx) : 0.0f;
+      const float we = exp_neg(of_key(chosen[u]) - mx);
+      const float w = idx[u] >= 0 ? we : 0.0f;
       const float den = a.renorm ? wave_sum(w) + (s - s) : s;     // s - s: a NaN in the row stays
       if (lane < k) {
         a.index[(int64_t)t * k + lane] = idx[u];
@@ -240,7 +257,7 @@ __device__ void choose(const RouteArgs& a, Shared& sh, float* prob, int t0, int 
   if (a.loss != nullptr) {
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      if (i * 64 + lane < E) prob[wave * E + i * 64 + lane] = psum[i];
+      if (lane * PER + i < E) prob[wave * E + lane * PER + i] = psum[i];
   }
 }
 
@@ -315,12 +332,12 @@ __device__ void place(const RouteArgs& a, Shared& sh, int t0, int t1, bool kept)
   for (int tb = t0; tb < t1; tb += 64) {
     const int nt = min(t1 - tb, 64);
     const int slots = nt * k;
-    for (int e = threadIdx.x; e < a.E; e += kThreads) sh.mask[e] = 0;
+    for (int e = threadIdx.x; e < a.E; e += (int)blockDim.x) sh.mask[e] = 0;
     if (!kept)
-      for (int s = threadIdx.x; s < slots; s += kThreads)
+      for (int s = threadIdx.x; s < slots; s += (int)blockDim.x)
         sh.index[s] = a.index[(int64_t)tb * k + s];
     __syncthreads();
-    for (int s = threadIdx.x; s < slots; s += kThreads) {
+    for (int s = threadIdx.x; s < slots; s += (int)blockDim.x) {
       const int e = sh.index[s];
       if (e >= 0) atomicOr(&sh.mask[e], 1ull << (s * inv >> 16));
     }
@@ -335,7 +352,7 @@ __device__ void place(const RouteArgs& a, Shared& sh, int t0, int t1, bool kept)
       if (threadIdx.x == 63) sh.unused_base += incl;
     }
     __syncthreads();
-    for (int s = threadIdx.x; s < slots; s += kThreads) {
+    for (int s = threadIdx.x; s < slots; s += (int)blockDim.x) {
       const int t = s * inv >> 16, e = sh.index[s];
       int at;
       if (e >= 0) {
@@ -348,7 +365,7 @@ __device__ void place(const RouteArgs& a, Shared& sh, int t0, int t1, bool kept)
     }
     if (tb + 64 >= t1) break;
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kThreads) sh.base[e] += __popcll(sh.mask[e]);
+    for (int e = threadIdx.x; e < a.E; e += (int)blockDim.x) sh.base[e] += __popcll(sh.mask[e]);
     __syncthreads();
   }
 }
@@ -386,94 +403,110 @@ __global__ void __launch_bounds__(kThreads) route_choose(RouteArgs a) {
   place(a, sh, t0, t1, true);
 }
 
-// Second launch: workgroups 1.. place one block's slots each; workgroup 0
-// writes counts, offsets and the loss.
-__global__ void __launch_bounds__(kThreads) route_place(RouteArgs a) {
-  __shared__ Shared sh;
-  extern __shared__ float dyn[];          // kThreads * 16 floats
-  const int blocks = gridDim.x - 1;
-  const int me = (int)blockIdx.x - 1;     // -1: counts and loss
-  // column sums of the blocks' counts: 8 experts to a thread, rows shared out,
-  // eight rows' loads in flight; then over the row shares
-  const int cols = a.hist_ld / 8;
-  const int rows = kThreads / cols;
-  const int col = threadIdx.x % cols, r0 = threadIdx.x / cols;
-  int2* const share = reinterpret_cast<int2*>(dyn);      // [rows][cols * 8]
-  if (r0 < rows) {
-    int all[8] = {}, mine[8] = {};
-    for (int b0 = r0; b0 < blocks; b0 += 8 * rows) {
-      uint4 v[8];
+// Second launch, a wave per expert (and one for the live tokens): the slots
+// of the expert in the blocks before each block, in all, and the sum of the
+// blocks' probabilities.
+__global__ void __launch_bounds__(256) route_scan(RouteArgs a, int blocks) {
+  constexpr int Q = kRouteMaxBlocks / 64;
+  const int lane = threadIdx.x & 63;
+  const int e = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (e > a.E) return;
+  int n[Q];
+  float p[Q];
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        v[u] = *reinterpret_cast<const uint4*>(
-            a.hist + (int64_t)min(b0 + u * rows, blocks - 1) * a.hist_ld + col * 8);
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int b = b0 + u * rows;
-        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-        const uint32_t in = b < blocks ? 0xFFFFu : 0u, before = b < me ? 0xFFFFu : 0u;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t c = i & 1 ? w[i / 2] >> 16 : w[i / 2];
-          all[i] += c & in;
-          mine[i] += c & before;
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) share[r0 * cols * 8 + col * 8 + i] = make_int2(all[i], mine[i]);
+  for (int q = 0; q < Q; ++q) {
+    const int b = min(lane * Q + q, blocks - 1);
+    n[q] = a.hist[(int64_t)b * a.hist_ld + e];
+    p[q] = a.loss != nullptr && e < a.E ? a.prob[(int64_t)b * a.E + e] : 0.0f;
   }
-  __syncthreads();
-  for (int e = threadIdx.x; e <= a.E; e += kThreads) {
-    int all = 0, mine = 0;
-    for (int r = 0; r < rows; ++r) {
-      const int2 c = share[r * cols * 8 + e];
-      all += c.x;
-      mine += c.y;
-    }
-    if (e < a.E) {
-      sh.total[e] = all;
-      sh.base[e] = me < 0 ? 0 : mine;
-    } else {
-      sh.live = all;
-    }
+  int sum = 0;
+  float ps = 0.0f;
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    if (lane * Q + q >= blocks) n[q] = 0, p[q] = 0.0f;
+    sum += n[q];
+    ps += p[q];
   }
-  __syncthreads();
-  if (me < 0) {
-    expert_offsets(a, sh, true);
-    if (a.loss == nullptr) return;
-    // the blocks' sums of probabilities: `seg` threads to an expert
-    int width = 64;
-    while (width < a.E) width *= 2;
-    const int seg = kThreads / width, e = threadIdx.x & (width - 1), s0 = threadIdx.x / width;
-    float p = 0.0f;
-    for (int b0 = s0; b0 < blocks; b0 += 16 * seg) {
-      float v[16];
-#pragma unroll
-      for (int u = 0; u < 16; ++u)
-        v[u] = a.prob[(int64_t)min(b0 + u * seg, blocks - 1) * a.E + min(e, a.E - 1)];
-#pragma unroll
-      for (int u = 0; u < 16; ++u) p += b0 + u * seg < blocks ? v[u] : 0.0f;
-    }
-    dyn[threadIdx.x] = p;
-    __syncthreads();
-    p = 0.0f;
-    if ((int)threadIdx.x < a.E)
-      for (int s = 0; s < seg; ++s) p += dyn[s * width + threadIdx.x];
-    write_loss(a, sh, p, sh.live);
+  const int incl = wave_scan(sum);
+  ps = wave_sum(ps);
+  const int total = __builtin_amdgcn_readlane(incl, 63);
+  if (e == a.E) {
+    if (lane == 0 && a.loss != nullptr) a.live[0] = total;
     return;
   }
-  // slots without an expert in the blocks before
-  int n = (int)threadIdx.x < a.E ? sh.base[threadIdx.x] : 0;
-  n = wave_scan(n);
-  if ((threadIdx.x & 63) == 63) sh.unused[threadIdx.x >> 6] = n;
+  int before = incl - sum;
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    const int b = lane * Q + q;
+    if (b < blocks) a.before[(int64_t)b * a.E + e] = before;
+    before += n[q];
+  }
+  if (lane == 0) {
+    a.counts[e] = total;
+    if (a.loss != nullptr) a.prob_sum[e] = ps;
+  }
+}
+
+// Third launch: a workgroup places one block's slots; the first one also
+// writes the offsets and the loss.
+__global__ void __launch_bounds__(256) route_place(RouteArgs a) {
+  __shared__ Shared sh;
+  constexpr int PT = kRouteMaxE / 256;       // experts of a thread
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int me = blockIdx.x, E = a.E;
+  const int e0 = threadIdx.x * PT;
+  int n[PT], before[PT], all = 0, prev = 0;
+#pragma unroll
+  for (int i = 0; i < PT; ++i) {
+    const int e = min(e0 + i, E - 1);
+    n[i] = a.counts[e];
+    before[i] = a.before[(int64_t)me * E + e];
+  }
+#pragma unroll
+  for (int i = 0; i < PT; ++i) {
+    if (e0 + i >= E) n[i] = before[i] = 0;
+    all += n[i];
+    prev += before[i];
+  }
+  const int incl = wave_scan(all), pincl = wave_scan(prev);
+  if (lane == 63) {
+    sh.scan[wave] = incl;
+    sh.scan[4 + wave] = pincl;
+  }
   __syncthreads();
-  int used_before = 0;
-  for (int w = 0; w < kWaves; ++w) used_before += sh.unused[w];
-  __syncthreads();
-  expert_offsets(a, sh, false);
+  int off = incl - all, used = 0, used_before = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    if (w < wave) off += sh.scan[w];
+    used += sh.scan[w];
+    used_before += sh.scan[4 + w];
+  }
+#pragma unroll
+  for (int i = 0; i < PT; ++i) {
+    if (e0 + i >= E) break;
+    sh.base[e0 + i] = off + before[i];
+    if (me == 0) a.offsets[e0 + i] = off;
+    off += n[i];
+  }
   const int t0 = me * a.block, t1 = min(a.T, t0 + a.block);
-  if (threadIdx.x == 0) sh.unused_base = sh.used + t0 * a.k - used_before;
+  if (threadIdx.x == 0) {
+    sh.unused_base = used + t0 * a.k - used_before;
+    if (me == 0) a.offsets[E] = used;
+  }
+  if (me == 0 && a.loss != nullptr) {
+    const float live = (float)max(a.live[0], 1);
+    float c = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PT; ++i) {
+      const float p = a.prob_sum[min(e0 + i, E - 1)];
+      if (e0 + i < E) c += ((float)n[i] / live) * (p / live);
+    }
+    c = wave_sum(c);
+    if (lane == 0) sh.sum[wave] = c;
+    __syncthreads();
+    if (threadIdx.x == 0)
+      a.loss[0] = a.alpha * (float)E / (float)a.k * (sh.sum[0] + sh.sum[1] + sh.sum[2] + sh.sum[3]);
+  }
   __syncthreads();
   place(a, sh, t0, t1, false);
 }
@@ -616,7 +649,10 @@ int launch_route(const RouteArgs& a, int blocks, void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (a.dtype == BSMM_BF16) launch_choose<uint16_t>(a, blocks, st);
   else launch_choose<float>(a, blocks, st);
-  if (blocks > 1) hipLaunchKernelGGL(route_place, dim3(blocks + 1), dim3(kThreads), kThreads * 64, st, a);
+  if (blocks > 1) {
+    hipLaunchKernelGGL(route_scan, dim3(a.E / 4 + 1), dim3(256), 0, st, a, blocks);
+    hipLaunchKernelGGL(route_place, dim3(blocks), dim3(256), 0, st, a);
+  }
   return hipGetLastError() == hipSuccess ? 0 : 1;
 }
 

@@ -53,7 +53,7 @@ extern "C" {
 size_t bsmm_route_workspace_bytes(int64_t T, int64_t E) {
   if (T <= 0 || T > kMaxT || E <= 0 || E > kRouteMaxE) return 0;
   const int blocks = block_count(T);
-  return blocks > 1 ? hist_bytes(blocks, E) + (size_t)blocks * (size_t)E * 4u : 0;
+  return blocks > 1 ? hist_bytes(blocks, E) + (size_t)blocks * (size_t)E * 8u : 0;
 }
 
 bsmm_status bsmm_route_topk(const void* logits, int64_t ldl, bsmm_dtype dtype,
@@ -89,6 +89,7 @@ bsmm_status bsmm_route_topk(const void* logits, int64_t ldl, bsmm_dtype dtype,
   a.prob = need ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
                                            hist_bytes(blocks, E))
                 : nullptr;
+  a.before = reinterpret_cast<int32_t*>(a.prob + (need ? (size_t)blocks * (size_t)E : 0));
   if (launch_route(a, blocks, stream) != 0)
     return fail(BSMM_ERR_HIP, "kernel launch failed (route)");
   return BSMM_OK;
