@@ -235,7 +235,7 @@ int launch_w4(const W4Args& a, void* ws, void* stream);
 // The expert router (bsmm_route.hip).  logits [T, E], row stride ldl; index,
 // weight [T, k] and order [T * k] contiguous; counts [E], offsets [E + 1].
 // loss, live and prob_sum are null together.  Tokens go to workgroups in
-// blocks of `block` (a multiple of 64, at most 65535 tokens); with more than
+// blocks of `block` (16 or a multiple of 64, at most 65535); with more than
 // one block, hist [blocks][hist_ld] holds each block's counts and, in column
 // E, its live tokens (hist_ld a multiple of 8 above E), prob [blocks][E] its
 // sums of probabilities, before [blocks][E] the slots of the blocks before it.

@@ -57,7 +57,8 @@ __device__ __forceinline__ float of_key(uint32_t k) {
 // Wave reductions by row shifts and row broadcasts; the total is lane 63's.
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
-  return max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xF, 0xF, false));
+  // lanes without a source take 0, the identity: one fused instruction
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true));
 }
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   v = dpp_max<0x111>(v);
@@ -145,12 +146,12 @@ struct Shared {
 // dependent wave reductions, and U chains fill each other's gaps (16384 x 256
 // top-8: 19 us with one, see the launch for U).  `keep`: the choices also go
 // to sh.index (64 tokens at most).
-template <typename T, int PER, int U>
+template <typename T, int PER, int U, int W>
 __device__ void choose(const RouteArgs& a, Shared& sh, float* prob, int t0, int t1, bool keep) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int E = a.E, k = a.k;
   float psum[PER] = {};
-  for (int tb = t0 + wave * U; tb < t1; tb += kWaves * U) {
+  for (int tb = t0 + wave * U; tb < t1; tb += W * U) {
     // all loads before their first use; lane u has token u's mask
     const int tu = tb + (lane & (U - 1));
     const int open = tu < t1 && (a.mask == nullptr || a.mask[min(tu, t1 - 1)] != 0);
@@ -262,16 +263,17 @@ __device__ void choose(const RouteArgs& a, Shared& sh, float* prob, int t0, int 
 }
 
 // Sum of the wave rows of prob for expert e.
+template <int W>
 __device__ __forceinline__ float prob_of(const float* prob, int E, int e) {
   float p = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) p += prob[w * E + e];
+  for (int w = 0; w < W; ++w) p += prob[w * E + e];
   return p;
 }
 
-// From sh.total: sh.base[e] += the expert's offset; the number of chosen
-// slots into sh.used.  `write`: also counts and offsets to memory.
-__device__ void expert_offsets(const RouteArgs& a, Shared& sh, bool write) {
+// From sh.total: the experts' offsets into sh.base, the number of chosen
+// slots into sh.used, counts and offsets to memory.
+__device__ void expert_offsets(const RouteArgs& a, Shared& sh) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int e = threadIdx.x;
   const int n = e < a.E ? sh.total[e] : 0;
@@ -286,15 +288,13 @@ __device__ void expert_offsets(const RouteArgs& a, Shared& sh, bool write) {
   }
   const int off = before + incl - n;
   if (e < a.E) {
-    sh.base[e] += off;
-    if (write) {
-      a.counts[e] = n;
-      a.offsets[e] = off;
-    }
+    sh.base[e] = off;
+    a.counts[e] = n;
+    a.offsets[e] = off;
   }
   if (e == 0) {
     sh.used = all;
-    if (write) a.offsets[a.E] = all;
+    a.offsets[a.E] = all;
   }
   __syncthreads();
 }
@@ -370,37 +370,39 @@ __device__ void place(const RouteArgs& a, Shared& sh, int t0, int t1, bool kept)
   }
 }
 
-// First launch: one block of tokens per workgroup.  With one block in all,
-// it also writes the rest.
-template <typename T, int PER, int U>
-__global__ void __launch_bounds__(kThreads) route_choose(RouteArgs a) {
+// First launch: one block of tokens per workgroup of W waves.  ONE: one block
+// in all (W = 16, a thread per expert), which also writes the rest.
+template <typename T, int PER, int U, int W, bool ONE>
+__global__ void __launch_bounds__(W * 64) route_choose(RouteArgs a) {
+  static_assert(!ONE || W == kWaves, "a thread per expert");
   __shared__ Shared sh;
-  extern __shared__ float prob[];       // [kWaves][E], loss only
-  for (int e = threadIdx.x; e < a.E; e += kThreads) {
+  extern __shared__ float prob[];       // [W][E], loss only
+  for (int e = threadIdx.x; e < a.E; e += W * 64) {
     sh.hist[e] = 0;
     sh.base[e] = 0;
   }
   if (threadIdx.x == 0) sh.live = 0;
   __syncthreads();
   const int t0 = blockIdx.x * a.block, t1 = min(a.T, t0 + a.block);
-  choose<T, PER, U>(a, sh, prob, t0, t1, gridDim.x == 1);
+  choose<T, PER, U, W>(a, sh, prob, t0, t1, ONE);
   __syncthreads();
-  const int e = threadIdx.x;
-  if (gridDim.x > 1) {
-    if (e < a.E) {
+  if constexpr (!ONE) {
+    for (int e = threadIdx.x; e < a.E; e += W * 64) {
       a.hist[(int64_t)blockIdx.x * a.hist_ld + e] = (uint16_t)sh.hist[e];
-      if (a.loss != nullptr) a.prob[(int64_t)blockIdx.x * a.E + e] = prob_of(prob, a.E, e);
+      if (a.loss != nullptr) a.prob[(int64_t)blockIdx.x * a.E + e] = prob_of<W>(prob, a.E, e);
     }
-    if (e == 0) a.hist[(int64_t)blockIdx.x * a.hist_ld + a.E] = (uint16_t)sh.live;
-    return;
+    if (threadIdx.x == 0) a.hist[(int64_t)blockIdx.x * a.hist_ld + a.E] = (uint16_t)sh.live;
+  } else {
+    const int e = threadIdx.x;
+    if (e < a.E) sh.total[e] = sh.hist[e];
+    __syncthreads();
+    expert_offsets(a, sh);
+    if (a.loss != nullptr)
+      write_loss(a, sh, e < a.E ? prob_of<W>(prob, a.E, e) : 0.0f, sh.live);
+    if (e == 0) sh.unused_base = sh.used;
+    __syncthreads();
+    place(a, sh, t0, t1, true);
   }
-  if (e < a.E) sh.total[e] = sh.hist[e];
-  __syncthreads();
-  expert_offsets(a, sh, true);
-  if (a.loss != nullptr) write_loss(a, sh, e < a.E ? prob_of(prob, a.E, e) : 0.0f, sh.live);
-  if (e == 0) sh.unused_base = sh.used;
-  __syncthreads();
-  place(a, sh, t0, t1, true);
 }
 
 // Second launch, a wave per expert (and one for the live tokens): the slots
@@ -602,15 +604,20 @@ __global__ void __launch_bounds__(256) route_backward(RouteBackArgs a) {
 // Tokens a wave takes at a time: as many chains as registers allow.
 template <int PER> constexpr int kTokens = PER <= 4 ? 4 : PER <= 8 ? 2 : 1;
 
+template <typename T, int PER, int U, int W, bool ONE>
+void launch_choose_as(const RouteArgs& a, int blocks, hipStream_t st) {
+  const size_t lds = a.loss != nullptr ? (size_t)W * a.E * 4 : 0;
+  hipLaunchKernelGGL((route_choose<T, PER, U, W, ONE>), dim3(blocks), dim3(W * 64), lds, st, a);
+}
+
 template <typename T, int PER>
 void launch_choose_per(const RouteArgs& a, int blocks, hipStream_t st) {
-  const size_t lds = a.loss != nullptr ? (size_t)kWaves * a.E * 4 : 0;
-  // with few tokens to a workgroup every wave takes one
-  if (a.T <= kWaves)
-    hipLaunchKernelGGL((route_choose<T, PER, 1>), dim3(blocks), dim3(kThreads), lds, st, a);
-  else
-    hipLaunchKernelGGL((route_choose<T, PER, kTokens<PER>>), dim3(blocks), dim3(kThreads), lds, st,
-                       a);
+  constexpr int U = kTokens<PER>;
+  // with few tokens every wave takes one; blocks of 16 tokens are 4 waves
+  if (blocks == 1 && a.T <= kWaves) launch_choose_as<T, PER, 1, kWaves, true>(a, blocks, st);
+  else if (blocks == 1) launch_choose_as<T, PER, U, kWaves, true>(a, blocks, st);
+  else if (a.block == 16) launch_choose_as<T, PER, U, 4, false>(a, blocks, st);
+  else launch_choose_as<T, PER, U, kWaves, false>(a, blocks, st);
 }
 
 template <typename T, int PER>

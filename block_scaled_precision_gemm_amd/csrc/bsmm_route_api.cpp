@@ -32,9 +32,13 @@ bsmm_status check_logits(const void* logits, int64_t ld, bsmm_dtype dtype, int64
   return BSMM_OK;
 }
 
+// One block up to 64 tokens; then at most one per compute unit, of 16 tokens
+// while that is enough (4096 tokens: small workgroups on all of the chip), of
+// multiples of 64 beyond.
 int tokens_per_block(int64_t T) {
+  if (T > 64 && T <= 16 * (int64_t)kRouteMaxBlocks) return 16;
   const int64_t per = 64 * (int64_t)kRouteMaxBlocks;
-  return (int)(64 * ((T + per - 1) / per > 1 ? (T + per - 1) / per : 1));
+  return (int)(64 * (T > per ? (T + per - 1) / per : 1));
 }
 int block_count(int64_t T) {
   const int b = tokens_per_block(T);
