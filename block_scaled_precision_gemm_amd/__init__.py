@@ -106,7 +106,7 @@ def load():
     L.bsmm_w4_expert_mm.argtypes = [vp, i64, st, vp, i64, i64, vp, i64, i64, st, vp, i64, i64, st,
                                     vp, vp, st, vp, vp, i64, st, i64, i64, i64, i64, i64, vp, sz,
                                     vp]
-    L.bsmm_w4_workspace_bytes.argtypes = [st, i64, i64, i64, i64]
+    L.bsmm_w4_workspace_bytes.argtypes = [st, i64, i64, i64, i64, i64, st]
     L.bsmm_w4_workspace_bytes.restype = sz
     L.bsmm_route_workspace_bytes.argtypes = [i64, i64]
     L.bsmm_route_workspace_bytes.restype = sz
@@ -872,11 +872,11 @@ def _w4_weight(w, ws, wst, scale, zero, K, u8):
     return group, code, sst, zero.data_ptr(), zst
 
 
-def _w4_workspace(xc, E, R, S, K, dev, stream, handle):
+def _w4_workspace(xc, E, R, S, N, K, group, dev, stream, handle):
     """Workspace pointer and bytes of a 4-bit product (fp32 x, many rows)."""
     if xc != F32:
         return None, 0
-    buf, n = _buffer(load().bsmm_w4_workspace_bytes(xc, E, R, S, K), dev, stream, handle)
+    buf, n = _buffer(load().bsmm_w4_workspace_bytes(xc, E, R, S, N, K, group), dev, stream, handle)
     return (buf.data_ptr(), n) if n else (None, 0)
 
 
@@ -916,7 +916,7 @@ def bsmm_w4_mm(x, w, scale, zero=None, *, out_dtype="bf16", out=None, stream=Non
     dev = x.device
     o, ldo = _w4_out(out, M, N, code, torch, dtypes, dev)
     hs = _stream(stream)
-    wsp, wsn = _w4_workspace(xc, 1, M, M, K, dev, stream, hs)
+    wsp, wsn = _w4_workspace(xc, 1, M, M, N, K, group, dev, stream, hs)
     status = load().bsmm_w4_mm(x.data_ptr(), xst[0], xc, w.data_ptr(), wst[0], scale.data_ptr(),
                                sst[0], sc, zp, zst[0], group, o.data_ptr(), ldo, code, M, N, K,
                                wsp, wsn, hs)
@@ -960,7 +960,7 @@ def bsmm_w4_expert_mm(x, w, scale, zero, order, offsets, *, slots_per_row=1, row
     dev = x.device
     o, ldo = _w4_out(out, S, N, code, torch, dtypes, dev)
     hs = _stream(stream)
-    wsp, wsn = _w4_workspace(xc, E, R, S, K, dev, stream, hs)
+    wsp, wsn = _w4_workspace(xc, E, R, S, N, K, group, dev, stream, hs)
     status = load().bsmm_w4_expert_mm(
         x.data_ptr(), xst[0], xc, w.data_ptr(), wst[0], wst[1], scale.data_ptr(), sst[0], sst[1],
         sc, zp, zst[0], zst[1], group, order.data_ptr(), offsets.data_ptr(), slots_per_row,

@@ -218,19 +218,17 @@ struct W4Args {
   void* out; int64_t ldo; bsmm_dtype out_dtype;
   int E, R, S, N, K;
 };
-// Many rows run on tiles; an fp32 x is then cut into three bf16 planes in the
-// workspace (w4_plane_bytes).  Tiles address x by 32-bit offsets.
+// The kernel for a call: 16 to 32 rows a workgroup (any call), or tiles of 128
+// or 256 rows by 128 columns.  On tiles an fp32 x is cut into three bf16
+// planes in the workspace (w4_plane_bytes), and x is addressed by 32-bit
+// offsets.
+enum class W4Plan { Rows, Tile128, Tile256 };
 inline size_t w4_plane_bytes(const W4Args& a) {
   return a.x_dtype == BSMM_F32 ? (size_t)3 * (size_t)a.R * (size_t)a.K * 2u : 0;
 }
-inline bool w4_tiled(const W4Args& a) {
-  const int64_t rows = a.offsets ? (a.S + a.E - 1) / a.E : a.S;
-  const size_t x = a.x_dtype == BSMM_F32 ? w4_plane_bytes(a)
-                                         : (size_t)a.R * (size_t)a.ldx * 2u;
-  return rows > 64 && a.K > 0 && x < (size_t)0xFFFF0000u;
-}
-// ws: null, or at least w4_plane_bytes bytes (rows on the small kernel then)
-int launch_w4(const W4Args& a, void* ws, void* stream);
+W4Plan w4_plan(const W4Args& a);
+// ws: w4_plane_bytes bytes for an fp32 x on tiles, else not used
+int launch_w4(const W4Args& a, W4Plan plan, void* ws, void* stream);
 
 // The expert router (bsmm_route.hip).  logits [T, E], row stride ldl; index,
 // weight [T, k] and order [T * k] contiguous; counts [E], offsets [E + 1].

@@ -185,7 +185,7 @@ __device__ __forceinline__ void to_lds(const void* src, uint8_t* dst) {
 
 // ---------------------------------------------------------------------------
 // Few rows: items of BM rows (4, 16 or 32); each of the W waves of a workgroup
-// has 16 * NT columns and one of ks ranges of K (W / ks column groups a
+// has 16 columns and one of ks ranges of K (W / ks column groups a
 // workgroup), and the ks partial sums are added through LDS in order.  A
 // wave's share is cut so that enough waves are in flight whatever the sizes.
 //
@@ -205,15 +205,15 @@ constexpr int64_t kRowTarget = 2048;    // waves that fill the chip: 8 a CU
 // come for SG groups at a time (a segment): loads of 4 groups, a group to a
 // quad.  A workgroup's is at most half of a CU's 160 KB: two workgroups a CU,
 // so that a grid a little above the number of CUs does not take two rounds.
-template <bool XF32, int BM, int NT>
+template <bool XF32, int BM>
 struct RowRing {
   static constexpr int W = BM <= 4 ? 8 : 4;                     // waves of a workgroup
   static constexpr int XL = BM * (XF32 ? 512 : 256) / 1024;     // x loads of a chunk
-  static constexpr int PER = XL + NT;                           // loads of a chunk
+  static constexpr int PER = XL + 1;                            // loads of a chunk
   static constexpr int SLOT = PER * 1024;
   static constexpr int SG = PER > 8 ? 8 : 16;
-  static constexpr int SEG_BYTES = SG * 16 * 4;                 // of one column tile
-  static constexpr int SCALES = 4 * NT * SEG_BYTES;
+  static constexpr int SEG_BYTES = SG * 16 * 4;
+  static constexpr int SCALES = 4 * SEG_BYTES;
   static constexpr int FIT = (80 * 1024 / W - SCALES) / SLOT;
   static constexpr int D = FIT < 4 ? FIT : 4;
   static constexpr int WAVE = D * SLOT + SCALES;
@@ -223,15 +223,15 @@ struct RowRing {
   static_assert(SG * 32 / 128 >= D, "segment length");
 };
 
-template <bool XF32, int G, int BM, int NT, bool ROUTED>
-__global__ void __launch_bounds__((RowRing<XF32, BM, NT>::W * 64))
+template <bool XF32, int G, int BM, bool ROUTED>
+__global__ void __launch_bounds__((RowRing<XF32, BM>::W * 64))
 w4_rows_kernel(W4Args a, int item0, int log_ks) {
-  using Ring = RowRing<XF32, BM, NT>;
-  constexpr int MT = (BM + 15) / 16, WN = 16 * NT, ES = XF32 ? 4 : 2;
+  using Ring = RowRing<XF32, BM>;
+  constexpr int MT = (BM + 15) / 16, ES = XF32 ? 4 : 2;
   constexpr int UNITS = 128 * ES / 16;  // 16-byte units of a row's chunk
   constexpr int D = Ring::D;
   // no division on the way to the first load: it is a microsecond of a call
-  const int ks = 1 << log_ks, cn = Ring::W >> log_ks, BN = WN * cn;
+  const int ks = 1 << log_ks, cn = Ring::W >> log_ks, BN = 16 * cn;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   const int tn = blockIdx.x, item = item0 + blockIdx.y;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -248,7 +248,7 @@ w4_rows_kernel(W4Args a, int item0, int log_ks) {
   const int K = a.K, KG = (int)((unsigned)K / G);
   const int chunks = (int)(((unsigned)K + 127) / 128), per = (chunks + ks - 1) >> log_ks;
   const int c0 = kw * per, c1 = min(c0 + per, chunks);
-  const int col0 = tn * BN + cw * WN;
+  const int n = tn * BN + cw * 16 + c16;       // the lane's column
 
   // Sources.  x: load t brings units 64 t + lane of the slot's x, unit p of
   // row r at p ^ (r % 16) so that 16 rows' reads of one unit spread over the
@@ -264,17 +264,12 @@ w4_rows_kernel(W4Args a, int item0, int log_ks) {
     xp[t] = static_cast<const uint8_t*>(a.x) + row * a.ldx * ES;
     xk[t] = u * (16 / ES);
   }
-  const uint8_t* wp[NT];
-  const uint8_t* sp[NT];
-  const uint8_t* zp[NT];
   const bool s16 = a.s_bf16 != 0, has_zero = a.zero != nullptr;
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int64_t n = min(col0 + 16 * j + c16, a.N - 1);
-    wp[j] = a.w + it.e * a.w_se + n * a.ldw;
-    sp[j] = static_cast<const uint8_t*>(a.scale) + (it.e * a.s_se + n * a.s_n) * (s16 ? 2 : 4);
-    zp[j] = has_zero ? a.zero + it.e * a.z_se + n * a.z_n : nullptr;
-  }
+  const int64_t nr = min(n, a.N - 1);
+  const uint8_t* const wp = a.w + it.e * a.w_se + nr * a.ldw;
+  const uint8_t* const sp =
+      static_cast<const uint8_t*>(a.scale) + (it.e * a.s_se + nr * a.s_n) * (s16 ? 2 : 4);
+  const uint8_t* const zp = has_zero ? a.zero + it.e * a.z_se + nr * a.z_n : nullptr;
   uint8_t* const ring = smem + wave * Ring::WAVE;
   uint8_t* const scl = ring + D * Ring::SLOT;
   auto load = [&](int c, uint8_t* slot) {
@@ -286,32 +281,28 @@ w4_rows_kernel(W4Args a, int item0, int log_ks) {
       to_lds<16>(xp[t] + (G == 128 || k < K ? k : xk[t] % 32) * ES, slot + t * 1024);
     }
     const int k = kc + quad * 32, kk = G == 128 || k < K ? k : 0;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) to_lds<16>(wp[j] + kk / 2, slot + (Ring::XL + j) * 1024);
+    to_lds<16>(wp + kk / 2, slot + Ring::XL * 1024);
   };
   // segment i of the wave's groups, to region i % 2
   constexpr int SEG = Ring::SG * G / 128;        // chunks of a segment
   const int g0 = c0 * 128 / G;
   auto load_segment = [&](int i) {
-    uint8_t* const dst = scl + (i & 1) * (2 * NT * Ring::SEG_BYTES);
+    uint8_t* const dst = scl + (i & 1) * (2 * Ring::SEG_BYTES);
     const int g = g0 + i * Ring::SG + quad;
     const int left = (c1 - c0) * (128 / G) - i * Ring::SG;     // groups the wave has left
     auto each = [&](auto one) {
 #pragma unroll
       for (int h = 0; h < Ring::SG / 4; ++h) {
         if (4 * h >= left) break;
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-          one(j, min(g + 4 * h, KG - 1), dst + j * Ring::SEG_BYTES + h * 256);
+        one(min(g + 4 * h, KG - 1), dst + h * 256);
       }
     };
-    if (s16) each([&](int j, int gg, uint8_t* to) { to_lds<2>(sp[j] + 2 * gg, to); });
-    else each([&](int j, int gg, uint8_t* to) { to_lds<4>(sp[j] + 4 * gg, to); });
-    if (has_zero)
-      each([&](int j, int gg, uint8_t* to) { to_lds<1>(zp[j] + gg, to + NT * Ring::SEG_BYTES); });
+    if (s16) each([&](int gg, uint8_t* to) { to_lds<2>(sp + 2 * gg, to); });
+    else each([&](int gg, uint8_t* to) { to_lds<4>(sp + 4 * gg, to); });
+    if (has_zero) each([&](int gg, uint8_t* to) { to_lds<1>(zp + gg, to + Ring::SEG_BYTES); });
   };
 
-  f32x4 acc[MT][NT] = {};
+  f32x4 acc[MT] = {};
   const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
   if (c0 < c1) {
     load(c0, ring);
@@ -333,31 +324,21 @@ w4_rows_kernel(W4Args a, int item0, int log_ks) {
     // before this chunk did, or with it (the first)
     const int in = (c - c0) & (SEG - 1), seg = (unsigned)(c - c0) / SEG;
     if (in == 0 && c + SEG < c1) load_segment(seg + 1);
-    const uint8_t* const sc = scl + (seg & 1) * (2 * NT * Ring::SEG_BYTES) + in * (128 / G) * 64;
-    f32x4 d[MT][NT], e[MT];
-    u32x4 wv[NT];
-    if (G == 128)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        wv[j] = *reinterpret_cast<const u32x4*>(slot + (Ring::XL + j) * 1024 + lane * 16);
+    const uint8_t* const sc = scl + (seg & 1) * (2 * Ring::SEG_BYTES) + in * (128 / G) * 64;
+    const uint8_t* const codes = slot + Ring::XL * 1024;
+    f32x4 d[MT], e[MT];
+    u32x4 wv;
+    if (G == 128) wv = *reinterpret_cast<const u32x4*>(codes + lane * 16);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       if (G != 128 && c * 128 + t * 32 >= K) break;      // uniform
       if (t * 32 % G == 0) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          e[i] = f32x4{};
-#pragma unroll
-          for (int j = 0; j < NT; ++j) d[i][j] = f32x4{};
-        }
+        for (int i = 0; i < MT; ++i) d[i] = e[i] = f32x4{};
       }
-      u32x4 wb[NT];
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        wb[j] = unpack(G == 128 ? wv[j][t]
-                                : *reinterpret_cast<const uint32_t*>(
-                                      slot + (Ring::XL + j) * 1024 + (16 * t + c16) * 16 +
-                                      quad * 4));
+      const u32x4 wb = unpack(G == 128 ? wv[t]
+                                       : *reinterpret_cast<const uint32_t*>(
+                                             codes + (16 * t + c16) * 16 + quad * 4));
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         const int r = BM < 16 ? c16 % BM : 16 * i + c16;
@@ -374,26 +355,21 @@ w4_rows_kernel(W4Args a, int item0, int log_ks) {
 #pragma unroll
         for (int h = (XF32 ? 3 : 1) - 1; h >= 0; --h) {
           e[i] = mfma(p.p[h], ones, e[i]);
-#pragma unroll
-          for (int j = 0; j < NT; ++j) d[i][j] = mfma(p.p[h], wb[j], d[i][j]);
+          d[i] = mfma(p.p[h], wb, d[i]);
         }
       }
       if ((t + 1) * 32 % G == 0) {
+        const uint8_t* const ss = sc + (t * 32 / G * 16 + c16) * 4;
+        const uint32_t sb = *reinterpret_cast<const uint32_t*>(ss);
+        const float sf = __uint_as_float(s16 ? sb << 16 : sb);
+        const float z =
+            16.0f + (has_zero ? (float)*reinterpret_cast<const uint32_t*>(ss + Ring::SEG_BYTES)
+                              : 8.0f);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const uint8_t* const ss = sc + j * Ring::SEG_BYTES + (t * 32 / G * 16 + c16) * 4;
-          const uint32_t sb = *reinterpret_cast<const uint32_t*>(ss);
-          const float s = __uint_as_float(s16 ? sb << 16 : sb);
-          const float z = 16.0f + (has_zero ? (float)*reinterpret_cast<const uint32_t*>(
-                                                  ss + NT * Ring::SEG_BYTES)
-                                            : 8.0f);
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              acc[i][j][r] = __builtin_fmaf(s, __builtin_fmaf(-z, e[i][r], d[i][j][r]),
-                                            acc[i][j][r]);
-        }
+          for (int r = 0; r < 4; ++r)
+            acc[i][r] = __builtin_fmaf(sf, __builtin_fmaf(-z, e[i][r], d[i][r]), acc[i][r]);
       }
     }
     wait_lgkm0();             // the slot has been read
@@ -407,23 +383,18 @@ w4_rows_kernel(W4Args a, int item0, int log_ks) {
     float* const red = reinterpret_cast<float*>(smem);
     __syncthreads();
     if (kw > 0) {
-      float* r0 = red + ((kw - 1) * cn + cw) * (MT * NT * 256);
+      float* r0 = red + ((kw - 1) * cn + cw) * (MT * 256);
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-          *reinterpret_cast<f32x4*>(r0 + (i * NT + j) * 256 + lane * 4) = acc[i][j];
+      for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4*>(r0 + i * 256 + lane * 4) = acc[i];
     }
     __syncthreads();
     if (kw > 0) return;
 #pragma unroll 1
     for (int w = 0; w < ks - 1; ++w) {
-      const float* r0 = red + (w * cn + cw) * (MT * NT * 256);
+      const float* r0 = red + (w * cn + cw) * (MT * 256);
 #pragma unroll
       for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-          acc[i][j] += *reinterpret_cast<const f32x4*>(r0 + (i * NT + j) * 256 + lane * 4);
+        acc[i] += *reinterpret_cast<const f32x4*>(r0 + i * 256 + lane * 4);
     }
   }
 #pragma unroll
@@ -439,11 +410,7 @@ w4_rows_kernel(W4Args a, int item0, int log_ks) {
         if (row < 0 || row >= a.S) continue;
         if (a.row_scale) rsc = a.row_scale[row];
       }
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int n = col0 + 16 * j + c16;
-        if (n < a.N) store_out(a, row * a.ldo + n, acc[i][j][r] * rsc);
-      }
+      if (n < a.N) store_out(a, row * a.ldo + n, acc[i][r] * rsc);
     }
 }
 
@@ -517,7 +484,7 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) w4_tile_kernel(W4Args a, Tile
   constexpr int CB = BN * 32 / NT;                  // code bytes per thread and step (8 or 16)
   constexpr int CW = CB / 4;
   constexpr int NG = G < 64 ? 64 / G : 1;           // scale groups in a step
-  static_assert(CB == 4 || CB == 8 || CB == 16, "one wide load of codes per thread");
+  static_assert(CB == 8 || CB == 16, "one wide load of codes per thread");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[3 * XS + 2 * BS];
   uint8_t* const xs = smem;
   uint8_t* const bs = smem + 3 * XS;
@@ -600,12 +567,10 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) w4_tile_kernel(W4Args a, Tile
       const u32x4 v = *reinterpret_cast<const u32x4*>(wp + at);
 #pragma unroll
       for (int i = 0; i < 4; ++i) c.w[i] = v[i];
-    } else if constexpr (CB == 8) {
+    } else {
       const uint2 v = *reinterpret_cast<const uint2*>(wp + at);
       c.w[0] = v.x;
       c.w[1] = v.y;
-    } else {
-      c.w[0] = *reinterpret_cast<const uint32_t*>(wp + at);
     }
     c.z = zp[past ? -(part * CB * 2 / G) : p.ks * kStepK / G];
   };
@@ -677,6 +642,11 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) w4_tile_kernel(W4Args a, Tile
   // instructions each.  A group's blocks (0, 0) and (0, 1) are folded in its
   // last turn, the other two in the next group's first.
   Frag f[2];
+  // the pairs of codes unpacked before product n: 8 in turns 1 and 2, or 16
+  // in turns 0 to 2
+  auto first_pair = [](int n) {
+    return CW == 4 ? (n < 12 ? n * 4 / 3 : 16) : n < 4 ? 0 : n < 12 ? n - 4 : 8;
+  };
   auto step = [&](auto odd, auto hot, int s, const Codes& next, Codes& after, const Scales& now,
                   Scales& later) {
     constexpr int ODD = decltype(odd)::value;
@@ -692,8 +662,6 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) w4_tile_kernel(W4Args a, Tile
     for (int t = 0; t < 4; ++t) {
       const bool first = G == 128 ? ODD == 0 && t == 0 : t * 16 % G == 0;
       const bool last = G == 128 ? ODD == 1 && t == 3 : (t + 1) * 16 % G == 0;
-      // the dword of codes that this turn unpacks (-1: none)
-      const int w = CW == 4 ? t : t - 1 < CW ? t - 1 : -1;
       if (t == 3) {
         // this wave's x loads of the next step have landed (newer: this
         // step's codes, zero point and x), its fragments and weights too;
@@ -726,10 +694,12 @@ __global__ void __launch_bounds__(WM * WN * 64, 2) w4_tile_kernel(W4Args a, Tile
           if (HOT || s + 2 < steps) load_codes(after, p2);
         }
         if (q == 3 && t == 0 && (HOT || s + 2 < steps)) load_x(p2, x2);
-        if (w >= 0) {
-          v[q] = unpack_pair(next.w[w < 0 ? 0 : w], q, z);
-          // the next step's weights (after the last step: to a slot nobody reads)
-          if (q == 3) write_code(v, w, (1 - ODD) * BS);
+        // the next step's weights (after the last step: to a slot nobody
+        // reads), all written before the barrier of turn 3
+#pragma unroll
+        for (int p = first_pair(4 * t + q); p < first_pair(4 * t + q + 1); ++p) {
+          v[p & 3] = unpack_pair(next.w[p >> 2], p & 3, z);
+          if ((p & 3) == 3) write_code(v, p >> 2, (1 - ODD) * BS);
         }
         if (HOT) __builtin_amdgcn_sched_barrier(0);
       }
@@ -805,7 +775,7 @@ __global__ void __launch_bounds__(256) split_planes(const float* __restrict__ x,
   }
 }
 
-template <int G, bool S16, int WM, int WN>
+template <int G, bool S16, int WM, int WN, bool ROUTED>
 void launch_tiles(const W4Args& a, void* ws, hipStream_t st) {
   constexpr int BM = 64 * WM, BN = 64 * WN;
   TileArgs t{};
@@ -828,41 +798,36 @@ void launch_tiles(const W4Args& a, void* ws, hipStream_t st) {
     t.planes = 1;
     t.x_bytes = (uint32_t)(((int64_t)(a.R - 1) * a.ldx + a.K) * 2);
   }
-  if (a.offsets) {
-    t.items = (int)(((int64_t)a.S + (int64_t)(a.E < a.S ? a.E : a.S) * (BM - 1)) / BM);
-    hipLaunchKernelGGL((w4_tile_kernel<G, S16, WM, WN, true>), dim3((unsigned)(t.items * t.ntn)),
-                       dim3(WM * WN * 64), 0, st, a, t);
-  } else {
-    t.items = (a.S + BM - 1) / BM;
-    hipLaunchKernelGGL((w4_tile_kernel<G, S16, WM, WN, false>), dim3((unsigned)(t.items * t.ntn)),
-                       dim3(WM * WN * 64), 0, st, a, t);
-  }
+  t.items = ROUTED ? (int)(((int64_t)a.S + (int64_t)(a.E < a.S ? a.E : a.S) * (BM - 1)) / BM)
+                   : (int)(((int64_t)a.S + BM - 1) / BM);
+  hipLaunchKernelGGL((w4_tile_kernel<G, S16, WM, WN, ROUTED>), dim3((unsigned)(t.items * t.ntn)),
+                     dim3(WM * WN * 64), 0, st, a, t);
 }
 
 // As many K ranges as leave about 8 waves to a CU, at most one per chunk.
-template <bool XF32, int G, int BM, int NT>
+template <bool XF32, int G, int BM>
 void launch_rows(const W4Args& a, hipStream_t st) {
   const int64_t act = a.E < a.S ? a.E : a.S;
   const int64_t items = a.offsets ? (a.S + act * (BM - 1)) / BM : ((int64_t)a.S + BM - 1) / BM;
   // routed: about half of a block is missing from an expert's last one
   const int64_t busy = a.offsets ? (a.S + act * (BM / 2)) / BM + 1 : items;
-  const int64_t tiles = busy * ((a.N + 16 * NT - 1) / (16 * NT));
+  const int64_t tiles = busy * ((a.N + 15) / 16);
   const int chunks = (a.K + 127) / 128;
-  constexpr int W = RowRing<XF32, BM, NT>::W;
+  constexpr int W = RowRing<XF32, BM>::W;
   int log_ks = 0;
   while ((1 << log_ks) < W && (tiles << log_ks) < kRowTarget && (2 << log_ks) <= chunks) ++log_ks;
-  const int BN = 16 * NT * (W >> log_ks);
+  const int BN = 16 * (W >> log_ks);
   const dim3 block(W * 64);
-  constexpr int lds = RowRing<XF32, BM, NT>::BYTES;
+  constexpr int lds = RowRing<XF32, BM>::BYTES;
   // at most 65535 items a launch
   for (int64_t i = 0; i < items; i += 65535) {
     const dim3 grid((unsigned)((a.N + BN - 1) / BN),
                     (unsigned)(items - i < 65535 ? items - i : 65535));
     if (a.offsets)
-      hipLaunchKernelGGL((w4_rows_kernel<XF32, G, BM, NT, true>), grid, block, lds, st, a, (int)i,
+      hipLaunchKernelGGL((w4_rows_kernel<XF32, G, BM, true>), grid, block, lds, st, a, (int)i,
                          log_ks);
     else
-      hipLaunchKernelGGL((w4_rows_kernel<XF32, G, BM, NT, false>), grid, block, lds, st, a, (int)i,
+      hipLaunchKernelGGL((w4_rows_kernel<XF32, G, BM, false>), grid, block, lds, st, a, (int)i,
                          log_ks);
   }
 }
@@ -870,16 +835,23 @@ void launch_rows(const W4Args& a, hipStream_t st) {
 template <bool XF32, int G>
 void launch_few(const W4Args& a, hipStream_t st) {
   const int64_t rows = a.offsets ? (a.S + a.E - 1) / a.E : a.S;
-  if (rows <= 4) launch_rows<XF32, G, 4, 1>(a, st);
-  else if (rows <= 16 || XF32) launch_rows<XF32, G, 16, 1>(a, st);
-  else launch_rows<XF32, G, XF32 ? 16 : 32, 1>(a, st);
+  if (rows <= 4) launch_rows<XF32, G, 4>(a, st);
+  else if (rows <= 16 || XF32) launch_rows<XF32, G, 16>(a, st);
+  else launch_rows<XF32, G, XF32 ? 16 : 32>(a, st);
+}
+
+template <int G, bool S16>
+void launch_plan(const W4Args& a, W4Plan plan, void* ws, hipStream_t st) {
+  if (plan == W4Plan::Tile256) launch_tiles<G, S16, 4, 2, false>(a, ws, st);
+  else if (a.offsets) launch_tiles<G, S16, 2, 2, true>(a, ws, st);
+  else launch_tiles<G, S16, 2, 2, false>(a, ws, st);
 }
 
 template <int G>
-void launch_group(const W4Args& a, void* ws, hipStream_t st) {
-  if (w4_tiled(a) && (a.x_dtype != BSMM_F32 || ws != nullptr)) {
-    if (a.s_bf16) launch_tiles<G, true, 4, 2>(a, ws, st);
-    else launch_tiles<G, false, 4, 2>(a, ws, st);
+void launch_group(const W4Args& a, W4Plan plan, void* ws, hipStream_t st) {
+  if (plan != W4Plan::Rows) {
+    if (a.s_bf16) launch_plan<G, true>(a, plan, ws, st);
+    else launch_plan<G, false>(a, plan, ws, st);
     return;
   }
   if (a.x_dtype == BSMM_F32) launch_few<true, G>(a, st);
@@ -888,11 +860,11 @@ void launch_group(const W4Args& a, void* ws, hipStream_t st) {
 
 }  // namespace
 
-int launch_w4(const W4Args& a, void* ws, void* stream) {
+int launch_w4(const W4Args& a, W4Plan plan, void* ws, void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (a.group == 32) launch_group<32>(a, ws, st);
-  else if (a.group == 64) launch_group<64>(a, ws, st);
-  else launch_group<128>(a, ws, st);
+  if (a.group == 32) launch_group<32>(a, plan, ws, st);
+  else if (a.group == 64) launch_group<64>(a, plan, ws, st);
+  else launch_group<128>(a, plan, ws, st);
   return hipGetLastError() == hipSuccess ? 0 : 1;
 }
 

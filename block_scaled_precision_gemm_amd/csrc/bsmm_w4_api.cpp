@@ -54,13 +54,72 @@ bsmm_status check_operands(const W4Args& a) {
 bsmm_status run(const W4Args& a, void* workspace, size_t workspace_bytes, void* stream) {
   const bsmm_status st = check_operands(a);
   if (st != BSMM_OK) return st;
-  if (workspace == nullptr || workspace_bytes < w4_plane_bytes(a) || !aligned(workspace, 16))
-    workspace = nullptr;
-  if (launch_w4(a, workspace, stream) != 0) return fail(BSMM_ERR_HIP, "kernel launch failed (w4)");
+  W4Plan plan = w4_plan(a);
+  if (a.x_dtype == BSMM_F32 &&
+      (workspace == nullptr || workspace_bytes < w4_plane_bytes(a) || !aligned(workspace, 16)))
+    plan = W4Plan::Rows;
+  if (launch_w4(a, plan, workspace, stream) != 0) return fail(BSMM_ERR_HIP, "kernel launch failed (w4)");
   return BSMM_OK;
 }
 
 }  // namespace
+
+// The times of the three kernels in us, fitted to device times of calls of
+// 24 to 4096 rows (weights 800 x 1472 to 5120 x 8192; the groups of 128 in
+// bf16 unless said otherwise); the least is taken.
+//
+// Rows: 5 plus the operations of the padded rows at the rate its matrix
+// instructions and folds reach (bf16 260 / 155 / 150 Tflop/s for groups of
+// 128 / 64 / 32, fp32 85).
+// Tiles: one K step after another (128 rows: 0.8 / 1.0 / 1.2 us, 256 rows:
+// 0.95 / 1.02 / 1.55; fp32 walks three planes), in rounds of the tiles that
+// the 256 CUs hold: one of 256 rows (a full round 15 % longer), two of 128
+// (then 1.65 times as long as one).  Routed tiles take 1.4 times that: blocks
+// that experts leave partly empty, codes that come from HBM.
+//
+//   rows x N x K              Rows   Tile128   Tile256   (us)
+//     260 x 5120 x 8192         92       100       126
+//     520 x 5120 x 8192        166        96       126
+//    1040 x 5120 x 8192        307       160       133
+//    1040 x 2048 x 4096         77        54        69
+//    2047 x 4096 x 4096                   86        77
+//     260 x 2048 x 4096 fp32    82       163       209   (groups of 64)
+//     800 x 5120 x 8192 fp32   749       467       430   (groups of 64)
+//    512 tokens x 4, 16 experts of 2048 x 2048:   rows 94, 128 59, 256 98
+//    1021 tokens x 8, 32 experts of 2048 x 4096:  rows 541, 128 281, 256 348
+//    128 tokens x 4, 16 experts of 2048 x 2048:   rows 34, 128 53, 256 90
+//
+// Routed calls therefore never take 256 rows: an expert's last tile is half
+// empty on average.
+W4Plan bsmm::w4_plan(const W4Args& a) {
+  const bool f32 = a.x_dtype == BSMM_F32;
+  const size_t x = f32 ? w4_plane_bytes(a) : (size_t)a.R * (size_t)a.ldx * 2u;
+  const int64_t act = a.E < a.S ? a.E : a.S;
+  // at most 32 rows (an expert): a tile would be three quarters empty
+  if (a.K == 0 || a.S <= 32 * act || x >= (size_t)0xFFFF0000u) return W4Plan::Rows;
+  // blocks of bm rows: dense all of them, routed with half a block to spare
+  // for each expert
+  auto blocks = [&](int64_t bm) {
+    return a.offsets ? ((int64_t)a.S + act * (bm / 2)) / bm + 1 : ((int64_t)a.S + bm - 1) / bm;
+  };
+  const int64_t tile_cols = ((int64_t)a.N + 127) / 128;
+  const double steps = (double)((a.K + 63) / 64) * (f32 ? 3 : 1);
+  const int g = a.group == 128 ? 0 : a.group == 64 ? 1 : 2;
+  static const double kRate[3] = {260e6, 155e6, 150e6};      // flop per us
+  static const double kStep128[3] = {0.8, 1.0, 1.2}, kStep256[3] = {0.95, 1.02, 1.55};
+
+  const int64_t bm = f32 ? 16 : 32;
+  const double rows = 5.0 + 2.0 * (double)(blocks(bm) * bm) * a.N * a.K / (f32 ? 85e6 : kRate[g]);
+  const int64_t n128 = blocks(128) * tile_cols, rest = n128 % 512;
+  const double rounds128 =
+      1.65 * (double)(n128 / 512) + (rest == 0 ? 0.0 : rest <= 256 ? 1.0 : 1.55);
+  const double t128 = 4.0 + rounds128 * steps * kStep128[g] * (a.offsets ? 1.4 : 1.0);
+  if (a.offsets) return rows <= t128 ? W4Plan::Rows : W4Plan::Tile128;
+  const double rounds256 = 1.15 * (double)((blocks(256) * tile_cols + 255) / 256);
+  const double t256 = 4.0 + rounds256 * steps * kStep256[g];
+  if (rows <= t128 && rows <= t256) return W4Plan::Rows;
+  return t128 <= t256 ? W4Plan::Tile128 : W4Plan::Tile256;
+}
 
 extern "C" {
 
@@ -100,17 +159,24 @@ bsmm_status bsmm_quant_w4(const void* w, int64_t ldw, bsmm_dtype w_dtype, uint8_
   return BSMM_OK;
 }
 
-size_t bsmm_w4_workspace_bytes(bsmm_dtype x_dtype, int64_t E, int64_t R, int64_t S, int64_t K) {
-  if (E <= 0 || R <= 0 || S <= 0 || K <= 0 || E > 1024 || R >= kMaxDim || S >= kMaxDim ||
-      K >= kMaxDim)
+size_t bsmm_w4_workspace_bytes(bsmm_dtype x_dtype, int64_t E, int64_t R, int64_t S, int64_t N,
+                               int64_t K, int group) {
+  if (E <= 0 || R <= 0 || S <= 0 || N <= 0 || K <= 0 || E > 1024 || R >= kMaxDim ||
+      S >= kMaxDim || N >= kMaxDim || K >= kMaxDim || x_dtype != BSMM_F32)
     return 0;
   W4Args a{};
   a.x_dtype = x_dtype;
-  a.E = (int)E; a.R = (int)R; a.S = (int)S; a.K = (int)K;
+  a.group = group;
+  a.E = (int)E; a.R = (int)R; a.S = (int)S; a.N = (int)N; a.K = (int)K;
   a.ldx = K;
+  // a routed call that could pass for a dense one (one expert, R = S) may
+  // take a tile where the other does not: enough for both
   static const int32_t routed = 0;
-  a.offsets = E > 1 || R != S ? &routed : nullptr;
-  return w4_tiled(a) ? w4_plane_bytes(a) : 0;
+  a.offsets = &routed;
+  bool tiled = w4_plan(a) != W4Plan::Rows;
+  a.offsets = nullptr;
+  if (E == 1 && R == S) tiled = tiled || w4_plan(a) != W4Plan::Rows;
+  return tiled ? w4_plane_bytes(a) : 0;
 }
 
 bsmm_status bsmm_w4_mm(const void* x, int64_t ldx, bsmm_dtype x_dtype, const uint8_t* w,

@@ -468,7 +468,8 @@ bsmm_status bsmm_quant_w4(const void* w, int64_t ldw, bsmm_dtype w_dtype, uint8_
  * bsmm_w4_workspace_bytes gives the bytes (0: none; E = 1 and S = R = M for
  * bsmm_w4_mm).  With less the call runs without it, slower.
  */
-size_t bsmm_w4_workspace_bytes(bsmm_dtype x_dtype, int64_t E, int64_t R, int64_t S, int64_t K);
+size_t bsmm_w4_workspace_bytes(bsmm_dtype x_dtype, int64_t E, int64_t R, int64_t S, int64_t N,
+                               int64_t K, int group);
 bsmm_status bsmm_w4_mm(const void* x, int64_t ldx, bsmm_dtype x_dtype, const uint8_t* w,
                        int64_t ldw, const void* scale, int64_t s_n, bsmm_dtype scale_dtype,
                        const uint8_t* zero, int64_t z_n, int group, void* out, int64_t ldo,

@@ -179,6 +179,38 @@ def test_mm_strided(M):
     same(y, w4.w4_mm(c["x"], c["q"], np.repeat(c["s"][:1], 96, 0)), "f32")
 
 
+# sizes at which the cost rule takes tiles of 128 rows and of 256 (the last of
+# each group of sizes), with one K step to several, odd edges, and for groups
+# of 32 a last step of one group
+TILES = [(32, 1100, 900, 32, "bf16"), (32, 1700, 1290, 352, "bf16"), (32, 1700, 1700, 352, "f32"),
+         (32, 2047, 2100, 288, "bf16"), (64, 65, 100, 64, "bf16"), (64, 1290, 1100, 320, "bf16"),
+         (64, 1030, 2300, 192, "f32"), (64, 2047, 2100, 448, "bf16"), (64, 2300, 2100, 128, "f32"),
+         (128, 500, 1300, 128, "bf16"), (128, 1200, 1030, 256, "bf16"),
+         (128, 1300, 1300, 384, "f32"), (128, 2047, 2100, 640, "bf16"),
+         (128, 2049, 2100, 256, "f32")]
+
+
+@pytest.mark.parametrize("group,M,N,K,dt", TILES)
+def test_mm_tiles_integers_exact(group, M, N, K, dt):
+    for st, zero, out in (("f32", True, "f32"), ("bf16", False, "bf16")):
+        c = integer_case(M, N, K, group, zero, dt, M + K)
+        y = bsmm.bsmm_w4_mm(dev(c["x"], TDT[dt]), dev(c["q"]), dev(c["s"], TDT[st]),
+                            dev(c["z"]) if zero else None, out_dtype=out)
+        same(y, w4.w4_mm(c["x"], c["q"], c["s"], c["z"]), out)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_mm_tiles_normal_data(group, dt):
+    rng = np.random.default_rng(group)
+    w = dev((rng.standard_normal((2051, 1024)) * 0.02).astype(np.float32))
+    x = dev(rng.standard_normal((2047, 1024)).astype(np.float32), TDT[dt])
+    for M, sym, st in ((800, True, "bf16"), (2047, False, "f32")):
+        q, s, z = bsmm.bsmm_quant_w4(w, group=group, symmetric=sym, scale_dtype=st)
+        close(lambda out: bsmm.bsmm_w4_mm(x[:M], q, s, z, out_dtype=out),
+              w4.w4_mm(host(x[:M]), host(q), host(s), None if sym else host(z)))
+
+
 def test_mm_degenerate():
     c = integer_case(3, 8, 64, 64, False, "bf16", 5)
     x, q, s = dev(c["x"], torch.bfloat16), dev(c["q"]), dev(c["s"])
@@ -252,6 +284,23 @@ def test_expert_integers_exact(T, k, E, second):
             row_scale=dev(rs) if second else None, out_dtype=out, out=out_t)
         same(y, w4.w4_expert_mm(c["x"], c["q"], c["s"], c["z"], order, offsets,
                                 1 if second else k, rs if second else None), out)
+
+
+@pytest.mark.parametrize("group,K,dt", [(32, 352, "bf16"), (64, 320, "bf16"), (64, 320, "f32"),
+                                        (128, 128, "bf16"), (128, 640, "bf16")])
+def test_expert_tiles_integers_exact(group, K, dt):
+    """Sizes at which the cost rule takes tiles of 128 rows."""
+    T, k, E, N = 500, 4, 8, 1500
+    for i, (second, unused) in enumerate(((False, 0.0), (True, 0.3))):
+        order, offsets = routing(T, k, E, 5 + i, unused)
+        c = integer_case(T * k if second else T, N, K, group, second, dt, K + i, E)
+        rs = np.exp2(np.random.default_rng(i).integers(-2, 2, T * k)).astype(np.float32)
+        y = bsmm.bsmm_w4_expert_mm(
+            dev(c["x"], TDT[dt]), dev(c["q"]), dev(c["s"]), dev(c["z"]) if second else None,
+            dev(order), dev(offsets), slots_per_row=1 if second else k,
+            row_scale=dev(rs) if second else None, out_dtype="f32")
+        same(y, w4.w4_expert_mm(c["x"], c["q"], c["s"], c["z"], order, offsets,
+                                1 if second else k, rs if second else None), "f32")
 
 
 @pytest.mark.parametrize("group", [32, 128])
