@@ -61,19 +61,6 @@ template <bool XF32> struct X8;
 template <> struct X8<false> { u32x4 v; };
 template <> struct X8<true> { u32x4 a, b; };
 
-template <bool XF32>
-__device__ __forceinline__ X8<XF32> load_x(const void* x, int64_t at) {
-  X8<XF32> r;
-  if constexpr (XF32) {
-    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const float*>(x) + at);
-    r.a = p[0];
-    r.b = p[1];
-  } else {
-    r.v = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(x) + at);
-  }
-  return r;
-}
-
 // the bf16 operands of 8 activations (1, or the 3 parts of fp32 values), in
 // the order 0 4 1 5 2 6 3 7
 template <bool XF32> struct Parts { u32x4 p[XF32 ? 3 : 1]; };

@@ -465,8 +465,8 @@ bsmm_status bsmm_quant_w4(const void* w, int64_t ldw, bsmm_dtype w_dtype, uint8_
  * activations are used in full precision.  M == 0 or N == 0 does nothing, K
  * == 0 writes zeros.  The workspace (16-byte aligned) holds fp32 activations
  * cut into bf16 parts where many rows make that worth it:
- * bsmm_w4_workspace_bytes gives the bytes (0: none; E = 1 and S = R = M for
- * bsmm_w4_mm).  With less the call runs without it, slower.
+ * bsmm_w4_workspace_bytes gives the bytes (0: none wanted; E = 1 and S = R =
+ * M for bsmm_w4_mm).  With less the call runs without it, slower.
  */
 size_t bsmm_w4_workspace_bytes(bsmm_dtype x_dtype, int64_t E, int64_t R, int64_t S, int64_t N,
                                int64_t K, int group);
