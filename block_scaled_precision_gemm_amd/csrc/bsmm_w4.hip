@@ -41,11 +41,13 @@ __device__ __forceinline__ uint32_t bf16_bits(float v) {
          0xFFFFu;
 }
 
-// 8 codes of a dword -> 16 + code as bf16, in the order 0 4 1 5 2 6 3 7
-__device__ __forceinline__ u32x4 unpack(uint32_t w) {
-  constexpr uint32_t kMask = 0x00780078u, kBias = 0x41804180u;
-  return u32x4{((w << 3) & kMask) | kBias, ((w >> 1) & kMask) | kBias,
-               ((w >> 5) & kMask) | kBias, ((w >> 9) & kMask) | kBias};
+// 8 codes of a dword -> 16 + code as bf16, in the order 0 4 1 5 2 6 3 7.
+// bias: 0x41804180 in a vector register, so that and-or is one instruction
+// with the mask in a scalar one.
+__device__ __forceinline__ u32x4 unpack(uint32_t w, uint32_t bias) {
+  constexpr uint32_t kMask = 0x00780078u;
+  return u32x4{((w << 3) & kMask) | bias, ((w >> 1) & kMask) | bias, ((w >> 5) & kMask) | bias,
+               ((w >> 9) & kMask) | bias};
 }
 
 // low / high halves of (a, b) as a pair
@@ -170,6 +172,23 @@ __device__ __forceinline__ void to_lds(const void* src, uint8_t* dst) {
   else __builtin_amdgcn_global_load_lds(from, to, 16, 0, 0);
 }
 
+// The same from base + voff + soff, 31 bits together: soff is the wave's, and
+// the load needs no vector instruction for its address.
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+__device__ __forceinline__ rsrc_t buffer_at(const void* base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, 0x7FFFFFFF,
+                                           0x00020000);
+}
+template <int SIZE>
+__device__ __forceinline__ void to_lds(rsrc_t rs, uint32_t voff, uint32_t soff, uint8_t* dst) {
+  auto* const to = (__attribute__((address_space(3))) void*)(uintptr_t)(uint32_t)(uintptr_t)dst;
+  const int v = (int)voff, s = (int)soff;
+  if constexpr (SIZE == 1) __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, to, 1, v, s, 0, 0);
+  else if constexpr (SIZE == 2) __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, to, 2, v, s, 0, 0);
+  else if constexpr (SIZE == 4) __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, to, 4, v, s, 0, 0);
+  else __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, to, 16, v, s, 0, 0);
+}
+
 // ---------------------------------------------------------------------------
 // Few rows: items of BM rows (4, 16 or 32); each of the W waves of a workgroup
 // has 16 columns and one of ks ranges of K (W / ks column groups a
@@ -211,8 +230,8 @@ struct RowRing {
 };
 
 template <bool XF32, int G, int BM, bool ROUTED>
-__global__ void __launch_bounds__((RowRing<XF32, BM>::W * 64))
-w4_rows_kernel(W4Args a, int item0, int log_ks) {
+__global__ void __launch_bounds__((RowRing<XF32, BM>::W * 64), 2)
+w4_rows_kernel(W4Args a, int item0, int log_ks, int wide) {
   using Ring = RowRing<XF32, BM>;
   constexpr int MT = (BM + 15) / 16, ES = XF32 ? 4 : 2;
   constexpr int UNITS = 128 * ES / 16;  // 16-byte units of a row's chunk
@@ -237,60 +256,105 @@ w4_rows_kernel(W4Args a, int item0, int log_ks) {
   const int c0 = kw * per, c1 = min(c0 + per, chunks);
   const int n = tn * BN + cw * 16 + c16;       // the lane's column
 
-  // Sources.  x: load t brings units 64 t + lane of the slot's x, unit p of
-  // row r at p ^ (r % 16) so that 16 rows' reads of one unit spread over the
-  // banks; rows past the end repeat the first (a row of the product depends
-  // on its own row of x alone, and theirs are not stored).
-  const uint8_t* xp[Ring::XL];
-  int xk[Ring::XL];
+  // Sources: a base that is the wave's plus 32-bit offsets of the lanes, so
+  // that a load needs no vector instruction: calls of several rows are bound
+  // by the instructions issued (a wave of 13 fp32 rows spent 62 % of its time
+  // on them).  `wide`: rows so far apart that the offsets do not fit; then,
+  // and where a chunk or segment reaches past the end of the row, every lane
+  // makes its address.
+  //
+  // x: load t brings units 64 t + lane of the slot's x, unit p of row r at p ^
+  // (r % 16) so that 16 rows' reads of one unit spread over the banks; rows
+  // past the end repeat the first (a row of the product depends on its own
+  // row of x alone, and theirs are not stored).
+  const int row0 = ROUTED ? 0 : it.p0;
+  const uint8_t* const xb = static_cast<const uint8_t*>(a.x) + row0 * a.ldx * ES;
+  int xr[Ring::XL], xk[Ring::XL];
+  uint32_t xo[Ring::XL];
 #pragma unroll
   for (int t = 0; t < Ring::XL; ++t) {
     const int r = (64 * t + lane) / UNITS, u = ((lane % UNITS) ^ (r & 15));
     int64_t row = it.p0 + (r < it.rows ? r : 0);
     if (ROUTED) row = min(max(a.order[row] / a.x_div, 0), a.R - 1);
-    xp[t] = static_cast<const uint8_t*>(a.x) + row * a.ldx * ES;
+    xr[t] = (int)row - row0;
     xk[t] = u * (16 / ES);
+    xo[t] = (uint32_t)(((int64_t)xr[t] * a.ldx + xk[t]) * ES);
   }
   const bool s16 = a.s_bf16 != 0, has_zero = a.zero != nullptr;
-  const int64_t nr = min(n, a.N - 1);
-  const uint8_t* const wp = a.w + it.e * a.w_se + nr * a.ldw;
-  const uint8_t* const sp =
-      static_cast<const uint8_t*>(a.scale) + (it.e * a.s_se + nr * a.s_n) * (s16 ? 2 : 4);
-  const uint8_t* const zp = has_zero ? a.zero + it.e * a.z_se + nr * a.z_n : nullptr;
+  const int ss = s16 ? 2 : 4;
+  const int col0 = min(tn * BN + cw * 16, a.N - 1);
+  const int64_t nc = min(n, a.N - 1) - col0;
+  const uint8_t* const wb = a.w + it.e * a.w_se + col0 * a.ldw;
+  const uint8_t* const sb =
+      static_cast<const uint8_t*>(a.scale) + (it.e * a.s_se + col0 * a.s_n) * ss;
+  const uint8_t* const zb = has_zero ? a.zero + it.e * a.z_se + col0 * a.z_n : nullptr;
+  const uint32_t wo = (uint32_t)(nc * a.ldw + quad * 16);
+  const uint32_t so = (uint32_t)((nc * a.s_n + quad) * ss), zo = (uint32_t)(nc * a.z_n + quad);
+  const rsrc_t xrs = buffer_at(xb), wrs = buffer_at(wb), srs = buffer_at(sb), zrs = buffer_at(zb);
   uint8_t* const ring = smem + wave * Ring::WAVE;
   uint8_t* const scl = ring + D * Ring::SLOT;
   auto load = [&](int c, uint8_t* slot) {
     const int kc = c * 128;
-    // past the end of the row: its start again, in products that are left out
+    if (!wide && (G == 128 || kc + 128 <= K)) {
 #pragma unroll
-    for (int t = 0; t < Ring::XL; ++t) {
-      const int k = kc + xk[t];
-      to_lds<16>(xp[t] + (G == 128 || k < K ? k : xk[t] % 32) * ES, slot + t * 1024);
+      for (int t = 0; t < Ring::XL; ++t) to_lds<16>(xrs, xo[t], kc * ES, slot + t * 1024);
+      to_lds<16>(wrs, wo, kc / 2, slot + Ring::XL * 1024);
+    } else {
+      // past the end of the row: its start again, in products that are left out
+#pragma unroll
+      for (int t = 0; t < Ring::XL; ++t) {
+        const int k = kc + xk[t];
+        to_lds<16>(xb + (xr[t] * a.ldx + (G == 128 || k < K ? k : xk[t] % 32)) * ES,
+                   slot + t * 1024);
+      }
+      const int k = kc + quad * 32;
+      to_lds<16>(wb + nc * a.ldw + (G == 128 || k < K ? k : 0) / 2, slot + Ring::XL * 1024);
     }
-    const int k = kc + quad * 32, kk = G == 128 || k < K ? k : 0;
-    to_lds<16>(wp + kk / 2, slot + Ring::XL * 1024);
   };
   // segment i of the wave's groups, to region i % 2
   constexpr int SEG = Ring::SG * G / 128;        // chunks of a segment
   const int g0 = c0 * 128 / G;
   auto load_segment = [&](int i) {
     uint8_t* const dst = scl + (i & 1) * (2 * Ring::SEG_BYTES);
-    const int g = g0 + i * Ring::SG + quad;
+    const int g = g0 + i * Ring::SG;
     const int left = (c1 - c0) * (128 / G) - i * Ring::SG;     // groups the wave has left
     auto each = [&](auto one) {
 #pragma unroll
       for (int h = 0; h < Ring::SG / 4; ++h) {
         if (4 * h >= left) break;
-        one(min(g + 4 * h, KG - 1), dst + h * 256);
+        one(g + 4 * h, dst + h * 256);
       }
     };
-    if (s16) each([&](int gg, uint8_t* to) { to_lds<2>(sp + 2 * gg, to); });
-    else each([&](int gg, uint8_t* to) { to_lds<4>(sp + 4 * gg, to); });
-    if (has_zero) each([&](int gg, uint8_t* to) { to_lds<1>(zp + gg, to + Ring::SEG_BYTES); });
+    if (!wide && g + Ring::SG <= KG) {
+      if (s16) each([&](int gg, uint8_t* to) { to_lds<2>(srs, so, 2 * gg, to); });
+      else each([&](int gg, uint8_t* to) { to_lds<4>(srs, so, 4 * gg, to); });
+      if (has_zero)
+        each([&](int gg, uint8_t* to) { to_lds<1>(zrs, zo, gg, to + Ring::SEG_BYTES); });
+    } else {
+      auto at = [&](int gg, int64_t ld) { return nc * ld + min(gg + quad, KG - 1); };
+      if (s16) each([&](int gg, uint8_t* to) { to_lds<2>(sb + 2 * at(gg, a.s_n), to); });
+      else each([&](int gg, uint8_t* to) { to_lds<4>(sb + 4 * at(gg, a.s_n), to); });
+      if (has_zero)
+        each([&](int gg, uint8_t* to) { to_lds<1>(zb + at(gg, a.z_n), to + Ring::SEG_BYTES); });
+    }
   };
 
   f32x4 acc[MT] = {};
   const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+  uint32_t bias = 0x41804180u;
+  asm("" : "+v"(bias));
+  // Without zero points both regions hold 8 for good: the groups' products
+  // then have no branch between them and overlap.  With this, the scale 0 for
+  // groups past the row, sums in ordinary registers (the launch bound's 2) and
+  // addresses without vector instructions, 70 x 5120 x 8192 fp32 takes 87 us
+  // (102 before), 13 x 4099 x 7168 fp32 26.7 (29.4), 64 routed tokens x 8
+  // 75 (80).
+  if (!has_zero) {
+#pragma unroll
+    for (int i = 0; i < 2 * Ring::SEG_BYTES / 256; ++i)
+      *reinterpret_cast<uint32_t*>(scl + (i & 1 ? 3 : 1) * Ring::SEG_BYTES + (i >> 1) * 256 +
+                                   lane * 4) = 8;
+  }
   if (c0 < c1) {
     load(c0, ring);
     load_segment(0);
@@ -318,40 +382,40 @@ w4_rows_kernel(W4Args a, int item0, int log_ks) {
     if (G == 128) wv = *reinterpret_cast<const u32x4*>(codes + lane * 16);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      if (G != 128 && c * 128 + t * 32 >= K) break;      // uniform
       if (t * 32 % G == 0) {
 #pragma unroll
         for (int i = 0; i < MT; ++i) d[i] = e[i] = f32x4{};
       }
-      const u32x4 wb = unpack(G == 128 ? wv[t]
+      const u32x4 wq = unpack(G == 128 ? wv[t]
                                        : *reinterpret_cast<const uint32_t*>(
-                                             codes + (16 * t + c16) * 16 + quad * 4));
+                                             codes + (16 * t + c16) * 16 + quad * 4),
+                              bias);
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         const int r = BM < 16 ? c16 % BM : 16 * i + c16;
         const int k = G == 128 ? quad * 32 + t * 8 : t * 32 + quad * 8;
-        const uint8_t* xr = slot + r * (UNITS * 16);
+        const uint8_t* xs = slot + r * (UNITS * 16);
         X8<XF32> x;
         if constexpr (XF32) {
-          x.a = *reinterpret_cast<const u32x4*>(xr + ((k / 4) ^ (r & 15)) * 16);
-          x.b = *reinterpret_cast<const u32x4*>(xr + ((k / 4 + 1) ^ (r & 15)) * 16);
+          x.a = *reinterpret_cast<const u32x4*>(xs + ((k / 4) ^ (r & 15)) * 16);
+          x.b = *reinterpret_cast<const u32x4*>(xs + ((k / 4 + 1) ^ (r & 15)) * 16);
         } else {
-          x.v = *reinterpret_cast<const u32x4*>(xr + ((k / 8) ^ (r & 15)) * 16);
+          x.v = *reinterpret_cast<const u32x4*>(xs + ((k / 8) ^ (r & 15)) * 16);
         }
         const Parts<XF32> p = parts(x);
 #pragma unroll
         for (int h = (XF32 ? 3 : 1) - 1; h >= 0; --h) {
           e[i] = mfma(p.p[h], ones, e[i]);
-          d[i] = mfma(p.p[h], wb, d[i]);
+          d[i] = mfma(p.p[h], wq, d[i]);
         }
       }
       if ((t + 1) * 32 % G == 0) {
-        const uint8_t* const ss = sc + (t * 32 / G * 16 + c16) * 4;
-        const uint32_t sb = *reinterpret_cast<const uint32_t*>(ss);
-        const float sf = __uint_as_float(s16 ? sb << 16 : sb);
-        const float z =
-            16.0f + (has_zero ? (float)*reinterpret_cast<const uint32_t*>(ss + Ring::SEG_BYTES)
-                              : 8.0f);
+        const uint8_t* const sl = sc + (t * 32 / G * 16 + c16) * 4;
+        const uint32_t sv = *reinterpret_cast<const uint32_t*>(sl);
+        // groups past the end of the row: scale 0
+        const bool in_row = G == 128 || c * 128 + t * 32 < K;
+        const float sf = in_row ? __uint_as_float(s16 ? sv << 16 : sv) : 0.0f;
+        const float z = 16.0f + (float)*reinterpret_cast<const uint32_t*>(sl + Ring::SEG_BYTES);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -805,6 +869,12 @@ void launch_rows(const W4Args& a, hipStream_t st) {
   while ((1 << log_ks) < W && (tiles << log_ks) < kRowTarget && (2 << log_ks) <= chunks) ++log_ks;
   const int BN = 16 * (W >> log_ks);
   const dim3 block(W * 64);
+  // the lanes' 32-bit offsets: from the item's first row (routed: from row 0)
+  // and from the wave's first column
+  const int64_t limit = (int64_t)1 << 31;
+  const int64_t x_rows = a.offsets ? a.R : BM;
+  const int wide = x_rows * a.ldx * (XF32 ? 4 : 2) >= limit || 16 * a.ldw >= limit ||
+                   64 * a.s_n >= limit || 16 * a.z_n >= limit;
   constexpr int lds = RowRing<XF32, BM>::BYTES;
   // at most 65535 items a launch
   for (int64_t i = 0; i < items; i += 65535) {
@@ -812,10 +882,10 @@ void launch_rows(const W4Args& a, hipStream_t st) {
                     (unsigned)(items - i < 65535 ? items - i : 65535));
     if (a.offsets)
       hipLaunchKernelGGL((w4_rows_kernel<XF32, G, BM, true>), grid, block, lds, st, a, (int)i,
-                         log_ks);
+                         log_ks, wide);
     else
       hipLaunchKernelGGL((w4_rows_kernel<XF32, G, BM, false>), grid, block, lds, st, a, (int)i,
-                         log_ks);
+                         log_ks, wide);
   }
 }
 

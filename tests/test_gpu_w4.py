@@ -179,6 +179,25 @@ def test_mm_strided(M):
     same(y, w4.w4_mm(c["x"], c["q"], np.repeat(c["s"][:1], 96, 0)), "f32")
 
 
+@pytest.mark.parametrize("far", ["x", "w", "scale", "zero"])
+@pytest.mark.parametrize("M,K,group", [(3, 288, 32), (5, 192, 64), (20, 256, 128)])
+def test_mm_rows_far_apart(far, M, K, group):
+    """Row strides whose multiples pass 31 bits."""
+    N = 3
+    c = integer_case(M, N, K, group, True, "bf16", K)
+    ops = dict(x=dev(c["x"], torch.bfloat16), w=dev(c["q"]), scale=dev(c["s"]), zero=dev(c["z"]))
+    t = ops[far]
+    ld = (1 << (28 if far == "zero" else 27)) // t.element_size()
+    rows = min(t.shape[0], 3)
+    wide = torch.zeros(rows * ld, dtype=t.dtype, device=DEV).view(rows, ld)
+    wide[:, :t.shape[1]] = t[:rows]
+    ops[far] = wide[:, :t.shape[1]]
+    if far == "x":
+        c["x"] = c["x"][:rows]
+    y = bsmm.bsmm_w4_mm(ops["x"], ops["w"], ops["scale"], ops["zero"], out_dtype="f32")
+    same(y, w4.w4_mm(c["x"], c["q"], c["s"], c["z"]), "f32")
+
+
 # sizes at which the cost rule takes tiles of 128 rows and of 256 (the last of
 # each group of sizes), with one K step to several, odd edges, and for groups
 # of 32 a last step of one group
