@@ -18,6 +18,10 @@
 // second launch sums them over the blocks before each, and a third places the
 // slots.  At most one block per compute unit keeps that table small; more
 // tokens make larger blocks.  Up to 64 tokens are one block and one launch.
+//
+// 16384 x 256 fp32, top-8 with the loss: choice 17 us (eight dependent wave
+// maxima a token), counts 4.9, slots 6.8; its gradient 10.6, 3.3 TB/s.  One
+// token of 64 experts: 5 us.
 
 #include <hip/hip_runtime.h>
 

@@ -74,8 +74,9 @@ bsmm_status run(const W4Args& a, void* workspace, size_t workspace_bytes, void* 
 // Tiles: one K step after another (128 rows: 0.8 / 1.0 / 1.2 us, 256 rows:
 // 0.95 / 1.02 / 1.55; fp32 walks three planes), in rounds of the tiles that
 // the 256 CUs hold: one of 256 rows (a full round 15 % longer), two of 128
-// (then 1.65 times as long as one).  Routed tiles take 1.25 times that: blocks
-// that experts leave partly empty, codes that come from HBM.
+// (then 1.65 times as long as one).  Routed, the number of tiles is a guess
+// and their codes come from HBM: 1.5 rounds, and one more for every 300 tiles
+// beyond 256.
 //
 //   rows x N x K              Rows   Tile128   Tile256   (us)
 //     260 x 5120 x 8192         92       100       126
@@ -85,9 +86,11 @@ bsmm_status run(const W4Args& a, void* workspace, size_t workspace_bytes, void* 
 //    2047 x 4096 x 4096                   86        77
 //     260 x 2048 x 4096 fp32    73       163       209   (groups of 64)
 //     800 x 5120 x 8192 fp32   749       467       430   (groups of 64)
-//    512 tokens x 4, 16 experts of 2048 x 2048:   rows 94, 128 50, 256 98
-//    1021 tokens x 8, 32 experts of 2048 x 4096:  rows 541, 128 256, 256 348
-//    128 tokens x 4, 16 experts of 2048 x 2048:   rows 34, 128 53, 256 90
+//    1021 tokens x 8, 32 experts of 2048 x 4096:   541       256       348
+//     256 tokens x 8, the same                     165       136
+//     128 tokens x 8, the same                     108       139
+//     512 tokens x 4, 16 experts of 2048 x 2048:    94        50        98
+//     200 tokens x 4, the same                      34        43
 //
 // Routed calls therefore never take 256 rows: an expert's last tile is half
 // empty on average.
@@ -112,8 +115,9 @@ W4Plan bsmm::w4_plan(const W4Args& a) {
   const double rows = 5.0 + 2.0 * (double)(blocks(bm) * bm) * a.N * a.K / (f32 ? 85e6 : kRate[g]);
   const int64_t n128 = blocks(128) * tile_cols, rest = n128 % 512;
   const double rounds128 =
-      1.65 * (double)(n128 / 512) + (rest == 0 ? 0.0 : rest <= 256 ? 1.0 : 1.55);
-  const double t128 = 4.0 + rounds128 * steps * kStep128[g] * (a.offsets ? 1.25 : 1.0);
+      a.offsets ? 1.5 + (n128 > 256 ? (double)(n128 - 256) / 300.0 : 0.0)
+                : 1.65 * (double)(n128 / 512) + (rest == 0 ? 0.0 : rest <= 256 ? 1.0 : 1.55);
+  const double t128 = 4.0 + rounds128 * steps * kStep128[g];
   if (a.offsets) return rows <= t128 ? W4Plan::Rows : W4Plan::Tile128;
   const double rounds256 = 1.15 * (double)((blocks(256) * tile_cols + 255) / 256);
   const double t256 = 4.0 + rounds256 * steps * kStep256[g];
