@@ -33,7 +33,6 @@ namespace bsmm {
 namespace {
 
 constexpr int kWaves = 16;              // waves of a workgroup
-constexpr int kThreads = kWaves * 64;
 constexpr uint32_t kNoKey = 0x007FFFFFu;   // the key of -inf; nothing at or below it is chosen
 
 typedef unsigned long long u64;
