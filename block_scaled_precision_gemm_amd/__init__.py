@@ -178,8 +178,12 @@ def _stream(stream):
     return torch.cuda.current_stream().cuda_stream
 
 
-_WS = {}          # workspace buffer per (device, stream handle)
+_WS = {}          # workspace (address, bytes) per (device, stream handle)
 _WS_NEED = {}     # workspace bytes per (op, G, M, N, K, out dtype); cleared by the override
+
+
+class _Address(int):
+    """A buffer's address that keeps the buffer alive."""
 
 
 def _workspace(op, G, M, N, K, out_dtype, device, stream, handle):
@@ -192,27 +196,50 @@ def _workspace(op, G, M, N, K, out_dtype, device, stream, handle):
     return _buffer(need, device, stream, handle)
 
 
+def _capturing(stream):
+    """Whether ``stream`` (None: the current one) is being captured."""
+    cuda = _torch().cuda
+    if stream is None:
+        return cuda.is_current_stream_capturing()
+    with cuda.stream(stream):
+        return cuda.is_current_stream_capturing()
+
+
+def _new_buffer(need, device, stream):
+    torch = _torch()
+    if stream is None:
+        buf = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        with torch.cuda.stream(stream):
+            buf = torch.empty(need, dtype=torch.uint8, device=device)
+    address = _Address(buf.data_ptr())
+    address.buffer = buf
+    return address, need
+
+
 def _buffer(need, device, stream, handle):
-    """A workspace of at least ``need`` bytes, cached per (device, stream) and
-    grown when a call needs more.  Calls on one stream run in order, so they
-    may share a buffer; calls on different streams get different buffers.  A
-    buffer is allocated while its stream is current, so the caching
-    allocator hands its memory to no other stream before the work queued on
-    that stream has finished, even once the buffer is replaced by a larger
-    one."""
+    """(address, bytes) of a workspace of at least ``need`` bytes, or (None, 0).
+
+    It is cached per (device, stream) and grown when a call needs more.  Calls
+    on one stream run in order, so they may share a buffer; calls on different
+    streams get different buffers.  A buffer is allocated while its stream is
+    current, so the caching allocator hands its memory to no other stream
+    before the work queued on that stream has finished, even once the buffer
+    is replaced by a larger one.
+
+    A call that is captured in a graph gets a buffer of its own instead, from
+    the graph's memory: the graph keeps the address, uses it at every replay
+    and on whatever stream it is replayed, none of which a buffer shared with
+    eager calls, or replaced by a larger one, would survive."""
     if need == 0:
         return None, 0
+    if _capturing(stream):
+        return _new_buffer(need, device, stream)
     wkey = (device, handle)
-    buf = _WS.get(wkey)
-    if buf is None or buf.numel() < need:
-        torch = _torch()
-        if stream is None:
-            buf = torch.empty(need, dtype=torch.uint8, device=device)
-        else:
-            with torch.cuda.stream(stream):
-                buf = torch.empty(need, dtype=torch.uint8, device=device)
-        _WS[wkey] = buf
-    return buf, buf.numel()
+    ws = _WS.get(wkey)
+    if ws is None or ws[1] < need:
+        ws = _WS[wkey] = _new_buffer(need, device, stream)
+    return ws
 
 
 def _dtype_code(dt):
@@ -259,8 +286,7 @@ def _ws_args(workspace, op, G, M, N, K, code, device, stream, handle):
     if workspace is False:
         return None, 0
     if workspace is None:
-        buf, n = _workspace(op, G, M, N, K, code, device, stream, handle)
-        return (buf.data_ptr() if buf is not None else None), n
+        return _workspace(op, G, M, N, K, code, device, stream, handle)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -876,8 +902,7 @@ def _w4_workspace(xc, E, R, S, N, K, group, dev, stream, handle):
     """Workspace pointer and bytes of a 4-bit product (fp32 x, many rows)."""
     if xc != F32:
         return None, 0
-    buf, n = _buffer(load().bsmm_w4_workspace_bytes(xc, E, R, S, N, K, group), dev, stream, handle)
-    return (buf.data_ptr(), n) if n else (None, 0)
+    return _buffer(load().bsmm_w4_workspace_bytes(xc, E, R, S, N, K, group), dev, stream, handle)
 
 
 def _w4_out(out, rows, cols, code, torch, dtypes, dev):
@@ -1031,7 +1056,7 @@ def bsmm_route_topk(logits, k, *, mask=None, renorm=True, alpha=None, stream=Non
     cp = op + 4 * S
     hs = _stream(stream)
     lib = load()
-    wbuf, wn = _buffer(lib.bsmm_route_workspace_bytes(T, E), dev, stream, hs)
+    wsp, wsn = _buffer(lib.bsmm_route_workspace_bytes(T, E), dev, stream, hs)
     lp = pp = tp = None
     if alpha is not None:
         sums = new((E + 1,), (1,), dtype=f32, device=dev)
@@ -1039,8 +1064,7 @@ def bsmm_route_topk(logits, k, *, mask=None, renorm=True, alpha=None, stream=Non
         tp = pp + 4 * E
     status = lib.bsmm_route_topk(
         logits.data_ptr(), ldl, code, mp, k, 1 if renorm else 0, alpha or 0.0, index.data_ptr(),
-        weight.data_ptr(), cp, cp + 4 * E, op, lp, pp, tp, T, E, wbuf.data_ptr() if wn else None,
-        wn, hs)
+        weight.data_ptr(), cp, cp + 4 * E, op, lp, pp, tp, T, E, wsp, wsn, hs)
     if status:
         _check(status)
     order, counts, offsets, live = torch.unsafe_split_with_sizes(ints, (S, E, E + 1, 1))

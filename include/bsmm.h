@@ -33,7 +33,8 @@
  *   call still succeeds with a plan that needs none (except
  *   bsmm_fp8_groupwise, whose kernels read repacked scales from it).  Results do not depend on
  *   the split: int32 accumulators are identical for every split, fp32 sums of
- *   the split partials are added in ascending split order.
+ *   the split partials are added in ascending split order.  A graph that
+ *   captured a call uses its workspace at every replay.
  * Threads: the library keeps no mutable state across calls except a
  *   thread-local error message and the optional plan override; calls on
  *   different streams may run concurrently.  Two calls that write the same

@@ -1,0 +1,128 @@
+"""Calls that need a workspace, in graphs: a graph's memory is its own,
+whatever eager calls or other graphs do between its replays.  Integers as in
+the products' tests, so that results must be equal."""
+
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_precision_gemm_amd as bsmm
+from oracle import route as R, w4
+from test_gpu_route import check_forward, logits
+from test_gpu_w4 import dev, integer_case, same
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+
+
+@pytest.fixture(autouse=True)
+def _lib(gpu_lib):
+    yield
+
+
+class RouteCall:
+    """The router on T tokens: three launches through a workspace."""
+
+    def __init__(self, T, E=40, k=4):
+        self.T, self.E, self.k = T, E, k
+        self.need = bsmm.load().bsmm_route_workspace_bytes(T, E)
+        self.x = torch.empty(T, E, device=DEV)
+
+    def feed(self, seed):
+        self.host = logits(self.T, self.E, "f32", seed)
+        self.x.copy_(dev(self.host))
+
+    def run(self):
+        self.out = bsmm.bsmm_route_topk(self.x, self.k, alpha=1.0)
+
+    def clear(self):
+        for t in self.out:
+            t.fill_(-9)
+
+    def check(self):
+        check_forward(self.out, R.route(self.host, self.k, alpha=1.0))
+
+
+class ProductCall:
+    """fp32 activations on tiles: two launches through a workspace."""
+
+    def __init__(self, M, N=2100, K=512):
+        self.M, self.N, self.K = M, N, K
+        self.need = bsmm.load().bsmm_w4_workspace_bytes(bsmm.F32, 1, M, M, N, K, 64)
+        c = integer_case(M, N, K, 64, True, "f32", 3)
+        self.w = [c["q"], c["s"], c["z"]]
+        self.dw = [dev(t) for t in self.w]
+        self.x = torch.empty(M, K, device=DEV)
+
+    def feed(self, seed):
+        self.host = np.random.default_rng(seed).integers(-3, 4, (self.M, self.K)) \
+            .astype(np.float32)
+        self.x.copy_(dev(self.host))
+
+    def run(self):
+        self.out = bsmm.bsmm_w4_mm(self.x, *self.dw, out_dtype="f32")
+
+    def clear(self):
+        self.out.fill_(-9)
+
+    def check(self):
+        same(self.out, w4.w4_mm(self.host, *self.w), "f32")
+
+
+CALLS = [(RouteCall, 300, 6000), (ProductCall, 1300, 2048)]
+
+
+def captured(call, **kw):
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, **kw):
+        call.run()
+    return g
+
+
+@pytest.mark.parametrize("kind,size,larger", CALLS)
+def test_graph_after_a_larger_eager_call(kind, size, larger):
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        call = kind(size)
+        assert call.need > 0
+        call.feed(0)
+        call.run()
+        g = captured(call, stream=s)
+        big = kind(larger)
+        assert big.need > call.need
+        big.feed(1)
+        big.run()
+        others = [torch.full((call.need,), 0x5A, dtype=torch.uint8, device=DEV) for _ in range(8)]
+        for i in range(3):
+            call.feed(10 + i)
+            call.clear()
+            big.run()
+            g.replay()
+            s.synchronize()
+            call.check()
+            big.check()
+            assert all((t == 0x5A).all() for t in others)
+
+
+@pytest.mark.parametrize("kind,size,_", CALLS)
+def test_two_graphs_at_once(kind, size, _):
+    calls = [kind(size), kind(size)]
+    for i, c in enumerate(calls):
+        c.feed(20 + i)
+        c.run()
+    torch.cuda.synchronize()
+    graphs = [captured(c) for c in calls]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for i in range(3):
+        for j, c in enumerate(calls):
+            c.feed(30 + 2 * i + j)
+            c.clear()
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for s, g in zip(streams, graphs):
+                with torch.cuda.stream(s):
+                    g.replay()
+        torch.cuda.synchronize()
+        for c in calls:
+            c.check()

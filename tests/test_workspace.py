@@ -1,0 +1,40 @@
+"""Which workspace the binding hands to a call (no GPU needed: the policy
+does not look at the device)."""
+
+import pytest
+import torch
+
+import block_scaled_precision_gemm_amd as bsmm
+
+CPU = torch.device("cpu")
+
+
+@pytest.fixture(autouse=True)
+def _own_cache(monkeypatch):
+    """These buffers are on the host: they stay out of the real cache, and
+    there is no stream to ask."""
+    monkeypatch.setattr(bsmm, "_WS", type(bsmm._WS)())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+
+
+def test_eager_calls_of_a_stream_share_a_buffer():
+    a, n = bsmm._buffer(64, CPU, None, 1)
+    assert n == 64 and bsmm._buffer(32, CPU, None, 1) == (a, 64)
+    b, n = bsmm._buffer(128, CPU, None, 1)
+    assert n == 128 and bsmm._buffer(64, CPU, None, 1) == (b, 128)
+    assert bsmm._buffer(64, CPU, None, 2)[0] != b
+    assert bsmm._buffer(0, CPU, None, 3) == (None, 0)
+
+
+def test_a_captured_call_has_its_own_buffer(monkeypatch):
+    """Nothing that a graph recorded is handed to another call, eager or
+    captured, and no cached address is recorded."""
+    eager, _ = bsmm._buffer(64, CPU, None, 1)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    a, n = bsmm._buffer(64, CPU, None, 1)
+    b, _ = bsmm._buffer(64, CPU, None, 1)
+    assert n == 64 and len({int(eager), int(a), int(b)}) == 3
+    # alive for as long as the address is held: until the call's launches
+    assert a.buffer.data_ptr() == a
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    assert bsmm._buffer(64, CPU, None, 1) == (eager, 64)
