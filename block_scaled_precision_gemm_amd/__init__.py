@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from typing import NamedTuple
 
 __all__ = [
@@ -178,7 +179,14 @@ def _stream(stream):
     return torch.cuda.current_stream().cuda_stream
 
 
-_WS = {}          # workspace (address, bytes) per (device, stream handle)
+class _Workspaces(threading.local):
+    """A host thread's workspaces: (address, bytes) per (device, stream handle)."""
+
+    def __init__(self):
+        self.by = {}
+
+
+_WS = _Workspaces()
 _WS_NEED = {}     # workspace bytes per (op, G, M, N, K, out dtype); cleared by the override
 
 
@@ -220,9 +228,11 @@ def _new_buffer(need, device, stream):
 def _buffer(need, device, stream, handle):
     """(address, bytes) of a workspace of at least ``need`` bytes, or (None, 0).
 
-    It is cached per (device, stream) and grown when a call needs more.  Calls
-    on one stream run in order, so they may share a buffer; calls on different
-    streams get different buffers.  A buffer is allocated while its stream is
+    It is cached per host thread, device and stream, and grown when a call
+    needs more.  One thread's calls on one stream run in order, so they may
+    share a buffer.  Two threads' calls on one stream do not: a call is several
+    launches, and between them another thread may queue its own (the C calls
+    release the interpreter's lock).  A buffer is allocated while its stream is
     current, so the caching allocator hands its memory to no other stream
     before the work queued on that stream has finished, even once the buffer
     is replaced by a larger one.
@@ -236,9 +246,9 @@ def _buffer(need, device, stream, handle):
     if _capturing(stream):
         return _new_buffer(need, device, stream)
     wkey = (device, handle)
-    ws = _WS.get(wkey)
+    ws = _WS.by.get(wkey)
     if ws is None or ws[1] < need:
-        ws = _WS[wkey] = _new_buffer(need, device, stream)
+        ws = _WS.by[wkey] = _new_buffer(need, device, stream)
     return ws
 
 

@@ -38,7 +38,8 @@
  * Threads: the library keeps no mutable state across calls except a
  *   thread-local error message and the optional plan override; calls on
  *   different streams may run concurrently.  Two calls that write the same
- *   output or share a workspace on different streams race.
+ *   output or share a workspace race on different streams, and from different
+ *   threads on one stream too: a call may be several launches.
  */
 #ifndef BSMM_H
 #define BSMM_H

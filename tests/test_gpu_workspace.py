@@ -1,6 +1,9 @@
-"""Calls that need a workspace, in graphs: a graph's memory is its own,
-whatever eager calls or other graphs do between its replays.  Integers as in
+"""Calls that need a workspace, in graphs and from several threads: a graph's
+memory is its own, whatever eager calls or other graphs do between its
+replays, and so is a host thread's.  Integers as in
 the products' tests, so that results must be equal."""
+
+import threading
 
 import numpy as np
 import pytest
@@ -126,3 +129,32 @@ def test_two_graphs_at_once(kind, size, _):
         torch.cuda.synchronize()
         for c in calls:
             c.check()
+
+
+@pytest.mark.parametrize("kind,size,larger", CALLS)
+def test_threads_on_one_stream(kind, size, larger):
+    s = torch.cuda.Stream()
+    calls = [kind(size), kind(larger), kind(size)]
+    for i, c in enumerate(calls):
+        c.feed(40 + i)
+    torch.cuda.synchronize()
+    start, errors = threading.Barrier(len(calls)), []
+
+    def work(c):
+        try:
+            start.wait(30)
+            with torch.cuda.stream(s):
+                for _ in range(20):
+                    c.run()
+                s.synchronize()
+        except Exception as e:      # reported by the test's own thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(c,)) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not errors
+    for c in calls:
+        c.check()

@@ -1,6 +1,8 @@
 """Which workspace the binding hands to a call (no GPU needed: the policy
 does not look at the device)."""
 
+from concurrent.futures import ThreadPoolExecutor
+
 import pytest
 import torch
 
@@ -38,3 +40,14 @@ def test_a_captured_call_has_its_own_buffer(monkeypatch):
     assert a.buffer.data_ptr() == a
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     assert bsmm._buffer(64, CPU, None, 1) == (eager, 64)
+
+
+def test_threads_have_their_own_buffers():
+    """The launches of two threads' calls on one stream may alternate."""
+    mine = bsmm._buffer(64, CPU, None, 1)
+    with ThreadPoolExecutor(1) as pool:
+        def theirs():
+            return pool.submit(bsmm._buffer, 64, CPU, None, 1).result()
+        other = theirs()
+        assert other[0] != mine[0]
+        assert theirs() == other and bsmm._buffer(64, CPU, None, 1) == mine
