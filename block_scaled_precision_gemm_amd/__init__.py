@@ -24,6 +24,7 @@ __all__ = [
     "bsmm_quant_fp8_columns", "bsmm_quant_fp8_weight", "bsmm_quant_fp8_blockwise_columns",
     "bsmm_quant_w4", "bsmm_w4_mm", "bsmm_w4_expert_mm",
     "bsmm_route_topk", "bsmm_route_topk_backward", "Route",
+    "bsmm_w4_workspace_bytes", "bsmm_route_workspace_bytes",
     "bsmm_workspace_bytes", "bsmm_query_plan", "bsmm_set_override", "bsmm_set_override_tail", "bsmm_set_streamk_grid", "bsmm_mfma_probe",
     "bsmm_variant_names", "bsmm_version", "bsmm_timing_enable", "bsmm_timing_read",
     "I32", "F32", "BF16", "E4M3", "OP_INT8_ROWWISE", "OP_FP8_BLOCKWISE", "OP_FP8_MX_BMM",
@@ -293,10 +294,15 @@ def _out(out, shape, code, device):
 
 
 def _ws_args(workspace, op, G, M, N, K, code, device, stream, handle):
-    if workspace is False:
-        return None, 0
     if workspace is None:
         return _workspace(op, G, M, N, K, code, device, stream, handle)
+    return _given(workspace)
+
+
+def _given(workspace):
+    """Pointer and bytes of a caller's workspace (False: none)."""
+    if workspace is False:
+        return None, 0
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -908,8 +914,10 @@ def _w4_weight(w, ws, wst, scale, zero, K, u8):
     return group, code, sst, zero.data_ptr(), zst
 
 
-def _w4_workspace(xc, E, R, S, N, K, group, dev, stream, handle):
+def _w4_workspace(workspace, xc, E, R, S, N, K, group, dev, stream, handle):
     """Workspace pointer and bytes of a 4-bit product (fp32 x, many rows)."""
+    if workspace is not None:
+        return _given(workspace)
     if xc != F32:
         return None, 0
     return _buffer(load().bsmm_w4_workspace_bytes(xc, E, R, S, N, K, group), dev, stream, handle)
@@ -929,12 +937,15 @@ def _w4_out(out, rows, cols, code, torch, dtypes, dev):
     return out, st[0]
 
 
-def bsmm_w4_mm(x, w, scale, zero=None, *, out_dtype="bf16", out=None, stream=None):
+def bsmm_w4_mm(x, w, scale, zero=None, *, out_dtype="bf16", out=None, workspace=None,
+               stream=None):
     """Activations times a 4-bit weight: x @ W.T with W = (code - zero) * scale.
 
     x: bf16 or fp32 [M, K].  w: uint8 [N, K/2], scale: bf16 or fp32
     [N, K/group], zero: uint8 [N, K/group] or None (8), as bsmm_quant_w4
     returns them (group 32, 64 or 128).  Returns [M, N], fp32 or bf16.
+    workspace: None for a cached one, False for none, or a 16-byte aligned
+    tensor of bsmm_w4_workspace_bytes bytes.
     """
     xs, ws = x.shape, w.shape
     if len(xs) != 2 or len(ws) != 2:
@@ -951,7 +962,7 @@ def bsmm_w4_mm(x, w, scale, zero=None, *, out_dtype="bf16", out=None, stream=Non
     dev = x.device
     o, ldo = _w4_out(out, M, N, code, torch, dtypes, dev)
     hs = _stream(stream)
-    wsp, wsn = _w4_workspace(xc, 1, M, M, N, K, group, dev, stream, hs)
+    wsp, wsn = _w4_workspace(workspace, xc, 1, M, M, N, K, group, dev, stream, hs)
     status = load().bsmm_w4_mm(x.data_ptr(), xst[0], xc, w.data_ptr(), wst[0], scale.data_ptr(),
                                sst[0], sc, zp, zst[0], group, o.data_ptr(), ldo, code, M, N, K,
                                wsp, wsn, hs)
@@ -961,7 +972,7 @@ def bsmm_w4_mm(x, w, scale, zero=None, *, out_dtype="bf16", out=None, stream=Non
 
 
 def bsmm_w4_expert_mm(x, w, scale, zero, order, offsets, *, slots_per_row=1, row_scale=None,
-                      out_dtype="bf16", out=None, stream=None):
+                      out_dtype="bf16", out=None, workspace=None, stream=None):
     """Routed rows times their experts' 4-bit weights.
 
     x: bf16 or fp32 [R, K].  w: uint8 [E, N, K/2], scale [E, N, K/group], zero
@@ -970,7 +981,8 @@ def bsmm_w4_expert_mm(x, w, scale, zero, order, offsets, *, slots_per_row=1, row
     returns them.  Slot s reads row s // slots_per_row of x: slots_per_row is
     the number of choices where x holds tokens, 1 where it holds slots.
     row_scale: fp32 [S] (the routing weights, slot order) or None.  Returns
-    [S, N] in slot order, zeros for slots without an expert.
+    [S, N] in slot order, zeros for slots without an expert.  workspace as for
+    bsmm_w4_mm.
     """
     xs, ws = x.shape, w.shape
     if len(xs) != 2 or len(ws) != 3:
@@ -995,7 +1007,7 @@ def bsmm_w4_expert_mm(x, w, scale, zero, order, offsets, *, slots_per_row=1, row
     dev = x.device
     o, ldo = _w4_out(out, S, N, code, torch, dtypes, dev)
     hs = _stream(stream)
-    wsp, wsn = _w4_workspace(xc, E, R, S, N, K, group, dev, stream, hs)
+    wsp, wsn = _w4_workspace(workspace, xc, E, R, S, N, K, group, dev, stream, hs)
     status = load().bsmm_w4_expert_mm(
         x.data_ptr(), xst[0], xc, w.data_ptr(), wst[0], wst[1], scale.data_ptr(), sst[0], sst[1],
         sc, zp, zst[0], zst[1], group, order.data_ptr(), offsets.data_ptr(), slots_per_row,
@@ -1040,7 +1052,8 @@ def _route_logits(logits):
     return shape[0], shape[1], st[0], code
 
 
-def bsmm_route_topk(logits, k, *, mask=None, renorm=True, alpha=None, stream=None):
+def bsmm_route_topk(logits, k, *, mask=None, renorm=True, alpha=None, workspace=None,
+                    stream=None):
     """Top-k experts of every token, with what their products need.
 
     logits: bf16 or fp32 [T, E], unit stride along E.  mask: bool or uint8
@@ -1049,6 +1062,8 @@ def bsmm_route_topk(logits, k, *, mask=None, renorm=True, alpha=None, stream=Non
     Returns a Route: index and weight [T, k], counts [E], offsets [E + 1] and
     order [T * k] (the slots t * k + j sorted by expert, for
     bsmm_w4_expert_mm), and with a loss live [1], prob_sum [E] and loss [1].
+    workspace: None for a cached one, or a 16-byte aligned tensor of
+    bsmm_route_workspace_bytes bytes.
     """
     T, E, ldl, code = _route_logits(logits)
     if not 1 <= k <= min(E, 32):
@@ -1066,7 +1081,8 @@ def bsmm_route_topk(logits, k, *, mask=None, renorm=True, alpha=None, stream=Non
     cp = op + 4 * S
     hs = _stream(stream)
     lib = load()
-    wsp, wsn = _buffer(lib.bsmm_route_workspace_bytes(T, E), dev, stream, hs)
+    wsp, wsn = (_buffer(lib.bsmm_route_workspace_bytes(T, E), dev, stream, hs)
+                if workspace is None else _given(workspace))
     lp = pp = tp = None
     if alpha is not None:
         sums = new((E + 1,), (1,), dtype=f32, device=dev)
@@ -1128,6 +1144,16 @@ def bsmm_route_topk_backward(logits, index, weight, counts, live, *, dweight=Non
 
 def bsmm_workspace_bytes(op, G, M, N, K, out_dtype):
     return load().bsmm_workspace_bytes(op, G, M, N, K, _dtype_code(out_dtype))
+
+
+def bsmm_w4_workspace_bytes(x_dtype, E, R, S, N, K, group):
+    """Workspace bytes bsmm_w4_expert_mm wants (bsmm_w4_mm: E = 1, R = S = M)."""
+    return load().bsmm_w4_workspace_bytes(_float_code(x_dtype, "x_dtype"), E, R, S, N, K, group)
+
+
+def bsmm_route_workspace_bytes(T, E):
+    """Workspace bytes bsmm_route_topk needs."""
+    return load().bsmm_route_workspace_bytes(T, E)
 
 
 def bsmm_query_plan(op, G, M, N, K, out_dtype, workspace_bytes=2**62):

@@ -29,15 +29,15 @@ class RouteCall:
 
     def __init__(self, T, E=40, k=4):
         self.T, self.E, self.k = T, E, k
-        self.need = bsmm.load().bsmm_route_workspace_bytes(T, E)
+        self.need = bsmm.bsmm_route_workspace_bytes(T, E)
         self.x = torch.empty(T, E, device=DEV)
 
     def feed(self, seed):
         self.host = logits(self.T, self.E, "f32", seed)
         self.x.copy_(dev(self.host))
 
-    def run(self):
-        self.out = bsmm.bsmm_route_topk(self.x, self.k, alpha=1.0)
+    def run(self, **kw):
+        self.out = bsmm.bsmm_route_topk(self.x, self.k, alpha=1.0, **kw)
 
     def clear(self):
         for t in self.out:
@@ -52,7 +52,7 @@ class ProductCall:
 
     def __init__(self, M, N=2100, K=512):
         self.M, self.N, self.K = M, N, K
-        self.need = bsmm.load().bsmm_w4_workspace_bytes(bsmm.F32, 1, M, M, N, K, 64)
+        self.need = bsmm.bsmm_w4_workspace_bytes("f32", 1, M, M, N, K, 64)
         c = integer_case(M, N, K, 64, True, "f32", 3)
         self.w = [c["q"], c["s"], c["z"]]
         self.dw = [dev(t) for t in self.w]
@@ -63,8 +63,8 @@ class ProductCall:
             .astype(np.float32)
         self.x.copy_(dev(self.host))
 
-    def run(self):
-        self.out = bsmm.bsmm_w4_mm(self.x, *self.dw, out_dtype="f32")
+    def run(self, **kw):
+        self.out = bsmm.bsmm_w4_mm(self.x, *self.dw, out_dtype="f32", **kw)
 
     def clear(self):
         self.out.fill_(-9)
@@ -158,3 +158,24 @@ def test_threads_on_one_stream(kind, size, larger):
     assert not errors
     for c in calls:
         c.check()
+
+
+@pytest.mark.parametrize("kind,size,_", CALLS)
+def test_given_workspace(kind, size, _):
+    """The caller's buffer is the one that is used, and no byte past it."""
+    call = kind(size)
+    call.feed(50)
+    buf = torch.full((call.need + 256,), 0x5A, dtype=torch.uint8, device=DEV)
+    cached = dict(bsmm._WS.by)
+    call.run(workspace=buf[:call.need])
+    call.check()
+    assert bsmm._WS.by == cached
+    assert not (buf[:call.need] == 0x5A).all() and (buf[call.need:] == 0x5A).all()
+
+
+def test_product_without_workspace():
+    call = ProductCall(300)
+    call.feed(51)
+    for ws in (False, torch.empty(16, dtype=torch.uint8, device=DEV)):
+        call.run(workspace=ws)
+        call.check()

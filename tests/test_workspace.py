@@ -51,3 +51,16 @@ def test_threads_have_their_own_buffers():
         other = theirs()
         assert other[0] != mine[0]
         assert theirs() == other and bsmm._buffer(64, CPU, None, 1) == mine
+
+
+def test_a_given_workspace():
+    """Its address and size are passed on, and the cache stays empty."""
+    ws = torch.empty(100, dtype=torch.float32)
+    for given, want in ((ws, (ws.data_ptr(), 400)), (False, (None, 0))):
+        got = bsmm._w4_workspace(given, bsmm.F32, 1, 2048, 2048, 4096, 4096, 128, CPU, None, 1)
+        assert got == want and not bsmm._WS.by
+    for call in (bsmm.bsmm_w4_mm, bsmm.bsmm_w4_expert_mm, bsmm.bsmm_route_topk):
+        assert "workspace" in call.__kwdefaults__
+    assert bsmm.bsmm_w4_workspace_bytes(torch.float32, 1, 2048, 2048, 4096, 4096, 128) == \
+        3 * 2048 * 4096 * 2
+    assert bsmm.bsmm_route_workspace_bytes(100, 64) > 0
