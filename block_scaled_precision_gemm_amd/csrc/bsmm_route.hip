@@ -326,7 +326,9 @@ __device__ void write_loss(const RouteArgs& a, Shared& sh, float p, int live) {
 }
 
 // Order of the slots of tokens [t0, t1): sh.base holds the position of each
-// expert's next slot, sh.unused_base that of the next slot without one.
+// expert's next slot, sh.unused_base that of the next slot without one.  They
+// come from the workspace: should a caller have let something else write it
+// between the launches, positions outside the order are not written.
 // `kept`: sh.index already has the choices (64 tokens at most).
 __device__ void place(const RouteArgs& a, Shared& sh, int t0, int t1, bool kept) {
   const int k = a.k;
@@ -364,7 +366,7 @@ __device__ void place(const RouteArgs& a, Shared& sh, int t0, int t1, bool kept)
         at = sh.unused[t];
         for (int j = s - 1; j >= t * k && sh.index[j] < 0; --j) ++at;
       }
-      a.order[at] = tb * k + s;
+      if ((unsigned)at < (unsigned)(a.T * k)) a.order[at] = tb * k + s;
     }
     if (tb + 64 >= t1) break;
     __syncthreads();

@@ -251,3 +251,31 @@ def test_streams_and_graph(T):
         e = bsmm.bsmm_route_topk_backward(x, r.index, r.weight, r.counts, r.live,
                                           dloss=torch.ones(1, device=DEV), alpha=1.0)
         assert torch.equal(d, e)
+
+
+def test_overwritten_workspace_stays_in_bounds():
+    """Positions that a shared workspace has spoiled are not written past the
+    order.  Spoiled here by counts that lie on the first block's row of slots
+    before it: that block's slots then move up by their experts' counts."""
+    T, E, k = 100, 8, 2
+    x = dev(logits(T, E, "f32", 12))
+    need = bsmm.bsmm_route_workspace_bytes(T, E)
+    blocks = 7                                   # of 16 tokens
+    ws = torch.zeros(need, dtype=torch.uint8, device=DEV)
+    ints = torch.full((T * k + 1024,), -7, dtype=torch.int32, device=DEV)
+    index = torch.empty(T, k, dtype=torch.int32, device=DEV)
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=DEV)
+    weight = torch.empty(T, k, device=DEV)
+    before = ws.data_ptr() + need - blocks * E * 4
+    assert bsmm.load().bsmm_route_topk(
+        x.data_ptr(), E, bsmm.F32, None, k, 1, 0.0, index.data_ptr(), weight.data_ptr(), before,
+        offsets.data_ptr(), ints.data_ptr(), None, None, None, T, E, ws.data_ptr(), need,
+        torch.cuda.current_stream().cuda_stream) == 0
+    got = host(ints)
+    assert (got[T * k:] == -7).all() and (got[:T * k] >= -7).all()
+    assert host(offsets)[E] == T * k
+    # the last expert's slots of the first block lie behind its run now
+    e = host(index).reshape(-1)
+    last = np.bincount(e, minlength=E).nonzero()[0][-1]
+    hit = np.flatnonzero(e[:16 * k] == last)
+    assert hit.size and not np.isin(hit, got[:T * k]).any()
