@@ -96,33 +96,37 @@ struct Item { int e, p0, rows; };
 // cut into blocks of bm, in expert order.  Runs in every wave alike: each
 // lane counts the blocks of its share of the experts, a scan over the lanes
 // finds the one that holds the item.  Offsets are clamped into [0, S], so
-// that no array content can lead outside the buffers.
-__device__ Item find_item(const int32_t* __restrict__ offsets, int E, int S, int bm, int item) {
+// that no array content can lead outside the buffers; offsets that do not
+// rise may count to more than 32 bits hold, and the sums then wrap, but an
+// item is taken only from within a run.
+__device__ Item find_item(const int32_t* __restrict__ offsets, int E, int S, unsigned bm,
+                          unsigned item) {
   const int lane = threadIdx.x & 63;
   const int per = (E + 63) / 64;
   const int e0 = min(lane * per, E), e1 = min(e0 + per, E);
-  int n = 0;
+  unsigned n = 0;
   for (int e = e0; e < e1; ++e) {
     const int lo = min(max(offsets[e], 0), S), hi = min(max(offsets[e + 1], lo), S);
-    n += (hi - lo + bm - 1) / bm;
+    n += ((unsigned)(hi - lo) + bm - 1) / bm;
   }
-  int incl = n;
+  unsigned incl = n;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int t = __shfl_up(incl, d);
+    const unsigned t = __shfl_up(incl, d);
     if (lane >= d) incl += t;
   }
   const unsigned long long past = __ballot(incl > item);
   if (past == 0) return Item{0, 0, 0};
   const int src = __ffsll(past) - 1;
-  int rest = item - (incl - n);
+  unsigned rest = item - (incl - n);
   Item r{0, 0, 0};
   if (lane == src) {
     for (int e = e0; e < e1; ++e) {
       const int lo = min(max(offsets[e], 0), S), hi = min(max(offsets[e + 1], lo), S);
-      const int b = (hi - lo + bm - 1) / bm;
+      const unsigned b = ((unsigned)(hi - lo) + bm - 1) / bm;
       if (rest < b) {
-        r = Item{e, lo + rest * bm, min(hi - lo - rest * bm, bm)};
+        const int at = (int)(rest * bm);
+        r = Item{e, lo + at, min(hi - lo - at, (int)bm)};
         break;
       }
       rest -= b;
@@ -143,8 +147,8 @@ __device__ __forceinline__ void store_out(const W4Args& a, int64_t at, float v) 
 // shared out over the items.
 __device__ __forceinline__ void zero_unused(const W4Args& a, int col, int cols, int item,
                                             int items, int threads) {
-  const int used = min(max(a.offsets[a.E], 0), a.S);
-  for (int p = used + item; p < a.S; p += items) {
+  const unsigned used = min(max(a.offsets[a.E], 0), a.S);
+  for (unsigned p = used + item; p < (unsigned)a.S; p += items) {    // both below 2^31
     const int slot = a.order[p];
     if (slot < 0 || slot >= a.S) continue;
     for (int i = threadIdx.x; i < cols; i += threads)

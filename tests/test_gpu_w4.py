@@ -363,6 +363,31 @@ def test_expert_lists_out_of_range():
     assert (got[[6, 11]] == -3).all()
 
 
+def test_expert_many_slots():
+    """More items than one launch holds, and offsets that fall: 512 runs of
+    all 2^27 slots count 2^32 blocks of 16 rows, and nothing outside the
+    arrays may be touched."""
+    E, K, S = 1024, 32, 1 << 27
+    c = integer_case(1, 1, K, 32, False, "f32", 15, E)
+    x, q, s = dev(c["x"]), dev(c["q"]), dev(c["s"])
+    order = torch.arange(S, dtype=torch.int32, device=DEV).flip(0).contiguous()
+    guard = torch.full((S + 2048, 1), -3.0, device=DEV)
+    out = guard[1024:1024 + S]
+    ends = np.sort(np.random.default_rng(1).integers(0, S + 1, E + 1)).astype(np.int32)
+    ends[0] = 0
+    each = dev(w4.w4_expert_mm(c["x"], c["q"], c["s"], None, np.arange(E), np.arange(E + 1), E)
+               .astype(np.float32))
+    bsmm.bsmm_w4_expert_mm(x, q, s, None, order, dev(ends), slots_per_row=S, out_dtype="f32",
+                           out=out)
+    want = torch.cat([torch.repeat_interleave(each, dev(np.diff(ends).astype(np.int64)), 0),
+                      torch.zeros(S - int(ends[-1]), 1, device=DEV)])
+    assert torch.equal(out, want.flip(0))
+    ends[::2], ends[1::2] = 0, S
+    bsmm.bsmm_w4_expert_mm(x, q, s, None, order, dev(ends), slots_per_row=S, out_dtype="f32",
+                           out=out)
+    assert (guard[:1024] == -3).all() and (guard[1024 + S:] == -3).all()
+
+
 # ----------------------------------------------------- streams and graphs --
 
 @pytest.mark.parametrize("M", [1, 40, 200])
