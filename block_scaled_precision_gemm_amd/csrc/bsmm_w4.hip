@@ -2,18 +2,16 @@
 //
 //   out[p, n] = sum_g scale[n, g] * sum_{k in g} (code[n, k] - zero[n, g]) * x[p, k]
 //
-// A code enters the matrix instruction as the bf16 number 16 + code, which
-// is the bit pattern 0x4180 | code << 3: two codes of a dword become a
-// packed pair with one shift and one and-or.  With d = sum (16 + code) x and
-// e = sum x over a group (e by the same instruction against ones), the
-// group's contribution is scale * (d - (16 + zero) * e): every product is
-// exact, the sums are fp32, and nothing is rounded to fewer bits before the
-// output.  fp32 activations are cut into three bf16 numbers that add up to
-// them exactly (8 + 8 + 8 bits), one matrix instruction each.
-//
-// The pair of codes in a dword's half words are 4 apart, so the activations'
-// 8 consecutive elements are paired alike (k, k + 4): the order of k inside
-// one matrix instruction is free as long as both operands share it.
+// The matrix instructions take code - zero, an integer of at most 8 bits and a
+// sign and so exact in bf16: every product is exact, the sums are fp32 and
+// hold nothing but the result's own terms, and nothing is rounded to fewer
+// bits before the output.  Sums of 16 + code less 16 + zero times the sum of x
+// take half the instructions to unpack, but both are larger than the result
+// wherever x has a mean, and fp32 loses by it: K = 8192 in groups of 128,
+// fp32 x of one sign 1e-5 of the result, one channel of 3000 that meets
+// weights of 0 1e-4; as it is 1.3e-7 for both.  fp32 activations are cut into
+// three bf16 numbers that add up to them exactly (8 + 8 + 8 bits), one matrix
+// instruction each.
 
 #include <hip/hip_runtime.h>
 
@@ -41,21 +39,25 @@ __device__ __forceinline__ uint32_t bf16_bits(float v) {
          0xFFFFu;
 }
 
-// 8 codes of a dword -> 16 + code as bf16, in the order 0 4 1 5 2 6 3 7.
-// bias: 0x41804180 in a vector register, so that and-or is one instruction
-// with the mask in a scalar one.
-__device__ __forceinline__ u32x4 unpack(uint32_t w, uint32_t bias) {
-  constexpr uint32_t kMask = 0x00780078u;
-  return u32x4{((w << 3) & kMask) | bias, ((w >> 1) & kMask) | bias, ((w >> 5) & kMask) | bias,
-               ((w >> 9) & kMask) | bias};
-}
-
-// low / high halves of (a, b) as a pair
-__device__ __forceinline__ uint32_t lo2(uint32_t a, uint32_t b) {
-  return __builtin_amdgcn_perm(b, a, 0x05040100u);
-}
+// high halves of (a, b) as a pair
 __device__ __forceinline__ uint32_t hi2(uint32_t a, uint32_t b) {
   return __builtin_amdgcn_perm(b, a, 0x07060302u);
+}
+
+// Codes 2q and 2q + 1 of a dword -> code - z as a pair of bf16 (integers of 8
+// bits and a sign: the upper halves of their fp32 forms)
+__device__ __forceinline__ uint32_t unpack_pair(uint32_t w, int q, float z) {
+  uint32_t e = w & 0x0F0F0F0Fu, o = (w >> 4) & 0x0F0F0F0Fu;
+  // opaque: keeps the byte conversions from being split into shift and convert
+  asm("" : "+v"(e), "+v"(o));
+  const float a = (float)((e >> (8 * q)) & 0xFFu) - z, b = (float)((o >> (8 * q)) & 0xFFu) - z;
+  return hi2(__float_as_uint(a), __float_as_uint(b));
+}
+
+// All 8, in order
+__device__ __forceinline__ u32x4 unpack(uint32_t w, float z) {
+  return u32x4{unpack_pair(w, 0, z), unpack_pair(w, 1, z), unpack_pair(w, 2, z),
+               unpack_pair(w, 3, z)};
 }
 
 // 8 consecutive activations of one row
@@ -63,14 +65,11 @@ template <bool XF32> struct X8;
 template <> struct X8<false> { u32x4 v; };
 template <> struct X8<true> { u32x4 a, b; };
 
-// the bf16 operands of 8 activations (1, or the 3 parts of fp32 values), in
-// the order 0 4 1 5 2 6 3 7
+// the bf16 operands of 8 activations (1, or the 3 parts of fp32 values)
 template <bool XF32> struct Parts { u32x4 p[XF32 ? 3 : 1]; };
 
 __device__ __forceinline__ Parts<false> parts(const X8<false>& x) {
-  Parts<false> r;
-  r.p[0] = u32x4{lo2(x.v.x, x.v.z), hi2(x.v.x, x.v.z), lo2(x.v.y, x.v.w), hi2(x.v.y, x.v.w)};
-  return r;
+  return Parts<false>{{x.v}};
 }
 // the part of v below its top 16 bits (exact)
 __device__ __forceinline__ uint32_t below(uint32_t v) {
@@ -81,7 +80,7 @@ __device__ __forceinline__ Parts<true> parts(const X8<true>& x) {
   u32x4 a = x.a, b = x.b;
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
-    r.p[i] = u32x4{hi2(a.x, b.x), hi2(a.y, b.y), hi2(a.z, b.z), hi2(a.w, b.w)};
+    r.p[i] = u32x4{hi2(a.x, a.y), hi2(a.z, a.w), hi2(b.x, b.y), hi2(b.z, b.w)};
     if (i < 2) {
       a = u32x4{below(a.x), below(a.y), below(a.z), below(a.w)};
       b = u32x4{below(b.x), below(b.y), below(b.z), below(b.w)};
@@ -351,9 +350,6 @@ w4_rows_kernel(W4Args a, int item0, int log_ks, int wide) {
   };
 
   f32x4 acc[MT] = {};
-  const u32x4 ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-  uint32_t bias = 0x41804180u;
-  asm("" : "+v"(bias));
   // Without zero points both regions hold 8 for good: the groups' products
   // then have no branch between them and overlap.  With this, the scale 0 for
   // groups past the row, sums in ordinary registers (the launch bound's 2) and
@@ -397,19 +393,22 @@ w4_rows_kernel(W4Args a, int item0, int log_ks, int wide) {
     if (in == 0 && c + SEG < c1) load_segment(seg + 1);
     const uint8_t* const sc = scl + (seg & 1) * (2 * Ring::SEG_BYTES) + in * (128 / G) * 64;
     const uint8_t* const codes = slot + Ring::XL * 1024;
-    f32x4 d[MT], e[MT];
+    f32x4 d[MT];
+    float z = 0.0f;
     u32x4 wv;
     if (G == 128) wv = *reinterpret_cast<const u32x4*>(codes + lane * 16);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
+      const uint8_t* const sl = sc + (t * 32 / G * 16 + c16) * 4;
       if (t * 32 % G == 0) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i) d[i] = e[i] = f32x4{};
+        for (int i = 0; i < MT; ++i) d[i] = f32x4{};
+        z = (float)*reinterpret_cast<const uint32_t*>(sl + Ring::SEG_BYTES);
       }
       const u32x4 wq = unpack(G == 128 ? wv[t]
                                        : *reinterpret_cast<const uint32_t*>(
                                              codes + (16 * t + c16) * 16 + quad * 4),
-                              bias);
+                              z);
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         const int r = BM < 16 ? c16 % BM : 16 * i + c16;
@@ -424,23 +423,18 @@ w4_rows_kernel(W4Args a, int item0, int log_ks, int wide) {
         }
         const Parts<XF32> p = parts(x);
 #pragma unroll
-        for (int h = (XF32 ? 3 : 1) - 1; h >= 0; --h) {
-          e[i] = mfma(p.p[h], ones, e[i]);
-          d[i] = mfma(p.p[h], wq, d[i]);
-        }
+        for (int h = (XF32 ? 3 : 1) - 1; h >= 0; --h) d[i] = mfma(p.p[h], wq, d[i]);
       }
       if ((t + 1) * 32 % G == 0) {
-        const uint8_t* const sl = sc + (t * 32 / G * 16 + c16) * 4;
         const uint32_t sv = *reinterpret_cast<const uint32_t*>(sl);
         // groups past the end of the row: scale 0
         const bool in_row = G == 128 || c * 128 + t * 32 < K;
         const float sf = in_row ? __uint_as_float(s16 ? sv << 16 : sv) : 0.0f;
-        const float z = 16.0f + (float)*reinterpret_cast<const uint32_t*>(sl + Ring::SEG_BYTES);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            acc[i][r] = __builtin_fmaf(sf, __builtin_fmaf(-z, e[i][r], d[i][r]), acc[i][r]);
+            acc[i][r] = __builtin_fmaf(sf, d[i][r], acc[i][r]);
       }
     }
     wait_lgkm0();             // the slot has been read
@@ -520,16 +514,6 @@ __device__ __forceinline__ void barrier() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-}
-
-// Codes 2q and 2q + 1 of a dword -> code - z as a pair of bf16 (integers of 5
-// bits: the upper halves of their fp32 forms)
-__device__ __forceinline__ uint32_t unpack_pair(uint32_t w, int q, float z) {
-  uint32_t e = w & 0x0F0F0F0Fu, o = (w >> 4) & 0x0F0F0F0Fu;
-  // opaque: keeps the byte conversions from being split into shift and convert
-  asm("" : "+v"(e), "+v"(o));
-  const float a = (float)((e >> (8 * q)) & 0xFFu) - z, b = (float)((o >> (8 * q)) & 0xFFu) - z;
-  return hi2(__float_as_uint(a), __float_as_uint(b));
 }
 
 // Logical workgroup ids: contiguous runs per XCD (hardware ids go round robin
