@@ -162,22 +162,24 @@ def _torch():
     return torch
 
 
-_RAW_STREAM = []
+_CURRENT = []     # torch's functions for the current device and its current stream
 
 
 def _stream(stream):
     """The HIP stream handle of ``stream``, or of the current stream of the
     current device (read without building a Stream object: the per-call
     host cost matters for decode-sized calls)."""
-    torch = _torch()
     if stream is not None:
         return stream.cuda_stream
-    if not _RAW_STREAM:
-        _RAW_STREAM.append(getattr(torch._C, "_cuda_getCurrentRawStream", None))
-    raw = _RAW_STREAM[0]
-    if raw is not None:
-        return raw(torch.cuda.current_device())
-    return torch.cuda.current_stream().cuda_stream
+    if not _CURRENT:
+        torch = _torch()
+        torch.cuda.current_device()          # initialises the device once
+        get = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
+        _CURRENT.append((get, raw))
+    get, raw = _CURRENT[0]
+    return raw(get())
 
 
 class _Workspaces(threading.local):
@@ -846,6 +848,7 @@ def bsmm_quant_w4(w, *, group=128, symmetric=True, scale_dtype="f32", values=Fal
     R, K = w2.shape
     if K % group:
         raise ValueError(f"the last dimension ({K}) must be a multiple of group ({group})")
+    _one_gpu("w", w)
     lead, dev, KG = w.shape[:-1], w.device, K // group
 
     def new(cols, dtype):
@@ -884,6 +887,20 @@ def _float_code(dt, name):
     if code is None:
         raise ValueError(f"{name}: expected bf16 or fp32, got {dt}")
     return code
+
+
+def _one_gpu(names, first, *others):
+    """Check that the tensors given (None: not given) are all on one GPU: a
+    kernel that reads a host address faults."""
+    gpu = first.get_device()
+    if gpu >= 0:
+        for t in others:
+            if t is not None and t.get_device() != gpu:
+                break
+        else:
+            return
+    raise ValueError(f"{names} must be on one GPU, got " + ", ".join(
+        "none" if t is None else str(t.device) for t in (first, *others)))
 
 
 def _w4_weight(w, ws, wst, scale, zero, K, u8):
@@ -959,6 +976,8 @@ def bsmm_w4_mm(x, w, scale, zero=None, *, out_dtype="bf16", out=None, workspace=
     group, sc, sst, zp, zst = _w4_weight(w, ws, wst, scale, zero, K, u8)
     if K and xst[1] != 1:
         raise ValueError(f"x must be row-major, got stride {xst}")
+    _one_gpu("x, w, scale, zero, out and workspace", x, w, scale, zero, out,
+             None if workspace is False else workspace)
     dev = x.device
     o, ldo = _w4_out(out, M, N, code, torch, dtypes, dev)
     hs = _stream(stream)
@@ -1004,6 +1023,8 @@ def bsmm_w4_expert_mm(x, w, scale, zero, order, offsets, *, slots_per_row=1, row
     if row_scale is not None and (row_scale.dtype is not f32 or row_scale.numel() != S or
                                   not row_scale.is_contiguous()):
         raise ValueError(f"row_scale must be contiguous fp32 of {S} elements")
+    _one_gpu("x, w, scale, zero, order, offsets, row_scale, out and workspace", x, w, scale, zero,
+             order, offsets, row_scale, out, None if workspace is False else workspace)
     dev = x.device
     o, ldo = _w4_out(out, S, N, code, torch, dtypes, dev)
     hs = _stream(stream)
@@ -1070,6 +1091,8 @@ def bsmm_route_topk(logits, k, *, mask=None, renorm=True, alpha=None, workspace=
         raise ValueError(f"k must be 1 to 32 and at most E = {E}, got {k}")
     torch, _, _, i32, f32 = _DTYPES["torch"]
     mp = None if mask is None else _route_mask(mask, T)
+    _one_gpu("logits, mask and workspace", logits, mask,
+             None if workspace is False else workspace)
     dev = logits.device
     # few allocations and views: a decode step is bound by the host
     S = T * k
@@ -1131,6 +1154,9 @@ def bsmm_route_topk_backward(logits, index, weight, counts, live, *, dweight=Non
             raise ValueError("live must be one int32 value")
         cp, lp = counts.data_ptr(), live.data_ptr()
     mp = None if mask is None else _route_mask(mask, T)
+    _one_gpu("logits, index, weight, counts, live, dweight, dloss, mask and out", logits, index,
+             weight if dweight is not None else None, counts if dloss is not None else None,
+             live if dloss is not None else None, dweight, dloss, mask, out)
     o, ldd = _w4_out(out, T, E, code, torch, dtypes, logits.device)
     status = load().bsmm_route_topk_backward(
         logits.data_ptr(), ldl, code, mp, index.data_ptr(),
