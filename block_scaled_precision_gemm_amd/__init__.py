@@ -867,17 +867,19 @@ def bsmm_quant_w4(w, *, group=128, symmetric=True, scale_dtype="f32", values=Fal
     return (q, scale, zero, v) if values else (q, scale, zero)
 
 
-_DTYPES = {}      # torch dtype, name or code -> library code, for float tensors (filled once)
+_DTYPES = {}      # torch dtype, name or code -> library code, for float tensors (made once)
 
 
 def _float_codes():
     """The codes of the float dtypes by torch dtype, name and code."""
+    global _DTYPES
     if not _DTYPES:
         torch = _torch()
-        _DTYPES.update({torch.bfloat16: BF16, torch.float32: F32, "bf16": BF16, "f32": F32,
-                        BF16: BF16, F32: F32})
-        _DTYPES["torch"] = (torch, {BF16: torch.bfloat16, F32: torch.float32}, torch.uint8,
-                            torch.int32, torch.float32)
+        # assigned whole: another thread sees all of it or nothing
+        _DTYPES = {torch.bfloat16: BF16, torch.float32: F32, "bf16": BF16, "f32": F32,
+                   BF16: BF16, F32: F32,
+                   "torch": (torch, {BF16: torch.bfloat16, F32: torch.float32}, torch.uint8,
+                             torch.int32, torch.float32)}
     return _DTYPES
 
 
