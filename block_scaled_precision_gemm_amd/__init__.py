@@ -842,7 +842,7 @@ def bsmm_quant_w4(w, *, group=128, symmetric=True, scale_dtype="f32", values=Fal
     """
     w2, code = _quant_input(w, "w")
     sc = _float_code(scale_dtype, "scale_dtype")
-    torch, dtypes, u8, _, _ = _DTYPES["torch"]
+    _, torch, dtypes, u8, _, _ = _DTYPES
     if group not in (32, 64, 128):
         raise ValueError("group must be 32, 64 or 128")
     R, K = w2.shape
@@ -867,25 +867,25 @@ def bsmm_quant_w4(w, *, group=128, symmetric=True, scale_dtype="f32", values=Fal
     return (q, scale, zero, v) if values else (q, scale, zero)
 
 
-_DTYPES = {}      # torch dtype, name or code -> library code, for float tensors (made once)
+_DTYPES = ()      # what _float_types returns (made once)
 
 
-def _float_codes():
-    """The codes of the float dtypes by torch dtype, name and code."""
+def _float_types():
+    """(library code by torch dtype, name and code of the float dtypes, torch,
+    torch dtype by code, uint8, int32, float32)."""
     global _DTYPES
     if not _DTYPES:
         torch = _torch()
         # assigned whole: another thread sees all of it or nothing
-        _DTYPES = {torch.bfloat16: BF16, torch.float32: F32, "bf16": BF16, "f32": F32,
-                   BF16: BF16, F32: F32,
-                   "torch": (torch, {BF16: torch.bfloat16, F32: torch.float32}, torch.uint8,
-                             torch.int32, torch.float32)}
+        _DTYPES = ({torch.bfloat16: BF16, torch.float32: F32, "bf16": BF16, "f32": F32,
+                    BF16: BF16, F32: F32}, torch, {BF16: torch.bfloat16, F32: torch.float32},
+                   torch.uint8, torch.int32, torch.float32)
     return _DTYPES
 
 
 def _float_code(dt, name):
     """F32 or BF16 for a float tensor's dtype."""
-    code = _float_codes().get(dt)
+    code = _float_types()[0].get(dt)
     if code is None:
         raise ValueError(f"{name}: expected bf16 or fp32, got {dt}")
     return code
@@ -971,7 +971,7 @@ def bsmm_w4_mm(x, w, scale, zero=None, *, out_dtype="bf16", out=None, workspace=
         raise ValueError("x and w must be 2-D")
     xc = _float_code(x.dtype, "x")
     code = _float_code(out_dtype, "out_dtype")
-    torch, dtypes, u8, _, _ = _DTYPES["torch"]
+    _, torch, dtypes, u8, _, _ = _DTYPES
     M, K = xs
     N = ws[0]
     xst, wst = x.stride(), w.stride()
@@ -1010,7 +1010,7 @@ def bsmm_w4_expert_mm(x, w, scale, zero, order, offsets, *, slots_per_row=1, row
         raise ValueError("x must be 2-D and w 3-D")
     xc = _float_code(x.dtype, "x")
     code = _float_code(out_dtype, "out_dtype")
-    torch, dtypes, u8, i32, f32 = _DTYPES["torch"]
+    _, torch, dtypes, u8, i32, f32 = _DTYPES
     R, K = xs
     E, N = ws[0], ws[1]
     xst, wst = x.stride(), w.stride()
@@ -1091,7 +1091,7 @@ def bsmm_route_topk(logits, k, *, mask=None, renorm=True, alpha=None, workspace=
     T, E, ldl, code = _route_logits(logits)
     if not 1 <= k <= min(E, 32):
         raise ValueError(f"k must be 1 to 32 and at most E = {E}, got {k}")
-    torch, _, _, i32, f32 = _DTYPES["torch"]
+    _, torch, _, _, i32, f32 = _DTYPES
     mp = None if mask is None else _route_mask(mask, T)
     _one_gpu("logits, mask and workspace", logits, mask,
              None if workspace is False else workspace)
@@ -1135,7 +1135,7 @@ def bsmm_route_topk_backward(logits, index, weight, counts, live, *, dweight=Non
     element or None.  Returns dlogits like logits.
     """
     T, E, ldl, code = _route_logits(logits)
-    torch, dtypes, _, i32, f32 = _DTYPES["torch"]
+    _, torch, dtypes, _, i32, f32 = _DTYPES
     if index.dim() != 2:
         raise ValueError("index must be 2-D [T, k]")
     shape = index.shape

@@ -1,4 +1,5 @@
-"""The binding's dtype table when several threads make it (no GPU needed)."""
+"""The binding's dtype table: when several threads make it, and what it does
+not hold (no GPU needed)."""
 
 import threading
 
@@ -42,9 +43,18 @@ def test_another_thread_during_the_first_use(at, monkeypatch):
                 t.join(30)
             return getattr(torch, name)
 
-    monkeypatch.setattr(bsmm, "_DTYPES", {})
+    monkeypatch.setattr(bsmm, "_DTYPES", type(bsmm._DTYPES)())
     slow = Slow()
     monkeypatch.setattr(bsmm, "_quant_input", lambda x, name: (x, bsmm.F32))
     monkeypatch.setattr(bsmm, "_torch", lambda: slow)
     refusal()
     assert not failed
+
+
+@pytest.mark.parametrize("dt", ["torch", None, (), 7, torch.float16])
+def test_other_names_are_refused(dt):
+    x, w, s = torch.zeros(2, 128), torch.zeros(8, 64, dtype=torch.uint8), torch.zeros(8, 1)
+    with pytest.raises(ValueError, match="expected bf16 or fp32"):
+        bsmm.bsmm_w4_mm(x, w, s, out_dtype=dt)
+    with pytest.raises(ValueError, match="expected bf16 or fp32"):
+        bsmm.bsmm_quant_w4(x, scale_dtype=dt)
