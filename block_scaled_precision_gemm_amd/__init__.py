@@ -861,8 +861,8 @@ def bsmm_quant_w4(w, *, group=128, symmetric=True, scale_dtype="f32", values=Fal
     zero = None if symmetric else new(KG, u8)
     v = new(K, w.dtype) if values else None
     _check(load().bsmm_quant_w4(
-        w2.data_ptr(), w2.stride(0), code, q.data_ptr(), K // 2, scale.data_ptr(), KG,
-        sc, None if symmetric else zero.data_ptr(), KG,
+        w2.data_ptr(), w2.stride(0) if R > 1 else K, code, q.data_ptr(), K // 2,
+        scale.data_ptr(), KG, sc, None if symmetric else zero.data_ptr(), KG,
         v.data_ptr() if values else None, K, group, R, K, _stream(stream)))
     return (q, scale, zero, v) if values else (q, scale, zero)
 
@@ -907,9 +907,10 @@ def _one_gpu(names, first, *others):
 
 def _w4_weight(w, ws, wst, scale, zero, K, u8):
     """Check a 4-bit weight (shape ws, strides wst) against K input features;
-    returns (group, scale dtype code, scale strides, zero pointer, zero
-    strides).  A decode call is bound by the host: one read of each shape and
-    stride."""
+    returns (group, row stride, scale dtype code, scale strides, zero pointer,
+    zero strides), strides as (of the expert, of the row).  The stride of a
+    dimension of one element says nothing: a row's length stands for it.  A
+    decode call is bound by the host: one read of each shape and stride."""
     code = _float_code(scale.dtype, "scale")
     if w.dtype is not u8 or 2 * ws[-1] != K:
         raise ValueError(f"w must be uint8 with {K // 2} bytes a row (K = {K}), got {w.dtype} "
@@ -923,14 +924,17 @@ def _w4_weight(w, ws, wst, scale, zero, K, u8):
     if (K and wst[-1] != 1) or (KG > 1 and sst[-1] != 1):
         raise ValueError("w and scale must be contiguous along their last dimension")
     group = K // KG if K else 32
+    many = ws[-2] > 1
+    ldw = wst[-2] if many else K // 2
+    sstride = (sst[0], sst[-2] if many else KG)
     if zero is None:
-        return group, code, sst, None, (0, 0, 0)
+        return group, ldw, code, sstride, None, (0, 0)
     zst = zero.stride()
     if zero.dtype is not u8 or zero.shape != ss:
         raise ValueError(f"zero must be uint8 {tuple(ss)}, got {zero.dtype} {tuple(zero.shape)}")
     if KG > 1 and zst[-1] != 1:
         raise ValueError("zero must be contiguous along its last dimension")
-    return group, code, sst, zero.data_ptr(), zst
+    return group, ldw, code, sstride, zero.data_ptr(), (zst[0], zst[-2] if many else KG)
 
 
 def _w4_workspace(workspace, xc, E, R, S, N, K, group, dev, stream, handle):
@@ -953,7 +957,7 @@ def _w4_out(out, rows, cols, code, torch, dtypes, dev):
     st = out.stride()
     if cols and st[1] != 1:
         raise ValueError("out must be contiguous along its last dimension")
-    return out, st[0]
+    return out, st[0] if rows > 1 else cols
 
 
 def bsmm_w4_mm(x, w, scale, zero=None, *, out_dtype="bf16", out=None, workspace=None,
@@ -975,7 +979,7 @@ def bsmm_w4_mm(x, w, scale, zero=None, *, out_dtype="bf16", out=None, workspace=
     M, K = xs
     N = ws[0]
     xst, wst = x.stride(), w.stride()
-    group, sc, sst, zp, zst = _w4_weight(w, ws, wst, scale, zero, K, u8)
+    group, ldw, sc, sst, zp, zst = _w4_weight(w, ws, wst, scale, zero, K, u8)
     if K and xst[1] != 1:
         raise ValueError(f"x must be row-major, got stride {xst}")
     _one_gpu("x, w, scale, zero, out and workspace", x, w, scale, zero, out,
@@ -984,9 +988,9 @@ def bsmm_w4_mm(x, w, scale, zero=None, *, out_dtype="bf16", out=None, workspace=
     o, ldo = _w4_out(out, M, N, code, torch, dtypes, dev)
     hs = _stream(stream)
     wsp, wsn = _w4_workspace(workspace, xc, 1, M, M, N, K, group, dev, stream, hs)
-    status = load().bsmm_w4_mm(x.data_ptr(), xst[0], xc, w.data_ptr(), wst[0], scale.data_ptr(),
-                               sst[0], sc, zp, zst[0], group, o.data_ptr(), ldo, code, M, N, K,
-                               wsp, wsn, hs)
+    status = load().bsmm_w4_mm(x.data_ptr(), xst[0] if M > 1 else K, xc, w.data_ptr(), ldw,
+                               scale.data_ptr(), sst[1], sc, zp, zst[1], group, o.data_ptr(), ldo,
+                               code, M, N, K, wsp, wsn, hs)
     if status:
         _check(status)
     return o
@@ -1014,7 +1018,7 @@ def bsmm_w4_expert_mm(x, w, scale, zero, order, offsets, *, slots_per_row=1, row
     R, K = xs
     E, N = ws[0], ws[1]
     xst, wst = x.stride(), w.stride()
-    group, sc, sst, zp, zst = _w4_weight(w, ws, wst, scale, zero, K, u8)
+    group, ldw, sc, sst, zp, zst = _w4_weight(w, ws, wst, scale, zero, K, u8)
     if K and xst[1] != 1:
         raise ValueError(f"x must be row-major, got stride {xst}")
     if order.dtype is not i32 or order.dim() != 1 or not order.is_contiguous():
@@ -1032,8 +1036,8 @@ def bsmm_w4_expert_mm(x, w, scale, zero, order, offsets, *, slots_per_row=1, row
     hs = _stream(stream)
     wsp, wsn = _w4_workspace(workspace, xc, E, R, S, N, K, group, dev, stream, hs)
     status = load().bsmm_w4_expert_mm(
-        x.data_ptr(), xst[0], xc, w.data_ptr(), wst[0], wst[1], scale.data_ptr(), sst[0], sst[1],
-        sc, zp, zst[0], zst[1], group, order.data_ptr(), offsets.data_ptr(), slots_per_row,
+        x.data_ptr(), xst[0] if R > 1 else K, xc, w.data_ptr(), wst[0] if E > 1 else 0, ldw,
+        scale.data_ptr(), sst[0], sst[1], sc, zp, zst[0], zst[1], group, order.data_ptr(), offsets.data_ptr(), slots_per_row,
         None if row_scale is None else row_scale.data_ptr(), o.data_ptr(), ldo, code, E, R, S, N,
         K, wsp, wsn, hs)
     if status:
@@ -1072,7 +1076,7 @@ def _route_logits(logits):
         raise ValueError("logits must be 2-D [T, E]")
     if shape[1] and st[1] != 1:
         raise ValueError(f"logits must be row-major, got stride {st}")
-    return shape[0], shape[1], st[0], code
+    return shape[0], shape[1], st[0] if shape[0] > 1 else shape[1], code
 
 
 def bsmm_route_topk(logits, k, *, mask=None, renorm=True, alpha=None, workspace=None,
