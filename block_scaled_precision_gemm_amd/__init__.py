@@ -1037,7 +1037,8 @@ def bsmm_w4_expert_mm(x, w, scale, zero, order, offsets, *, slots_per_row=1, row
     wsp, wsn = _w4_workspace(workspace, xc, E, R, S, N, K, group, dev, stream, hs)
     status = load().bsmm_w4_expert_mm(
         x.data_ptr(), xst[0] if R > 1 else K, xc, w.data_ptr(), wst[0] if E > 1 else 0, ldw,
-        scale.data_ptr(), sst[0], sst[1], sc, zp, zst[0], zst[1], group, order.data_ptr(), offsets.data_ptr(), slots_per_row,
+        scale.data_ptr(), sst[0], sst[1], sc, zp, zst[0], zst[1], group, order.data_ptr(),
+        offsets.data_ptr(), slots_per_row,
         None if row_scale is None else row_scale.data_ptr(), o.data_ptr(), ldo, code, E, R, S, N,
         K, wsp, wsn, hs)
     if status:

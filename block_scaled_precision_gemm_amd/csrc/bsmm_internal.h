@@ -218,8 +218,8 @@ struct W4Args {
   void* out; int64_t ldo; bsmm_dtype out_dtype;
   int E, R, S, N, K;
 };
-// The kernel for a call: 16 to 32 rows a workgroup (any call), or tiles of 128
-// or 256 rows by 128 columns.  On tiles an fp32 x is cut into three bf16
+// The kernel for a call: 4, 16 or 32 rows a workgroup (any call), or tiles of
+// 128 or 256 rows by 128 columns.  On tiles an fp32 x is cut into three bf16
 // planes in the workspace (w4_plane_bytes), and x is addressed by 32-bit
 // offsets.
 enum class W4Plan { Rows, Tile128, Tile256 };

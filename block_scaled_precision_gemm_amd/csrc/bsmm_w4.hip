@@ -230,11 +230,10 @@ struct RowRing {
   static constexpr int SG = PER > 8 ? 8 : 16;
   static constexpr int SEG_BYTES = SG * 16 * 4;
   static constexpr int SCALES = 4 * SEG_BYTES;
-  static constexpr int FIT = (80 * 1024 / W - SCALES) / SLOT;
-  static constexpr int D = FIT < 4 ? FIT : 4;
+  static constexpr int D = (80 * 1024 / W - SCALES) / SLOT;     // as many as fit
   static constexpr int WAVE = D * SLOT + SCALES;
   static constexpr int BYTES = W * WAVE;
-  static_assert(D >= 2 && (D - 1) * PER < 64, "ring depth");
+  static_assert((D == 2 || D == 3) && (D - 1) * PER < 64, "ring depth");
   // a segment is loaded before the last chunk that precedes its own
   static_assert(SG * 32 / 128 >= D, "segment length");
 };
@@ -384,8 +383,7 @@ w4_rows_kernel(W4Args a, int item0, int log_ks, int wide) {
     // in flight: the newest ones, whatever scales were loaded among them.
     const int newer = c1 - 1 - c;
     if (newer >= D - 1) wait_vmcnt<(D - 1) * Ring::PER>();
-    else if (D > 3 && newer == 2) wait_vmcnt<(D > 3 ? 2 : 0) * Ring::PER>();
-    else if (D > 2 && newer == 1) wait_vmcnt<(D > 2 ? 1 : 0) * Ring::PER>();
+    else if (D == 3 && newer == 1) wait_vmcnt<Ring::PER>();
     else wait_vmcnt<0>();
     // a segment's first chunk fetches the next segment; its own one landed
     // before this chunk did, or with it (the first)
