@@ -24,7 +24,7 @@ __all__ = [
     "bsmm_quant_fp8_columns", "bsmm_quant_fp8_weight", "bsmm_quant_fp8_blockwise_columns",
     "bsmm_quant_w4", "bsmm_w4_mm", "bsmm_w4_expert_mm",
     "bsmm_route_topk", "bsmm_route_topk_backward", "Route",
-    "bsmm_w4_workspace_bytes", "bsmm_route_workspace_bytes",
+    "bsmm_w4_workspace_bytes", "bsmm_w4_plan_name", "bsmm_route_workspace_bytes",
     "bsmm_workspace_bytes", "bsmm_query_plan", "bsmm_set_override", "bsmm_set_override_tail", "bsmm_set_streamk_grid", "bsmm_mfma_probe",
     "bsmm_variant_names", "bsmm_version", "bsmm_timing_enable", "bsmm_timing_read",
     "I32", "F32", "BF16", "E4M3", "OP_INT8_ROWWISE", "OP_FP8_BLOCKWISE", "OP_FP8_MX_BMM",
@@ -110,6 +110,8 @@ def load():
                                     vp]
     L.bsmm_w4_workspace_bytes.argtypes = [st, i64, i64, i64, i64, i64, st]
     L.bsmm_w4_workspace_bytes.restype = sz
+    L.bsmm_w4_plan_name.argtypes = [st, st, i64, i64, i64, i64, i64, st]
+    L.bsmm_w4_plan_name.restype = ctypes.c_char_p
     L.bsmm_route_workspace_bytes.argtypes = [i64, i64]
     L.bsmm_route_workspace_bytes.restype = sz
     L.bsmm_route_topk.argtypes = [vp, i64, st, vp, st, st, ctypes.c_float, vp, vp, vp, vp, vp, vp,
@@ -1182,6 +1184,14 @@ def bsmm_workspace_bytes(op, G, M, N, K, out_dtype):
 def bsmm_w4_workspace_bytes(x_dtype, E, R, S, N, K, group):
     """Workspace bytes bsmm_w4_expert_mm wants (bsmm_w4_mm: E = 1, R = S = M)."""
     return load().bsmm_w4_workspace_bytes(_float_code(x_dtype, "x_dtype"), E, R, S, N, K, group)
+
+
+def bsmm_w4_plan_name(x_dtype, routed, E, R, S, N, K, group):
+    """The kernel of a bsmm_w4_expert_mm (``routed``) or bsmm_w4_mm call: rows4,
+    rows16, rows32, tile128 or tile256; None for sizes that have none."""
+    name = load().bsmm_w4_plan_name(_float_code(x_dtype, "x_dtype"), 1 if routed else 0, E, R, S,
+                                    N, K, group)
+    return name and name.decode()
 
 
 def bsmm_route_workspace_bytes(T, E):

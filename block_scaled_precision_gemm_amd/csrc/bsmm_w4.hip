@@ -923,18 +923,12 @@ void launch_rows(const W4Args& a, hipStream_t st) {
   }
 }
 
-// Rows an item by the rows of the call, routed by an expert's average: those
-// above it take several items, which read the codes again, so that 4 rows are
-// for averages of at most 2 (2048 x 4096, 8 of 32 experts, fp32: 12 tokens 93
-// us with 4 rows, 85 with 16; 8 tokens, average 2, 69 and 83).  8 rows were
-// never better than 16 (8 x 5120 x 8192 bf16 14.7 and 14.9, 32 tokens x 8 of
-// 32 experts 68 and 55).
 template <bool XF32, int G>
 void launch_few(const W4Args& a, hipStream_t st) {
-  const int64_t rows = a.offsets ? (a.S + a.E - 1) / a.E : a.S;
-  if (rows <= (a.offsets ? 2 : 4)) launch_rows<XF32, G, 4>(a, st);
-  else if (rows <= 16 || XF32) launch_rows<XF32, G, 16>(a, st);
-  else launch_rows<XF32, G, XF32 ? 16 : 32>(a, st);
+  const int rows = w4_item_rows(a);
+  if (rows == 4) launch_rows<XF32, G, 4>(a, st);
+  else if (rows == 16) launch_rows<XF32, G, 16>(a, st);
+  else launch_rows<XF32, G, XF32 ? 16 : 32>(a, st);        // fp32 never gets here
 }
 
 template <int G, bool S16>

@@ -183,6 +183,28 @@ size_t bsmm_w4_workspace_bytes(bsmm_dtype x_dtype, int64_t E, int64_t R, int64_t
   return tiled ? w4_plane_bytes(a) : 0;
 }
 
+const char* bsmm_w4_plan_name(bsmm_dtype x_dtype, int routed, int64_t E, int64_t R, int64_t S,
+                              int64_t N, int64_t K, int group) {
+  if (E <= 0 || R <= 0 || S <= 0 || N <= 0 || K <= 0 || E > 1024 || R >= kMaxDim ||
+      S >= kMaxDim || N >= kMaxDim || K >= kMaxDim || !float_dtype(x_dtype) ||
+      (group != 32 && group != 64 && group != 128) || K % group != 0)
+    return nullptr;
+  static const int32_t some = 0;
+  W4Args a{};
+  a.x_dtype = x_dtype;
+  a.group = group;
+  a.E = (int)E; a.R = (int)R; a.S = (int)S; a.N = (int)N; a.K = (int)K;
+  a.ldx = K;
+  a.offsets = routed ? &some : nullptr;
+  switch (w4_plan(a)) {
+    case W4Plan::Tile128: return "tile128";
+    case W4Plan::Tile256: return "tile256";
+    case W4Plan::Rows: break;
+  }
+  const int rows = w4_item_rows(a);
+  return rows == 4 ? "rows4" : rows == 16 ? "rows16" : "rows32";
+}
+
 bsmm_status bsmm_w4_mm(const void* x, int64_t ldx, bsmm_dtype x_dtype, const uint8_t* w,
                        int64_t ldw, const void* scale, int64_t s_n, bsmm_dtype scale_dtype,
                        const uint8_t* zero, int64_t z_n, int group, void* out, int64_t ldo,

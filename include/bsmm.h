@@ -472,6 +472,14 @@ bsmm_status bsmm_quant_w4(const void* w, int64_t ldw, bsmm_dtype w_dtype, uint8_
  */
 size_t bsmm_w4_workspace_bytes(bsmm_dtype x_dtype, int64_t E, int64_t R, int64_t S, int64_t N,
                                int64_t K, int group);
+/*
+ * The kernel that a call takes with the workspace above and ldx = K: "rows4",
+ * "rows16" or "rows32" (workgroups of so many rows) or "tile128" or "tile256"
+ * (tiles of so many rows); NULL for sizes that the calls refuse or do nothing
+ * for.  Results do not differ beyond the order of fp32 sums.
+ */
+const char* bsmm_w4_plan_name(bsmm_dtype x_dtype, int routed, int64_t E, int64_t R, int64_t S,
+                              int64_t N, int64_t K, int group);
 bsmm_status bsmm_w4_mm(const void* x, int64_t ldx, bsmm_dtype x_dtype, const uint8_t* w,
                        int64_t ldw, const void* scale, int64_t s_n, bsmm_dtype scale_dtype,
                        const uint8_t* zero, int64_t z_n, int group, void* out, int64_t ldo,
