@@ -230,9 +230,11 @@ W4Plan w4_plan(const W4Args& a);
 // Rows of a workgroup of W4Plan::Rows, by the rows of the call, routed by an
 // expert's average: rows above that take several workgroups, which read the
 // codes again, so that 4 rows are for averages of at most 2 (2048 x 4096, 8 of
-// 32 experts, fp32: 12 tokens 93 us with 4 rows, 85 with 16; 8 tokens, average
-// 2, 69 and 83).  8 rows were never better than 16 (8 x 5120 x 8192 bf16 14.7
-// and 14.9, 32 tokens x 8 of 32 experts 68 and 55).
+// 32 experts, fp32: 12 tokens 92 us with 4 rows, 80 with 16; 8 tokens, average
+// 2, 67 and 80; bf16 48 and 45, 35 and 45).  Dense, 5 rows of 5120 x 8192 bf16
+// take 19.5 us with 4 and 14.5 with 16, 24 rows 22.8 with 16 and 17.6 with 32.
+// 8 rows were never better than 16 (8 x 5120 x 8192 bf16 14.7 and 14.9, 32
+// tokens x 8 of 32 experts 68 and 55).
 inline int w4_item_rows(const W4Args& a) {
   const int64_t rows = a.offsets ? ((int64_t)a.S + a.E - 1) / a.E : a.S;
   return rows <= (a.offsets ? 2 : 4) ? 4 : rows <= 16 || a.x_dtype == BSMM_F32 ? 16 : 32;

@@ -208,11 +208,12 @@ __device__ __forceinline__ void to_lds(rsrc_t rs, uint32_t voff, uint32_t soff, 
 // reads one dword of each 32-element block, so that one product stays inside
 // one group, and every lane reads the scale of the block's own lanes.
 //
-// One row is bound by the weight's bytes and the start of the waves (1 x 5120
-// x 8192 bf16: 22 MB in 10.4 us, 14.2 from HBM; reading the same bytes in this
-// layout and nothing else takes 6), several rows by the instructions issued
-// (13 x 4099 x 7168 fp32: 24 us; 33 tokens x 4 of 16 experts of 4096 x 1024,
-// fp32: 30 us).
+// One row is bound by the start of the waves and the latency of their loads
+// (1 x 5120 x 8192 bf16: 22 MB in 10.7 us, 11.7 with weights that are in no
+// cache; reading the same bytes in this layout and nothing else takes 6),
+// several rows by the instructions issued (13 x 4099 x 7168 fp32: 23 us, 460
+// instructions a chunk and wave; 33 tokens x 4 of 16 experts of 4096 x 1024,
+// fp32: 30 to 35 us, by the experts' loads).
 // ---------------------------------------------------------------------------
 // Waves that fill the chip: 8 a CU (1024 or 4096 were no faster anywhere).
 constexpr int64_t kRowTarget = 2048;
@@ -267,7 +268,7 @@ w4_rows_kernel(W4Args a, int item0, int log_ks, int wide) {
 
   // Sources: a base that is the wave's plus 32-bit offsets of the lanes, so
   // that a load needs no vector instruction: calls of several rows are bound
-  // by the instructions issued (a wave of 13 fp32 rows spent 62 % of its time
+  // by the instructions issued (a wave of 13 fp32 rows spends 61 % of its time
   // on them).  `wide`: rows so far apart that the offsets do not fit; then,
   // and where a chunk or segment reaches past the end of the row, every lane
   // makes its address.
@@ -350,11 +351,11 @@ w4_rows_kernel(W4Args a, int item0, int log_ks, int wide) {
 
   f32x4 acc[MT] = {};
   // Without zero points both regions hold 8 for good: the groups' products
-  // then have no branch between them and overlap.  With this, the scale 0 for
+  // then have no branch between them and overlap.  This, the scale 0 for
   // groups past the row, sums in ordinary registers (the launch bound's 2) and
-  // addresses without vector instructions, 70 x 5120 x 8192 fp32 takes 87 us
-  // (102 before), 13 x 4099 x 7168 fp32 26.7 (29.4), 64 routed tokens x 8
-  // 75 (80).
+  // addresses without vector instructions took 70 x 5120 x 8192 fp32 from 102
+  // to 87 us, 13 x 4099 x 7168 fp32 from 29.4 to 26.7, 64 routed tokens x 8
+  // from 80 to 75.
   if (!has_zero) {
 #pragma unroll
     for (int i = 0; i < 2 * Ring::SEG_BYTES / 256; ++i)

@@ -79,18 +79,21 @@ bsmm_status run(const W4Args& a, void* workspace, size_t workspace_bytes, void* 
 // beyond 256.
 //
 //   rows x N x K              Rows   Tile128   Tile256   (us)
-//     260 x 5120 x 8192         92       100       126
-//     520 x 5120 x 8192        166        96       126
-//    1040 x 5120 x 8192        307       160       133
-//    1040 x 2048 x 4096         77        54        69
-//    2047 x 4096 x 4096                   86        77
-//     260 x 2048 x 4096 fp32    73       163       209   (groups of 64)
-//     800 x 5120 x 8192 fp32   749       467       430   (groups of 64)
-//    1021 tokens x 8, 32 experts of 2048 x 4096:   541       256       348
-//     256 tokens x 8, the same                     165       136
-//     128 tokens x 8, the same                     108       139
-//     512 tokens x 4, 16 experts of 2048 x 2048:    94        50        98
-//     200 tokens x 4, the same                      34        43
+//     130 x 5120 x 8192         55        93       123
+//     260 x 5120 x 8192         99        99       125
+//     520 x 5120 x 8192        151        95       123
+//    1040 x 5120 x 8192        276       146       128
+//    1040 x 2048 x 4096         72        51        66
+//    2047 x 4096 x 4096        212        87        76
+//    2047 x 5120 x 8192        486       232       258
+//     260 x 2048 x 4096 fp32    72       147       206   (groups of 64)
+//     800 x 5120 x 8192 fp32   608       432       403   (groups of 64)
+//    1021 tokens x 8, 32 experts of 2048 x 4096:   477       233       274
+//     256 tokens x 8, the same                     141       123
+//     128 tokens x 8, the same                      86       118
+//     512 tokens x 4, 16 experts of 2048 x 2048:    74        48        76
+//     300 tokens x 4, the same                      52        45
+//     200 tokens x 4, the same                      46        45
 //
 // Routed calls therefore never take 256 rows: an expert's last tile is half
 // empty on average.

@@ -464,11 +464,14 @@ bsmm_status bsmm_quant_w4(const void* w, int64_t ldw, bsmm_dtype w_dtype, uint8_
  * Any M and N; K a multiple of group (32, 64 or 128).  x, w and their row
  * strides 16-byte aligned (ldx a multiple of 8 elements), out 4-byte aligned.
  * |x| up to 2^100: NaN, infinities and larger values are unsupported.  fp32
- * activations are used in full precision.  M == 0 or N == 0 does nothing, K
+ * activations are used in full precision, and every product is exact: the
+ * error is that of the fp32 sums of the (code - zero) * x.  M == 0 or N == 0 does nothing, K
  * == 0 writes zeros.  The workspace (16-byte aligned) holds fp32 activations
  * cut into bf16 parts where many rows make that worth it:
  * bsmm_w4_workspace_bytes gives the bytes (0: none wanted; E = 1 and S = R =
- * M for bsmm_w4_mm).  With less the call runs without it, slower.
+ * M for bsmm_w4_mm).  With less the call runs without it, slower.  So does a
+ * call whose x (M * ldx elements of bf16, or three bf16 parts of M * K fp32
+ * ones) reaches 4 GiB, at about half the speed: cut it by rows.
  */
 size_t bsmm_w4_workspace_bytes(bsmm_dtype x_dtype, int64_t E, int64_t R, int64_t S, int64_t N,
                                int64_t K, int group);

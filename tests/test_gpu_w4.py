@@ -12,6 +12,8 @@ zero) have a size of about 22 sqrt(G) each, an fp32 addition errs by at most
 4.6 sqrt(G), that is 2**-23 * 3.9 * sqrt(G), 5.3e-6 at G = 128, in the
 Frobenius norm, and 1e-4 of the result's rms leaves an element 19 times that.
 A bf16 output must be the fp32 output of the same call rounded to nearest even.
+(The kernels sum (code - zero) x, which errs less than these two sums: this
+limit is an upper one, test_gpu_w4_accuracy.py has theirs.)
 """
 
 import numpy as np
