@@ -1059,18 +1059,22 @@ __device__ __forceinline__ void static_for(F&& f) {
 // Count one arrival in a tile's counter and return the count it makes.  A
 // counter holds a launch's 40-bit tag above a 24-bit count; a value with
 // another tag (an earlier launch, or whatever the workspace held) counts as
-// zero.  The first exchange guesses that this is the last of n arrivals,
-// so the last one, whose adds follow, needs a single atomic round trip; a
-// wrong guess costs one more, and every failure after it means another
-// arrival's exchange succeeded, so at most n + 1 attempts.
+// zero.  The last arrival leaves zero behind: a launch that a graph replays
+// has the same tag every time.  The first exchange guesses that this is the
+// last of n arrivals, so the last one, whose adds follow, needs a single
+// atomic round trip; a wrong guess costs one more, and every failure after it
+// means another arrival's exchange succeeded, so at most n + 1 attempts.
 __device__ __forceinline__ int count_arrival(uint64_t* ctr, uint64_t tag, int n) {
   uint64_t old = (tag << 24) | (uint64_t)(n - 1);
+  int count;
   uint64_t now;
   do {
     now = (old >> 24) == tag ? old + 1 : ((tag << 24) | 1u);
+    count = (int)(now & 0xFFFFFFu);
+    if (count == n) now = 0;
   } while (!__hip_atomic_compare_exchange_strong(ctr, &old, now, __ATOMIC_RELAXED,
                                                  __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-  return (int)(now & 0xFFFFFFu);
+  return count;
 }
 
 namespace narrow {

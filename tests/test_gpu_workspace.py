@@ -11,6 +11,7 @@ import torch
 
 import block_scaled_precision_gemm_amd as bsmm
 from oracle import route as R, w4
+from synth import fp8_mx_bmm_inputs, int8_rowwise_inputs
 from test_gpu_route import check_forward, logits
 from test_gpu_w4 import dev, integer_case, same
 
@@ -179,3 +180,51 @@ def test_product_without_workspace():
     for ws in (False, torch.empty(16, dtype=torch.uint8, device=DEV)):
         call.run(workspace=ws)
         call.check()
+
+
+def gemm(kind):
+    """(a call whose tiles are split between workgroups, counted in the
+    workspace; the operand to change between calls; other contents for it)"""
+    if kind == "narrow":
+        G, M, N, K = 8, 128, 1024, 4096
+        plan = bsmm.bsmm_query_plan(bsmm.OP_FP8_MX_BMM, G, M, N, K, "bf16")
+        assert plan["variant"].startswith("n128") and plan["split_k"] > 1, plan
+        ps = [fp8_mx_bmm_inputs(G, M, N, K, i) for i in range(3)]
+        x, w, sx, sw = (dev(ps[0][n]) for n in ("x", "w", "x_scale", "w_scale"))
+        return (lambda **kw: bsmm.bsmm_fp8_mx_bmm(x, w, sx, sw, layout=ps[0]["layout"], **kw),
+                x, [dev(p["x"]) for p in ps])
+    M, N, K = 2048, 2304, 512
+    bsmm.bsmm_set_override("t256x256skp", 0)
+    ps = [int8_rowwise_inputs(M, N, K, i) for i in range(3)]
+    a, b = dev(ps[0]["a"]), dev(ps[0]["b_nk"]).t()
+    sa, sb = dev(ps[0]["scale_a"]).reshape(-1, 1), dev(ps[0]["scale_b"]).reshape(1, -1)
+    return (lambda **kw: bsmm.bsmm_int8_rowwise(a, b, sa, sb, **kw), a,
+            [dev(p["a"]) for p in ps])
+
+
+@pytest.mark.parametrize("kind", ["narrow", "stream-K"])
+def test_graph_of_a_split_gemm(kind):
+    """Every replay counts its tiles' parts anew: the counters hold a tag of
+    the launch, which replays share."""
+    try:
+        if kind == "stream-K":
+            bsmm.bsmm_set_streamk_grid(50)
+        call, operand, contents = gemm(kind)
+        want = []
+        for t in contents:
+            operand.copy_(t)
+            want.append(call().clone())
+        out = torch.empty_like(want[0])
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(out=out)
+        for i in (0, 1, 2, 0, 1):
+            operand.copy_(contents[i])
+            out.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want[i]), i
+    finally:
+        bsmm.bsmm_set_override(None, 0)
+        bsmm.bsmm_set_streamk_grid(0)
