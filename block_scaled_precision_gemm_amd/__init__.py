@@ -23,6 +23,8 @@ __all__ = [
     "bsmm_quant_int8_rowwise", "bsmm_quant_fp8_blockwise", "bsmm_quant_fp8_mx",
     "bsmm_quant_fp8_columns", "bsmm_quant_fp8_weight", "bsmm_quant_fp8_blockwise_columns",
     "bsmm_quant_w4", "bsmm_w4_mm", "bsmm_w4_expert_mm",
+    "bsmm_expert_mm", "bsmm_expert_wgrad",
+    "bsmm_quant_int8_mx", "bsmm_swiglu", "bsmm_swiglu_backward",
     "bsmm_route_topk", "bsmm_route_topk_backward", "Route",
     "bsmm_w4_workspace_bytes", "bsmm_w4_plan_name", "bsmm_route_workspace_bytes",
     "bsmm_workspace_bytes", "bsmm_query_plan", "bsmm_set_override", "bsmm_set_override_tail", "bsmm_set_streamk_grid", "bsmm_mfma_probe",
@@ -108,6 +110,14 @@ def load():
     L.bsmm_w4_expert_mm.argtypes = [vp, i64, st, vp, i64, i64, vp, i64, i64, st, vp, i64, i64, st,
                                     vp, vp, st, vp, vp, i64, st, i64, i64, i64, i64, i64, vp, sz,
                                     vp]
+    L.bsmm_expert_mm.argtypes = [vp, i64, vp, i64, i64, i64, st, vp, vp, st, vp, vp, i64, st, i64,
+                                 i64, i64, i64, i64, vp, sz, vp]
+    L.bsmm_expert_wgrad.argtypes = [vp, i64, st, st, vp, i64, st, vp, i64, vp, vp, vp, i64, i64,
+                                    st, i64, i64, i64, i64, i64, i64, vp, sz, vp]
+    L.bsmm_quant_int8_mx.argtypes = [vp, i64, st, vp, i64, vp, i64, vp, i64, i64, i64, vp]
+    L.bsmm_swiglu.argtypes = [vp, i64, st, vp, i64, vp, i64, vp, i64, i64, i64, vp]
+    L.bsmm_swiglu_backward.argtypes = [vp, i64, st, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp,
+                                       i64, i64, vp]
     L.bsmm_w4_workspace_bytes.argtypes = [st, i64, i64, i64, i64, i64, st]
     L.bsmm_w4_workspace_bytes.restype = sz
     L.bsmm_w4_plan_name.argtypes = [st, st, i64, i64, i64, i64, i64, st]
@@ -124,7 +134,9 @@ def load():
               "bsmm_quant_int8_rowwise", "bsmm_quant_fp8_blockwise", "bsmm_quant_fp8_mx",
               "bsmm_quant_fp8_mx32", "bsmm_quant_fp8_columns", "bsmm_quant_fp8_weight",
               "bsmm_quant_fp8_blockwise_columns", "bsmm_quant_w4", "bsmm_w4_mm",
-              "bsmm_w4_expert_mm", "bsmm_route_topk", "bsmm_route_topk_backward"):
+              "bsmm_w4_expert_mm", "bsmm_expert_mm", "bsmm_expert_wgrad", "bsmm_quant_int8_mx",
+              "bsmm_swiglu", "bsmm_swiglu_backward", "bsmm_route_topk",
+              "bsmm_route_topk_backward"):
         getattr(L, f).restype = st
     L.bsmm_workspace_bytes.argtypes = [st, i64, i64, i64, i64, st]
     L.bsmm_workspace_bytes.restype = sz
@@ -1046,6 +1058,249 @@ def bsmm_w4_expert_mm(x, w, scale, zero, order, offsets, *, slots_per_row=1, row
     if status:
         _check(status)
     return o
+
+
+def _stream_of(t, stream):
+    """_stream, where t is on the device that it belongs to."""
+    at = t.get_device()
+    if stream is not None:
+        if stream.device_index != at:
+            raise ValueError(f"tensors on cuda:{at}, but a stream of cuda:{stream.device_index}")
+        return stream.cuda_stream
+    handle = _stream(None)
+    now = _CURRENT[0][0]()
+    if now != at:
+        raise ValueError(f"tensors on cuda:{at}, but the current device is cuda:{now}")
+    return handle
+
+
+def _slots_per_row(n, name):
+    if not 1 <= n < 2**31:
+        raise ValueError(f"{name} must be at least 1 and below 2^31, got {n}")
+
+
+def _routed(order, offsets, E, S, i32):
+    """Check a Route's order (None: slots as they are) and offsets; returns
+    order's address."""
+    if order is not None and (order.dtype is not i32 or order.dim() != 1 or
+                              order.shape[0] != S or not order.is_contiguous()):
+        raise ValueError(f"order must be a contiguous int32 [{S}] tensor")
+    if offsets.dtype is not i32 or offsets.shape != (E + 1,) or not offsets.is_contiguous():
+        raise ValueError(f"offsets must be a contiguous int32 [{E + 1}] tensor")
+    return None if order is None else order.data_ptr()
+
+
+def _row_stride(t, shape, stride, name):
+    """The row stride of a 2-D tensor whose rows are contiguous."""
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if shape[1] > 1 and stride[1] != 1:
+        raise ValueError(f"{name} must be row-major, got stride {stride}")
+    return stride[0] if shape[0] > 1 else shape[1]
+
+
+def bsmm_expert_mm(x, w, order, offsets, *, slots_per_row=1, row_scale=None, out_dtype="bf16",
+                   out=None, stream=None):
+    """Routed rows times their experts' weights.
+
+    x: bf16 or fp32 [R, K].  w: [E, N, K] of x's type, contiguous along its
+    last dimension or its middle one: a weight w [E, N, K] for the product,
+    ``w.transpose(1, 2)`` for the gradient of its input from the rows of dy.
+    order: int32 [S] and offsets: int32 [E + 1] as bsmm_route_topk returns
+    them; order None: the slots are sorted (S = R * slots_per_row).  Slot s
+    reads row s // slots_per_row of x.  row_scale: fp32 [S] or None.  Returns
+    [S, N] in slot order, zeros for slots without an expert.
+    """
+    xs, ws = x.shape, w.shape
+    if len(ws) != 3:
+        raise ValueError("w must be 3-D")
+    xc = _float_code(x.dtype, "x")
+    code = _float_code(out_dtype, "out_dtype")
+    _, torch, dtypes, _, i32, f32 = _DTYPES
+    ldx = _row_stride(x, xs, x.stride(), "x")
+    R, K = xs
+    E, N = ws[0], ws[1]
+    if w.dtype is not x.dtype or ws[2] != K:
+        raise ValueError(f"w must be {x.dtype} with {K} columns, got {w.dtype} {tuple(ws)}")
+    # a dimension of one element has no stride to speak of
+    se, sn, sk = w.stride()
+    if K == 1:
+        sk = 1
+    elif N == 1 and sk != 1:
+        sn = 1
+    if K > 1 and N > 1 and sn != 1 and sk != 1:
+        raise ValueError(f"w must be contiguous along N or K, got stride {w.stride()}")
+    _slots_per_row(slots_per_row, "slots_per_row")
+    S = R * slots_per_row if order is None else order.shape[0]
+    op = _routed(order, offsets, E, S, i32)
+    if row_scale is not None and (row_scale.dtype is not f32 or row_scale.numel() != S or
+                                  not row_scale.is_contiguous()):
+        raise ValueError(f"row_scale must be contiguous fp32 of {S} elements")
+    _one_gpu("x, w, order, offsets, row_scale and out", x, w, order, offsets, row_scale, out)
+    o, ldo = _w4_out(out, S, N, code, torch, dtypes, x.device)
+    status = load().bsmm_expert_mm(
+        x.data_ptr(), ldx, w.data_ptr(), se if E > 1 else 0, sn, sk, xc, op, offsets.data_ptr(),
+        slots_per_row, None if row_scale is None else row_scale.data_ptr(), o.data_ptr(), ldo,
+        code, E, R, S, N, K, None, 0, _stream_of(x, stream))
+    if status:
+        _check(status)
+    return o
+
+
+def bsmm_expert_wgrad(dy, x, order, offsets, *, x_scale=None, dy_slots_per_row=1,
+                      x_slots_per_row=1, out_dtype="f32", out=None, stream=None):
+    """The experts' weight gradients, dw[e] = sum of dy[s]^T x[s] over e's slots.
+
+    dy: bf16 or fp32 [Ry, N].  x: [Rx, K] of dy's type, or with x_scale the
+    int8 codes and bytes of bsmm_quant_int8_mx.  Slot s reads row s //
+    dy_slots_per_row of dy and s // x_slots_per_row of x.  order: int32 [S] and
+    offsets: int32 [E + 1] as bsmm_route_topk returns them; order None: the
+    slots are sorted (S = Ry * dy_slots_per_row), and with offsets [0, S] this
+    is a dense layer's gradient.  Returns [E, N, K], zeros for experts without
+    slots.
+    """
+    yc = _float_code(dy.dtype, "dy")
+    code = _float_code(out_dtype, "out_dtype")
+    _, torch, dtypes, u8, i32, _ = _DTYPES
+    ys, xs = dy.shape, x.shape
+    ldy, ldx = _row_stride(dy, ys, dy.stride(), "dy"), _row_stride(x, xs, x.stride(), "x")
+    Ry, N = ys
+    Rx, K = xs
+    sp, s_r = None, 0
+    if x_scale is None:
+        if x.dtype is not dy.dtype:
+            raise ValueError(f"x must be {dy.dtype}, or int8 codes with x_scale; got {x.dtype}")
+    else:
+        if x.dtype is not torch.int8 or K % 32:
+            raise ValueError(f"a checkpoint is int8 with K % 32 == 0, got {x.dtype} {tuple(xs)}")
+        ss = x_scale.shape
+        if x_scale.dtype is not u8 or ss != (Rx, K // 32):
+            raise ValueError(f"x_scale must be uint8 [{Rx}, {K // 32}], got {x_scale.dtype} "
+                             f"{tuple(ss)}")
+        s_r = _row_stride(x_scale, ss, x_scale.stride(), "x_scale")
+        sp = x_scale.data_ptr()
+    _slots_per_row(dy_slots_per_row, "dy_slots_per_row")
+    _slots_per_row(x_slots_per_row, "x_slots_per_row")
+    S = Ry * dy_slots_per_row if order is None else order.shape[0]
+    E = offsets.shape[0] - 1 if offsets.dim() == 1 else -1
+    if E < 0:
+        raise ValueError("offsets must be 1-D [E + 1]")
+    op = _routed(order, offsets, E, S, i32)
+    _one_gpu("dy, x, x_scale, order, offsets and out", dy, x, x_scale, order, offsets, out)
+    if out is None:
+        o, se, ldw = torch.empty((E, N, K), dtype=dtypes[code], device=dy.device), N * K, K
+    else:
+        if tuple(out.shape) != (E, N, K) or out.dtype is not dtypes[code]:
+            raise ValueError(f"out must be {(E, N, K)} {dtypes[code]}, got {tuple(out.shape)} "
+                             f"{out.dtype}")
+        o, (se, ldw, sk) = out, out.stride()
+        if K > 1 and sk != 1:
+            raise ValueError("out must be contiguous along its last dimension")
+        ldw = ldw if N > 1 else K
+    status = load().bsmm_expert_wgrad(
+        dy.data_ptr(), ldy, yc, dy_slots_per_row, x.data_ptr(), ldx, x_slots_per_row, sp, s_r, op,
+        offsets.data_ptr(), o.data_ptr(), se if E > 1 else 0, ldw, code, E, Ry, Rx, S, N, K, None,
+        0, _stream_of(dy, stream))
+    if status:
+        _check(status)
+    return o
+
+
+def bsmm_quant_int8_mx(x, *, values=False, stream=None):
+    """An 8-bit checkpoint of activations x [..., K] (bf16 or fp32; K a
+    multiple of 32): int8 codes and a power of two per 32 elements of a row.
+
+    Returns (q int8 [..., K], scale uint8 e8m0 bytes [..., K/32]), which stand
+    for q * 2^(scale - 133): the x of bsmm_expert_wgrad.  ``values=True``
+    appends these values as a tensor like x.
+    """
+    x2, code = _quant_input(x)
+    _, torch, _, u8, _, _ = _DTYPES or _float_types()
+    R, K = x2.shape
+    if K % 32:
+        raise ValueError(f"the last dimension ({K}) must be a multiple of 32")
+    _one_gpu("x", x)
+    lead, dev = tuple(x.shape[:-1]), x.device
+    q = torch.empty(lead + (K,), dtype=torch.int8, device=dev)
+    scale = torch.empty(lead + (K // 32,), dtype=u8, device=dev)
+    v = torch.empty(lead + (K,), dtype=x.dtype, device=dev) if values else None
+    _check(load().bsmm_quant_int8_mx(
+        x2.data_ptr(), x2.stride(0) if R > 1 else K, code, q.data_ptr(), K, scale.data_ptr(),
+        K // 32, v.data_ptr() if values else None, K, R, K, _stream_of(x, stream)))
+    return (q, scale, v) if values else (q, scale)
+
+
+def bsmm_swiglu(h, *, checkpoint=False, out=None, stream=None):
+    """The gate of a feed-forward layer: silu(h[:, :F]) * h[:, F:].
+
+    h: bf16 or fp32 [R, 2F], F a multiple of 32.  Returns [R, F] of h's type;
+    with ``checkpoint`` (that, q int8 [R, 2F], scale uint8 [R, 2F/32]), the
+    8-bit checkpoint of h for bsmm_swiglu_backward (as bsmm_quant_int8_mx
+    makes it, from the same read).
+    """
+    code = _float_code(h.dtype, "h")
+    _, torch, dtypes, u8, _, _ = _DTYPES
+    hs = h.shape
+    ldh = _row_stride(h, hs, h.stride(), "h")
+    R, F = hs[0], hs[1] // 2
+    if hs[1] % 64:
+        raise ValueError(f"h must have 2F columns, F a multiple of 32, got {hs[1]}")
+    _one_gpu("h and out", h, out)
+    dev = h.device
+    a, lda = _w4_out(out, R, F, code, torch, dtypes, dev)
+    q = scale = None
+    if checkpoint:
+        q = torch.empty_strided((R, 2 * F), (2 * F, 1), dtype=torch.int8, device=dev)
+        scale = torch.empty_strided((R, F // 16), (F // 16, 1), dtype=u8, device=dev)
+    status = load().bsmm_swiglu(
+        h.data_ptr(), ldh, code, a.data_ptr(), lda, q.data_ptr() if checkpoint else None, 2 * F,
+        scale.data_ptr() if checkpoint else None, F // 16, R, F, _stream_of(h, stream))
+    if status:
+        _check(status)
+    return (a, q, scale) if checkpoint else a
+
+
+def bsmm_swiglu_backward(da, q, scale, *, row_scale=None, act=True, stream=None):
+    """The gradient of row_scale * bsmm_swiglu(h) from the checkpoint of h.
+
+    da: bf16 or fp32 [R, F].  q int8 [R, 2F] and scale uint8 [R, 2F/32] as
+    bsmm_swiglu returns them.  row_scale: fp32 [R] (the routing weights, where
+    they belong to the rows of the gate's output) or None.  Returns (dh
+    [R, 2F], act [R, F] = row_scale * the gate's output, both of da's type,
+    drow fp32 [R], row_scale's gradient); act and drow are None where ``act``
+    is false or row_scale is not given.
+    """
+    code = _float_code(da.dtype, "da")
+    _, torch, _, u8, _, f32 = _DTYPES
+    ds = da.shape
+    ldda = _row_stride(da, ds, da.stride(), "da")
+    R, F = ds
+    if F % 32:
+        raise ValueError(f"the columns of da ({F}) must be a multiple of 32")
+    if q.dtype is not torch.int8 or q.shape != (R, 2 * F):
+        raise ValueError(f"q must be int8 [{R}, {2 * F}], got {q.dtype} {tuple(q.shape)}")
+    if scale.dtype is not u8 or scale.shape != (R, F // 16):
+        raise ValueError(f"scale must be uint8 [{R}, {F // 16}], got {scale.dtype} "
+                         f"{tuple(scale.shape)}")
+    ldq = _row_stride(q, q.shape, q.stride(), "q")
+    s_r = _row_stride(scale, scale.shape, scale.stride(), "scale")
+    if row_scale is not None and (row_scale.dtype is not f32 or row_scale.numel() != R or
+                                  not row_scale.is_contiguous()):
+        raise ValueError(f"row_scale must be contiguous fp32 of {R} elements")
+    _one_gpu("da, q, scale and row_scale", da, q, scale, row_scale)
+    dev = da.device
+    new = torch.empty_strided
+    dh = new((R, 2 * F), (2 * F, 1), dtype=da.dtype, device=dev)
+    a = new((R, F), (F, 1), dtype=da.dtype, device=dev) if act else None
+    drow = None if row_scale is None else new((R,), (1,), dtype=f32, device=dev)
+    status = load().bsmm_swiglu_backward(
+        da.data_ptr(), ldda, code, q.data_ptr(), ldq, scale.data_ptr(), s_r,
+        None if row_scale is None else row_scale.data_ptr(), dh.data_ptr(), 2 * F,
+        a.data_ptr() if act else None, F, None if drow is None else drow.data_ptr(), R, F,
+        _stream_of(da, stream))
+    if status:
+        _check(status)
+    return dh, a, drow
 
 
 class Route(NamedTuple):

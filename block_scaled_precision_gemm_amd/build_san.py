@@ -31,7 +31,7 @@ def device_objects():
     probe, scratch); empty if it has not run."""
     objs = sorted(glob.glob(os.path.join(OBJDIR, "bsmm_kernels_*.o")))
     for name in ("bsmm_pack.o", "bsmm_quant.o", "bsmm_probe.o", "bsmm_scratch.o",
-                 "bsmm_w4.o", "bsmm_route.o"):
+                 "bsmm_w4.o", "bsmm_route.o", "bsmm_expert.o", "bsmm_ckpt.o"):
         objs.append(os.path.join(OBJDIR, name))
     return [o for o in objs if os.path.exists(o)]
 

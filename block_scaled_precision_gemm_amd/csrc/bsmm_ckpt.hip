@@ -1,0 +1,241 @@
+// 8-bit checkpoints of activations, and the gate silu(g) * u of a feed-forward
+// layer with its gradient from one (gfx950).
+//
+// A checkpoint holds int8 codes and, per 32 elements of a row, a power of two
+// as an e8m0 byte (the OCP microscaling format MXINT8): with amax = m 2^p, m
+// in [1, 2),
+//   byte = p + 127 (0 below 2^-127, 127 for amax 0),  code = rne(x 2^(6-p))
+//   within +-127,  value = code 2^(byte - 133)
+// A block that holds an infinity or a NaN gets byte 255, codes 0, and stands
+// for NaNs.  Integers and not e4m3: an activation kept for the backward pass
+// wants precision near its block's maximum, not range (largest error 2^-7 of
+// amax where e4m3 has 2^-4 of the element), and a value has at most 7 bits, so
+// that it is exact in bf16 and the products that read it need no rounding.
+//
+// All kernels read and write each byte once: bound by HBM.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "bsmm.h"
+#include "bsmm_internal.h"
+#include "bsmm_routed.h"
+
+namespace bsmm {
+namespace {
+
+// ---- 8 consecutive elements of a row, as fp32 --------------------------------
+
+__device__ __forceinline__ void load8(const uint16_t* p, float (&f)[8]) {
+  const u32x4 v = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(v[i] << 16);
+    f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
+  const f32x4 a = reinterpret_cast<const f32x4*>(p)[0], b = reinterpret_cast<const f32x4*>(p)[1];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[i] = a[i];
+    f[4 + i] = b[i];
+  }
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float (&f)[8]) {
+  u32x4 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{f[2 * i], f[2 * i + 1]}),
+                                                                bf16x2_t));
+  *reinterpret_cast<u32x4*>(p) = v;
+}
+__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
+  reinterpret_cast<f32x4*>(p)[0] = f32x4{f[0], f[1], f[2], f[3]};
+  reinterpret_cast<f32x4*>(p)[1] = f32x4{f[4], f[5], f[6], f[7]};
+}
+
+// ---- codes ---------------------------------------------------------------------
+
+// The byte of the 32 elements that a quad of lanes holds, 8 each.
+__device__ __forceinline__ int block_byte(const float (&f)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0xB1, 0xF, 0xF, false));
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x4E, 0xF, 0xF, false));
+  // the exponent field is p + 127, 0 for subnormals and 255 for inf and NaN
+  return m == 0 ? 127 : (int)(m >> 23);
+}
+
+// Codes (as integers in f) and their packed form.
+__device__ __forceinline__ uint2 encode(float (&f)[8], int byte) {
+  uint32_t c[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float t = __builtin_rintf(__builtin_ldexpf(f[i], 133 - byte));
+    f[i] = byte == 255 ? 0.0f : __builtin_amdgcn_fmed3f(t, -127.0f, 127.0f);
+    c[i] = (uint32_t)(int)f[i];
+  }
+  auto four = [](uint32_t p, uint32_t q, uint32_t r, uint32_t s) {
+    const uint32_t lo = __builtin_amdgcn_perm(q, p, 0x0C0C0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(s, r, 0x0C0C0400u);
+    return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+  };
+  return make_uint2(four(c[0], c[1], c[2], c[3]), four(c[4], c[5], c[6], c[7]));
+}
+
+// What 8 codes stand for.
+__device__ __forceinline__ void decode(uint2 c, int byte, float (&f)[8]) {
+  const float s = byte == 255 ? __builtin_nanf("") : __builtin_ldexpf(1.0f, byte - 133);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    f[i] = (float)(int8_t)(((i < 4 ? c.x : c.y) >> (8 * (i & 3))) & 0xFFu) * s;
+}
+
+// The codes of the lane's 8 elements, and their byte by a quad's first lane.
+__device__ __forceinline__ void save8(float (&f)[8], int8_t* q, uint8_t* scale, int k, int byte) {
+  const uint2 c = encode(f, byte);
+  *reinterpret_cast<uint2*>(q + k) = c;
+  if ((k & 31) == 0) scale[k >> 5] = (uint8_t)byte;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) quant_int8_mx(QuantI8MxArgs a, unsigned chunks) {
+  const unsigned per_row = (unsigned)a.K / 8;
+  for (unsigned i = blockIdx.x * 256 + threadIdx.x; i < chunks; i += gridDim.x * 256) {
+    const int64_t row = i / per_row;
+    const int k = (int)(i - (unsigned)row * per_row) * 8;
+    float f[8];
+    load8(static_cast<const T*>(a.x) + row * a.ldx + k, f);
+    const int byte = block_byte(f);
+    save8(f, a.q + row * a.ldq, a.scale + row * a.s_r, k, byte);
+    if (a.values) {
+      const float s = byte == 255 ? __builtin_nanf("") : __builtin_ldexpf(1.0f, byte - 133);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] *= s;
+      store8(static_cast<T*>(a.values) + row * a.ldv + k, f);
+    }
+  }
+}
+
+// ---- gate ----------------------------------------------------------------------
+
+// e^-g = 2^t with t = -g log2(e): the product's rounding and the constant's,
+// which would cost |g| 2^-24 of the result, are added back.
+__device__ __forceinline__ float exp_minus(float g) {
+  const float c = -1.44269502162933349609375f, c2 = -1.925963033500011079e-8f;
+  const float t = g * c;
+  // beyond these 2^t is 0 or infinite whatever the rest says
+  const float rest = __builtin_fabsf(t) < 256.0f ? __builtin_fmaf(g, c2, __builtin_fmaf(g, c, -t))
+                                                 : 0.0f;
+  return __builtin_amdgcn_exp2f(t) * __builtin_fmaf(rest, 0.693147180559945309f, 1.0f);
+}
+
+template <typename T, bool CKPT>
+__global__ void __launch_bounds__(256) swiglu(SwigluArgs a, unsigned chunks) {
+  const unsigned per_row = (unsigned)a.F / 8;
+  for (unsigned i = blockIdx.x * 256 + threadIdx.x; i < chunks; i += gridDim.x * 256) {
+    const int64_t row = i / per_row;
+    const int k = (int)(i - (unsigned)row * per_row) * 8;
+    const T* h = static_cast<const T*>(a.h) + row * a.ldh + k;
+    float g[8], u[8], v[8];
+    load8(h, g);
+    load8(h + a.F, u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = g[j] * __builtin_amdgcn_rcpf(1.0f + exp_minus(g[j])) * u[j];
+    store8(static_cast<T*>(a.a) + row * a.lda + k, v);
+    if constexpr (CKPT) {
+      int8_t* q = a.q + row * a.ldq;
+      uint8_t* s = a.scale + row * a.s_r;
+      save8(g, q, s, k, block_byte(g));
+      save8(u, q + a.F, s + a.F / 32, k, block_byte(u));
+    }
+  }
+}
+
+// A wave to a row, so that the row's sum needs no other wave.
+template <typename T>
+__global__ void __launch_bounds__(256) swiglu_backward(SwigluBackArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= a.R) return;
+  const T* da = static_cast<const T*>(a.da) + row * a.ldda;
+  const int8_t* q = a.q + row * a.ldq;
+  const uint8_t* s = a.scale + row * a.s_r;
+  T* dh = static_cast<T*>(a.dh) + row * a.lddh;
+  const float r = a.row_scale ? a.row_scale[row] : 1.0f;
+  float sum = 0.0f;
+  for (int k = lane * 8; k < a.F; k += 512) {
+    float d[8], g[8], u[8];
+    load8(da + k, d);
+    decode(*reinterpret_cast<const uint2*>(q + k), s[k >> 5], g);
+    decode(*reinterpret_cast<const uint2*>(q + a.F + k), s[(a.F + k) >> 5], u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      // finite, so that 1 - sg = e sg is a number where sg is 0; a NaN stays
+      // one through the products with g
+      const float e = __builtin_fminf(exp_minus(g[j]), 0x1p126f);
+      const float sg = __builtin_amdgcn_rcpf(1.0f + e);
+      const float silu = g[j] * sg, act = silu * u[j];
+      sum = __builtin_fmaf(d[j], act, sum);
+      const float rd = r * d[j];
+      // silu' = sg (1 + g (1 - sg))
+      const float slope = __builtin_fmaf(silu, e * sg, sg);
+      g[j] = rd * u[j] * slope;
+      u[j] = rd * silu;
+      d[j] = r * act;
+    }
+    store8(dh + k, g);
+    store8(dh + a.F + k, u);
+    if (a.act) store8(static_cast<T*>(a.act) + row * a.ldact + k, d);
+  }
+  if (a.drow) {
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) sum += __shfl_xor(sum, m);
+    if (lane == 0) a.drow[row] = sum;
+  }
+}
+
+unsigned blocks_for(int64_t chunks) {
+  const int64_t b = (chunks + 255) / 256;
+  return (unsigned)(b < 65536 ? b : 65536);
+}
+
+}  // namespace
+
+int launch_quant_int8_mx(const QuantI8MxArgs& a, void* stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const int64_t chunks = a.R * (a.K / 8);
+  const dim3 grid(blocks_for(chunks)), block(256);
+  if (a.x_dtype == BSMM_BF16)
+    hipLaunchKernelGGL(quant_int8_mx<uint16_t>, grid, block, 0, st, a, (unsigned)chunks);
+  else
+    hipLaunchKernelGGL(quant_int8_mx<float>, grid, block, 0, st, a, (unsigned)chunks);
+  return hipGetLastError() == hipSuccess ? 0 : 1;
+}
+
+int launch_swiglu(const SwigluArgs& a, void* stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const int64_t chunks = a.R * (a.F / 8);
+  const dim3 grid(blocks_for(chunks)), block(256);
+  const unsigned n = (unsigned)chunks;
+  if (a.dtype == BSMM_BF16) {
+    if (a.q) hipLaunchKernelGGL((swiglu<uint16_t, true>), grid, block, 0, st, a, n);
+    else hipLaunchKernelGGL((swiglu<uint16_t, false>), grid, block, 0, st, a, n);
+  } else {
+    if (a.q) hipLaunchKernelGGL((swiglu<float, true>), grid, block, 0, st, a, n);
+    else hipLaunchKernelGGL((swiglu<float, false>), grid, block, 0, st, a, n);
+  }
+  return hipGetLastError() == hipSuccess ? 0 : 1;
+}
+
+int launch_swiglu_backward(const SwigluBackArgs& a, void* stream) {
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const dim3 grid((unsigned)((a.R + 3) / 4)), block(256);
+  if (a.dtype == BSMM_BF16) hipLaunchKernelGGL(swiglu_backward<uint16_t>, grid, block, 0, st, a);
+  else hipLaunchKernelGGL(swiglu_backward<float>, grid, block, 0, st, a);
+  return hipGetLastError() == hipSuccess ? 0 : 1;
+}
+
+}  // namespace bsmm

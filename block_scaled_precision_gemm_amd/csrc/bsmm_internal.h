@@ -242,6 +242,73 @@ inline int w4_item_rows(const W4Args& a) {
 // ws: w4_plane_bytes bytes for an fp32 x on tiles, else not used
 int launch_w4(const W4Args& a, W4Plan plan, void* ws, void* stream);
 
+// A product of routed rows with their experts' bf16 or fp32 weights
+// (bsmm_expert.hip).  Slots, order, offsets and row_scale as in W4Args (order
+// null: slot p at position p).  Element (n, k) of expert e's weight is at e *
+// w_se + n * ldw + k, or with w_across at e * w_se + k * ldw + n.
+struct ExpertArgs {
+  const void* x; int64_t ldx; bsmm_dtype dtype;      // of x and w
+  const void* w; int64_t w_se, ldw; int w_across;
+  const int32_t* order;
+  const int32_t* offsets;
+  const float* row_scale;
+  int x_div;
+  void* out; int64_t ldo; bsmm_dtype out_dtype;
+  int E, R, S, N, K;
+};
+int launch_expert_mm(const ExpertArgs& a, void* stream);
+
+// The weights' gradient: dw[e] (row stride ldw) sums dy[s / y_div]^T x[s /
+// x_div] over the slots of e; slots outside [0, S) add nothing.  x_scale null:
+// x of dy's type; else x is int8 codes with e8m0 bytes x_scale[row * s_r + k /
+// 32].
+struct WgradArgs {
+  const void* dy; int64_t ldy; bsmm_dtype dtype; int y_div;
+  const void* x; int64_t ldx; int x_div;
+  const uint8_t* x_scale; int64_t s_r;
+  const int32_t* order;
+  const int32_t* offsets;
+  void* dw; int64_t w_se, ldw; bsmm_dtype out_dtype;
+  int E, S, N, K;
+};
+int launch_expert_wgrad(const WgradArgs& a, void* stream);
+
+// 8-bit checkpoints (bsmm_ckpt.hip): int8 codes q [R, K] and a byte per 32
+// elements of a row, scale[r * s_r + k / 32]; code * 2^(byte - 133).
+struct QuantI8MxArgs {
+  const void* x; int64_t ldx; bsmm_dtype x_dtype;
+  int8_t* q; int64_t ldq;
+  uint8_t* scale; int64_t s_r;
+  void* values; int64_t ldv;             // null, or what the codes stand for, x's type
+  int64_t R, K;
+};
+int launch_quant_int8_mx(const QuantI8MxArgs& a, void* stream);
+
+// a[r, f] = silu(h[r, f]) * h[r, F + f]; with q the codes of h's rows too.
+struct SwigluArgs {
+  const void* h; int64_t ldh; bsmm_dtype dtype;      // of h and a
+  void* a; int64_t lda;
+  int8_t* q; int64_t ldq;                // null: no checkpoint
+  uint8_t* scale; int64_t s_r;
+  int64_t R, F;
+};
+int launch_swiglu(const SwigluArgs& a, void* stream);
+
+// Its gradient from the codes of h, for da of row_scale * a (null: 1): dh [R,
+// 2F], act = row_scale * a (null: not wanted), drow = sum of da * a (null
+// without row_scale).
+struct SwigluBackArgs {
+  const void* da; int64_t ldda; bsmm_dtype dtype;    // of da, dh and act
+  const int8_t* q; int64_t ldq;
+  const uint8_t* scale; int64_t s_r;
+  const float* row_scale;
+  void* dh; int64_t lddh;
+  void* act; int64_t ldact;
+  float* drow;
+  int64_t R, F;
+};
+int launch_swiglu_backward(const SwigluBackArgs& a, void* stream);
+
 // The expert router (bsmm_route.hip).  logits [T, E], row stride ldl; index,
 // weight [T, k] and order [T * k] contiguous; counts [E], offsets [E + 1].
 // loss, live and prob_sum are null together.  Tokens go to workgroups in

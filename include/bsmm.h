@@ -514,6 +514,99 @@ bsmm_status bsmm_w4_expert_mm(const void* x, int64_t ldx, bsmm_dtype x_dtype, co
                               size_t workspace_bytes, void* stream);
 
 /*
+ * Routed rows times their experts' weights in bf16 or fp32 (`dtype`, of x and
+ * w):
+ *   out(s, n) = row_scale[s] * sum_k x(s / slots_per_row, k) * w(e, n, k)
+ *     for every s = order[i], offsets[e] <= i < offsets[e + 1]
+ *   out(s, :) = 0 for s = order[i], i >= offsets[E]
+ *   x    (r, k) at x[r*ldx + k], R rows
+ *   w    (e, n, k) at w[e*w_se + n*w_sn + k*w_sk], one of w_sn and w_sk 1 and
+ *        the other at least the row: a weight [E, N, K] for the product, the
+ *        same weight with N and K exchanged for the gradient of its input
+ *   out  (s, n) at out[s*ldo + n], fp32 or bf16 (RNE)
+ * order, offsets, slots_per_row and row_scale as for bsmm_w4_expert_mm; order
+ * NULL: slot i at position i.  fp32 sums of unrounded products in a fixed
+ * order.  Any N and K; pointers aligned to their types (16-byte aligned rows
+ * are faster).  E <= 1024.  S == 0 or N == 0 does nothing, K == 0 writes
+ * zeros.  The workspace is not used yet and may be NULL.
+ */
+bsmm_status bsmm_expert_mm(const void* x, int64_t ldx, const void* w, int64_t w_se, int64_t w_sn,
+                           int64_t w_sk, bsmm_dtype dtype, const int32_t* order,
+                           const int32_t* offsets, int slots_per_row, const float* row_scale,
+                           void* out, int64_t ldo, bsmm_dtype out_dtype, int64_t E, int64_t R,
+                           int64_t S, int64_t N, int64_t K, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * The weights' gradient of that product:
+ *   dw(e, n, k) = sum over s = order[i], offsets[e] <= i < offsets[e + 1], of
+ *                 dy(s / dy_slots_per_row, n) * x(s / x_slots_per_row, k)
+ *   dy   (r, n) at dy[r*ldy + n], Ry rows, fp32 or bf16 (`dtype`)
+ *   x    (r, k) at x[r*ldx + k], Rx rows: of dy's type, or with x_scale the
+ *        int8 codes of bsmm_quant_int8_mx, (r, k)'s byte at x_scale[r*s_r +
+ *        k/32] (K % 32 == 0)
+ *   dw   (e, n, k) at dw[e*w_se + n*ldw + k], fp32 or bf16 (RNE)
+ * An expert without slots gets zeros.  order NULL: slot i at position i (E =
+ * 1 and offsets {0, S}: a dense layer's gradient).  S <= Ry *
+ * dy_slots_per_row and S <= Rx * x_slots_per_row.  Sums, sizes, alignment and
+ * workspace as for bsmm_expert_mm (a checkpoint: rows of codes at multiples
+ * of 8 bytes are faster).  E, N or K 0 does nothing; S == 0 writes zeros.
+ */
+bsmm_status bsmm_expert_wgrad(const void* dy, int64_t ldy, bsmm_dtype dtype, int dy_slots_per_row,
+                              const void* x, int64_t ldx, int x_slots_per_row,
+                              const uint8_t* x_scale, int64_t s_r, const int32_t* order,
+                              const int32_t* offsets, void* dw, int64_t w_se, int64_t ldw,
+                              bsmm_dtype out_dtype, int64_t E, int64_t Ry, int64_t Rx, int64_t S,
+                              int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/*
+ * An 8-bit checkpoint of activations x [R, K] (bf16 or fp32): int8 codes with
+ * an e8m0 byte per 32 elements of a row, the OCP microscaling format MXINT8.
+ * With amax = m * 2^p the block's largest magnitude, m in [1, 2):
+ *   scale(r, c) = max(p + 127, 0), 127 for amax 0
+ *   q(r, k)     = rne(x * 2^(6-p)) within +-127
+ *   value       = q * 2^(scale - 133): at most 7 bits, exact in bf16 and fp32
+ * A block with an infinity or a NaN gets byte 255 and codes 0 and stands for
+ * NaNs.  values (NULL or [R, K] of x's type, row stride ldv): the values.
+ *   Requirements: K % 32 == 0, R * K / 32 < 2^29; x and values 16-byte
+ *   aligned, ldx and ldv multiples of 8 elements; q 8-byte aligned, ldq a
+ *   multiple of 8; s_r at least K / 32.  R == 0 or K == 0 does nothing.
+ */
+bsmm_status bsmm_quant_int8_mx(const void* x, int64_t ldx, bsmm_dtype x_dtype, int8_t* q,
+                               int64_t ldq, uint8_t* scale, int64_t s_r, void* values,
+                               int64_t ldv, int64_t R, int64_t K, void* stream);
+
+/*
+ * The gate of a feed-forward layer on h [R, 2F] (bf16 or fp32):
+ *   a(r, f) = silu(h(r, f)) * h(r, F + f),  silu(g) = g / (1 + e^-g)
+ * a [R, F] of h's type, computed in fp32.  With q and scale (both or neither)
+ * also the checkpoint of h, [R, 2F], as bsmm_quant_int8_mx writes it, from the
+ * same read.  F % 32 == 0; rows as for bsmm_quant_int8_mx.
+ */
+bsmm_status bsmm_swiglu(const void* h, int64_t ldh, bsmm_dtype dtype, void* a, int64_t lda,
+                        int8_t* q, int64_t ldq, uint8_t* scale, int64_t s_r, int64_t R, int64_t F,
+                        void* stream);
+
+/*
+ * Its gradient from the checkpoint of h: with g, u the two halves' values and
+ * s = 1 / (1 + e^-g), for da [R, F] (bf16 or fp32), the gradient of
+ * row_scale(r) * a (NULL: 1),
+ *   dh(r, f)     = row_scale * da * u * s * (1 + g * (1 - s))
+ *   dh(r, F + f) = row_scale * da * g * s
+ *   act(r, f)    = row_scale * g * s * u      (NULL: not wanted)
+ *   drow(r)      = sum_f da * g * s * u       (NULL: not wanted)
+ * dh [R, 2F] and act [R, F] of da's type, drow fp32; a row's sum in a fixed
+ * order.  act and dy are bsmm_expert_wgrad's operands for the layer's second
+ * weight, dh the first one's gradient; drow is the routing weight's.
+ * F % 32 == 0; rows as for bsmm_quant_int8_mx.
+ */
+bsmm_status bsmm_swiglu_backward(const void* da, int64_t ldda, bsmm_dtype dtype, const int8_t* q,
+                                 int64_t ldq, const uint8_t* scale, int64_t s_r,
+                                 const float* row_scale, void* dh, int64_t lddh, void* act,
+                                 int64_t ldact, float* drow, int64_t R, int64_t F, void* stream);
+
+/*
  * The router of a mixture-of-experts layer: every token's k experts, their
  * weights, the experts' loads, the slots sorted by expert and, for training,
  * the balance loss.  logits [T, E] (fp32 or bf16, row stride ldl elements);
