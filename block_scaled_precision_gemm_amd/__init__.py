@@ -25,6 +25,7 @@ __all__ = [
     "bsmm_quant_w4", "bsmm_w4_mm", "bsmm_w4_expert_mm",
     "bsmm_expert_mm", "bsmm_expert_wgrad",
     "bsmm_quant_int8_mx", "bsmm_swiglu", "bsmm_swiglu_backward",
+    "bsmm_expert_wgrad_workspace_bytes",
     "bsmm_route_topk", "bsmm_route_topk_backward", "Route",
     "bsmm_w4_workspace_bytes", "bsmm_w4_plan_name", "bsmm_route_workspace_bytes",
     "bsmm_workspace_bytes", "bsmm_query_plan", "bsmm_set_override", "bsmm_set_override_tail", "bsmm_set_streamk_grid", "bsmm_mfma_probe",
@@ -114,6 +115,8 @@ def load():
                                  i64, i64, i64, i64, vp, sz, vp]
     L.bsmm_expert_wgrad.argtypes = [vp, i64, st, st, vp, i64, st, vp, i64, vp, vp, vp, i64, i64,
                                     st, i64, i64, i64, i64, i64, i64, vp, sz, vp]
+    L.bsmm_expert_wgrad_workspace_bytes.argtypes = [st, st, i64, i64]
+    L.bsmm_expert_wgrad_workspace_bytes.restype = sz
     L.bsmm_quant_int8_mx.argtypes = [vp, i64, st, vp, i64, vp, i64, vp, i64, i64, i64, vp]
     L.bsmm_swiglu.argtypes = [vp, i64, st, vp, i64, vp, i64, vp, i64, i64, i64, vp]
     L.bsmm_swiglu_backward.argtypes = [vp, i64, st, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp,
@@ -1148,7 +1151,7 @@ def bsmm_expert_mm(x, w, order, offsets, *, slots_per_row=1, row_scale=None, out
 
 
 def bsmm_expert_wgrad(dy, x, order, offsets, *, x_scale=None, dy_slots_per_row=1,
-                      x_slots_per_row=1, out_dtype="f32", out=None, stream=None):
+                      x_slots_per_row=1, out_dtype="f32", out=None, workspace=None, stream=None):
     """The experts' weight gradients, dw[e] = sum of dy[s]^T x[s] over e's slots.
 
     dy: bf16 or fp32 [Ry, N].  x: [Rx, K] of dy's type, or with x_scale the
@@ -1157,7 +1160,9 @@ def bsmm_expert_wgrad(dy, x, order, offsets, *, x_scale=None, dy_slots_per_row=1
     offsets: int32 [E + 1] as bsmm_route_topk returns them; order None: the
     slots are sorted (S = Ry * dy_slots_per_row), and with offsets [0, S] this
     is a dense layer's gradient.  Returns [E, N, K], zeros for experts without
-    slots.
+    slots.  workspace (a checkpoint with bf16 dy): None for a cached one, False
+    for none, or a 16-byte aligned tensor of bsmm_expert_wgrad_workspace_bytes
+    bytes.
     """
     yc = _float_code(dy.dtype, "dy")
     code = _float_code(out_dtype, "out_dtype")
@@ -1186,7 +1191,8 @@ def bsmm_expert_wgrad(dy, x, order, offsets, *, x_scale=None, dy_slots_per_row=1
     if E < 0:
         raise ValueError("offsets must be 1-D [E + 1]")
     op = _routed(order, offsets, E, S, i32)
-    _one_gpu("dy, x, x_scale, order, offsets and out", dy, x, x_scale, order, offsets, out)
+    _one_gpu("dy, x, x_scale, order, offsets, out and workspace", dy, x, x_scale, order, offsets,
+             out, None if workspace is False else workspace)
     if out is None:
         o, se, ldw = torch.empty((E, N, K), dtype=dtypes[code], device=dy.device), N * K, K
     else:
@@ -1197,10 +1203,17 @@ def bsmm_expert_wgrad(dy, x, order, offsets, *, x_scale=None, dy_slots_per_row=1
         if K > 1 and sk != 1:
             raise ValueError("out must be contiguous along its last dimension")
         ldw = ldw if N > 1 else K
+    hs = _stream_of(dy, stream)
+    wsp, wsn = None, 0
+    if workspace is not None:
+        wsp, wsn = _given(workspace)
+    elif sp is not None:
+        wsp, wsn = _buffer(load().bsmm_expert_wgrad_workspace_bytes(yc, 1, Rx, K), dy.device,
+                           stream, hs)
     status = load().bsmm_expert_wgrad(
         dy.data_ptr(), ldy, yc, dy_slots_per_row, x.data_ptr(), ldx, x_slots_per_row, sp, s_r, op,
-        offsets.data_ptr(), o.data_ptr(), se if E > 1 else 0, ldw, code, E, Ry, Rx, S, N, K, None,
-        0, _stream_of(dy, stream))
+        offsets.data_ptr(), o.data_ptr(), se if E > 1 else 0, ldw, code, E, Ry, Rx, S, N, K, wsp,
+        wsn, hs)
     if status:
         _check(status)
     return o
@@ -1447,6 +1460,12 @@ def bsmm_w4_plan_name(x_dtype, routed, E, R, S, N, K, group):
     name = load().bsmm_w4_plan_name(_float_code(x_dtype, "x_dtype"), 1 if routed else 0, E, R, S,
                                     N, K, group)
     return name and name.decode()
+
+
+def bsmm_expert_wgrad_workspace_bytes(dtype, checkpoint, Rx, K):
+    """Workspace bytes bsmm_expert_wgrad wants for dy of ``dtype`` and x [Rx, K]."""
+    return load().bsmm_expert_wgrad_workspace_bytes(_float_code(dtype, "dtype"),
+                                                    1 if checkpoint else 0, Rx, K)
 
 
 def bsmm_route_workspace_bytes(T, E):

@@ -119,6 +119,21 @@ __global__ void __launch_bounds__(256) quant_int8_mx(QuantI8MxArgs a, unsigned c
   }
 }
 
+// A checkpoint's values in bf16, rows of K
+__global__ void __launch_bounds__(256) restore_bf16(const int8_t* q, int64_t ldq,
+                                                    const uint8_t* scale, int64_t s_r,
+                                                    uint16_t* out, unsigned K, int64_t chunks) {
+  const unsigned per_row = K / 8;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < chunks;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t row = chunks <= 0x7FFFFFFF ? (unsigned)i / per_row : i / per_row;
+    const int k = (int)(i - row * per_row) * 8;
+    float f[8];
+    decode(*reinterpret_cast<const uint2*>(q + row * ldq + k), scale[row * s_r + (k >> 5)], f);
+    store8(out + row * K + k, f);
+  }
+}
+
 // ---- gate ----------------------------------------------------------------------
 
 // e^-g = 2^t with t = -g log2(e): the product's rounding and the constant's,
@@ -212,6 +227,15 @@ int launch_quant_int8_mx(const QuantI8MxArgs& a, void* stream) {
     hipLaunchKernelGGL(quant_int8_mx<uint16_t>, grid, block, 0, st, a, (unsigned)chunks);
   else
     hipLaunchKernelGGL(quant_int8_mx<float>, grid, block, 0, st, a, (unsigned)chunks);
+  return hipGetLastError() == hipSuccess ? 0 : 1;
+}
+
+int launch_restore_bf16(const void* q, int64_t ldq, const uint8_t* scale, int64_t s_r, void* out,
+                        int64_t R, int64_t K, void* stream) {
+  const int64_t chunks = R * (K / 8);
+  hipLaunchKernelGGL(restore_bf16, dim3(blocks_for(chunks)), dim3(256), 0,
+                     static_cast<hipStream_t>(stream), static_cast<const int8_t*>(q), ldq, scale,
+                     s_r, static_cast<uint16_t*>(out), (unsigned)K, chunks);
   return hipGetLastError() == hipSuccess ? 0 : 1;
 }
 

@@ -12,6 +12,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <cstdlib>
 #include <type_traits>
 
 #include "bsmm_internal.h"
@@ -311,13 +312,587 @@ __global__ void __launch_bounds__(256, 2) expert_wgrad_kernel(WgradArgs a, int n
     }
 }
 
+// ---------------------------------------------------------------------------
+// bf16 with aligned rows: tiles of BM = 64 MI rows by 256 columns, eight waves
+// of 32 MI x 64 (MI x 2 blocks of 32 x 32 x 16 instructions), the contraction
+// in steps of 64.
+//
+// Both tiles stand in LDS as rows of 128 bytes with the contraction inside.
+// Operands that lie in memory that way go global -> LDS directly, as many
+// steps ahead as 156 KB hold.  The other kind goes through registers: a wave
+// has 8 neighbouring elements of the contraction (rows in memory) and a lane 4
+// columns, which it transposes with 16 byte permutations and writes as 4 x 16
+// bytes, the loads a step ahead.  (The transposing LDS read would spare that,
+// but the compiler waits for every direct load in flight before one, and
+// before an LDS write, so that a tile that needs one takes the other operand
+// through registers too.)
+//
+// The source order is the schedule: a turn's fragments are read during the
+// turn before, and the barrier stands before the last turn, whose products
+// then cover the first fragments of the next step.  After it nobody reads the
+// step's slot any more, and the direct loads of the step that gets it go out.
+// ---------------------------------------------------------------------------
+constexpr int kWide = 256;                      // columns of a tile
+__device__ const uint32_t kZeros[128] = {};     // a row of zeros
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+// a load from global memory, whatever the pointer was chosen from
+template <typename V>
+__device__ __forceinline__ V load_global(const void* p) {
+  return *(const __attribute__((address_space(1))) V*)(uintptr_t)p;
+}
+
+// Unit c of row r of a tile that is written transposed: a write's 64 rows r =
+// 4 lane + j and a read's 32 neighbouring rows both spread over the 8 units.
+__device__ __forceinline__ int turned_off(int r, int c) {
+  return (r << 7) + ((c ^ ((r >> 2) & 7) ^ ((r & 3) << 1)) << 4);
+}
+
+template <int MI> struct Wide {
+  static constexpr int BM = 64 * MI, ROWS = 32 * MI;   // of the tile, of a wave
+  static constexpr int A = BM * 128, B = kWide * 128;  // bytes of a step's tiles
+  static constexpr int SLOT = A + B;
+  static constexpr int DIRECT = 156 * 1024 / SLOT > 3 ? 3 : 156 * 1024 / SLOT;   // slots
+  static constexpr int LA = MI, LB = 4;                // loads of a wave and step
+};
+constexpr int kWideSlots = 2 * Wide<4>::SLOT;   // the ring's bytes at most: the rows' slots
+                                                // and scales stand behind it
+static_assert(3 * Wide<2>::SLOT > kWideSlots, "");
+constexpr int kWideRing = 3 * Wide<2>::SLOT;
+constexpr int kWideBytes = kWideRing + 2 * 256 * 4;
+
+__device__ __forceinline__ void lds_done() {
+  __builtin_amdgcn_s_waitcnt(0xC07F);           // lgkmcnt(0), in the compiler's count too
+}
+
+// 8 rows x 4 columns on their way to an operand's tile
+struct Turn { u32x2 row[8]; };
+// columns 2 h and 2 h + 1 of them
+__device__ __forceinline__ void put_turned(const Turn& v, uint8_t* tile, int octet, int h) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int c = 2 * h; c < 2 * h + 2; ++c) {
+    u32x4 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = h ? v.row[2 * i].y : v.row[2 * i].x;
+      const uint32_t b = h ? v.row[2 * i + 1].y : v.row[2 * i + 1].x;
+      o[i] = __builtin_amdgcn_perm(b, a, c & 1 ? 0x07060302u : 0x05040100u);
+    }
+    *reinterpret_cast<u32x4*>(tile + turned_off(4 * lane + c, octet)) = o;
+  }
+}
+
+// The products of one tile.  D > 0: direct(last, s, slot) issues a wave's MI +
+// 4 direct loads of step s into one of D slots.  D = 0: fetch(last, s) issues
+// its loads to registers, put(slot, h) writes half h of those.  last: whether
+// s may be the last step, which may end early.
+//
+// The fragments enter the instruction exchanged: a lane's 16 results of a
+// block are 4 x 4 neighbouring columns of one row.
+template <int MI, int D, bool A_TURNED, bool B_TURNED, typename Direct, typename Fetch,
+          typename Put>
+__device__ __forceinline__ void wide_products(uint8_t* smem, int steps, f32x16 (&acc)[MI][2],
+                                              const Direct& direct, const Fetch& fetch,
+                                              const Put& put) {
+  using W = Wide<MI>;
+  constexpr int SLOTS = D > 0 ? D : 2, ND = MI + 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wm = (wave >> 2) * W::ROWS, wn = (wave & 3) * 64;
+  struct Frag { u32x4 a[MI], b[2]; };
+  auto frags = [&](Frag& f, const uint8_t* slot, int t) {
+    const int c = 2 * t + (lane >> 5), r = lane & 31;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      f.b[j] = *reinterpret_cast<const u32x4*>(
+          slot + W::A + (wn + 32 * j) * 128 + (B_TURNED ? turned_off(r, c) : lds_off(r, c)));
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+      f.a[i] = *reinterpret_cast<const u32x4*>(
+          slot + (wm + 32 * i) * 128 + (A_TURNED ? turned_off(r, c) : lds_off(r, c)));
+  };
+  auto products = [&](const Frag& f) {
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[i][j] = product<uint16_t>(f.b[j], f.a[i], acc[i][j]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  if (steps == 0) return;
+  constexpr std::true_type last{};
+  if constexpr (D > 0) {
+#pragma unroll
+    for (int s = 0; s < D; ++s)
+      if (s < steps) direct(last, s, smem + s * W::SLOT);
+    if (D == 3 && steps > 2) wait_vmcnt<2 * ND>();
+    else if (steps > 1) wait_vmcnt<ND>();
+    else wait_vmcnt<0>();
+  } else {
+    fetch(last, 0);
+    put(smem, 0);
+    put(smem, 1);
+    if (steps > 1) fetch(last, 1);
+  }
+  lds_done();
+  barrier();
+  Frag f[2];
+  frags(f[0], smem, 0);
+  uint8_t* slot = smem;
+  // HOT: enough steps follow, so the body has no branch
+  auto step = [&](auto end, int s) {
+    constexpr bool HOT = !decltype(end)::value;
+    uint8_t* const next = slot == smem + (SLOTS - 1) * W::SLOT ? smem : slot + W::SLOT;
+    lds_done();
+    frags(f[1], slot, 1);
+    products(f[0]);
+    frags(f[0], slot, 2);
+    if (D == 0 && (HOT || s + 1 < steps)) put(next, 0);
+    products(f[1]);
+    frags(f[1], slot, 3);
+    if (D == 0 && (HOT || s + 1 < steps)) put(next, 1);
+    if (D == 0 && (HOT || s + 2 < steps)) fetch(end, s + 2);
+    products(f[0]);
+    // this wave's direct loads of the next step have landed, its tiles are
+    // written and it has read this step's fragments; then everyone
+    if (D > 0) {
+      if (D == 3 && (HOT || s + 2 < steps)) wait_vmcnt<ND>(); else wait_vmcnt<0>();
+    }
+    lds_done();
+    barrier();
+    if (D > 0 && (HOT || s + D < steps)) direct(end, s + D, slot);
+    if (HOT || s + 1 < steps) frags(f[0], next, 0);
+    products(f[1]);
+    slot = next;
+  };
+  int s = 0;
+#pragma unroll 1
+  for (; s + SLOTS + 1 < steps; ++s) step(std::false_type{}, s);
+#pragma unroll 1
+  for (; s < steps; ++s) step(last, s);
+}
+
+// A wave's 32 MI x 64 results to memory, a block of 32 rows at a time through
+// LDS, so that a store covers whole runs of a row.  row(m): the address of
+// column 0 of the wave's row m (null: not stored), scale(m) its factor; cols:
+// the columns from there to the end; vec: rows 16-byte aligned there.
+template <int MI, typename Row, typename Scale>
+__device__ __forceinline__ void wide_store(uint8_t* smem, const f32x16 (&acc)[MI][2],
+                                           bsmm_dtype dt, int cols, bool vec, const Row& row,
+                                           const Scale& scale) {
+  constexpr int PITCH = 64 * 4 + 16;                   // reads and writes without conflicts
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  uint8_t* const part = smem + wave * (32 * PITCH);
+  barrier();                                           // nobody reads the ring any more
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<f32x4*>(part + (lane & 31) * PITCH +
+                                  (32 * j + 8 * g + 4 * (lane >> 5)) * 4) =
+            f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
+                  acc[i][j][4 * g + 3]};
+    if (dt == BSMM_BF16) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int m = 8 * q + (lane >> 3), c = (lane & 7) * 8;
+        const f32x4* const p = reinterpret_cast<const f32x4*>(part + m * PITCH + c * 4);
+        const float f = scale(32 * i + m);
+        const f32x4 v = p[0] * f, w = p[1] * f;
+        uint8_t* const to = static_cast<uint8_t*>(row(32 * i + m));
+        if (to == nullptr) continue;
+        if (vec && c + 8 <= cols) {
+          u32x4 o;
+          o[0] = bf16_pair(v[0], v[1]);
+          o[1] = bf16_pair(v[2], v[3]);
+          o[2] = bf16_pair(w[0], w[1]);
+          o[3] = bf16_pair(w[2], w[3]);
+          *reinterpret_cast<u32x4*>(to + c * 2) = o;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (c + k < cols)
+              reinterpret_cast<uint16_t*>(to)[c + k] = (uint16_t)bf16_bits(k < 4 ? v[k & 3]
+                                                                                 : w[k & 3]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int m = 4 * q + (lane >> 4), c = (lane & 15) * 4;
+        const f32x4 v = *reinterpret_cast<const f32x4*>(part + m * PITCH + c * 4) *
+                        scale(32 * i + m);
+        uint8_t* const to = static_cast<uint8_t*>(row(32 * i + m));
+        if (to == nullptr) continue;
+        if (vec && c + 4 <= cols) {
+          *reinterpret_cast<f32x4*>(to + c * 4) = v;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (c + k < cols) reinterpret_cast<float*>(to)[c + k] = v[k];
+        }
+      }
+    }
+  }
+}
+
+// An item of at most 64 MI rows from column n0.
+template <int MI, bool W_ACROSS>
+__device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& it, int n0,
+                                               uint8_t* smem, const int* slots,
+                                               const float* scales, bool vec) {
+  using W = Wide<MI>;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // load t of an operand brings rows 64 t + 8 wave + lane / 8 of its tile;
+  // rows and columns past the end repeat others (not stored)
+  const uint16_t* const w = static_cast<const uint16_t*>(a.w) + it.e * a.w_se;
+  const int xk = ((lane & 7) ^ swz(8 * wave + (lane >> 3))) * 8;
+  const uint16_t* xp[MI];
+  const uint16_t* wp[4];
+#pragma unroll
+  for (int t = 0; t < MI; ++t) {
+    const int s = max(slots[64 * t + 8 * wave + (lane >> 3)], 0);
+    xp[t] = static_cast<const uint16_t*>(a.x) + (int64_t)min(s / a.x_div, a.R - 1) * a.ldx + xk;
+  }
+  if constexpr (!W_ACROSS) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      wp[t] = w + (int64_t)min(n0 + 64 * t + 8 * wave + (lane >> 3), a.N - 1) * a.ldw + xk;
+  }
+  const uint16_t* const zero = reinterpret_cast<const uint16_t*>(kZeros);
+  auto direct = [&](auto last, int s, uint8_t* slot) {
+    const bool in = !decltype(last)::value || s * 64 + xk < a.K;
+#pragma unroll
+    for (int t = 0; t < MI; ++t)
+      to_lds<16>(in ? xp[t] + s * 64 : zero, slot + (t * 8 + wave) * 1024);
+    if constexpr (!W_ACROSS) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        to_lds<16>(in ? wp[t] + s * 64 : zero, slot + W::A + (t * 8 + wave) * 1024);
+    }
+  };
+  u32x4 xv[MI];
+  Turn v;
+  const uint32_t at = (uint32_t)min(4 * lane, a.N - 4 - n0) * 2;
+  auto fetch = [&](auto last, int s) {
+    const bool in = !decltype(last)::value || s * 64 + xk < a.K;
+#pragma unroll
+    for (int t = 0; t < MI; ++t) xv[t] = load_global<u32x4>(in ? xp[t] + s * 64 : zero);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = s * 64 + wave * 8 + i;
+      const uint16_t* row = w + (int64_t)k * a.ldw + n0;
+      if (decltype(last)::value) row = k < a.K ? row : zero;
+      v.row[i] = load_global<u32x2>(reinterpret_cast<const uint8_t*>(row) + at);
+    }
+  };
+  auto put = [&](uint8_t* slot, int h) {
+#pragma unroll
+    for (int t = h * MI / 2; t < (h + 1) * MI / 2; ++t)
+      *reinterpret_cast<u32x4*>(slot + (t * 8 + wave) * 1024 + lane * 16) = xv[t];
+    put_turned(v, slot + W::A, wave, h);
+  };
+  f32x16 acc[MI][2] = {};
+  wide_products<MI, W_ACROSS ? 0 : W::DIRECT, false, W_ACROSS>(
+      smem, (int)(((unsigned)a.K + 63) / 64), acc, direct, fetch, put);
+  const int wm = (wave >> 2) * W::ROWS, col = n0 + (wave & 3) * 64;
+  const int size = a.out_dtype == BSMM_BF16 ? 2 : 4;
+  uint8_t* const out = static_cast<uint8_t*>(a.out) + (int64_t)col * size;
+  wide_store<MI>(
+      smem, acc, a.out_dtype, a.N - col, vec,
+      [&](int m) -> void* {
+        const int slot = slots[wm + m];
+        return slot < 0 ? nullptr : out + slot * a.ldo * size;
+      },
+      [&](int m) { return scales[wm + m]; });
+}
+
+template <bool W_ACROSS>
+__global__ void __launch_bounds__(512, 2) expert_mm_wide(ExpertArgs a, int items, int ntn,
+                                                         int vec) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  int* const slots = reinterpret_cast<int*>(smem + kWideRing);
+  float* const scales = reinterpret_cast<float*>(slots + 256);
+  int item, tn;
+  tile_of(items, ntn, item, tn);
+  const Item it = find_item(a.offsets, a.E, a.S, 256, item);
+  const int n0 = tn * kWide;
+  const unsigned used = min(max(a.offsets[a.E], 0), a.S);
+  for (unsigned p = used + item; p < (unsigned)a.S; p += items) {    // both below 2^31
+    const int slot = slot_at(a.order, p);
+    if (slot >= 0 && slot < a.S && (int)threadIdx.x < min(kWide, a.N - n0))
+      put(a.out, a.out_dtype, slot * a.ldo + n0 + threadIdx.x, 0.0f);
+  }
+  if (it.rows == 0) return;
+  // the rows' slots (-1: not stored) and scales
+  if (threadIdx.x < 256) {
+    const int r = threadIdx.x;
+    const int s = r < it.rows ? slot_at(a.order, it.p0 + r) : -1;
+    const bool in = s >= 0 && s < a.S;
+    slots[r] = in ? s : -1;
+    scales[r] = in && a.row_scale ? a.row_scale[s] : 1.0f;
+  }
+  __syncthreads();
+  // only as many rows as there are, to 64: an expert's last item would
+  // multiply 128 empty rows on average
+  const int mi = (it.rows + 63) / 64;
+  if (mi == 4) expert_mm_item<4, W_ACROSS>(a, it, n0, smem, slots, scales, vec);
+  else if (mi == 3) expert_mm_item<3, W_ACROSS>(a, it, n0, smem, slots, scales, vec);
+  else if (mi == 2) expert_mm_item<2, W_ACROSS>(a, it, n0, smem, slots, scales, vec);
+  else expert_mm_item<1, W_ACROSS>(a, it, n0, smem, slots, scales, vec);
+}
+
+// n / d for 0 <= n < 2^31 (Granlund and Montgomery, "Division by invariant
+// integers using multiplication", 1994): (mulhi(m, n) + n) >> l
+struct Divisor { uint32_t m; int l; };
+__device__ __forceinline__ uint32_t divide(uint32_t n, Divisor d) {
+  return (__umulhi(d.m, n) + n) >> d.l;
+}
+
+__global__ void __launch_bounds__(512, 2) expert_wgrad_wide(WgradArgs a, int ntn, int ntk,
+                                                            Divisor yd, Divisor xd, int vec) {
+  using W = Wide<4>;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  int item, tk;
+  tile_of(a.E * ntn, ntk, item, tk);
+  const int e = item / ntn, n0 = item % ntn * 256, k0 = tk * kWide, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lo = min(max(a.offsets[e], 0), a.S), hi = min(max(a.offsets[e + 1], lo), a.S);
+  const uint8_t* const zero = reinterpret_cast<const uint8_t*>(kZeros);
+  const uint8_t* const dy = static_cast<const uint8_t*>(a.dy) + n0 * 2;
+  const uint8_t* const x = static_cast<const uint8_t*>(a.x) + k0 * 2;
+  const uint32_t ay = (uint32_t)min(4 * lane, a.N - 4 - n0) * 2;
+  const uint32_t ax = (uint32_t)min(4 * lane, a.K - 4 - k0) * 2;
+  // the wave's 8 positions of a step; lane i < 8 has the slot of the i-th
+  auto slot_of = [&](int s) {
+    return lo < hi ? slot_at(a.order, min(lo + s * 64 + wave * 8 + (lane & 7), hi - 1)) : 0;
+  };
+  int mine = slot_of(0);
+  Turn vy, vx;
+  auto fetch = [&](auto last, int s) {
+    const uint32_t slot = min(max(mine, 0), a.S - 1);
+    const int64_t oy = (int64_t)divide(slot, yd) * a.ldy * 2;
+    const int64_t ox = (int64_t)divide(slot, xd) * a.ldx * 2;
+    const int rows = decltype(last)::value ? hi - lo - s * 64 - wave * 8 : 8;
+    auto lane_of = [](int64_t v, int i) {
+      const uint32_t l = __builtin_amdgcn_readlane((int)v, i);
+      return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), i) << 32 | l);
+    };
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint8_t* ry = dy + lane_of(oy, i);
+      const uint8_t* rx = x + lane_of(ox, i);
+      if (decltype(last)::value) {
+        ry = i < rows ? ry : zero;
+        rx = i < rows ? rx : zero;
+      }
+      vy.row[i] = load_global<u32x2>(ry + ay);
+      vx.row[i] = load_global<u32x2>(rx + ax);
+    }
+    mine = slot_of(s + 1);
+  };
+  auto put_both = [&](uint8_t* slot, int h) {
+    put_turned(vy, slot, wave, h);
+    put_turned(vx, slot + W::A, wave, h);
+  };
+  f32x16 acc[4][2] = {};
+  wide_products<4, 0, true, true>(smem, (int)(((unsigned)(hi - lo) + 63) / 64), acc,
+                                  [](auto, int, uint8_t*) {}, fetch, put_both);
+  const int row0 = n0 + (wave >> 2) * 128, col = k0 + (wave & 3) * 64;
+  const int size = a.out_dtype == BSMM_BF16 ? 2 : 4;
+  uint8_t* const out = static_cast<uint8_t*>(a.dw) + (e * a.w_se + col) * size;
+  wide_store<4>(
+      smem, acc, a.out_dtype, a.K - col, vec,
+      [&](int m) -> void* {
+        return row0 + m < a.N ? out + (row0 + m) * a.ldw * size : nullptr;
+      },
+      [](int) { return 1.0f; });
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: items of 16 rows by 64 columns, 16 x 16 instructions with the
+// weight as the first operand.  The eight waves of a workgroup share out cn =
+// 8 / ks column groups and ks ranges of the contraction; partial sums are
+// added through LDS in order.
+//
+// Everything goes straight to registers, kDepth chunks of 64 bytes (32 bf16 or
+// 16 fp32 of the contraction) ahead: no barrier, each weight byte is used by
+// one wave.  Along, a lane's 16 bytes are one column's.  Across, a lane has 4
+// neighbouring columns: of bf16 8 rows, transposed by byte permutations, of
+// fp32 4 rows, each lane's 4 values then belonging to 4 column blocks.
+// ---------------------------------------------------------------------------
+constexpr int kRowsWaves = 8, kDepth = 4;
+
+// A chunk of one wave: x's fragment and those of its 4 column blocks
+template <typename T, bool ACROSS> struct Chunk {
+  u32x4 x;
+  std::conditional_t<ACROSS && sizeof(T) == 2, u32x2, u32x4>
+      w[ACROSS && sizeof(T) == 2 ? 8 : 4];
+};
+
+template <typename T, bool W_ACROSS>
+__global__ void __launch_bounds__(kRowsWaves * 64, 4) expert_mm_rows(ExpertArgs a, int item0,
+                                                                     int log_ks) {
+  constexpr int U = Elem<T>::U, CHUNK = 4 * U;         // elements of a lane's unit, a chunk
+  __shared__ __attribute__((aligned(16))) float part[kRowsWaves][16][68];
+  const int lane = threadIdx.x & 63, c16 = lane & 15, quad = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ks = 1 << log_ks, cn = kRowsWaves >> log_ks;
+  const int kw = wave & (ks - 1), cw = wave >> log_ks;
+  const int item = item0 + blockIdx.y;
+  const Item it = find_item(a.offsets, a.E, a.S, 16, item);
+  const int n0 = (blockIdx.x * cn + cw) * 64, cols = cn * 64;
+  const unsigned used = min(max(a.offsets[a.E], 0), a.S);
+  for (unsigned p = used + item; p < (unsigned)a.S; p += gridDim.y) {    // both below 2^31
+    const int slot = slot_at(a.order, p);
+    if (slot < 0 || slot >= a.S) continue;
+    const int n = blockIdx.x * cols + threadIdx.x;     // cols <= 512, the workgroup's threads
+    if ((int)threadIdx.x < cols && n < a.N) put(a.out, a.out_dtype, slot * a.ldo + n, 0.0f);
+  }
+  if (it.rows == 0) return;
+
+  const int slot = slot_at(a.order, it.p0 + (c16 < it.rows ? c16 : 0));
+  const int64_t row = min(max(slot / a.x_div, 0), a.R - 1);
+  const T* const x = static_cast<const T*>(a.x) + row * a.ldx + quad * U;
+  const T* const w = static_cast<const T*>(a.w) + it.e * a.w_se;
+  const T* wp[4];
+  if constexpr (W_ACROSS) {
+    wp[0] = w + (int64_t)(quad * U) * a.ldw + min(n0 + 4 * c16, a.N - 4);
+  } else {
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      wp[t] = w + (int64_t)min(n0 + 16 * t + c16, a.N - 1) * a.ldw + quad * U;
+  }
+  const T* const zero = reinterpret_cast<const T*>(kZeros);
+  using C = Chunk<T, W_ACROSS>;
+  auto load = [&](C& v, int c) {
+    const int k = c * CHUNK;
+    const bool in = k + quad * U < a.K;                // K % U == 0
+    v.x = load_global<u32x4>(in ? x + k : zero);
+    if constexpr (W_ACROSS) {
+      const T* const p = wp[0] + k * a.ldw;
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        v.w[i] = load_global<std::remove_reference_t<decltype(v.w[0])>>(in ? p + i * a.ldw : zero);
+    } else {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) v.w[t] = load_global<u32x4>(in ? wp[t] + k : zero);
+    }
+  };
+  f32x4 acc[4] = {};
+  auto consume = [&](const C& v) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      if constexpr (sizeof(T) == 2) {
+        u32x4 f;
+        if constexpr (W_ACROSS) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            f[i] = __builtin_amdgcn_perm(v.w[2 * i + 1][t >> 1], v.w[2 * i][t >> 1],
+                                         t & 1 ? 0x07060302u : 0x05040100u);
+        } else {
+          f = v.w[t];
+        }
+        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            __builtin_bit_cast(bf16x8, f), __builtin_bit_cast(bf16x8, v.x), acc[t], 0, 0, 0);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+              __uint_as_float(W_ACROSS ? v.w[j][t] : v.w[t][j]), __uint_as_float(v.x[j]), acc[t],
+              0, 0, 0);
+      }
+    }
+  };
+  const int chunks = (int)(((unsigned)a.K + CHUNK - 1) / CHUNK), per = (chunks + ks - 1) >> log_ks;
+  int c = min(kw * per, chunks);
+  const int end = n0 < a.N ? min(c + per, chunks) : c;
+  C v[kDepth];
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d)
+    if (c + d < end) load(v[d], c + d);
+#pragma unroll 1
+  for (; c + 2 * kDepth <= end; c += kDepth) {
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      consume(v[d]);
+      load(v[d], c + kDepth + d);
+    }
+  }
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d)
+    if (c + d < end) {
+      consume(v[d]);
+      if (c + kDepth + d < end) load(v[d], c + kDepth + d);
+    }
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d)
+    if (c + kDepth + d < end) consume(v[d]);
+
+  // a lane has row c16 and of column block t the columns 4 quad + r
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      part[wave][c16][W_ACROSS ? 16 * quad + 4 * r + t : 16 * t + 4 * quad + r] = acc[t][r];
+  __syncthreads();
+  // row m of the item to threads m, m + 16 ..: neighbouring threads have
+  // neighbouring columns
+  for (int i = threadIdx.x; i < it.rows * cols; i += kRowsWaves * 64) {
+    const int m = i / cols, n = i - m * cols, at = blockIdx.x * cols + n;
+    const int s = slot_at(a.order, it.p0 + m);
+    if (at >= a.N || s < 0 || s >= a.S) continue;
+    float sum = 0.0f;
+    for (int j = 0; j < ks; ++j) sum += part[((n >> 6) << log_ks) + j][m][n & 63];
+    put(a.out, a.out_dtype, s * a.ldo + at, a.row_scale ? sum * a.row_scale[s] : sum);
+  }
+}
+
+Divisor divisor(uint32_t d) {
+  int l = 0;
+  while (((uint64_t)1 << l) < d) ++l;
+  return Divisor{(uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << l) - d)) / d + 1), l};
+}
+
 template <typename T>
 bool vec_ok(const void* p, int64_t ld) {
   return (uintptr_t)p % 16 == 0 && ld % Elem<T>::U == 0;
 }
 
+template <typename T, bool W_ACROSS>
+void launch_rows(const ExpertArgs& a, hipStream_t st) {
+  const int64_t act = a.E < a.S ? a.E : a.S, items = (a.S + act * 15) / 16;
+  const int64_t groups = ((int64_t)a.N + 63) / 64;
+  static const int target = getenv("TGT") ? atoi(getenv("TGT")) : 2048;
+  const int64_t busy = (a.S + act * 8) / 16 + 1;
+  int log_ks = 0;
+  while (log_ks < 3 && (busy * groups << log_ks) < target) ++log_ks;
+  const int64_t ntn = (groups + (8 >> log_ks) - 1) / (8 >> log_ks);
+  for (int64_t i = 0; i < items; i += 65535)        // at most so many items a launch
+    hipLaunchKernelGGL((expert_mm_rows<T, W_ACROSS>),
+                       dim3((unsigned)ntn, (unsigned)(items - i < 65535 ? items - i : 65535)),
+                       dim3(kRowsWaves * 64), 0, st, a, (int)i, log_ks);
+}
+
 template <typename T>
 void launch_mm(const ExpertArgs& a, hipStream_t st) {
+  static const int few = getenv("FEW") ? atoi(getenv("FEW")) : 16;
+  if (vec_ok<T>(a.x, a.ldx) && vec_ok<T>(a.w, a.ldw) && a.w_se % Elem<T>::U == 0 &&
+      a.K % Elem<T>::U == 0 && (!a.w_across || a.N % Elem<T>::U == 0) && a.S <= few * a.E) {
+    if (a.w_across) launch_rows<T, true>(a, st); else launch_rows<T, false>(a, st);
+    return;
+  }
+  if (sizeof(T) == 2 && vec_ok<T>(a.x, a.ldx) && vec_ok<T>(a.w, a.ldw) && a.w_se % 8 == 0 &&
+      a.K % 8 == 0 && (!a.w_across || a.N % 8 == 0) && a.S > 0) {
+    const int64_t act = a.E < a.S ? a.E : a.S;
+    const int items = (int)((a.S + act * 255) / 256), ntn = (a.N + kWide - 1) / kWide;
+    const int vec = (uintptr_t)a.out % 16 == 0 && a.ldo % (a.out_dtype == BSMM_BF16 ? 8 : 4) == 0;
+    if (a.w_across) hipLaunchKernelGGL((expert_mm_wide<true>), dim3((unsigned)(items * ntn)), dim3(512), kWideBytes, st, a, items, ntn, vec);
+    else hipLaunchKernelGGL((expert_mm_wide<false>), dim3((unsigned)(items * ntn)), dim3(512), kWideBytes, st, a, items, ntn, vec);
+    return;
+  }
   const int64_t act = a.E < a.S ? a.E : a.S;
   const int items = (int)((a.S + act * (kTile - 1)) / kTile), ntn = (a.N + kTile - 1) / kTile;
   const dim3 grid((unsigned)(items * ntn)), block(256);
@@ -332,7 +907,19 @@ void launch_mm(const ExpertArgs& a, hipStream_t st) {
 }
 
 template <typename T>
-void launch_wgrad(const WgradArgs& a, hipStream_t st) {
+void launch_wgrad(WgradArgs a, void* ws, hipStream_t st) {
+  if (sizeof(T) == 2 && a.x_scale && ws) {
+    if (launch_restore_bf16(a.x, a.ldx, a.x_scale, a.s_r, ws, a.Rx, a.K, st)) return;
+    a.x = ws; a.ldx = a.K; a.x_scale = nullptr;
+  }
+  if (sizeof(T) == 2 && !a.x_scale && vec_ok<T>(a.dy, a.ldy) && vec_ok<T>(a.x, a.ldx) && a.N % 8 == 0 &&
+      a.K % 8 == 0) {
+    const int ntn = (a.N + 255) / 256, ntk = (a.K + 255) / 256;
+    hipLaunchKernelGGL(expert_wgrad_wide, dim3((unsigned)((int64_t)a.E * ntn * ntk)), dim3(512),
+                       kWideBytes, st, a, ntn, ntk, divisor(a.y_div), divisor(a.x_div),
+                       (uintptr_t)a.dw % 16 == 0 && a.ldw % 8 == 0 && a.w_se % 8 == 0);
+    return;
+  }
   const int ntn = (a.N + kTile - 1) / kTile, ntk = (a.K + kTile - 1) / kTile;
   const dim3 grid((unsigned)((int64_t)a.E * ntn * ntk)), block(256);
   const bool yv = vec_ok<T>(a.dy, a.ldy);
@@ -356,10 +943,10 @@ int launch_expert_mm(const ExpertArgs& a, void* stream) {
   return hipGetLastError() == hipSuccess ? 0 : 1;
 }
 
-int launch_expert_wgrad(const WgradArgs& a, void* stream) {
+int launch_expert_wgrad(const WgradArgs& a, void* ws, void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (a.dtype == BSMM_BF16) launch_wgrad<uint16_t>(a, st);
-  else launch_wgrad<float>(a, st);
+  if (a.dtype == BSMM_BF16) launch_wgrad<uint16_t>(a, ws, st);
+  else launch_wgrad<float>(a, ws, st);
   return hipGetLastError() == hipSuccess ? 0 : 1;
 }
 

@@ -77,6 +77,12 @@ bsmm_status bsmm_expert_mm(const void* x, int64_t ldx, const void* w, int64_t w_
   return BSMM_OK;
 }
 
+size_t bsmm_expert_wgrad_workspace_bytes(bsmm_dtype dtype, int checkpoint, int64_t Rx, int64_t K) {
+  if (dtype != BSMM_BF16 || !checkpoint || Rx <= 0 || K <= 0 || Rx >= kMaxDim || K >= kMaxDim)
+    return 0;
+  return (size_t)Rx * (size_t)K * 2u;
+}
+
 bsmm_status bsmm_expert_wgrad(const void* dy, int64_t ldy, bsmm_dtype dtype, int dy_slots_per_row,
                               const void* x, int64_t ldx, int x_slots_per_row,
                               const uint8_t* x_scale, int64_t s_r, const int32_t* order,
@@ -126,10 +132,11 @@ bsmm_status bsmm_expert_wgrad(const void* dy, int64_t ldy, bsmm_dtype dtype, int
   a.x_scale = x_scale; a.s_r = s_r;
   a.order = order; a.offsets = offsets;
   a.dw = dw; a.w_se = w_se; a.ldw = ldw; a.out_dtype = out_dtype;
-  a.E = (int)E; a.S = (int)S; a.N = (int)N; a.K = (int)K;
-  (void)workspace;
-  (void)workspace_bytes;
-  if (launch_expert_wgrad(a, stream) != 0)
+  a.E = (int)E; a.Rx = (int)Rx; a.S = (int)S; a.N = (int)N; a.K = (int)K;
+  const size_t need = bsmm_expert_wgrad_workspace_bytes(dtype, x_scale != nullptr, Rx, K);
+  void* ws = need > 0 && S > 0 && workspace_bytes >= need && aligned(workspace, 16) &&
+                     aligned(x, 8) && ldx % 8 == 0 ? workspace : nullptr;
+  if (launch_expert_wgrad(a, ws, stream) != 0)
     return fail(BSMM_ERR_HIP, "kernel launch failed (expert weight gradient)");
   return BSMM_OK;
 }

@@ -269,9 +269,13 @@ struct WgradArgs {
   const int32_t* order;
   const int32_t* offsets;
   void* dw; int64_t w_se, ldw; bsmm_dtype out_dtype;
-  int E, S, N, K;
+  int E, Rx, S, N, K;
 };
-int launch_expert_wgrad(const WgradArgs& a, void* stream);
+// ws: null, or Rx * K * 2 bytes for a checkpoint and bf16 dy
+int launch_expert_wgrad(const WgradArgs& a, void* ws, void* stream);
+// A checkpoint's values in bf16, rows of K (0 on success)
+int launch_restore_bf16(const void* q, int64_t ldq, const uint8_t* scale, int64_t s_r, void* out,
+                        int64_t R, int64_t K, void* stream);
 
 // 8-bit checkpoints (bsmm_ckpt.hip): int8 codes q [R, K] and a byte per 32
 // elements of a row, scale[r * s_r + k / 32]; code * 2^(byte - 133).

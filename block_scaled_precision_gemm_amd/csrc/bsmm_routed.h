@@ -23,6 +23,10 @@ __device__ __forceinline__ uint32_t bf16_bits(float v) {
          0xFFFFu;
 }
 
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{lo, hi}), bf16x2_t));
+}
+
 struct Item { int e, p0, rows; };
 
 // Work item `item` of a routed product: every expert's run of positions is

@@ -551,7 +551,11 @@ bsmm_status bsmm_expert_mm(const void* x, int64_t ldx, const void* w, int64_t w_
  * dy_slots_per_row and S <= Rx * x_slots_per_row.  Sums, sizes, alignment and
  * workspace as for bsmm_expert_mm (a checkpoint: rows of codes at multiples
  * of 8 bytes are faster).  E, N or K 0 does nothing; S == 0 writes zeros.
+ * The workspace (16-byte aligned) holds a checkpoint's values in bf16 while
+ * the call runs: bsmm_expert_wgrad_workspace_bytes gives the bytes (0: none
+ * wanted).  With less the call runs without it, slower.
  */
+size_t bsmm_expert_wgrad_workspace_bytes(bsmm_dtype dtype, int checkpoint, int64_t Rx, int64_t K);
 bsmm_status bsmm_expert_wgrad(const void* dy, int64_t ldy, bsmm_dtype dtype, int dy_slots_per_row,
                               const void* x, int64_t ldx, int x_slots_per_row,
                               const uint8_t* x_scale, int64_t s_r, const int32_t* order,
