@@ -366,102 +366,116 @@ __device__ __forceinline__ void lds_done() {
 
 // 8 rows x 4 columns on their way to an operand's tile
 struct Turn { u32x2 row[8]; };
-// columns 2 h and 2 h + 1 of them
-__device__ __forceinline__ void put_turned(const Turn& v, uint8_t* tile, int octet, int h) {
-  const int lane = threadIdx.x & 63;
+// column c of them
+__device__ __forceinline__ void put_turned(const Turn& v, uint8_t* tile, int octet, int c) {
+  u32x4 o;
 #pragma unroll
-  for (int c = 2 * h; c < 2 * h + 2; ++c) {
-    u32x4 o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t a = h ? v.row[2 * i].y : v.row[2 * i].x;
-      const uint32_t b = h ? v.row[2 * i + 1].y : v.row[2 * i + 1].x;
-      o[i] = __builtin_amdgcn_perm(b, a, c & 1 ? 0x07060302u : 0x05040100u);
-    }
-    *reinterpret_cast<u32x4*>(tile + turned_off(4 * lane + c, octet)) = o;
-  }
+  for (int i = 0; i < 4; ++i)
+    o[i] = __builtin_amdgcn_perm(v.row[2 * i + 1][c >> 1], v.row[2 * i][c >> 1],
+                                 c & 1 ? 0x07060302u : 0x05040100u);
+  *reinterpret_cast<u32x4*>(tile + turned_off(4 * (threadIdx.x & 63) + c, octet)) = o;
 }
 
-// The products of one tile.  D > 0: direct(last, s, slot) issues a wave's MI +
-// 4 direct loads of step s into one of D slots.  D = 0: fetch(last, s) issues
-// its loads to registers, put(slot, h) writes half h of those.  last: whether
-// s may be the last step, which may end early.
+// The products of one tile.  D > 0: ops.direct(last, s, slot, i) issues load i
+// of a wave's MI + 4 direct loads of step s into one of D slots.  D = 0:
+// ops.fetch(last, s, i) issues load i of NR to registers (ops.begin(last, s)
+// before the first), ops.put(slot, i) writes part i of NP of them.  last:
+// whether s may be the last step, which may end early.
 //
 // The fragments enter the instruction exchanged: a lane's 16 results of a
 // block are 4 x 4 neighbouring columns of one row.
-template <int MI, int D, bool A_TURNED, bool B_TURNED, typename Direct, typename Fetch,
-          typename Put>
+template <int MI, int D, bool A_TURNED, bool B_TURNED, int NR, int NP, typename Ops>
 __device__ __forceinline__ void wide_products(uint8_t* smem, int steps, f32x16 (&acc)[MI][2],
-                                              const Direct& direct, const Fetch& fetch,
-                                              const Put& put) {
+                                              Ops& ops) {
   using W = Wide<MI>;
-  constexpr int SLOTS = D > 0 ? D : 2, ND = MI + 4;
+  constexpr int SLOTS = D > 0 ? D : 2, ND = MI + 4, M = 2 * MI;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm = (wave >> 2) * W::ROWS, wn = (wave & 3) * 64;
   struct Frag { u32x4 a[MI], b[2]; };
-  auto frags = [&](Frag& f, const uint8_t* slot, int t) {
+  // fragment x of turn t: the two of the columns, then those of the rows
+  auto read = [&](Frag& f, const uint8_t* slot, int t, int x) {
     const int c = 2 * t + (lane >> 5), r = lane & 31;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      f.b[j] = *reinterpret_cast<const u32x4*>(
-          slot + W::A + (wn + 32 * j) * 128 + (B_TURNED ? turned_off(r, c) : lds_off(r, c)));
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-      f.a[i] = *reinterpret_cast<const u32x4*>(
-          slot + (wm + 32 * i) * 128 + (A_TURNED ? turned_off(r, c) : lds_off(r, c)));
-  };
-  auto products = [&](const Frag& f) {
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = product<uint16_t>(f.b[j], f.a[i], acc[i][j]);
-    __builtin_amdgcn_sched_barrier(0);
+    if (x < 2)
+      f.b[x] = *reinterpret_cast<const u32x4*>(
+          slot + W::A + (wn + 32 * x) * 128 + (B_TURNED ? turned_off(r, c) : lds_off(r, c)));
+    else
+      f.a[x - 2] = *reinterpret_cast<const u32x4*>(
+          slot + (wm + 32 * (x - 2)) * 128 + (A_TURNED ? turned_off(r, c) : lds_off(r, c)));
   };
   if (steps == 0) return;
   constexpr std::true_type last{};
+  constexpr int H = ND / 2;             // direct loads of a step's first half
   if constexpr (D > 0) {
 #pragma unroll
     for (int s = 0; s < D; ++s)
-      if (s < steps) direct(last, s, smem + s * W::SLOT);
-    if (D == 3 && steps > 2) wait_vmcnt<2 * ND>();
-    else if (steps > 1) wait_vmcnt<ND>();
+#pragma unroll
+      for (int i = 0; i < (s < D - 1 ? ND : H); ++i)
+        if (s < steps) ops.direct(last, s, smem + s * W::SLOT, i);
+    if (D == 3 && steps > 2) wait_vmcnt<ND + H>();
+    else if (steps > 1) wait_vmcnt<D == 3 ? ND : H>();
     else wait_vmcnt<0>();
   } else {
-    fetch(last, 0);
-    put(smem, 0);
-    put(smem, 1);
-    if (steps > 1) fetch(last, 1);
+    ops.begin(last, 0);
+#pragma unroll
+    for (int i = 0; i < NR; ++i) ops.fetch(last, 0, i);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) ops.put(smem, i);
+    if (steps > 1) {
+      ops.begin(last, 1);
+#pragma unroll
+      for (int i = 0; i < NR; ++i) ops.fetch(last, 1, i);
+    }
   }
   lds_done();
   barrier();
   Frag f[2];
-  frags(f[0], smem, 0);
+#pragma unroll
+  for (int x = 0; x < MI + 2; ++x) read(f[0], smem, 0, x);
   uint8_t* slot = smem;
+  uint8_t* before = smem + (SLOTS - 1) * W::SLOT;
   // HOT: enough steps follow, so the body has no branch
   auto step = [&](auto end, int s) {
     constexpr bool HOT = !decltype(end)::value;
     uint8_t* const next = slot == smem + (SLOTS - 1) * W::SLOT ? smem : slot + W::SLOT;
-    lds_done();
-    frags(f[1], slot, 1);
-    products(f[0]);
-    frags(f[0], slot, 2);
-    if (D == 0 && (HOT || s + 1 < steps)) put(next, 0);
-    products(f[1]);
-    frags(f[1], slot, 3);
-    if (D == 0 && (HOT || s + 1 < steps)) put(next, 1);
-    if (D == 0 && (HOT || s + 2 < steps)) fetch(end, s + 2);
-    products(f[0]);
-    // this wave's direct loads of the next step have landed, its tiles are
-    // written and it has read this step's fragments; then everyone
-    if (D > 0) {
-      if (D == 3 && (HOT || s + 2 < steps)) wait_vmcnt<ND>(); else wait_vmcnt<0>();
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      if (t == 3) {
+        // this wave's direct loads of the next step have landed, its tiles are
+        // written and it has read this step's fragments; then everyone
+        if (D > 0) {
+          if (D == 3 && (HOT || s + 2 < steps)) wait_vmcnt<ND>(); else wait_vmcnt<0>();
+        }
+        lds_done();
+        barrier();
+      }
+      if (D == 0 && t == 2 && (HOT || s + 2 < steps)) ops.begin(end, s + 2);
+      __builtin_amdgcn_sched_barrier(0);
+      // between the products, so that no queue fills up and stops them: the
+      // next fragments, and the loads and writes
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        const int i = m >> 1, j = m & 1;
+        acc[i][j] = product<uint16_t>(f[t & 1].b[j], f[t & 1].a[i], acc[i][j]);
+        auto share = [&](int n, auto one) {
+#pragma unroll
+          for (int x = n * m / M; x < n * (m + 1) / M; ++x) one(x);
+        };
+        if (t < 3) share(MI + 2, [&](int x) { read(f[(t + 1) & 1], slot, t + 1, x); });
+        else if (HOT || s + 1 < steps) share(MI + 2, [&](int x) { read(f[0], next, 0, x); });
+        if (D > 0) {
+          if (t == 0 && (HOT || s + D - 1 < steps))
+            share(ND - H, [&](int x) { ops.direct(end, s + D - 1, before, H + x); });
+          if (t == 3 && (HOT || s + D < steps))
+            share(H, [&](int x) { ops.direct(end, s + D, slot, x); });
+        } else {
+          if (t == 1 && (HOT || s + 1 < steps)) share(NP, [&](int x) { ops.put(next, x); });
+          if (t == 2 && (HOT || s + 2 < steps))
+            share(NR, [&](int x) { ops.fetch(end, s + 2, x); });
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
-    lds_done();
-    barrier();
-    if (D > 0 && (HOT || s + D < steps)) direct(end, s + D, slot);
-    if (HOT || s + 1 < steps) frags(f[0], next, 0);
-    products(f[1]);
+    before = slot;
     slot = next;
   };
   int s = 0;
@@ -547,56 +561,55 @@ __device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // load t of an operand brings rows 64 t + 8 wave + lane / 8 of its tile;
   // rows and columns past the end repeat others (not stored)
-  const uint16_t* const w = static_cast<const uint16_t*>(a.w) + it.e * a.w_se;
-  const int xk = ((lane & 7) ^ swz(8 * wave + (lane >> 3))) * 8;
-  const uint16_t* xp[MI];
-  const uint16_t* wp[4];
+  struct {
+    const ExpertArgs& a;
+    int wave, lane, n0, xk;
+    uint32_t at;
+    const uint16_t* w;
+    const uint16_t* xp[MI];
+    const uint16_t* wp[4];
+    u32x4 xv[MI];
+    Turn v;
+    __device__ __forceinline__ const uint16_t* along(bool last, const uint16_t* p, int s) const {
+      return !last || s * 64 + xk < a.K ? p + s * 64 : reinterpret_cast<const uint16_t*>(kZeros);
+    }
+    __device__ __forceinline__ void direct(bool last, int s, uint8_t* slot, int i) {
+      if (i < MI) to_lds<16>(along(last, xp[i], s), slot + (i * 8 + wave) * 1024);
+      else to_lds<16>(along(last, wp[i - MI], s), slot + W::A + ((i - MI) * 8 + wave) * 1024);
+    }
+    __device__ __forceinline__ void begin(bool, int) {}
+    __device__ __forceinline__ void fetch(bool last, int s, int i) {
+      if (i < MI) {
+        xv[i] = load_global<u32x4>(along(last, xp[i], s));
+      } else {
+        const int k = s * 64 + wave * 8 + i - MI;
+        const uint16_t* row = w + (int64_t)k * a.ldw + n0;
+        if (last) row = k < a.K ? row : reinterpret_cast<const uint16_t*>(kZeros);
+        v.row[i - MI] = load_global<u32x2>(reinterpret_cast<const uint8_t*>(row) + at);
+      }
+    }
+    __device__ __forceinline__ void put(uint8_t* slot, int i) {
+      if (i < MI) *reinterpret_cast<u32x4*>(slot + (i * 8 + wave) * 1024 + lane * 16) = xv[i];
+      else put_turned(v, slot + W::A, wave, i - MI);
+    }
+  } ops{a, wave, lane, n0, ((lane & 7) ^ swz(8 * wave + (lane >> 3))) * 8,
+        (uint32_t)min(4 * lane, a.N - 4 - n0) * 2,
+        static_cast<const uint16_t*>(a.w) + it.e * a.w_se, {}, {}, {}, {}};
 #pragma unroll
   for (int t = 0; t < MI; ++t) {
     const int s = max(slots[64 * t + 8 * wave + (lane >> 3)], 0);
-    xp[t] = static_cast<const uint16_t*>(a.x) + (int64_t)min(s / a.x_div, a.R - 1) * a.ldx + xk;
+    ops.xp[t] = static_cast<const uint16_t*>(a.x) + (int64_t)min(s / a.x_div, a.R - 1) * a.ldx +
+                ops.xk;
   }
   if constexpr (!W_ACROSS) {
 #pragma unroll
     for (int t = 0; t < 4; ++t)
-      wp[t] = w + (int64_t)min(n0 + 64 * t + 8 * wave + (lane >> 3), a.N - 1) * a.ldw + xk;
+      ops.wp[t] = ops.w + (int64_t)min(n0 + 64 * t + 8 * wave + (lane >> 3), a.N - 1) * a.ldw +
+                  ops.xk;
   }
-  const uint16_t* const zero = reinterpret_cast<const uint16_t*>(kZeros);
-  auto direct = [&](auto last, int s, uint8_t* slot) {
-    const bool in = !decltype(last)::value || s * 64 + xk < a.K;
-#pragma unroll
-    for (int t = 0; t < MI; ++t)
-      to_lds<16>(in ? xp[t] + s * 64 : zero, slot + (t * 8 + wave) * 1024);
-    if constexpr (!W_ACROSS) {
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-        to_lds<16>(in ? wp[t] + s * 64 : zero, slot + W::A + (t * 8 + wave) * 1024);
-    }
-  };
-  u32x4 xv[MI];
-  Turn v;
-  const uint32_t at = (uint32_t)min(4 * lane, a.N - 4 - n0) * 2;
-  auto fetch = [&](auto last, int s) {
-    const bool in = !decltype(last)::value || s * 64 + xk < a.K;
-#pragma unroll
-    for (int t = 0; t < MI; ++t) xv[t] = load_global<u32x4>(in ? xp[t] + s * 64 : zero);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int k = s * 64 + wave * 8 + i;
-      const uint16_t* row = w + (int64_t)k * a.ldw + n0;
-      if (decltype(last)::value) row = k < a.K ? row : zero;
-      v.row[i] = load_global<u32x2>(reinterpret_cast<const uint8_t*>(row) + at);
-    }
-  };
-  auto put = [&](uint8_t* slot, int h) {
-#pragma unroll
-    for (int t = h * MI / 2; t < (h + 1) * MI / 2; ++t)
-      *reinterpret_cast<u32x4*>(slot + (t * 8 + wave) * 1024 + lane * 16) = xv[t];
-    put_turned(v, slot + W::A, wave, h);
-  };
   f32x16 acc[MI][2] = {};
-  wide_products<MI, W_ACROSS ? 0 : W::DIRECT, false, W_ACROSS>(
-      smem, (int)(((unsigned)a.K + 63) / 64), acc, direct, fetch, put);
+  wide_products<MI, W_ACROSS ? 0 : W::DIRECT, false, W_ACROSS, MI + 8, MI + 4>(
+      smem, (int)(((unsigned)a.K + 63) / 64), acc, ops);
   const int wm = (wave >> 2) * W::ROWS, col = n0 + (wave & 3) * 64;
   const int size = a.out_dtype == BSMM_BF16 ? 2 : 4;
   uint8_t* const out = static_cast<uint8_t*>(a.out) + (int64_t)col * size;
@@ -660,46 +673,51 @@ __global__ void __launch_bounds__(512, 2) expert_wgrad_wide(WgradArgs a, int ntn
   const int e = item / ntn, n0 = item % ntn * 256, k0 = tk * kWide, lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lo = min(max(a.offsets[e], 0), a.S), hi = min(max(a.offsets[e + 1], lo), a.S);
-  const uint8_t* const zero = reinterpret_cast<const uint8_t*>(kZeros);
-  const uint8_t* const dy = static_cast<const uint8_t*>(a.dy) + n0 * 2;
-  const uint8_t* const x = static_cast<const uint8_t*>(a.x) + k0 * 2;
-  const uint32_t ay = (uint32_t)min(4 * lane, a.N - 4 - n0) * 2;
-  const uint32_t ax = (uint32_t)min(4 * lane, a.K - 4 - k0) * 2;
   // the wave's 8 positions of a step; lane i < 8 has the slot of the i-th
-  auto slot_of = [&](int s) {
-    return lo < hi ? slot_at(a.order, min(lo + s * 64 + wave * 8 + (lane & 7), hi - 1)) : 0;
-  };
-  int mine = slot_of(0);
-  Turn vy, vx;
-  auto fetch = [&](auto last, int s) {
-    const uint32_t slot = min(max(mine, 0), a.S - 1);
-    const int64_t oy = (int64_t)divide(slot, yd) * a.ldy * 2;
-    const int64_t ox = (int64_t)divide(slot, xd) * a.ldx * 2;
-    const int rows = decltype(last)::value ? hi - lo - s * 64 - wave * 8 : 8;
-    auto lane_of = [](int64_t v, int i) {
+  struct {
+    const WgradArgs& a;
+    Divisor yd, xd;
+    int wave, lane, lo, hi;
+    const uint8_t* dy;
+    const uint8_t* x;
+    uint32_t ay, ax;
+    int mine;
+    int64_t oy, ox;
+    int rows;
+    Turn vy, vx;
+    __device__ __forceinline__ int slot_of(int s) const {
+      return lo < hi ? slot_at(a.order, min(lo + s * 64 + wave * 8 + (lane & 7), hi - 1)) : 0;
+    }
+    __device__ __forceinline__ void direct(bool, int, uint8_t*, int) {}
+    __device__ __forceinline__ void begin(bool last, int s) {
+      const uint32_t slot = min(max(mine, 0), a.S - 1);
+      oy = (int64_t)divide(slot, yd) * a.ldy * 2;
+      ox = (int64_t)divide(slot, xd) * a.ldx * 2;
+      rows = last ? hi - lo - s * 64 - wave * 8 : 8;
+      mine = slot_of(s + 1);
+    }
+    static __device__ __forceinline__ int64_t lane_of(int64_t v, int i) {
       const uint32_t l = __builtin_amdgcn_readlane((int)v, i);
       return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), i) << 32 | l);
-    };
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint8_t* ry = dy + lane_of(oy, i);
-      const uint8_t* rx = x + lane_of(ox, i);
-      if (decltype(last)::value) {
-        ry = i < rows ? ry : zero;
-        rx = i < rows ? rx : zero;
-      }
-      vy.row[i] = load_global<u32x2>(ry + ay);
-      vx.row[i] = load_global<u32x2>(rx + ax);
     }
-    mine = slot_of(s + 1);
-  };
-  auto put_both = [&](uint8_t* slot, int h) {
-    put_turned(vy, slot, wave, h);
-    put_turned(vx, slot + W::A, wave, h);
-  };
+    // dy's rows, then x's
+    __device__ __forceinline__ void fetch(bool last, int, int i) {
+      const bool second = i >= 8;
+      const int r = i & 7;
+      const uint8_t* p = second ? x + lane_of(ox, r) : dy + lane_of(oy, r);
+      if (last) p = r < rows ? p : reinterpret_cast<const uint8_t*>(kZeros);
+      (second ? vx : vy).row[r] = load_global<u32x2>(p + (second ? ax : ay));
+    }
+    __device__ __forceinline__ void put(uint8_t* slot, int i) {
+      if (i < 4) put_turned(vy, slot, wave, i);
+      else put_turned(vx, slot + W::A, wave, i - 4);
+    }
+  } ops{a, yd, xd, wave, lane, lo, hi, static_cast<const uint8_t*>(a.dy) + n0 * 2,
+        static_cast<const uint8_t*>(a.x) + k0 * 2, (uint32_t)min(4 * lane, a.N - 4 - n0) * 2,
+        (uint32_t)min(4 * lane, a.K - 4 - k0) * 2, 0, 0, 0, 0, {}, {}};
+  ops.mine = ops.slot_of(0);
   f32x16 acc[4][2] = {};
-  wide_products<4, 0, true, true>(smem, (int)(((unsigned)(hi - lo) + 63) / 64), acc,
-                                  [](auto, int, uint8_t*) {}, fetch, put_both);
+  wide_products<4, 0, true, true, 16, 8>(smem, (int)(((unsigned)(hi - lo) + 63) / 64), acc, ops);
   const int row0 = n0 + (wave >> 2) * 128, col = k0 + (wave & 3) * 64;
   const int size = a.out_dtype == BSMM_BF16 ? 2 : 4;
   uint8_t* const out = static_cast<uint8_t*>(a.dw) + (e * a.w_se + col) * size;
