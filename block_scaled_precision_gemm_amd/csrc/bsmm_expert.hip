@@ -350,15 +350,13 @@ __device__ __forceinline__ int turned_off(int r, int c) {
 template <int MI> struct Wide {
   static constexpr int BM = 64 * MI, ROWS = 32 * MI;   // of the tile, of a wave
   static constexpr int A = BM * 128, B = kWide * 128;  // bytes of a step's tiles
-  static constexpr int SLOT = A + B;
-  static constexpr int DIRECT = 156 * 1024 / SLOT > 3 ? 3 : 156 * 1024 / SLOT;   // slots
-  static constexpr int LA = MI, LB = 4;                // loads of a wave and step
+  // slots of the rows' and the columns' tiles where loads are direct (through
+  // registers 2 each): the weights come from HBM, so they get three
+  static constexpr int DA = MI > 2 ? 2 : 3, DB = 3;
 };
-constexpr int kWideSlots = 2 * Wide<4>::SLOT;   // the ring's bytes at most: the rows' slots
-                                                // and scales stand behind it
-static_assert(3 * Wide<2>::SLOT > kWideSlots, "");
-constexpr int kWideRing = 3 * Wide<2>::SLOT;
-constexpr int kWideBytes = kWideRing + 2 * 256 * 4;
+constexpr int kWideBytes = 2 * Wide<4>::A + 3 * Wide<4>::B;      // all of the CU's 160 KB
+constexpr int kWidePitch = 64 * 4 + 16;         // of a row of results in LDS
+constexpr int kWideStage = 8 * 32 * kWidePitch; // the waves' results; the rows' slots follow
 
 __device__ __forceinline__ void lds_done() {
   __builtin_amdgcn_s_waitcnt(0xC07F);           // lgkmcnt(0), in the compiler's count too
@@ -376,50 +374,55 @@ __device__ __forceinline__ void put_turned(const Turn& v, uint8_t* tile, int oct
   *reinterpret_cast<u32x4*>(tile + turned_off(4 * (threadIdx.x & 63) + c, octet)) = o;
 }
 
-// The products of one tile.  D > 0: ops.direct(last, s, slot, i) issues load i
-// of a wave's MI + 4 direct loads of step s into one of D slots.  D = 0:
+// The products of one tile.  DIRECT: ops.direct_a(last, s, slot, i) and
+// direct_b issue load i of a wave's MI and 4 direct loads of step s.  Else
 // ops.fetch(last, s, i) issues load i of NR to registers (ops.begin(last, s)
-// before the first), ops.put(slot, i) writes part i of NP of them.  last:
+// before the first), ops.put(a, b, i) writes part i of NP of them.  last:
 // whether s may be the last step, which may end early.
 //
 // The fragments enter the instruction exchanged: a lane's 16 results of a
 // block are 4 x 4 neighbouring columns of one row.
-template <int MI, int D, bool A_TURNED, bool B_TURNED, int NR, int NP, typename Ops>
+template <int MI, bool DIRECT, bool A_TURNED, bool B_TURNED, int NR, int NP, typename Ops>
 __device__ __forceinline__ void wide_products(uint8_t* smem, int steps, f32x16 (&acc)[MI][2],
                                               Ops& ops) {
   using W = Wide<MI>;
-  constexpr int SLOTS = D > 0 ? D : 2, ND = MI + 4, M = 2 * MI;
+  constexpr int DA = DIRECT ? W::DA : 2, DB = DIRECT ? W::DB : 2, M = 2 * MI;
+  uint8_t* const bs = smem + DA * W::A;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm = (wave >> 2) * W::ROWS, wn = (wave & 3) * 64;
   struct Frag { u32x4 a[MI], b[2]; };
   // fragment x of turn t: the two of the columns, then those of the rows
-  auto read = [&](Frag& f, const uint8_t* slot, int t, int x) {
+  auto read = [&](Frag& f, const uint8_t* at, const uint8_t* bt, int t, int x) {
     const int c = 2 * t + (lane >> 5), r = lane & 31;
     if (x < 2)
       f.b[x] = *reinterpret_cast<const u32x4*>(
-          slot + W::A + (wn + 32 * x) * 128 + (B_TURNED ? turned_off(r, c) : lds_off(r, c)));
+          bt + (wn + 32 * x) * 128 + (B_TURNED ? turned_off(r, c) : lds_off(r, c)));
     else
       f.a[x - 2] = *reinterpret_cast<const u32x4*>(
-          slot + (wm + 32 * (x - 2)) * 128 + (A_TURNED ? turned_off(r, c) : lds_off(r, c)));
+          at + (wm + 32 * (x - 2)) * 128 + (A_TURNED ? turned_off(r, c) : lds_off(r, c)));
   };
   if (steps == 0) return;
   constexpr std::true_type last{};
-  constexpr int H = ND / 2;             // direct loads of a step's first half
-  if constexpr (D > 0) {
+  if constexpr (DIRECT) {
+    // in the order of the loop: the rows' tile of a step before the columns'
 #pragma unroll
-    for (int s = 0; s < D; ++s)
+    for (int s = 0; s < DA; ++s) {
+      if (s >= steps) break;
 #pragma unroll
-      for (int i = 0; i < (s < D - 1 ? ND : H); ++i)
-        if (s < steps) ops.direct(last, s, smem + s * W::SLOT, i);
-    if (D == 3 && steps > 2) wait_vmcnt<ND + H>();
-    else if (steps > 1) wait_vmcnt<D == 3 ? ND : H>();
+      for (int i = 0; i < MI; ++i) ops.direct_a(last, s, smem + s * W::A, i);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (s < 2) ops.direct_b(last, s, bs + s * W::B, i);
+    }
+    if (DA == 3 && steps > 2) wait_vmcnt<2 * MI + 4>();
+    else if (steps > 1) wait_vmcnt<MI + 4>();
     else wait_vmcnt<0>();
   } else {
     ops.begin(last, 0);
 #pragma unroll
     for (int i = 0; i < NR; ++i) ops.fetch(last, 0, i);
 #pragma unroll
-    for (int i = 0; i < NP; ++i) ops.put(smem, i);
+    for (int i = 0; i < NP; ++i) ops.put(smem, bs, i);
     if (steps > 1) {
       ops.begin(last, 1);
 #pragma unroll
@@ -430,25 +433,28 @@ __device__ __forceinline__ void wide_products(uint8_t* smem, int steps, f32x16 (
   barrier();
   Frag f[2];
 #pragma unroll
-  for (int x = 0; x < MI + 2; ++x) read(f[0], smem, 0, x);
-  uint8_t* slot = smem;
-  uint8_t* before = smem + (SLOTS - 1) * W::SLOT;
+  for (int x = 0; x < MI + 2; ++x) read(f[0], smem, bs, 0, x);
+  // this step's slots, and the columns' one of the step before
+  uint8_t* at = smem;
+  uint8_t* bt = bs;
+  uint8_t* old = bs + (DB - 1) * W::B;
   // HOT: enough steps follow, so the body has no branch
   auto step = [&](auto end, int s) {
     constexpr bool HOT = !decltype(end)::value;
-    uint8_t* const next = slot == smem + (SLOTS - 1) * W::SLOT ? smem : slot + W::SLOT;
+    uint8_t* const an = at == smem + (DA - 1) * W::A ? smem : at + W::A;
+    uint8_t* const bn = bt == bs + (DB - 1) * W::B ? bs : bt + W::B;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       if (t == 3) {
         // this wave's direct loads of the next step have landed, its tiles are
         // written and it has read this step's fragments; then everyone
-        if (D > 0) {
-          if (D == 3 && (HOT || s + 2 < steps)) wait_vmcnt<ND>(); else wait_vmcnt<0>();
+        if (DIRECT) {
+          if (HOT || s + 2 < steps) wait_vmcnt<DA == 3 ? MI + 4 : 4>(); else wait_vmcnt<0>();
         }
         lds_done();
         barrier();
       }
-      if (D == 0 && t == 2 && (HOT || s + 2 < steps)) ops.begin(end, s + 2);
+      if (!DIRECT && t == 2 && (HOT || s + 2 < steps)) ops.begin(end, s + 2);
       __builtin_amdgcn_sched_barrier(0);
       // between the products, so that no queue fills up and stops them: the
       // next fragments, and the loads and writes
@@ -460,27 +466,28 @@ __device__ __forceinline__ void wide_products(uint8_t* smem, int steps, f32x16 (
 #pragma unroll
           for (int x = n * m / M; x < n * (m + 1) / M; ++x) one(x);
         };
-        if (t < 3) share(MI + 2, [&](int x) { read(f[(t + 1) & 1], slot, t + 1, x); });
-        else if (HOT || s + 1 < steps) share(MI + 2, [&](int x) { read(f[0], next, 0, x); });
-        if (D > 0) {
-          if (t == 0 && (HOT || s + D - 1 < steps))
-            share(ND - H, [&](int x) { ops.direct(end, s + D - 1, before, H + x); });
-          if (t == 3 && (HOT || s + D < steps))
-            share(H, [&](int x) { ops.direct(end, s + D, slot, x); });
+        if (t < 3) share(MI + 2, [&](int x) { read(f[(t + 1) & 1], at, bt, t + 1, x); });
+        else if (HOT || s + 1 < steps) share(MI + 2, [&](int x) { read(f[0], an, bn, 0, x); });
+        if (DIRECT) {
+          if (t == 0 && (HOT || s + 2 < steps))
+            share(4, [&](int x) { ops.direct_b(end, s + 2, old, x); });
+          if (t == 3 && (HOT || s + DA < steps))
+            share(MI, [&](int x) { ops.direct_a(end, s + DA, at, x); });
         } else {
-          if (t == 1 && (HOT || s + 1 < steps)) share(NP, [&](int x) { ops.put(next, x); });
+          if (t == 1 && (HOT || s + 1 < steps)) share(NP, [&](int x) { ops.put(an, bn, x); });
           if (t == 2 && (HOT || s + 2 < steps))
             share(NR, [&](int x) { ops.fetch(end, s + 2, x); });
         }
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    before = slot;
-    slot = next;
+    old = bt;
+    at = an;
+    bt = bn;
   };
   int s = 0;
 #pragma unroll 1
-  for (; s + SLOTS + 1 < steps; ++s) step(std::false_type{}, s);
+  for (; s + 4 < steps; ++s) step(std::false_type{}, s);
 #pragma unroll 1
   for (; s < steps; ++s) step(last, s);
 }
@@ -488,15 +495,16 @@ __device__ __forceinline__ void wide_products(uint8_t* smem, int steps, f32x16 (
 // A wave's 32 MI x 64 results to memory, a block of 32 rows at a time through
 // LDS, so that a store covers whole runs of a row.  row(m): the address of
 // column 0 of the wave's row m (null: not stored), scale(m) its factor; cols:
-// the columns from there to the end; vec: rows 16-byte aligned there.
+// the columns from there to the end; vec: rows 16-byte aligned there.  The
+// stores pass the caches by: they would push out what the next tiles read
+// (4096 tokens x 8 of 32 experts, fp32 gradients of 2048 x 4096: 810 -> 767 us).
 template <int MI, typename Row, typename Scale>
 __device__ __forceinline__ void wide_store(uint8_t* smem, const f32x16 (&acc)[MI][2],
                                            bsmm_dtype dt, int cols, bool vec, const Row& row,
                                            const Scale& scale) {
-  constexpr int PITCH = 64 * 4 + 16;                   // reads and writes without conflicts
+  constexpr int PITCH = kWidePitch;                    // reads and writes without conflicts
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   uint8_t* const part = smem + wave * (32 * PITCH);
-  barrier();                                           // nobody reads the ring any more
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
 #pragma unroll
@@ -522,7 +530,7 @@ __device__ __forceinline__ void wide_store(uint8_t* smem, const f32x16 (&acc)[MI
           o[1] = bf16_pair(v[2], v[3]);
           o[2] = bf16_pair(w[0], w[1]);
           o[3] = bf16_pair(w[2], w[3]);
-          *reinterpret_cast<u32x4*>(to + c * 2) = o;
+          __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(to + c * 2));
         } else {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
@@ -540,7 +548,7 @@ __device__ __forceinline__ void wide_store(uint8_t* smem, const f32x16 (&acc)[MI
         uint8_t* const to = static_cast<uint8_t*>(row(32 * i + m));
         if (to == nullptr) continue;
         if (vec && c + 4 <= cols) {
-          *reinterpret_cast<f32x4*>(to + c * 4) = v;
+          __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(to + c * 4));
         } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -551,12 +559,26 @@ __device__ __forceinline__ void wide_store(uint8_t* smem, const f32x16 (&acc)[MI
   }
 }
 
+// The slots (-1: not stored) and scales of an item's rows.
+__device__ __forceinline__ void item_slots(const ExpertArgs& a, const Item& it, int rows,
+                                           int* slots, float* scales) {
+  const int r = threadIdx.x;
+  if (r >= rows) return;
+  const int s = r < it.rows ? slot_at(a.order, it.p0 + r) : -1;
+  const bool in = s >= 0 && s < a.S;
+  slots[r] = in ? s : -1;
+  scales[r] = in && a.row_scale ? a.row_scale[s] : 1.0f;
+}
+
 // An item of at most 64 MI rows from column n0.
 template <int MI, bool W_ACROSS>
 __device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& it, int n0,
-                                               uint8_t* smem, const int* slots,
-                                               const float* scales, bool vec) {
+                                               uint8_t* smem, bool vec) {
   using W = Wide<MI>;
+  int* const slots = reinterpret_cast<int*>(smem + kWideStage);
+  float* const scales = reinterpret_cast<float*>(slots + 256);
+  item_slots(a, it, 64 * MI, slots, scales);
+  __syncthreads();
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // load t of an operand brings rows 64 t + 8 wave + lane / 8 of its tile;
@@ -573,9 +595,11 @@ __device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& 
     __device__ __forceinline__ const uint16_t* along(bool last, const uint16_t* p, int s) const {
       return !last || s * 64 + xk < a.K ? p + s * 64 : reinterpret_cast<const uint16_t*>(kZeros);
     }
-    __device__ __forceinline__ void direct(bool last, int s, uint8_t* slot, int i) {
-      if (i < MI) to_lds<16>(along(last, xp[i], s), slot + (i * 8 + wave) * 1024);
-      else to_lds<16>(along(last, wp[i - MI], s), slot + W::A + ((i - MI) * 8 + wave) * 1024);
+    __device__ __forceinline__ void direct_a(bool last, int s, uint8_t* slot, int i) {
+      to_lds<16>(along(last, xp[i], s), slot + (i * 8 + wave) * 1024);
+    }
+    __device__ __forceinline__ void direct_b(bool last, int s, uint8_t* slot, int i) {
+      to_lds<16>(along(last, wp[i], s), slot + (i * 8 + wave) * 1024);
     }
     __device__ __forceinline__ void begin(bool, int) {}
     __device__ __forceinline__ void fetch(bool last, int s, int i) {
@@ -588,9 +612,9 @@ __device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& 
         v.row[i - MI] = load_global<u32x2>(reinterpret_cast<const uint8_t*>(row) + at);
       }
     }
-    __device__ __forceinline__ void put(uint8_t* slot, int i) {
-      if (i < MI) *reinterpret_cast<u32x4*>(slot + (i * 8 + wave) * 1024 + lane * 16) = xv[i];
-      else put_turned(v, slot + W::A, wave, i - MI);
+    __device__ __forceinline__ void put(uint8_t* at, uint8_t* bt, int i) {
+      if (i < MI) *reinterpret_cast<u32x4*>(at + (i * 8 + wave) * 1024 + lane * 16) = xv[i];
+      else put_turned(v, bt, wave, i - MI);
     }
   } ops{a, wave, lane, n0, ((lane & 7) ^ swz(8 * wave + (lane >> 3))) * 8,
         (uint32_t)min(4 * lane, a.N - 4 - n0) * 2,
@@ -607,9 +631,13 @@ __device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& 
       ops.wp[t] = ops.w + (int64_t)min(n0 + 64 * t + 8 * wave + (lane >> 3), a.N - 1) * a.ldw +
                   ops.xk;
   }
+  __syncthreads();                      // the slots have been read
   f32x16 acc[MI][2] = {};
-  wide_products<MI, W_ACROSS ? 0 : W::DIRECT, false, W_ACROSS, MI + 8, MI + 4>(
+  wide_products<MI, !W_ACROSS, false, W_ACROSS, MI + 8, MI + 4>(
       smem, (int)(((unsigned)a.K + 63) / 64), acc, ops);
+  barrier();                            // nobody reads the tiles any more
+  item_slots(a, it, 64 * MI, slots, scales);
+  __syncthreads();
   const int wm = (wave >> 2) * W::ROWS, col = n0 + (wave & 3) * 64;
   const int size = a.out_dtype == BSMM_BF16 ? 2 : 4;
   uint8_t* const out = static_cast<uint8_t*>(a.out) + (int64_t)col * size;
@@ -624,37 +652,30 @@ __device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& 
 
 template <bool W_ACROSS>
 __global__ void __launch_bounds__(512, 2) expert_mm_wide(ExpertArgs a, int items, int ntn,
-                                                         int vec) {
+                                                         int group, int vec) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-  int* const slots = reinterpret_cast<int*>(smem + kWideRing);
-  float* const scales = reinterpret_cast<float*>(slots + 256);
   int item, tn;
-  tile_of(items, ntn, item, tn);
+  tile_of(items, ntn, item, tn, group);
   const Item it = find_item(a.offsets, a.E, a.S, 256, item);
   const int n0 = tn * kWide;
+  // zero rows for the slots of no expert, a wave to a row
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const unsigned used = min(max(a.offsets[a.E], 0), a.S);
-  for (unsigned p = used + item; p < (unsigned)a.S; p += items) {    // both below 2^31
+  for (unsigned p = used + item * 8 + wave; p < (unsigned)a.S; p += items * 8) {
     const int slot = slot_at(a.order, p);
-    if (slot >= 0 && slot < a.S && (int)threadIdx.x < min(kWide, a.N - n0))
-      put(a.out, a.out_dtype, slot * a.ldo + n0 + threadIdx.x, 0.0f);
+    if (slot < 0 || slot >= a.S) continue;
+#pragma unroll
+    for (int c = threadIdx.x & 63; c < kWide; c += 64)
+      if (n0 + c < a.N) put(a.out, a.out_dtype, slot * a.ldo + n0 + c, 0.0f);
   }
   if (it.rows == 0) return;
-  // the rows' slots (-1: not stored) and scales
-  if (threadIdx.x < 256) {
-    const int r = threadIdx.x;
-    const int s = r < it.rows ? slot_at(a.order, it.p0 + r) : -1;
-    const bool in = s >= 0 && s < a.S;
-    slots[r] = in ? s : -1;
-    scales[r] = in && a.row_scale ? a.row_scale[s] : 1.0f;
-  }
-  __syncthreads();
   // only as many rows as there are, to 64: an expert's last item would
   // multiply 128 empty rows on average
   const int mi = (it.rows + 63) / 64;
-  if (mi == 4) expert_mm_item<4, W_ACROSS>(a, it, n0, smem, slots, scales, vec);
-  else if (mi == 3) expert_mm_item<3, W_ACROSS>(a, it, n0, smem, slots, scales, vec);
-  else if (mi == 2) expert_mm_item<2, W_ACROSS>(a, it, n0, smem, slots, scales, vec);
-  else expert_mm_item<1, W_ACROSS>(a, it, n0, smem, slots, scales, vec);
+  if (mi == 4) expert_mm_item<4, W_ACROSS>(a, it, n0, smem, vec);
+  else if (mi == 3) expert_mm_item<3, W_ACROSS>(a, it, n0, smem, vec);
+  else if (mi == 2) expert_mm_item<2, W_ACROSS>(a, it, n0, smem, vec);
+  else expert_mm_item<1, W_ACROSS>(a, it, n0, smem, vec);
 }
 
 // n / d for 0 <= n < 2^31 (Granlund and Montgomery, "Division by invariant
@@ -666,7 +687,6 @@ __device__ __forceinline__ uint32_t divide(uint32_t n, Divisor d) {
 
 __global__ void __launch_bounds__(512, 2) expert_wgrad_wide(WgradArgs a, int ntn, int ntk,
                                                             Divisor yd, Divisor xd, int vec) {
-  using W = Wide<4>;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   int item, tk;
   tile_of(a.E * ntn, ntk, item, tk);
@@ -688,7 +708,8 @@ __global__ void __launch_bounds__(512, 2) expert_wgrad_wide(WgradArgs a, int ntn
     __device__ __forceinline__ int slot_of(int s) const {
       return lo < hi ? slot_at(a.order, min(lo + s * 64 + wave * 8 + (lane & 7), hi - 1)) : 0;
     }
-    __device__ __forceinline__ void direct(bool, int, uint8_t*, int) {}
+    __device__ __forceinline__ void direct_a(bool, int, uint8_t*, int) {}
+    __device__ __forceinline__ void direct_b(bool, int, uint8_t*, int) {}
     __device__ __forceinline__ void begin(bool last, int s) {
       const uint32_t slot = min(max(mine, 0), a.S - 1);
       oy = (int64_t)divide(slot, yd) * a.ldy * 2;
@@ -708,16 +729,17 @@ __global__ void __launch_bounds__(512, 2) expert_wgrad_wide(WgradArgs a, int ntn
       if (last) p = r < rows ? p : reinterpret_cast<const uint8_t*>(kZeros);
       (second ? vx : vy).row[r] = load_global<u32x2>(p + (second ? ax : ay));
     }
-    __device__ __forceinline__ void put(uint8_t* slot, int i) {
-      if (i < 4) put_turned(vy, slot, wave, i);
-      else put_turned(vx, slot + W::A, wave, i - 4);
+    __device__ __forceinline__ void put(uint8_t* at, uint8_t* bt, int i) {
+      if (i < 4) put_turned(vy, at, wave, i);
+      else put_turned(vx, bt, wave, i - 4);
     }
   } ops{a, yd, xd, wave, lane, lo, hi, static_cast<const uint8_t*>(a.dy) + n0 * 2,
         static_cast<const uint8_t*>(a.x) + k0 * 2, (uint32_t)min(4 * lane, a.N - 4 - n0) * 2,
         (uint32_t)min(4 * lane, a.K - 4 - k0) * 2, 0, 0, 0, 0, {}, {}};
   ops.mine = ops.slot_of(0);
   f32x16 acc[4][2] = {};
-  wide_products<4, 0, true, true, 16, 8>(smem, (int)(((unsigned)(hi - lo) + 63) / 64), acc, ops);
+  wide_products<4, false, true, true, 16, 8>(smem, (int)(((unsigned)(hi - lo) + 63) / 64), acc, ops);
+  barrier();                            // nobody reads the tiles any more
   const int row0 = n0 + (wave >> 2) * 128, col = k0 + (wave & 3) * 64;
   const int size = a.out_dtype == BSMM_BF16 ? 2 : 4;
   uint8_t* const out = static_cast<uint8_t*>(a.dw) + (e * a.w_se + col) * size;
@@ -907,8 +929,8 @@ void launch_mm(const ExpertArgs& a, hipStream_t st) {
     const int64_t act = a.E < a.S ? a.E : a.S;
     const int items = (int)((a.S + act * 255) / 256), ntn = (a.N + kWide - 1) / kWide;
     const int vec = (uintptr_t)a.out % 16 == 0 && a.ldo % (a.out_dtype == BSMM_BF16 ? 8 : 4) == 0;
-    if (a.w_across) hipLaunchKernelGGL((expert_mm_wide<true>), dim3((unsigned)(items * ntn)), dim3(512), kWideBytes, st, a, items, ntn, vec);
-    else hipLaunchKernelGGL((expert_mm_wide<false>), dim3((unsigned)(items * ntn)), dim3(512), kWideBytes, st, a, items, ntn, vec);
+    if (a.w_across) hipLaunchKernelGGL((expert_mm_wide<true>), dim3((unsigned)(items * ntn)), dim3(512), kWideBytes, st, a, items, ntn, 4, vec);
+    else hipLaunchKernelGGL((expert_mm_wide<false>), dim3((unsigned)(items * ntn)), dim3(512), kWideBytes, st, a, items, ntn, 4, vec);
     return;
   }
   const int64_t act = a.E < a.S ? a.E : a.S;
