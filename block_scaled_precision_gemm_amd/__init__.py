@@ -25,7 +25,7 @@ __all__ = [
     "bsmm_quant_w4", "bsmm_w4_mm", "bsmm_w4_expert_mm",
     "bsmm_expert_mm", "bsmm_expert_wgrad",
     "bsmm_quant_int8_mx", "bsmm_swiglu", "bsmm_swiglu_backward",
-    "bsmm_expert_wgrad_workspace_bytes",
+    "bsmm_expert_mm_workspace_bytes", "bsmm_expert_wgrad_workspace_bytes",
     "bsmm_route_topk", "bsmm_route_topk_backward", "Route",
     "bsmm_w4_workspace_bytes", "bsmm_w4_plan_name", "bsmm_route_workspace_bytes",
     "bsmm_workspace_bytes", "bsmm_query_plan", "bsmm_set_override", "bsmm_set_override_tail", "bsmm_set_streamk_grid", "bsmm_mfma_probe",
@@ -115,7 +115,9 @@ def load():
                                  i64, i64, i64, i64, vp, sz, vp]
     L.bsmm_expert_wgrad.argtypes = [vp, i64, st, st, vp, i64, st, vp, i64, vp, vp, vp, i64, i64,
                                     st, i64, i64, i64, i64, i64, i64, vp, sz, vp]
-    L.bsmm_expert_wgrad_workspace_bytes.argtypes = [st, st, i64, i64]
+    L.bsmm_expert_mm_workspace_bytes.argtypes = [st, st, i64, i64, i64, i64]
+    L.bsmm_expert_mm_workspace_bytes.restype = sz
+    L.bsmm_expert_wgrad_workspace_bytes.argtypes = [st, st, i64, i64, i64, i64, i64]
     L.bsmm_expert_wgrad_workspace_bytes.restype = sz
     L.bsmm_quant_int8_mx.argtypes = [vp, i64, st, vp, i64, vp, i64, vp, i64, i64, i64, vp]
     L.bsmm_swiglu.argtypes = [vp, i64, st, vp, i64, vp, i64, vp, i64, i64, i64, vp]
@@ -1103,7 +1105,7 @@ def _row_stride(t, shape, stride, name):
 
 
 def bsmm_expert_mm(x, w, order, offsets, *, slots_per_row=1, row_scale=None, out_dtype="bf16",
-                   out=None, stream=None):
+                   out=None, workspace=None, stream=None):
     """Routed rows times their experts' weights.
 
     x: bf16 or fp32 [R, K].  w: [E, N, K] of x's type, contiguous along its
@@ -1112,7 +1114,9 @@ def bsmm_expert_mm(x, w, order, offsets, *, slots_per_row=1, row_scale=None, out
     order: int32 [S] and offsets: int32 [E + 1] as bsmm_route_topk returns
     them; order None: the slots are sorted (S = R * slots_per_row).  Slot s
     reads row s // slots_per_row of x.  row_scale: fp32 [S] or None.  Returns
-    [S, N] in slot order, zeros for slots without an expert.
+    [S, N] in slot order, zeros for slots without an expert.  workspace: None
+    for a cached one, False for none, or a 16-byte aligned tensor of
+    bsmm_expert_mm_workspace_bytes bytes.
     """
     xs, ws = x.shape, w.shape
     if len(ws) != 3:
@@ -1139,12 +1143,23 @@ def bsmm_expert_mm(x, w, order, offsets, *, slots_per_row=1, row_scale=None, out
     if row_scale is not None and (row_scale.dtype is not f32 or row_scale.numel() != S or
                                   not row_scale.is_contiguous()):
         raise ValueError(f"row_scale must be contiguous fp32 of {S} elements")
-    _one_gpu("x, w, order, offsets, row_scale and out", x, w, order, offsets, row_scale, out)
+    _one_gpu("x, w, order, offsets, row_scale, out and workspace", x, w, order, offsets, row_scale,
+             out, None if workspace is False else workspace)
     o, ldo = _w4_out(out, S, N, code, torch, dtypes, x.device)
+    hs = _stream_of(x, stream)
+    if workspace is None:
+        key = ("expert_mm", xc, sk == 1, E, S, N, K)
+        need = _WS_NEED.get(key)
+        if need is None:
+            need = _WS_NEED[key] = load().bsmm_expert_mm_workspace_bytes(
+                xc, 0 if sk == 1 else 1, E, S, N, K)
+        wsp, wsn = _buffer(need, x.device, stream, hs)
+    else:
+        wsp, wsn = _given(workspace)
     status = load().bsmm_expert_mm(
         x.data_ptr(), ldx, w.data_ptr(), se if E > 1 else 0, sn, sk, xc, op, offsets.data_ptr(),
         slots_per_row, None if row_scale is None else row_scale.data_ptr(), o.data_ptr(), ldo,
-        code, E, R, S, N, K, None, 0, _stream_of(x, stream))
+        code, E, R, S, N, K, wsp, wsn, hs)
     if status:
         _check(status)
     return o
@@ -1160,9 +1175,8 @@ def bsmm_expert_wgrad(dy, x, order, offsets, *, x_scale=None, dy_slots_per_row=1
     offsets: int32 [E + 1] as bsmm_route_topk returns them; order None: the
     slots are sorted (S = Ry * dy_slots_per_row), and with offsets [0, S] this
     is a dense layer's gradient.  Returns [E, N, K], zeros for experts without
-    slots.  workspace (a checkpoint with bf16 dy): None for a cached one, False
-    for none, or a 16-byte aligned tensor of bsmm_expert_wgrad_workspace_bytes
-    bytes.
+    slots.  workspace: None for a cached one, False for none, or a 16-byte
+    aligned tensor of bsmm_expert_wgrad_workspace_bytes bytes.
     """
     yc = _float_code(dy.dtype, "dy")
     code = _float_code(out_dtype, "out_dtype")
@@ -1204,12 +1218,15 @@ def bsmm_expert_wgrad(dy, x, order, offsets, *, x_scale=None, dy_slots_per_row=1
             raise ValueError("out must be contiguous along its last dimension")
         ldw = ldw if N > 1 else K
     hs = _stream_of(dy, stream)
-    wsp, wsn = None, 0
-    if workspace is not None:
+    if workspace is None:
+        key = ("expert_wgrad", yc, sp is None, E, Rx, S, N, K)
+        need = _WS_NEED.get(key)
+        if need is None:
+            need = _WS_NEED[key] = load().bsmm_expert_wgrad_workspace_bytes(
+                yc, 0 if sp is None else 1, E, Rx, S, N, K)
+        wsp, wsn = _buffer(need, dy.device, stream, hs)
+    else:
         wsp, wsn = _given(workspace)
-    elif sp is not None:
-        wsp, wsn = _buffer(load().bsmm_expert_wgrad_workspace_bytes(yc, 1, Rx, K), dy.device,
-                           stream, hs)
     status = load().bsmm_expert_wgrad(
         dy.data_ptr(), ldy, yc, dy_slots_per_row, x.data_ptr(), ldx, x_slots_per_row, sp, s_r, op,
         offsets.data_ptr(), o.data_ptr(), se if E > 1 else 0, ldw, code, E, Ry, Rx, S, N, K, wsp,
@@ -1462,10 +1479,16 @@ def bsmm_w4_plan_name(x_dtype, routed, E, R, S, N, K, group):
     return name and name.decode()
 
 
-def bsmm_expert_wgrad_workspace_bytes(dtype, checkpoint, Rx, K):
+def bsmm_expert_mm_workspace_bytes(dtype, transposed, E, S, N, K):
+    """Workspace bytes bsmm_expert_mm wants (transposed: w is contiguous along N)."""
+    return load().bsmm_expert_mm_workspace_bytes(_float_code(dtype, "dtype"),
+                                                 1 if transposed else 0, E, S, N, K)
+
+
+def bsmm_expert_wgrad_workspace_bytes(dtype, checkpoint, E, Rx, S, N, K):
     """Workspace bytes bsmm_expert_wgrad wants for dy of ``dtype`` and x [Rx, K]."""
     return load().bsmm_expert_wgrad_workspace_bytes(_float_code(dtype, "dtype"),
-                                                    1 if checkpoint else 0, Rx, K)
+                                                    1 if checkpoint else 0, E, Rx, S, N, K)
 
 
 def bsmm_route_workspace_bytes(T, E):

@@ -12,20 +12,20 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
-#include <cstdlib>
 #include <type_traits>
 
+#include "bsmm_check.h"
 #include "bsmm_internal.h"
 #include "bsmm_routed.h"
 
 namespace bsmm {
 namespace {
 
-// A tile of an operand in LDS is 128 bytes of the contraction (kStep
-// elements) for 128 rows or columns of the output.  Two layouts, as the
-// operand lies in memory:
+// A tile of an operand in LDS is 128 bytes of the contraction (STEP elements)
+// for 64 MB rows or columns of the output.  Two layouts, as the operand lies
+// in memory:
 //   along   rows of 128 bytes, the contraction inside a row
-//   across  a row for every element of the contraction, 128 elements long
+//   across  a row for every element of the contraction, 64 MB elements long
 // The 16-byte units of a row are exchanged by XOR so that a fragment's reads
 // spread over the banks.
 template <typename T> struct Elem;
@@ -35,26 +35,32 @@ template <> struct Elem<uint16_t> {       // bf16 bits
 template <> struct Elem<float> {
   static constexpr int U = 4, STEP = 32;
 };
-constexpr int kTile = 128;                      // rows and columns of a tile
-constexpr int kTileBytes = kTile * 128;
 
-template <typename T>
+// Byte offset of unit u of row k in an `across` tile.
+template <typename T, int MB>
 __device__ __forceinline__ int across_off(int k, int u) {
-  if constexpr (sizeof(T) == 2) return k * 256 + ((u ^ ((k & 3) << 2 | ((k >> 3) & 1) << 1)) << 4);
-  else return k * 512 + ((u ^ ((k >> 2) & 1) << 3) << 4);
+  constexpr int ROW = 64 * MB * sizeof(T), UNITS = ROW / 16;
+  if constexpr (sizeof(T) == 2)
+    return k * ROW + (((u ^ ((k & 3) << 2 | ((k >> 3) & 1) << 1)) & (UNITS - 1)) << 4);
+  else
+    return k * ROW + ((u ^ (((k >> 2) & 1) << 3)) << 4);
 }
 
 // A unit's worth of elements at p, `left` of them inside the operand (the
-// others 0).  VEC: p is 16-byte aligned.
-template <typename T, bool VEC>
+// others 0).  One load whatever the address: the hardware takes any that is
+// aligned to the element.
+template <typename T>
 __device__ __forceinline__ u32x4 fetch(const T* p, int left) {
   constexpr int U = Elem<T>::U;
-  if (VEC && left >= U) return *reinterpret_cast<const u32x4*>(p);
-  T e[U];
+  u32x4 v = {0, 0, 0, 0};
+  if (left >= U) {
+    __builtin_memcpy(&v, p, 16);
+  } else if (left > 0) {
+    T e[U];
 #pragma unroll
-  for (int i = 0; i < U; ++i) e[i] = i < left ? p[i] : T(0);
-  u32x4 v;
-  __builtin_memcpy(&v, e, 16);
+    for (int i = 0; i < U; ++i) e[i] = i < left ? p[i] : T(0);
+    __builtin_memcpy(&v, e, 16);
+  }
   return v;
 }
 
@@ -98,20 +104,20 @@ __device__ __forceinline__ uint2 read_transposed(const uint8_t* p) {
   return __builtin_bit_cast(
       uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(uintptr_t)(uint32_t)(uintptr_t)p));
 }
-template <typename T>
+template <typename T, int MB>
 __device__ __forceinline__ u32x4 frag_across(const uint8_t* tile, int c0, int t) {
   const int lane = threadIdx.x & 63, half = lane >> 5;
   if constexpr (sizeof(T) == 2) {
     const int c = c0 + (lane & 16) + (lane & 3) * 4, k = 16 * t + 8 * half + ((lane >> 2) & 3);
-    const uint2 a = read_transposed(tile + across_off<T>(k, c >> 3) + (c & 7) * 2);
-    const uint2 b = read_transposed(tile + across_off<T>(k + 4, c >> 3) + (c & 7) * 2);
+    const uint2 a = read_transposed(tile + across_off<T, MB>(k, c >> 3) + (c & 7) * 2);
+    const uint2 b = read_transposed(tile + across_off<T, MB>(k + 4, c >> 3) + (c & 7) * 2);
     return u32x4{a.x, a.y, b.x, b.y};
   } else {
     const int c = c0 + (lane & 31), k = 8 * t + 4 * half;
     u32x4 v;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      v[i] = *reinterpret_cast<const uint32_t*>(tile + across_off<T>(k + i, c >> 2) + (c & 3) * 4);
+      v[i] = *reinterpret_cast<const uint32_t*>(tile + across_off<T, MB>(k + i, c >> 2) + (c & 3) * 4);
     return v;
   }
 }
@@ -130,36 +136,37 @@ __device__ __forceinline__ f32x16 product(u32x4 a, u32x4 b, f32x16 c) {
   }
 }
 
-// A wave's 64 x 64 of the tile's products over `steps` steps of the
+// A wave's 32 MB x 32 MB of the tile's products over `steps` steps of the
 // contraction; load(s) brings step s to the thread's registers, store(buffer)
 // takes them to LDS.
-template <typename T, bool A_ACROSS, bool B_ACROSS, typename Load, typename Store>
-__device__ __forceinline__ void tile_products(uint8_t* smem, int steps, f32x16 (&acc)[2][2],
+template <typename T, int MB, bool A_ACROSS, bool B_ACROSS, typename Load, typename Store>
+__device__ __forceinline__ void tile_products(uint8_t* smem, int steps, f32x16 (&acc)[MB][MB],
                                               const Load& load, const Store& store) {
-  const int wave = threadIdx.x >> 6, wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+  constexpr int BYTES = 64 * MB * 128;
+  const int wave = threadIdx.x >> 6, wm = (wave >> 1) * 32 * MB, wn = (wave & 1) * 32 * MB;
   if (steps > 0) {
     load(0);
     store(smem);
   }
   __syncthreads();
   for (int s = 0; s < steps; ++s) {
-    const uint8_t* at = smem + (s & 1) * 2 * kTileBytes;
-    const uint8_t* bt = at + kTileBytes;
+    const uint8_t* at = smem + (s & 1) * 2 * BYTES;
+    const uint8_t* bt = at + BYTES;
     if (s + 1 < steps) load(s + 1);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      u32x4 a[2], b[2];
+      u32x4 a[MB], b[MB];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        a[i] = A_ACROSS ? frag_across<T>(at, wm + 32 * i, t) : frag_along(at, wm + 32 * i, t);
-        b[i] = B_ACROSS ? frag_across<T>(bt, wn + 32 * i, t) : frag_along(bt, wn + 32 * i, t);
+      for (int i = 0; i < MB; ++i) {
+        a[i] = A_ACROSS ? frag_across<T, MB>(at, wm + 32 * i, t) : frag_along(at, wm + 32 * i, t);
+        b[i] = B_ACROSS ? frag_across<T, MB>(bt, wn + 32 * i, t) : frag_along(bt, wn + 32 * i, t);
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < MB; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = product<T>(a[i], b[j], acc[i][j]);
+        for (int j = 0; j < MB; ++j) acc[i][j] = product<T>(a[i], b[j], acc[i][j]);
     }
-    if (s + 1 < steps) store(smem + ((s + 1) & 1) * 2 * kTileBytes);
+    if (s + 1 < steps) store(smem + ((s + 1) & 1) * 2 * BYTES);
     __syncthreads();
   }
 }
@@ -176,34 +183,119 @@ __device__ __forceinline__ int row_of(int i, int r) {
 
 __device__ __forceinline__ int slot_at(const int32_t* order, int p) { return order ? order[p] : p; }
 
-template <typename T, bool W_ACROSS, bool VEC>
-__global__ void __launch_bounds__(256, 2) expert_mm_kernel(ExpertArgs a, int items, int ntn) {
-  constexpr int U = Elem<T>::U, STEP = Elem<T>::STEP, UPR = kTile / U;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[4 * kTileBytes];
-  int item, tn;
-  tile_of(items, ntn, item, tn);
-  const Item it = find_item(a.offsets, a.E, a.S, kTile, item);
-  const int n0 = tn * kTile;
-  // zero rows for the slots of no expert, shared out over the items
+// n / d for 0 <= n < 2^31 (Granlund and Montgomery, "Division by invariant
+// integers using multiplication", 1994): (mulhi(m, n) + n) >> l
+struct Divisor { uint32_t m; int l; };
+__device__ __forceinline__ uint32_t divide(uint32_t n, Divisor d) {
+  return (__umulhi(d.m, n) + n) >> d.l;
+}
+
+// The slots (-1: not stored) and scales of an item's rows.
+__device__ __forceinline__ void item_slots(const ExpertArgs& a, const Item& it, int rows,
+                                           int* slots, float* scales) {
+  const int r = threadIdx.x;
+  if (r >= rows) return;
+  const int s = r < it.rows ? slot_at(a.order, it.p0 + r) : -1;
+  const bool in = s >= 0 && s < a.S;
+  slots[r] = in ? s : -1;
+  scales[r] = in && a.row_scale ? a.row_scale[s] : 1.0f;
+}
+
+// Zero rows for the slots of no expert in columns [n0, n0 + cols), shared out
+// over the items, a wave to a row.
+__device__ __forceinline__ void zero_rows(const ExpertArgs& a, int n0, int cols, int item,
+                                          int items) {
+  const int waves = blockDim.x >> 6;
   const unsigned used = min(max(a.offsets[a.E], 0), a.S);
-  for (unsigned p = used + item; p < (unsigned)a.S; p += items) {    // both below 2^31
+  for (unsigned p = used + item * waves + (threadIdx.x >> 6); p < (unsigned)a.S;
+       p += items * waves) {                                         // all below 2^31
     const int slot = slot_at(a.order, p);
-    if (slot >= 0 && slot < a.S && (int)threadIdx.x < min(kTile, a.N - n0))
-      put(a.out, a.out_dtype, slot * a.ldo + n0 + threadIdx.x, 0.0f);
+    if (slot < 0 || slot >= a.S) continue;
+    for (int c = threadIdx.x & 63; c < cols; c += 64)
+      if (n0 + c < a.N) put(a.out, a.out_dtype, slot * a.ldo + n0 + c, 0.0f);
   }
+}
+
+// A call whose tiles are few is cut along the contraction too: `splits` parts,
+// fp32, one behind the other in the workspace (the launch's out), which
+// reduce_parts adds in order.  These find the part of an item and its range,
+// and point the output at it.
+__device__ __forceinline__ void part_of(ExpertArgs& a, int items, int splits, int step, int& item,
+                                        int& s0, int& s1) {
+  const int steps = (int)(((unsigned)a.K + step - 1) / step);
+  const int part = splits > 1 ? item / items : 0, per = (steps + splits - 1) / splits;
+  item -= part * items;
+  s0 = min(part * per, steps);
+  s1 = min(s0 + per, steps);
+  if (splits > 1) a.out = static_cast<float*>(a.out) + (int64_t)part * a.S * a.N;
+}
+__device__ __forceinline__ int run_of(WgradArgs& a, int ntn, int splits, int step, int& item,
+                                      int& lo, int& hi) {
+  const int part = splits > 1 ? item / (a.E * ntn) : 0;
+  item -= part * a.E * ntn;
+  const int e = item / ntn;
+  lo = min(max(a.offsets[e], 0), a.S);
+  hi = min(max(a.offsets[e + 1], lo), a.S);
+  if (splits > 1) {
+    const int per = ((hi - lo + step - 1) / step + splits - 1) / splits;    // steps of a part
+    lo = (int)min((int64_t)lo + (int64_t)part * per * step, (int64_t)hi);
+    hi = (int)min((int64_t)lo + (int64_t)per * step, (int64_t)hi);
+    a.dw = static_cast<float*>(a.dw) + (int64_t)part * a.E * a.N * a.K;
+  }
+  return e;
+}
+
+// out(r, c) at out[(r / inner) * outer_ld + (r % inner) * ld + c] = the sum of
+// the parts' [rows, cols].
+__global__ void __launch_bounds__(256) reduce_parts(const float* __restrict__ parts, int splits,
+                                                    void* out, bsmm_dtype dt, int64_t rows,
+                                                    int cols, int64_t inner, int64_t outer_ld,
+                                                    int64_t ld) {
+  const int64_t n = rows * cols;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = n <= 0x7FFFFFFF ? (unsigned)i / (unsigned)cols : i / cols;
+    const int64_t o = n <= 0x7FFFFFFF ? (unsigned)r / (unsigned)inner : r / inner;
+    float v = 0.0f;
+    for (int s = 0; s < splits; ++s) v += parts[s * n + i];
+    put(out, dt, o * outer_ld + (r - o * inner) * ld + (i - r * cols), v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Any type, alignment and size: tiles of 64 MB x 64 MB (four waves of 32 MB x
+// 32 MB), both operands through registers into two slots of LDS, in the layout
+// they have in memory; bf16 that lies across is transposed by the LDS read.
+// fp32 runs at the fp32 matrix instruction's rate.
+// ---------------------------------------------------------------------------
+template <typename T, int MB, bool W_ACROSS>
+__global__ void __launch_bounds__(256, 2) expert_mm_kernel(ExpertArgs a, int items, int ntn,
+                                                           int splits) {
+  constexpr int U = Elem<T>::U, STEP = Elem<T>::STEP, TILE = 64 * MB, BYTES = TILE * 128;
+  constexpr int UPR = TILE / U, NU = 2 * MB;          // units of an across row, of a thread
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[4 * BYTES];
+  __shared__ int slots[TILE];
+  __shared__ float scales[TILE];
+  int item, tn, s0, s1;
+  tile_of(items * splits, ntn, item, tn);
+  part_of(a, items, splits, STEP, item, s0, s1);
+  const Item it = find_item(a.offsets, a.E, a.S, TILE, item);
+  const int n0 = tn * TILE;
+  zero_rows(a, n0, TILE, item, items);
   if (it.rows == 0) return;
+  item_slots(a, it, TILE, slots, scales);
+  __syncthreads();
 
   const T* const x = static_cast<const T*>(a.x);
   const T* const w = static_cast<const T*>(a.w) + it.e * a.w_se;
-  // the thread's four units of each tile
+  // the thread's units of each tile
   const int u8 = threadIdx.x & 7;
-  const T* xr[4];
-  const T* wr[4];
+  const T* xr[NU];
+  const T* wr[NU];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < NU; ++i) {
     const int r = i * 32 + (threadIdx.x >> 3);
-    const int s = slot_at(a.order, it.p0 + min(r, it.rows - 1));
-    xr[i] = x + (int64_t)min(max(s / a.x_div, 0), a.R - 1) * a.ldx + u8 * U;
+    const int s = max(slots[min(r, it.rows - 1)], 0);
+    xr[i] = x + (int64_t)min(s / a.x_div, a.R - 1) * a.ldx + u8 * U;
     if (!W_ACROSS) {
       wr[i] = w + (int64_t)min(n0 + r, a.N - 1) * a.ldw + u8 * U;
     } else {
@@ -211,102 +303,112 @@ __global__ void __launch_bounds__(256, 2) expert_mm_kernel(ExpertArgs a, int ite
       wr[i] = w + (int64_t)(q / UPR) * a.ldw + n0 + q % UPR * U;
     }
   }
-  u32x4 va[4], vb[4];
+  u32x4 va[NU], vb[NU];
   auto load = [&](int s) {
-    const int k = s * STEP;
+    const int k = (s0 + s) * STEP;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      va[i] = fetch<T, VEC>(xr[i] + k, a.K - k - u8 * U);
+    for (int i = 0; i < NU; ++i) {
+      va[i] = fetch<T>(xr[i] + k, a.K - k - u8 * U);
       if (!W_ACROSS) {
-        vb[i] = fetch<T, VEC>(wr[i] + k, a.K - k - u8 * U);
+        vb[i] = fetch<T>(wr[i] + k, a.K - k - u8 * U);
       } else {
         const int q = i * 256 + threadIdx.x;
-        vb[i] = fetch<T, VEC>(wr[i] + (int64_t)k * a.ldw,
-                              k + q / UPR < a.K ? a.N - n0 - q % UPR * U : 0);
+        vb[i] = fetch<T>(wr[i] + (int64_t)k * a.ldw,
+                         k + q / UPR < a.K ? a.N - n0 - q % UPR * U : 0);
       }
     }
   };
   auto store = [&](uint8_t* to) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < NU; ++i) {
       const int q = i * 256 + threadIdx.x;
       *reinterpret_cast<u32x4*>(to + lds_off(q >> 3, q & 7)) = va[i];
-      *reinterpret_cast<u32x4*>(to + kTileBytes + (W_ACROSS ? across_off<T>(q / UPR, q % UPR)
-                                                            : lds_off(q >> 3, q & 7))) = vb[i];
+      *reinterpret_cast<u32x4*>(to + BYTES + (W_ACROSS ? across_off<T, MB>(q / UPR, q % UPR)
+                                                       : lds_off(q >> 3, q & 7))) = vb[i];
     }
   };
-  f32x16 acc[2][2] = {};
-  tile_products<T, false, W_ACROSS>(smem, (int)(((unsigned)a.K + STEP - 1) / STEP), acc, load,
-                                    store);
+  f32x16 acc[MB][MB] = {};
+  tile_products<T, MB, false, W_ACROSS>(smem, s1 - s0, acc, load, store);
 
-  const int wave = threadIdx.x >> 6, wm = (wave >> 1) * 64;
-  const int col = n0 + (wave & 1) * 64 + (threadIdx.x & 31);
+  const int wave = threadIdx.x >> 6, wm = (wave >> 1) * 32 * MB;
+  const int col = n0 + (wave & 1) * 32 * MB + (threadIdx.x & 31);
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < MB; ++i)
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      const int m = wm + row_of(i, r);
-      if (m >= it.rows) continue;
-      const int slot = slot_at(a.order, it.p0 + m);
-      if (slot < 0 || slot >= a.S) continue;
-      const float f = a.row_scale ? a.row_scale[slot] : 1.0f;
+      const int m = wm + row_of(i, r), slot = slots[m];
+      if (slot < 0) continue;
+      const float f = scales[m];
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < MB; ++j)
         if (col + 32 * j < a.N)
           put(a.out, a.out_dtype, slot * a.ldo + col + 32 * j, acc[i][j][r] * f);
     }
 }
 
 // CODES: x is an 8-bit checkpoint.
-template <typename T, bool CODES, bool VEC>
-__global__ void __launch_bounds__(256, 2) expert_wgrad_kernel(WgradArgs a, int ntn, int ntk) {
-  constexpr int U = Elem<T>::U, STEP = Elem<T>::STEP, UPR = kTile / U;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[4 * kTileBytes];
-  int item, tk;
-  tile_of(a.E * ntn, ntk, item, tk);
-  const int e = item / ntn, n0 = item % ntn * kTile, k0 = tk * kTile;
-  const int lo = min(max(a.offsets[e], 0), a.S), hi = min(max(a.offsets[e + 1], lo), a.S);
+template <typename T, int MB, bool CODES>
+__global__ void __launch_bounds__(256, 2) expert_wgrad_kernel(WgradArgs a, int ntn, int ntk,
+                                                              int splits, Divisor yd,
+                                                              Divisor xd) {
+  constexpr int U = Elem<T>::U, STEP = Elem<T>::STEP, TILE = 64 * MB, BYTES = TILE * 128;
+  constexpr int UPR = TILE / U, NU = 2 * MB;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[4 * BYTES];
+  int item, tk, lo, hi;
+  tile_of(splits * a.E * ntn, ntk, item, tk);
+  const int e = run_of(a, ntn, splits, STEP, item, lo, hi);
+  const int n0 = item % ntn * TILE, k0 = tk * TILE;
 
-  u32x4 va[4], vb[4];
+  // the thread's units are the same columns of rows 256 / UPR apart
+  const int u = threadIdx.x % UPR, row = threadIdx.x / UPR;
+  const int cy = n0 + u * U, cx = k0 + u * U;
+  u32x4 va[NU], vb[NU];
+  int next[NU];                         // the slots of the next step's rows
+  auto slots_of = [&](int s) {
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const int p = lo + s * STEP + i * (256 / UPR) + row;
+      next[i] = p < hi ? slot_at(a.order, p) : -1;
+    }
+  };
+  slots_of(0);
   auto load = [&](int s) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int q = i * 256 + threadIdx.x, u = q % UPR, p = lo + s * STEP + q / UPR;
-      const int slot = p < hi ? slot_at(a.order, p) : -1;
-      const bool in = slot >= 0 && slot < a.S;
-      const int64_t ry = in ? slot / a.y_div : 0, rx = in ? slot / a.x_div : 0;
-      va[i] = fetch<T, VEC>(static_cast<const T*>(a.dy) + ry * a.ldy + n0 + u * U,
-                            in ? a.N - n0 - u * U : 0);
-      const int c = k0 + u * U, left = in ? a.K - c : 0;
+    for (int i = 0; i < NU; ++i) {
+      const bool in = next[i] >= 0 && next[i] < a.S;
+      const int64_t ry = in ? divide(next[i], yd) : 0, rx = in ? divide(next[i], xd) : 0;
+      va[i] = fetch<T>(static_cast<const T*>(a.dy) + ry * a.ldy + cy, in ? a.N - cy : 0);
       if constexpr (CODES)
-        vb[i] = fetch_codes<T>(static_cast<const int8_t*>(a.x) + rx * a.ldx + c,
-                               a.x_scale + rx * a.s_r + c / 32, left);
+        vb[i] = fetch_codes<T>(static_cast<const int8_t*>(a.x) + rx * a.ldx + cx,
+                               a.x_scale + rx * a.s_r + cx / 32, in ? a.K - cx : 0);
       else
-        vb[i] = fetch<T, VEC>(static_cast<const T*>(a.x) + rx * a.ldx + c, left);
+        vb[i] = fetch<T>(static_cast<const T*>(a.x) + rx * a.ldx + cx, in ? a.K - cx : 0);
     }
+    slots_of(s + 1);
   };
   auto store = [&](uint8_t* to) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int q = i * 256 + threadIdx.x, at = across_off<T>(q / UPR, q % UPR);
+    for (int i = 0; i < NU; ++i) {
+      const int at = across_off<T, MB>(i * (256 / UPR) + row, u);
       *reinterpret_cast<u32x4*>(to + at) = va[i];
-      *reinterpret_cast<u32x4*>(to + kTileBytes + at) = vb[i];
+      *reinterpret_cast<u32x4*>(to + BYTES + at) = vb[i];
     }
   };
-  f32x16 acc[2][2] = {};
-  tile_products<T, true, true>(smem, (int)(((unsigned)(hi - lo) + STEP - 1) / STEP), acc, load,
-                               store);
+  f32x16 acc[MB][MB] = {};
+  tile_products<T, MB, true, true>(smem, (int)(((unsigned)(hi - lo) + STEP - 1) / STEP), acc, load,
+                                   store);
 
   const int wave = threadIdx.x >> 6;
-  const int row0 = n0 + (wave >> 1) * 64, col = k0 + (wave & 1) * 64 + (threadIdx.x & 31);
+  const int row0 = n0 + (wave >> 1) * 32 * MB;
+  const int col = k0 + (wave & 1) * 32 * MB + (threadIdx.x & 31);
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < MB; ++i)
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       const int n = row0 + row_of(i, r);
       if (n >= a.N) continue;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < MB; ++j)
         if (col + 32 * j < a.K)
           put(a.dw, a.out_dtype, e * a.w_se + n * a.ldw + col + 32 * j, acc[i][j][r]);
     }
@@ -559,21 +661,10 @@ __device__ __forceinline__ void wide_store(uint8_t* smem, const f32x16 (&acc)[MI
   }
 }
 
-// The slots (-1: not stored) and scales of an item's rows.
-__device__ __forceinline__ void item_slots(const ExpertArgs& a, const Item& it, int rows,
-                                           int* slots, float* scales) {
-  const int r = threadIdx.x;
-  if (r >= rows) return;
-  const int s = r < it.rows ? slot_at(a.order, it.p0 + r) : -1;
-  const bool in = s >= 0 && s < a.S;
-  slots[r] = in ? s : -1;
-  scales[r] = in && a.row_scale ? a.row_scale[s] : 1.0f;
-}
-
 // An item of at most 64 MI rows from column n0.
 template <int MI, bool W_ACROSS>
 __device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& it, int n0,
-                                               uint8_t* smem, bool vec) {
+                                               int s0, int s1, uint8_t* smem, bool vec) {
   using W = Wide<MI>;
   int* const slots = reinterpret_cast<int*>(smem + kWideStage);
   float* const scales = reinterpret_cast<float*>(slots + 256);
@@ -588,11 +679,13 @@ __device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& 
     int wave, lane, n0, xk;
     uint32_t at;
     const uint16_t* w;
+    int s0;
     const uint16_t* xp[MI];
     const uint16_t* wp[4];
     u32x4 xv[MI];
     Turn v;
     __device__ __forceinline__ const uint16_t* along(bool last, const uint16_t* p, int s) const {
+      s += s0;
       return !last || s * 64 + xk < a.K ? p + s * 64 : reinterpret_cast<const uint16_t*>(kZeros);
     }
     __device__ __forceinline__ void direct_a(bool last, int s, uint8_t* slot, int i) {
@@ -606,7 +699,7 @@ __device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& 
       if (i < MI) {
         xv[i] = load_global<u32x4>(along(last, xp[i], s));
       } else {
-        const int k = s * 64 + wave * 8 + i - MI;
+        const int k = (s0 + s) * 64 + wave * 8 + i - MI;
         const uint16_t* row = w + (int64_t)k * a.ldw + n0;
         if (last) row = k < a.K ? row : reinterpret_cast<const uint16_t*>(kZeros);
         v.row[i - MI] = load_global<u32x2>(reinterpret_cast<const uint8_t*>(row) + at);
@@ -618,7 +711,7 @@ __device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& 
     }
   } ops{a, wave, lane, n0, ((lane & 7) ^ swz(8 * wave + (lane >> 3))) * 8,
         (uint32_t)min(4 * lane, a.N - 4 - n0) * 2,
-        static_cast<const uint16_t*>(a.w) + it.e * a.w_se, {}, {}, {}, {}};
+        static_cast<const uint16_t*>(a.w) + it.e * a.w_se, s0, {}, {}, {}, {}};
 #pragma unroll
   for (int t = 0; t < MI; ++t) {
     const int s = max(slots[64 * t + 8 * wave + (lane >> 3)], 0);
@@ -634,7 +727,7 @@ __device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& 
   __syncthreads();                      // the slots have been read
   f32x16 acc[MI][2] = {};
   wide_products<MI, !W_ACROSS, false, W_ACROSS, MI + 8, MI + 4>(
-      smem, (int)(((unsigned)a.K + 63) / 64), acc, ops);
+      smem, s1 - s0, acc, ops);
   barrier();                            // nobody reads the tiles any more
   item_slots(a, it, 64 * MI, slots, scales);
   __syncthreads();
@@ -652,47 +745,34 @@ __device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& 
 
 template <bool W_ACROSS>
 __global__ void __launch_bounds__(512, 2) expert_mm_wide(ExpertArgs a, int items, int ntn,
-                                                         int group, int vec) {
+                                                         int splits, int vec) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-  int item, tn;
-  tile_of(items, ntn, item, tn, group);
+  // groups of 4 items: half of an XCD's 32 workgroups (8 and 2 were within 1 %)
+  int item, tn, s0, s1;
+  tile_of(items * splits, ntn, item, tn, 4);
+  part_of(a, items, splits, 64, item, s0, s1);
   const Item it = find_item(a.offsets, a.E, a.S, 256, item);
   const int n0 = tn * kWide;
-  // zero rows for the slots of no expert, a wave to a row
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const unsigned used = min(max(a.offsets[a.E], 0), a.S);
-  for (unsigned p = used + item * 8 + wave; p < (unsigned)a.S; p += items * 8) {
-    const int slot = slot_at(a.order, p);
-    if (slot < 0 || slot >= a.S) continue;
-#pragma unroll
-    for (int c = threadIdx.x & 63; c < kWide; c += 64)
-      if (n0 + c < a.N) put(a.out, a.out_dtype, slot * a.ldo + n0 + c, 0.0f);
-  }
+  zero_rows(a, n0, kWide, item, items);
   if (it.rows == 0) return;
   // only as many rows as there are, to 64: an expert's last item would
   // multiply 128 empty rows on average
   const int mi = (it.rows + 63) / 64;
-  if (mi == 4) expert_mm_item<4, W_ACROSS>(a, it, n0, smem, vec);
-  else if (mi == 3) expert_mm_item<3, W_ACROSS>(a, it, n0, smem, vec);
-  else if (mi == 2) expert_mm_item<2, W_ACROSS>(a, it, n0, smem, vec);
-  else expert_mm_item<1, W_ACROSS>(a, it, n0, smem, vec);
-}
-
-// n / d for 0 <= n < 2^31 (Granlund and Montgomery, "Division by invariant
-// integers using multiplication", 1994): (mulhi(m, n) + n) >> l
-struct Divisor { uint32_t m; int l; };
-__device__ __forceinline__ uint32_t divide(uint32_t n, Divisor d) {
-  return (__umulhi(d.m, n) + n) >> d.l;
+  if (mi == 4) expert_mm_item<4, W_ACROSS>(a, it, n0, s0, s1, smem, vec);
+  else if (mi == 3) expert_mm_item<3, W_ACROSS>(a, it, n0, s0, s1, smem, vec);
+  else if (mi == 2) expert_mm_item<2, W_ACROSS>(a, it, n0, s0, s1, smem, vec);
+  else expert_mm_item<1, W_ACROSS>(a, it, n0, s0, s1, smem, vec);
 }
 
 __global__ void __launch_bounds__(512, 2) expert_wgrad_wide(WgradArgs a, int ntn, int ntk,
-                                                            Divisor yd, Divisor xd, int vec) {
+                                                            int splits, Divisor yd, Divisor xd,
+                                                            int vec) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-  int item, tk;
-  tile_of(a.E * ntn, ntk, item, tk);
-  const int e = item / ntn, n0 = item % ntn * 256, k0 = tk * kWide, lane = threadIdx.x & 63;
+  int item, tk, lo, hi;
+  tile_of(splits * a.E * ntn, ntk, item, tk);
+  const int e = run_of(a, ntn, splits, 64, item, lo, hi);
+  const int n0 = item % ntn * 256, k0 = tk * kWide, lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lo = min(max(a.offsets[e], 0), a.S), hi = min(max(a.offsets[e + 1], lo), a.S);
   // the wave's 8 positions of a step; lane i < 8 has the slot of the i-th
   struct {
     const WgradArgs& a;
@@ -784,13 +864,7 @@ __global__ void __launch_bounds__(kRowsWaves * 64, 4) expert_mm_rows(ExpertArgs 
   const int item = item0 + blockIdx.y;
   const Item it = find_item(a.offsets, a.E, a.S, 16, item);
   const int n0 = (blockIdx.x * cn + cw) * 64, cols = cn * 64;
-  const unsigned used = min(max(a.offsets[a.E], 0), a.S);
-  for (unsigned p = used + item; p < (unsigned)a.S; p += gridDim.y) {    // both below 2^31
-    const int slot = slot_at(a.order, p);
-    if (slot < 0 || slot >= a.S) continue;
-    const int n = blockIdx.x * cols + threadIdx.x;     // cols <= 512, the workgroup's threads
-    if ((int)threadIdx.x < cols && n < a.N) put(a.out, a.out_dtype, slot * a.ldo + n, 0.0f);
-  }
+  zero_rows(a, blockIdx.x * cols, cols, item, gridDim.y);
   if (it.rows == 0) return;
 
   const int slot = slot_at(a.order, it.p0 + (c16 < it.rows ? c16 : 0));
@@ -896,16 +970,16 @@ Divisor divisor(uint32_t d) {
   return Divisor{(uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << l) - d)) / d + 1), l};
 }
 
-template <typename T>
-bool vec_ok(const void* p, int64_t ld) {
-  return (uintptr_t)p % 16 == 0 && ld % Elem<T>::U == 0;
-}
-
 template <typename T, bool W_ACROSS>
 void launch_rows(const ExpertArgs& a, hipStream_t st) {
-  const int64_t act = a.E < a.S ? a.E : a.S, items = (a.S + act * 15) / 16;
+  const int64_t act = a.E < a.S ? a.E : a.S, items = ((int64_t)a.S + act * 15) / 16;
   const int64_t groups = ((int64_t)a.N + 63) / 64;
-  static const int target = getenv("TGT") ? atoi(getenv("TGT")) : 2048;
+  // Waves that fill the chip; experts of more than 6 rows on average have
+  // second items, which read the weights again: better while they are read
+  // first, so all of a workgroup's waves take the same columns (32 tokens x 8
+  // of 32 experts of 2048 x 4096: 175 and 140 us; 33 x 4 of 16 of 4099 x 1024
+  // fp32: 99 and 78; 8 x 8 of 32, two rows: 105 and 112).
+  const int64_t target = a.S <= 6 * act ? 2048 : 8192;
   const int64_t busy = (a.S + act * 8) / 16 + 1;
   int log_ks = 0;
   while (log_ks < 3 && (busy * groups << log_ks) < target) ++log_ks;
@@ -916,77 +990,109 @@ void launch_rows(const ExpertArgs& a, hipStream_t st) {
                        dim3(kRowsWaves * 64), 0, st, a, (int)i, log_ks);
 }
 
-template <typename T>
-void launch_mm(const ExpertArgs& a, hipStream_t st) {
-  static const int few = getenv("FEW") ? atoi(getenv("FEW")) : 16;
-  if (vec_ok<T>(a.x, a.ldx) && vec_ok<T>(a.w, a.ldw) && a.w_se % Elem<T>::U == 0 &&
-      a.K % Elem<T>::U == 0 && (!a.w_across || a.N % Elem<T>::U == 0) && a.S <= few * a.E) {
-    if (a.w_across) launch_rows<T, true>(a, st); else launch_rows<T, false>(a, st);
-    return;
-  }
-  if (sizeof(T) == 2 && vec_ok<T>(a.x, a.ldx) && vec_ok<T>(a.w, a.ldw) && a.w_se % 8 == 0 &&
-      a.K % 8 == 0 && (!a.w_across || a.N % 8 == 0) && a.S > 0) {
-    const int64_t act = a.E < a.S ? a.E : a.S;
-    const int items = (int)((a.S + act * 255) / 256), ntn = (a.N + kWide - 1) / kWide;
-    const int vec = (uintptr_t)a.out % 16 == 0 && a.ldo % (a.out_dtype == BSMM_BF16 ? 8 : 4) == 0;
-    if (a.w_across) hipLaunchKernelGGL((expert_mm_wide<true>), dim3((unsigned)(items * ntn)), dim3(512), kWideBytes, st, a, items, ntn, 4, vec);
-    else hipLaunchKernelGGL((expert_mm_wide<false>), dim3((unsigned)(items * ntn)), dim3(512), kWideBytes, st, a, items, ntn, 4, vec);
-    return;
+void launch_reduce(const float* parts, int splits, void* out, bsmm_dtype dt, int64_t rows,
+                   int cols, int64_t inner, int64_t outer_ld, int64_t ld, hipStream_t st) {
+  const int64_t blocks = (rows * cols + 255) / 256;
+  hipLaunchKernelGGL(reduce_parts, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), 0,
+                     st, parts, splits, out, dt, rows, cols, inner, outer_ld, ld);
+}
+
+// 16-byte aligned rows of a bf16 or fp32 output, for the wide tiles' stores
+int vec_rows(const void* p, int64_t ld, bsmm_dtype dt) {
+  return aligned(p, 16) && ld % (dt == BSMM_BF16 ? 8 : 4) == 0;
+}
+
+template <typename T, bool W_ACROSS>
+void launch_mm(ExpertArgs a, ExpertPlan plan, int splits, void* ws, hipStream_t st) {
+  if (plan == ExpertPlan::Rows) return launch_rows<T, W_ACROSS>(a, st);
+  void* const out = a.out;
+  const int64_t ldo = a.ldo;
+  const bsmm_dtype dt = a.out_dtype;
+  if (splits > 1) {
+    a.out = ws;
+    a.ldo = a.N;
+    a.out_dtype = BSMM_F32;
   }
   const int64_t act = a.E < a.S ? a.E : a.S;
-  const int items = (int)((a.S + act * (kTile - 1)) / kTile), ntn = (a.N + kTile - 1) / kTile;
-  const dim3 grid((unsigned)(items * ntn)), block(256);
-  const bool vec = vec_ok<T>(a.x, a.ldx) && vec_ok<T>(a.w, a.ldw) && a.w_se % Elem<T>::U == 0;
-  if (a.w_across) {
-    if (vec) hipLaunchKernelGGL((expert_mm_kernel<T, true, true>), grid, block, 0, st, a, items, ntn);
-    else hipLaunchKernelGGL((expert_mm_kernel<T, true, false>), grid, block, 0, st, a, items, ntn);
+  const int tile = plan == ExpertPlan::Wide ? 256 : plan == ExpertPlan::Tiles128 ? 128 : 64;
+  const int items = (int)(((int64_t)a.S + act * (tile - 1)) / tile), ntn = (a.N + tile - 1) / tile;
+  const dim3 grid((unsigned)((int64_t)items * splits * ntn));
+  if (plan == ExpertPlan::Wide) {
+    if constexpr (sizeof(T) == 2)
+      hipLaunchKernelGGL((expert_mm_wide<W_ACROSS>), grid, dim3(512), kWideBytes, st, a, items, ntn,
+                         splits, vec_rows(a.out, a.ldo, a.out_dtype));
+  } else if (plan == ExpertPlan::Tiles128) {
+    if constexpr (sizeof(T) == 2)
+      hipLaunchKernelGGL((expert_mm_kernel<T, 2, W_ACROSS>), grid, dim3(256), 0, st, a, items, ntn,
+                         splits);
   } else {
-    if (vec) hipLaunchKernelGGL((expert_mm_kernel<T, false, true>), grid, block, 0, st, a, items, ntn);
-    else hipLaunchKernelGGL((expert_mm_kernel<T, false, false>), grid, block, 0, st, a, items, ntn);
+    hipLaunchKernelGGL((expert_mm_kernel<T, 1, W_ACROSS>), grid, dim3(256), 0, st, a, items, ntn,
+                       splits);
   }
+  if (splits > 1)
+    launch_reduce(static_cast<const float*>(ws), splits, out, dt, a.S, a.N, a.S, 0, ldo, st);
+}
+
+template <typename T, int MB>
+void launch_wgrad_tiles(const WgradArgs& a, int ntn, int ntk, int splits, hipStream_t st) {
+  const dim3 grid((unsigned)((int64_t)splits * a.E * ntn * ntk)), block(256);
+  const Divisor yd = divisor(a.y_div), xd = divisor(a.x_div);
+  if (a.x_scale)
+    hipLaunchKernelGGL((expert_wgrad_kernel<T, MB, true>), grid, block, 0, st, a, ntn, ntk, splits,
+                       yd, xd);
+  else
+    hipLaunchKernelGGL((expert_wgrad_kernel<T, MB, false>), grid, block, 0, st, a, ntn, ntk, splits,
+                       yd, xd);
 }
 
 template <typename T>
-void launch_wgrad(WgradArgs a, void* ws, hipStream_t st) {
-  if (sizeof(T) == 2 && a.x_scale && ws) {
-    if (launch_restore_bf16(a.x, a.ldx, a.x_scale, a.s_r, ws, a.Rx, a.K, st)) return;
-    a.x = ws; a.ldx = a.K; a.x_scale = nullptr;
+void launch_wgrad(WgradArgs a, ExpertPlan plan, int splits, void* ws, hipStream_t st) {
+  void* const dw = a.dw;
+  const int64_t w_se = a.w_se, ldw = a.ldw;
+  const bsmm_dtype dt = a.out_dtype;
+  if (splits > 1) {
+    a.dw = ws;
+    a.ldw = a.K;
+    a.w_se = (int64_t)a.N * a.K;
+    a.out_dtype = BSMM_F32;
   }
-  if (sizeof(T) == 2 && !a.x_scale && vec_ok<T>(a.dy, a.ldy) && vec_ok<T>(a.x, a.ldx) && a.N % 8 == 0 &&
-      a.K % 8 == 0) {
-    const int ntn = (a.N + 255) / 256, ntk = (a.K + 255) / 256;
-    hipLaunchKernelGGL(expert_wgrad_wide, dim3((unsigned)((int64_t)a.E * ntn * ntk)), dim3(512),
-                       kWideBytes, st, a, ntn, ntk, divisor(a.y_div), divisor(a.x_div),
-                       (uintptr_t)a.dw % 16 == 0 && a.ldw % 8 == 0 && a.w_se % 8 == 0);
-    return;
-  }
-  const int ntn = (a.N + kTile - 1) / kTile, ntk = (a.K + kTile - 1) / kTile;
-  const dim3 grid((unsigned)((int64_t)a.E * ntn * ntk)), block(256);
-  const bool yv = vec_ok<T>(a.dy, a.ldy);
-  if (a.x_scale) {
-    if (yv) hipLaunchKernelGGL((expert_wgrad_kernel<T, true, true>), grid, block, 0, st, a, ntn, ntk);
-    else hipLaunchKernelGGL((expert_wgrad_kernel<T, true, false>), grid, block, 0, st, a, ntn, ntk);
+  const int tile = plan == ExpertPlan::Wide ? 256 : plan == ExpertPlan::Tiles128 ? 128 : 64;
+  const int ntn = (a.N + tile - 1) / tile, ntk = (a.K + tile - 1) / tile;
+  if (plan == ExpertPlan::Wide) {
+    if constexpr (sizeof(T) == 2)
+      hipLaunchKernelGGL(expert_wgrad_wide, dim3((unsigned)((int64_t)splits * a.E * ntn * ntk)),
+                         dim3(512), kWideBytes, st, a, ntn, ntk, splits, divisor(a.y_div),
+                         divisor(a.x_div),
+                         vec_rows(a.dw, a.ldw, a.out_dtype) &&
+                             vec_rows(a.dw, a.w_se, a.out_dtype));
+  } else if (plan == ExpertPlan::Tiles128) {
+    launch_wgrad_tiles<T, 2>(a, ntn, ntk, splits, st);
   } else {
-    if (yv && vec_ok<T>(a.x, a.ldx))
-      hipLaunchKernelGGL((expert_wgrad_kernel<T, false, true>), grid, block, 0, st, a, ntn, ntk);
-    else
-      hipLaunchKernelGGL((expert_wgrad_kernel<T, false, false>), grid, block, 0, st, a, ntn, ntk);
+    launch_wgrad_tiles<T, 1>(a, ntn, ntk, splits, st);
   }
+  if (splits > 1)
+    launch_reduce(static_cast<const float*>(ws), splits, dw, dt, (int64_t)a.E * a.N, a.K, a.N, w_se,
+                  ldw, st);
 }
 
 }  // namespace
 
-int launch_expert_mm(const ExpertArgs& a, void* stream) {
+int launch_expert_mm(const ExpertArgs& a, ExpertPlan plan, int splits, void* ws, void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (a.dtype == BSMM_BF16) launch_mm<uint16_t>(a, st);
-  else launch_mm<float>(a, st);
+  if (a.dtype == BSMM_BF16) {
+    if (a.w_across) launch_mm<uint16_t, true>(a, plan, splits, ws, st);
+    else launch_mm<uint16_t, false>(a, plan, splits, ws, st);
+  } else {
+    if (a.w_across) launch_mm<float, true>(a, plan, splits, ws, st);
+    else launch_mm<float, false>(a, plan, splits, ws, st);
+  }
   return hipGetLastError() == hipSuccess ? 0 : 1;
 }
 
-int launch_expert_wgrad(const WgradArgs& a, void* ws, void* stream) {
+int launch_expert_wgrad(const WgradArgs& a, ExpertPlan plan, int splits, void* ws, void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (a.dtype == BSMM_BF16) launch_wgrad<uint16_t>(a, ws, st);
-  else launch_wgrad<float>(a, ws, st);
+  if (a.dtype == BSMM_BF16) launch_wgrad<uint16_t>(a, plan, splits, ws, st);
+  else launch_wgrad<float>(a, plan, splits, ws, st);
   return hipGetLastError() == hipSuccess ? 0 : 1;
 }
 

@@ -15,11 +15,134 @@ namespace {
 bool float_dtype(bsmm_dtype d) { return d == BSMM_F32 || d == BSMM_BF16; }
 uintptr_t dtype_bytes(bsmm_dtype d) { return d == BSMM_BF16 ? 2 : 4; }
 constexpr int64_t kMaxExperts = 1024;
-constexpr int64_t kRowTile = 128;
+
+// A kernel and the ranges of the contraction it is cut into.
+struct Choice { ExpertPlan plan; int splits; double us; };
+
+// The time of a plan in us: `tiles` workgroups (times splits) of `steps`
+// contraction steps, `outs` elements of output.  A step of a workgroup takes
+// step_us, or each_us for every workgroup on its CU if that is more; a tile
+// `fixed` besides.  More ranges fill the chip, but write and read their fp32
+// sums, at 4 TB/s and in another launch; they are taken where that is to save
+// a seventh (300 tokens x 4 of 16 experts of 2048 x 2048 bf16: 43 us in one
+// range, 60 in two; 4000 x 2 of 4 of 300 x 200, weight gradient: 62 us in one,
+// 29 in eight).
+Choice best_split(ExpertPlan plan, int64_t tiles, int64_t steps, double outs, double step_us,
+                  double each_us, double fixed, size_t room) {
+  Choice best{plan, 1, 1e30};
+  for (int s = 1; s <= 16 && (s == 1 || steps >= 4 * s); ++s) {
+    if (s > 1 && (outs * 4 * s > (double)room || tiles * s > (int64_t)1 << 20)) break;
+    const double on_cu = (double)((tiles * s + 255) / 256);
+    const double step = each_us * on_cu > step_us ? each_us * on_cu : step_us;
+    const double us = (double)((steps + s - 1) / s) * step + fixed * on_cu +
+                      (s > 1 ? 8.0 + outs * 8 * s / 4e6 : 0.0);
+    if (us * (s > 1 && best.splits == 1 ? 1.17 : 1.0) < best.us) best = Choice{plan, s, us};
+  }
+  return best;
+}
+
+bool aligned_rows(const void* p, int64_t ld, bsmm_dtype d) {
+  return aligned(p, 16) && ld % (d == BSMM_BF16 ? 8 : 4) == 0;
+}
+
+// Measured (us; the average is of rows to an expert):
+//                                            Rows  Wide  Tiles64  Tiles128
+//   16 tokens x 8 of 32, 2048 x 4096 bf16     111   118                     (average 4)
+//   32 x 8 of 32, the same                    140   122                     (8)
+//   64 x 8 of 32, the same                    155   160                     (16)
+//   64 x 2 of 8, 1024 x 2048 bf16              14    20                     (16)
+//   64 x 8 of 32, input gradient bf16         120   141                     (16)
+//   96 x 8 of 32, the same                    136   137                     (24)
+//   64 x 4 of 16, 4096 x 1024 fp32             90          114              (16)
+//   128 x 4 of 16, the same                   129          130              (32)
+//   128 x 4 of 16, input gradient fp32        102          175              (32)
+//   333 x 2 of 6, 1001 x 515 fp32                           22       50
+//   2000 x 4 of 16, 1001 x 2051 fp32                       381      448
+//   2000 x 4 of 16, 1001 x 2051 bf16                       122      107
+Choice mm_plan(const ExpertArgs& a, size_t room) {
+  const bool bf16 = a.dtype == BSMM_BF16;
+  const int unit = bf16 ? 8 : 4;
+  const int64_t act = a.E < a.S ? a.E : a.S;
+  const bool rows = aligned_rows(a.x, a.ldx, a.dtype) && aligned_rows(a.w, a.ldw, a.dtype) &&
+                    a.w_se % unit == 0 && a.K % unit == 0 && (!a.w_across || a.N % unit == 0);
+  // items of bm rows: an expert's last one is half empty on average
+  auto items = [&](int64_t bm) {
+    return a.S < bm * act ? act : ((int64_t)a.S + act * (bm / 2)) / bm;
+  };
+  auto tiles = [&](int64_t bm) { return items(bm) * (((int64_t)a.N + bm - 1) / bm); };
+  const int64_t few = !bf16 ? 32 : a.w_across || tiles(256) < 256 ? 16 : 6;
+  if (rows && a.S <= few * act) return Choice{ExpertPlan::Rows, 1, 0};
+  const double outs = (double)a.S * a.N;
+  const int64_t steps = ((int64_t)a.K + 63) / 64;
+  if (bf16 && rows) {
+    // a tile of 64 rows takes 0.6 us a step, of 256 1.5
+    const double fill = a.S < 256 * act ? (double)a.S / (256.0 * act) : 1.0;
+    const double step = 0.6 + 0.9 * fill;
+    return best_split(ExpertPlan::Wide, tiles(256), steps, outs, step, step, 9, room);
+  }
+  const Choice small = best_split(ExpertPlan::Tiles64, tiles(64), bf16 ? steps : 2 * steps, outs,
+                                  0.7, bf16 ? 0.5 : 0.55, 1, room);
+  if (!bf16 || tiles(128) < 512) return small;
+  return Choice{ExpertPlan::Tiles128, 1, 0};
+}
+
+//                                              Wide  Tiles64  Tiles128   (us)
+//   333 tokens x 2 of 6, 1001 x 515 fp32                  22        26
+//   1000 x 4 of 16, 1024 x 2048 fp32                     298       251
+//   4000 x 2 of 4, 300 x 200 bf16                         62       119
+Choice wgrad_plan(const WgradArgs& a, bool codes, size_t room) {
+  const bool bf16 = a.dtype == BSMM_BF16;
+  const int64_t act = a.E < a.S ? a.E : a.S > 0 ? a.S : 1;
+  const int64_t run = ((int64_t)a.S + act - 1) / act;
+  const double outs = (double)a.E * a.N * a.K;
+  auto tiles = [&](int64_t t) {
+    return a.E * (((int64_t)a.N + t - 1) / t) * (((int64_t)a.K + t - 1) / t);
+  };
+  const int64_t steps = (run + (bf16 ? 63 : 31)) / (bf16 ? 64 : 32);
+  Choice c = best_split(ExpertPlan::Tiles64, tiles(64), steps, outs, 0.7, bf16 ? 0.5 : 0.8, 1, room);
+  const Choice d = best_split(ExpertPlan::Tiles128, tiles(128), steps, outs, bf16 ? 1.2 : 2.2,
+                              bf16 ? 1.9 : 2.0, 9, room);
+  if (d.us < c.us) c = d;
+  // loads of 8 bytes
+  if (bf16 && !codes && aligned(a.dy, 8) && a.ldy % 4 == 0 && a.N % 4 == 0 && aligned(a.x, 8) &&
+      a.ldx % 4 == 0 && a.K % 4 == 0) {
+    const Choice w = best_split(ExpertPlan::Wide, tiles(256), steps, outs, 1.7, 1.7,
+                                a.out_dtype == BSMM_F32 ? 14 : 9, room);
+    if (w.us < c.us) c = w;
+  }
+  return c;
+}
+
+// A checkpoint's values in bf16, before the parts.
+size_t restored_bytes(bsmm_dtype dtype, int checkpoint, int64_t Rx, int64_t K) {
+  return dtype == BSMM_BF16 && checkpoint ? ((size_t)Rx * (size_t)K * 2u + 15u) / 16u * 16u : 0;
+}
+
+constexpr size_t kEnough = (size_t)256 << 20;       // no plan's parts are larger
 
 }  // namespace
 
 extern "C" {
+
+size_t bsmm_expert_mm_workspace_bytes(bsmm_dtype dtype, int transposed, int64_t E, int64_t S,
+                                      int64_t N, int64_t K) {
+  if (!float_dtype(dtype) || E <= 0 || S <= 0 || N <= 0 || K <= 0 || E > kMaxExperts ||
+      S >= kMaxDim || N >= kMaxDim || K >= kMaxDim)
+    return 0;
+  // aligned or not
+  size_t need = 0;
+  for (int odd = 0; odd < 2; ++odd) {
+    ExpertArgs a{};
+    a.dtype = dtype;
+    a.w_across = transposed;
+    a.ldx = odd;
+    a.E = (int)E; a.S = (int)S; a.N = (int)N; a.K = (int)K;
+    const Choice c = mm_plan(a, kEnough);
+    const size_t bytes = c.splits > 1 ? (size_t)c.splits * (size_t)S * (size_t)N * 4u : 0;
+    if (bytes > need) need = bytes;
+  }
+  return need;
+}
 
 bsmm_status bsmm_expert_mm(const void* x, int64_t ldx, const void* w, int64_t w_se, int64_t w_sn,
                            int64_t w_sk, bsmm_dtype dtype, const int32_t* order,
@@ -70,17 +193,32 @@ bsmm_status bsmm_expert_mm(const void* x, int64_t ldx, const void* w, int64_t w_
   a.x_div = slots_per_row;
   a.out = out; a.ldo = ldo; a.out_dtype = out_dtype;
   a.E = (int)E; a.R = (int)R; a.S = (int)S; a.N = (int)N; a.K = (int)K;
-  (void)workspace;
-  (void)workspace_bytes;
-  if (launch_expert_mm(a, stream) != 0)
+  const Choice c = mm_plan(a, workspace != nullptr && aligned(workspace, 16) ? workspace_bytes : 0);
+  if (launch_expert_mm(a, c.plan, c.splits, workspace, stream) != 0)
     return fail(BSMM_ERR_HIP, "kernel launch failed (expert product)");
   return BSMM_OK;
 }
 
-size_t bsmm_expert_wgrad_workspace_bytes(bsmm_dtype dtype, int checkpoint, int64_t Rx, int64_t K) {
-  if (dtype != BSMM_BF16 || !checkpoint || Rx <= 0 || K <= 0 || Rx >= kMaxDim || K >= kMaxDim)
+size_t bsmm_expert_wgrad_workspace_bytes(bsmm_dtype dtype, int checkpoint, int64_t E, int64_t Rx,
+                                         int64_t S, int64_t N, int64_t K) {
+  if (!float_dtype(dtype) || E <= 0 || Rx <= 0 || S <= 0 || N <= 0 || K <= 0 || E > kMaxExperts ||
+      Rx >= kMaxDim || S >= kMaxDim || N >= kMaxDim || K >= kMaxDim)
     return 0;
-  return (size_t)Rx * (size_t)K * 2u;
+  size_t need = 0;
+  for (int odd = 0; odd < 2; ++odd) {
+    WgradArgs a{};
+    a.dtype = dtype;
+    a.ldy = odd;
+    a.E = (int)E; a.S = (int)S; a.N = (int)N; a.K = (int)K;
+    // fp32 or bf16 output
+    for (int bf = 0; bf < 2; ++bf) {
+      a.out_dtype = bf ? BSMM_BF16 : BSMM_F32;
+      const Choice c = wgrad_plan(a, false, kEnough);
+      const size_t bytes = c.splits > 1 ? (size_t)c.splits * (size_t)E * N * K * 4u : 0;
+      if (bytes > need) need = bytes;
+    }
+  }
+  return need + restored_bytes(dtype, checkpoint, Rx, K);
 }
 
 bsmm_status bsmm_expert_wgrad(const void* dy, int64_t ldy, bsmm_dtype dtype, int dy_slots_per_row,
@@ -114,7 +252,7 @@ bsmm_status bsmm_expert_wgrad(const void* dy, int64_t ldy, bsmm_dtype dtype, int
   CHECK(w_se >= (E > 1 ? (N - 1) * ldw + K : 0), BSMM_ERR_LAYOUT,
         "expert stride %lld below a weight's extent", (long long)w_se);
   CHECK(aligned(dw, dtype_bytes(out_dtype)), BSMM_ERR_ALIGN, "dw not aligned to its type");
-  CHECK(E * (N / kRowTile + 1) * (K / kRowTile + 1) < kMaxDim, BSMM_ERR_UNSUPPORTED,
+  CHECK(E * (N / 64 + 1) * (K / 64 + 1) < kMaxDim, BSMM_ERR_UNSUPPORTED,
         "E * N * K beyond the largest grid");
   if (S > 0) {
     CHECK(dy != nullptr && x != nullptr, BSMM_ERR_NULL, "dy or x is NULL");
@@ -133,10 +271,24 @@ bsmm_status bsmm_expert_wgrad(const void* dy, int64_t ldy, bsmm_dtype dtype, int
   a.order = order; a.offsets = offsets;
   a.dw = dw; a.w_se = w_se; a.ldw = ldw; a.out_dtype = out_dtype;
   a.E = (int)E; a.Rx = (int)Rx; a.S = (int)S; a.N = (int)N; a.K = (int)K;
-  const size_t need = bsmm_expert_wgrad_workspace_bytes(dtype, x_scale != nullptr, Rx, K);
-  void* ws = need > 0 && S > 0 && workspace_bytes >= need && aligned(workspace, 16) &&
-                     aligned(x, 8) && ldx % 8 == 0 ? workspace : nullptr;
-  if (launch_expert_wgrad(a, ws, stream) != 0)
+  uint8_t* ws = aligned(workspace, 16) ? static_cast<uint8_t*>(workspace) : nullptr;
+  size_t room = ws != nullptr ? workspace_bytes : 0;
+  Choice c = wgrad_plan(a, x_scale != nullptr, room);
+  // bf16: the codes are restored first where the wide tiles take them then
+  const size_t values = restored_bytes(dtype, x_scale != nullptr, Rx, K);
+  if (values > 0 && S > 0 && room >= values && aligned(x, 8) && ldx % 8 == 0) {
+    WgradArgs b = a;
+    b.x = ws; b.ldx = K; b.x_scale = nullptr;
+    const Choice r = wgrad_plan(b, false, room - values);
+    if (r.plan == ExpertPlan::Wide) {
+      if (launch_restore_bf16(x, ldx, x_scale, s_r, ws, Rx, K, stream) != 0)
+        return fail(BSMM_ERR_HIP, "kernel launch failed (checkpoint values)");
+      a = b;
+      c = r;
+      ws += values;
+    }
+  }
+  if (launch_expert_wgrad(a, c.plan, c.splits, ws, stream) != 0)
     return fail(BSMM_ERR_HIP, "kernel launch failed (expert weight gradient)");
   return BSMM_OK;
 }

@@ -256,7 +256,11 @@ struct ExpertArgs {
   void* out; int64_t ldo; bsmm_dtype out_dtype;
   int E, R, S, N, K;
 };
-int launch_expert_mm(const ExpertArgs& a, void* stream);
+// Its kernels and the weight gradient's: items of 16 rows (aligned), tiles of
+// up to 256 x 256 (aligned bf16), 128 x 128 or 64 x 64 (anything).  splits > 1:
+// ranges of the contraction, their sums in ws (splits * S * N fp32).
+enum class ExpertPlan { Rows, Wide, Tiles128, Tiles64 };
+int launch_expert_mm(const ExpertArgs& a, ExpertPlan plan, int splits, void* ws, void* stream);
 
 // The weights' gradient: dw[e] (row stride ldw) sums dy[s / y_div]^T x[s /
 // x_div] over the slots of e; slots outside [0, S) add nothing.  x_scale null:
@@ -271,8 +275,8 @@ struct WgradArgs {
   void* dw; int64_t w_se, ldw; bsmm_dtype out_dtype;
   int E, Rx, S, N, K;
 };
-// ws: null, or Rx * K * 2 bytes for a checkpoint and bf16 dy
-int launch_expert_wgrad(const WgradArgs& a, void* ws, void* stream);
+// splits > 1: parts of every run, their sums in ws (splits * E * N * K fp32)
+int launch_expert_wgrad(const WgradArgs& a, ExpertPlan plan, int splits, void* ws, void* stream);
 // A checkpoint's values in bf16, rows of K (0 on success)
 int launch_restore_bf16(const void* q, int64_t ldq, const uint8_t* scale, int64_t s_r, void* out,
                         int64_t R, int64_t K, void* stream);

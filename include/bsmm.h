@@ -528,8 +528,13 @@ bsmm_status bsmm_w4_expert_mm(const void* x, int64_t ldx, bsmm_dtype x_dtype, co
  * NULL: slot i at position i.  fp32 sums of unrounded products in a fixed
  * order.  Any N and K; pointers aligned to their types (16-byte aligned rows
  * are faster).  E <= 1024.  S == 0 or N == 0 does nothing, K == 0 writes
- * zeros.  The workspace is not used yet and may be NULL.
+ * zeros.  The workspace (16-byte aligned) holds fp32 sums over ranges of K
+ * where a call has too few tiles to fill the chip:
+ * bsmm_expert_mm_workspace_bytes gives the bytes (0: none wanted; transposed:
+ * w_sn is 1).  With less the call runs with fewer ranges.
  */
+size_t bsmm_expert_mm_workspace_bytes(bsmm_dtype dtype, int transposed, int64_t E, int64_t S,
+                                      int64_t N, int64_t K);
 bsmm_status bsmm_expert_mm(const void* x, int64_t ldx, const void* w, int64_t w_se, int64_t w_sn,
                            int64_t w_sk, bsmm_dtype dtype, const int32_t* order,
                            const int32_t* offsets, int slots_per_row, const float* row_scale,
@@ -551,11 +556,13 @@ bsmm_status bsmm_expert_mm(const void* x, int64_t ldx, const void* w, int64_t w_
  * dy_slots_per_row and S <= Rx * x_slots_per_row.  Sums, sizes, alignment and
  * workspace as for bsmm_expert_mm (a checkpoint: rows of codes at multiples
  * of 8 bytes are faster).  E, N or K 0 does nothing; S == 0 writes zeros.
- * The workspace (16-byte aligned) holds a checkpoint's values in bf16 while
- * the call runs: bsmm_expert_wgrad_workspace_bytes gives the bytes (0: none
- * wanted).  With less the call runs without it, slower.
+ * The workspace (16-byte aligned) holds a checkpoint's values in bf16, and
+ * fp32 sums over parts of the slots where dw has too few tiles to fill the
+ * chip: bsmm_expert_wgrad_workspace_bytes gives the bytes (0: none wanted).
+ * With less the call runs without, slower.
  */
-size_t bsmm_expert_wgrad_workspace_bytes(bsmm_dtype dtype, int checkpoint, int64_t Rx, int64_t K);
+size_t bsmm_expert_wgrad_workspace_bytes(bsmm_dtype dtype, int checkpoint, int64_t E, int64_t Rx,
+                                         int64_t S, int64_t N, int64_t K);
 bsmm_status bsmm_expert_wgrad(const void* dy, int64_t ldy, bsmm_dtype dtype, int dy_slots_per_row,
                               const void* x, int64_t ldx, int x_slots_per_row,
                               const uint8_t* x_scale, int64_t s_r, const int32_t* order,
