@@ -1072,11 +1072,13 @@ def _stream_of(t, stream):
         if stream.device_index != at:
             raise ValueError(f"tensors on cuda:{at}, but a stream of cuda:{stream.device_index}")
         return stream.cuda_stream
-    handle = _stream(None)
-    now = _CURRENT[0][0]()
+    if not _CURRENT:
+        _stream(None)
+    get, raw = _CURRENT[0]
+    now = get()
     if now != at:
         raise ValueError(f"tensors on cuda:{at}, but the current device is cuda:{now}")
-    return handle
+    return raw(now)
 
 
 def _slots_per_row(n, name):
@@ -1244,19 +1246,27 @@ def bsmm_quant_int8_mx(x, *, values=False, stream=None):
     for q * 2^(scale - 133): the x of bsmm_expert_wgrad.  ``values=True``
     appends these values as a tensor like x.
     """
-    x2, code = _quant_input(x)
-    _, torch, _, u8, _, _ = _DTYPES or _float_types()
+    code = _float_code(x.dtype, "x")
+    _, torch, _, u8, _, _ = _DTYPES
+    xs = x.shape
+    x2 = x if len(xs) == 2 else _quant_input(x)[0]
     R, K = x2.shape
     if K % 32:
         raise ValueError(f"the last dimension ({K}) must be a multiple of 32")
+    ldx = _row_stride(x2, (R, K), x2.stride(), "x")
     _one_gpu("x", x)
-    lead, dev = tuple(x.shape[:-1]), x.device
-    q = torch.empty(lead + (K,), dtype=torch.int8, device=dev)
-    scale = torch.empty(lead + (K // 32,), dtype=u8, device=dev)
-    v = torch.empty(lead + (K,), dtype=x.dtype, device=dev) if values else None
-    _check(load().bsmm_quant_int8_mx(
-        x2.data_ptr(), x2.stride(0) if R > 1 else K, code, q.data_ptr(), K, scale.data_ptr(),
-        K // 32, v.data_ptr() if values else None, K, R, K, _stream_of(x, stream)))
+    dev, new = x.device, torch.empty_strided
+    q = new((R, K), (K, 1), dtype=torch.int8, device=dev)
+    scale = new((R, K // 32), (K // 32, 1), dtype=u8, device=dev)
+    v = new((R, K), (K, 1), dtype=x.dtype, device=dev) if values else None
+    status = load().bsmm_quant_int8_mx(
+        x2.data_ptr(), ldx, code, q.data_ptr(), K, scale.data_ptr(), K // 32,
+        v.data_ptr() if values else None, K, R, K, _stream_of(x, stream))
+    if status:
+        _check(status)
+    if x2 is not x:
+        q, scale = q.view(xs), scale.view(*xs[:-1], K // 32)
+        v = v.view(xs) if values else None
     return (q, scale, v) if values else (q, scale)
 
 
@@ -1312,8 +1322,8 @@ def bsmm_swiglu_backward(da, q, scale, *, row_scale=None, act=True, stream=None)
     if scale.dtype is not u8 or scale.shape != (R, F // 16):
         raise ValueError(f"scale must be uint8 [{R}, {F // 16}], got {scale.dtype} "
                          f"{tuple(scale.shape)}")
-    ldq = _row_stride(q, q.shape, q.stride(), "q")
-    s_r = _row_stride(scale, scale.shape, scale.stride(), "scale")
+    ldq = _row_stride(q, (R, 2 * F), q.stride(), "q")
+    s_r = _row_stride(scale, (R, F // 16), scale.stride(), "scale")
     if row_scale is not None and (row_scale.dtype is not f32 or row_scale.numel() != R or
                                   not row_scale.is_contiguous()):
         raise ValueError(f"row_scale must be contiguous fp32 of {R} elements")
