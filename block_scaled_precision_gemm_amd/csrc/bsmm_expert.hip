@@ -744,14 +744,14 @@ __device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& 
 }
 
 template <bool W_ACROSS>
-__global__ void __launch_bounds__(512, 2) expert_mm_wide(ExpertArgs a, int items, int ntn,
-                                                         int splits, int vec) {
+__global__ void __launch_bounds__(512, 2) expert_mm_wide(ExpertArgs a, int rows, int items,
+                                                         int ntn, int splits, int vec) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   // groups of 4 items: half of an XCD's 32 workgroups (8 and 2 were within 1 %)
   int item, tn, s0, s1;
   tile_of(items * splits, ntn, item, tn, 4);
   part_of(a, items, splits, 64, item, s0, s1);
-  const Item it = find_item(a.offsets, a.E, a.S, 256, item);
+  const Item it = find_item(a.offsets, a.E, a.S, rows, item);
   const int n0 = tn * kWide;
   zero_rows(a, n0, kWide, item, items);
   if (it.rows == 0) return;
@@ -1003,7 +1003,7 @@ int vec_rows(const void* p, int64_t ld, bsmm_dtype dt) {
 }
 
 template <typename T, bool W_ACROSS>
-void launch_mm(ExpertArgs a, ExpertPlan plan, int splits, void* ws, hipStream_t st) {
+void launch_mm(ExpertArgs a, ExpertPlan plan, int rows, int splits, void* ws, hipStream_t st) {
   if (plan == ExpertPlan::Rows) return launch_rows<T, W_ACROSS>(a, st);
   void* const out = a.out;
   const int64_t ldo = a.ldo;
@@ -1014,13 +1014,14 @@ void launch_mm(ExpertArgs a, ExpertPlan plan, int splits, void* ws, hipStream_t 
     a.out_dtype = BSMM_F32;
   }
   const int64_t act = a.E < a.S ? a.E : a.S;
-  const int tile = plan == ExpertPlan::Wide ? 256 : plan == ExpertPlan::Tiles128 ? 128 : 64;
-  const int items = (int)(((int64_t)a.S + act * (tile - 1)) / tile), ntn = (a.N + tile - 1) / tile;
+  const int bn = plan == ExpertPlan::Wide ? kWide : plan == ExpertPlan::Tiles128 ? 128 : 64;
+  const int bm = plan == ExpertPlan::Wide ? rows : bn;
+  const int items = (int)(((int64_t)a.S + act * (bm - 1)) / bm), ntn = (a.N + bn - 1) / bn;
   const dim3 grid((unsigned)((int64_t)items * splits * ntn));
   if (plan == ExpertPlan::Wide) {
     if constexpr (sizeof(T) == 2)
-      hipLaunchKernelGGL((expert_mm_wide<W_ACROSS>), grid, dim3(512), kWideBytes, st, a, items, ntn,
-                         splits, vec_rows(a.out, a.ldo, a.out_dtype));
+      hipLaunchKernelGGL((expert_mm_wide<W_ACROSS>), grid, dim3(512), kWideBytes, st, a, rows, items,
+                         ntn, splits, vec_rows(a.out, a.ldo, a.out_dtype));
   } else if (plan == ExpertPlan::Tiles128) {
     if constexpr (sizeof(T) == 2)
       hipLaunchKernelGGL((expert_mm_kernel<T, 2, W_ACROSS>), grid, dim3(256), 0, st, a, items, ntn,
@@ -1077,14 +1078,15 @@ void launch_wgrad(WgradArgs a, ExpertPlan plan, int splits, void* ws, hipStream_
 
 }  // namespace
 
-int launch_expert_mm(const ExpertArgs& a, ExpertPlan plan, int splits, void* ws, void* stream) {
+int launch_expert_mm(const ExpertArgs& a, ExpertPlan plan, int rows, int splits, void* ws,
+                     void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (a.dtype == BSMM_BF16) {
-    if (a.w_across) launch_mm<uint16_t, true>(a, plan, splits, ws, st);
-    else launch_mm<uint16_t, false>(a, plan, splits, ws, st);
+    if (a.w_across) launch_mm<uint16_t, true>(a, plan, rows, splits, ws, st);
+    else launch_mm<uint16_t, false>(a, plan, rows, splits, ws, st);
   } else {
-    if (a.w_across) launch_mm<float, true>(a, plan, splits, ws, st);
-    else launch_mm<float, false>(a, plan, splits, ws, st);
+    if (a.w_across) launch_mm<float, true>(a, plan, rows, splits, ws, st);
+    else launch_mm<float, false>(a, plan, rows, splits, ws, st);
   }
   return hipGetLastError() == hipSuccess ? 0 : 1;
 }

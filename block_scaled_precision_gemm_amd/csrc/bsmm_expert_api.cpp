@@ -2,6 +2,7 @@
 // and the C entry points bsmm_expert_mm and bsmm_expert_wgrad of
 // include/bsmm.h.  Everything here runs on the host before any HIP call.
 
+#include <cmath>
 #include <cstdint>
 
 #include "bsmm.h"
@@ -17,7 +18,7 @@ uintptr_t dtype_bytes(bsmm_dtype d) { return d == BSMM_BF16 ? 2 : 4; }
 constexpr int64_t kMaxExperts = 1024;
 
 // A kernel and the ranges of the contraction it is cut into.
-struct Choice { ExpertPlan plan; int splits; double us; };
+struct Choice { ExpertPlan plan; int splits; double us; int rows; };
 
 // The time of a plan in us: `tiles` workgroups (times splits) of `steps`
 // contraction steps, `outs` elements of output.  A step of a workgroup takes
@@ -27,16 +28,21 @@ struct Choice { ExpertPlan plan; int splits; double us; };
 // a seventh (300 tokens x 4 of 16 experts of 2048 x 2048 bf16: 43 us in one
 // range, 60 in two; 4000 x 2 of 4 of 300 x 200, weight gradient: 62 us in one,
 // 29 in eight).
+//
+// guess: the number of tiles is one (the experts' loads are not known on the
+// host), so a last round that is nearly full may take another one.
 Choice best_split(ExpertPlan plan, int64_t tiles, int64_t steps, double outs, double step_us,
-                  double each_us, double fixed, size_t room) {
-  Choice best{plan, 1, 1e30};
+                  double each_us, double fixed, size_t room, bool guess = false) {
+  Choice best{plan, 1, 1e30, 0};
   for (int s = 1; s <= 16 && (s == 1 || steps >= 4 * s); ++s) {
     if (s > 1 && (outs * 4 * s > (double)room || tiles * s > (int64_t)1 << 20)) break;
-    const double on_cu = (double)((tiles * s + 255) / 256);
+    const double t = (double)(tiles * s) / 256.0, whole = std::floor(t), rest = t - whole;
+    const double on_cu = whole + (rest > 0.0 ? 1.0 : 0.0) +
+                         (guess && rest > 0.8 ? (rest - 0.8) * 5.0 : 0.0);
     const double step = each_us * on_cu > step_us ? each_us * on_cu : step_us;
     const double us = (double)((steps + s - 1) / s) * step + fixed * on_cu +
                       (s > 1 ? 8.0 + outs * 8 * s / 4e6 : 0.0);
-    if (us * (s > 1 && best.splits == 1 ? 1.17 : 1.0) < best.us) best = Choice{plan, s, us};
+    if (us * (s > 1 && best.splits == 1 ? 1.17 : 1.0) < best.us) best = Choice{plan, s, us, 0};
   }
   return best;
 }
@@ -67,23 +73,41 @@ Choice mm_plan(const ExpertArgs& a, size_t room) {
                     a.w_se % unit == 0 && a.K % unit == 0 && (!a.w_across || a.N % unit == 0);
   // items of bm rows: an expert's last one is half empty on average
   auto items = [&](int64_t bm) {
-    return a.S < bm * act ? act : ((int64_t)a.S + act * (bm / 2)) / bm;
+    if (act == 1) return ((int64_t)a.S + bm - 1) / bm;
+    const int64_t n = ((int64_t)a.S + act * (bm / 2)) / bm;
+    return n > act ? n : act;
   };
-  auto tiles = [&](int64_t bm) { return items(bm) * (((int64_t)a.N + bm - 1) / bm); };
-  const int64_t few = !bf16 ? 32 : a.w_across || tiles(256) < 256 ? 16 : 6;
-  if (rows && a.S <= few * act) return Choice{ExpertPlan::Rows, 1, 0};
+  auto tiles = [&](int64_t bm, int64_t bn) { return items(bm) * (((int64_t)a.N + bn - 1) / bn); };
+  const int64_t few = !bf16 ? 32 : a.w_across || tiles(256, 256) < 256 ? 16 : 6;
+  if (rows && a.S <= few * act) return Choice{ExpertPlan::Rows, 1, 0, 0};
   const double outs = (double)a.S * a.N;
   const int64_t steps = ((int64_t)a.K + 63) / 64;
   if (bf16 && rows) {
-    // a tile of 64 rows takes 0.6 us a step, of 256 1.5
-    const double fill = a.S < 256 * act ? (double)a.S / (256.0 * act) : 1.0;
-    const double step = 0.6 + 0.9 * fill;
-    return best_split(ExpertPlan::Wide, tiles(256), steps, outs, step, step, 9, room);
+    // Items of at most 256, 192 or 128 rows, whichever's rounds of tiles end
+    // first: a step of 64 rows takes 0.62 us, of 128 0.95, of 192 1.25, of 256
+    // 1.55, and any 1.65 where the weights come from HBM and not from the 256
+    // MB behind the L2s (512 tokens x 4 of 16, 2048 x 2048: 42 us in items of
+    // 128, 51 of 256; 1500 x 2 of 8, 2048 x 4096: 67 and 124; 1021 x 8 of 32,
+    // the same, 537 MB: 234 of 192, 216 of 256).
+    const bool hbm = (double)a.E * a.N * a.K * 2 > 256e6;
+    Choice best{ExpertPlan::Wide, 1, 1e30, 0};
+    for (int bm = 256; bm >= 128; bm -= 64) {
+      static const double kStep[4] = {0.62, 0.95, 1.25, 1.55};
+      // an expert of the average size, and half as many again
+      const int64_t most = ((int64_t)a.S + act - 1) / act * 3 / 2;
+      const double height = kStep[(most < bm ? (most + 63) / 64 : bm / 64) - 1];
+      const double step = hbm && height < 1.65 ? 1.65 : height;
+      Choice c = best_split(ExpertPlan::Wide, tiles(bm, 256), steps, outs, step, step, 8, room,
+                            act > 1);
+      c.rows = bm;
+      if (c.us < 0.97 * best.us) best = c;
+    }
+    return best;
   }
-  const Choice small = best_split(ExpertPlan::Tiles64, tiles(64), bf16 ? steps : 2 * steps, outs,
+  const Choice small = best_split(ExpertPlan::Tiles64, tiles(64, 64), bf16 ? steps : 2 * steps, outs,
                                   0.7, bf16 ? 0.5 : 0.55, 1, room);
-  if (!bf16 || tiles(128) < 512) return small;
-  return Choice{ExpertPlan::Tiles128, 1, 0};
+  if (!bf16 || tiles(128, 128) < 512) return small;
+  return Choice{ExpertPlan::Tiles128, 1, 0, 0};
 }
 
 //                                              Wide  Tiles64  Tiles128   (us)
@@ -194,7 +218,7 @@ bsmm_status bsmm_expert_mm(const void* x, int64_t ldx, const void* w, int64_t w_
   a.out = out; a.ldo = ldo; a.out_dtype = out_dtype;
   a.E = (int)E; a.R = (int)R; a.S = (int)S; a.N = (int)N; a.K = (int)K;
   const Choice c = mm_plan(a, workspace != nullptr && aligned(workspace, 16) ? workspace_bytes : 0);
-  if (launch_expert_mm(a, c.plan, c.splits, workspace, stream) != 0)
+  if (launch_expert_mm(a, c.plan, c.rows, c.splits, workspace, stream) != 0)
     return fail(BSMM_ERR_HIP, "kernel launch failed (expert product)");
   return BSMM_OK;
 }

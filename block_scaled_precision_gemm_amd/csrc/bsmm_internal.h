@@ -257,10 +257,12 @@ struct ExpertArgs {
   int E, R, S, N, K;
 };
 // Its kernels and the weight gradient's: items of 16 rows (aligned), tiles of
-// up to 256 x 256 (aligned bf16), 128 x 128 or 64 x 64 (anything).  splits > 1:
-// ranges of the contraction, their sums in ws (splits * S * N fp32).
+// up to `rows` x 256 (aligned bf16; rows 128, 192 or 256), 128 x 128 or 64 x 64
+// (anything).  splits > 1: ranges of the contraction, their sums in ws (splits
+// * S * N fp32).
 enum class ExpertPlan { Rows, Wide, Tiles128, Tiles64 };
-int launch_expert_mm(const ExpertArgs& a, ExpertPlan plan, int splits, void* ws, void* stream);
+int launch_expert_mm(const ExpertArgs& a, ExpertPlan plan, int rows, int splits, void* ws,
+                     void* stream);
 
 // The weights' gradient: dw[e] (row stride ldw) sums dy[s / y_div]^T x[s /
 // x_div] over the slots of e; slots outside [0, S) add nothing.  x_scale null:
