@@ -131,3 +131,28 @@ def test_noops():
     assert gate(R=0, h=None, a=None) == OK
     assert gate(F=0, h=None, a=None) == OK
     assert back(R=0, da=None, q=None, s=None, dh=None) == OK
+
+
+def test_workspaces():
+    """Where tiles are few, for a bf16 checkpoint, and nothing else."""
+    mm_need = bsmm.load().bsmm_expert_mm_workspace_bytes
+    assert mm_need(BF16, 0, 8, 4096, 4096, 4096) == 0
+    need = mm_need(BF16, 0, 1, 300, 130, 4096)
+    assert need > 0 and need % (300 * 130 * 4) == 0
+    assert mm_need(F32, 1, 1, 300, 130, 4096) > 0
+    for bad in ((I32, 0, 1, 300, 130, 4096), (BF16, 0, 0, 300, 130, 4096), (BF16, 0, 1, 0, 9, 9),
+                (BF16, 0, 1, 9, -1, 9), (BF16, 0, 1, 2**31, 9, 9), (BF16, 0, 1025, 9, 9, 9)):
+        assert mm_need(*bad) == 0
+    w_need = bsmm.load().bsmm_expert_wgrad_workspace_bytes
+    assert w_need(BF16, 0, 8, 4096, 4096, 4096, 4096) == 0
+    assert w_need(BF16, 1, 8, 4096, 4096, 4096, 4096) == 4096 * 4096 * 2
+    assert w_need(F32, 1, 8, 4096, 4096, 4096, 4096) == 0
+    need = w_need(F32, 0, 1, 9000, 9000, 64, 72)
+    assert need > 0 and need % (64 * 72 * 4) == 0
+    assert w_need(BF16, 1, 1, 9000, 9000, 64, 96) > 9000 * 96 * 2
+    for bad in ((I32, 1, 1, 9, 9, 9, 32), (BF16, 1, 0, 9, 9, 9, 32), (BF16, 1, 1, 2**31, 9, 9, 32),
+                (BF16, 1, 1, 9, -1, 9, 32)):
+        assert w_need(*bad) == 0
+    # the largest sizes: no overflow on the way (see the sanitized run of these tests)
+    mm_need(BF16, 1, 1024, 2**31 - 1, 2**31 - 1, 2**31 - 1)
+    w_need(BF16, 1, 1024, 2**31 - 1, 2**31 - 1, 2**31 - 1, 2**31 - 1)

@@ -87,10 +87,12 @@ def test_rejects(call):
 
 CALLS = {
     "mm": (lambda **a: mm(**a), dict(x=t(4, 8), w=t(2, 6, 8), order=t(8, dt=I), offsets=t(3, dt=I),
-                                     row_scale=t(8, dt=F), out=t(8, 6))),
+                                     row_scale=t(8, dt=F), out=t(8, 6),
+                                     workspace=t(64, dt=U8))),
     "wgrad": (lambda **a: wgrad(**a), dict(dy=t(8, 6), x=t(8, 32, dt=I8), x_scale=t(8, 1, dt=U8),
                                            order=t(8, dt=I), offsets=t(3, dt=I),
-                                           out=t(2, 6, 32, dt=F))),
+                                           out=t(2, 6, 32, dt=F),
+                                           workspace=t(64, dt=U8))),
     "quant": (lambda **a: quant(**a), dict(x=t(4, 32))),
     "gate": (lambda **a: gate(**a), dict(h=t(4, 64), out=t(4, 32))),
     "back": (lambda **a: back(**a), dict(da=t(4, 32), q=t(4, 64, dt=I8), scale=t(4, 2, dt=U8),
