@@ -832,8 +832,8 @@ __global__ void __launch_bounds__(512, 2) expert_wgrad_wide(WgradArgs a, int ntn
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: items of 16 rows by 64 columns, 16 x 16 instructions with the
-// weight as the first operand.  The eight waves of a workgroup share out cn =
+// Few rows: items of 16 or, along, 32 rows by 64 columns, 16 x 16 instructions
+// with the weight as the first operand.  The eight waves of a workgroup share out cn =
 // 8 / ks column groups and ks ranges of the contraction; partial sums are
 // added through LDS in order.
 //
@@ -843,33 +843,33 @@ __global__ void __launch_bounds__(512, 2) expert_wgrad_wide(WgradArgs a, int ntn
 // neighbouring columns: of bf16 8 rows, transposed by byte permutations, of
 // fp32 4 rows, each lane's 4 values then belonging to 4 column blocks.
 // ---------------------------------------------------------------------------
-constexpr int kRowsWaves = 8, kDepth = 4;
+constexpr int kRowsWaves = 8;
 
-// A chunk of one wave: x's fragment and those of its 4 column blocks
-template <typename T, bool ACROSS> struct Chunk {
-  u32x4 x;
+// A chunk of one wave: x's fragments and those of its 4 column blocks
+template <typename T, bool ACROSS, int MB> struct Chunk {
+  u32x4 x[MB];
   std::conditional_t<ACROSS && sizeof(T) == 2, u32x2, u32x4>
       w[ACROSS && sizeof(T) == 2 ? 8 : 4];
 };
 
-template <typename T, bool W_ACROSS>
-__global__ void __launch_bounds__(kRowsWaves * 64, 4) expert_mm_rows(ExpertArgs a, int item0,
-                                                                     int log_ks) {
-  constexpr int U = Elem<T>::U, CHUNK = 4 * U;         // elements of a lane's unit, a chunk
-  __shared__ __attribute__((aligned(16))) float part[kRowsWaves][16][68];
+// An item of at most 16 MB rows; column group blockIdx.x * cn + cw.
+template <typename T, bool W_ACROSS, int MB>
+__device__ __forceinline__ void expert_rows_item(const ExpertArgs& a, const Item& it, int log_ks,
+                                                 float (&part)[kRowsWaves][16][68]) {
+  constexpr int U = Elem<T>::U, CHUNK = 4 * U, kDepth = MB == 1 ? 4 : 3;
   const int lane = threadIdx.x & 63, c16 = lane & 15, quad = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ks = 1 << log_ks, cn = kRowsWaves >> log_ks;
   const int kw = wave & (ks - 1), cw = wave >> log_ks;
-  const int item = item0 + blockIdx.y;
-  const Item it = find_item(a.offsets, a.E, a.S, 16, item);
   const int n0 = (blockIdx.x * cn + cw) * 64, cols = cn * 64;
-  zero_rows(a, blockIdx.x * cols, cols, item, gridDim.y);
-  if (it.rows == 0) return;
 
-  const int slot = slot_at(a.order, it.p0 + (c16 < it.rows ? c16 : 0));
-  const int64_t row = min(max(slot / a.x_div, 0), a.R - 1);
-  const T* const x = static_cast<const T*>(a.x) + row * a.ldx + quad * U;
+  const T* x[MB];
+#pragma unroll
+  for (int b = 0; b < MB; ++b) {
+    const int slot = slot_at(a.order, it.p0 + min(16 * b + c16, it.rows - 1));
+    const int64_t row = min(max(slot / a.x_div, 0), a.R - 1);
+    x[b] = static_cast<const T*>(a.x) + row * a.ldx + quad * U;
+  }
   const T* const w = static_cast<const T*>(a.w) + it.e * a.w_se;
   const T* wp[4];
   if constexpr (W_ACROSS) {
@@ -880,11 +880,12 @@ __global__ void __launch_bounds__(kRowsWaves * 64, 4) expert_mm_rows(ExpertArgs 
       wp[t] = w + (int64_t)min(n0 + 16 * t + c16, a.N - 1) * a.ldw + quad * U;
   }
   const T* const zero = reinterpret_cast<const T*>(kZeros);
-  using C = Chunk<T, W_ACROSS>;
+  using C = Chunk<T, W_ACROSS, MB>;
   auto load = [&](C& v, int c) {
     const int k = c * CHUNK;
     const bool in = k + quad * U < a.K;                // K % U == 0
-    v.x = load_global<u32x4>(in ? x + k : zero);
+#pragma unroll
+    for (int b = 0; b < MB; ++b) v.x[b] = load_global<u32x4>(in ? x[b] + k : zero);
     if constexpr (W_ACROSS) {
       const T* const p = wp[0] + k * a.ldw;
 #pragma unroll
@@ -895,7 +896,7 @@ __global__ void __launch_bounds__(kRowsWaves * 64, 4) expert_mm_rows(ExpertArgs 
       for (int t = 0; t < 4; ++t) v.w[t] = load_global<u32x4>(in ? wp[t] + k : zero);
     }
   };
-  f32x4 acc[4] = {};
+  f32x4 acc[MB][4] = {};
   auto consume = [&](const C& v) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -909,14 +910,19 @@ __global__ void __launch_bounds__(kRowsWaves * 64, 4) expert_mm_rows(ExpertArgs 
         } else {
           f = v.w[t];
         }
-        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-            __builtin_bit_cast(bf16x8, f), __builtin_bit_cast(bf16x8, v.x), acc[t], 0, 0, 0);
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+          acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f),
+                                                              __builtin_bit_cast(bf16x8, v.x[b]),
+                                                              acc[b][t], 0, 0, 0);
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-              __uint_as_float(W_ACROSS ? v.w[j][t] : v.w[t][j]), __uint_as_float(v.x[j]), acc[t],
-              0, 0, 0);
+#pragma unroll
+          for (int b = 0; b < MB; ++b)
+            acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                __uint_as_float(W_ACROSS ? v.w[j][t] : v.w[t][j]), __uint_as_float(v.x[b][j]),
+                acc[b][t], 0, 0, 0);
       }
     }
   };
@@ -945,23 +951,42 @@ __global__ void __launch_bounds__(kRowsWaves * 64, 4) expert_mm_rows(ExpertArgs 
   for (int d = 0; d < kDepth; ++d)
     if (c + kDepth + d < end) consume(v[d]);
 
-  // a lane has row c16 and of column block t the columns 4 quad + r
 #pragma unroll
-  for (int t = 0; t < 4; ++t)
+  for (int b = 0; b < MB; ++b) {
+    if (b > 0) __syncthreads();
+    // a lane has row c16 and of column block t the columns 4 quad + r
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      part[wave][c16][W_ACROSS ? 16 * quad + 4 * r + t : 16 * t + 4 * quad + r] = acc[t][r];
-  __syncthreads();
-  // row m of the item to threads m, m + 16 ..: neighbouring threads have
-  // neighbouring columns
-  for (int i = threadIdx.x; i < it.rows * cols; i += kRowsWaves * 64) {
-    const int m = i / cols, n = i - m * cols, at = blockIdx.x * cols + n;
-    const int s = slot_at(a.order, it.p0 + m);
-    if (at >= a.N || s < 0 || s >= a.S) continue;
-    float sum = 0.0f;
-    for (int j = 0; j < ks; ++j) sum += part[((n >> 6) << log_ks) + j][m][n & 63];
-    put(a.out, a.out_dtype, s * a.ldo + at, a.row_scale ? sum * a.row_scale[s] : sum);
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        part[wave][c16][W_ACROSS ? 16 * quad + 4 * r + t : 16 * t + 4 * quad + r] = acc[b][t][r];
+    __syncthreads();
+    // row m of the block to threads m, m + 16 ..: neighbouring threads have
+    // neighbouring columns
+    const int rows = min(it.rows - 16 * b, 16);
+    for (int i = threadIdx.x; i < rows * cols; i += kRowsWaves * 64) {
+      const int m = i / cols, n = i - m * cols, at = blockIdx.x * cols + n;
+      const int s = slot_at(a.order, it.p0 + 16 * b + m);
+      if (at >= a.N || s < 0 || s >= a.S) continue;
+      float sum = 0.0f;
+      for (int j = 0; j < ks; ++j) sum += part[((n >> 6) << log_ks) + j][m][n & 63];
+      put(a.out, a.out_dtype, s * a.ldo + at, a.row_scale ? sum * a.row_scale[s] : sum);
+    }
   }
+}
+
+template <typename T, bool W_ACROSS>
+__global__ void __launch_bounds__(kRowsWaves * 64, 4) expert_mm_rows(ExpertArgs a, int item0,
+                                                                     int bm, int log_ks) {
+  __shared__ __attribute__((aligned(16))) float part[kRowsWaves][16][68];
+  const int item = item0 + blockIdx.y, cols = (kRowsWaves >> log_ks) * 64;
+  const Item it = find_item(a.offsets, a.E, a.S, bm, item);
+  zero_rows(a, blockIdx.x * cols, cols, item, gridDim.y);
+  if (it.rows == 0) return;
+  if constexpr (!W_ACROSS) {
+    if (it.rows > 16) return expert_rows_item<T, W_ACROSS, 2>(a, it, log_ks, part);
+  }
+  expert_rows_item<T, W_ACROSS, 1>(a, it, log_ks, part);
 }
 
 Divisor divisor(uint32_t d) {
@@ -972,22 +997,33 @@ Divisor divisor(uint32_t d) {
 
 template <typename T, bool W_ACROSS>
 void launch_rows(const ExpertArgs& a, hipStream_t st) {
-  const int64_t act = a.E < a.S ? a.E : a.S, items = ((int64_t)a.S + act * 15) / 16;
-  const int64_t groups = ((int64_t)a.N + 63) / 64;
-  // Waves that fill the chip; experts of more than 6 rows on average have
-  // second items, which read the weights again: better while they are read
-  // first, so all of a workgroup's waves take the same columns (32 tokens x 8
-  // of 32 experts of 2048 x 4096: 175 and 140 us; 33 x 4 of 16 of 4099 x 1024
-  // fp32: 99 and 78; 8 x 8 of 32, two rows: 105 and 112).
-  const int64_t target = a.S <= 6 * act ? 2048 : 8192;
-  const int64_t busy = (a.S + act * 8) / 16 + 1;
+  const int64_t act = a.E < a.S ? a.E : a.S, groups = ((int64_t)a.N + 63) / 64;
+  // (64 x 2 of 8 of 1024 x 2048: 14.3 us in items of 16, 16.3 of 32; others below)
+  const int bm = W_ACROSS || act * groups < 256 ? 16 : 32;
+  const int64_t items = ((int64_t)a.S + act * (bm - 1)) / bm;
+  // Waves that fill the chip, in workgroups of even cost.  Along: 1024 groups
+  // in 1, 2, 4 or 8 ranges take 176, 126, 106, 112 us (8 tokens x 8 of 32
+  // experts of 2048 x 4096); where experts have items of either kind, 150,
+  // 129, 125, 108 (128 x 4 of 16 of 4096 x 1024 fp32).  Across, an expert's
+  // second item reads the weights again: better while the first does, so all
+  // waves take the same columns then (64 x 4 of 16 of 4096 x 1024 fp32: 266,
+  // 141, 81, 78 us; 32 x 8 of 32 of 2048 x 4096: 124, 109, 106, 111; 16 x 8:
+  // 92, 94, 95, 103).
+  int64_t busy, target;
+  if (W_ACROSS) {
+    busy = (a.S + act * 8) / 16 + 1;
+    target = a.S <= 6 * act ? 2048 : 8192;
+  } else {
+    busy = a.S <= 16 * act ? act : (a.S + act * 16) / 32;
+    target = a.S <= 16 * act ? 4096 : 32768;
+  }
   int log_ks = 0;
   while (log_ks < 3 && (busy * groups << log_ks) < target) ++log_ks;
   const int64_t ntn = (groups + (8 >> log_ks) - 1) / (8 >> log_ks);
   for (int64_t i = 0; i < items; i += 65535)        // at most so many items a launch
     hipLaunchKernelGGL((expert_mm_rows<T, W_ACROSS>),
                        dim3((unsigned)ntn, (unsigned)(items - i < 65535 ? items - i : 65535)),
-                       dim3(kRowsWaves * 64), 0, st, a, (int)i, log_ks);
+                       dim3(kRowsWaves * 64), 0, st, a, (int)i, bm, log_ks);
 }
 
 void launch_reduce(const float* parts, int splits, void* out, bsmm_dtype dt, int64_t rows,

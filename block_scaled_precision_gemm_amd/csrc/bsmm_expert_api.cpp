@@ -78,7 +78,7 @@ Choice mm_plan(const ExpertArgs& a, size_t room) {
     return n > act ? n : act;
   };
   auto tiles = [&](int64_t bm, int64_t bn) { return items(bm) * (((int64_t)a.N + bn - 1) / bn); };
-  const int64_t few = !bf16 ? 32 : a.w_across || tiles(256, 256) < 256 ? 16 : 6;
+  const int64_t few = bf16 ? 16 : a.w_across ? 32 : 48;
   if (rows && a.S <= few * act) return Choice{ExpertPlan::Rows, 1, 0, 0};
   const double outs = (double)a.S * a.N;
   const int64_t steps = ((int64_t)a.K + 63) / 64;

@@ -67,6 +67,28 @@ def test_gradient_runs(loads, dt):
         assert np.array_equal(host(got), torch.from_numpy(want).to(torch.bfloat16).double().numpy())
 
 
+# on average 16 rows or fewer, with items of one block of 16, of two, and second items
+FEW = [[0, 1, 15, 16, 17, 31, 32, 33, 64, 5, 0, 2, 20, 3, 1, 0], [1] * 16, [20, 12] * 8]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("back", [False, True])
+@pytest.mark.parametrize("N,K", [(1030, 40), (1024, 1032), (4100, 8), (200, 520)])
+@pytest.mark.parametrize("loads", FEW, ids=lambda v: f"{len(v)}x{max(v)}")
+def test_few_rows(loads, N, K, back, dt):
+    rng = np.random.default_rng(sum(loads) + N)
+    if back:
+        N, K = K, N // 8 * 8                              # [E, K, N] in memory, rows of 8
+    off, S, E = sorted_offsets(loads), sum(loads) + 5, len(loads)
+    x, w = ints(rng, S, K, top=2), ints(rng, E, N, K, top=2)
+    wg = dev(w.transpose(0, 2, 1).copy(), TDT[dt]).transpose(1, 2) if back else dev(w, TDT[dt])
+    order = rng.permutation(S).astype(np.int32)
+    scale = np.exp2(rng.integers(-2, 3, S)).astype(np.float32)
+    got = bsmm.bsmm_expert_mm(dev(x, TDT[dt]), wg, dev(order), dev(off), row_scale=dev(scale),
+                              out_dtype="f32")
+    assert np.array_equal(host(got), X.expert_mm(x, w, order, off, 1, scale))
+
+
 PARTS = [  # few tiles and a long contraction
     ("mm", 300, 2, 130, 4096), ("mm", 300, 2, 130, 4099), ("mm", 70, 1, 64, 9000),
     ("wgrad", 9000, 1, 64, 72), ("wgrad", 9000, 2, 33, 31), ("wgrad", 20000, 1, 256, 512),
