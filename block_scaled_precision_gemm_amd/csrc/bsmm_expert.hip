@@ -216,6 +216,23 @@ __device__ __forceinline__ void zero_rows(const ExpertArgs& a, int n0, int cols,
   }
 }
 
+// A workgroup's tile of `rows` x cols of them (false: none).  Tiles are ordered
+// in groups of `group` rows by all columns, and runs of `run` of them dealt out
+// to the XCDs (hardware ids go round robin over 8): the workgroups that an XCD
+// holds at a time share operands in its L2, and experts that have many rows,
+// or items that do not exist, fall to all XCDs alike.
+__device__ __forceinline__ bool deal_tile(int rows, int cols, int run, int group, int& row,
+                                          int& col) {
+  const int xcd = blockIdx.x & 7, local = blockIdx.x >> 3, turn = local / run;
+  const int id = (turn * 8 + xcd) * run + (local - turn * run);
+  if (id >= rows * cols) return false;
+  const int width = group * cols, g = id / width, first = group * g, n = min(rows - first, group);
+  const int in = id - g * width;
+  row = first + in % n;
+  col = in / n;
+  return true;
+}
+
 // A call whose tiles are few is cut along the contraction too: `splits` parts,
 // fp32, one behind the other in the workspace (the launch's out), which
 // reduce_parts adds in order.  These find the part of an item and its range,
@@ -269,14 +286,14 @@ __global__ void __launch_bounds__(256) reduce_parts(const float* __restrict__ pa
 // ---------------------------------------------------------------------------
 template <typename T, int MB, bool W_ACROSS>
 __global__ void __launch_bounds__(256, 2) expert_mm_kernel(ExpertArgs a, int items, int ntn,
-                                                           int splits) {
+                                                           int splits, int run) {
   constexpr int U = Elem<T>::U, STEP = Elem<T>::STEP, TILE = 64 * MB, BYTES = TILE * 128;
   constexpr int UPR = TILE / U, NU = 2 * MB;          // units of an across row, of a thread
   __shared__ __attribute__((aligned(1024))) uint8_t smem[4 * BYTES];
   __shared__ int slots[TILE];
   __shared__ float scales[TILE];
   int item, tn, s0, s1;
-  tile_of(items * splits, ntn, item, tn);
+  if (!deal_tile(items * splits, ntn, run, 4, item, tn)) return;
   part_of(a, items, splits, STEP, item, s0, s1);
   const Item it = find_item(a.offsets, a.E, a.S, TILE, item);
   const int n0 = tn * TILE;
@@ -349,13 +366,13 @@ __global__ void __launch_bounds__(256, 2) expert_mm_kernel(ExpertArgs a, int ite
 // CODES: x is an 8-bit checkpoint.
 template <typename T, int MB, bool CODES>
 __global__ void __launch_bounds__(256, 2) expert_wgrad_kernel(WgradArgs a, int ntn, int ntk,
-                                                              int splits, Divisor yd,
+                                                              int splits, int run, Divisor yd,
                                                               Divisor xd) {
   constexpr int U = Elem<T>::U, STEP = Elem<T>::STEP, TILE = 64 * MB, BYTES = TILE * 128;
   constexpr int UPR = TILE / U, NU = 2 * MB;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[4 * BYTES];
   int item, tk, lo, hi;
-  tile_of(splits * a.E * ntn, ntk, item, tk);
+  if (!deal_tile(splits * a.E * ntn, ntk, run, 1, item, tk)) return;
   const int e = run_of(a, ntn, splits, STEP, item, lo, hi);
   const int n0 = item % ntn * TILE, k0 = tk * TILE;
 
@@ -679,13 +696,22 @@ __device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& 
     int wave, lane, n0, xk;
     uint32_t at;
     const uint16_t* w;
-    int s0;
+    int s0, n, turn;
+    // Step s of the walk, which an expert starts `turn` steps in.  All tiles
+    // walk at a time, and experts a power of two of bytes apart would take the
+    // same memory channels (64 rows x 32 experts of 2048 x 4096: 127 us, 99
+    // with the turn, 98 without it at 2048 x 4160).  It follows from the expert
+    // alone, and so does the order of the sums.
+    __device__ __forceinline__ int step(int s) const {
+      s += turn;
+      return s0 + (s < n ? s : s - n);
+    }
     const uint16_t* xp[MI];
     const uint16_t* wp[4];
     u32x4 xv[MI];
     Turn v;
     __device__ __forceinline__ const uint16_t* along(bool last, const uint16_t* p, int s) const {
-      s += s0;
+      s = step(s);
       return !last || s * 64 + xk < a.K ? p + s * 64 : reinterpret_cast<const uint16_t*>(kZeros);
     }
     __device__ __forceinline__ void direct_a(bool last, int s, uint8_t* slot, int i) {
@@ -699,7 +725,7 @@ __device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& 
       if (i < MI) {
         xv[i] = load_global<u32x4>(along(last, xp[i], s));
       } else {
-        const int k = (s0 + s) * 64 + wave * 8 + i - MI;
+        const int k = step(s) * 64 + wave * 8 + i - MI;
         const uint16_t* row = w + (int64_t)k * a.ldw + n0;
         if (last) row = k < a.K ? row : reinterpret_cast<const uint16_t*>(kZeros);
         v.row[i - MI] = load_global<u32x2>(reinterpret_cast<const uint8_t*>(row) + at);
@@ -711,7 +737,8 @@ __device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& 
     }
   } ops{a, wave, lane, n0, ((lane & 7) ^ swz(8 * wave + (lane >> 3))) * 8,
         (uint32_t)min(4 * lane, a.N - 4 - n0) * 2,
-        static_cast<const uint16_t*>(a.w) + it.e * a.w_se, s0, {}, {}, {}, {}};
+        static_cast<const uint16_t*>(a.w) + it.e * a.w_se, s0, s1 - s0,
+        a.K % 64 == 0 && s1 > s0 ? it.e % (s1 - s0) : 0, {}, {}, {}, {}};
 #pragma unroll
   for (int t = 0; t < MI; ++t) {
     const int s = max(slots[64 * t + 8 * wave + (lane >> 3)], 0);
@@ -745,11 +772,12 @@ __device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& 
 
 template <bool W_ACROSS>
 __global__ void __launch_bounds__(512, 2) expert_mm_wide(ExpertArgs a, int rows, int items,
-                                                         int ntn, int splits, int vec) {
+                                                         int ntn, int splits, int run, int vec) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-  // groups of 4 items: half of an XCD's 32 workgroups (8 and 2 were within 1 %)
+  // groups of 4 items (1, 2 and 8 were within 2 %; one expert of 8192^3: 8 the
+  // same, 2 and 1 took 2 and 7 % more)
   int item, tn, s0, s1;
-  tile_of(items * splits, ntn, item, tn, 4);
+  if (!deal_tile(items * splits, ntn, run, 4, item, tn)) return;
   part_of(a, items, splits, 64, item, s0, s1);
   const Item it = find_item(a.offsets, a.E, a.S, rows, item);
   const int n0 = tn * kWide;
@@ -765,11 +793,11 @@ __global__ void __launch_bounds__(512, 2) expert_mm_wide(ExpertArgs a, int rows,
 }
 
 __global__ void __launch_bounds__(512, 2) expert_wgrad_wide(WgradArgs a, int ntn, int ntk,
-                                                            int splits, Divisor yd, Divisor xd,
-                                                            int vec) {
+                                                            int splits, int run, Divisor yd,
+                                                            Divisor xd, int vec) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   int item, tk, lo, hi;
-  tile_of(splits * a.E * ntn, ntk, item, tk);
+  if (!deal_tile(splits * a.E * ntn, ntk, run, 1, item, tk)) return;
   const int e = run_of(a, ntn, splits, 64, item, lo, hi);
   const int n0 = item % ntn * 256, k0 = tk * kWide, lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -881,6 +909,9 @@ __device__ __forceinline__ void expert_rows_item(const ExpertArgs& a, const Item
   }
   const T* const zero = reinterpret_cast<const T*>(kZeros);
   using C = Chunk<T, W_ACROSS, MB>;
+  const int chunks = (int)(((unsigned)a.K + CHUNK - 1) / CHUNK), per = (chunks + ks - 1) >> log_ks;
+  int c = min(kw * per, chunks);
+  const int end = n0 < a.N ? min(c + per, chunks) : c;
   auto load = [&](C& v, int c) {
     const int k = c * CHUNK;
     const bool in = k + quad * U < a.K;                // K % U == 0
@@ -926,9 +957,6 @@ __device__ __forceinline__ void expert_rows_item(const ExpertArgs& a, const Item
       }
     }
   };
-  const int chunks = (int)(((unsigned)a.K + CHUNK - 1) / CHUNK), per = (chunks + ks - 1) >> log_ks;
-  int c = min(kw * per, chunks);
-  const int end = n0 < a.N ? min(c + per, chunks) : c;
   C v[kDepth];
 #pragma unroll
   for (int d = 0; d < kDepth; ++d)
@@ -1038,6 +1066,24 @@ int vec_rows(const void* p, int64_t ld, bsmm_dtype dt) {
   return aligned(p, 16) && ld % (dt == BSMM_BF16 ? 8 : 4) == 0;
 }
 
+// Runs of tiles for deal_tile, and the grid.  Runs of 8, so that the XCDs' work
+// is even: with an eighth of the grid to each, most of the items that do not
+// exist fell to the last XCDs, and an expert's tiles to one (300 tokens x 8 of
+// 32 experts of 2048 x 4096: 128 us in runs of 8, 162 in eighths; 4096 x 8 of
+// 64, input gradient: 699 and 793; 4096 x 8 of 32, weight gradient: 682 and
+// 784; runs of 16, 32, 64 there: 701, 744, 754).  One expert's tiles are even,
+// and neighbours share more operands in eighths (2048 x 4096 x 4096: 62 us,
+// 65 in runs of 8).
+struct Deal {
+  int run;
+  dim3 grid;
+  Deal(int64_t tiles, int64_t real, bool one) {
+    const int64_t eighth = (real + 7) / 8;
+    run = (int)(one || eighth < 8 ? eighth : 8);
+    grid = dim3((unsigned)((tiles + 8 * run - 1) / (8 * run) * (8 * run)));
+  }
+};
+
 template <typename T, bool W_ACROSS>
 void launch_mm(ExpertArgs a, ExpertPlan plan, int rows, int splits, void* ws, hipStream_t st) {
   if (plan == ExpertPlan::Rows) return launch_rows<T, W_ACROSS>(a, st);
@@ -1053,18 +1099,22 @@ void launch_mm(ExpertArgs a, ExpertPlan plan, int rows, int splits, void* ws, hi
   const int bn = plan == ExpertPlan::Wide ? kWide : plan == ExpertPlan::Tiles128 ? 128 : 64;
   const int bm = plan == ExpertPlan::Wide ? rows : bn;
   const int items = (int)(((int64_t)a.S + act * (bm - 1)) / bm), ntn = (a.N + bn - 1) / bn;
-  const dim3 grid((unsigned)((int64_t)items * splits * ntn));
+  int64_t real = ((int64_t)a.S + act * (bm / 2)) / bm;
+  if (real < act) real = act;
+  const Deal deal((int64_t)items * splits * ntn, (real < items ? real : items) * splits * ntn,
+                  act == 1);
+  const dim3 grid = deal.grid;
   if (plan == ExpertPlan::Wide) {
     if constexpr (sizeof(T) == 2)
       hipLaunchKernelGGL((expert_mm_wide<W_ACROSS>), grid, dim3(512), kWideBytes, st, a, rows, items,
-                         ntn, splits, vec_rows(a.out, a.ldo, a.out_dtype));
+                         ntn, splits, deal.run, vec_rows(a.out, a.ldo, a.out_dtype));
   } else if (plan == ExpertPlan::Tiles128) {
     if constexpr (sizeof(T) == 2)
       hipLaunchKernelGGL((expert_mm_kernel<T, 2, W_ACROSS>), grid, dim3(256), 0, st, a, items, ntn,
-                         splits);
+                         splits, deal.run);
   } else {
     hipLaunchKernelGGL((expert_mm_kernel<T, 1, W_ACROSS>), grid, dim3(256), 0, st, a, items, ntn,
-                       splits);
+                       splits, deal.run);
   }
   if (splits > 1)
     launch_reduce(static_cast<const float*>(ws), splits, out, dt, a.S, a.N, a.S, 0, ldo, st);
@@ -1072,14 +1122,16 @@ void launch_mm(ExpertArgs a, ExpertPlan plan, int rows, int splits, void* ws, hi
 
 template <typename T, int MB>
 void launch_wgrad_tiles(const WgradArgs& a, int ntn, int ntk, int splits, hipStream_t st) {
-  const dim3 grid((unsigned)((int64_t)splits * a.E * ntn * ntk)), block(256);
+  const int64_t tiles = (int64_t)splits * a.E * ntn * ntk;
+  const Deal deal(tiles, tiles, false);
+  const dim3 grid = deal.grid, block(256);
   const Divisor yd = divisor(a.y_div), xd = divisor(a.x_div);
   if (a.x_scale)
     hipLaunchKernelGGL((expert_wgrad_kernel<T, MB, true>), grid, block, 0, st, a, ntn, ntk, splits,
-                       yd, xd);
+                       deal.run, yd, xd);
   else
     hipLaunchKernelGGL((expert_wgrad_kernel<T, MB, false>), grid, block, 0, st, a, ntn, ntk, splits,
-                       yd, xd);
+                       deal.run, yd, xd);
 }
 
 template <typename T>
@@ -1096,10 +1148,11 @@ void launch_wgrad(WgradArgs a, ExpertPlan plan, int splits, void* ws, hipStream_
   const int tile = plan == ExpertPlan::Wide ? 256 : plan == ExpertPlan::Tiles128 ? 128 : 64;
   const int ntn = (a.N + tile - 1) / tile, ntk = (a.K + tile - 1) / tile;
   if (plan == ExpertPlan::Wide) {
+    const int64_t tiles = (int64_t)splits * a.E * ntn * ntk;
+    const Deal deal(tiles, tiles, false);
     if constexpr (sizeof(T) == 2)
-      hipLaunchKernelGGL(expert_wgrad_wide, dim3((unsigned)((int64_t)splits * a.E * ntn * ntk)),
-                         dim3(512), kWideBytes, st, a, ntn, ntk, splits, divisor(a.y_div),
-                         divisor(a.x_div),
+      hipLaunchKernelGGL(expert_wgrad_wide, deal.grid, dim3(512), kWideBytes, st, a, ntn, ntk,
+                         splits, deal.run, divisor(a.y_div), divisor(a.x_div),
                          vec_rows(a.dw, a.ldw, a.out_dtype) &&
                              vec_rows(a.dw, a.w_se, a.out_dtype));
   } else if (plan == ExpertPlan::Tiles128) {

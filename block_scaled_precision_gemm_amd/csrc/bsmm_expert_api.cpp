@@ -28,17 +28,13 @@ struct Choice { ExpertPlan plan; int splits; double us; int rows; };
 // a seventh (300 tokens x 4 of 16 experts of 2048 x 2048 bf16: 43 us in one
 // range, 60 in two; 4000 x 2 of 4 of 300 x 200, weight gradient: 62 us in one,
 // 29 in eight).
-//
-// guess: the number of tiles is one (the experts' loads are not known on the
-// host), so a last round that is nearly full may take another one.
 Choice best_split(ExpertPlan plan, int64_t tiles, int64_t steps, double outs, double step_us,
-                  double each_us, double fixed, size_t room, bool guess = false) {
+                  double each_us, double fixed, size_t room) {
   Choice best{plan, 1, 1e30, 0};
   for (int s = 1; s <= 16 && (s == 1 || steps >= 4 * s); ++s) {
     if (s > 1 && (outs * 4 * s > (double)room || tiles * s > (int64_t)1 << 20)) break;
     const double t = (double)(tiles * s) / 256.0, whole = std::floor(t), rest = t - whole;
-    const double on_cu = whole + (rest > 0.0 ? 1.0 : 0.0) +
-                         (guess && rest > 0.8 ? (rest - 0.8) * 5.0 : 0.0);
+    const double on_cu = whole + (rest > 0.0 ? 1.0 : 0.0);
     const double step = each_us * on_cu > step_us ? each_us * on_cu : step_us;
     const double us = (double)((steps + s - 1) / s) * step + fixed * on_cu +
                       (s > 1 ? 8.0 + outs * 8 * s / 4e6 : 0.0);
@@ -47,21 +43,48 @@ Choice best_split(ExpertPlan plan, int64_t tiles, int64_t steps, double outs, do
   return best;
 }
 
+// The time of the wide tiles in us, in items of at most bm rows and `parts`
+// ranges of `steps` steps.  The experts' loads are not known on the host: a
+// third of them each with 0.6, 1 and 1.4 of the average.  A step of 64, 128,
+// 192 or 256 rows takes 0.62, 0.95, 1.25 or 1.55 us, a tile 6 besides; CUs take
+// tiles as they get free, so that all end within a fifth of a tile of each
+// other.  (Of 33 shapes' best heights of item this finds those that cost 1.6 %
+// more than the best on average, and 18 % at most.)
+double wide_us(const ExpertArgs& a, int64_t act, int bm, int64_t steps, int parts) {
+  static const double kStep[4] = {0.62, 0.95, 1.25, 1.55};
+  static const double kLoad[3] = {0.6, 1.0, 1.4};
+  const double each = (double)act / 3 * parts * (double)(((int64_t)a.N + 255) / 256);
+  double work = 0.0, longest = 0.0;
+  for (double part : kLoad) {
+    const int64_t load = (int64_t)((double)a.S / (double)act * (act > 1 ? part : 1.0)) + 1;
+    auto add = [&](int64_t rows, int64_t n) {
+      if (rows == 0 || n == 0) return;
+      const double us = (double)steps * kStep[(rows + 63) / 64 - 1] + 6;
+      work += (double)n * us * each;
+      if (us > longest) longest = us;
+    };
+    add(bm, load / bm);
+    add(load % bm, 1);
+  }
+  const double us = work / 256 + 0.2 * longest;
+  return us > longest ? us : longest;
+}
+
 bool aligned_rows(const void* p, int64_t ld, bsmm_dtype d) {
   return aligned(p, 16) && ld % (d == BSMM_BF16 ? 8 : 4) == 0;
 }
 
 // Measured (us; the average is of rows to an expert):
 //                                            Rows  Wide  Tiles64  Tiles128
-//   16 tokens x 8 of 32, 2048 x 4096 bf16     111   118                     (average 4)
-//   32 x 8 of 32, the same                    140   122                     (8)
-//   64 x 8 of 32, the same                    155   160                     (16)
-//   64 x 2 of 8, 1024 x 2048 bf16              14    20                     (16)
-//   64 x 8 of 32, input gradient bf16         120   141                     (16)
-//   96 x 8 of 32, the same                    136   137                     (24)
-//   64 x 4 of 16, 4096 x 1024 fp32             90          114              (16)
-//   128 x 4 of 16, the same                   129          130              (32)
-//   128 x 4 of 16, input gradient fp32        102          175              (32)
+//   1 token x 8 of 64, 2048 x 4096 bf16        33    32                     (64 tiles of 256)
+//   64 x 2 of 8, 1024 x 2048 bf16              14    17                     (32)
+//   32 x 2 of 8, 4096 x 8192 bf16             117   122                     (128)
+//   16 x 4 of 16, 4096 x 4096 bf16            111   105                     (256)
+//   8 x 8 of 32, 2048 x 4096 bf16             105    87                     (256)
+//   64 x 8 of 32, the same                    134    92                     (256)
+//   64 x 4 of 16, 4096 x 1024 fp32             78           96              (average 16)
+//   128 x 4 of 16, the same                   108           97              (32)
+//   128 x 4 of 16, input gradient fp32        102          118              (32)
 //   333 x 2 of 6, 1001 x 515 fp32                           22       50
 //   2000 x 4 of 16, 1001 x 2051 fp32                       381      448
 //   2000 x 4 of 16, 1001 x 2051 bf16                       122      107
@@ -78,30 +101,26 @@ Choice mm_plan(const ExpertArgs& a, size_t room) {
     return n > act ? n : act;
   };
   auto tiles = [&](int64_t bm, int64_t bn) { return items(bm) * (((int64_t)a.N + bn - 1) / bn); };
-  const int64_t few = bf16 ? 16 : a.w_across ? 32 : 48;
-  if (rows && a.S <= few * act) return Choice{ExpertPlan::Rows, 1, 0, 0};
+  const int64_t few = bf16 ? tiles(256, 256) < 256 ? 16 : 0 : a.w_across ? 32 : 24;
+  if (getenv("FEW") ? rows && a.S <= atoi(getenv("FEW"))*act : rows && a.S <= few * act) return Choice{ExpertPlan::Rows, 1, 0, 0};
   const double outs = (double)a.S * a.N;
   const int64_t steps = ((int64_t)a.K + 63) / 64;
   if (bf16 && rows) {
-    // Items of at most 256, 192 or 128 rows, whichever's rounds of tiles end
-    // first: a step of 64 rows takes 0.62 us, of 128 0.95, of 192 1.25, of 256
-    // 1.55, and any 1.65 where the weights come from HBM and not from the 256
-    // MB behind the L2s (512 tokens x 4 of 16, 2048 x 2048: 42 us in items of
-    // 128, 51 of 256; 1500 x 2 of 8, 2048 x 4096: 67 and 124; 1021 x 8 of 32,
-    // the same, 537 MB: 234 of 192, 216 of 256).
-    const bool hbm = (double)a.E * a.N * a.K * 2 > 256e6;
+    // Items of at most 256, 192 or 128 rows: fewer weights are read again, or
+    // the chip is fuller (1021 tokens x 8 of 32, 2048 x 4096: 194, 182, 198 us;
+    // 1500 x 4 of 16, 2048 x 2048: 57, 75, 67; 512 x 4 of 16, the same: 46, 41,
+    // 38).
     Choice best{ExpertPlan::Wide, 1, 1e30, 0};
-    for (int bm = 256; bm >= 128; bm -= 64) {
-      static const double kStep[4] = {0.62, 0.95, 1.25, 1.55};
-      // an expert of the average size, and half as many again
-      const int64_t most = ((int64_t)a.S + act - 1) / act * 3 / 2;
-      const double height = kStep[(most < bm ? (most + 63) / 64 : bm / 64) - 1];
-      const double step = hbm && height < 1.65 ? 1.65 : height;
-      Choice c = best_split(ExpertPlan::Wide, tiles(bm, 256), steps, outs, step, step, 8, room,
-                            act > 1);
-      c.rows = bm;
-      if (c.us < 0.97 * best.us) best = c;
-    }
+    for (int bm = 256; bm >= 128; bm -= 64)
+      for (int p = 1; p <= 16 && (p == 1 || steps >= 4 * p); ++p) {
+        if (p > 1 && (outs * 4 * p > (double)room || tiles(bm, 256) * p > (int64_t)1 << 20)) break;
+        double us = wide_us(a, act, bm, (steps + p - 1) / p, p);
+        if (p > 1) us += 8.0 + outs * 8 * p / 4e6;
+        // rather one range, and larger items
+        const double worth = (p > 1 && best.splits == 1 ? 1.17 : 1.0) *
+                             (bm < best.rows ? 1.03 : 1.0);
+        if (us * worth < best.us) best = Choice{ExpertPlan::Wide, p, us, bm};
+      }
     return best;
   }
   const Choice small = best_split(ExpertPlan::Tiles64, tiles(64, 64), bf16 ? steps : 2 * steps, outs,
