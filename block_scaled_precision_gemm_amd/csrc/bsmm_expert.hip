@@ -225,7 +225,7 @@ __device__ __forceinline__ bool deal_tile(int rows, int cols, int run, int group
                                           int& col) {
   const int xcd = blockIdx.x & 7, local = blockIdx.x >> 3, turn = local / run;
   const int id = (turn * 8 + xcd) * run + (local - turn * run);
-  if (id >= rows * cols) return false;
+  if ((unsigned)id >= (unsigned)(rows * cols)) return false;
   const int width = group * cols, g = id / width, first = group * g, n = min(rows - first, group);
   const int in = id - g * width;
   row = first + in % n;
@@ -263,7 +263,8 @@ __device__ __forceinline__ int run_of(WgradArgs& a, int ntn, int splits, int ste
 }
 
 // out(r, c) at out[(r / inner) * outer_ld + (r % inner) * ld + c] = the sum of
-// the parts' [rows, cols].
+// the parts' [rows, cols].  Bound by its launch and the parts' bytes, which the
+// plans count (bsmm_expert_api.cpp, best_split).
 __global__ void __launch_bounds__(256) reduce_parts(const float* __restrict__ parts, int splits,
                                                     void* out, bsmm_dtype dt, int64_t rows,
                                                     int cols, int64_t inner, int64_t outer_ld,
@@ -282,7 +283,11 @@ __global__ void __launch_bounds__(256) reduce_parts(const float* __restrict__ pa
 // Any type, alignment and size: tiles of 64 MB x 64 MB (four waves of 32 MB x
 // 32 MB), both operands through registers into two slots of LDS, in the layout
 // they have in memory; bf16 that lies across is transposed by the LDS read.
-// fp32 runs at the fp32 matrix instruction's rate.
+// fp32 runs at the fp32 matrix instruction's rate, a sixteenth of bf16's, which
+// bounds it where there are enough tiles (900 tokens x 4 of 16 experts of 1024
+// x 2048: 172 us, 88 of the 151 TFLOP/s of a large product); tiles of 64 are
+// for calls with few of 128 (333 x 2 of 6 of 1001 x 515: 22 and 50 us, its
+// weight gradient 17 us, all start and latency).
 // ---------------------------------------------------------------------------
 template <typename T, int MB, bool W_ACROSS>
 __global__ void __launch_bounds__(256, 2) expert_mm_kernel(ExpertArgs a, int items, int ntn,
@@ -437,19 +442,30 @@ __global__ void __launch_bounds__(256, 2) expert_wgrad_kernel(WgradArgs a, int n
 // in steps of 64.
 //
 // Both tiles stand in LDS as rows of 128 bytes with the contraction inside.
-// Operands that lie in memory that way go global -> LDS directly, as many
-// steps ahead as 156 KB hold.  The other kind goes through registers: a wave
-// has 8 neighbouring elements of the contraction (rows in memory) and a lane 4
-// columns, which it transposes with 16 byte permutations and writes as 4 x 16
-// bytes, the loads a step ahead.  (The transposing LDS read would spare that,
-// but the compiler waits for every direct load in flight before one, and
-// before an LDS write, so that a tile that needs one takes the other operand
-// through registers too.)
+// Operands that lie in memory that way go global -> LDS directly, two or three
+// steps ahead: the slots take all 160 KB.  The other kind goes through
+// registers: a wave has 8 neighbouring elements of the contraction (rows in
+// memory) and a lane 4 columns, which it transposes with 16 byte permutations
+// and writes as 4 x 16 bytes, the loads a step ahead.  (The transposing LDS
+// read would spare that, but the compiler waits for every direct load in flight
+// before one, and before an LDS write, so that a tile that needs one takes the
+// other operand through registers too.)
 //
 // The source order is the schedule: a turn's fragments are read during the
 // turn before, and the barrier stands before the last turn, whose products
 // then cover the first fragments of the next step.  After it nobody reads the
 // step's slot any more, and the direct loads of the step that gets it go out.
+//
+// The matrix cores bound long products: 8192^3 812 us (1354 TFLOP/s; the
+// library's rate for it is 1384), the input's gradient 957 us (1149: the
+// transposition takes turns of the vector unit and of LDS), the weights'
+// gradient 1010 us (1089).  A step of 256 rows takes 1.48, 1.68 and 1.7 us; a
+// tile 9.5 us besides, its first loads and its stores, 18 with fp32 results.
+// Experts' weights from HBM bound few rows (64 tokens x 8 of 32 of 2048 x 4096,
+// 537 MB: 92 us), and between the two the tiles that experts leave partly empty
+// (4096 x 8 of 64: 568 us, 968 TFLOP/s).  Slower: four waves of 128 x 128, two
+// workgroups a CU of 128 x 256 and steps of 32, groups of waves a turn apart,
+// workgroups that take tile after tile, full items first.
 // ---------------------------------------------------------------------------
 constexpr int kWide = 256;                      // columns of a tile
 __device__ const uint32_t kZeros[128] = {};     // a row of zeros
@@ -867,7 +883,11 @@ __global__ void __launch_bounds__(512, 2) expert_wgrad_wide(WgradArgs a, int ntn
 //
 // Everything goes straight to registers, kDepth chunks of 64 bytes (32 bf16 or
 // 16 fp32 of the contraction) ahead: no barrier, each weight byte is used by
-// one wave.  Along, a lane's 16 bytes are one column's.  Across, a lane has 4
+// one wave.  Bound by the weights' bytes (1 token x 8 of 64 experts of 2048 x
+// 4096 bf16, 134 MB: 33 us, 4.1 TB/s; 33 x 4 of 16 of 4099 x 1024 fp32, 268 MB:
+// 76 us, 3.5 TB/s, a few workgroups in a second round).  Items of 32 rows have
+// three chunks ahead, for their registers (64 x 4 of 16 of 4096 x 1024 fp32: 90
+// us in items of 16, 78 of 32); across, they spill.  Along, a lane's 16 bytes are one column's.  Across, a lane has 4
 // neighbouring columns: of bf16 8 rows, transposed by byte permutations, of
 // fp32 4 rows, each lane's 4 values then belonging to 4 column blocks.
 // ---------------------------------------------------------------------------

@@ -256,8 +256,8 @@ struct ExpertArgs {
   void* out; int64_t ldo; bsmm_dtype out_dtype;
   int E, R, S, N, K;
 };
-// Its kernels and the weight gradient's: items of 16 rows (aligned), tiles of
-// up to `rows` x 256 (aligned bf16; rows 128, 192 or 256), 128 x 128 or 64 x 64
+// Its kernels and the weight gradient's: items of 16 or 32 rows (aligned), tiles
+// of up to `rows` x 256 (aligned bf16; rows 128, 192 or 256), 128 x 128 or 64 x 64
 // (anything).  splits > 1: ranges of the contraction, their sums in ws (splits
 // * S * N fp32).
 enum class ExpertPlan { Rows, Wide, Tiles128, Tiles64 };
@@ -265,9 +265,9 @@ int launch_expert_mm(const ExpertArgs& a, ExpertPlan plan, int rows, int splits,
                      void* stream);
 
 // The weights' gradient: dw[e] (row stride ldw) sums dy[s / y_div]^T x[s /
-// x_div] over the slots of e; slots outside [0, S) add nothing.  x_scale null:
-// x of dy's type; else x is int8 codes with e8m0 bytes x_scale[row * s_r + k /
-// 32].
+// x_div] over the slots of e.  A slot outside [0, S) makes its expert's sums
+// undefined, but leads to no access outside the operands.  x_scale null: x of
+// dy's type; else x is int8 codes with e8m0 bytes x_scale[row * s_r + k / 32].
 struct WgradArgs {
   const void* dy; int64_t ldy; bsmm_dtype dtype; int y_div;
   const void* x; int64_t ldx; int x_div;

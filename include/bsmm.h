@@ -552,7 +552,9 @@ bsmm_status bsmm_expert_mm(const void* x, int64_t ldx, const void* w, int64_t w_
  *        k/32] (K % 32 == 0)
  *   dw   (e, n, k) at dw[e*w_se + n*ldw + k], fp32 or bf16 (RNE)
  * An expert without slots gets zeros.  order NULL: slot i at position i (E =
- * 1 and offsets {0, S}: a dense layer's gradient).  S <= Ry *
+ * 1 and offsets {0, S}: a dense layer's gradient).  Offsets that do not rise
+ * and slots outside [0, S) give undefined sums, but no access outside the
+ * operands.  S <= Ry *
  * dy_slots_per_row and S <= Rx * x_slots_per_row.  Sums, sizes, alignment and
  * workspace as for bsmm_expert_mm (a checkpoint: rows of codes at multiples
  * of 8 bytes are faster).  E, N or K 0 does nothing; S == 0 writes zeros.
@@ -576,7 +578,7 @@ bsmm_status bsmm_expert_wgrad(const void* dy, int64_t ldy, bsmm_dtype dtype, int
  * an e8m0 byte per 32 elements of a row, the OCP microscaling format MXINT8.
  * With amax = m * 2^p the block's largest magnitude, m in [1, 2):
  *   scale(r, c) = max(p + 127, 0), 127 for amax 0
- *   q(r, k)     = rne(x * 2^(6-p)) within +-127
+ *   q(r, k)     = rne(x * 2^(133 - scale)) within +-127
  *   value       = q * 2^(scale - 133): at most 7 bits, exact in bf16 and fp32
  * A block with an infinity or a NaN gets byte 255 and codes 0 and stands for
  * NaNs.  values (NULL or [R, K] of x's type, row stride ldv): the values.

@@ -36,7 +36,7 @@ LOADS = [
 def test_item_heights(loads, back, dt):
     rng = np.random.default_rng(sum(loads))
     off, S, E = sorted_offsets(loads), sum(loads) + 5, len(loads)      # 5 slots without an expert
-    for N, K in ((264, 72), (40, 328), (520, 8)):
+    for N, K in ((264, 72), (40, 328), (520, 8), (320, 640)):
         w = ints(rng, E, N, K, top=2)
         x = ints(rng, S, N if back else K, top=2)
         wg, wh = (dev(w, TDT[dt]).transpose(1, 2), w.transpose(0, 2, 1)) if back else \
