@@ -64,30 +64,41 @@ __device__ __forceinline__ u32x4 fetch(const T* p, int left) {
   return v;
 }
 
-// The same from 8-bit codes and their block's exponent byte.
-template <typename T>
-__device__ __forceinline__ u32x4 fetch_codes(const int8_t* p, const uint8_t* scale, int left) {
-  constexpr int U = Elem<T>::U;
-  if (left <= 0) return u32x4{0, 0, 0, 0};          // whole blocks: all or nothing
+// The same from 8-bit codes and their block's exponent byte, in two halves, so
+// that nothing waits for the load before the values are wanted.
+struct Codes {
   uint32_t c[2];
-  __builtin_memcpy(c, p, U);
+  int byte;
+};
+template <typename T>
+__device__ __forceinline__ Codes fetch_codes(const int8_t* p, const uint8_t* scale, int left) {
+  Codes v{{0, 0}, 127};
+  if (left > 0) {                                   // whole blocks: all or nothing
+    __builtin_memcpy(v.c, p, Elem<T>::U);
+    v.byte = *scale;
+  }
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ u32x4 value_of(const Codes& q) {
   // 2^(byte - 133), 255 a NaN
-  const int b = *scale;
-  const float s = b == 255 ? __builtin_nanf("") : __builtin_ldexpf(1.0f, b - 133);
+  const float s = q.byte == 255 ? __builtin_nanf("") : __builtin_ldexpf(1.0f, q.byte - 133);
   u32x4 v;
-  if constexpr (U == 8) {
+  if constexpr (Elem<T>::U == 8) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t w = c[i >> 1] >> (16 * (i & 1));
+      const uint32_t w = q.c[i >> 1] >> (16 * (i & 1));
       const float lo = (float)(int8_t)(w & 0xFF) * s, hi = (float)(int8_t)((w >> 8) & 0xFF) * s;
       v[i] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __float_as_uint((float)(int8_t)((c[0] >> (8 * i)) & 0xFF) * s);
+    for (int i = 0; i < 4; ++i)
+      v[i] = __float_as_uint((float)(int8_t)((q.c[0] >> (8 * i)) & 0xFF) * s);
   }
   return v;
 }
+template <typename T> __device__ __forceinline__ u32x4 value_of(u32x4 v) { return v; }
 
 // Fragments of turn t (a quarter of the tile's 128 bytes) for 32 rows or
 // columns from c0.  A lane holds 16 bytes of one row: of bf16 the 8 elements
@@ -136,38 +147,51 @@ __device__ __forceinline__ f32x16 product(u32x4 a, u32x4 b, f32x16 c) {
   }
 }
 
+// Steps that are on their way in registers while one is multiplied (1000 tokens
+// x 4 of 32 experts of 1024 x 1024 fp32: 128 us with one, 116 with two, 118
+// with three; 4000 x 2 of 8 of 1001 x 2051 bf16: 101, 97, 94, but its weight
+// gradient 124, 120, 127)
+constexpr int kAhead = 2;
+
 // A wave's 32 MB x 32 MB of the tile's products over `steps` steps of the
-// contraction; load(s) brings step s to the thread's registers, store(buffer)
-// takes them to LDS.
+// contraction; load(d, s) brings step s to the thread's registers of set d,
+// store(d, buffer) takes them to LDS.
 template <typename T, int MB, bool A_ACROSS, bool B_ACROSS, typename Load, typename Store>
 __device__ __forceinline__ void tile_products(uint8_t* smem, int steps, f32x16 (&acc)[MB][MB],
                                               const Load& load, const Store& store) {
-  constexpr int BYTES = 64 * MB * 128;
+  constexpr int BYTES = 64 * MB * 128, D = kAhead;
   const int wave = threadIdx.x >> 6, wm = (wave >> 1) * 32 * MB, wn = (wave & 1) * 32 * MB;
-  if (steps > 0) {
-    load(0);
-    store(smem);
-  }
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+    if (d < steps) load(d, d);
+  if (steps > 0) store(0, smem);
+  if (D < steps) load(0, D);
   __syncthreads();
-  for (int s = 0; s < steps; ++s) {
-    const uint8_t* at = smem + (s & 1) * 2 * BYTES;
-    const uint8_t* bt = at + BYTES;
-    if (s + 1 < steps) load(s + 1);
+  for (int s0 = 0; s0 < steps; s0 += D) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      u32x4 a[MB], b[MB];
+    for (int d = 0; d < D; ++d) {
+      const int s = s0 + d;
+      if (s >= steps) break;
+      const uint8_t* at = smem + (s & 1) * 2 * BYTES;
+      const uint8_t* bt = at + BYTES;
 #pragma unroll
-      for (int i = 0; i < MB; ++i) {
-        a[i] = A_ACROSS ? frag_across<T, MB>(at, wm + 32 * i, t) : frag_along(at, wm + 32 * i, t);
-        b[i] = B_ACROSS ? frag_across<T, MB>(bt, wn + 32 * i, t) : frag_along(bt, wn + 32 * i, t);
+      for (int t = 0; t < 4; ++t) {
+        u32x4 a[MB], b[MB];
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+          a[i] = A_ACROSS ? frag_across<T, MB>(at, wm + 32 * i, t) : frag_along(at, wm + 32 * i, t);
+          b[i] = B_ACROSS ? frag_across<T, MB>(bt, wn + 32 * i, t) : frag_along(bt, wn + 32 * i, t);
+        }
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+          for (int j = 0; j < MB; ++j) acc[i][j] = product<T>(a[i], b[j], acc[i][j]);
       }
-#pragma unroll
-      for (int i = 0; i < MB; ++i)
-#pragma unroll
-        for (int j = 0; j < MB; ++j) acc[i][j] = product<T>(a[i], b[j], acc[i][j]);
+      const int e = d + 1 == D ? 0 : d + 1;          // step s + 1's set
+      if (s + 1 < steps) store(e, smem + ((s + 1) & 1) * 2 * BYTES);
+      if (s + 1 + D < steps) load(e, s + 1 + D);
+      __syncthreads();
     }
-    if (s + 1 < steps) store(smem + ((s + 1) & 1) * 2 * BYTES);
-    __syncthreads();
   }
 }
 
@@ -285,7 +309,7 @@ __global__ void __launch_bounds__(256) reduce_parts(const float* __restrict__ pa
 // they have in memory; bf16 that lies across is transposed by the LDS read.
 // fp32 runs at the fp32 matrix instruction's rate, a sixteenth of bf16's, which
 // bounds it where there are enough tiles (900 tokens x 4 of 16 experts of 1024
-// x 2048: 172 us, 88 of the 151 TFLOP/s of a large product); tiles of 64 are
+// x 2048: 165 us, 92 of the 151 TFLOP/s of a large product); tiles of 64 are
 // for calls with few of 128 (333 x 2 of 6 of 1001 x 515: 22 and 50 us, its
 // weight gradient 17 us, all start and latency).
 // ---------------------------------------------------------------------------
@@ -325,28 +349,28 @@ __global__ void __launch_bounds__(256, 2) expert_mm_kernel(ExpertArgs a, int ite
       wr[i] = w + (int64_t)(q / UPR) * a.ldw + n0 + q % UPR * U;
     }
   }
-  u32x4 va[NU], vb[NU];
-  auto load = [&](int s) {
+  u32x4 va[kAhead][NU], vb[kAhead][NU];
+  auto load = [&](int d, int s) {
     const int k = (s0 + s) * STEP;
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      va[i] = fetch<T>(xr[i] + k, a.K - k - u8 * U);
+      va[d][i] = fetch<T>(xr[i] + k, a.K - k - u8 * U);
       if (!W_ACROSS) {
-        vb[i] = fetch<T>(wr[i] + k, a.K - k - u8 * U);
+        vb[d][i] = fetch<T>(wr[i] + k, a.K - k - u8 * U);
       } else {
         const int q = i * 256 + threadIdx.x;
-        vb[i] = fetch<T>(wr[i] + (int64_t)k * a.ldw,
-                         k + q / UPR < a.K ? a.N - n0 - q % UPR * U : 0);
+        vb[d][i] = fetch<T>(wr[i] + (int64_t)k * a.ldw,
+                            k + q / UPR < a.K ? a.N - n0 - q % UPR * U : 0);
       }
     }
   };
-  auto store = [&](uint8_t* to) {
+  auto store = [&](int d, uint8_t* to) {
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
       const int q = i * 256 + threadIdx.x;
-      *reinterpret_cast<u32x4*>(to + lds_off(q >> 3, q & 7)) = va[i];
+      *reinterpret_cast<u32x4*>(to + lds_off(q >> 3, q & 7)) = va[d][i];
       *reinterpret_cast<u32x4*>(to + BYTES + (W_ACROSS ? across_off<T, MB>(q / UPR, q % UPR)
-                                                       : lds_off(q >> 3, q & 7))) = vb[i];
+                                                       : lds_off(q >> 3, q & 7))) = vb[d][i];
     }
   };
   f32x16 acc[MB][MB] = {};
@@ -384,36 +408,40 @@ __global__ void __launch_bounds__(256, 2) expert_wgrad_kernel(WgradArgs a, int n
   // the thread's units are the same columns of rows 256 / UPR apart
   const int u = threadIdx.x % UPR, row = threadIdx.x / UPR;
   const int cy = n0 + u * U, cx = k0 + u * U;
-  u32x4 va[NU], vb[NU];
-  int next[NU];                         // the slots of the next step's rows
-  auto slots_of = [&](int s) {
+  constexpr int D = kAhead;
+  u32x4 va[D][NU];
+  std::conditional_t<CODES, Codes, u32x4> vb[D][NU];
+  int next[D][NU];                      // the slots of a set's next rows
+  auto slots_of = [&](int d, int s) {
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      const int p = lo + s * STEP + i * (256 / UPR) + row;
-      next[i] = p < hi ? slot_at(a.order, p) : -1;
+      const int64_t p = lo + (int64_t)s * STEP + i * (256 / UPR) + row;
+      next[d][i] = p < hi ? slot_at(a.order, (int)p) : -1;
     }
   };
-  slots_of(0);
-  auto load = [&](int s) {
+#pragma unroll
+  for (int d = 0; d < D; ++d) slots_of(d, d);
+  auto load = [&](int d, int s) {
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      const bool in = next[i] >= 0 && next[i] < a.S;
-      const int64_t ry = in ? divide(next[i], yd) : 0, rx = in ? divide(next[i], xd) : 0;
-      va[i] = fetch<T>(static_cast<const T*>(a.dy) + ry * a.ldy + cy, in ? a.N - cy : 0);
+      const int slot = next[d][i];
+      const bool in = slot >= 0 && slot < a.S;
+      const int64_t ry = in ? divide(slot, yd) : 0, rx = in ? divide(slot, xd) : 0;
+      va[d][i] = fetch<T>(static_cast<const T*>(a.dy) + ry * a.ldy + cy, in ? a.N - cy : 0);
       if constexpr (CODES)
-        vb[i] = fetch_codes<T>(static_cast<const int8_t*>(a.x) + rx * a.ldx + cx,
-                               a.x_scale + rx * a.s_r + cx / 32, in ? a.K - cx : 0);
+        vb[d][i] = fetch_codes<T>(static_cast<const int8_t*>(a.x) + rx * a.ldx + cx,
+                                  a.x_scale + rx * a.s_r + cx / 32, in ? a.K - cx : 0);
       else
-        vb[i] = fetch<T>(static_cast<const T*>(a.x) + rx * a.ldx + cx, in ? a.K - cx : 0);
+        vb[d][i] = fetch<T>(static_cast<const T*>(a.x) + rx * a.ldx + cx, in ? a.K - cx : 0);
     }
-    slots_of(s + 1);
+    slots_of(d, s + D);
   };
-  auto store = [&](uint8_t* to) {
+  auto store = [&](int d, uint8_t* to) {
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
       const int at = across_off<T, MB>(i * (256 / UPR) + row, u);
-      *reinterpret_cast<u32x4*>(to + at) = va[i];
-      *reinterpret_cast<u32x4*>(to + BYTES + at) = vb[i];
+      *reinterpret_cast<u32x4*>(to + at) = va[d][i];
+      *reinterpret_cast<u32x4*>(to + BYTES + at) = value_of<T>(vb[d][i]);
     }
   };
   f32x16 acc[MB][MB] = {};
