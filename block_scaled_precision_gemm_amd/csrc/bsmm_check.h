@@ -13,6 +13,10 @@ bsmm_status fail(bsmm_status s, const char* fmt, ...) __attribute__((format(prin
 constexpr int64_t kMaxDim = (int64_t)1 << 31;
 
 inline bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
+// rows of bf16 or fp32 at 16-byte aligned addresses
+inline bool aligned_rows(const void* p, int64_t ld, bsmm_dtype d) {
+  return aligned(p, 16) && ld % (d == BSMM_BF16 ? 8 : 4) == 0;
+}
 
 }  // namespace bsmm
 

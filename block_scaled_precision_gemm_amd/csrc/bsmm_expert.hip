@@ -309,9 +309,9 @@ __global__ void __launch_bounds__(256) reduce_parts(const float* __restrict__ pa
 // they have in memory; bf16 that lies across is transposed by the LDS read.
 // fp32 runs at the fp32 matrix instruction's rate, a sixteenth of bf16's, which
 // bounds it where there are enough tiles (900 tokens x 4 of 16 experts of 1024
-// x 2048: 165 us, 92 of the 151 TFLOP/s of a large product); tiles of 64 are
-// for calls with few of 128 (333 x 2 of 6 of 1001 x 515: 22 and 50 us, its
-// weight gradient 17 us, all start and latency).
+// x 2048: 165 us, 92 of the 151 TFLOP/s of a large product).  Tiles of 128 are
+// for gradients of many of them; few tiles are bound by latency (333 x 2 of 6
+// of 1001 x 515: 22 us in tiles of 64, its weight gradient 17).
 // ---------------------------------------------------------------------------
 template <typename T, int MB, bool W_ACROSS>
 __global__ void __launch_bounds__(256, 2) expert_mm_kernel(ExpertArgs a, int items, int ntn,
@@ -465,14 +465,15 @@ __global__ void __launch_bounds__(256, 2) expert_wgrad_kernel(WgradArgs a, int n
 }
 
 // ---------------------------------------------------------------------------
-// bf16 with aligned rows: tiles of BM = 64 MI rows by 256 columns, eight waves
+// bf16: tiles of BM = 64 MI rows by 256 columns, eight waves
 // of 32 MI x 64 (MI x 2 blocks of 32 x 32 x 16 instructions), the contraction
 // in steps of 64.
 //
 // Both tiles stand in LDS as rows of 128 bytes with the contraction inside.
 // Operands that lie in memory that way go global -> LDS directly, two or three
-// steps ahead: the slots take all 160 KB.  The other kind goes through
-// registers: a wave has 8 neighbouring elements of the contraction (rows in
+// steps ahead: the slots take all 160 KB.  (Not with rows that are not 16-byte
+// aligned: 1000 tokens x 2 of 8 experts of 2048 x 2000 take 36 us, x 2001,
+// through registers, 46.)  The other kind goes through registers: a wave has 8 neighbouring elements of the contraction (rows in
 // memory) and a lane 4 columns, which it transposes with 16 byte permutations
 // and writes as 4 x 16 bytes, the loads a step ahead.  (The transposing LDS
 // read would spare that, but the compiler waits for every direct load in flight
@@ -498,6 +499,11 @@ __global__ void __launch_bounds__(256, 2) expert_wgrad_kernel(WgradArgs a, int n
 constexpr int kWide = 256;                      // columns of a tile
 __device__ const uint32_t kZeros[128] = {};     // a row of zeros
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+// in memory, aligned to its elements alone: the instructions take any such
+// address, and at the same rate
+typedef unsigned u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef unsigned u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 // a load from global memory, whatever the pointer was chosen from
 template <typename V>
 __device__ __forceinline__ V load_global(const void* p) {
@@ -527,6 +533,27 @@ __device__ __forceinline__ void lds_done() {
 
 // 8 rows x 4 columns on their way to an operand's tile
 struct Turn { u32x2 row[8]; };
+// A lane's 4 columns are columns 4 lane .. of a tile that begins at column c0
+// of n (>= 4), and are loaded 8 bytes at a time from the last 4 of n at most:
+// where n % 4 != 0 the lane that reaches past the end moves its columns back
+// down.  (Those of the lanes behind it are not stored.)
+struct Columns {
+  int first;                             // of the lanes' offsets `at`, in bytes
+  uint32_t at;
+  int down;                              // bits, 0 in most lanes
+  bool odd;                              // whether any lane of the tile has some
+  __device__ __forceinline__ Columns(int c0, int n, int lane)
+      : first(min(c0, n - 4)), at((uint32_t)min(4 * lane, n - 4 - first) * 2),
+        odd(n % 4 != 0 && c0 + 256 > n) {
+    down = 16 * min(max(c0 + 4 * lane - first - (int)at / 2, 0), 3);
+  }
+  __device__ __forceinline__ void place(Turn& v) const {
+    if (!odd) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v.row[i] = __builtin_bit_cast(u32x2, __builtin_bit_cast(uint64_t, v.row[i]) >> down);
+  }
+};
 // column c of them
 __device__ __forceinline__ void put_turned(const Turn& v, uint8_t* tile, int octet, int c) {
   u32x4 o;
@@ -658,12 +685,11 @@ __device__ __forceinline__ void wide_products(uint8_t* smem, int steps, f32x16 (
 // A wave's 32 MI x 64 results to memory, a block of 32 rows at a time through
 // LDS, so that a store covers whole runs of a row.  row(m): the address of
 // column 0 of the wave's row m (null: not stored), scale(m) its factor; cols:
-// the columns from there to the end; vec: rows 16-byte aligned there.  The
-// stores pass the caches by: they would push out what the next tiles read
+// the columns from there to the end.  The stores pass the caches by: they would push out what the next tiles read
 // (4096 tokens x 8 of 32 experts, fp32 gradients of 2048 x 4096: 810 -> 767 us).
 template <int MI, typename Row, typename Scale>
 __device__ __forceinline__ void wide_store(uint8_t* smem, const f32x16 (&acc)[MI][2],
-                                           bsmm_dtype dt, int cols, bool vec, const Row& row,
+                                           bsmm_dtype dt, int cols, const Row& row,
                                            const Scale& scale) {
   constexpr int PITCH = kWidePitch;                    // reads and writes without conflicts
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -687,13 +713,13 @@ __device__ __forceinline__ void wide_store(uint8_t* smem, const f32x16 (&acc)[MI
         const f32x4 v = p[0] * f, w = p[1] * f;
         uint8_t* const to = static_cast<uint8_t*>(row(32 * i + m));
         if (to == nullptr) continue;
-        if (vec && c + 8 <= cols) {
+        if (c + 8 <= cols) {
           u32x4 o;
           o[0] = bf16_pair(v[0], v[1]);
           o[1] = bf16_pair(v[2], v[3]);
           o[2] = bf16_pair(w[0], w[1]);
           o[3] = bf16_pair(w[2], w[3]);
-          __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(to + c * 2));
+          __builtin_nontemporal_store(o, reinterpret_cast<u32x4_any*>(to + c * 2));
         } else {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
@@ -710,8 +736,8 @@ __device__ __forceinline__ void wide_store(uint8_t* smem, const f32x16 (&acc)[MI
                         scale(32 * i + m);
         uint8_t* const to = static_cast<uint8_t*>(row(32 * i + m));
         if (to == nullptr) continue;
-        if (vec && c + 4 <= cols) {
-          __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(to + c * 4));
+        if (c + 4 <= cols) {
+          __builtin_nontemporal_store(v, reinterpret_cast<f32x4_any*>(to + c * 4));
         } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -723,9 +749,9 @@ __device__ __forceinline__ void wide_store(uint8_t* smem, const f32x16 (&acc)[MI
 }
 
 // An item of at most 64 MI rows from column n0.
-template <int MI, bool W_ACROSS>
+template <int MI, bool W_ACROSS, bool DIRECT>
 __device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& it, int n0,
-                                               int s0, int s1, uint8_t* smem, bool vec) {
+                                               int s0, int s1, uint8_t* smem) {
   using W = Wide<MI>;
   int* const slots = reinterpret_cast<int*>(smem + kWideStage);
   float* const scales = reinterpret_cast<float*>(slots + 256);
@@ -737,8 +763,8 @@ __device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& 
   // rows and columns past the end repeat others (not stored)
   struct {
     const ExpertArgs& a;
-    int wave, lane, n0, xk;
-    uint32_t at;
+    int wave, lane, xk;
+    Columns cols;
     const uint16_t* w;
     int s0, n, turn;
     // Step s of the walk, which an expert starts `turn` steps in.  All tiles
@@ -752,8 +778,14 @@ __device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& 
     }
     const uint16_t* xp[MI];
     const uint16_t* wp[4];
-    u32x4 xv[MI];
+    u32x4 xv[MI], wv[4];
     Turn v;
+    // the lane's unit of a row that lies along
+    __device__ __forceinline__ u32x4 unit(bool last, const uint16_t* p, int s) const {
+      if (!last || a.K % 8 == 0) return load_global<u32x4_any>(along(last, p, s));
+      s = step(s);
+      return bsmm::fetch<uint16_t>(p + s * 64, a.K - xk - s * 64);
+    }
     __device__ __forceinline__ const uint16_t* along(bool last, const uint16_t* p, int s) const {
       s = step(s);
       return !last || s * 64 + xk < a.K ? p + s * 64 : reinterpret_cast<const uint16_t*>(kZeros);
@@ -767,22 +799,31 @@ __device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& 
     __device__ __forceinline__ void begin(bool, int) {}
     __device__ __forceinline__ void fetch(bool last, int s, int i) {
       if (i < MI) {
-        xv[i] = load_global<u32x4>(along(last, xp[i], s));
+        xv[i] = unit(last, xp[i], s);
+      } else if (!W_ACROSS) {
+        wv[i - MI] = unit(last, wp[i - MI], s);
       } else {
         const int k = step(s) * 64 + wave * 8 + i - MI;
-        const uint16_t* row = w + (int64_t)k * a.ldw + n0;
+        const uint16_t* row = w + (int64_t)k * a.ldw + cols.first;
         if (last) row = k < a.K ? row : reinterpret_cast<const uint16_t*>(kZeros);
-        v.row[i - MI] = load_global<u32x2>(reinterpret_cast<const uint8_t*>(row) + at);
+        v.row[i - MI] =
+            load_global<u32x2_any>(reinterpret_cast<const uint8_t*>(row) + cols.at);
       }
     }
     __device__ __forceinline__ void put(uint8_t* at, uint8_t* bt, int i) {
-      if (i < MI) *reinterpret_cast<u32x4*>(at + (i * 8 + wave) * 1024 + lane * 16) = xv[i];
-      else put_turned(v, bt, wave, i - MI);
+      if (i < MI) {
+        *reinterpret_cast<u32x4*>(at + (i * 8 + wave) * 1024 + lane * 16) = xv[i];
+      } else if (!W_ACROSS) {
+        *reinterpret_cast<u32x4*>(bt + ((i - MI) * 8 + wave) * 1024 + lane * 16) = wv[i - MI];
+      } else {
+        if (i == MI) cols.place(v);
+        put_turned(v, bt, wave, i - MI);
+      }
     }
-  } ops{a, wave, lane, n0, ((lane & 7) ^ swz(8 * wave + (lane >> 3))) * 8,
-        (uint32_t)min(4 * lane, a.N - 4 - n0) * 2,
+  } ops{a, wave, lane, ((lane & 7) ^ swz(8 * wave + (lane >> 3))) * 8,
+        Columns(n0, W_ACROSS ? a.N : 4, lane),
         static_cast<const uint16_t*>(a.w) + it.e * a.w_se, s0, s1 - s0,
-        a.K % 64 == 0 && s1 > s0 ? it.e % (s1 - s0) : 0, {}, {}, {}, {}};
+        a.K % 64 == 0 && s1 > s0 ? it.e % (s1 - s0) : 0, {}, {}, {}, {}, {}};
 #pragma unroll
   for (int t = 0; t < MI; ++t) {
     const int s = max(slots[64 * t + 8 * wave + (lane >> 3)], 0);
@@ -797,7 +838,7 @@ __device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& 
   }
   __syncthreads();                      // the slots have been read
   f32x16 acc[MI][2] = {};
-  wide_products<MI, !W_ACROSS, false, W_ACROSS, MI + 8, MI + 4>(
+  wide_products<MI, DIRECT, false, W_ACROSS, MI + (W_ACROSS ? 8 : 4), MI + 4>(
       smem, s1 - s0, acc, ops);
   barrier();                            // nobody reads the tiles any more
   item_slots(a, it, 64 * MI, slots, scales);
@@ -806,7 +847,7 @@ __device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& 
   const int size = a.out_dtype == BSMM_BF16 ? 2 : 4;
   uint8_t* const out = static_cast<uint8_t*>(a.out) + (int64_t)col * size;
   wide_store<MI>(
-      smem, acc, a.out_dtype, a.N - col, vec,
+      smem, acc, a.out_dtype, a.N - col,
       [&](int m) -> void* {
         const int slot = slots[wm + m];
         return slot < 0 ? nullptr : out + slot * a.ldo * size;
@@ -814,9 +855,10 @@ __device__ __forceinline__ void expert_mm_item(const ExpertArgs& a, const Item& 
       [&](int m) { return scales[wm + m]; });
 }
 
-template <bool W_ACROSS>
+// DIRECT: rows along, 16-byte aligned, whole units.
+template <bool W_ACROSS, bool DIRECT>
 __global__ void __launch_bounds__(512, 2) expert_mm_wide(ExpertArgs a, int rows, int items,
-                                                         int ntn, int splits, int run, int vec) {
+                                                         int ntn, int splits, int run) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   // groups of 4 items (1, 2 and 8 were within 2 %; one expert of 8192^3: 8 the
   // same, 2 and 1 took 2 and 7 % more)
@@ -830,15 +872,15 @@ __global__ void __launch_bounds__(512, 2) expert_mm_wide(ExpertArgs a, int rows,
   // only as many rows as there are, to 64: an expert's last item would
   // multiply 128 empty rows on average
   const int mi = (it.rows + 63) / 64;
-  if (mi == 4) expert_mm_item<4, W_ACROSS>(a, it, n0, s0, s1, smem, vec);
-  else if (mi == 3) expert_mm_item<3, W_ACROSS>(a, it, n0, s0, s1, smem, vec);
-  else if (mi == 2) expert_mm_item<2, W_ACROSS>(a, it, n0, s0, s1, smem, vec);
-  else expert_mm_item<1, W_ACROSS>(a, it, n0, s0, s1, smem, vec);
+  if (mi == 4) expert_mm_item<4, W_ACROSS, DIRECT>(a, it, n0, s0, s1, smem);
+  else if (mi == 3) expert_mm_item<3, W_ACROSS, DIRECT>(a, it, n0, s0, s1, smem);
+  else if (mi == 2) expert_mm_item<2, W_ACROSS, DIRECT>(a, it, n0, s0, s1, smem);
+  else expert_mm_item<1, W_ACROSS, DIRECT>(a, it, n0, s0, s1, smem);
 }
 
 __global__ void __launch_bounds__(512, 2) expert_wgrad_wide(WgradArgs a, int ntn, int ntk,
                                                             int splits, int run, Divisor yd,
-                                                            Divisor xd, int vec) {
+                                                            Divisor xd) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   int item, tk, lo, hi;
   if (!deal_tile(splits * a.E * ntn, ntk, run, 1, item, tk)) return;
@@ -852,7 +894,7 @@ __global__ void __launch_bounds__(512, 2) expert_wgrad_wide(WgradArgs a, int ntn
     int wave, lane, lo, hi;
     const uint8_t* dy;
     const uint8_t* x;
-    uint32_t ay, ax;
+    Columns cy, cx;
     int mine;
     int64_t oy, ox;
     int rows;
@@ -879,15 +921,19 @@ __global__ void __launch_bounds__(512, 2) expert_wgrad_wide(WgradArgs a, int ntn
       const int r = i & 7;
       const uint8_t* p = second ? x + lane_of(ox, r) : dy + lane_of(oy, r);
       if (last) p = r < rows ? p : reinterpret_cast<const uint8_t*>(kZeros);
-      (second ? vx : vy).row[r] = load_global<u32x2>(p + (second ? ax : ay));
+      (second ? vx : vy).row[r] = load_global<u32x2_any>(p + (second ? cx.at : cy.at));
     }
     __device__ __forceinline__ void put(uint8_t* at, uint8_t* bt, int i) {
+      if (i == 0) cy.place(vy);
+      if (i == 4) cx.place(vx);
       if (i < 4) put_turned(vy, at, wave, i);
       else put_turned(vx, bt, wave, i - 4);
     }
-  } ops{a, yd, xd, wave, lane, lo, hi, static_cast<const uint8_t*>(a.dy) + n0 * 2,
-        static_cast<const uint8_t*>(a.x) + k0 * 2, (uint32_t)min(4 * lane, a.N - 4 - n0) * 2,
-        (uint32_t)min(4 * lane, a.K - 4 - k0) * 2, 0, 0, 0, 0, {}, {}};
+  } ops{a, yd, xd, wave, lane, lo, hi, static_cast<const uint8_t*>(a.dy),
+        static_cast<const uint8_t*>(a.x), Columns(n0, a.N, lane), Columns(k0, a.K, lane),
+        0, 0, 0, 0, {}, {}};
+  ops.dy += (int64_t)ops.cy.first * 2;
+  ops.x += (int64_t)ops.cx.first * 2;
   ops.mine = ops.slot_of(0);
   f32x16 acc[4][2] = {};
   wide_products<4, false, true, true, 16, 8>(smem, (int)(((unsigned)(hi - lo) + 63) / 64), acc, ops);
@@ -896,7 +942,7 @@ __global__ void __launch_bounds__(512, 2) expert_wgrad_wide(WgradArgs a, int ntn
   const int size = a.out_dtype == BSMM_BF16 ? 2 : 4;
   uint8_t* const out = static_cast<uint8_t*>(a.dw) + (e * a.w_se + col) * size;
   wide_store<4>(
-      smem, acc, a.out_dtype, a.K - col, vec,
+      smem, acc, a.out_dtype, a.K - col,
       [&](int m) -> void* {
         return row0 + m < a.N ? out + (row0 + m) * a.ldw * size : nullptr;
       },
@@ -1109,11 +1155,6 @@ void launch_reduce(const float* parts, int splits, void* out, bsmm_dtype dt, int
                      st, parts, splits, out, dt, rows, cols, inner, outer_ld, ld);
 }
 
-// 16-byte aligned rows of a bf16 or fp32 output, for the wide tiles' stores
-int vec_rows(const void* p, int64_t ld, bsmm_dtype dt) {
-  return aligned(p, 16) && ld % (dt == BSMM_BF16 ? 8 : 4) == 0;
-}
-
 // Runs of tiles for deal_tile, and the grid.  Runs of 8, so that the XCDs' work
 // is even: with an eighth of the grid to each, most of the items that do not
 // exist fell to the last XCDs, and an expert's tiles to one (300 tokens x 8 of
@@ -1144,7 +1185,7 @@ void launch_mm(ExpertArgs a, ExpertPlan plan, int rows, int splits, void* ws, hi
     a.out_dtype = BSMM_F32;
   }
   const int64_t act = a.E < a.S ? a.E : a.S;
-  const int bn = plan == ExpertPlan::Wide ? kWide : plan == ExpertPlan::Tiles128 ? 128 : 64;
+  const int bn = plan == ExpertPlan::Wide ? kWide : 64;
   const int bm = plan == ExpertPlan::Wide ? rows : bn;
   const int items = (int)(((int64_t)a.S + act * (bm - 1)) / bm), ntn = (a.N + bn - 1) / bn;
   int64_t real = ((int64_t)a.S + act * (bm / 2)) / bm;
@@ -1154,12 +1195,16 @@ void launch_mm(ExpertArgs a, ExpertPlan plan, int rows, int splits, void* ws, hi
   const dim3 grid = deal.grid;
   if (plan == ExpertPlan::Wide) {
     if constexpr (sizeof(T) == 2)
-      hipLaunchKernelGGL((expert_mm_wide<W_ACROSS>), grid, dim3(512), kWideBytes, st, a, rows, items,
-                         ntn, splits, deal.run, vec_rows(a.out, a.ldo, a.out_dtype));
-  } else if (plan == ExpertPlan::Tiles128) {
-    if constexpr (sizeof(T) == 2)
-      hipLaunchKernelGGL((expert_mm_kernel<T, 2, W_ACROSS>), grid, dim3(256), 0, st, a, items, ntn,
-                         splits, deal.run);
+    {
+      const bool direct = !W_ACROSS && a.K % 8 == 0 && aligned_rows(a.x, a.ldx, a.dtype) &&
+                          aligned_rows(a.w, a.ldw, a.dtype) && a.w_se % 8 == 0;
+      if (direct)
+        hipLaunchKernelGGL((expert_mm_wide<W_ACROSS, !W_ACROSS>), grid, dim3(512), kWideBytes, st,
+                           a, rows, items, ntn, splits, deal.run);
+      else
+        hipLaunchKernelGGL((expert_mm_wide<W_ACROSS, false>), grid, dim3(512), kWideBytes, st, a,
+                           rows, items, ntn, splits, deal.run);
+    }
   } else {
     hipLaunchKernelGGL((expert_mm_kernel<T, 1, W_ACROSS>), grid, dim3(256), 0, st, a, items, ntn,
                        splits, deal.run);
@@ -1200,9 +1245,7 @@ void launch_wgrad(WgradArgs a, ExpertPlan plan, int splits, void* ws, hipStream_
     const Deal deal(tiles, tiles, false);
     if constexpr (sizeof(T) == 2)
       hipLaunchKernelGGL(expert_wgrad_wide, deal.grid, dim3(512), kWideBytes, st, a, ntn, ntk,
-                         splits, deal.run, divisor(a.y_div), divisor(a.x_div),
-                         vec_rows(a.dw, a.ldw, a.out_dtype) &&
-                             vec_rows(a.dw, a.w_se, a.out_dtype));
+                         splits, deal.run, divisor(a.y_div), divisor(a.x_div));
   } else if (plan == ExpertPlan::Tiles128) {
     launch_wgrad_tiles<T, 2>(a, ntn, ntk, splits, st);
   } else {

@@ -16,6 +16,8 @@ namespace {
 bool float_dtype(bsmm_dtype d) { return d == BSMM_F32 || d == BSMM_BF16; }
 uintptr_t dtype_bytes(bsmm_dtype d) { return d == BSMM_BF16 ? 2 : 4; }
 constexpr int64_t kMaxExperts = 1024;
+// positions are counted a few steps past the last slot, in 32 bits
+constexpr int64_t kMaxSlots = kMaxDim - 1024;
 
 // A kernel and the ranges of the contraction it is cut into.
 struct Choice { ExpertPlan plan; int splits; double us; int rows; };
@@ -70,24 +72,18 @@ double wide_us(const ExpertArgs& a, int64_t act, int bm, int64_t steps, int part
   return us > longest ? us : longest;
 }
 
-bool aligned_rows(const void* p, int64_t ld, bsmm_dtype d) {
-  return aligned(p, 16) && ld % (d == BSMM_BF16 ? 8 : 4) == 0;
-}
-
 // Measured (us; the average is of rows to an expert):
-//                                            Rows  Wide  Tiles64  Tiles128
-//   1 token x 8 of 64, 2048 x 4096 bf16        33    32                     (64 tiles of 256)
-//   64 x 2 of 8, 1024 x 2048 bf16              14    17                     (32)
-//   32 x 2 of 8, 4096 x 8192 bf16             117   122                     (128)
-//   16 x 4 of 16, 4096 x 4096 bf16            111   105                     (256)
-//   8 x 8 of 32, 2048 x 4096 bf16             105    87                     (256)
-//   64 x 8 of 32, the same                    134    92                     (256)
-//   64 x 4 of 16, 4096 x 1024 fp32             78           96              (average 16)
-//   128 x 4 of 16, the same                   108           97              (32)
-//   128 x 4 of 16, input gradient fp32        102          118              (32)
-//   333 x 2 of 6, 1001 x 515 fp32                           22       50
-//   2000 x 4 of 16, 1001 x 2051 fp32                       381      448
-//   2000 x 4 of 16, 1001 x 2051 bf16                       122      107
+//                                            Rows  Wide  Tiles64
+//   1 token x 8 of 64, 2048 x 4096 bf16        33    32           (64 tiles of 256)
+//   64 x 2 of 8, 1024 x 2048 bf16              14    17           (32)
+//   32 x 2 of 8, 4096 x 8192 bf16             117   122           (128)
+//   16 x 4 of 16, 4096 x 4096 bf16            111   105           (256)
+//   8 x 8 of 32, 2048 x 4096 bf16             105    87           (256)
+//   64 x 8 of 32, the same                    134    92           (256)
+//   2000 x 4 of 16, 1001 x 2051 bf16                  65    122  (unaligned)
+//   64 x 4 of 16, 4096 x 1024 fp32             78            96   (average 16)
+//   128 x 4 of 16, the same                   108            97   (32)
+//   128 x 4 of 16, input gradient fp32        102           118   (32)
 Choice mm_plan(const ExpertArgs& a, size_t room) {
   const bool bf16 = a.dtype == BSMM_BF16;
   const int unit = bf16 ? 8 : 4;
@@ -105,7 +101,8 @@ Choice mm_plan(const ExpertArgs& a, size_t room) {
   if (getenv("FEW") ? rows && a.S <= atoi(getenv("FEW"))*act : rows && a.S <= few * act) return Choice{ExpertPlan::Rows, 1, 0, 0};
   const double outs = (double)a.S * a.N;
   const int64_t steps = ((int64_t)a.K + 63) / 64;
-  if (bf16 && rows) {
+  // (of any alignment, but 4 columns at least where they are transposed)
+  if (bf16 && (!a.w_across || a.N >= 4)) {
     // Items of at most 256, 192 or 128 rows: fewer weights are read again, or
     // the chip is fuller (1021 tokens x 8 of 32, 2048 x 4096: 194, 182, 198 us;
     // 1500 x 4 of 16, 2048 x 2048: 57, 75, 67; 512 x 4 of 16, the same: 46, 41,
@@ -121,12 +118,13 @@ Choice mm_plan(const ExpertArgs& a, size_t room) {
                              (bm < best.rows ? 1.03 : 1.0);
         if (us * worth < best.us) best = Choice{ExpertPlan::Wide, p, us, bm};
       }
-    return best;
+    if (rows) return best;           // else through registers, a tenth slower
+    const Choice small = best_split(ExpertPlan::Tiles64, tiles(64, 64), steps, outs, 0.7, 0.5, 1,
+                                    room);
+    return 1.1 * best.us < small.us ? best : small;
   }
-  const Choice small = best_split(ExpertPlan::Tiles64, tiles(64, 64), bf16 ? steps : 2 * steps, outs,
-                                  0.7, bf16 ? 0.5 : 0.55, 1, room);
-  if (!bf16 || tiles(128, 128) < 512) return small;
-  return Choice{ExpertPlan::Tiles128, 1, 0, 0};
+  return best_split(ExpertPlan::Tiles64, tiles(64, 64), bf16 ? steps : 2 * steps, outs, 0.7,
+                    bf16 ? 0.5 : 0.55, 1, room);
 }
 
 //                                              Wide  Tiles64  Tiles128   (us)
@@ -146,9 +144,8 @@ Choice wgrad_plan(const WgradArgs& a, bool codes, size_t room) {
   const Choice d = best_split(ExpertPlan::Tiles128, tiles(128), steps, outs, bf16 ? 1.2 : 2.2,
                               bf16 ? 1.9 : 2.0, 9, room);
   if (d.us < c.us) c = d;
-  // loads of 8 bytes
-  if (bf16 && !codes && aligned(a.dy, 8) && a.ldy % 4 == 0 && a.N % 4 == 0 && aligned(a.x, 8) &&
-      a.ldx % 4 == 0 && a.K % 4 == 0) {
+  // loads of 4 columns
+  if (bf16 && !codes && a.N >= 4 && a.K >= 4) {
     const Choice w = best_split(ExpertPlan::Wide, tiles(256), steps, outs, 1.7, 1.7,
                                 a.out_dtype == BSMM_F32 ? 14 : 9, room);
     if (w.us < c.us) c = w;
@@ -198,7 +195,7 @@ bsmm_status bsmm_expert_mm(const void* x, int64_t ldx, const void* w, int64_t w_
   CHECK(E >= 0 && R >= 0 && S >= 0 && N >= 0 && K >= 0, BSMM_ERR_SHAPE,
         "negative size E=%lld R=%lld S=%lld N=%lld K=%lld", (long long)E, (long long)R,
         (long long)S, (long long)N, (long long)K);
-  CHECK(R < kMaxDim && S < kMaxDim && N < kMaxDim && K < kMaxDim, BSMM_ERR_UNSUPPORTED,
+  CHECK(R < kMaxDim && S < kMaxSlots && N < kMaxDim && K < kMaxDim, BSMM_ERR_UNSUPPORTED,
         "size beyond 2^31");
   CHECK(E <= kMaxExperts, BSMM_ERR_UNSUPPORTED, "E=%lld beyond %lld experts", (long long)E,
         (long long)kMaxExperts);
@@ -276,7 +273,7 @@ bsmm_status bsmm_expert_wgrad(const void* dy, int64_t ldy, bsmm_dtype dtype, int
   CHECK(E >= 0 && Ry >= 0 && Rx >= 0 && S >= 0 && N >= 0 && K >= 0, BSMM_ERR_SHAPE,
         "negative size E=%lld Ry=%lld Rx=%lld S=%lld N=%lld K=%lld", (long long)E, (long long)Ry,
         (long long)Rx, (long long)S, (long long)N, (long long)K);
-  CHECK(Ry < kMaxDim && Rx < kMaxDim && S < kMaxDim && N < kMaxDim && K < kMaxDim,
+  CHECK(Ry < kMaxDim && Rx < kMaxDim && S < kMaxSlots && N < kMaxDim && K < kMaxDim,
         BSMM_ERR_UNSUPPORTED, "size beyond 2^31");
   CHECK(E <= kMaxExperts, BSMM_ERR_UNSUPPORTED, "E=%lld beyond %lld experts", (long long)E,
         (long long)kMaxExperts);

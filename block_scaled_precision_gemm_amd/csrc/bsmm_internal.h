@@ -257,8 +257,8 @@ struct ExpertArgs {
   int E, R, S, N, K;
 };
 // Its kernels and the weight gradient's: items of 16 or 32 rows (aligned), tiles
-// of up to `rows` x 256 (aligned bf16; rows 128, 192 or 256), 128 x 128 or 64 x 64
-// (anything).  splits > 1: ranges of the contraction, their sums in ws (splits
+// of up to `rows` x 256 (bf16; rows 128, 192 or 256), 128 x 128 (the gradient's)
+// or 64 x 64.  splits > 1: ranges of the contraction, their sums in ws (splits
 // * S * N fp32).
 enum class ExpertPlan { Rows, Wide, Tiles128, Tiles64 };
 int launch_expert_mm(const ExpertArgs& a, ExpertPlan plan, int rows, int splits, void* ws,

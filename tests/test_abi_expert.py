@@ -36,7 +36,7 @@ def mm(*, x=P, ldx=64, w=P, w_se=2048, w_sn=64, w_sk=1, dt=BF16, order=P, offset
     (dict(w_sn=63), LAYOUT), (dict(w_sn=64, w_sk=2), LAYOUT), (dict(w_sn=1, w_sk=31), LAYOUT),
     (dict(w_sn=0), LAYOUT), (dict(w_sn=-64), LAYOUT), (dict(x=P + 1), ALIGN), (dict(w=P + 1), ALIGN),
     (dict(dt=F32, x=P + 2), ALIGN), (dict(dt=F32, w=P + 2), ALIGN),
-    (dict(R=2**30, S=2**30, N=2**20, ldo=2**20), UNSUP),
+    (dict(R=2**30, S=2**30, N=2**20, ldo=2**20), UNSUP), (dict(R=2**30, S=2**31 - 1024), UNSUP),
 ])
 def test_mm_rejects(kw, status):
     assert mm(**kw) == status
@@ -58,6 +58,7 @@ def wgrad(*, dy=P, ldy=32, dt=BF16, yper=1, x=P, ldx=64, xper=2, sc=None, s_r=2,
     (dict(dt=I32), DTYPE), (dict(odt=E4M3), DTYPE), (dict(E=-1), SHAPE), (dict(Ry=-1), SHAPE),
     (dict(Rx=-1), SHAPE), (dict(S=-1), SHAPE), (dict(N=-1), SHAPE), (dict(K=-1), SHAPE),
     (dict(Rx=2**31), UNSUP), (dict(K=2**31), UNSUP), (dict(E=1025), UNSUP), (dict(yper=0), ARG),
+    (dict(S=2**31 - 1024, Rx=2**30, yper=2**30), UNSUP),
     (dict(xper=0), ARG), (dict(S=17, Rx=9), SHAPE), (dict(S=17, Ry=17), SHAPE),
     (dict(sc=P, K=48), UNSUP), (dict(offsets=None), NULL), (dict(dw=None), NULL),
     (dict(dy=None), NULL), (dict(x=None), NULL), (dict(order=P + 1), ALIGN),

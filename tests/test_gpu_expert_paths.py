@@ -89,6 +89,52 @@ def test_few_rows(loads, N, K, back, dt):
     assert np.array_equal(host(got), X.expert_mm(x, w, order, off, 1, scale))
 
 
+ODD = [(261, 333), (258, 129), (1031, 67), (515, 640), (7, 70), (4, 1), (3, 65), (256, 250),
+       (513, 15)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("N,K", ODD)
+def test_odd_sizes(N, K, shift, dt):
+    """Rows that end in a unit, tiles that end in four columns, and rows that
+    begin at any element; what surrounds the rows is NaN."""
+    rng = np.random.default_rng(N * K + shift)
+    t, loads = TDT[dt], LOADS[0]
+    off, S, E = sorted_offsets(loads), sum(loads) + 5, len(loads)
+    order = rng.permutation(S).astype(np.int32)
+
+    def inside(v):
+        """v as a view into a wider tensor of NaN."""
+        wide = torch.full((*v.shape[:-1], v.shape[-1] + shift + 2), float("nan"), device=DEV,
+                          dtype=t)
+        wide[..., shift:shift + v.shape[-1]] = dev(v, t)
+        return wide[..., shift:shift + v.shape[-1]]
+
+    x, w, y = ints(rng, S, K, top=2), ints(rng, E, N, K, top=2), ints(rng, S, N, top=2)
+    xg, yg, og, fg = inside(x), inside(y), dev(order), dev(off)
+    got = bsmm.bsmm_expert_mm(xg, inside(w), og, fg, out_dtype="f32")
+    assert np.array_equal(host(got), X.expert_mm(x, w, order, off))
+    wt = inside(w.transpose(0, 2, 1)).transpose(1, 2)                     # contiguous along N
+    for odt in ("f32", "bf16"):
+        o = inside(np.zeros((S, N))) if odt == dt else None
+        got = bsmm.bsmm_expert_mm(xg, wt, og, fg, out_dtype=odt, out=o)
+        want = torch.from_numpy(X.expert_mm(x, w, order, off)).to(TDT[odt]).double().numpy()
+        assert np.array_equal(host(got), want), odt
+        if o is not None:
+            rest = o._base.clone()
+            rest[..., shift:shift + N] = float("nan")
+            assert rest.isnan().all()
+        o = inside(np.zeros((E, N, K))) if odt == dt else None
+        got = bsmm.bsmm_expert_wgrad(yg, xg, og, fg, out_dtype=odt, out=o)
+        want = torch.from_numpy(X.expert_wgrad(y, x, order, off)).to(TDT[odt]).double().numpy()
+        assert np.array_equal(host(got), want), odt
+        if o is not None:
+            rest = o._base.clone()
+            rest[..., shift:shift + K] = float("nan")
+            assert rest.isnan().all()
+
+
 PARTS = [  # few tiles and a long contraction
     ("mm", 300, 2, 130, 4096), ("mm", 300, 2, 130, 4099), ("mm", 70, 1, 64, 9000),
     ("wgrad", 9000, 1, 64, 72), ("wgrad", 9000, 2, 33, 31), ("wgrad", 20000, 1, 256, 512),
