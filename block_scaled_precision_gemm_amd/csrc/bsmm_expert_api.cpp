@@ -129,8 +129,13 @@ Choice mm_plan(const ExpertArgs& a, size_t room) {
 
 //                                              Wide  Tiles64  Tiles128   (us)
 //   333 tokens x 2 of 6, 1001 x 515 fp32                  22        26
-//   1000 x 4 of 16, 1024 x 2048 fp32                     298       251
+//   1000 x 4 of 16, 1024 x 2048 fp32                     196       193
 //   4000 x 2 of 4, 300 x 200 bf16                         62       119
+//   2121 x 8 of 17, 448 x 480 bf16               44       28        39
+//   1832 x 8 of 8, 96 x 2037 bf16                60       51        85
+//   484 x 2 of 21, 448 x 2880 bf16               23       32        36
+//   1818 x 1 of 2, 1824 x 1568, checkpoint       42       41        34    (Wide: restored)
+//   3692 x 2 of 2, 381 x 2592, checkpoint        65      107       100
 Choice wgrad_plan(const WgradArgs& a, bool codes, size_t room) {
   const bool bf16 = a.dtype == BSMM_BF16;
   const int64_t act = a.E < a.S ? a.E : a.S > 0 ? a.S : 1;
@@ -140,9 +145,13 @@ Choice wgrad_plan(const WgradArgs& a, bool codes, size_t room) {
     return a.E * (((int64_t)a.N + t - 1) / t) * (((int64_t)a.K + t - 1) / t);
   };
   const int64_t steps = (run + (bf16 ? 63 : 31)) / (bf16 ? 64 : 32);
-  Choice c = best_split(ExpertPlan::Tiles64, tiles(64), steps, outs, 0.7, bf16 ? 0.5 : 0.8, 1, room);
-  const Choice d = best_split(ExpertPlan::Tiles128, tiles(128), steps, outs, bf16 ? 1.2 : 2.2,
-                              bf16 ? 1.9 : 2.0, 9, room);
+  // pieces of rows that are not aligned are in one line more
+  const bool odd = bf16 && (a.ldy % 4 != 0 || (!codes && a.ldx % 4 != 0));
+  Choice c = best_split(ExpertPlan::Tiles64, tiles(64), steps, outs, odd ? 1.0 : 0.7,
+                        !bf16 || odd ? 0.8 : 0.5, 1, room);
+  const Choice d = best_split(ExpertPlan::Tiles128, tiles(128), steps, outs,
+                              odd ? 2.6 : bf16 ? 2.0 : 2.2, !bf16 || odd ? 2.0 : 1.25,
+                              bf16 ? 4 : 9, room);
   if (d.us < c.us) c = d;
   // loads of 4 columns
   if (bf16 && !codes && a.N >= 4 && a.K >= 4) {
@@ -320,7 +329,8 @@ bsmm_status bsmm_expert_wgrad(const void* dy, int64_t ldy, bsmm_dtype dtype, int
     WgradArgs b = a;
     b.x = ws; b.ldx = K; b.x_scale = nullptr;
     const Choice r = wgrad_plan(b, false, room - values);
-    if (r.plan == ExpertPlan::Wide) {
+    // 3 bytes an element and a launch
+    if (r.plan == ExpertPlan::Wide && r.us + 4.0 + (double)Rx * (double)K * 3 / 4e6 < c.us) {
       if (launch_restore_bf16(x, ldx, x_scale, s_r, ws, Rx, K, stream) != 0)
         return fail(BSMM_ERR_HIP, "kernel launch failed (checkpoint values)");
       a = b;

@@ -191,6 +191,21 @@ def test_checkpoint_workspace(odt):
         assert np.array_equal(host(got), want)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("codes", [False, True])
+def test_gradient_of_many_tiles(codes, dt):
+    """Long runs and many columns, without a workspace."""
+    rng = np.random.default_rng(9)
+    S, N, K, t = 2000, 2047, 2048, TDT[dt]
+    off, order = sorted_offsets([900, 1090]), rng.permutation(S).astype(np.int32)
+    dy, x = ints(rng, S, N, top=1), ints(rng, S, K, top=1)
+    scale = np.full((S, K // 32), 133, np.uint8)
+    xg = dev(x.astype(np.int8)) if codes else dev(x, t)
+    got = bsmm.bsmm_expert_wgrad(dev(dy, t), xg, dev(order), dev(off), workspace=False,
+                                 x_scale=dev(scale) if codes else None)
+    assert np.array_equal(host(got), X.expert_wgrad(dy, x, order, off))
+
+
 def far(shape, row, dt):
     """[rows, cols] whose rows are `row` elements apart, zeros."""
     buf = torch.empty(row * (shape[0] - 1) + shape[1], device=DEV, dtype=dt)
