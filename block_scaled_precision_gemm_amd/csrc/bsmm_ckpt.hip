@@ -150,6 +150,26 @@ __device__ __forceinline__ float exp_minus(float g) {
   return __builtin_amdgcn_exp2f(t) * __builtin_fmaf(rest, 0.693147180559945309f, 1.0f);
 }
 
+// sigma(g) = 1 / (1 + e^-g) and sigma(-g) = 1 - sigma(g), from p = e^-|g| in
+// [0, 1]: as 1 / (1 + p) and p / (1 + p) neither leaves fp32, and the small one
+// falls to 0 below -104 (e^-104 < 2^-150) instead of to a power of two that a
+// large g would multiply.  p = 2^n 2^f with the exponent's whole part n kept
+// apart, so that it is as exact among the subnormals.  A NaN gate gives
+// numbers here: the callers multiply by g, which keeps it.
+struct Sigma {
+  float s, c;
+};
+__device__ __forceinline__ Sigma sigma(float g) {
+  // log2(e) and what is missing of it
+  const float c = -1.44269502162933349609375f, c2 = -1.925963033500011079e-8f;
+  const float x = __builtin_fminf(__builtin_fabsf(g), 104.0f);
+  const float n = __builtin_rintf(x * c);
+  const float f = __builtin_fmaf(x, c2, __builtin_fmaf(x, c, -n));
+  const float p = __builtin_ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
+  const float big = __builtin_amdgcn_rcpf(1.0f + p), small = p * big;
+  return g < 0.0f ? Sigma{small, big} : Sigma{big, small};
+}
+
 // 32768 x 2048 bf16 with the checkpoint: 100 us, 5.4 TB/s.
 template <typename T, bool CKPT>
 __global__ void __launch_bounds__(256) swiglu(SwigluArgs a, unsigned chunks) {
@@ -193,15 +213,12 @@ __global__ void __launch_bounds__(256) swiglu_backward(SwigluBackArgs a) {
     decode(*reinterpret_cast<const uint2*>(q + a.F + k), s[(a.F + k) >> 5], u);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      // finite, so that 1 - sg = e sg is a number where sg is 0; a NaN stays
-      // one through the products with g
-      const float e = __builtin_fminf(exp_minus(g[j]), 0x1p126f);
-      const float sg = __builtin_amdgcn_rcpf(1.0f + e);
-      const float silu = g[j] * sg, act = silu * u[j];
+      const Sigma sg = sigma(g[j]);
+      const float silu = g[j] * sg.s, act = silu * u[j];
       sum = __builtin_fmaf(d[j], act, sum);
       const float rd = r * d[j];
       // silu' = sg (1 + g (1 - sg))
-      const float slope = __builtin_fmaf(silu, e * sg, sg);
+      const float slope = __builtin_fmaf(silu, sg.c, sg.s);
       g[j] = rd * u[j] * slope;
       u[j] = rd * silu;
       d[j] = r * act;
