@@ -139,35 +139,39 @@ __global__ void __launch_bounds__(256) restore_bf16(const int8_t* q, int64_t ldq
 
 // ---- gate ----------------------------------------------------------------------
 
-// e^-g = 2^t with t = -g log2(e): the product's rounding and the constant's,
-// which would cost |g| 2^-24 of the result, are added back.
-__device__ __forceinline__ float exp_minus(float g) {
-  const float c = -1.44269502162933349609375f, c2 = -1.925963033500011079e-8f;
-  const float t = g * c;
-  // beyond these 2^t is 0 or infinite whatever the rest says
-  const float rest = __builtin_fabsf(t) < 256.0f ? __builtin_fmaf(g, c2, __builtin_fmaf(g, c, -t))
-                                                 : 0.0f;
-  return __builtin_amdgcn_exp2f(t) * __builtin_fmaf(rest, 0.693147180559945309f, 1.0f);
+// log2(e) and what is missing of it, negative
+constexpr float kLog2e = -1.44269502162933349609375f, kLog2eRest = -1.925963033500011079e-8f;
+
+// sigma(g) = 1 / (1 + e^-g) = 2^-25 / (2^-25 + e) with e = 2^-25 e^-g, which
+// stays in fp32 down to g = -104, below which sigma is 0 (e^-104 < 2^-150); and
+// the sum stays below 2^126, from where on its reciprocal would be flushed.
+// Above 30 sigma is 1.  e^-g = 2^n 2^f, the exponent's whole part n - 25 read
+// from the low bits of a sum with 1.5 * 2^23 - 25.  A NaN gate gives a number:
+// the caller multiplies by g, which keeps it.
+__device__ __forceinline__ float sigma(float g) {
+  constexpr float kWhole = 12582912.0f - 25.0f;
+  const float x = __builtin_amdgcn_fmed3f(g, -104.0f, 30.0f);
+  const float t = __builtin_fmaf(x, kLog2e, kWhole), n = t - kWhole;
+  const float f = __builtin_fmaf(x, kLog2eRest, __builtin_fmaf(x, kLog2e, -n));
+  const float e = __uint_as_float(__float_as_uint(__builtin_amdgcn_exp2f(f)) +
+                                  (__float_as_uint(t) << 23));
+  return __builtin_amdgcn_rcpf(e + 0x1p-25f) * 0x1p-25f;
 }
 
-// sigma(g) = 1 / (1 + e^-g) and sigma(-g) = 1 - sigma(g), from p = e^-|g| in
-// [0, 1]: as 1 / (1 + p) and p / (1 + p) neither leaves fp32, and the small one
-// falls to 0 below -104 (e^-104 < 2^-150) instead of to a power of two that a
-// large g would multiply.  p = 2^n 2^f with the exponent's whole part n kept
-// apart, so that it is as exact among the subnormals.  A NaN gate gives
-// numbers here: the callers multiply by g, which keeps it.
-struct Sigma {
+// sigma(g) and sigma(-g) = 1 - sigma(g), from p = e^-|g| in [0, 1]: as 1 / (1 +
+// p) and p / (1 + p) neither leaves fp32, and the small one falls to 0 where it
+// is below 2^-150, on either side, instead of to a power of two that a large g
+// would multiply.
+struct Sigmas {
   float s, c;
 };
-__device__ __forceinline__ Sigma sigma(float g) {
-  // log2(e) and what is missing of it
-  const float c = -1.44269502162933349609375f, c2 = -1.925963033500011079e-8f;
+__device__ __forceinline__ Sigmas sigmas(float g) {
   const float x = __builtin_fminf(__builtin_fabsf(g), 104.0f);
-  const float n = __builtin_rintf(x * c);
-  const float f = __builtin_fmaf(x, c2, __builtin_fmaf(x, c, -n));
+  const float n = __builtin_rintf(x * kLog2e);
+  const float f = __builtin_fmaf(x, kLog2eRest, __builtin_fmaf(x, kLog2e, -n));
   const float p = __builtin_ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
   const float big = __builtin_amdgcn_rcpf(1.0f + p), small = p * big;
-  return g < 0.0f ? Sigma{small, big} : Sigma{big, small};
+  return g < 0.0f ? Sigmas{small, big} : Sigmas{big, small};
 }
 
 // 32768 x 2048 bf16 with the checkpoint: 100 us, 5.4 TB/s.
@@ -182,7 +186,7 @@ __global__ void __launch_bounds__(256) swiglu(SwigluArgs a, unsigned chunks) {
     load8(h, g);
     load8(h + a.F, u);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = g[j] * __builtin_amdgcn_rcpf(1.0f + exp_minus(g[j])) * u[j];
+    for (int j = 0; j < 8; ++j) v[j] = g[j] * sigma(g[j]) * u[j];
     store8(static_cast<T*>(a.a) + row * a.lda + k, v);
     if constexpr (CKPT) {
       int8_t* q = a.q + row * a.ldq;
@@ -213,7 +217,7 @@ __global__ void __launch_bounds__(256) swiglu_backward(SwigluBackArgs a) {
     decode(*reinterpret_cast<const uint2*>(q + a.F + k), s[(a.F + k) >> 5], u);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const Sigma sg = sigma(g[j]);
+      const Sigmas sg = sigmas(g[j]);
       const float silu = g[j] * sg.s, act = silu * u[j];
       sum = __builtin_fmaf(d[j], act, sum);
       const float rd = r * d[j];

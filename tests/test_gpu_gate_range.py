@@ -80,3 +80,23 @@ def test_masked_gate():
     dh, act, drow = bsmm.bsmm_swiglu_backward(da, q, s, row_scale=r)
     assert not a[1].any() and not dh[1].any() and not act[1].any() and drow[1] == 0
     assert a[0].all() and torch.equal(a[0], a[2]) and torch.equal(dh[0], dh[2])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("top", [4.0, 2.0**60])
+def test_gate(top, dt):
+    """Where e^-g leaves fp32 or its reciprocal is subnormal too."""
+    h = dev(gates(96, 2, top), TDT[dt])
+    a = bsmm.bsmm_swiglu(h)
+    want, u = X.swiglu(host(h)), host(h)[:, 96:]
+    within(a, want, dt, REL * np.abs(want), 2.0**-141 * np.abs(u))
+    assert torch.equal(a, bsmm.bsmm_swiglu(h, checkpoint=True)[0])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_infinite_gates(dt):
+    """silu(inf) is inf, silu(-inf) = -inf * 0 a NaN, as in the formula."""
+    h = torch.ones(2, 64, device="cuda:0", dtype=TDT[dt])
+    h[0, 3], h[1, 4] = float("inf"), float("-inf")
+    a = host(bsmm.bsmm_swiglu(h))
+    assert a[0, 3] == np.inf and np.isnan(a[1, 4]) and np.isfinite(a).sum() == 62
