@@ -26,6 +26,7 @@ __all__ = [
     "bsmm_expert_mm", "bsmm_expert_wgrad",
     "bsmm_quant_int8_mx", "bsmm_swiglu", "bsmm_swiglu_backward",
     "bsmm_expert_mm_workspace_bytes", "bsmm_expert_wgrad_workspace_bytes",
+    "bsmm_expert_mm_plan_name", "bsmm_expert_wgrad_plan_name",
     "bsmm_route_topk", "bsmm_route_topk_backward", "Route",
     "bsmm_w4_workspace_bytes", "bsmm_w4_plan_name", "bsmm_route_workspace_bytes",
     "bsmm_workspace_bytes", "bsmm_query_plan", "bsmm_set_override", "bsmm_set_override_tail", "bsmm_set_streamk_grid", "bsmm_mfma_probe",
@@ -119,6 +120,10 @@ def load():
     L.bsmm_expert_mm_workspace_bytes.restype = sz
     L.bsmm_expert_wgrad_workspace_bytes.argtypes = [st, st, i64, i64, i64, i64, i64]
     L.bsmm_expert_wgrad_workspace_bytes.restype = sz
+    L.bsmm_expert_mm_plan_name.argtypes = [st, st, st, i64, i64, i64, i64, sz, vp]
+    L.bsmm_expert_mm_plan_name.restype = ctypes.c_char_p
+    L.bsmm_expert_wgrad_plan_name.argtypes = [st, st, st, st, i64, i64, i64, i64, i64, sz, vp]
+    L.bsmm_expert_wgrad_plan_name.restype = ctypes.c_char_p
     L.bsmm_quant_int8_mx.argtypes = [vp, i64, st, vp, i64, vp, i64, vp, i64, i64, i64, vp]
     L.bsmm_swiglu.argtypes = [vp, i64, st, vp, i64, vp, i64, vp, i64, i64, i64, vp]
     L.bsmm_swiglu_backward.argtypes = [vp, i64, st, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp,
@@ -1499,6 +1504,34 @@ def bsmm_expert_wgrad_workspace_bytes(dtype, checkpoint, E, Rx, S, N, K):
     """Workspace bytes bsmm_expert_wgrad wants for dy of ``dtype`` and x [Rx, K]."""
     return load().bsmm_expert_wgrad_workspace_bytes(_float_code(dtype, "dtype"),
                                                     1 if checkpoint else 0, E, Rx, S, N, K)
+
+
+def bsmm_expert_mm_plan_name(dtype, transposed, E, S, N, K, *, aligned=True, workspace=None):
+    """The kernel of a bsmm_expert_mm call and its ranges of K: (rows, wide128,
+    wide192, wide256 or tile64, ranges); None for sizes that have none.
+    aligned: whether rows are at multiples of 16 bytes.  workspace: its bytes,
+    None for as many as the call wants."""
+    code, parts = _float_code(dtype, "dtype"), ctypes.c_int(0)
+    t = 1 if transposed else 0
+    if workspace is None:
+        workspace = load().bsmm_expert_mm_workspace_bytes(code, t, E, S, N, K)
+    name = load().bsmm_expert_mm_plan_name(code, t, 1 if aligned else 0, E, S, N, K, workspace,
+                                           ctypes.byref(parts))
+    return name and (name.decode(), parts.value)
+
+
+def bsmm_expert_wgrad_plan_name(dtype, checkpoint, E, Rx, S, N, K, *, out_dtype="f32",
+                                aligned=True, workspace=None):
+    """The kernel of a bsmm_expert_wgrad call and its parts of the slots:
+    (wide256, tile128, tile64 or restored, parts), as bsmm_expert_mm_plan_name."""
+    code, odt, parts = _float_code(dtype, "dtype"), _float_code(out_dtype, "out_dtype"), \
+        ctypes.c_int(0)
+    c = 1 if checkpoint else 0
+    if workspace is None:
+        workspace = load().bsmm_expert_wgrad_workspace_bytes(code, c, E, Rx, S, N, K)
+    name = load().bsmm_expert_wgrad_plan_name(code, c, odt, 1 if aligned else 0, E, Rx, S, N, K,
+                                              workspace, ctypes.byref(parts))
+    return name and (name.decode(), parts.value)
 
 
 def bsmm_route_workspace_bytes(T, E):

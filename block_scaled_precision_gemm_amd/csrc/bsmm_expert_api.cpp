@@ -167,6 +167,54 @@ size_t restored_bytes(bsmm_dtype dtype, int checkpoint, int64_t Rx, int64_t K) {
   return dtype == BSMM_BF16 && checkpoint ? ((size_t)Rx * (size_t)K * 2u + 15u) / 16u * 16u : 0;
 }
 
+// A weight gradient's kernel, and whether it multiplies a checkpoint's values
+// restored to bf16 in the workspace first (whole: the codes' rows allow it).
+struct WgradChoice { Choice c; bool restored; };
+WgradChoice wgrad_choice(const WgradArgs& a, bool whole, size_t room) {
+  const bool codes = a.x_scale != nullptr;
+  WgradChoice w{wgrad_plan(a, codes, room), false};
+  // bf16: the codes are restored first where the wide tiles take them then
+  const size_t values = restored_bytes(a.dtype, codes, a.Rx, a.K);
+  if (values > 0 && a.S > 0 && whole && room >= values) {
+    WgradArgs b = a;
+    b.ldx = a.K;
+    const Choice r = wgrad_plan(b, false, room - values);
+    // 3 bytes an element and a launch
+    if (r.plan == ExpertPlan::Wide && r.us + 4.0 + (double)a.Rx * (double)a.K * 3 / 4e6 < w.c.us)
+      w = WgradChoice{r, true};
+  }
+  return w;
+}
+
+// Any non-null scales, for the queries: plans do not read them.
+constexpr uint8_t kSome = 0;
+
+// Arguments of those sizes, rows aligned or not (false: no such call).
+bool mm_sizes(bsmm_dtype dtype, int transposed, bool rows, int64_t E, int64_t S, int64_t N,
+              int64_t K, ExpertArgs& a) {
+  if (!float_dtype(dtype) || E <= 0 || S <= 0 || N <= 0 || K <= 0 || E > kMaxExperts ||
+      S >= kMaxDim || N >= kMaxDim || K >= kMaxDim)
+    return false;
+  a = ExpertArgs{};
+  a.dtype = dtype;
+  a.w_across = transposed;
+  a.ldx = rows ? 0 : 1;
+  a.E = (int)E; a.S = (int)S; a.N = (int)N; a.K = (int)K;
+  return true;
+}
+bool wgrad_sizes(bsmm_dtype dtype, int checkpoint, bool rows, int64_t E, int64_t Rx, int64_t S,
+                 int64_t N, int64_t K, WgradArgs& a) {
+  if (!float_dtype(dtype) || E <= 0 || Rx <= 0 || S <= 0 || N <= 0 || K <= 0 || E > kMaxExperts ||
+      Rx >= kMaxDim || S >= kMaxDim || N >= kMaxDim || K >= kMaxDim)
+    return false;
+  a = WgradArgs{};
+  a.dtype = dtype;
+  a.x_scale = checkpoint ? &kSome : nullptr;
+  a.ldy = rows ? 0 : 1;
+  a.E = (int)E; a.Rx = (int)Rx; a.S = (int)S; a.N = (int)N; a.K = (int)K;
+  return true;
+}
+
 constexpr size_t kEnough = (size_t)256 << 20;       // no plan's parts are larger
 
 }  // namespace
@@ -175,22 +223,27 @@ extern "C" {
 
 size_t bsmm_expert_mm_workspace_bytes(bsmm_dtype dtype, int transposed, int64_t E, int64_t S,
                                       int64_t N, int64_t K) {
-  if (!float_dtype(dtype) || E <= 0 || S <= 0 || N <= 0 || K <= 0 || E > kMaxExperts ||
-      S >= kMaxDim || N >= kMaxDim || K >= kMaxDim)
-    return 0;
-  // aligned or not
   size_t need = 0;
-  for (int odd = 0; odd < 2; ++odd) {
-    ExpertArgs a{};
-    a.dtype = dtype;
-    a.w_across = transposed;
-    a.ldx = odd;
-    a.E = (int)E; a.S = (int)S; a.N = (int)N; a.K = (int)K;
+  ExpertArgs a;
+  for (int rows = 0; rows < 2; ++rows) {
+    if (!mm_sizes(dtype, transposed, rows, E, S, N, K, a)) return 0;
     const Choice c = mm_plan(a, kEnough);
     const size_t bytes = c.splits > 1 ? (size_t)c.splits * (size_t)S * (size_t)N * 4u : 0;
     if (bytes > need) need = bytes;
   }
   return need;
+}
+
+const char* bsmm_expert_mm_plan_name(bsmm_dtype dtype, int transposed, int aligned, int64_t E,
+                                     int64_t S, int64_t N, int64_t K, size_t workspace_bytes,
+                                     int* parts) {
+  ExpertArgs a;
+  if (!mm_sizes(dtype, transposed, aligned != 0, E, S, N, K, a)) return nullptr;
+  const Choice c = mm_plan(a, workspace_bytes);
+  if (parts != nullptr) *parts = c.splits;
+  if (c.plan == ExpertPlan::Rows) return "rows";
+  if (c.plan == ExpertPlan::Tiles64) return "tile64";
+  return c.rows == 256 ? "wide256" : c.rows == 192 ? "wide192" : "wide128";
 }
 
 bsmm_status bsmm_expert_mm(const void* x, int64_t ldx, const void* w, int64_t w_se, int64_t w_sn,
@@ -250,15 +303,10 @@ bsmm_status bsmm_expert_mm(const void* x, int64_t ldx, const void* w, int64_t w_
 
 size_t bsmm_expert_wgrad_workspace_bytes(bsmm_dtype dtype, int checkpoint, int64_t E, int64_t Rx,
                                          int64_t S, int64_t N, int64_t K) {
-  if (!float_dtype(dtype) || E <= 0 || Rx <= 0 || S <= 0 || N <= 0 || K <= 0 || E > kMaxExperts ||
-      Rx >= kMaxDim || S >= kMaxDim || N >= kMaxDim || K >= kMaxDim)
-    return 0;
   size_t need = 0;
-  for (int odd = 0; odd < 2; ++odd) {
-    WgradArgs a{};
-    a.dtype = dtype;
-    a.ldy = odd;
-    a.E = (int)E; a.S = (int)S; a.N = (int)N; a.K = (int)K;
+  WgradArgs a;
+  for (int rows = 0; rows < 2; ++rows) {
+    if (!wgrad_sizes(dtype, 0, rows, E, Rx, S, N, K, a)) return 0;
     // fp32 or bf16 output
     for (int bf = 0; bf < 2; ++bf) {
       a.out_dtype = bf ? BSMM_BF16 : BSMM_F32;
@@ -268,6 +316,21 @@ size_t bsmm_expert_wgrad_workspace_bytes(bsmm_dtype dtype, int checkpoint, int64
     }
   }
   return need + restored_bytes(dtype, checkpoint, Rx, K);
+}
+
+const char* bsmm_expert_wgrad_plan_name(bsmm_dtype dtype, int checkpoint, bsmm_dtype out_dtype,
+                                        int aligned, int64_t E, int64_t Rx, int64_t S, int64_t N,
+                                        int64_t K, size_t workspace_bytes, int* parts) {
+  WgradArgs a;
+  if (!float_dtype(out_dtype) || (checkpoint && K % 32 != 0) ||
+      !wgrad_sizes(dtype, checkpoint, aligned != 0, E, Rx, S, N, K, a))
+    return nullptr;
+  a.out_dtype = out_dtype;
+  const WgradChoice w = wgrad_choice(a, aligned != 0, workspace_bytes);
+  if (parts != nullptr) *parts = w.c.splits;
+  if (w.restored) return "restored";
+  return w.c.plan == ExpertPlan::Wide ? "wide256"
+         : w.c.plan == ExpertPlan::Tiles128 ? "tile128" : "tile64";
 }
 
 bsmm_status bsmm_expert_wgrad(const void* dy, int64_t ldy, bsmm_dtype dtype, int dy_slots_per_row,
@@ -321,24 +384,17 @@ bsmm_status bsmm_expert_wgrad(const void* dy, int64_t ldy, bsmm_dtype dtype, int
   a.dw = dw; a.w_se = w_se; a.ldw = ldw; a.out_dtype = out_dtype;
   a.E = (int)E; a.Rx = (int)Rx; a.S = (int)S; a.N = (int)N; a.K = (int)K;
   uint8_t* ws = aligned(workspace, 16) ? static_cast<uint8_t*>(workspace) : nullptr;
-  size_t room = ws != nullptr ? workspace_bytes : 0;
-  Choice c = wgrad_plan(a, x_scale != nullptr, room);
-  // bf16: the codes are restored first where the wide tiles take them then
-  const size_t values = restored_bytes(dtype, x_scale != nullptr, Rx, K);
-  if (values > 0 && S > 0 && room >= values && aligned(x, 8) && ldx % 8 == 0) {
-    WgradArgs b = a;
-    b.x = ws; b.ldx = K; b.x_scale = nullptr;
-    const Choice r = wgrad_plan(b, false, room - values);
-    // 3 bytes an element and a launch
-    if (r.plan == ExpertPlan::Wide && r.us + 4.0 + (double)Rx * (double)K * 3 / 4e6 < c.us) {
-      if (launch_restore_bf16(x, ldx, x_scale, s_r, ws, Rx, K, stream) != 0)
-        return fail(BSMM_ERR_HIP, "kernel launch failed (checkpoint values)");
-      a = b;
-      c = r;
-      ws += values;
-    }
+  const WgradChoice w = wgrad_choice(a, aligned(x, 8) && ldx % 8 == 0,
+                                     ws != nullptr ? workspace_bytes : 0);
+  if (w.restored) {
+    if (launch_restore_bf16(x, ldx, x_scale, s_r, ws, Rx, K, stream) != 0)
+      return fail(BSMM_ERR_HIP, "kernel launch failed (checkpoint values)");
+    a.x = ws;
+    a.ldx = K;
+    a.x_scale = nullptr;
+    ws += restored_bytes(dtype, 1, Rx, K);
   }
-  if (launch_expert_wgrad(a, c.plan, c.splits, ws, stream) != 0)
+  if (launch_expert_wgrad(a, w.c.plan, w.c.splits, ws, stream) != 0)
     return fail(BSMM_ERR_HIP, "kernel launch failed (expert weight gradient)");
   return BSMM_OK;
 }

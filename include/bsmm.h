@@ -535,6 +535,16 @@ bsmm_status bsmm_w4_expert_mm(const void* x, int64_t ldx, bsmm_dtype x_dtype, co
  */
 size_t bsmm_expert_mm_workspace_bytes(bsmm_dtype dtype, int transposed, int64_t E, int64_t S,
                                       int64_t N, int64_t K);
+/*
+ * The kernel that a call takes with `workspace_bytes` of workspace, rows 16-byte
+ * aligned or not: "rows" (16 or 32 rows of an expert by 64 columns), "wide128",
+ * "wide192" or "wide256" (up to so many rows by 256 columns, bf16) or "tile64";
+ * *parts (where not NULL) gets the ranges of K.  NULL for sizes that have none.
+ * Results do not differ beyond the order of fp32 sums.
+ */
+const char* bsmm_expert_mm_plan_name(bsmm_dtype dtype, int transposed, int aligned, int64_t E,
+                                     int64_t S, int64_t N, int64_t K, size_t workspace_bytes,
+                                     int* parts);
 bsmm_status bsmm_expert_mm(const void* x, int64_t ldx, const void* w, int64_t w_se, int64_t w_sn,
                            int64_t w_sk, bsmm_dtype dtype, const int32_t* order,
                            const int32_t* offsets, int slots_per_row, const float* row_scale,
@@ -565,6 +575,14 @@ bsmm_status bsmm_expert_mm(const void* x, int64_t ldx, const void* w, int64_t w_
  */
 size_t bsmm_expert_wgrad_workspace_bytes(bsmm_dtype dtype, int checkpoint, int64_t E, int64_t Rx,
                                          int64_t S, int64_t N, int64_t K);
+/*
+ * The kernel that a call takes, as bsmm_expert_mm_plan_name: "wide256" (bf16),
+ * "tile128", "tile64", or "restored" (a checkpoint's values in the workspace
+ * first, then as wide256); *parts gets the parts of an expert's slots.
+ */
+const char* bsmm_expert_wgrad_plan_name(bsmm_dtype dtype, int checkpoint, bsmm_dtype out_dtype,
+                                        int aligned, int64_t E, int64_t Rx, int64_t S, int64_t N,
+                                        int64_t K, size_t workspace_bytes, int* parts);
 bsmm_status bsmm_expert_wgrad(const void* dy, int64_t ldy, bsmm_dtype dtype, int dy_slots_per_row,
                               const void* x, int64_t ldx, int x_slots_per_row,
                               const uint8_t* x_scale, int64_t s_r, const int32_t* order,
