@@ -98,7 +98,7 @@ Choice mm_plan(const ExpertArgs& a, size_t room) {
   };
   auto tiles = [&](int64_t bm, int64_t bn) { return items(bm) * (((int64_t)a.N + bn - 1) / bn); };
   const int64_t few = bf16 ? tiles(256, 256) < 256 ? 16 : 0 : a.w_across ? 32 : 24;
-  if (getenv("FEW") ? rows && a.S <= atoi(getenv("FEW"))*act : rows && a.S <= few * act) return Choice{ExpertPlan::Rows, 1, 0, 0};
+  if (rows && a.S <= few * act) return Choice{ExpertPlan::Rows, 1, 0, 0};
   const double outs = (double)a.S * a.N;
   const int64_t steps = ((int64_t)a.K + 63) / 64;
   // (of any alignment, but 4 columns at least where they are transposed)

@@ -1,6 +1,9 @@
 """The queries for the kernel of an experts' product and of its weight
 gradient, and the rules behind them (no GPU needed)."""
 
+import os
+import re
+
 import pytest
 
 import block_scaled_precision_gemm_amd as bsmm
@@ -46,3 +49,20 @@ def test_sizes_without_a_kernel(bad):
     assert mm("f32", False, *bad) is None and mm("bf16", True, *bad) is None
     assert wgrad("f32", False, E, S, S, N, K) is None
     assert wgrad("bf16", True, 1, 9, 9, 9, 40) is None
+
+
+@pytest.mark.parametrize("value", ["0", "", "100000"])
+def test_the_environment_changes_no_plan(value, monkeypatch):
+    sizes = [("bf16", False, 64, 8, 2048, 4096), ("bf16", False, 64, 8168, 2048, 4096),
+             ("f32", True, 16, 64, 1024, 4096), ("f32", False, 16, 900, 1024, 2048)]
+    before = [mm(*c) for c in sizes]
+    monkeypatch.setenv("FEW", value)
+    assert [mm(*c) for c in sizes] == before
+
+
+def test_every_variable_has_the_librarys_name():
+    csrc = os.path.join(os.path.dirname(bsmm.__file__), "csrc")
+    for name in sorted(os.listdir(csrc)):
+        with open(os.path.join(csrc, name)) as f:
+            for argument in re.findall(r"getenv\(([^)]*)\)", f.read()):
+                assert argument.startswith('"BSMM_'), (name, argument)
