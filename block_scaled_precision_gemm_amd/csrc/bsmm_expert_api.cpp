@@ -167,23 +167,47 @@ size_t restored_bytes(bsmm_dtype dtype, int checkpoint, int64_t Rx, int64_t K) {
   return dtype == BSMM_BF16 && checkpoint ? ((size_t)Rx * (size_t)K * 2u + 15u) / 16u * 16u : 0;
 }
 
-// A weight gradient's kernel, and whether it multiplies a checkpoint's values
-// restored to bf16 in the workspace first (whole: the codes' rows allow it).
+constexpr size_t kEnough = (size_t)256 << 20;       // no plan's parts are larger
+
+// The kernel of a call with `room` bytes of workspace.  First without a look at
+// the room, so that the order of the sums does not follow from what a buffer
+// happens to hold beyond the bytes that the query gives; with fewer than that
+// plan needs, the best that they allow.
+size_t parts_bytes(const ExpertArgs& a, const Choice& c) {
+  return c.splits > 1 ? (size_t)c.splits * (size_t)a.S * (size_t)a.N * 4u : 0;
+}
+Choice mm_choice(const ExpertArgs& a, size_t room) {
+  const Choice c = mm_plan(a, kEnough);
+  return parts_bytes(a, c) <= room ? c : mm_plan(a, room);
+}
+
+// The same for the weight gradient, and whether it multiplies a checkpoint's
+// values, restored to bf16 at the workspace's start (whole: the codes' rows
+// allow it).
 struct WgradChoice { Choice c; bool restored; };
+size_t parts_bytes(const WgradArgs& a, const Choice& c) {
+  return c.splits > 1 ? (size_t)c.splits * (size_t)a.E * (size_t)a.N * (size_t)a.K * 4u : 0;
+}
 WgradChoice wgrad_choice(const WgradArgs& a, bool whole, size_t room) {
   const bool codes = a.x_scale != nullptr;
-  WgradChoice w{wgrad_plan(a, codes, room), false};
-  // bf16: the codes are restored first where the wide tiles take them then
   const size_t values = restored_bytes(a.dtype, codes, a.Rx, a.K);
-  if (values > 0 && a.S > 0 && whole && room >= values) {
-    WgradArgs b = a;
-    b.ldx = a.K;
-    const Choice r = wgrad_plan(b, false, room - values);
-    // 3 bytes an element and a launch
-    if (r.plan == ExpertPlan::Wide && r.us + 4.0 + (double)a.Rx * (double)a.K * 3 / 4e6 < w.c.us)
-      w = WgradChoice{r, true};
-  }
-  return w;
+  // `parts` bytes for sums, and room for the values or none
+  auto best = [&](size_t parts, size_t parts_behind_values, bool fits) {
+    WgradChoice w{wgrad_plan(a, codes, parts), false};
+    if (values > 0 && a.S > 0 && whole && fits) {
+      WgradArgs b = a;
+      b.ldx = a.K;
+      const Choice r = wgrad_plan(b, false, parts_behind_values);
+      // where the wide tiles take them then: 3 bytes an element and a launch
+      if (r.plan == ExpertPlan::Wide &&
+          r.us + 4.0 + (double)a.Rx * (double)a.K * 3 / 4e6 < w.c.us)
+        w = WgradChoice{r, true};
+    }
+    return w;
+  };
+  const WgradChoice w = best(kEnough, kEnough, true);
+  if (parts_bytes(a, w.c) + (w.restored ? values : 0) <= room) return w;
+  return best(room, room - values, room >= values);
 }
 
 // Any non-null scales, for the queries: plans do not read them.
@@ -215,7 +239,6 @@ bool wgrad_sizes(bsmm_dtype dtype, int checkpoint, bool rows, int64_t E, int64_t
   return true;
 }
 
-constexpr size_t kEnough = (size_t)256 << 20;       // no plan's parts are larger
 
 }  // namespace
 
@@ -227,8 +250,7 @@ size_t bsmm_expert_mm_workspace_bytes(bsmm_dtype dtype, int transposed, int64_t 
   ExpertArgs a;
   for (int rows = 0; rows < 2; ++rows) {
     if (!mm_sizes(dtype, transposed, rows, E, S, N, K, a)) return 0;
-    const Choice c = mm_plan(a, kEnough);
-    const size_t bytes = c.splits > 1 ? (size_t)c.splits * (size_t)S * (size_t)N * 4u : 0;
+    const size_t bytes = parts_bytes(a, mm_plan(a, kEnough));
     if (bytes > need) need = bytes;
   }
   return need;
@@ -239,7 +261,7 @@ const char* bsmm_expert_mm_plan_name(bsmm_dtype dtype, int transposed, int align
                                      int* parts) {
   ExpertArgs a;
   if (!mm_sizes(dtype, transposed, aligned != 0, E, S, N, K, a)) return nullptr;
-  const Choice c = mm_plan(a, workspace_bytes);
+  const Choice c = mm_choice(a, workspace_bytes);
   if (parts != nullptr) *parts = c.splits;
   if (c.plan == ExpertPlan::Rows) return "rows";
   if (c.plan == ExpertPlan::Tiles64) return "tile64";
@@ -295,7 +317,7 @@ bsmm_status bsmm_expert_mm(const void* x, int64_t ldx, const void* w, int64_t w_
   a.x_div = slots_per_row;
   a.out = out; a.ldo = ldo; a.out_dtype = out_dtype;
   a.E = (int)E; a.R = (int)R; a.S = (int)S; a.N = (int)N; a.K = (int)K;
-  const Choice c = mm_plan(a, workspace != nullptr && aligned(workspace, 16) ? workspace_bytes : 0);
+  const Choice c = mm_choice(a, workspace != nullptr && aligned(workspace, 16) ? workspace_bytes : 0);
   if (launch_expert_mm(a, c.plan, c.rows, c.splits, workspace, stream) != 0)
     return fail(BSMM_ERR_HIP, "kernel launch failed (expert product)");
   return BSMM_OK;
@@ -307,13 +329,13 @@ size_t bsmm_expert_wgrad_workspace_bytes(bsmm_dtype dtype, int checkpoint, int64
   WgradArgs a;
   for (int rows = 0; rows < 2; ++rows) {
     if (!wgrad_sizes(dtype, 0, rows, E, Rx, S, N, K, a)) return 0;
-    // fp32 or bf16 output
-    for (int bf = 0; bf < 2; ++bf) {
-      a.out_dtype = bf ? BSMM_BF16 : BSMM_F32;
-      const Choice c = wgrad_plan(a, false, kEnough);
-      const size_t bytes = c.splits > 1 ? (size_t)c.splits * (size_t)E * N * K * 4u : 0;
-      if (bytes > need) need = bytes;
-    }
+    // codes as they are or restored, fp32 or bf16 output
+    for (int codes = 0; codes <= (checkpoint != 0); ++codes)
+      for (int bf = 0; bf < 2; ++bf) {
+        a.out_dtype = bf ? BSMM_BF16 : BSMM_F32;
+        const size_t bytes = parts_bytes(a, wgrad_plan(a, codes != 0, kEnough));
+        if (bytes > need) need = bytes;
+      }
   }
   return need + restored_bytes(dtype, checkpoint, Rx, K);
 }

@@ -531,7 +531,8 @@ bsmm_status bsmm_w4_expert_mm(const void* x, int64_t ldx, bsmm_dtype x_dtype, co
  * zeros.  The workspace (16-byte aligned) holds fp32 sums over ranges of K
  * where a call has too few tiles to fill the chip:
  * bsmm_expert_mm_workspace_bytes gives the bytes (0: none wanted; transposed:
- * w_sn is 1).  With less the call runs with fewer ranges.
+ * w_sn is 1).  With more than that nothing changes; with less the call runs
+ * with fewer ranges.
  */
 size_t bsmm_expert_mm_workspace_bytes(bsmm_dtype dtype, int transposed, int64_t E, int64_t S,
                                       int64_t N, int64_t K);
@@ -571,7 +572,8 @@ bsmm_status bsmm_expert_mm(const void* x, int64_t ldx, const void* w, int64_t w_
  * The workspace (16-byte aligned) holds a checkpoint's values in bf16, and
  * fp32 sums over parts of the slots where dw has too few tiles to fill the
  * chip: bsmm_expert_wgrad_workspace_bytes gives the bytes (0: none wanted).
- * With less the call runs without, slower.
+ * With more than that nothing changes; with less the call runs with fewer
+ * parts or without, slower.
  */
 size_t bsmm_expert_wgrad_workspace_bytes(bsmm_dtype dtype, int checkpoint, int64_t E, int64_t Rx,
                                          int64_t S, int64_t N, int64_t K);

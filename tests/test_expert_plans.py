@@ -2,6 +2,7 @@
 gradient, and the rules behind them (no GPU needed)."""
 
 import os
+import random
 import re
 
 import pytest
@@ -66,3 +67,63 @@ def test_every_variable_has_the_librarys_name():
         with open(os.path.join(csrc, name)) as f:
             for argument in re.findall(r"getenv\(([^)]*)\)", f.read()):
                 assert argument.startswith('"BSMM_'), (name, argument)
+
+
+def random_sizes(n, seed):
+    rng = random.Random(seed)
+    log = lambda lo, hi: int(round(lo * (hi / lo) ** rng.random()))  # noqa: E731
+    for _ in range(n):
+        N, K = log(16, 8192), log(16, 8192)
+        if rng.random() < 0.6:
+            N, K = max(32, N // 32 * 32), max(32, K // 32 * 32)
+        yield rng.random() < 0.5, log(1, 64), log(1, 30000), N, K
+
+
+NAMED = [(True, 1, 804, 2872, 3136), (True, 4, 1222, 1840, 2688), (True, 15, 11712, 72, 1760)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_a_larger_workspace_changes_nothing(dt):
+    """The order of the sums follows from the call alone: with the bytes that
+    the query gives the plan is that of any larger workspace, such as one that
+    other calls have left."""
+    for back, E, S, N, K in NAMED + list(random_sizes(4000, 1)):
+        for rows in (True, False):
+            same = {mm(dt, back, E, S, N, K, aligned=rows, workspace=room)
+                    for room in (None, 2**27 + 12345, 2**28, 2**40)
+                    if room is None or
+                    room >= bsmm.bsmm_expert_mm_workspace_bytes(dt, back, E, S, N, K)}
+            assert len(same) == 1, (back, E, S, N, K, rows, same)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("checkpoint", [False, True])
+def test_a_larger_workspace_changes_no_gradient(checkpoint, dt):
+    for second, E, S, N, K in random_sizes(4000, 2):
+        K = max(32, K // 32 * 32) if checkpoint else K
+        Rx = max(1, S // 4) if second else S
+        need = bsmm.bsmm_expert_wgrad_workspace_bytes(dt, checkpoint, E, Rx, S, N, K)
+        for odt in ("bf16", "f32"):
+            for rows in (True, False):
+                same = {wgrad(dt, checkpoint, E, Rx, S, N, K, out_dtype=odt, aligned=rows,
+                              workspace=room)
+                        for room in (None, 2**27 + 12345, 2**28, 2**40)
+                        if room is None or room >= need}
+                assert len(same) == 1, (E, Rx, S, N, K, odt, rows, same)
+
+
+def test_a_smaller_workspace_is_enough_for_its_plan():
+    rng = random.Random(3)
+    for back, E, S, N, K in NAMED + list(random_sizes(2000, 4)):
+        need = bsmm.bsmm_expert_mm_workspace_bytes("bf16", back, E, S, N, K)
+        for room in (0, need // 2, rng.randint(0, need)):
+            parts = mm("bf16", back, E, S, N, K, workspace=room)[1]
+            assert parts == 1 or parts * S * N * 4 <= room
+        K = max(32, K // 32 * 32)
+        values = S * K * 2
+        need = bsmm.bsmm_expert_wgrad_workspace_bytes("bf16", True, E, S, S, N, K)
+        for room in (0, need // 2, values - 1, values, rng.randint(0, need)):
+            name, parts = wgrad("bf16", True, E, S, S, N, K, workspace=room)
+            used = (values if name == "restored" else 0) + \
+                (parts * E * N * K * 4 if parts > 1 else 0)
+            assert used <= room
