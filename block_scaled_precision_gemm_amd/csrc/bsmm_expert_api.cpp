@@ -16,8 +16,9 @@ namespace {
 bool float_dtype(bsmm_dtype d) { return d == BSMM_F32 || d == BSMM_BF16; }
 uintptr_t dtype_bytes(bsmm_dtype d) { return d == BSMM_BF16 ? 2 : 4; }
 constexpr int64_t kMaxExperts = 1024;
-// positions are counted a few steps past the last slot, in 32 bits
-constexpr int64_t kMaxSlots = kMaxDim - 1024;
+// of slots, columns and the contraction: all are counted up to a tile and a few
+// steps past the last one, in 32 bits
+constexpr int64_t kMaxSize = kMaxDim - 1024;
 
 // A kernel and the ranges of the contraction it is cut into.
 struct Choice { ExpertPlan plan; int splits; double us; int rows; };
@@ -217,7 +218,7 @@ constexpr uint8_t kSome = 0;
 bool mm_sizes(bsmm_dtype dtype, int transposed, bool rows, int64_t E, int64_t S, int64_t N,
               int64_t K, ExpertArgs& a) {
   if (!float_dtype(dtype) || E <= 0 || S <= 0 || N <= 0 || K <= 0 || E > kMaxExperts ||
-      S >= kMaxDim || N >= kMaxDim || K >= kMaxDim)
+      S >= kMaxSize || N >= kMaxSize || K >= kMaxSize)
     return false;
   a = ExpertArgs{};
   a.dtype = dtype;
@@ -229,7 +230,7 @@ bool mm_sizes(bsmm_dtype dtype, int transposed, bool rows, int64_t E, int64_t S,
 bool wgrad_sizes(bsmm_dtype dtype, int checkpoint, bool rows, int64_t E, int64_t Rx, int64_t S,
                  int64_t N, int64_t K, WgradArgs& a) {
   if (!float_dtype(dtype) || E <= 0 || Rx <= 0 || S <= 0 || N <= 0 || K <= 0 || E > kMaxExperts ||
-      Rx >= kMaxDim || S >= kMaxDim || N >= kMaxDim || K >= kMaxDim)
+      Rx >= kMaxDim || S >= kMaxSize || N >= kMaxSize || K >= kMaxSize)
     return false;
   a = WgradArgs{};
   a.dtype = dtype;
@@ -279,8 +280,8 @@ bsmm_status bsmm_expert_mm(const void* x, int64_t ldx, const void* w, int64_t w_
   CHECK(E >= 0 && R >= 0 && S >= 0 && N >= 0 && K >= 0, BSMM_ERR_SHAPE,
         "negative size E=%lld R=%lld S=%lld N=%lld K=%lld", (long long)E, (long long)R,
         (long long)S, (long long)N, (long long)K);
-  CHECK(R < kMaxDim && S < kMaxSlots && N < kMaxDim && K < kMaxDim, BSMM_ERR_UNSUPPORTED,
-        "size beyond 2^31");
+  CHECK(R < kMaxDim && S < kMaxSize && N < kMaxSize && K < kMaxSize, BSMM_ERR_UNSUPPORTED,
+        "R beyond 2^31, or S, N or K beyond 2^31 - 1024");
   CHECK(E <= kMaxExperts, BSMM_ERR_UNSUPPORTED, "E=%lld beyond %lld experts", (long long)E,
         (long long)kMaxExperts);
   CHECK(slots_per_row >= 1, BSMM_ERR_ARG, "slots_per_row=%d", slots_per_row);
@@ -367,8 +368,8 @@ bsmm_status bsmm_expert_wgrad(const void* dy, int64_t ldy, bsmm_dtype dtype, int
   CHECK(E >= 0 && Ry >= 0 && Rx >= 0 && S >= 0 && N >= 0 && K >= 0, BSMM_ERR_SHAPE,
         "negative size E=%lld Ry=%lld Rx=%lld S=%lld N=%lld K=%lld", (long long)E, (long long)Ry,
         (long long)Rx, (long long)S, (long long)N, (long long)K);
-  CHECK(Ry < kMaxDim && Rx < kMaxDim && S < kMaxSlots && N < kMaxDim && K < kMaxDim,
-        BSMM_ERR_UNSUPPORTED, "size beyond 2^31");
+  CHECK(Ry < kMaxDim && Rx < kMaxDim && S < kMaxSize && N < kMaxSize && K < kMaxSize,
+        BSMM_ERR_UNSUPPORTED, "Ry or Rx beyond 2^31, or S, N or K beyond 2^31 - 1024");
   CHECK(E <= kMaxExperts, BSMM_ERR_UNSUPPORTED, "E=%lld beyond %lld experts", (long long)E,
         (long long)kMaxExperts);
   CHECK(dy_slots_per_row >= 1 && x_slots_per_row >= 1, BSMM_ERR_ARG, "slots per row %d and %d",

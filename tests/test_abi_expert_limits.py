@@ -1,0 +1,27 @@
+"""Sizes of the experts' products next to 2^31, where their kernels' 32-bit
+counts of elements, a tile past the last one, would wrap: refused, before any
+HIP call and so without a GPU (see test_abi_expert.py)."""
+
+import pytest
+
+import block_scaled_precision_gemm_amd as bsmm
+from test_abi_expert import BF16, F32, UNSUP, mm, wgrad
+
+TOP = 2**31 - 1024
+
+
+@pytest.mark.parametrize("n", [TOP, TOP + 1, 2**31 - 64, 2**31 - 1, 2**31])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_refused(n, dt):
+    assert mm(dt=dt, E=1, K=n, ldx=2**31, w_sn=2**31, w_se=2**36) == UNSUP
+    assert mm(dt=dt, E=1, K=n, ldx=2**31, w_sn=1, w_sk=32, w_se=2**36) == UNSUP
+    assert mm(dt=dt, E=1, R=1, S=1, per=1, N=n, ldo=2**31) == UNSUP
+    assert mm(dt=dt, E=1, R=1, S=1, per=1, N=n, ldo=2**31, w_sn=1, w_sk=2**31) == UNSUP
+    assert wgrad(dt=dt, E=1, N=n, ldy=2**31, w_se=2**62) == UNSUP
+    assert wgrad(dt=dt, E=1, K=n, ldx=2**31, ldw=2**31, w_se=2**62) == UNSUP
+    code = "bf16" if dt == BF16 else "f32"
+    for size in ((n, 64, 64), (64, n, 64), (64, 64, n)):
+        assert bsmm.bsmm_expert_mm_plan_name(code, False, 1, *size) is None
+        assert bsmm.bsmm_expert_mm_workspace_bytes(code, False, 1, *size) == 0
+        assert bsmm.bsmm_expert_wgrad_plan_name(code, False, 1, 64, *size) is None
+        assert bsmm.bsmm_expert_wgrad_workspace_bytes(code, False, 1, 64, *size) == 0
