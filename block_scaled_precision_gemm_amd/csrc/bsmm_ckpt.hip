@@ -202,44 +202,46 @@ __global__ void __launch_bounds__(256) swiglu(SwigluArgs a, unsigned chunks) {
 template <typename T>
 __global__ void __launch_bounds__(256) swiglu_backward(SwigluBackArgs a) {
   const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= a.R) return;
-  const T* da = static_cast<const T*>(a.da) + row * a.ldda;
-  const int8_t* q = a.q + row * a.ldq;
-  const uint8_t* s = a.scale + row * a.s_r;
-  T* dh = static_cast<T*>(a.dh) + row * a.lddh;
-  const float r = a.row_scale ? a.row_scale[row] : 1.0f;
-  float sum = 0.0f;
-  for (int k = lane * 8; k < a.F; k += 512) {
-    float d[8], g[8], u[8];
-    load8(da + k, d);
-    decode(*reinterpret_cast<const uint2*>(q + k), s[k >> 5], g);
-    decode(*reinterpret_cast<const uint2*>(q + a.F + k), s[(a.F + k) >> 5], u);
+  for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); row < a.R;
+       row += (int64_t)gridDim.x * 4) {
+    const T* da = static_cast<const T*>(a.da) + row * a.ldda;
+    const int8_t* q = a.q + row * a.ldq;
+    const uint8_t* s = a.scale + row * a.s_r;
+    T* dh = static_cast<T*>(a.dh) + row * a.lddh;
+    const float r = a.row_scale ? a.row_scale[row] : 1.0f;
+    float sum = 0.0f;
+    for (int k = lane * 8; k < a.F; k += 512) {
+      float d[8], g[8], u[8];
+      load8(da + k, d);
+      decode(*reinterpret_cast<const uint2*>(q + k), s[k >> 5], g);
+      decode(*reinterpret_cast<const uint2*>(q + a.F + k), s[(a.F + k) >> 5], u);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const Sigmas sg = sigmas(g[j]);
-      const float silu = g[j] * sg.s, act = silu * u[j];
-      sum = __builtin_fmaf(d[j], act, sum);
-      const float rd = r * d[j];
-      // silu' = sg (1 + g (1 - sg))
-      const float slope = __builtin_fmaf(silu, sg.c, sg.s);
-      g[j] = rd * u[j] * slope;
-      u[j] = rd * silu;
-      d[j] = r * act;
+      for (int j = 0; j < 8; ++j) {
+        const Sigmas sg = sigmas(g[j]);
+        const float silu = g[j] * sg.s, act = silu * u[j];
+        sum = __builtin_fmaf(d[j], act, sum);
+        const float rd = r * d[j];
+        // silu' = sg (1 + g (1 - sg))
+        const float slope = __builtin_fmaf(silu, sg.c, sg.s);
+        g[j] = rd * u[j] * slope;
+        u[j] = rd * silu;
+        d[j] = r * act;
+      }
+      store8(dh + k, g);
+      store8(dh + a.F + k, u);
+      if (a.act) store8(static_cast<T*>(a.act) + row * a.ldact + k, d);
     }
-    store8(dh + k, g);
-    store8(dh + a.F + k, u);
-    if (a.act) store8(static_cast<T*>(a.act) + row * a.ldact + k, d);
-  }
-  if (a.drow) {
+    if (a.drow) {
 #pragma unroll
-    for (int m = 32; m > 0; m >>= 1) sum += __shfl_xor(sum, m);
-    if (lane == 0) a.drow[row] = sum;
+      for (int m = 32; m > 0; m >>= 1) sum += __shfl_xor(sum, m);
+      if (lane == 0) a.drow[row] = sum;
+    }
   }
 }
 
-unsigned blocks_for(int64_t chunks) {
-  const int64_t b = (chunks + 255) / 256;
+// Workgroups for `threads` of work, 256 each; beyond 65536 of them they loop.
+unsigned blocks_for(int64_t threads) {
+  const int64_t b = (threads + 255) / 256;
   return (unsigned)(b < 65536 ? b : 65536);
 }
 
@@ -282,7 +284,7 @@ int launch_swiglu(const SwigluArgs& a, void* stream) {
 
 int launch_swiglu_backward(const SwigluBackArgs& a, void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const dim3 grid((unsigned)((a.R + 3) / 4)), block(256);
+  const dim3 grid(blocks_for(a.R * 64)), block(256);
   if (a.dtype == BSMM_BF16) hipLaunchKernelGGL(swiglu_backward<uint16_t>, grid, block, 0, st, a);
   else hipLaunchKernelGGL(swiglu_backward<float>, grid, block, 0, st, a);
   return hipGetLastError() == hipSuccess ? 0 : 1;
