@@ -1117,35 +1117,46 @@ Divisor divisor(uint32_t d) {
   return Divisor{(uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << l) - d)) / d + 1), l};
 }
 
+// The launch of items of few rows: at most bm of them, by cn = 8 >> log_ks
+// groups of 64 columns.
+struct RowsGrid {
+  int bm, log_ks;
+  int64_t items, ntn;
+  explicit RowsGrid(const ExpertArgs& a) {
+    const int64_t act = a.E < a.S ? a.E : a.S, groups = ((int64_t)a.N + 63) / 64;
+    // (64 x 2 of 8 of 1024 x 2048: 14.3 us in items of 16, 16.3 of 32; others below)
+    bm = a.w_across || act * groups < 256 ? 16 : 32;
+    items = ((int64_t)a.S + act * (bm - 1)) / bm;
+    // Waves that fill the chip, in workgroups of even cost.  Along: 1024 groups
+    // in 1, 2, 4 or 8 ranges take 176, 126, 106, 112 us (8 tokens x 8 of 32
+    // experts of 2048 x 4096); where experts have items of either kind, 150,
+    // 129, 125, 108 (128 x 4 of 16 of 4096 x 1024 fp32).  Across, an expert's
+    // second item reads the weights again: better while the first does, so all
+    // waves take the same columns then (64 x 4 of 16 of 4096 x 1024 fp32: 266,
+    // 141, 81, 78 us; 32 x 8 of 32 of 2048 x 4096: 124, 109, 106, 111; 16 x 8:
+    // 92, 94, 95, 103).
+    int64_t busy, target;
+    if (a.w_across) {
+      busy = (a.S + act * 8) / 16 + 1;
+      target = a.S <= 6 * act ? 2048 : 8192;
+    } else {
+      busy = a.S <= 16 * act ? act : (a.S + act * 16) / 32;
+      target = a.S <= 16 * act ? 4096 : 32768;
+    }
+    log_ks = 0;
+    while (log_ks < 3 && (busy * groups << log_ks) < target) ++log_ks;
+    ntn = (groups + (8 >> log_ks) - 1) / (8 >> log_ks);
+  }
+};
+
 template <typename T, bool W_ACROSS>
 void launch_rows(const ExpertArgs& a, hipStream_t st) {
-  const int64_t act = a.E < a.S ? a.E : a.S, groups = ((int64_t)a.N + 63) / 64;
-  // (64 x 2 of 8 of 1024 x 2048: 14.3 us in items of 16, 16.3 of 32; others below)
-  const int bm = W_ACROSS || act * groups < 256 ? 16 : 32;
-  const int64_t items = ((int64_t)a.S + act * (bm - 1)) / bm;
-  // Waves that fill the chip, in workgroups of even cost.  Along: 1024 groups
-  // in 1, 2, 4 or 8 ranges take 176, 126, 106, 112 us (8 tokens x 8 of 32
-  // experts of 2048 x 4096); where experts have items of either kind, 150,
-  // 129, 125, 108 (128 x 4 of 16 of 4096 x 1024 fp32).  Across, an expert's
-  // second item reads the weights again: better while the first does, so all
-  // waves take the same columns then (64 x 4 of 16 of 4096 x 1024 fp32: 266,
-  // 141, 81, 78 us; 32 x 8 of 32 of 2048 x 4096: 124, 109, 106, 111; 16 x 8:
-  // 92, 94, 95, 103).
-  int64_t busy, target;
-  if (W_ACROSS) {
-    busy = (a.S + act * 8) / 16 + 1;
-    target = a.S <= 6 * act ? 2048 : 8192;
-  } else {
-    busy = a.S <= 16 * act ? act : (a.S + act * 16) / 32;
-    target = a.S <= 16 * act ? 4096 : 32768;
-  }
-  int log_ks = 0;
-  while (log_ks < 3 && (busy * groups << log_ks) < target) ++log_ks;
-  const int64_t ntn = (groups + (8 >> log_ks) - 1) / (8 >> log_ks);
-  for (int64_t i = 0; i < items; i += 65535)        // at most so many items a launch
+  const RowsGrid g(a);
+  for (int64_t i = 0; i < g.items; i += 65535)      // at most so many items a launch
     hipLaunchKernelGGL((expert_mm_rows<T, W_ACROSS>),
-                       dim3((unsigned)ntn, (unsigned)(items - i < 65535 ? items - i : 65535)),
-                       dim3(kRowsWaves * 64), 0, st, a, (int)i, bm, log_ks);
+                       dim3((unsigned)g.ntn,
+                            (unsigned)(g.items - i < 65535 ? g.items - i : 65535)),
+                       dim3(kRowsWaves * 64), 0, st, a, (int)i, g.bm, g.log_ks);
 }
 
 void launch_reduce(const float* parts, int splits, void* out, bsmm_dtype dt, int64_t rows,
@@ -1165,12 +1176,53 @@ void launch_reduce(const float* parts, int splits, void* out, bsmm_dtype dt, int
 // 65 in runs of 8).
 struct Deal {
   int run;
-  dim3 grid;
+  int64_t grid;
   Deal(int64_t tiles, int64_t real, bool one) {
     const int64_t eighth = (real + 7) / 8;
     run = (int)(one || eighth < 8 ? eighth : 8);
-    grid = dim3((unsigned)((tiles + 8 * run - 1) / (8 * run) * (8 * run)));
+    grid = (tiles + 8 * run - 1) / (8 * run) * (8 * run);
   }
+};
+
+// Items, columns of tiles and the dealing of a product's tiles, and of the
+// weight gradient's.
+struct MmGrid {
+  int items, ntn, threads;
+  Deal deal;
+  MmGrid(const ExpertArgs& a, ExpertPlan plan, int rows, int splits)
+      : MmGrid(a, plan == ExpertPlan::Wide ? rows : 64, plan == ExpertPlan::Wide ? kWide : 64,
+               splits) {
+    threads = plan == ExpertPlan::Wide ? 512 : 256;
+  }
+
+ private:
+  static int items_of(const ExpertArgs& a, int bm) {
+    const int64_t act = a.E < a.S ? a.E : a.S;
+    return (int)(((int64_t)a.S + act * (bm - 1)) / bm);
+  }
+  static int64_t real_of(const ExpertArgs& a, int bm) {
+    const int64_t act = a.E < a.S ? a.E : a.S;
+    const int64_t real = ((int64_t)a.S + act * (bm / 2)) / bm, items = items_of(a, bm);
+    return real < act ? act : real < items ? real : items;
+  }
+  MmGrid(const ExpertArgs& a, int bm, int bn, int splits)
+      : items(items_of(a, bm)), ntn((a.N + bn - 1) / bn), threads(0),
+        deal((int64_t)items * splits * ntn, real_of(a, bm) * splits * ntn,
+             (a.E < a.S ? a.E : a.S) == 1) {}
+};
+struct WgradGrid {
+  int ntn, ntk, threads;
+  Deal deal;
+  WgradGrid(const WgradArgs& a, ExpertPlan plan, int splits)
+      : WgradGrid(a, plan == ExpertPlan::Wide ? 256 : plan == ExpertPlan::Tiles128 ? 128 : 64,
+                  splits) {
+    threads = plan == ExpertPlan::Wide ? 512 : 256;
+  }
+
+ private:
+  WgradGrid(const WgradArgs& a, int tile, int splits)
+      : ntn((a.N + tile - 1) / tile), ntk((a.K + tile - 1) / tile), threads(0),
+        deal((int64_t)splits * a.E * ntn * ntk, (int64_t)splits * a.E * ntn * ntk, false) {}
 };
 
 template <typename T, bool W_ACROSS>
@@ -1184,47 +1236,37 @@ void launch_mm(ExpertArgs a, ExpertPlan plan, int rows, int splits, void* ws, hi
     a.ldo = a.N;
     a.out_dtype = BSMM_F32;
   }
-  const int64_t act = a.E < a.S ? a.E : a.S;
-  const int bn = plan == ExpertPlan::Wide ? kWide : 64;
-  const int bm = plan == ExpertPlan::Wide ? rows : bn;
-  const int items = (int)(((int64_t)a.S + act * (bm - 1)) / bm), ntn = (a.N + bn - 1) / bn;
-  int64_t real = ((int64_t)a.S + act * (bm / 2)) / bm;
-  if (real < act) real = act;
-  const Deal deal((int64_t)items * splits * ntn, (real < items ? real : items) * splits * ntn,
-                  act == 1);
-  const dim3 grid = deal.grid;
+  const MmGrid g(a, plan, rows, splits);
+  const dim3 grid((unsigned)g.deal.grid), block(g.threads);
   if (plan == ExpertPlan::Wide) {
-    if constexpr (sizeof(T) == 2)
-    {
+    if constexpr (sizeof(T) == 2) {
       const bool direct = !W_ACROSS && a.K % 8 == 0 && aligned_rows(a.x, a.ldx, a.dtype) &&
                           aligned_rows(a.w, a.ldw, a.dtype) && a.w_se % 8 == 0;
       if (direct)
-        hipLaunchKernelGGL((expert_mm_wide<W_ACROSS, !W_ACROSS>), grid, dim3(512), kWideBytes, st,
-                           a, rows, items, ntn, splits, deal.run);
+        hipLaunchKernelGGL((expert_mm_wide<W_ACROSS, !W_ACROSS>), grid, block, kWideBytes, st, a,
+                           rows, g.items, g.ntn, splits, g.deal.run);
       else
-        hipLaunchKernelGGL((expert_mm_wide<W_ACROSS, false>), grid, dim3(512), kWideBytes, st, a,
-                           rows, items, ntn, splits, deal.run);
+        hipLaunchKernelGGL((expert_mm_wide<W_ACROSS, false>), grid, block, kWideBytes, st, a, rows,
+                           g.items, g.ntn, splits, g.deal.run);
     }
   } else {
-    hipLaunchKernelGGL((expert_mm_kernel<T, 1, W_ACROSS>), grid, dim3(256), 0, st, a, items, ntn,
-                       splits, deal.run);
+    hipLaunchKernelGGL((expert_mm_kernel<T, 1, W_ACROSS>), grid, block, 0, st, a, g.items, g.ntn,
+                       splits, g.deal.run);
   }
   if (splits > 1)
     launch_reduce(static_cast<const float*>(ws), splits, out, dt, a.S, a.N, a.S, 0, ldo, st);
 }
 
 template <typename T, int MB>
-void launch_wgrad_tiles(const WgradArgs& a, int ntn, int ntk, int splits, hipStream_t st) {
-  const int64_t tiles = (int64_t)splits * a.E * ntn * ntk;
-  const Deal deal(tiles, tiles, false);
-  const dim3 grid = deal.grid, block(256);
+void launch_wgrad_tiles(const WgradArgs& a, const WgradGrid& g, int splits, hipStream_t st) {
+  const dim3 grid((unsigned)g.deal.grid), block(g.threads);
   const Divisor yd = divisor(a.y_div), xd = divisor(a.x_div);
   if (a.x_scale)
-    hipLaunchKernelGGL((expert_wgrad_kernel<T, MB, true>), grid, block, 0, st, a, ntn, ntk, splits,
-                       deal.run, yd, xd);
+    hipLaunchKernelGGL((expert_wgrad_kernel<T, MB, true>), grid, block, 0, st, a, g.ntn, g.ntk,
+                       splits, g.deal.run, yd, xd);
   else
-    hipLaunchKernelGGL((expert_wgrad_kernel<T, MB, false>), grid, block, 0, st, a, ntn, ntk, splits,
-                       deal.run, yd, xd);
+    hipLaunchKernelGGL((expert_wgrad_kernel<T, MB, false>), grid, block, 0, st, a, g.ntn, g.ntk,
+                       splits, g.deal.run, yd, xd);
 }
 
 template <typename T>
@@ -1238,18 +1280,16 @@ void launch_wgrad(WgradArgs a, ExpertPlan plan, int splits, void* ws, hipStream_
     a.w_se = (int64_t)a.N * a.K;
     a.out_dtype = BSMM_F32;
   }
-  const int tile = plan == ExpertPlan::Wide ? 256 : plan == ExpertPlan::Tiles128 ? 128 : 64;
-  const int ntn = (a.N + tile - 1) / tile, ntk = (a.K + tile - 1) / tile;
+  const WgradGrid g(a, plan, splits);
   if (plan == ExpertPlan::Wide) {
-    const int64_t tiles = (int64_t)splits * a.E * ntn * ntk;
-    const Deal deal(tiles, tiles, false);
     if constexpr (sizeof(T) == 2)
-      hipLaunchKernelGGL(expert_wgrad_wide, deal.grid, dim3(512), kWideBytes, st, a, ntn, ntk,
-                         splits, deal.run, divisor(a.y_div), divisor(a.x_div));
+      hipLaunchKernelGGL(expert_wgrad_wide, dim3((unsigned)g.deal.grid), dim3(g.threads),
+                         kWideBytes, st, a, g.ntn, g.ntk, splits, g.deal.run, divisor(a.y_div),
+                         divisor(a.x_div));
   } else if (plan == ExpertPlan::Tiles128) {
-    launch_wgrad_tiles<T, 2>(a, ntn, ntk, splits, st);
+    launch_wgrad_tiles<T, 2>(a, g, splits, st);
   } else {
-    launch_wgrad_tiles<T, 1>(a, ntn, ntk, splits, st);
+    launch_wgrad_tiles<T, 1>(a, g, splits, st);
   }
   if (splits > 1)
     launch_reduce(static_cast<const float*>(ws), splits, dw, dt, (int64_t)a.E * a.N, a.K, a.N, w_se,
@@ -1257,6 +1297,17 @@ void launch_wgrad(WgradArgs a, ExpertPlan plan, int splits, void* ws, hipStream_
 }
 
 }  // namespace
+
+uint64_t expert_mm_threads(const ExpertArgs& a, ExpertPlan plan, int rows, int splits) {
+  if (plan == ExpertPlan::Rows) return (uint64_t)RowsGrid(a).ntn * (kRowsWaves * 64);   // in x
+  const MmGrid g(a, plan, rows, splits);
+  return (uint64_t)g.deal.grid * (uint64_t)g.threads;
+}
+
+uint64_t expert_wgrad_threads(const WgradArgs& a, ExpertPlan plan, int splits) {
+  const WgradGrid g(a, plan, splits);
+  return (uint64_t)g.deal.grid * (uint64_t)g.threads;
+}
 
 int launch_expert_mm(const ExpertArgs& a, ExpertPlan plan, int rows, int splits, void* ws,
                      void* stream) {

@@ -294,7 +294,7 @@ bsmm_status bsmm_expert_mm(const void* x, int64_t ldx, const void* w, int64_t w_
         "order, offsets or row_scale not 4-byte aligned");
   CHECK(ldo >= N, BSMM_ERR_SHAPE, "ldo=%lld below N", (long long)ldo);
   CHECK(aligned(out, dtype_bytes(out_dtype)), BSMM_ERR_ALIGN, "out not aligned to its type");
-  // the grid's tiles, at least 16 rows by 16 columns each
+  // tiles are counted in 31 bits, of at least 16 rows by 16 columns each
   CHECK((S / 16 + E + 1) * (N / 16 + 1) < kMaxDim, BSMM_ERR_UNSUPPORTED,
         "S * N beyond the largest grid");
   ExpertArgs a{};
@@ -319,6 +319,8 @@ bsmm_status bsmm_expert_mm(const void* x, int64_t ldx, const void* w, int64_t w_
   a.out = out; a.ldo = ldo; a.out_dtype = out_dtype;
   a.E = (int)E; a.R = (int)R; a.S = (int)S; a.N = (int)N; a.K = (int)K;
   const Choice c = mm_choice(a, workspace != nullptr && aligned(workspace, 16) ? workspace_bytes : 0);
+  CHECK(expert_mm_threads(a, c.plan, c.rows, c.splits) < kMaxThreads, BSMM_ERR_UNSUPPORTED,
+        "S * N beyond the largest grid");
   if (launch_expert_mm(a, c.plan, c.rows, c.splits, workspace, stream) != 0)
     return fail(BSMM_ERR_HIP, "kernel launch failed (expert product)");
   return BSMM_OK;
@@ -409,6 +411,8 @@ bsmm_status bsmm_expert_wgrad(const void* dy, int64_t ldy, bsmm_dtype dtype, int
   uint8_t* ws = aligned(workspace, 16) ? static_cast<uint8_t*>(workspace) : nullptr;
   const WgradChoice w = wgrad_choice(a, aligned(x, 8) && ldx % 8 == 0,
                                      ws != nullptr ? workspace_bytes : 0);
+  CHECK(expert_wgrad_threads(a, w.c.plan, w.c.splits) < kMaxThreads, BSMM_ERR_UNSUPPORTED,
+        "E * N * K beyond the largest grid");
   if (w.restored) {
     if (launch_restore_bf16(x, ldx, x_scale, s_r, ws, Rx, K, stream) != 0)
       return fail(BSMM_ERR_HIP, "kernel launch failed (checkpoint values)");

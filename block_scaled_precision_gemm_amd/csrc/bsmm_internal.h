@@ -261,6 +261,11 @@ struct ExpertArgs {
 // or 64 x 64.  splits > 1: ranges of the contraction, their sums in ws (splits
 // * S * N fp32).
 enum class ExpertPlan { Rows, Wide, Tiles128, Tiles64 };
+// A launch counts its threads in 32 bits, and one of more runs as many as the
+// low 32 bits say, without an error: its caller refuses it.
+constexpr uint64_t kMaxThreads = (uint64_t)1 << 32;
+// The threads of a plan's largest launch
+uint64_t expert_mm_threads(const ExpertArgs& a, ExpertPlan plan, int rows, int splits);
 int launch_expert_mm(const ExpertArgs& a, ExpertPlan plan, int rows, int splits, void* ws,
                      void* stream);
 
@@ -277,6 +282,7 @@ struct WgradArgs {
   void* dw; int64_t w_se, ldw; bsmm_dtype out_dtype;
   int E, Rx, S, N, K;
 };
+uint64_t expert_wgrad_threads(const WgradArgs& a, ExpertPlan plan, int splits);
 // splits > 1: parts of every run, their sums in ws (splits * E * N * K fp32)
 int launch_expert_wgrad(const WgradArgs& a, ExpertPlan plan, int splits, void* ws, void* stream);
 // A checkpoint's values in bf16, rows of K (0 on success)

@@ -527,8 +527,9 @@ bsmm_status bsmm_w4_expert_mm(const void* x, int64_t ldx, bsmm_dtype x_dtype, co
  * order, offsets, slots_per_row and row_scale as for bsmm_w4_expert_mm; order
  * NULL: slot i at position i.  fp32 sums of unrounded products in a fixed
  * order.  Any N and K; pointers aligned to their types (16-byte aligned rows
- * are faster).  E <= 1024; S, N and K < 2^31 - 1024.  S == 0 or N == 0 does
- * nothing, K == 0 writes zeros.  The workspace (16-byte aligned) holds fp32 sums over ranges of K
+ * are faster).  E <= 1024; S, N and K < 2^31 - 1024.  A call of so many tiles
+ * (64 x 64 at least, partly empty ones among them) that they need 2^32 threads
+ * is refused.  S == 0 or N == 0 does nothing, K == 0 writes zeros.  The workspace (16-byte aligned) holds fp32 sums over ranges of K
  * where a call has too few tiles to fill the chip:
  * bsmm_expert_mm_workspace_bytes gives the bytes (0: none wanted; transposed:
  * w_sn is 1).  With more than that nothing changes; with less the call runs

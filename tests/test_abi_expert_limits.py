@@ -25,3 +25,20 @@ def test_refused(n, dt):
         assert bsmm.bsmm_expert_mm_workspace_bytes(code, False, 1, *size) == 0
         assert bsmm.bsmm_expert_wgrad_plan_name(code, False, 1, 64, *size) is None
         assert bsmm.bsmm_expert_wgrad_workspace_bytes(code, False, 1, 64, *size) == 0
+
+
+@pytest.mark.parametrize("kw", [
+    # few rows of many experts by very many columns
+    dict(E=1024, R=1024, S=1024, per=1, N=2**24, K=1, ldx=1, w_sn=1, w_se=0, ldo=2**24),
+    dict(E=1024, R=1024, S=1024, per=1, N=2**24, K=8, ldx=9, w_sn=8, w_se=0, ldo=2**24),
+    # very many rows
+    dict(dt=F32, E=1, R=2**30, S=2**30, per=1, N=16, K=8, ldx=8, w_sn=8, w_se=0, ldo=16),
+])
+def test_grids_of_more_threads_than_32_bits_count(kw):
+    """Such a launch runs as many as the low 32 bits say, and reports nothing."""
+    assert mm(**kw) == UNSUP
+
+
+def test_gradient_grids_of_more_threads_than_32_bits_count():
+    assert wgrad(dt=F32, E=1024, N=2**14, K=2**13, ldy=2**14, ldx=2**13, ldw=2**13,
+                 w_se=2**27) == UNSUP
