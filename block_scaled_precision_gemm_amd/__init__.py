@@ -122,7 +122,8 @@ def load():
     L.bsmm_expert_wgrad_workspace_bytes.restype = sz
     L.bsmm_expert_mm_plan_name.argtypes = [st, st, st, i64, i64, i64, i64, sz, vp]
     L.bsmm_expert_mm_plan_name.restype = ctypes.c_char_p
-    L.bsmm_expert_wgrad_plan_name.argtypes = [st, st, st, st, i64, i64, i64, i64, i64, sz, vp]
+    L.bsmm_expert_wgrad_plan_name.argtypes = [st, st, st, st, st, i64, i64, i64, i64, i64, sz,
+                                              vp]
     L.bsmm_expert_wgrad_plan_name.restype = ctypes.c_char_p
     L.bsmm_quant_int8_mx.argtypes = [vp, i64, st, vp, i64, vp, i64, vp, i64, i64, i64, vp]
     L.bsmm_swiglu.argtypes = [vp, i64, st, vp, i64, vp, i64, vp, i64, i64, i64, vp]
@@ -1521,16 +1522,18 @@ def bsmm_expert_mm_plan_name(dtype, transposed, E, S, N, K, *, aligned=True, wor
 
 
 def bsmm_expert_wgrad_plan_name(dtype, checkpoint, E, Rx, S, N, K, *, out_dtype="f32",
-                                aligned=True, workspace=None):
+                                dy_aligned=True, x_aligned=True, workspace=None):
     """The kernel of a bsmm_expert_wgrad call and its parts of the slots:
-    (wide256, tile128, tile64 or restored, parts), as bsmm_expert_mm_plan_name."""
-    code, odt, parts = _float_code(dtype, "dtype"), _float_code(out_dtype, "out_dtype"), \
-        ctypes.c_int(0)
+    (wide256, tile128, tile64 or restored, parts), as bsmm_expert_mm_plan_name.
+    dy_aligned, x_aligned: whether row strides are multiples of 4 elements (a
+    checkpoint's: rows at multiples of 8 bytes)."""
+    code, parts = _float_code(dtype, "dtype"), ctypes.c_int(0)
     c = 1 if checkpoint else 0
     if workspace is None:
         workspace = load().bsmm_expert_wgrad_workspace_bytes(code, c, E, Rx, S, N, K)
-    name = load().bsmm_expert_wgrad_plan_name(code, c, odt, 1 if aligned else 0, E, Rx, S, N, K,
-                                              workspace, ctypes.byref(parts))
+    name = load().bsmm_expert_wgrad_plan_name(
+        code, c, _float_code(out_dtype, "out_dtype"), 1 if dy_aligned else 0,
+        1 if x_aligned else 0, E, Rx, S, N, K, workspace, ctypes.byref(parts))
     return name and (name.decode(), parts.value)
 
 

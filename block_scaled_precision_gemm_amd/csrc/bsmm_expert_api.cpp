@@ -227,15 +227,16 @@ bool mm_sizes(bsmm_dtype dtype, int transposed, bool rows, int64_t E, int64_t S,
   a.E = (int)E; a.S = (int)S; a.N = (int)N; a.K = (int)K;
   return true;
 }
-bool wgrad_sizes(bsmm_dtype dtype, int checkpoint, bool rows, int64_t E, int64_t Rx, int64_t S,
-                 int64_t N, int64_t K, WgradArgs& a) {
+bool wgrad_sizes(bsmm_dtype dtype, int checkpoint, bool dy_rows, bool x_rows, int64_t E,
+                 int64_t Rx, int64_t S, int64_t N, int64_t K, WgradArgs& a) {
   if (!float_dtype(dtype) || E <= 0 || Rx <= 0 || S <= 0 || N <= 0 || K <= 0 || E > kMaxExperts ||
       Rx >= kMaxDim || S >= kMaxSize || N >= kMaxSize || K >= kMaxSize)
     return false;
   a = WgradArgs{};
   a.dtype = dtype;
   a.x_scale = checkpoint ? &kSome : nullptr;
-  a.ldy = rows ? 0 : 1;
+  a.ldy = dy_rows ? 0 : 1;
+  a.ldx = x_rows ? 0 : 1;
   a.E = (int)E; a.Rx = (int)Rx; a.S = (int)S; a.N = (int)N; a.K = (int)K;
   return true;
 }
@@ -331,7 +332,7 @@ size_t bsmm_expert_wgrad_workspace_bytes(bsmm_dtype dtype, int checkpoint, int64
   size_t need = 0;
   WgradArgs a;
   for (int rows = 0; rows < 2; ++rows) {
-    if (!wgrad_sizes(dtype, 0, rows, E, Rx, S, N, K, a)) return 0;
+    if (!wgrad_sizes(dtype, 0, rows, true, E, Rx, S, N, K, a)) return 0;
     // codes as they are or restored, fp32 or bf16 output
     for (int codes = 0; codes <= (checkpoint != 0); ++codes)
       for (int bf = 0; bf < 2; ++bf) {
@@ -344,14 +345,15 @@ size_t bsmm_expert_wgrad_workspace_bytes(bsmm_dtype dtype, int checkpoint, int64
 }
 
 const char* bsmm_expert_wgrad_plan_name(bsmm_dtype dtype, int checkpoint, bsmm_dtype out_dtype,
-                                        int aligned, int64_t E, int64_t Rx, int64_t S, int64_t N,
-                                        int64_t K, size_t workspace_bytes, int* parts) {
+                                        int dy_aligned, int x_aligned, int64_t E, int64_t Rx,
+                                        int64_t S, int64_t N, int64_t K, size_t workspace_bytes,
+                                        int* parts) {
   WgradArgs a;
   if (!float_dtype(out_dtype) || (checkpoint && K % 32 != 0) ||
-      !wgrad_sizes(dtype, checkpoint, aligned != 0, E, Rx, S, N, K, a))
+      !wgrad_sizes(dtype, checkpoint, dy_aligned != 0, x_aligned != 0, E, Rx, S, N, K, a))
     return nullptr;
   a.out_dtype = out_dtype;
-  const WgradChoice w = wgrad_choice(a, aligned != 0, workspace_bytes);
+  const WgradChoice w = wgrad_choice(a, x_aligned != 0, workspace_bytes);
   if (parts != nullptr) *parts = w.c.splits;
   if (w.restored) return "restored";
   return w.c.plan == ExpertPlan::Wide ? "wide256"

@@ -582,10 +582,13 @@ size_t bsmm_expert_wgrad_workspace_bytes(bsmm_dtype dtype, int checkpoint, int64
  * The kernel that a call takes, as bsmm_expert_mm_plan_name: "wide256" (bf16),
  * "tile128", "tile64", or "restored" (a checkpoint's values in the workspace
  * first, then as wide256); *parts gets the parts of an expert's slots.
+ * dy_aligned and x_aligned: row strides that are multiples of 4 elements, or a
+ * checkpoint's codes in rows at multiples of 8 bytes.
  */
 const char* bsmm_expert_wgrad_plan_name(bsmm_dtype dtype, int checkpoint, bsmm_dtype out_dtype,
-                                        int aligned, int64_t E, int64_t Rx, int64_t S, int64_t N,
-                                        int64_t K, size_t workspace_bytes, int* parts);
+                                        int dy_aligned, int x_aligned, int64_t E, int64_t Rx,
+                                        int64_t S, int64_t N, int64_t K, size_t workspace_bytes,
+                                        int* parts);
 bsmm_status bsmm_expert_wgrad(const void* dy, int64_t ldy, bsmm_dtype dtype, int dy_slots_per_row,
                               const void* x, int64_t ldx, int x_slots_per_row,
                               const uint8_t* x_scale, int64_t s_r, const int32_t* order,

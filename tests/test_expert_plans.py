@@ -36,7 +36,7 @@ def test_weight_gradient():
     assert wgrad("bf16", False, 32, 4096, 32768, 2048, 4096) == ("wide256", 1)
     assert wgrad("bf16", True, 32, 4096, 32768, 2048, 4096) == ("restored", 1)
     assert wgrad("bf16", True, 32, 4096, 32768, 2048, 4096, workspace=0) == ("tile128", 1)
-    assert wgrad("bf16", True, 32, 4096, 32768, 2048, 4096, aligned=False)[0] == "tile128"
+    assert wgrad("bf16", True, 32, 4096, 32768, 2048, 4096, x_aligned=False)[0] == "tile128"
     assert wgrad("f32", True, 32, 4096, 32768, 2048, 4096)[0].startswith("tile")
     assert wgrad("f32", False, 6, 333, 666, 1001, 515) == ("tile64", 1)
     assert wgrad("bf16", False, 1, 9000, 9000, 64, 72)[1] > 1
@@ -104,9 +104,9 @@ def test_a_larger_workspace_changes_no_gradient(checkpoint, dt):
         Rx = max(1, S // 4) if second else S
         need = bsmm.bsmm_expert_wgrad_workspace_bytes(dt, checkpoint, E, Rx, S, N, K)
         for odt in ("bf16", "f32"):
-            for rows in (True, False):
-                same = {wgrad(dt, checkpoint, E, Rx, S, N, K, out_dtype=odt, aligned=rows,
-                              workspace=room)
+            for rows in ((True, True), (True, False), (False, True), (False, False)):
+                same = {wgrad(dt, checkpoint, E, Rx, S, N, K, out_dtype=odt, workspace=room,
+                              dy_aligned=rows[0], x_aligned=rows[1])
                         for room in (None, 2**27 + 12345, 2**28, 2**40)
                         if room is None or room >= need}
                 assert len(same) == 1, (E, Rx, S, N, K, odt, rows, same)
