@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(256) swiglu_backward(SwigluBackArgs a) {
         const float rd = r * d[j];
         // silu' = sg (1 + g (1 - sg))
         const float slope = __builtin_fmaf(silu, sg.c, sg.s);
-        g[j] = rd * u[j] * slope;
+        g[j] = rd * (u[j] * slope);              // the slope is at most 1.1
         u[j] = rd * silu;
         d[j] = r * act;
       }

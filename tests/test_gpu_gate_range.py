@@ -71,6 +71,28 @@ def test_gradient(top, weighted, dt):
         within(drow, er, "f32", (REL + F * 2.0**-24) * total, 2.0**-141 * np.abs(d * u).sum(1))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_gradient_of_large_ups(dt):
+    """da * u leaves fp32 where the slope brings their product back into it."""
+    F, rng = 64, np.random.default_rng(6)
+    low = [g for g in GATES if g <= -60]
+    g = np.repeat(np.array(low)[:, None], F, 1)
+    u = np.where(rng.random(g.shape) < 0.5, -1, 1) * 2.0**120
+    q, s = bsmm.bsmm_quant_int8_mx(dev(np.concatenate([g, u], 1).astype(np.float32), TDT[dt]))
+    h = X.restore(host(q), host(s))
+    d = rng.uniform(2.0**11, 2.0**12, u.shape).astype(np.float32)
+    da, r = dev(d, TDT[dt]), np.full(len(low), 2.0, np.float32)
+    dh, act, drow = bsmm.bsmm_swiglu_backward(da, q, s, row_scale=dev(r))
+    eh, ea, er = X.swiglu_backward(host(da), h, r)
+    g, u, d = h[:, :F], h[:, F:], 2 * host(da)
+    terms = X.sigmoid(g) * (1 + np.abs(g) * X.sigmoid(-g))
+    within(dh, eh, dt, 2 * REL * np.concatenate([np.abs(d * u) * terms, np.abs(eh[:, F:])], 1),
+           2.0**-141 * np.concatenate([np.abs(d * u), np.abs(d)], 1))
+    within(act, ea, dt, REL * np.abs(ea), 2.0**-140 * np.abs(u))
+    total = np.abs(host(da) * X.swiglu(h)).sum(1)
+    within(drow, er, "f32", (REL + F * 2.0**-24) * total, 2.0**-141 * np.abs(d * u).sum(1))
+
+
 def test_masked_gate():
     """A gate at the type's lowest value passes nothing on, in either direction."""
     h = torch.full((3, 128), 2.0, device="cuda:0", dtype=torch.bfloat16)
