@@ -315,7 +315,8 @@ bsmm_status bsmm_expert_mm(const void* x, int64_t ldx, const void* w, int64_t w_
   }
   a.x = x; a.ldx = ldx; a.dtype = dtype;
   a.w = w; a.w_se = w_se;
-  a.order = order; a.offsets = offsets; a.row_scale = row_scale;
+  a.order = order; a.offsets = offsets;
+  a.row_scale = K > 0 ? row_scale : nullptr;       // zeros, whatever the scale
   a.x_div = slots_per_row;
   a.out = out; a.ldo = ldo; a.out_dtype = out_dtype;
   a.E = (int)E; a.R = (int)R; a.S = (int)S; a.N = (int)N; a.K = (int)K;

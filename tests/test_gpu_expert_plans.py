@@ -280,3 +280,17 @@ def test_the_same_bits_whatever_the_workspace_holds():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(static, first)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("back", [False, True])
+def test_no_columns_give_zeros_whatever_the_scale(back, dt):
+    scale = torch.tensor([1.0, float("inf"), float("nan"), -1.0, float("-inf"), 0.0], device=DEV)
+    x = torch.empty(6, 0, device=DEV, dtype=TDT[dt])
+    w = torch.empty(2, 0, 40, device=DEV, dtype=TDT[dt]).transpose(1, 2) if back else \
+        torch.empty(2, 40, 0, device=DEV, dtype=TDT[dt])
+    for odt in ("f32", "bf16"):
+        out = torch.full((6, 40), float("nan"), device=DEV, dtype=TDT[odt])
+        bsmm.bsmm_expert_mm(x, w, None, dev(np.array([0, 3, 5], np.int32)), row_scale=scale,
+                            out_dtype=odt, out=out)
+        assert not host(out).any()
