@@ -493,12 +493,19 @@ void launch_tiles(const QuantArgs& a, hipStream_t st) {
                      a.s_kb, (int)a.K, static_cast<float*>(a.scale2), a.s2_m, a.s2_kb);
 }
 
+// At most 2^23 rows a launch, which counts its threads in 32 bits: one of more
+// runs as many as the low 32 bits say, without an error.
 template <typename T, int WPR, int NV>
 void launch_rows(const QuantArgs& a, hipStream_t st) {
-  const unsigned grid = (unsigned)(WPR == 1 ? (a.M + 3) / 4 : a.M);
-  hipLaunchKernelGGL((quant_int8_rows<T, WPR, NV>), dim3(grid), dim3(256), 0, st,
-                     static_cast<const T*>(a.x), a.ldx, static_cast<int8_t*>(a.q), a.ldq,
-                     static_cast<float*>(a.scale), a.s_m, (int)a.M, (int)a.K);
+  constexpr int64_t kRows = (int64_t)1 << 23;
+  for (int64_t m = 0; m < a.M; m += kRows) {
+    const int64_t rows = a.M - m < kRows ? a.M - m : kRows;
+    const unsigned grid = (unsigned)(WPR == 1 ? (rows + 3) / 4 : rows);
+    hipLaunchKernelGGL((quant_int8_rows<T, WPR, NV>), dim3(grid), dim3(256), 0, st,
+                       static_cast<const T*>(a.x) + m * a.ldx, a.ldx,
+                       static_cast<int8_t*>(a.q) + m * a.ldq, a.ldq,
+                       static_cast<float*>(a.scale) + m * a.s_m, a.s_m, (int)rows, (int)a.K);
+  }
 }
 
 // Short rows: a wave per row.  Longer rows: a workgroup per row, so each
