@@ -58,6 +58,11 @@ bsmm_status run(const W4Args& a, void* workspace, size_t workspace_bytes, void* 
   if (a.x_dtype == BSMM_F32 &&
       (workspace == nullptr || workspace_bytes < w4_plane_bytes(a) || !aligned(workspace, 16)))
     plan = W4Plan::Rows;
+  // A launch counts its threads in 32 bits.  Rows: 4 lanes a column (more where
+  // there are few); tiles: 256 threads to 128 x 128, or 512 to 256 x 128.
+  const int64_t tiles = ((int64_t)a.S / 128 + a.E + 1) * ((int64_t)a.N / 128 + 1);
+  CHECK(plan == W4Plan::Rows ? a.N < (1 << 30) - 128 : tiles < (1 << 24), BSMM_ERR_UNSUPPORTED,
+        "rows * N beyond the largest grid");
   if (launch_w4(a, plan, workspace, stream) != 0) return fail(BSMM_ERR_HIP, "kernel launch failed (w4)");
   return BSMM_OK;
 }

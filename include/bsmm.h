@@ -472,6 +472,8 @@ bsmm_status bsmm_quant_w4(const void* w, int64_t ldw, bsmm_dtype w_dtype, uint8_
  * M for bsmm_w4_mm).  With less the call runs without it, slower.  So does a
  * call whose x (M * ldx elements of bf16, or three bf16 parts of M * K fp32
  * ones) reaches 4 GiB, at about half the speed: cut it by rows.
+ * A call of 2^32 threads is refused (N from 2^30 - 128 on, or 2^24 tiles of 128
+ * x 128).
  */
 size_t bsmm_w4_workspace_bytes(bsmm_dtype x_dtype, int64_t E, int64_t R, int64_t S, int64_t N,
                                int64_t K, int group);
