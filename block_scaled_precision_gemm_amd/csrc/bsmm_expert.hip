@@ -113,7 +113,8 @@ typedef __attribute__((address_space(3))) i16x4* lds_i16x4_t;
 // the lane gets its column
 __device__ __forceinline__ uint2 read_transposed(const uint8_t* p) {
   return __builtin_bit_cast(
-      uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(uintptr_t)(uint32_t)(uintptr_t)p));
+      uint2,
+      __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t)(uintptr_t)(uint32_t)(uintptr_t)p));
 }
 template <typename T, int MB>
 __device__ __forceinline__ u32x4 frag_across(const uint8_t* tile, int c0, int t) {
@@ -128,7 +129,8 @@ __device__ __forceinline__ u32x4 frag_across(const uint8_t* tile, int c0, int t)
     u32x4 v;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      v[i] = *reinterpret_cast<const uint32_t*>(tile + across_off<T, MB>(k + i, c >> 2) + (c & 3) * 4);
+      v[i] = *reinterpret_cast<const uint32_t*>(tile + across_off<T, MB>(k + i, c >> 2) +
+                                                (c & 3) * 4);
     return v;
   }
 }
@@ -304,20 +306,20 @@ __global__ void __launch_bounds__(256) reduce_parts(const float* __restrict__ pa
 }
 
 // ---------------------------------------------------------------------------
-// Any type, alignment and size: tiles of 64 MB x 64 MB (four waves of 32 MB x
-// 32 MB), both operands through registers into two slots of LDS, in the layout
-// they have in memory; bf16 that lies across is transposed by the LDS read.
-// fp32 runs at the fp32 matrix instruction's rate, a sixteenth of bf16's, which
-// bounds it where there are enough tiles (900 tokens x 4 of 16 experts of 1024
-// x 2048: 165 us, 92 of the 151 TFLOP/s of a large product).  Tiles of 128 are
-// for gradients of many of them; few tiles are bound by latency (333 x 2 of 6
-// of 1001 x 515: 22 us in tiles of 64, its weight gradient 17).
+// Any type, alignment and size: tiles of 64 x 64 (four waves of 32 x 32; 128 x
+// 128 and 64 x 64 in gradients of many tiles, MB = 2), both operands through
+// registers into two slots of LDS, in the layout they have in memory; bf16 that
+// lies across is transposed by the LDS read.  fp32 runs at the fp32 matrix
+// instruction's rate, a sixteenth of bf16's, which bounds it where there are
+// enough tiles (900 tokens x 4 of 16 experts of 1024 x 2048: 165 us, 92 of the
+// 151 TFLOP/s of a large product).  Few tiles are bound by latency (333 x 2 of 6
+// of 1001 x 515: 22 us, its weight gradient 17).
 // ---------------------------------------------------------------------------
-template <typename T, int MB, bool W_ACROSS>
+template <typename T, bool W_ACROSS>
 __global__ void __launch_bounds__(256, 2) expert_mm_kernel(ExpertArgs a, int items, int ntn,
                                                            int splits, int run) {
-  constexpr int U = Elem<T>::U, STEP = Elem<T>::STEP, TILE = 64 * MB, BYTES = TILE * 128;
-  constexpr int UPR = TILE / U, NU = 2 * MB;          // units of an across row, of a thread
+  constexpr int U = Elem<T>::U, STEP = Elem<T>::STEP, TILE = 64, BYTES = TILE * 128;
+  constexpr int UPR = TILE / U, NU = 2;               // units of an across row, of a thread
   __shared__ __attribute__((aligned(1024))) uint8_t smem[4 * BYTES];
   __shared__ int slots[TILE];
   __shared__ float scales[TILE];
@@ -369,27 +371,21 @@ __global__ void __launch_bounds__(256, 2) expert_mm_kernel(ExpertArgs a, int ite
     for (int i = 0; i < NU; ++i) {
       const int q = i * 256 + threadIdx.x;
       *reinterpret_cast<u32x4*>(to + lds_off(q >> 3, q & 7)) = va[d][i];
-      *reinterpret_cast<u32x4*>(to + BYTES + (W_ACROSS ? across_off<T, MB>(q / UPR, q % UPR)
+      *reinterpret_cast<u32x4*>(to + BYTES + (W_ACROSS ? across_off<T, 1>(q / UPR, q % UPR)
                                                        : lds_off(q >> 3, q & 7))) = vb[d][i];
     }
   };
-  f32x16 acc[MB][MB] = {};
-  tile_products<T, MB, false, W_ACROSS>(smem, s1 - s0, acc, load, store);
+  f32x16 acc[1][1] = {};
+  tile_products<T, 1, false, W_ACROSS>(smem, s1 - s0, acc, load, store);
 
-  const int wave = threadIdx.x >> 6, wm = (wave >> 1) * 32 * MB;
-  const int col = n0 + (wave & 1) * 32 * MB + (threadIdx.x & 31);
+  const int wave = threadIdx.x >> 6, wm = (wave >> 1) * 32;
+  const int col = n0 + (wave & 1) * 32 + (threadIdx.x & 31);
+  if (col >= a.N) return;
 #pragma unroll
-  for (int i = 0; i < MB; ++i)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int m = wm + row_of(i, r), slot = slots[m];
-      if (slot < 0) continue;
-      const float f = scales[m];
-#pragma unroll
-      for (int j = 0; j < MB; ++j)
-        if (col + 32 * j < a.N)
-          put(a.out, a.out_dtype, slot * a.ldo + col + 32 * j, acc[i][j][r] * f);
-    }
+  for (int r = 0; r < 16; ++r) {
+    const int m = wm + row_of(0, r), slot = slots[m];
+    if (slot >= 0) put(a.out, a.out_dtype, slot * a.ldo + col, acc[0][0][r] * scales[m]);
+  }
 }
 
 // CODES: x is an 8-bit checkpoint.
@@ -473,12 +469,13 @@ __global__ void __launch_bounds__(256, 2) expert_wgrad_kernel(WgradArgs a, int n
 // Operands that lie in memory that way go global -> LDS directly, two or three
 // steps ahead: the slots take all 160 KB.  (Not with rows that are not 16-byte
 // aligned: 1000 tokens x 2 of 8 experts of 2048 x 2000 take 36 us, x 2001,
-// through registers, 46.)  The other kind goes through registers: a wave has 8 neighbouring elements of the contraction (rows in
-// memory) and a lane 4 columns, which it transposes with 16 byte permutations
-// and writes as 4 x 16 bytes, the loads a step ahead.  (The transposing LDS
-// read would spare that, but the compiler waits for every direct load in flight
-// before one, and before an LDS write, so that a tile that needs one takes the
-// other operand through registers too.)
+// through registers, 46.)  The other kind goes through registers: a wave has 8
+// neighbouring elements of the contraction (rows in memory) and a lane 4
+// columns, which it transposes with 16 byte permutations and writes as 4 x 16
+// bytes, the loads a step ahead.  (The transposing LDS read would spare that,
+// but the compiler waits for every direct load in flight before one, and before
+// an LDS write, so that a tile that needs one takes the other operand through
+// registers too.)
 //
 // The source order is the schedule: a turn's fragments are read during the
 // turn before, and the barrier stands before the last turn, whose products
@@ -685,8 +682,9 @@ __device__ __forceinline__ void wide_products(uint8_t* smem, int steps, f32x16 (
 // A wave's 32 MI x 64 results to memory, a block of 32 rows at a time through
 // LDS, so that a store covers whole runs of a row.  row(m): the address of
 // column 0 of the wave's row m (null: not stored), scale(m) its factor; cols:
-// the columns from there to the end.  The stores pass the caches by: they would push out what the next tiles read
-// (4096 tokens x 8 of 32 experts, fp32 gradients of 2048 x 4096: 810 -> 767 us).
+// the columns from there to the end.  The stores pass the caches by: they would
+// push out what the next tiles read (4096 tokens x 8 of 32 experts, fp32
+// gradients of 2048 x 4096: 810 -> 767 us).
 template <int MI, typename Row, typename Scale>
 __device__ __forceinline__ void wide_store(uint8_t* smem, const f32x16 (&acc)[MI][2],
                                            bsmm_dtype dt, int cols, const Row& row,
@@ -936,7 +934,8 @@ __global__ void __launch_bounds__(512, 2) expert_wgrad_wide(WgradArgs a, int ntn
   ops.x += (int64_t)ops.cx.first * 2;
   ops.mine = ops.slot_of(0);
   f32x16 acc[4][2] = {};
-  wide_products<4, false, true, true, 16, 8>(smem, (int)(((unsigned)(hi - lo) + 63) / 64), acc, ops);
+  wide_products<4, false, true, true, 16, 8>(smem, (int)(((unsigned)(hi - lo) + 63) / 64), acc,
+                                             ops);
   barrier();                            // nobody reads the tiles any more
   const int row0 = n0 + (wave >> 2) * 128, col = k0 + (wave & 3) * 64;
   const int size = a.out_dtype == BSMM_BF16 ? 2 : 4;
@@ -951,9 +950,9 @@ __global__ void __launch_bounds__(512, 2) expert_wgrad_wide(WgradArgs a, int ntn
 
 // ---------------------------------------------------------------------------
 // Few rows: items of 16 or, along, 32 rows by 64 columns, 16 x 16 instructions
-// with the weight as the first operand.  The eight waves of a workgroup share out cn =
-// 8 / ks column groups and ks ranges of the contraction; partial sums are
-// added through LDS in order.
+// with the weight as the first operand.  The eight waves of a workgroup share
+// out cn = 8 / ks column groups and ks ranges of the contraction; partial sums
+// are added through LDS in order.
 //
 // Everything goes straight to registers, kDepth chunks of 64 bytes (32 bf16 or
 // 16 fp32 of the contraction) ahead: no barrier, each weight byte is used by
@@ -961,9 +960,10 @@ __global__ void __launch_bounds__(512, 2) expert_wgrad_wide(WgradArgs a, int ntn
 // 4096 bf16, 134 MB: 33 us, 4.1 TB/s; 33 x 4 of 16 of 4099 x 1024 fp32, 268 MB:
 // 76 us, 3.5 TB/s, a few workgroups in a second round).  Items of 32 rows have
 // three chunks ahead, for their registers (64 x 4 of 16 of 4096 x 1024 fp32: 90
-// us in items of 16, 78 of 32); across, they spill.  Along, a lane's 16 bytes are one column's.  Across, a lane has 4
-// neighbouring columns: of bf16 8 rows, transposed by byte permutations, of
-// fp32 4 rows, each lane's 4 values then belonging to 4 column blocks.
+// us in items of 16, 78 of 32); across, they spill.  Along, a lane's 16 bytes
+// are one column's.  Across, a lane has 4 neighbouring columns: of bf16 8 rows,
+// transposed by byte permutations, of fp32 4 rows, each lane's 4 values then
+// belonging to 4 column blocks.
 // ---------------------------------------------------------------------------
 constexpr int kRowsWaves = 8;
 
@@ -1098,10 +1098,10 @@ __device__ __forceinline__ void expert_rows_item(const ExpertArgs& a, const Item
 }
 
 template <typename T, bool W_ACROSS>
-__global__ void __launch_bounds__(kRowsWaves * 64, 4) expert_mm_rows(ExpertArgs a, int item0,
-                                                                     int bm, int log_ks) {
+__global__ void __launch_bounds__(kRowsWaves * 64, 4) expert_mm_rows(ExpertArgs a, int bm,
+                                                                     int log_ks) {
   __shared__ __attribute__((aligned(16))) float part[kRowsWaves][16][68];
-  const int item = item0 + blockIdx.y, cols = (kRowsWaves >> log_ks) * 64;
+  const int item = blockIdx.y, cols = (kRowsWaves >> log_ks) * 64;
   const Item it = find_item(a.offsets, a.E, a.S, bm, item);
   zero_rows(a, blockIdx.x * cols, cols, item, gridDim.y);
   if (it.rows == 0) return;
@@ -1151,12 +1151,9 @@ struct RowsGrid {
 
 template <typename T, bool W_ACROSS>
 void launch_rows(const ExpertArgs& a, hipStream_t st) {
-  const RowsGrid g(a);
-  for (int64_t i = 0; i < g.items; i += 65535)      // at most so many items a launch
-    hipLaunchKernelGGL((expert_mm_rows<T, W_ACROSS>),
-                       dim3((unsigned)g.ntn,
-                            (unsigned)(g.items - i < 65535 ? g.items - i : 65535)),
-                       dim3(kRowsWaves * 64), 0, st, a, (int)i, g.bm, g.log_ks);
+  const RowsGrid g(a);                              // some thousand items at most
+  hipLaunchKernelGGL((expert_mm_rows<T, W_ACROSS>), dim3((unsigned)g.ntn, (unsigned)g.items),
+                     dim3(kRowsWaves * 64), 0, st, a, g.bm, g.log_ks);
 }
 
 void launch_reduce(const float* parts, int splits, void* out, bsmm_dtype dt, int64_t rows,
@@ -1250,7 +1247,7 @@ void launch_mm(ExpertArgs a, ExpertPlan plan, int rows, int splits, void* ws, hi
                            g.items, g.ntn, splits, g.deal.run);
     }
   } else {
-    hipLaunchKernelGGL((expert_mm_kernel<T, 1, W_ACROSS>), grid, block, 0, st, a, g.items, g.ntn,
+    hipLaunchKernelGGL((expert_mm_kernel<T, W_ACROSS>), grid, block, 0, st, a, g.items, g.ntn,
                        splits, g.deal.run);
   }
   if (splits > 1)

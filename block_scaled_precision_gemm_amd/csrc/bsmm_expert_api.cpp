@@ -51,8 +51,10 @@ Choice best_split(ExpertPlan plan, int64_t tiles, int64_t steps, double outs, do
 // third of them each with 0.6, 1 and 1.4 of the average.  A step of 64, 128,
 // 192 or 256 rows takes 0.62, 0.95, 1.25 or 1.55 us, a tile 6 besides; CUs take
 // tiles as they get free, so that all end within a fifth of a tile of each
-// other.  (Of 33 shapes' best heights of item this finds those that cost 1.6 %
-// more than the best on average, and 18 % at most.)
+// other.  The constants are fitted to the times of 33 shapes, in full grids with
+// the experts' weights from HBM; a step and a tile by themselves take what the
+// kernel's comment says.  (Of those shapes' best heights of item the model finds
+// heights that cost 1.6 % more on average, and 18 % at most.)
 double wide_us(const ExpertArgs& a, int64_t act, int bm, int64_t steps, int parts) {
   static const double kStep[4] = {0.62, 0.95, 1.25, 1.55};
   static const double kLoad[3] = {0.6, 1.0, 1.4};
@@ -75,7 +77,8 @@ double wide_us(const ExpertArgs& a, int64_t act, int bm, int64_t steps, int part
 
 // Measured (us; the average is of rows to an expert):
 //                                            Rows  Wide  Tiles64
-//   1 token x 8 of 64, 2048 x 4096 bf16        33    32           (64 tiles of 256)
+//   1 token x 8 of 64, 2048 x 4096 bf16        33    32           (64 tiles of 256;
+//     Wide in four ranges, with a workspace and a second launch, for 3 %)
 //   64 x 2 of 8, 1024 x 2048 bf16              14    17           (32)
 //   32 x 2 of 8, 4096 x 8192 bf16             117   122           (128)
 //   16 x 4 of 16, 4096 x 4096 bf16            111   105           (256)
@@ -320,7 +323,8 @@ bsmm_status bsmm_expert_mm(const void* x, int64_t ldx, const void* w, int64_t w_
   a.x_div = slots_per_row;
   a.out = out; a.ldo = ldo; a.out_dtype = out_dtype;
   a.E = (int)E; a.R = (int)R; a.S = (int)S; a.N = (int)N; a.K = (int)K;
-  const Choice c = mm_choice(a, workspace != nullptr && aligned(workspace, 16) ? workspace_bytes : 0);
+  const Choice c =
+      mm_choice(a, workspace != nullptr && aligned(workspace, 16) ? workspace_bytes : 0);
   CHECK(expert_mm_threads(a, c.plan, c.rows, c.splits) < kMaxThreads, BSMM_ERR_UNSUPPORTED,
         "S * N beyond the largest grid");
   if (launch_expert_mm(a, c.plan, c.rows, c.splits, workspace, stream) != 0)

@@ -122,13 +122,13 @@ __device__ __forceinline__ void barrier() {
 }
 
 // Logical workgroup ids: contiguous runs per XCD (hardware ids go round robin
-// over 8), then groups of `group` row blocks by all column blocks, so that the
+// over 8), then groups of 8 row blocks by all column blocks, so that the
 // workgroups an XCD holds at a time share x rows and weight columns in its L2.
-__device__ __forceinline__ void tile_of(int items, int ntn, int& item, int& tn, int group = 8) {
+__device__ __forceinline__ void tile_of(int items, int ntn, int& item, int& tn) {
   const int total = gridDim.x, hw = blockIdx.x;
   const int per = total >> 3, rem = total & 7, xcd = hw & 7, local = hw >> 3;
   const int id = xcd < rem ? xcd * (per + 1) + local : rem * (per + 1) + (xcd - rem) * per + local;
-  const int width = group * ntn, g = id / width, first = group * g, n = min(items - first, group);
+  const int width = 8 * ntn, g = id / width, first = 8 * g, n = min(items - first, 8);
   const int in = id - g * width;
   item = first + in % n;
   tn = in / n;

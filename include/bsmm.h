@@ -465,15 +465,14 @@ bsmm_status bsmm_quant_w4(const void* w, int64_t ldw, bsmm_dtype w_dtype, uint8_
  * strides 16-byte aligned (ldx a multiple of 8 elements), out 4-byte aligned.
  * |x| up to 2^100: NaN, infinities and larger values are unsupported.  fp32
  * activations are used in full precision, and every product is exact: the
- * error is that of the fp32 sums of the (code - zero) * x.  M == 0 or N == 0 does nothing, K
- * == 0 writes zeros.  The workspace (16-byte aligned) holds fp32 activations
- * cut into bf16 parts where many rows make that worth it:
- * bsmm_w4_workspace_bytes gives the bytes (0: none wanted; E = 1 and S = R =
- * M for bsmm_w4_mm).  With less the call runs without it, slower.  So does a
+ * error is that of the fp32 sums of the (code - zero) * x.  M == 0 or N == 0
+ * does nothing, K == 0 writes zeros.  The workspace (16-byte aligned) holds
+ * fp32 activations cut into bf16 parts where many rows make that worth it:
+ * bsmm_w4_workspace_bytes gives the bytes (0: none wanted; E = 1 and S = R = M
+ * for bsmm_w4_mm).  With less the call runs without it, slower.  So does a
  * call whose x (M * ldx elements of bf16, or three bf16 parts of M * K fp32
- * ones) reaches 4 GiB, at about half the speed: cut it by rows.
- * A call of 2^32 threads is refused (N from 2^30 - 128 on, or 2^24 tiles of 128
- * x 128).
+ * ones) reaches 4 GiB, at about half the speed: cut it by rows.  A call of 2^32
+ * threads is refused (N from 2^30 - 128 on, or 2^24 tiles of 128 x 128).
  */
 size_t bsmm_w4_workspace_bytes(bsmm_dtype x_dtype, int64_t E, int64_t R, int64_t S, int64_t N,
                                int64_t K, int group);
@@ -531,11 +530,11 @@ bsmm_status bsmm_w4_expert_mm(const void* x, int64_t ldx, bsmm_dtype x_dtype, co
  * order.  Any N and K; pointers aligned to their types (16-byte aligned rows
  * are faster).  E <= 1024; S, N and K < 2^31 - 1024.  A call of so many tiles
  * (64 x 64 at least, partly empty ones among them) that they need 2^32 threads
- * is refused.  S == 0 or N == 0 does nothing, K == 0 writes zeros.  The workspace (16-byte aligned) holds fp32 sums over ranges of K
- * where a call has too few tiles to fill the chip:
- * bsmm_expert_mm_workspace_bytes gives the bytes (0: none wanted; transposed:
- * w_sn is 1).  With more than that nothing changes; with less the call runs
- * with fewer ranges.
+ * is refused.  S == 0 or N == 0 does nothing, K == 0 writes zeros.  The
+ * workspace (16-byte aligned) holds fp32 sums over ranges of K where a call
+ * has too few tiles to fill the chip: bsmm_expert_mm_workspace_bytes gives the
+ * bytes (0: none wanted; transposed: w_sn is 1).  With more than that nothing
+ * changes; with less the call runs with fewer ranges.
  */
 size_t bsmm_expert_mm_workspace_bytes(bsmm_dtype dtype, int transposed, int64_t E, int64_t S,
                                       int64_t N, int64_t K);
@@ -565,18 +564,17 @@ bsmm_status bsmm_expert_mm(const void* x, int64_t ldx, const void* w, int64_t w_
  *        int8 codes of bsmm_quant_int8_mx, (r, k)'s byte at x_scale[r*s_r +
  *        k/32] (K % 32 == 0)
  *   dw   (e, n, k) at dw[e*w_se + n*ldw + k], fp32 or bf16 (RNE)
- * An expert without slots gets zeros.  order NULL: slot i at position i (E =
- * 1 and offsets {0, S}: a dense layer's gradient).  Offsets that do not rise
- * and slots outside [0, S) give undefined sums, but no access outside the
- * operands.  S <= Ry *
- * dy_slots_per_row and S <= Rx * x_slots_per_row.  Sums, sizes, alignment and
- * workspace as for bsmm_expert_mm (a checkpoint: rows of codes at multiples
- * of 8 bytes are faster).  E, N or K 0 does nothing; S == 0 writes zeros.
- * The workspace (16-byte aligned) holds a checkpoint's values in bf16, and
- * fp32 sums over parts of the slots where dw has too few tiles to fill the
- * chip: bsmm_expert_wgrad_workspace_bytes gives the bytes (0: none wanted).
- * With more than that nothing changes; with less the call runs with fewer
- * parts or without, slower.
+ * An expert without slots gets zeros.  order NULL: slot i at position i (E = 1
+ * and offsets {0, S}: a dense layer's gradient).  Offsets that do not rise and
+ * slots outside [0, S) give undefined sums, but no access outside the
+ * operands.  S <= Ry * dy_slots_per_row and S <= Rx * x_slots_per_row.  Sums,
+ * sizes, alignment and workspace as for bsmm_expert_mm (a checkpoint: rows of
+ * codes at multiples of 8 bytes are faster).  E, N or K 0 does nothing; S == 0
+ * writes zeros.  The workspace (16-byte aligned) holds a checkpoint's values in
+ * bf16, and fp32 sums over parts of the slots where dw has too few tiles to
+ * fill the chip: bsmm_expert_wgrad_workspace_bytes gives the bytes (0: none
+ * wanted).  With more than that nothing changes; with less the call runs with
+ * fewer parts or without, slower.
  */
 size_t bsmm_expert_wgrad_workspace_bytes(bsmm_dtype dtype, int checkpoint, int64_t E, int64_t Rx,
                                          int64_t S, int64_t N, int64_t K);

@@ -22,7 +22,8 @@ pytestmark = pytest.mark.gpu
 TOP = 127 * 2.0**121                     # the largest value of a checkpoint
 GATES = [-TOP, -1e38, -1e30, -1e9, -1000.0, -200.0, -150.0, -120.0, -104.5, -103.0, -100.0, -95.0,
          -92.0, -90.0, -89.0, -88.5, -88.0, -87.5, -87.0, -60.0, -17.0, -1.0, -1e-20, -1e-39, 0.0,
-         1e-39, 1e-20, 1.0, 17.0, 87.0, 88.5, 90.0, 104.5, 1000.0, 1e9, 1e18]   # times 2^60 in fp32 too
+         1e-39, 1e-20, 1.0, 17.0, 87.0, 88.5, 90.0, 104.5, 1000.0, 1e9,
+         1e18]                           # times 2^60 in fp32 too
 
 
 @pytest.fixture(autouse=True)
