@@ -2385,10 +2385,19 @@ int launch_sk(const Problem& p, const Launch& l) {
 // Entry used by the variant table: one kernel configuration for one
 // (operation, output type).  Instantiated below for the pair this
 // translation unit is compiled for.
-// Skinny launch (M <= 16): one workgroup per 16 columns of each batch.
+// Skinny launch (M <= 16): one workgroup per 16 columns of each batch.  Of 2^24
+// and more the runtime, which counts a launch's threads in 32 bits, would run
+// the rest of the division and report nothing: the tile kernel takes those.
+constexpr int64_t kMaxBlocks = (((int64_t)1 << 32) - 1) / 256;
 template <int OP, int OUT, int SPF>
 int launch_skinny(const Problem& p, const Launch& l) {
   if (p.M > 16 || l.row_begin != 0 || l.row_end != p.M) return 1;
+  const int64_t grid = ((int64_t)p.N + 15) / 16 * p.G;
+  if (grid > kMaxBlocks) {
+    Launch l2 = l;
+    l2.psa = nullptr;
+    return launch_tile<OP, OUT, 2, 1, 5, false>(p, l2);
+  }
   KArgs k;
   k.p = p;
   k.row_begin = 0;
@@ -2407,7 +2416,6 @@ int launch_skinny(const Problem& p, const Launch& l) {
     hipLaunchKernelGGL((zero_out<OP, OUT>), dim3(1024), dim3(256), 0, s, k);
     return check_launch();
   }
-  const int64_t grid = (int64_t)k.tiles_n * p.G;
   hipLaunchKernelGGL((skinny_kernel<OP, OUT, SPF>), dim3((unsigned)grid), dim3(256), 0, s, k);
   return check_launch();
 }
@@ -2426,7 +2434,8 @@ int launch_narrow(const Problem& p, const Launch& l) {
   // ranges of ceil(KB / S) blocks; as many as that leaves non-empty
   const int nk_max = KB > 0 ? (KB + S - 1) / S : 0;
   if (nk_max > 0) S = (KB + nk_max - 1) / nk_max;
-  bool ok = narrow::supported<OP>() && rows <= narrow::BM && p.N % BN == 0;
+  bool ok = narrow::supported<OP>() && rows <= narrow::BM && p.N % BN == 0 &&
+            (int64_t)p.N / BN * p.G * S <= kMaxBlocks;
   if constexpr (OP == BSMM_OP_FP8_MX_BMM) ok = ok && narrow::scales_fit<uint8_t>(nk_max);
   if constexpr (OP == BSMM_OP_FP8_BLOCKWISE) ok = ok && narrow::scales_fit<float>(nk_max);
   if (!ok) {
