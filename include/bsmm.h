@@ -617,9 +617,10 @@ bsmm_status bsmm_quant_int8_mx(const void* x, int64_t ldx, bsmm_dtype x_dtype, i
 /*
  * The gate of a feed-forward layer on h [R, 2F] (bf16 or fp32):
  *   a(r, f) = silu(h(r, f)) * h(r, F + f),  silu(g) = g / (1 + e^-g)
- * a [R, F] of h's type, computed in fp32.  With q and scale (both or neither)
- * also the checkpoint of h, [R, 2F], as bsmm_quant_int8_mx writes it, from the
- * same read.  F % 32 == 0; rows as for bsmm_quant_int8_mx.
+ * a [R, F] of h's type, computed in fp32 (for any g: 0 where silu falls below
+ * fp32, a NaN for -inf).  With q and scale (both or neither) also the checkpoint
+ * of h, [R, 2F], as bsmm_quant_int8_mx writes it, from the same read.  F % 32 ==
+ * 0; rows as for bsmm_quant_int8_mx.
  */
 bsmm_status bsmm_swiglu(const void* h, int64_t ldh, bsmm_dtype dtype, void* a, int64_t lda,
                         int8_t* q, int64_t ldq, uint8_t* scale, int64_t s_r, int64_t R, int64_t F,
