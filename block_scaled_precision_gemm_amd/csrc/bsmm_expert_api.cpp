@@ -244,7 +244,6 @@ bool wgrad_sizes(bsmm_dtype dtype, int checkpoint, bool dy_rows, bool x_rows, in
   return true;
 }
 
-
 }  // namespace
 
 extern "C" {
